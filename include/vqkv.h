@@ -317,6 +317,78 @@ vqkv_status vqkv_encode_paged(const vqkv_encode_args* args, const vqkv_paging* p
 vqkv_status vqkv_decode_attn_paged(const vqkv_decode_args* args, const vqkv_paging* paging, void* stream);
 
 /*
+ * vqkv_evict_select — which tokens each (sequence, KV head) keeps when its
+ * cache is cut to n_keep tokens.
+ *
+ * For sequence b (L = seq_lens[b] clamped to [0, max_seq_len]) and KV head h,
+ * K = min(L, n_keep) tokens are kept: the first n_sink and the last n_recent
+ * of its L tokens, then those of the largest mass, ties to the lowest
+ * position.  A NaN mass ranks below every number; -0 equals +0.  keep[b][h][i]
+ * (i < K) receives their positions in ascending order; entries i >= K are not
+ * written.  keep_lens[b] = K.  Needs no workspace.
+ *
+ * n_sink, n_recent >= 0 and n_sink + n_recent <= n_keep.
+ */
+typedef struct {
+  int32_t B;                  /* sequences, 0..65535 */
+  int32_t Hkv;                /* KV heads, 1..65535 */
+  int32_t cap_len;            /* row length of mass, 1..2^30 */
+  int32_t max_seq_len;        /* upper bound of seq_lens, 0 <= max_seq_len <= cap_len */
+  int32_t n_keep;             /* tokens kept per (sequence, KV head), >= 1; row length of keep */
+  int32_t n_sink, n_recent;   /* always kept: the first / last tokens of a sequence */
+  const float* mass;          /* device fp32 [B][Hkv][cap_len] */
+  const int32_t* seq_lens;    /* device [B] */
+  int32_t* keep;              /* device int32 [B][Hkv][n_keep] out */
+  int32_t* keep_lens;         /* device int32 [B] out */
+  uint32_t* error_flags;      /* device, optional: VQKV_DEVERR_SEQ_LEN */
+} vqkv_evict_select_args;
+
+vqkv_status vqkv_evict_select(const vqkv_evict_select_args* args, void* stream);
+
+/*
+ * vqkv_cache_compact — moves chosen tokens up in the packed cache, in place:
+ * after an eviction (the kept positions of vqkv_evict_select move to the
+ * front) or a draft verification (the accepted path of a draft tree moves to
+ * the end of the prefix).
+ *
+ * For sequence b, KV head h and i < counts[b] (clamped to [0, n_src]), the
+ * codes of token src[b][h][i] replace those of token d = start[b] + i in the K
+ * and the V stream, and mass[b][h][src] replaces mass[b][h][d].  Every token
+ * is read before any call's write can reach it, so the call behaves as if it
+ * copied the sources out first.  A source must satisfy d <= src <
+ * seq_lens[b] (tokens only move up); one that does not leaves token d as it
+ * is and sets VQKV_DEVERR_POSITION, as does a d at or past cap_len.  Sources
+ * need not ascend and may repeat.  No other token's codes change.  Where mass
+ * is given, entries start[b] + counts[b] <= t < seq_lens[b] become 0 (those
+ * tokens are no longer held; a token appended there later starts at 0).
+ *
+ * seq_lens is the length before the call (clamped to [0, cap_len], with
+ * VQKV_DEVERR_SEQ_LEN); the length afterwards is start[b] + counts[b].  A
+ * start outside [0, cap_len] sets VQKV_DEVERR_POSITION and changes nothing of
+ * that sequence.  Blocks of a paged cache that several sequences share must not
+ * be moved into; a table entry outside [0, num_blocks) is not dereferenced:
+ * its tokens stay as they are and VQKV_DEVERR_BLOCK is set.
+ */
+typedef struct {
+  int32_t mode;               /* vqkv_mode */
+  int32_t B;                  /* sequences, 0..65535 */
+  int32_t Hkv;                /* KV heads, 1..21845 */
+  int32_t cap_len;            /* cache capacity in tokens, 1..2^30 */
+  int32_t n_src;              /* entries per row of src, >= 0 */
+  int32_t src_heads;          /* Hkv, or 1: the same sources for every head */
+  uint8_t* k_codes;           /* device [B][Hkv][vqkv_code_bytes], or a pool; 16-byte aligned */
+  uint8_t* v_codes;           /* the same for the values */
+  const int32_t* seq_lens;    /* device [B] */
+  const int32_t* src;         /* device [B][src_heads][n_src] absolute positions */
+  const int32_t* counts;      /* device [B] */
+  const int32_t* start;       /* device [B], or NULL: 0 */
+  float* mass;                /* device fp32 [B][Hkv][cap_len], or NULL */
+  uint32_t* error_flags;      /* device, optional */
+} vqkv_cache_compact_args;
+
+vqkv_status vqkv_cache_compact(const vqkv_cache_compact_args* args, const vqkv_paging* paging, void* stream);
+
+/*
  * vqkv_decode_attn_fp16 — the same decode attention over a plain fp16 KV
  * cache, the comparison point for the quantised path on the same shapes
  * (the paper measures its speed-up against FP16 attention, summary page,

@@ -32,7 +32,8 @@ EXPORTED = ["vqkv_code_bytes", "vqkv_decode_workspace_bytes", "vqkv_decode_num_s
             "vqkv_decode_attn_static", "vqkv_decode_static_error", "vqkv_encode_paged", "vqkv_decode_attn_paged", "vqkv_test_decode_ring_timeout",
             "vqkv_fp16_decode_workspace_bytes", "vqkv_decode_attn_fp16", "vqkv_smoothing", "vqkv_calib_transform",
             "vqkv_kmeans_workspace_bytes", "vqkv_kmeans", "vqkv_kmeans_seed", "vqkv_kmeans_assign",
-            "vqkv_kmeans_update_workspace_bytes", "vqkv_kmeans_update", "vqkv_status_string"]
+            "vqkv_kmeans_update_workspace_bytes", "vqkv_kmeans_update", "vqkv_status_string",
+            "vqkv_evict_select", "vqkv_cache_compact"]
 STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -88,6 +89,21 @@ class KmeansArgs(ctypes.Structure):
 class DecodeAppendArgs(ctypes.Structure):
     _fields_ = [("decode", DecodeArgs), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
                 ("near_tie_count", ctypes.c_void_p)]
+
+
+class EvictSelectArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("cap_len", ctypes.c_int32),
+                ("max_seq_len", ctypes.c_int32), ("n_keep", ctypes.c_int32), ("n_sink", ctypes.c_int32),
+                ("n_recent", ctypes.c_int32), ("mass", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("keep", ctypes.c_void_p), ("keep_lens", ctypes.c_void_p), ("error_flags", ctypes.c_void_p)]
+
+
+class CacheCompactArgs(ctypes.Structure):
+    _fields_ = [("mode", ctypes.c_int32), ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("cap_len", ctypes.c_int32),
+                ("n_src", ctypes.c_int32), ("src_heads", ctypes.c_int32), ("k_codes", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("src", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("start", ctypes.c_void_p), ("mass", ctypes.c_void_p),
+                ("error_flags", ctypes.c_void_p)]
 
 
 _lib = None
@@ -157,6 +173,10 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.vqkv_kmeans_update.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                          ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_size_t, ctypes.c_void_p]
+        L.vqkv_evict_select.restype = ctypes.c_int
+        L.vqkv_evict_select.argtypes = [ctypes.POINTER(EvictSelectArgs), ctypes.c_void_p]
+        L.vqkv_cache_compact.restype = ctypes.c_int
+        L.vqkv_cache_compact.argtypes = [ctypes.POINTER(CacheCompactArgs), ctypes.POINTER(Paging), ctypes.c_void_p]
         L.vqkv_status_string.restype = ctypes.c_char_p
         L.vqkv_status_string.argtypes = [ctypes.c_int]
         _lib = L
@@ -362,6 +382,97 @@ def fp16_decode_workspace(B, Hq, Hkv, cap_len, max_seq_len, num_splits=0, device
     if n == 0:
         raise VqkvError(1, "vqkv_fp16_decode_workspace_bytes")
     return torch.zeros((n + 255) // 256 * 256, dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------- editing a cache
+
+def _need(what, dtype, *tensors) -> None:
+    """Raises unless every given tensor (None is skipped) is a contiguous ``dtype`` tensor on the current device."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t in tensors:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{what}: {name} must be {dtype}, not {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: {name} must be on the current CUDA device")
+
+
+def _need_shape(what, name, t, *shape) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: {name} must have shape {shape}, not {tuple(t.shape)}")
+
+
+def _need_cache(what, mode, B, Hkv, cap_len, k_codes, v_codes, block_table, block_tokens, num_blocks) -> None:
+    """Shapes of a contiguous cache [B][Hkv][bytes], or of the pools and the table of a paged one."""
+    if block_table is None:
+        shape = (B, Hkv, vqkv_code_bytes(mode, cap_len))
+    else:
+        shape = (num_blocks, Hkv, vqkv_code_bytes(mode, block_tokens))
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"{what}: block_table must have shape ({B}, max_blocks)")
+    _need_shape(what, "k_codes", k_codes, *shape)
+    _need_shape(what, "v_codes", v_codes, *shape)
+
+
+def vqkv_evict_select(mass, seq_lens, keep, keep_lens, n_sink=0, n_recent=0, max_seq_len=None, error_flags=None,
+                      stream=None) -> None:
+    """The positions each (sequence, KV head) keeps when its cache is cut to keep.shape[2] tokens.
+
+    mass fp32 [B][Hkv][cap_len]; seq_lens int32 [B]; writes keep int32
+    [B][Hkv][n_keep] (ascending; only the first keep_lens[b] entries of a row)
+    and keep_lens int32 [B].  Always kept: the first n_sink and the last
+    n_recent tokens; then those of the largest mass, ties to the lowest position.
+    """
+    import torch
+    what = "vqkv_evict_select"
+    _need(what, torch.float32, ("mass", mass))
+    _need(what, torch.int32, ("seq_lens", seq_lens), ("keep", keep), ("keep_lens", keep_lens),
+          ("error_flags", error_flags))
+    B, Hkv, cap = mass.shape
+    n_keep = keep.shape[-1]
+    _need_shape(what, "keep", keep, B, Hkv, n_keep)
+    _need_shape(what, "seq_lens", seq_lens, B)
+    _need_shape(what, "keep_lens", keep_lens, B)
+    a = EvictSelectArgs(B=B, Hkv=Hkv, cap_len=cap, max_seq_len=cap if max_seq_len is None else max_seq_len,
+                        n_keep=n_keep, n_sink=n_sink, n_recent=n_recent, mass=_ptr(mass), seq_lens=_ptr(seq_lens),
+                        keep=_ptr(keep), keep_lens=_ptr(keep_lens), error_flags=_ptr(error_flags))
+    _check(lib().vqkv_evict_select(ctypes.byref(a), _stream(stream)), what)
+
+
+def vqkv_cache_compact(mode, k_codes, v_codes, seq_lens, src, counts, cap_len, start=None, mass=None,
+                       error_flags=None, block_table=None, block_tokens=0, num_blocks=0, stream=None) -> None:
+    """Token start[b] + i of every stream takes the codes (and mass) of token src[b][h][i], in place.
+
+    src int32 [B][Hkv or 1][n] absolute positions, start[b] + i <= src <
+    seq_lens[b]; counts int32 [B] entries used; start int32 [B] or None (0).
+    k_codes / v_codes uint8 [B][Hkv][bytes], or pools with block_table.  mass
+    (fp32 [B][Hkv][cap_len], optional) moves along and is cleared behind the
+    last moved token.
+    """
+    import torch
+    what = "vqkv_cache_compact"
+    _need(what, torch.uint8, ("k_codes", k_codes), ("v_codes", v_codes))
+    _need(what, torch.int32, ("seq_lens", seq_lens), ("src", src), ("counts", counts), ("start", start),
+          ("error_flags", error_flags), ("block_table", block_table))
+    _need(what, torch.float32, ("mass", mass))
+    B, heads, n = src.shape
+    Hkv = k_codes.shape[1]
+    _need_cache(what, mode, B, Hkv, cap_len, k_codes, v_codes, block_table, block_tokens, num_blocks)
+    _need_shape(what, "seq_lens", seq_lens, B)
+    _need_shape(what, "counts", counts, B)
+    if start is not None:
+        _need_shape(what, "start", start, B)
+    if mass is not None:
+        _need_shape(what, "mass", mass, B, Hkv, cap_len)
+    a = CacheCompactArgs(mode=mode, B=B, Hkv=Hkv, cap_len=cap_len, n_src=n, src_heads=heads, k_codes=_ptr(k_codes),
+                         v_codes=_ptr(v_codes), seq_lens=_ptr(seq_lens), src=_ptr(src), counts=_ptr(counts),
+                         start=_ptr(start), mass=_ptr(mass), error_flags=_ptr(error_flags))
+    pg = ctypes.byref(paging(block_table, block_tokens, num_blocks)) if block_table is not None else None
+    _check(lib().vqkv_cache_compact(ctypes.byref(a), pg, _stream(stream)), what)
 
 
 # ---------------------------------------------------------------- calibration

@@ -13,6 +13,8 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr size_t kWsHeader = 256;   // word 0: device error flags
+constexpr int kMaxGridYZ = 65535;   // CUDA's limit on gridDim.y and gridDim.z
+constexpr int kMaxTokens = 1 << 30; // longest row of the cache-editing calls (positions plus a stride stay in 32 bits)
 
 struct DeviceInfo {
   bool ready = false;
@@ -42,6 +44,7 @@ vqkv_status device_info(DeviceInfo* out) {
     if (decode_fp16_prepare() != cudaSuccess || decode_fp16_occupancy(&d.decode_bpsm[kModeFp16]) != cudaSuccess)
       return VQKV_ERR_CUDA;
     if (d.decode_bpsm[kModeFp16] < 1) d.decode_bpsm[kModeFp16] = 1;
+    if (evict_select_prepare() != cudaSuccess) return VQKV_ERR_CUDA;
     d.ready = true;
   }
   *out = d;
@@ -524,6 +527,75 @@ vqkv_status vqkv_decode_attn_fp16(const vqkv_fp16_decode_args* a, void* stream) 
   if (p.defer_merge && p.n_splits > 1 && launch_combine(p, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return VQKV_ERR_CUDA;
   return VQKV_OK;
+}
+
+vqkv_status vqkv_evict_select(const vqkv_evict_select_args* a, void* stream) {
+  if (a == nullptr) return VQKV_ERR_INVALID_ARG;
+  if (a->B < 0 || a->Hkv < 1 || a->cap_len < 1 || a->max_seq_len < 0 || a->max_seq_len > a->cap_len || a->n_keep < 1 ||
+      a->n_sink < 0 || a->n_recent < 0 || (long long)a->n_sink + a->n_recent > a->n_keep)
+    return VQKV_ERR_INVALID_ARG;
+  if (a->B > kMaxGridYZ || a->Hkv > kMaxGridYZ || a->cap_len > kMaxTokens) return VQKV_ERR_UNSUPPORTED;
+  if (a->B == 0) return VQKV_OK;
+  if (!a->mass || !a->seq_lens || !a->keep || !a->keep_lens) return VQKV_ERR_INVALID_ARG;
+  if (!aligned(a->mass, 4) || !aligned(a->seq_lens, 4) || !aligned(a->keep, 4) || !aligned(a->keep_lens, 4) ||
+      !aligned(a->error_flags, 4))
+    return VQKV_ERR_INVALID_ARG;
+  DeviceInfo di;
+  const vqkv_status st = device_info(&di);
+  if (st != VQKV_OK) return st;
+  SelectParams p;
+  p.mass = a->mass;
+  p.seq_lens = a->seq_lens;
+  p.keep = a->keep;
+  p.keep_lens = a->keep_lens;
+  p.err = a->error_flags;
+  p.B = a->B;
+  p.Hkv = a->Hkv;
+  p.cap_len = a->cap_len;
+  p.max_seq_len = a->max_seq_len;
+  p.n_keep = a->n_keep;
+  p.n_sink = a->n_sink;
+  p.n_recent = a->n_recent;
+  return launch_evict_select(p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
+}
+
+vqkv_status vqkv_cache_compact(const vqkv_cache_compact_args* a, const vqkv_paging* pg, void* stream) {
+  if (a == nullptr) return VQKV_ERR_INVALID_ARG;
+  if (!is_code_mode(a->mode)) return VQKV_ERR_UNSUPPORTED;
+  if (a->B < 0 || a->Hkv < 1 || a->cap_len < 1 || a->n_src < 0) return VQKV_ERR_INVALID_ARG;
+  if (a->src_heads != 1 && a->src_heads != a->Hkv) return VQKV_ERR_INVALID_ARG;
+  if (a->B > kMaxGridYZ || 3LL * a->Hkv > kMaxGridYZ || a->cap_len > kMaxTokens) return VQKV_ERR_UNSUPPORTED;
+  if (pg != nullptr) {
+    const vqkv_status st = validate_paging(pg, a->mode, a->cap_len);
+    if (st != VQKV_OK) return st;
+    if (a->B > 0 && (!pg->block_table || !aligned(pg->block_table, 4))) return VQKV_ERR_INVALID_ARG;
+  }
+  if (a->B == 0) return VQKV_OK;
+  if (!a->k_codes || !a->v_codes || !a->seq_lens || !a->counts || (!a->src && a->n_src > 0)) return VQKV_ERR_INVALID_ARG;
+  if (!aligned(a->k_codes, 16) || !aligned(a->v_codes, 16) || !aligned(a->seq_lens, 4) || !aligned(a->src, 4) ||
+      !aligned(a->counts, 4) || !aligned(a->start, 4) || !aligned(a->mass, 4) || !aligned(a->error_flags, 4))
+    return VQKV_ERR_INVALID_ARG;
+  if (a->n_src == 0 && a->mass == nullptr) return VQKV_OK;
+  DeviceInfo di;
+  const vqkv_status st = device_info(&di);
+  if (st != VQKV_OK) return st;
+  CompactParams p;
+  p.codes[VQKV_ROLE_K] = a->k_codes;
+  p.codes[VQKV_ROLE_V] = a->v_codes;
+  p.seq_lens = a->seq_lens;
+  p.src = a->src;
+  p.counts = a->counts;
+  p.start = a->start;
+  p.mass = a->mass;
+  p.err = a->error_flags;
+  p.stream_bytes = (long long)vqkv_code_bytes(a->mode, a->cap_len);
+  p.B = a->B;
+  p.Hkv = a->Hkv;
+  p.src_heads = a->src_heads;
+  p.n_src = a->n_src;
+  p.cap_len = a->cap_len;
+  set_paging(p, pg, a->mode);
+  return launch_compact(a->mode, p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
 }
 
 const char* vqkv_status_string(vqkv_status s) {

@@ -1,0 +1,554 @@
+// Editing a packed cache under a running model: which tokens a sequence keeps
+// (vqkv_evict_select) and the in-place move of chosen tokens
+// (vqkv_cache_compact).
+#include "common.cuh"
+#include "internal.h"
+
+namespace vqkv {
+namespace {
+
+// ------------------------------------------------------------------ clusters
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+// Shared address of the same variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t cluster_ld(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_st(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+template <typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Args...), dim3 grid, int cluster, int threads, size_t smem, cudaStream_t stream,
+                           const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// ------------------------------------------------------------------ compaction
+//
+// Token d = start + i of a stream takes the bytes of token src[i] >= d.  In
+// place this is safe when every read of a source happens before the write of
+// that position.  A cluster of CTAs owns one stream and walks it in rounds of
+// consecutive destination tokens; a round's sources are >= its destinations,
+// so its writes can only hit sources of the same or an earlier round.  Hence:
+// read round r + 1 into registers, meet at the cluster barrier (every read of
+// rounds <= r + 1 is done), write round r.
+//
+// The layouts keep every token's bytes to itself, spread over the 32 lanes'
+// runs of a 16-token group (include/vqkv.h).  A lane of the destination group
+// gathers its run: a K run holds SLOTS = 2 tokens (gid, gid + 8), a V run 4
+// (2tig, 2tig + 1, 2tig + 8, 2tig + 9), each SB bytes, and only the run of
+// the source token's own lane position is read.
+
+constexpr int CP_WARPS = 16;
+constexpr int CP_THREADS = CP_WARPS * 32;
+
+template <int BYTES>
+struct Bytes {
+  uint32_t w[(BYTES + 3) / 4];
+};
+
+__device__ __forceinline__ uint32_t ld8(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld16(const uint8_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld32(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld64(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld128(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+// Bytes a token has in one lane's run, and the run's words.
+template <int MODE, int ROLE>
+struct RunGeo {
+  static constexpr int SLOTS = ROLE == VQKV_ROLE_K ? 2 : 4;
+  static constexpr int W = MODE == VQKV_MODE_VQ2    ? 4
+                           : MODE == VQKV_MODE_VQ4  ? 8
+                           : MODE == VQKV_MODE_VQ3  ? 6
+                           : MODE == VQKV_MODE_VQ15 ? 3
+                                                    : (ROLE == VQKV_ROLE_K ? 3 : 5);
+  static constexpr int SB = MODE == VQKV_MODE_VQ125 ? 5 : W * 4 / SLOTS;
+  // V runs of the byte codes interleave their tokens: byte k of every word is slot k
+  static constexpr bool INTERLEAVED = ROLE == VQKV_ROLE_V && (MODE == VQKV_MODE_VQ2 || MODE == VQKV_MODE_VQ4);
+};
+
+// The SB bytes of token r (0..15) of a 16-token group in the run of lane
+// position x (K: x = tig, V: x = gid); p: the group's tile, u: the group
+// within it (1.5 bit).
+template <int MODE, int ROLE>
+__device__ __forceinline__ Bytes<RunGeo<MODE, ROLE>::SB> load_slot(const uint8_t* p, int r, int u, int x) {
+  Bytes<RunGeo<MODE, ROLE>::SB> o;
+  const int L = ROLE == VQKV_ROLE_K ? 4 * (r & 7) + x : 4 * x + ((r & 7) >> 1);
+  const int slot = ROLE == VQKV_ROLE_K ? r >> 3 : (r & 1) + 2 * (r >> 3);
+  if constexpr (RunGeo<MODE, ROLE>::INTERLEAVED) {
+    const uint32_t sel = 0x0040u + (uint32_t)slot * 0x0011u;   // byte `slot` of two words
+#pragma unroll
+    for (int h = 0; h < RunGeo<MODE, ROLE>::W / 4; ++h) {
+      const uint4 a = ld128(p + 512 * h + 16 * L);
+      o.w[h] = __byte_perm(__byte_perm(a.x, a.y, sel), __byte_perm(a.z, a.w, sel), 0x5410);
+    }
+  } else if constexpr (MODE == VQKV_MODE_VQ2) {
+    const uint2 a = ld64(p + 16 * L + 8 * slot);
+    o.w[0] = a.x, o.w[1] = a.y;
+  } else if constexpr (MODE == VQKV_MODE_VQ4) {
+    const uint4 a = ld128(p + 512 * slot + 16 * L);
+    o.w[0] = a.x, o.w[1] = a.y, o.w[2] = a.z, o.w[3] = a.w;
+  } else if constexpr (MODE == VQKV_MODE_VQ3 && ROLE == VQKV_ROLE_K) {
+    o.w[0] = ld32(p + 16 * L + 12 * slot);   // run bytes 0..11 or 12..23 (plane 1 from byte 16)
+    const uint2 a = ld64(slot ? p + 512 + 8 * L : p + 16 * L + 8);
+    const uint32_t mid = slot ? a.x : ld32(p + 16 * L + 4);
+    o.w[1] = mid, o.w[2] = slot ? a.y : a.x;
+  } else if constexpr (MODE == VQKV_MODE_VQ3) {
+    uint32_t h[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int n = 6 * slot + 2 * k;
+      h[k] = ld16(n < 16 ? p + 16 * L + n : p + 512 + 8 * L + n - 16);
+    }
+    o.w[0] = h[0] | (h[1] << 16), o.w[1] = h[2];
+  } else if constexpr (MODE == VQKV_MODE_VQ15 && ROLE == VQKV_ROLE_K) {
+    const uint8_t* q = p + 48 * L + 12 * u + 6 * slot;
+    const uint32_t a = ld16(q), b = ld16(q + 2), c = ld16(q + 4);
+    o.w[0] = a | (b << 16), o.w[1] = c;
+  } else if constexpr (MODE == VQKV_MODE_VQ15) {
+    const uint8_t* q = p + 48 * L + 12 * u + 3 * slot;
+    o.w[0] = ld8(q) | (ld8(q + 1) << 8) | (ld8(q + 2) << 16);
+  } else {
+    constexpr int P0 = ROLE == VQKV_ROLE_K ? 8 : 16, P1 = ROLE == VQKV_ROLE_K ? 2 : 4;
+    uint32_t b[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      const int n = 5 * slot + k;
+      b[k] = ld8(n < P0 ? p + P0 * L + n : p + 256 + P1 * L + n - P0);
+    }
+    o.w[0] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24), o.w[1] = b[4];
+  }
+  return o;
+}
+
+// Slot k's bytes into the run (k is a constant after unrolling).
+template <int MODE, int ROLE>
+__device__ __forceinline__ void put_slot(uint32_t (&run)[RunGeo<MODE, ROLE>::W], int k,
+                                         const Bytes<RunGeo<MODE, ROLE>::SB>& v) {
+  using G = RunGeo<MODE, ROLE>;
+  if constexpr (G::INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < G::W; ++i) run[i] |= ((v.w[i >> 2] >> (8 * (i & 3))) & 0xffu) << (8 * k);
+  } else {
+#pragma unroll
+    for (int n = 0; n < G::SB; ++n) {
+      const uint32_t byte = (v.w[n >> 2] >> (8 * (n & 3))) & 0xffu;
+      const int at = G::SB * k + n;
+      run[at >> 2] |= byte << (8 * (at & 3));
+    }
+  }
+}
+
+// The lane's run of a 16-token group.
+template <int MODE, int ROLE>
+__device__ __forceinline__ void store_run(uint8_t* p, int u, int lane, const uint32_t (&w)[RunGeo<MODE, ROLE>::W]) {
+  if constexpr (MODE == VQKV_MODE_VQ2) {
+    *reinterpret_cast<uint4*>(p + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if constexpr (MODE == VQKV_MODE_VQ4) {
+    *reinterpret_cast<uint4*>(p + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p + 512 + 16 * lane) = make_uint4(w[4], w[5], w[6], w[7]);
+  } else if constexpr (MODE == VQKV_MODE_VQ3) {
+    *reinterpret_cast<uint4*>(p + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint2*>(p + 512 + 8 * lane) = make_uint2(w[4], w[5]);
+  } else if constexpr (MODE == VQKV_MODE_VQ15) {
+    uint32_t* q = reinterpret_cast<uint32_t*>(p + 48 * lane + 12 * u);
+    q[0] = w[0], q[1] = w[1], q[2] = w[2];
+  } else if constexpr (ROLE == VQKV_ROLE_K) {
+    *reinterpret_cast<uint2*>(p + 8 * lane) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint16_t*>(p + 256 + 2 * lane) = (uint16_t)w[2];
+  } else if (lane < 16) {   // 16 runs, each with the four tokens of two lane columns
+    *reinterpret_cast<uint4*>(p + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint32_t*>(p + 256 + 4 * lane) = w[4];
+  }
+}
+
+// The call's view of one (sequence, KV head): destinations start .. start + n - 1.
+struct Move {
+  int b, kvh, L, start, n;
+  const int32_t* src;
+
+  __device__ __forceinline__ Move(const CompactParams& p, int b_, int kvh_, bool report) : b(b_), kvh(kvh_) {
+    const int raw = p.seq_lens[b];
+    L = min(max(raw, 0), p.cap_len);
+    start = p.start != nullptr ? p.start[b] : 0;
+    const int c = min(max(p.counts[b], 0), p.n_src);
+    const bool outside = start < 0 || start > p.cap_len;   // nothing moves, nothing is cleared
+    if (outside) start = L;
+    n = outside ? 0 : min(c, p.cap_len - start);
+    if (report && p.err != nullptr) {
+      if (raw != L) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
+      if (outside || n < c) atomicOr(p.err, VQKV_DEVERR_POSITION);
+    }
+    src = p.src + ((size_t)b * p.src_heads + (p.src_heads > 1 ? kvh : 0)) * p.n_src;
+  }
+  // The token whose bytes token d takes (d itself where it stays).
+  __device__ __forceinline__ int source(const CompactParams& p, int d, bool report) const {
+    const int i = d - start;
+    if (i < 0 || i >= n) return d;
+    const int s = src[i];
+    if (s >= d && s < L) return s;
+    if (report && p.err != nullptr) atomicOr(p.err, VQKV_DEVERR_POSITION);
+    return d;
+  }
+};
+
+template <int MODE, int ROLE, bool PAGED>
+__device__ __forceinline__ void move_codes(const CompactParams& p, const Move& mv, int rank, int cluster) {
+  using G = RunGeo<MODE, ROLE>;
+  constexpr int TT = MODE == VQKV_MODE_VQ15 ? 64 : 16;
+  constexpr int TILE_BYTES = MODE == VQKV_MODE_VQ2    ? 512
+                             : MODE == VQKV_MODE_VQ4  ? 1024
+                             : MODE == VQKV_MODE_VQ3  ? 768
+                             : MODE == VQKV_MODE_VQ15 ? 1536
+                                                      : 320;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  uint8_t* codes = p.codes[ROLE];
+  const int first = mv.start >> 4, last = mv.n > 0 ? (mv.start + mv.n + 15) >> 4 : first;   // 16-token groups
+  const int rounds = (last - first + cluster * CP_WARPS - 1) / (cluster * CP_WARPS);
+
+  // Round k's group of this warp: its run in w, its place (-1: nothing to write).
+  auto load = [&](int k, uint32_t (&w)[G::W], long long& place) {
+    const int grp = first + (k * cluster + rank) * CP_WARPS + warp;
+    place = -1;
+#pragma unroll
+    for (int i = 0; i < G::W; ++i) w[i] = 0u;
+    if (grp >= last) return;
+    bool bad = false;
+    const long long dst = tile_offset<PAGED>(p, mv.b, mv.kvh, (grp << 4) / TT, TILE_BYTES, &bad);
+    // lane r < 16: where token 16 grp + r comes from: tile offset | position within the tile
+    const int d = (grp << 4) + (lane & 15);
+    int s = mv.source(p, d, ROLE == VQKV_ROLE_K && lane < 16);
+    bool sbad = false;
+    long long from = tile_offset<PAGED>(p, mv.b, mv.kvh, s / TT, TILE_BYTES, &sbad);
+    if (sbad) from = dst, s = d;
+    from |= s & 63;   // tile offsets are multiples of 64
+    if (PAGED && (bad || sbad) && p.err != nullptr) atomicOr(p.err, VQKV_DEVERR_BLOCK);
+    if (bad || __all_sync(0xffffffffu, s == d)) return;   // nothing moves: leave the group as it is
+    place = dst | ((grp & 3) << 4);
+#pragma unroll
+    for (int k2 = 0; k2 < G::SLOTS; ++k2) {
+      const int r = ROLE == VQKV_ROLE_K ? gid + 8 * k2 : 2 * tig + (k2 & 1) + 8 * (k2 >> 1);
+      const long long f = __shfl_sync(0xffffffffu, from, r);
+      if (!(MODE == VQKV_MODE_VQ125 && ROLE == VQKV_ROLE_V) || lane < 16) {
+        const int at = (int)(f & 63);
+        put_slot<MODE, ROLE>(w, k2, load_slot<MODE, ROLE>(codes + (f & ~63LL), at & 15, (at >> 4) & 3,
+                                                          ROLE == VQKV_ROLE_K ? tig : gid));
+      }
+    }
+  };
+  uint32_t cur[G::W], nxt[G::W];
+  long long cur_at = -1, nxt_at = -1;
+  if (rounds > 0) load(0, cur, cur_at);
+  for (int k = 0; k < rounds; ++k) {
+    if (k + 1 < rounds) load(k + 1, nxt, nxt_at);
+    if (cluster > 1) cluster_sync(); else __syncthreads();
+    if (cur_at >= 0) store_run<MODE, ROLE>(codes + (cur_at & ~63LL), (int)((cur_at >> 4) & 3), lane, cur);
+#pragma unroll
+    for (int i = 0; i < G::W; ++i) cur[i] = nxt[i];
+    cur_at = nxt_at;
+  }
+}
+
+__device__ __forceinline__ void move_mass(const CompactParams& p, const Move& mv, int rank, int cluster) {
+  constexpr int U = 4;
+  float* row = p.mass + ((size_t)mv.b * p.Hkv + mv.kvh) * p.cap_len;
+  const int per = cluster * CP_THREADS * U;
+  const int rounds = (mv.n + per - 1) / per;
+  auto load = [&](int k, float (&v)[U], int (&at)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = k * per + (rank * U + u) * CP_THREADS + (int)threadIdx.x, d = mv.start + i;
+      at[u] = -1;
+      if (i < mv.n) {
+        const int s = mv.source(p, d, false);
+        if (s != d) {
+          at[u] = d;
+          v[u] = __uint_as_float(ld32(reinterpret_cast<const uint8_t*>(row + s)));
+        }
+      }
+    }
+  };
+  float cur[U], nxt[U];
+  int cur_at[U], nxt_at[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) cur[u] = nxt[u] = 0.f, cur_at[u] = nxt_at[u] = -1;
+  if (rounds > 0) load(0, cur, cur_at);
+  for (int k = 0; k < rounds; ++k) {
+    if (k + 1 < rounds) load(k + 1, nxt, nxt_at);
+    if (cluster > 1) cluster_sync(); else __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (cur_at[u] >= 0) row[cur_at[u]] = cur[u];
+      cur[u] = nxt[u], cur_at[u] = nxt_at[u];
+    }
+  }
+  // every source has been read: clear what the sequence no longer holds
+  for (int t = mv.start + mv.n + rank * CP_THREADS + (int)threadIdx.x; t < mv.L; t += cluster * CP_THREADS) row[t] = 0.f;
+}
+
+// grid (cluster, Hkv x streams, B): stream 0 = K codes, 1 = V codes, 2 = mass.
+template <int MODE, bool PAGED>
+__global__ void __launch_bounds__(CP_THREADS) compact_kernel(const CompactParams p) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int streams = p.mass != nullptr ? 3 : 2;
+  const int kvh = blockIdx.y / streams, stream = blockIdx.y - kvh * streams, b = blockIdx.z;
+  const Move mv(p, b, kvh, stream == 0 && kvh == 0 && blockIdx.x == 0 && threadIdx.x == 0);
+  if (stream == 0)
+    move_codes<MODE, VQKV_ROLE_K, PAGED>(p, mv, blockIdx.x, gridDim.x);
+  else if (stream == 1)
+    move_codes<MODE, VQKV_ROLE_V, PAGED>(p, mv, blockIdx.x, gridDim.x);
+  else
+    move_mass(p, mv, blockIdx.x, gridDim.x);
+}
+
+// ------------------------------------------------------------------ selection
+//
+// The K largest of a row of n fp32 weights, in position order.  A cluster
+// owns one (sequence, KV head) row, each CTA a contiguous part of it (kept in
+// shared memory as order-preserving 32-bit keys while it fits).  Radix select
+// from the top: three passes over 11, 11 and 10 key bits find the K-th
+// largest key; per pass the CTAs' 2048-bin counts are added through
+// distributed shared memory.  Then the kept positions are counted per warp
+// and CTA, and written by ballot ranks: larger keys all, keys equal to the
+// K-th while some are still needed, lowest position first.
+
+constexpr int SEL_THREADS = 1024;
+constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_BINS = 2048;
+constexpr int SEL_MAX_CLUSTER = 8;
+constexpr int SEL_CACHE = 40960;   // keys of a CTA's part kept in shared memory (160 KB)
+
+// Larger weight <=> larger key; NaN below everything, -0 as +0.
+__device__ __forceinline__ uint32_t weight_key(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);   // -0 + 0 = +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const SelectParams p) {
+  extern __shared__ uint32_t s_keys[];   // [min(part, SEL_CACHE)]
+  __shared__ uint32_t s_hist[SEL_BINS], s_total[SEL_BINS];
+  __shared__ uint32_t s_warp[SEL_WARPS], s_warp2[SEL_WARPS];
+  __shared__ uint32_t s_digit, s_above;
+  __shared__ uint32_t s_cta[2 * SEL_MAX_CLUSTER];   // per CTA: larger, equal
+  const int CL = gridDim.x, rank = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int raw = p.seq_lens[b], L = min(max(raw, 0), p.max_seq_len);
+  if (threadIdx.x == 0 && rank == 0 && kvh == 0) {
+    if (raw != L && p.err != nullptr) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
+    p.keep_lens[b] = min(L, p.n_keep);
+  }
+  int32_t* keep = p.keep + ((size_t)b * p.Hkv + kvh) * p.n_keep;
+  if (L <= p.n_keep) {   // everything stays
+    for (int t = rank * SEL_THREADS + (int)threadIdx.x; t < L; t += CL * SEL_THREADS) keep[t] = t;
+    return;
+  }
+  // parts of whole warp strides, so that each warp walks a contiguous piece
+  const int piece = ((L + CL * SEL_WARPS - 1) / (CL * SEL_WARPS) + 31) & ~31;
+  const int c0 = min(rank * SEL_WARPS * piece, L), c1 = min(c0 + SEL_WARPS * piece, L);
+  const float* mass = p.mass + ((size_t)b * p.Hkv + kvh) * p.cap_len;
+  const bool cached = SEL_WARPS * piece <= p.cache_keys;
+  auto make_key = [&](int t) -> uint32_t {
+    if (t < p.n_sink || t >= L - p.n_recent) return 0xffffffffu;   // above +inf: always kept
+    return weight_key(mass[t]);
+  };
+  auto key_at = [&](int t) -> uint32_t { return cached ? s_keys[t - c0] : make_key(t); };
+
+  uint32_t prefix = 0;                 // key bits found so far
+  uint32_t need = (uint32_t)p.n_keep;  // tokens still to take among keys with that prefix
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bits = pass == 2 ? 10 : 11;
+    for (int i = threadIdx.x; i < SEL_BINS; i += SEL_THREADS) s_hist[i] = 0u;
+    __syncthreads();
+    const uint32_t mask = (1u << bits) - 1u;
+    if (pass == 0) {
+      for (int t = c0 + (int)threadIdx.x; t < c1; t += SEL_THREADS) {
+        const uint32_t k = make_key(t);
+        if (cached) s_keys[t - c0] = k;
+        atomicAdd(&s_hist[k >> shift], 1u);
+      }
+    } else {
+      for (int t = c0 + (int)threadIdx.x; t < c1; t += SEL_THREADS) {
+        const uint32_t k = key_at(t);
+        if ((k >> (shift + bits)) == prefix) atomicAdd(&s_hist[(k >> shift) & mask], 1u);
+      }
+    }
+    if (CL > 1) {   // this CTA adds a share of the bins and gives every CTA the sums
+      cluster_sync();
+      const int share = SEL_BINS / CL;
+      if ((int)threadIdx.x < share) {
+        const int bin = rank * share + threadIdx.x;
+        const uint32_t h = smem_u32(&s_hist[bin]), o = smem_u32(&s_total[bin]);
+        uint32_t sum = 0;
+        for (int r = 0; r < CL; ++r) sum += cluster_ld(cluster_addr(h, r));
+        for (int r = 0; r < CL; ++r) cluster_st(cluster_addr(o, r), sum);
+      }
+      cluster_sync();
+    } else {
+      __syncthreads();
+    }
+    // bins from the top: thread i holds bins 2047 - 2i and 2046 - 2i
+    const uint32_t* tot = CL > 1 ? s_total : s_hist;
+    const int hi = SEL_BINS - 1 - 2 * (int)threadIdx.x;
+    const uint32_t x0 = tot[hi], x1 = tot[hi - 1];
+    uint32_t inc = x0 + x1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t v = s_warp[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      s_warp2[lane] = v;
+    }
+    __syncthreads();
+    const uint32_t before = inc - x0 - x1 + (warp > 0 ? s_warp2[warp - 1] : 0u);   // tokens in higher bins
+    if (before < need && need <= before + x0) {
+      s_digit = hi, s_above = before;
+    } else if (before + x0 < need && need <= before + x0 + x1) {
+      s_digit = hi - 1, s_above = before + x0;
+    }
+    __syncthreads();
+    prefix = (prefix << bits) | s_digit;
+    need -= s_above;
+    __syncthreads();
+  }
+  // prefix is the K-th largest key; `need` of the keys equal to it are kept
+  const int w0 = min(c0 + warp * piece, c1), w1 = min(w0 + piece, c1);
+  uint32_t larger = 0, equal = 0;
+  for (int t = w0 + lane; t < w1; t += 32) {
+    const uint32_t k = key_at(t);
+    larger += k > prefix;
+    equal += k == prefix;
+  }
+  larger = __reduce_add_sync(0xffffffffu, larger);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) s_warp[warp] = larger, s_warp2[warp] = equal;
+  __syncthreads();
+  uint32_t cl = s_warp[lane], ce = s_warp2[lane];   // SEL_WARPS == 32
+  uint32_t gl = __reduce_add_sync(0xffffffffu, lane < warp ? cl : 0u);
+  uint32_t ge = __reduce_add_sync(0xffffffffu, lane < warp ? ce : 0u);
+  if (CL > 1) {
+    cl = __reduce_add_sync(0xffffffffu, cl);
+    ce = __reduce_add_sync(0xffffffffu, ce);
+    if ((int)threadIdx.x < CL) {
+      cluster_st(cluster_addr(smem_u32(&s_cta[2 * rank]), threadIdx.x), cl);
+      cluster_st(cluster_addr(smem_u32(&s_cta[2 * rank + 1]), threadIdx.x), ce);
+    }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) gl += s_cta[2 * r], ge += s_cta[2 * r + 1];
+  }
+  uint32_t at = gl + min(ge, need), seen = ge;   // kept / equal tokens before this warp's piece
+  const uint32_t lt = (1u << lane) - 1u;
+  for (int t0 = w0; t0 < w1; t0 += 32) {
+    const int t = t0 + lane;
+    const uint32_t k = t < w1 ? key_at(t) : 0u;
+    const bool eq = t < w1 && k == prefix;
+    const uint32_t beq = __ballot_sync(0xffffffffu, eq);
+    const bool kept = t < w1 && (k > prefix || (eq && seen + __popc(beq & lt) < need));
+    const uint32_t bk = __ballot_sync(0xffffffffu, kept);
+    if (kept) keep[at + __popc(bk & lt)] = t;
+    at += __popc(bk);
+    seen += __popc(beq);
+  }
+}
+
+using CompactKernel = void (*)(CompactParams);
+template <int MODE>
+constexpr CompactKernel compact_of(bool paged) {
+  return paged ? (CompactKernel)compact_kernel<MODE, true> : (CompactKernel)compact_kernel<MODE, false>;
+}
+
+}  // namespace
+
+cudaError_t launch_compact(int mode, const CompactParams& p, int sms, cudaStream_t stream) {
+  const bool paged = p.block_table != nullptr;
+  const CompactKernel k = mode == VQKV_MODE_VQ2    ? compact_of<VQKV_MODE_VQ2>(paged)
+                          : mode == VQKV_MODE_VQ4  ? compact_of<VQKV_MODE_VQ4>(paged)
+                          : mode == VQKV_MODE_VQ3  ? compact_of<VQKV_MODE_VQ3>(paged)
+                          : mode == VQKV_MODE_VQ15 ? compact_of<VQKV_MODE_VQ15>(paged)
+                                                   : compact_of<VQKV_MODE_VQ125>(paged);
+  // CTAs per stream: enough that one round holds the destinations, at most
+  // eight (the portable cluster), fewer when the streams alone fill the GPU
+  const long long streams = (long long)p.B * p.Hkv * (p.mass != nullptr ? 3 : 2);
+  const long long groups = ((long long)p.n_src + 30) / 16;
+  int cluster = 1;
+  while (cluster < 8 && (long long)cluster * CP_WARPS < groups && streams * cluster < 2LL * sms) cluster *= 2;
+  return launch_cluster(k, dim3(cluster, p.Hkv * (p.mass != nullptr ? 3 : 2), p.B), cluster, CP_THREADS, 0, stream, p);
+}
+
+cudaError_t evict_select_prepare() {
+  return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_CACHE * 4);
+}
+
+cudaError_t launch_evict_select(SelectParams p, int sms, cudaStream_t stream) {
+  // CTAs per row: spread the rows over the GPU, but at least 4096 tokens each
+  const long long rows = (long long)p.B * p.Hkv;
+  int cluster = 1;
+  while (cluster < SEL_MAX_CLUSTER && rows * cluster * 2 <= sms && p.max_seq_len > 4096 * cluster) cluster *= 2;
+  const long long part = ((long long)p.max_seq_len + cluster * SEL_WARPS - 1) / (cluster * SEL_WARPS);
+  const long long keys = (part + 31) / 32 * 32 * SEL_WARPS;
+  p.cache_keys = keys <= SEL_CACHE ? (int)keys : 0;
+  return launch_cluster(evict_select_kernel, dim3(cluster, p.Hkv, p.B), cluster, SEL_THREADS, (size_t)p.cache_keys * 4,
+                        stream, p);
+}
+
+}  // namespace vqkv

@@ -97,6 +97,36 @@ cudaError_t launch_decode_fp16(const DecodeParams& p, dim3 grid, cudaStream_t st
 vqkv_status decode_validate(const vqkv_decode_args* a);   // every check of vqkv_decode_attn
 size_t decode_ticket_region_bytes(int B, int Hkv);       // error word + tickets, bytes
 
+// Cache editing (cache_edit.cu): the in-place move of chosen tokens, and the
+// choice of the tokens a sequence keeps.
+struct CompactParams {
+  uint8_t* codes[2];        // [B][Hkv][stream_bytes] K, V, or their pools
+  const int32_t* seq_lens;  // [B]
+  const int32_t* src;       // [B][src_heads][n_src]
+  const int32_t* counts;    // [B]
+  const int32_t* start;     // [B] or nullptr
+  float* mass;              // [B][Hkv][cap_len] or nullptr
+  unsigned* err;
+  long long stream_bytes;
+  int B, Hkv, src_heads, n_src, cap_len;
+  // Paged cache: block table or nullptr.
+  const int32_t* block_table = nullptr;
+  int max_blocks = 0, block_tiles = 0, block_shift = 0, num_blocks = 0;   // block_tiles = 1 << block_shift
+  long long block_bytes = 0;
+};
+struct SelectParams {
+  const float* mass;        // [B][Hkv][cap_len]
+  const int32_t* seq_lens;  // [B]
+  int32_t* keep;            // [B][Hkv][n_keep]
+  int32_t* keep_lens;       // [B]
+  unsigned* err;
+  int B, Hkv, cap_len, max_seq_len, n_keep, n_sink, n_recent;
+  int cache_keys = 0;       // keys of a CTA's part that fit in its shared memory (0: read again per pass)
+};
+cudaError_t launch_compact(int mode, const CompactParams& p, int sms, cudaStream_t stream);
+cudaError_t evict_select_prepare();   // set smem attributes (once per device)
+cudaError_t launch_evict_select(SelectParams p, int sms, cudaStream_t stream);
+
 // Encode kernels (encode.cu).
 cudaError_t encode_prepare(int mode);
 cudaError_t encode_occupancy(int mode, int* blocks_per_sm);
