@@ -317,6 +317,38 @@ vqkv_status vqkv_encode_paged(const vqkv_encode_args* args, const vqkv_paging* p
 vqkv_status vqkv_decode_attn_paged(const vqkv_decode_args* args, const vqkv_paging* paging, void* stream);
 
 /*
+ * vqkv_decode_attn_tree — attention of drafted tokens that form a tree (the
+ * verification step of speculative decoding with several continuations).
+ *
+ * The last M = n_queries tokens of each sequence are drafts, encoded at
+ * positions L - M .. L - 1 (L = seq_lens[b], clamped as in vqkv_decode_attn);
+ * decode.q and decode.out are fp16 [B][M][Hq][128].  Query m of sequence b
+ * sees every cached token t < L - M and the drafts that its mask names:
+ * token L - M + j for each set bit j < M of tree_mask[b * M + m] (its
+ * ancestors and, normally, itself; bits at or above M are ignored, and so is
+ * a bit whose token lies before position 0).  A query that sees nothing is a
+ * zero row.  A sequence with fewer drafts than M leaves the last draft
+ * positions unused: no mask names them, and the rows of those queries carry
+ * whatever their own masks select.
+ *
+ * M <= 64 with any group Hq / Hkv <= 8 (up to 512 softmax columns per KV
+ * head).  paging: NULL for the contiguous cache, else the block pools of the
+ * paged calls above.  The workspace holds
+ * vqkv_decode_tree_workspace_bytes(args) bytes; everything else is as in
+ * vqkv_decode_attn.  q' and the softmax weights are rounded to fp16 for the
+ * tensor cores, sums and softmax statistics are fp32.
+ */
+typedef struct {
+  vqkv_decode_args decode;    /* q, out: [B][n_queries][Hq][128]; num_splits: 0 = automatic */
+  int32_t n_queries;          /* M, 1..64 */
+  const uint64_t* tree_mask;  /* device [B][M], 8-byte aligned */
+} vqkv_decode_tree_args;
+
+/* Workspace bytes (sizes only, as vqkv_decode_workspace_bytes; also reads n_queries). */
+size_t vqkv_decode_tree_workspace_bytes(const vqkv_decode_tree_args* args);
+vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* args, const vqkv_paging* paging, void* stream);
+
+/*
  * vqkv_evict_select — which tokens each (sequence, KV head) keeps when its
  * cache is cut to n_keep tokens.
  *

@@ -17,6 +17,9 @@ VQKV_MODE_VQ15 = 1
 VQKV_MODE_VQ4 = 2
 VQKV_MODE_VQ3 = 3
 VQKV_MODE_VQ125 = 4
+# codebook entries and channels per code of each mode (include/vqkv.h)
+CODEBOOK_SHAPE = {VQKV_MODE_VQ2: (256, 4), VQKV_MODE_VQ15: (4096, 8), VQKV_MODE_VQ4: (256, 2), VQKV_MODE_VQ3: (4096, 4),
+                  VQKV_MODE_VQ125: (1024, 8)}
 VQKV_ROLE_K = 0
 VQKV_ROLE_V = 1
 VQKV_DEVERR_SEQ_LEN = 0x1
@@ -33,7 +36,7 @@ EXPORTED = ["vqkv_code_bytes", "vqkv_decode_workspace_bytes", "vqkv_decode_num_s
             "vqkv_fp16_decode_workspace_bytes", "vqkv_decode_attn_fp16", "vqkv_smoothing", "vqkv_calib_transform",
             "vqkv_kmeans_workspace_bytes", "vqkv_kmeans", "vqkv_kmeans_seed", "vqkv_kmeans_assign",
             "vqkv_kmeans_update_workspace_bytes", "vqkv_kmeans_update", "vqkv_status_string",
-            "vqkv_evict_select", "vqkv_cache_compact"]
+            "vqkv_evict_select", "vqkv_cache_compact", "vqkv_decode_tree_workspace_bytes", "vqkv_decode_attn_tree"]
 STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -89,6 +92,10 @@ class KmeansArgs(ctypes.Structure):
 class DecodeAppendArgs(ctypes.Structure):
     _fields_ = [("decode", DecodeArgs), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
                 ("near_tie_count", ctypes.c_void_p)]
+
+
+class DecodeTreeArgs(ctypes.Structure):
+    _fields_ = [("decode", DecodeArgs), ("n_queries", ctypes.c_int32), ("tree_mask", ctypes.c_void_p)]
 
 
 class EvictSelectArgs(ctypes.Structure):
@@ -173,6 +180,10 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.vqkv_kmeans_update.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                          ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_size_t, ctypes.c_void_p]
+        L.vqkv_decode_tree_workspace_bytes.restype = ctypes.c_size_t
+        L.vqkv_decode_tree_workspace_bytes.argtypes = [ctypes.POINTER(DecodeTreeArgs)]
+        L.vqkv_decode_attn_tree.restype = ctypes.c_int
+        L.vqkv_decode_attn_tree.argtypes = [ctypes.POINTER(DecodeTreeArgs), ctypes.POINTER(Paging), ctypes.c_void_p]
         L.vqkv_evict_select.restype = ctypes.c_int
         L.vqkv_evict_select.argtypes = [ctypes.POINTER(EvictSelectArgs), ctypes.c_void_p]
         L.vqkv_cache_compact.restype = ctypes.c_int
@@ -384,7 +395,7 @@ def fp16_decode_workspace(B, Hq, Hkv, cap_len, max_seq_len, num_splits=0, device
     return torch.zeros((n + 255) // 256 * 256, dtype=torch.uint8, device=device)
 
 
-# ---------------------------------------------------------------- editing a cache
+# ---------------------------------------------------------------- drafts and a changing cache
 
 def _need(what, dtype, *tensors) -> None:
     """Raises unless every given tensor (None is skipped) is a contiguous ``dtype`` tensor on the current device."""
@@ -416,6 +427,71 @@ def _need_cache(what, mode, B, Hkv, cap_len, k_codes, v_codes, block_table, bloc
             raise ValueError(f"{what}: block_table must have shape ({B}, max_blocks)")
     _need_shape(what, "k_codes", k_codes, *shape)
     _need_shape(what, "v_codes", v_codes, *shape)
+
+
+def _new_workspace(nbytes, what, device):
+    import torch
+    if nbytes == 0:
+        raise VqkvError(1, what)
+    return torch.zeros((nbytes + 255) // 256 * 256, dtype=torch.uint8, device=device)
+
+
+def _multi_decode_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace, cap_len,
+                       max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks) -> DecodeArgs:
+    """Checked arguments of a call with q, out [B][M][Hq][128]."""
+    import torch
+    _need(what, torch.float16, ("q", q), ("k_codebook", k_codebook), ("v_codebook", v_codebook), ("out", out))
+    _need(what, torch.uint8, ("k_codes", k_codes), ("v_codes", v_codes), ("workspace", workspace))
+    _need(what, torch.int32, ("seq_lens", seq_lens), ("block_table", block_table))
+    _need(what, torch.float32, ("s", s))
+    B, M, Hq, D = q.shape
+    Hkv = k_codebook.shape[0]
+    _need_cache(what, mode, B, Hkv, cap_len, k_codes, v_codes, block_table, block_tokens, num_blocks)
+    _need_shape(what, "out", out, B, M, Hq, D)
+    _need_shape(what, "seq_lens", seq_lens, B)
+    _need_shape(what, "s", s, Hkv, D)
+    if mode in CODEBOOK_SHAPE:   # the C entry refuses other modes
+        _need_shape(what, "k_codebook", k_codebook, Hkv, *CODEBOOK_SHAPE[mode])
+        _need_shape(what, "v_codebook", v_codebook, Hkv, *CODEBOOK_SHAPE[mode])
+    return DecodeArgs(mode=mode, B=B, Hq=Hq, Hkv=Hkv, head_dim=D, cap_len=cap_len, max_seq_len=max_seq_len,
+                      q=_ptr(q), k_codes=_ptr(k_codes), v_codes=_ptr(v_codes), seq_lens=_ptr(seq_lens),
+                      k_codebook=_ptr(k_codebook), v_codebook=_ptr(v_codebook), s=_ptr(s),
+                      softmax_scale=softmax_scale, num_splits=num_splits, workspace=_ptr(workspace),
+                      workspace_bytes=workspace.numel(), out=_ptr(out))
+
+
+def _size_args(mode, B, Hq, Hkv, cap_len, max_seq_len, num_splits) -> DecodeArgs:
+    return DecodeArgs(mode=mode, B=B, Hq=Hq, Hkv=Hkv, head_dim=128, cap_len=cap_len, max_seq_len=max_seq_len,
+                      num_splits=num_splits)
+
+
+def decode_tree_workspace(mode, B, Hq, Hkv, n_queries, cap_len, max_seq_len, num_splits=0, device="cuda"):
+    """A zero-filled workspace tensor of the size vqkv_decode_attn_tree needs."""
+    a = DecodeTreeArgs(decode=_size_args(mode, B, Hq, Hkv, cap_len, max_seq_len, num_splits), n_queries=n_queries)
+    return _new_workspace(int(lib().vqkv_decode_tree_workspace_bytes(ctypes.byref(a))),
+                          "vqkv_decode_tree_workspace_bytes", device)
+
+
+def vqkv_decode_attn_tree(mode, q, tree_mask, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace,
+                          cap_len, max_seq_len, softmax_scale=0.0, num_splits=0, block_table=None, block_tokens=0,
+                          num_blocks=0, stream=None) -> None:
+    """Attention of M <= 64 drafted tokens per sequence: q and out fp16 [B][M][Hq][128].
+
+    The drafts are the last M of the seq_lens[b] cached tokens; draft m sees
+    the tokens before them and draft j where bit j of tree_mask[b][m] (int64
+    [B][M]) is set.  k_codes / v_codes: [B][Hkv][bytes], or pools with
+    block_table.
+    """
+    import torch
+    what = "vqkv_decode_attn_tree"
+    _need(what, torch.int64, ("tree_mask", tree_mask))
+    d = _multi_decode_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace,
+                           cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks)
+    M = q.shape[1]
+    _need_shape(what, "tree_mask", tree_mask, d.B, M)
+    a = DecodeTreeArgs(decode=d, n_queries=M, tree_mask=_ptr(tree_mask))
+    pg = ctypes.byref(paging(block_table, block_tokens, num_blocks)) if block_table is not None else None
+    _check(lib().vqkv_decode_attn_tree(ctypes.byref(a), pg, _stream(stream)), what)
 
 
 def vqkv_evict_select(mass, seq_lens, keep, keep_lens, n_sink=0, n_recent=0, max_seq_len=None, error_flags=None,

@@ -35,7 +35,8 @@ vqkv_status device_info(DeviceInfo* out) {
   if (!d.ready) {
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return VQKV_ERR_NO_DEVICE;
     for (int m = 0; m < kCodeModes; ++m) {
-      if (decode_prepare(m) != cudaSuccess || encode_prepare(m) != cudaSuccess) return VQKV_ERR_CUDA;
+      if (decode_prepare(m) != cudaSuccess || encode_prepare(m) != cudaSuccess || decode_tree_prepare(m) != cudaSuccess)
+        return VQKV_ERR_CUDA;
       if (decode_occupancy(m, &d.decode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
       if (encode_occupancy(m, &d.encode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
       if (d.decode_bpsm[m] < 1) d.decode_bpsm[m] = 1;
@@ -229,6 +230,55 @@ vqkv_status validate_encode(const vqkv_encode_args* a) {
 
 PlanInput plan_input(const vqkv_decode_args* a) {
   return PlanInput{a->mode, a->B, a->Hq, a->Hkv, a->max_seq_len, a->num_splits};
+}
+
+// Draft-tree attention: split plan of one CTA per SM (its shared memory).
+struct TreePlan {
+  int n_splits = 1, tps = 1, cgroups = 1;
+  size_t ws_bytes = 0;
+};
+
+vqkv_status validate_tree_sizes(const vqkv_decode_tree_args* at) {
+  if (at == nullptr) return VQKV_ERR_INVALID_ARG;
+  const vqkv_status st = validate_decode_sizes(&at->decode);
+  if (st != VQKV_OK) return st;
+  if (at->n_queries < 1) return VQKV_ERR_INVALID_ARG;
+  if (at->n_queries > 64) return VQKV_ERR_UNSUPPORTED;   // one mask word per query
+  const int cg = (at->n_queries * (at->decode.Hq / at->decode.Hkv) + decode_tree_cols() - 1) / decode_tree_cols();
+  if ((long long)at->decode.B * cg > kMaxGridYZ || at->decode.Hkv > kMaxGridYZ || at->decode.cap_len > kMaxTokens)
+    return VQKV_ERR_UNSUPPORTED;
+  return VQKV_OK;
+}
+
+vqkv_status plan_tree(const vqkv_decode_tree_args* at, TreePlan* pl) {
+  DeviceInfo di;
+  const vqkv_status st = device_info(&di);
+  if (st != VQKV_OK) return st;
+  const vqkv_decode_args* a = &at->decode;
+  const int cols = at->n_queries * (a->Hq / a->Hkv);
+  pl->cgroups = (cols + decode_tree_cols() - 1) / decode_tree_cols();
+  const long long tiles = std::max(1, (a->max_seq_len + decode_tree_tile() - 1) / decode_tree_tile());
+  const long long pairs = (long long)std::max(a->B, 1) * a->Hkv * pl->cgroups;
+  long long best_n = 1;
+  if (a->num_splits > 0) {
+    best_n = std::min<long long>(a->num_splits, tiles);
+  } else {
+    // fewest (waves of CTAs) x (tiles per CTA + the prologue's and epilogue's worth of tiles)
+    const double setup_tiles = 10.0;
+    double best = 1e300;
+    const long long hi = std::min<long long>(tiles, 4 * ((di.sms + pairs - 1) / pairs) + 8);
+    for (long long n = 1; n <= hi; ++n) {
+      const double cost = (double)((pairs * n + di.sms - 1) / di.sms) * ((double)((tiles + n - 1) / n) + setup_tiles);
+      if (cost < best - 1e-9) best = cost, best_n = n;
+    }
+  }
+  const long long tps = (tiles + best_n - 1) / best_n;
+  pl->tps = (int)tps;
+  pl->n_splits = (int)((tiles + tps - 1) / tps);
+  pl->ws_bytes = kWsHeader;
+  if (pl->n_splits > 1)
+    pl->ws_bytes += sizeof(float) * (size_t)std::max(a->B, 1) * a->Hkv * pl->n_splits * cols * kPartialStride;
+  return VQKV_OK;
 }
 
 vqkv_status validate_fp16(const vqkv_fp16_decode_args* a, bool sizes_only) {
@@ -526,6 +576,66 @@ vqkv_status vqkv_decode_attn_fp16(const vqkv_fp16_decode_args* a, void* stream) 
   if (launch_decode_fp16(p, grid, static_cast<cudaStream_t>(stream)) != cudaSuccess) return VQKV_ERR_CUDA;
   if (p.defer_merge && p.n_splits > 1 && launch_combine(p, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return VQKV_ERR_CUDA;
+  return VQKV_OK;
+}
+
+size_t vqkv_decode_tree_workspace_bytes(const vqkv_decode_tree_args* a) {
+  TreePlan pl;
+  if (validate_tree_sizes(a) != VQKV_OK || plan_tree(a, &pl) != VQKV_OK) return 0;
+  return pl.ws_bytes;
+}
+
+vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_paging* pg, void* stream) {
+  vqkv_status st = validate_tree_sizes(at);
+  if (st != VQKV_OK) return st;
+  const vqkv_decode_args* a = &at->decode;
+  st = validate_decode(a);
+  if (st != VQKV_OK) return st;
+  if (pg != nullptr) {
+    st = validate_paging(pg, a->mode, a->cap_len);
+    if (st != VQKV_OK) return st;
+    if (a->B > 0 && (!pg->block_table || !aligned(pg->block_table, 4))) return VQKV_ERR_INVALID_ARG;
+  }
+  if (a->B == 0) return VQKV_OK;
+  if (!at->tree_mask || !aligned(at->tree_mask, 8)) return VQKV_ERR_INVALID_ARG;
+  TreePlan pl;
+  st = plan_tree(at, &pl);
+  if (st != VQKV_OK) return st;
+  if (a->workspace == nullptr || a->workspace_bytes < pl.ws_bytes) return VQKV_ERR_WORKSPACE;
+  if (!aligned(a->workspace, 256)) return VQKV_ERR_INVALID_ARG;
+  unsigned char* ws = static_cast<unsigned char*>(a->workspace);
+  DecodeParams p{};
+  p.q = reinterpret_cast<const __half*>(a->q);
+  p.kc = a->k_codes;
+  p.vc = a->v_codes;
+  p.seq_lens = a->seq_lens;
+  p.kcb = reinterpret_cast<const __half*>(a->k_codebook);
+  p.vcb = reinterpret_cast<const __half*>(a->v_codebook);
+  p.s = a->s;
+  p.out = reinterpret_cast<__half*>(a->out);
+  p.err = reinterpret_cast<unsigned*>(ws);
+  p.partials = reinterpret_cast<float*>(ws + kWsHeader);
+  p.stream_bytes = (long long)vqkv_code_bytes(a->mode, a->cap_len);
+  p.B = a->B;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.g = a->Hq / a->Hkv;
+  p.M = at->n_queries;
+  p.ncols = p.M * p.g;
+  p.cgroups = pl.cgroups;
+  p.max_seq_len = a->max_seq_len;
+  p.n_splits = pl.n_splits;
+  p.tps = pl.tps;
+  p.bpg = 1;
+  p.defer_merge = 1;
+  const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt(128.0f);
+  p.qscale = scale * 1.4426950408889634f / std::sqrt(128.0f);
+  set_paging(p, pg, a->mode);
+  const dim3 grid(pl.n_splits, a->Hkv, a->B * pl.cgroups);
+  if (launch_decode_tree(a->mode, p, reinterpret_cast<const unsigned long long*>(at->tree_mask), grid,
+                         static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return VQKV_ERR_CUDA;
+  if (pl.n_splits > 1 && launch_combine(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return VQKV_ERR_CUDA;
   return VQKV_OK;
 }
 

@@ -46,6 +46,7 @@
 #include "common.cuh"
 #include "decode_common.cuh"
 #include "encode_common.cuh"
+#include "gather.cuh"
 #include "internal.h"
 
 namespace vqkv {
@@ -138,62 +139,9 @@ static_assert(CombineSmem<V2_WARPS>::kBytes <= V2Geo<VQKV_MODE_VQ2>::MBAR_OFF,
 constexpr size_t kV15Smem = 2 * V15_CB_BYTES + CombineSmem<V15_WARPS>::kBytes;
 static_assert(V15_Q_OFF + 8 * V15_Q_PITCH * 4 <= (int)kV15Smem, "q' must fit in the combine area");
 
-// The lane's 4 channels of query column col0 + warp (query c / g, head
-// c % g) and their smoothing factors, for warps 0..nloc-1.
-struct QueryLoad {
-  uint2 q;
-  float4 s;
-};
-__device__ __forceinline__ QueryLoad load_query(const DecodeParams& p, int b, int kvh, int warp, int lane, int col0,
-                                                int nloc) {
-  QueryLoad r{make_uint2(0u, 0u), make_float4(0.f, 0.f, 0.f, 0.f)};
-  if (warp < nloc) {
-    const int c = col0 + warp;
-    const int m = c / p.g, hq = kvh * p.g + c - m * p.g;
-    r.q = *reinterpret_cast<const uint2*>(p.q + (((size_t)b * p.M + m) * p.Hq + hq) * kHeadDim + 4 * lane);
-    r.s = *reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 4 * lane);
-  }
-  return r;
-}
-
-// q' of the CTA's softmax column col0 + warp into row `warp` of s_qp (fp32,
-// scaled, rows `pitch` floats apart), by warps 0..nloc-1.
-__device__ __forceinline__ void transform_query(const DecodeParams& p, const QueryLoad& r, int warp, int lane,
-                                                float* s_qp, int pitch, int nloc) {
-  if (warp < nloc) {
-    const __half2 q01 = *reinterpret_cast<const __half2*>(&r.q.x);
-    const __half2 q23 = *reinterpret_cast<const __half2*>(&r.q.y);
-    float v[4] = {__low2float(q01) * r.s.x, __high2float(q01) * r.s.y, __low2float(q23) * r.s.z,
-                  __high2float(q23) * r.s.w};
-    fwht128_f32(v, lane);
-    float4 o = make_float4(v[0] * p.qscale, v[1] * p.qscale, v[2] * p.qscale, v[3] * p.qscale);
-    *reinterpret_cast<float4*>(s_qp + warp * pitch + 4 * lane) = o;
-  }
-}
-
 __device__ __forceinline__ void transform_queries(const DecodeParams& p, int b, int kvh, int warp,
                                                   int lane, float* s_qp, int pitch, int col0, int nloc) {
   transform_query(p, load_query(p, b, kvh, warp, lane, col0, nloc), warp, lane, s_qp, pitch, nloc);
-}
-
-// Shared-memory offset of a gathered centroid: one byte permute puts code
-// byte K of `codes` into bits 8..15 and the lane's replica offset (byte 0 of
-// `lane_byte`) into bits 0..7: (code << 8) | replica offset.
-template <int K>
-__device__ __forceinline__ uint32_t cb_offset(uint32_t codes, uint32_t lane_byte) {
-  return __byte_perm(codes, lane_byte, 0x5504 | (K << 4));
-}
-
-template <typename T>
-__device__ __forceinline__ T lds_at(const unsigned char* base, uint32_t off) {
-  return *reinterpret_cast<const T*>(base + off);
-}
-
-// 24-bit code pair at byte b (a multiple of 3) of a lane's run of words.
-template <int LW>
-__device__ __forceinline__ uint32_t pair_at(const uint32_t (&w)[LW], int b) {
-  const int i = b >> 2, sh = (b & 3) * 8;
-  return (sh <= 8 ? (w[i] >> sh) : __funnelshift_r(w[i], w[i + 1], sh)) & 0xffffffu;
 }
 
 // One step of the tile-ring decode over T consecutive 16-token tiles.
@@ -317,19 +265,6 @@ __device__ __forceinline__ void vq2_step(const unsigned char* s_cb, uint32_t kby
     }
   }
 }
-
-// 10-bit code at bit b of a lane's run words (b is a constant after
-// unrolling, so the word indices are too).
-template <int N>
-__device__ __forceinline__ uint32_t bits10(const uint32_t (&w)[N], int b) {
-  const int i = b >> 5, sh = b & 31;
-  return (i + 1 < N ? __funnelshift_r(w[i], w[i + 1], sh) : w[i] >> sh) & 0x3ffu;
-}
-
-// Byte offset of centroid c in copy `rep` of a 1024-entry codebook whose four
-// copies are interleaved in 128-byte rows: copy r holds its even / odd
-// entries in 16-byte bank groups 2r / 2r+1.
-__device__ __forceinline__ uint32_t cb10_offset(uint32_t c) { return ((c >> 1) << 7) | ((c & 1u) << 4); }
 
 // One step of the 1.25-bit decode over T consecutive 16-token tiles.
 // Scores: a 16-byte gather is channels 8j..8j+7 of subvector j = 4 s2 + tig
@@ -838,14 +773,6 @@ __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeP
     finish_sequence<V2_WARPS, GROUPS, Dim>(p, b, kvh, span, s_comb, &s_last);
     __syncthreads();   // (a warp that timed out still takes part in every barrier)
   }
-}
-
-// 24-bit code pair k (bytes 3k..3k+2) of a lane's 12-byte run (3 words).
-__device__ __forceinline__ uint32_t pair24(uint32_t w0, uint32_t w1, uint32_t w2, int k) {
-  if (k == 0) return w0 & 0xffffffu;
-  if (k == 1) return __funnelshift_r(w0, w1, 24) & 0xffffffu;
-  if (k == 2) return __funnelshift_r(w1, w2, 16) & 0xffffffu;
-  return w2 >> 8;
 }
 
 template <int Q, bool PAGED>

@@ -97,6 +97,16 @@ cudaError_t launch_decode_fp16(const DecodeParams& p, dim3 grid, cudaStream_t st
 vqkv_status decode_validate(const vqkv_decode_args* a);   // every check of vqkv_decode_attn
 size_t decode_ticket_region_bytes(int B, int Hkv);       // error word + tickets, bytes
 
+// Draft-tree attention (decode_tree.cu): partials as in the split plan,
+// [B][Hkv][n_splits][ncols], always merged by launch_combine (n_splits > 1);
+// grid (n_splits, Hkv, B x cgroups), cgroups groups of decode_tree_cols()
+// columns, splits of p.tps tiles of decode_tree_tile() tokens.
+int decode_tree_cols();
+int decode_tree_tile();
+cudaError_t decode_tree_prepare(int mode);
+cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, dim3 grid,
+                               cudaStream_t stream);
+
 // Cache editing (cache_edit.cu): the in-place move of chosen tokens, and the
 // choice of the tokens a sequence keeps.
 struct CompactParams {

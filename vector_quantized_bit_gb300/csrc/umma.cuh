@@ -3,7 +3,7 @@
 // accumulator in tensor memory, completion through an mbarrier, and loads
 // of the accumulator into registers.
 //
-// Operand layout used by every caller: K-major, no swizzle.  A matrix of R
+// Operand layout of the encoder: K-major, no swizzle.  A matrix of R
 // rows x 16 fp16 (one MMA's K) is stored as 8-row x 16-byte core matrices:
 // element (row r, k) at byte (r / 8) * 256 + (k / 8) * 128 + (r % 8) * 16 +
 // (k % 8) * 2, i.e. the two K core matrices of an 8-row group are adjacent
@@ -31,6 +31,21 @@ __device__ __forceinline__ uint64_t umma_desc_kmajor(uint32_t saddr) {
   return d;
 }
 
+// Shared-memory matrix descriptor of a tile whose rows are 128 bytes with the
+// 128-byte swizzle (the 16-byte pieces of row r permuted by xor with r % 8),
+// starting at shared address `saddr`: layout type 2, 8-row groups `sbo` bytes
+// apart.  K-major operand: a row is 64 fp16 of K, `lbo` is unused.  MN-major
+// operand: a row is 64 fp16 of M or N at one k, the next 64 are `lbo` bytes on.
+__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t saddr, uint32_t sbo, uint32_t lbo) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(lbo >> 4) << 16;
+  d |= (uint64_t)(sbo >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+constexpr uint32_t kIdescBMnMajor = 1u << 16;   // B is MN-major
+
 // Instruction descriptor of kind::f16 with fp16 A and B (both K-major) and
 // an fp32 accumulator, shape M x N (M = 64 or 128, N a multiple of 16 up to
 // 256).
@@ -55,6 +70,16 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] . B[desc]^T, issued by one thread: A holds row m in
+// lane m, two consecutive k per 32-bit column.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -91,6 +116,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+
+// Writes 32 consecutive 32-bit columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // tmem_ld32 that also returns min over the 32 columns (NaN ignored, as by
 // min.f32); m must be +inf on entry.  The minimum, like the values, is valid
