@@ -349,6 +349,35 @@ size_t vqkv_decode_tree_workspace_bytes(const vqkv_decode_tree_args* args);
 vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* args, const vqkv_paging* paging, void* stream);
 
 /*
+ * vqkv_decode_attn_mass — decode attention that also accumulates the
+ * attention weight each cached token receives, the measure by which
+ * vqkv_evict_select chooses what a sequence keeps.
+ *
+ * decode.q / decode.out are fp16 [B][M][Hq][128]; O is what
+ * vqkv_decode_attn_multi returns for the same arguments (M = 1: what
+ * vqkv_decode_attn returns), up to rounding.  In addition, for every
+ * sequence b, KV head h and t < L,
+ *     mass[b][h][t] += sum over the M queries and the Hq / Hkv query heads
+ *                      of KV head h of softmax(score)_t.
+ * Entries t >= L are not touched.  The scores are computed from q' split into
+ * two fp16 parts, so the added weights carry fp32 accuracy.  Each entry is
+ * summed by one thread in a fixed order: the result does not depend on
+ * scheduling.
+ *
+ * M * (Hq / Hkv) <= 64.  paging as in vqkv_decode_attn_tree (mass is indexed
+ * by logical position).  The workspace (vqkv_decode_mass_workspace_bytes) also
+ * holds the call's scores, 16 bytes per token and KV head for every 4 columns.
+ */
+typedef struct {
+  vqkv_decode_args decode;    /* q, out: [B][n_queries][Hq][128] */
+  int32_t n_queries;          /* M >= 1 */
+  float* mass;                /* device fp32 [B][Hkv][cap_len], 4-byte aligned, accumulated into */
+} vqkv_decode_mass_args;
+
+size_t vqkv_decode_mass_workspace_bytes(const vqkv_decode_mass_args* args);
+vqkv_status vqkv_decode_attn_mass(const vqkv_decode_mass_args* args, const vqkv_paging* paging, void* stream);
+
+/*
  * vqkv_evict_select — which tokens each (sequence, KV head) keeps when its
  * cache is cut to n_keep tokens.
  *

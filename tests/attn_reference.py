@@ -20,7 +20,9 @@ def attend(q, kc, vc, kcb, vcb, s, lens, visible, scale=None):
 
     Returns O fp64 [B][M][Hq][128], the weights summed over queries and heads
     [b][h] -> fp64 [L], and a bound on |dO| of fp16-rounded q' and P (below).
+    attend.score_size is the largest scale * sum |q'_c K'_tc| seen.
     """
+    attend.score_size = 0.0
     B, M, Hq, D = q.shape
     Hkv = kcb.shape[0]
     g = Hq // Hkv
@@ -49,7 +51,9 @@ def attend(q, kc, vc, kcb, vcb, s, lens, visible, scale=None):
                 # an unrounded sum) by another 2^-11.  dO = sum dp (v - o) + o sum dp, and the
                 # result is rounded to fp16 once more.  fp32 sums add a few 2^-20 at these lengths.
                 qr = vo.transform_query(qh, s[h])
-                e = HALF_STEP * scale * (np.abs(qr) @ np.abs(kr[see]).T).max(axis=1) + 2.0 ** -18
+                size = scale * (np.abs(qr) @ np.abs(kr[see]).T).max(axis=1)
+                attend.score_size = max(attend.score_size, float(size.max()))
+                e = HALF_STEP * size + 2.0 ** -18
                 spread = np.einsum("ht,td->hd", p[:, see], np.abs(v[see]))
                 rel = (np.exp(2 * e) - 1 + HALF_STEP + 2.0 ** -16)[:, None]
                 tol[b, m, h * g:(h + 1) * g] = rel * (spread + np.abs(o)) + HALF_STEP * np.abs(o) * (1 + rel) + 2.0 ** -24
@@ -65,3 +69,26 @@ def check_output(got, ref, tol):
     assert (d <= tol).all(), (float((d - tol).max()), np.unravel_index(int((d - tol).argmax()), d.shape))
     if np.linalg.norm(ref) > 0:
         assert np.linalg.norm(d) <= 2e-3 * np.linalg.norm(ref), np.linalg.norm(d) / np.linalg.norm(ref)
+
+
+def check_mass(got, before, ref, lens, score_size):
+    """Accumulated weights against before + the fp64 weights.
+
+    Scores carry fp32 accuracy: q' = hi + lo to 2^-22, its transform 10
+    roundings of 2^-24, the tensor-core sum of 128 products in fp32 up to 40
+    steps of 2^-23; together under 2^-17 of scale * sum |q' K'| = score_size.
+    A normalised weight moves by at most twice that, plus exp2, the sum l, its
+    reciprocal and the sum over columns (under 2^-17 in all), and the
+    addition to the old value rounds once.  Rounding errors average out, so
+    the 2-norm holds at 1e-5.
+    """
+    rel = 2 * 2.0 ** -17 * score_size + 2.0 ** -17
+    for b in range(got.shape[0]):
+        L = int(lens[b])
+        for h in range(got.shape[1]):
+            want = before[b, h, :L].astype(np.float64) + ref[b][h]
+            d = np.abs(got[b, h, :L] - want)
+            assert (d <= rel * ref[b][h] + 2.0 ** -23 * np.abs(want) + 1e-37).all(), (b, h, float(d.max()))
+            if L:
+                assert np.linalg.norm(d) <= 1e-5 * np.linalg.norm(want)
+            assert np.array_equal(got[b, h, L:], before[b, h, L:])

@@ -47,6 +47,27 @@ def test_tree_empty_and_null(lib):
     assert lib.vqkv_decode_tree_workspace_bytes(None) == 0
 
 
+def _mass(n_queries=2, mass=0xa000, **kw):
+    return _lib.DecodeMassArgs(decode=_dec(**kw), n_queries=n_queries, mass=mass)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n_queries=0), 1), (dict(n_queries=17), 2), (dict(n_queries=2**31 - 1), 2), (dict(mass=None), 1),
+    (dict(mass=0xa002), 1), (dict(mode=7), 2), (dict(head_dim=64), 2), (dict(max_seq_len=65), 1), (dict(q=None), 1),
+    (dict(v_codes=0x3008), 1), (dict(B=65536), 2), (dict(cap_len=2**30 + 1), 2),
+])
+def test_mass_validation(lib, kw, status):
+    assert lib.vqkv_decode_attn_mass(ctypes.byref(_mass(**kw)), None, None) == status
+    if not set(kw) & {"mass", "q", "v_codes"}:
+        assert lib.vqkv_decode_mass_workspace_bytes(ctypes.byref(_mass(**kw))) == 0
+
+
+def test_mass_empty_and_null(lib):
+    assert lib.vqkv_decode_attn_mass(ctypes.byref(_mass(B=0, q=None, mass=None)), None, None) == 0
+    assert lib.vqkv_decode_attn_mass(None, None, None) == 1
+    assert lib.vqkv_decode_mass_workspace_bytes(None) == 0
+
+
 @pytest.mark.parametrize("kw", [dict(block_tokens=100), dict(max_blocks=0), dict(num_blocks=0), dict(max_blocks=1),
                                 dict(block_table=None), dict(block_table=0x9002)])
 def test_paging_validation(lib, kw):
@@ -54,10 +75,11 @@ def test_paging_validation(lib, kw):
     for k, v in kw.items():
         setattr(pg, k, v)
     assert lib.vqkv_decode_attn_tree(ctypes.byref(_tree(cap_len=128, max_seq_len=128)), ctypes.byref(pg), None) == 1
+    assert lib.vqkv_decode_attn_mass(ctypes.byref(_mass(cap_len=128, max_seq_len=128)), ctypes.byref(pg), None) == 1
 
 
 def test_struct_layout_matches_header(tmp_path):
-    fields = {"vqkv_decode_tree_args": _lib.DecodeTreeArgs}
+    fields = {"vqkv_decode_tree_args": _lib.DecodeTreeArgs, "vqkv_decode_mass_args": _lib.DecodeMassArgs}
     lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "vqkv.h"', "int main(void){"]
     for cname, cls in fields.items():
         lines.append(f'printf("{cname} %zu\\n", sizeof({cname}));')

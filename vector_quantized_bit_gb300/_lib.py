@@ -36,7 +36,8 @@ EXPORTED = ["vqkv_code_bytes", "vqkv_decode_workspace_bytes", "vqkv_decode_num_s
             "vqkv_fp16_decode_workspace_bytes", "vqkv_decode_attn_fp16", "vqkv_smoothing", "vqkv_calib_transform",
             "vqkv_kmeans_workspace_bytes", "vqkv_kmeans", "vqkv_kmeans_seed", "vqkv_kmeans_assign",
             "vqkv_kmeans_update_workspace_bytes", "vqkv_kmeans_update", "vqkv_status_string",
-            "vqkv_evict_select", "vqkv_cache_compact", "vqkv_decode_tree_workspace_bytes", "vqkv_decode_attn_tree"]
+            "vqkv_evict_select", "vqkv_cache_compact", "vqkv_decode_tree_workspace_bytes", "vqkv_decode_attn_tree",
+            "vqkv_decode_mass_workspace_bytes", "vqkv_decode_attn_mass"]
 STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -96,6 +97,10 @@ class DecodeAppendArgs(ctypes.Structure):
 
 class DecodeTreeArgs(ctypes.Structure):
     _fields_ = [("decode", DecodeArgs), ("n_queries", ctypes.c_int32), ("tree_mask", ctypes.c_void_p)]
+
+
+class DecodeMassArgs(ctypes.Structure):
+    _fields_ = [("decode", DecodeArgs), ("n_queries", ctypes.c_int32), ("mass", ctypes.c_void_p)]
 
 
 class EvictSelectArgs(ctypes.Structure):
@@ -184,6 +189,10 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.vqkv_decode_tree_workspace_bytes.argtypes = [ctypes.POINTER(DecodeTreeArgs)]
         L.vqkv_decode_attn_tree.restype = ctypes.c_int
         L.vqkv_decode_attn_tree.argtypes = [ctypes.POINTER(DecodeTreeArgs), ctypes.POINTER(Paging), ctypes.c_void_p]
+        L.vqkv_decode_mass_workspace_bytes.restype = ctypes.c_size_t
+        L.vqkv_decode_mass_workspace_bytes.argtypes = [ctypes.POINTER(DecodeMassArgs)]
+        L.vqkv_decode_attn_mass.restype = ctypes.c_int
+        L.vqkv_decode_attn_mass.argtypes = [ctypes.POINTER(DecodeMassArgs), ctypes.POINTER(Paging), ctypes.c_void_p]
         L.vqkv_evict_select.restype = ctypes.c_int
         L.vqkv_evict_select.argtypes = [ctypes.POINTER(EvictSelectArgs), ctypes.c_void_p]
         L.vqkv_cache_compact.restype = ctypes.c_int
@@ -492,6 +501,31 @@ def vqkv_decode_attn_tree(mode, q, tree_mask, k_codes, v_codes, seq_lens, k_code
     a = DecodeTreeArgs(decode=d, n_queries=M, tree_mask=_ptr(tree_mask))
     pg = ctypes.byref(paging(block_table, block_tokens, num_blocks)) if block_table is not None else None
     _check(lib().vqkv_decode_attn_tree(ctypes.byref(a), pg, _stream(stream)), what)
+
+
+def decode_mass_workspace(mode, B, Hq, Hkv, n_queries, cap_len, max_seq_len, num_splits=0, device="cuda"):
+    """A zero-filled workspace tensor of the size vqkv_decode_attn_mass needs."""
+    a = DecodeMassArgs(decode=_size_args(mode, B, Hq, Hkv, cap_len, max_seq_len, num_splits), n_queries=n_queries)
+    return _new_workspace(int(lib().vqkv_decode_mass_workspace_bytes(ctypes.byref(a))),
+                          "vqkv_decode_mass_workspace_bytes", device)
+
+
+def vqkv_decode_attn_mass(mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, mass, workspace, cap_len,
+                          max_seq_len, softmax_scale=0.0, num_splits=0, block_table=None, block_tokens=0, num_blocks=0,
+                          stream=None) -> None:
+    """Decode attention (q, out fp16 [B][M][Hq][128], causal as in
+    vqkv_decode_attn_multi) that adds each cached token's attention weight,
+    summed over the M queries and the heads of its KV head, to mass (fp32
+    [B][Hkv][cap_len])."""
+    import torch
+    what = "vqkv_decode_attn_mass"
+    _need(what, torch.float32, ("mass", mass))
+    d = _multi_decode_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace,
+                           cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks)
+    _need_shape(what, "mass", mass, d.B, d.Hkv, cap_len)
+    a = DecodeMassArgs(decode=d, n_queries=q.shape[1], mass=_ptr(mass))
+    pg = ctypes.byref(paging(block_table, block_tokens, num_blocks)) if block_table is not None else None
+    _check(lib().vqkv_decode_attn_mass(ctypes.byref(a), pg, _stream(stream)), what)
 
 
 def vqkv_evict_select(mass, seq_lens, keep, keep_lens, n_sink=0, n_recent=0, max_seq_len=None, error_flags=None,

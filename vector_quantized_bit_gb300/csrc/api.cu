@@ -35,7 +35,8 @@ vqkv_status device_info(DeviceInfo* out) {
   if (!d.ready) {
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return VQKV_ERR_NO_DEVICE;
     for (int m = 0; m < kCodeModes; ++m) {
-      if (decode_prepare(m) != cudaSuccess || encode_prepare(m) != cudaSuccess || decode_tree_prepare(m) != cudaSuccess)
+      if (decode_prepare(m) != cudaSuccess || encode_prepare(m) != cudaSuccess || decode_tree_prepare(m) != cudaSuccess ||
+          decode_mass_prepare(m) != cudaSuccess)
         return VQKV_ERR_CUDA;
       if (decode_occupancy(m, &d.decode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
       if (encode_occupancy(m, &d.encode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
@@ -138,6 +139,7 @@ struct PlanInput {
   // every CTA of the plan runs at once, the splits are sized for
   // max_seq_len + credit_tiles, so that split comes out this much shorter.
   int credit_tiles = 0;
+  int width = 8;   // softmax columns per CTA
 };
 
 vqkv_status plan_decode(const PlanInput* a, DecodePlan* pl) {
@@ -154,7 +156,7 @@ vqkv_status plan_decode(const PlanInput* a, DecodePlan* pl) {
   // across sequences only when the batch alone cannot fill the GPU.
   int bpg = 1;
   if (a->mode == VQKV_MODE_VQ15 && (long long)B * a->Hkv < slots) bpg = B;
-  const int cgroups = (g * a->M + 7) / 8;   // CTAs per (sequence group, KV head, split)
+  const int cgroups = (g * a->M + a->width - 1) / a->width;   // CTAs per (sequence group, KV head, split)
   // Flat plan for batches on the tile-ring decode: one wave of CTAs per (KV
   // head, column group), each taking an equal share of all sequences' tiles,
   // balanced by the actual lengths on the device (ragged batches leave no CTA
@@ -230,6 +232,69 @@ vqkv_status validate_encode(const vqkv_encode_args* a) {
 
 PlanInput plan_input(const vqkv_decode_args* a) {
   return PlanInput{a->mode, a->B, a->Hq, a->Hkv, a->max_seq_len, a->num_splits};
+}
+
+// The fields of a decode over packed codes that do not depend on its plan.
+DecodeParams packed_params(const vqkv_decode_args* a, int M, const vqkv_paging* pg) {
+  DecodeParams p{};
+  p.q = reinterpret_cast<const __half*>(a->q);
+  p.kc = a->k_codes;
+  p.vc = a->v_codes;
+  p.seq_lens = a->seq_lens;
+  p.kcb = reinterpret_cast<const __half*>(a->k_codebook);
+  p.vcb = reinterpret_cast<const __half*>(a->v_codebook);
+  p.s = a->s;
+  p.out = reinterpret_cast<__half*>(a->out);
+  p.err = static_cast<unsigned*>(a->workspace);
+  p.stream_bytes = (long long)vqkv_code_bytes(a->mode, a->cap_len);
+  p.B = a->B;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.g = a->Hq / a->Hkv;
+  p.M = M;
+  p.ncols = M * p.g;
+  p.max_seq_len = a->max_seq_len;
+  const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt(128.0f);
+  p.qscale = scale * 1.4426950408889634f / std::sqrt(128.0f);
+  set_paging(p, pg, a->mode);
+  return p;
+}
+
+// Decode with attention weights: the decode's plan at 4 columns per CTA, then
+// the columns' statistics and the scores behind its workspace.
+struct MassPlan {
+  DecodePlan d;
+  size_t stats_off = 0, scores_off = 0, ws_bytes = 0;
+  int score_row = 0;
+};
+
+vqkv_status validate_mass_sizes(const vqkv_decode_mass_args* am) {
+  if (am == nullptr) return VQKV_ERR_INVALID_ARG;
+  const vqkv_status st = validate_decode_sizes(&am->decode);
+  if (st != VQKV_OK) return st;
+  const vqkv_decode_args& a = am->decode;
+  if (am->n_queries < 1) return VQKV_ERR_INVALID_ARG;
+  if (am->n_queries > 64 || am->n_queries * (a.Hq / a.Hkv) > 64) return VQKV_ERR_UNSUPPORTED;
+  const int cg = (am->n_queries * (a.Hq / a.Hkv) + 3) / 4;
+  if ((long long)a.B * cg > kMaxGridYZ || a.Hkv > kMaxGridYZ || a.cap_len > kMaxTokens) return VQKV_ERR_UNSUPPORTED;
+  return VQKV_OK;
+}
+
+vqkv_status plan_mass(const vqkv_decode_mass_args* am, MassPlan* pl) {
+  const vqkv_decode_args& a = am->decode;
+  PlanInput in = plan_input(&a);
+  in.M = am->n_queries;
+  in.width = 4;
+  const vqkv_status st = plan_decode(&in, &pl->d);
+  if (st != VQKV_OK) return st;
+  const size_t pairs = (size_t)std::max(a.B, 1) * a.Hkv;
+  const size_t cols = (size_t)am->n_queries * (a.Hq / a.Hkv);
+  // rows to the end of the last step: whole 16-token tiles, up to three of them
+  pl->score_row = (a.max_seq_len + 15) / 16 * 16 + 48;
+  pl->stats_off = round_up(pl->d.ws_bytes, 256);
+  pl->scores_off = round_up(pl->stats_off + pairs * cols * sizeof(float2), 256);
+  pl->ws_bytes = pl->scores_off + pairs * pl->d.cgroups * pl->score_row * 4 * sizeof(float);
+  return VQKV_OK;
 }
 
 // Draft-tree attention: split plan of one CTA per SM (its shared memory).
@@ -579,6 +644,49 @@ vqkv_status vqkv_decode_attn_fp16(const vqkv_fp16_decode_args* a, void* stream) 
   return VQKV_OK;
 }
 
+size_t vqkv_decode_mass_workspace_bytes(const vqkv_decode_mass_args* a) {
+  MassPlan pl;
+  if (validate_mass_sizes(a) != VQKV_OK || plan_mass(a, &pl) != VQKV_OK) return 0;
+  return pl.ws_bytes;
+}
+
+vqkv_status vqkv_decode_attn_mass(const vqkv_decode_mass_args* am, const vqkv_paging* pg, void* stream) {
+  vqkv_status st = validate_mass_sizes(am);
+  if (st != VQKV_OK) return st;
+  const vqkv_decode_args* a = &am->decode;
+  st = validate_decode(a);
+  if (st != VQKV_OK) return st;
+  if (pg != nullptr) {
+    st = validate_paging(pg, a->mode, a->cap_len);
+    if (st != VQKV_OK) return st;
+    if (a->B > 0 && (!pg->block_table || !aligned(pg->block_table, 4))) return VQKV_ERR_INVALID_ARG;
+  }
+  if (a->B == 0) return VQKV_OK;
+  if (!am->mass || !aligned(am->mass, 4)) return VQKV_ERR_INVALID_ARG;
+  MassPlan pl;
+  st = plan_mass(am, &pl);
+  if (st != VQKV_OK) return st;
+  if (a->workspace == nullptr || a->workspace_bytes < pl.ws_bytes) return VQKV_ERR_WORKSPACE;
+  if (!aligned(a->workspace, 256)) return VQKV_ERR_INVALID_ARG;
+  unsigned char* ws = static_cast<unsigned char*>(a->workspace);
+  DecodeParams p = packed_params(a, am->n_queries, pg);
+  p.tickets = reinterpret_cast<unsigned*>(ws + pl.d.tickets_off);
+  p.partials = reinterpret_cast<float*>(ws + pl.d.partials_off);
+  p.stats = reinterpret_cast<float2*>(ws + pl.stats_off);
+  p.scores = reinterpret_cast<float*>(ws + pl.scores_off);
+  p.score_row = pl.score_row;
+  p.mass = am->mass;
+  p.cap_len = a->cap_len;
+  p.n_splits = pl.d.n_splits;
+  p.tps = pl.d.tps;
+  p.bpg = pl.d.bpg;
+  p.defer_merge = pl.d.bpg > 1 ? 1 : 0;
+  p.flat = pl.d.flat;
+  p.cgroups = pl.d.cgroups;
+  const dim3 grid(pl.d.n_splits, a->Hkv, pl.d.n_bgroups * pl.d.cgroups);
+  return launch_decode_mass(a->mode, p, grid, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
+}
+
 size_t vqkv_decode_tree_workspace_bytes(const vqkv_decode_tree_args* a) {
   TreePlan pl;
   if (validate_tree_sizes(a) != VQKV_OK || plan_tree(a, &pl) != VQKV_OK) return 0;
@@ -604,33 +712,13 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_pa
   if (a->workspace == nullptr || a->workspace_bytes < pl.ws_bytes) return VQKV_ERR_WORKSPACE;
   if (!aligned(a->workspace, 256)) return VQKV_ERR_INVALID_ARG;
   unsigned char* ws = static_cast<unsigned char*>(a->workspace);
-  DecodeParams p{};
-  p.q = reinterpret_cast<const __half*>(a->q);
-  p.kc = a->k_codes;
-  p.vc = a->v_codes;
-  p.seq_lens = a->seq_lens;
-  p.kcb = reinterpret_cast<const __half*>(a->k_codebook);
-  p.vcb = reinterpret_cast<const __half*>(a->v_codebook);
-  p.s = a->s;
-  p.out = reinterpret_cast<__half*>(a->out);
-  p.err = reinterpret_cast<unsigned*>(ws);
+  DecodeParams p = packed_params(a, at->n_queries, pg);
   p.partials = reinterpret_cast<float*>(ws + kWsHeader);
-  p.stream_bytes = (long long)vqkv_code_bytes(a->mode, a->cap_len);
-  p.B = a->B;
-  p.Hq = a->Hq;
-  p.Hkv = a->Hkv;
-  p.g = a->Hq / a->Hkv;
-  p.M = at->n_queries;
-  p.ncols = p.M * p.g;
   p.cgroups = pl.cgroups;
-  p.max_seq_len = a->max_seq_len;
   p.n_splits = pl.n_splits;
   p.tps = pl.tps;
   p.bpg = 1;
   p.defer_merge = 1;
-  const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt(128.0f);
-  p.qscale = scale * 1.4426950408889634f / std::sqrt(128.0f);
-  set_paging(p, pg, a->mode);
   const dim3 grid(pl.n_splits, a->Hkv, a->B * pl.cgroups);
   if (launch_decode_tree(a->mode, p, reinterpret_cast<const unsigned long long*>(at->tree_mask), grid,
                          static_cast<cudaStream_t>(stream)) != cudaSuccess)

@@ -165,8 +165,11 @@ __device__ __forceinline__ void mask_scores(float (&sc)[4], int t0, const Column
 enum QueryLayout : int { kOneQuery = 0, kQueries = 1, kQueryGroups = 2 };
 
 // The CTA's columns: col0 .. col0 + nloc - 1 of the KV head's ncols
-// (column group blockIdx.z % cgroups).
-__device__ __forceinline__ int cta_col0(const DecodeParams& p) { return 8 * (int)(blockIdx.z % p.cgroups); }
+// (column group blockIdx.z % cgroups, of WIDTH columns).
+template <int WIDTH = 8>
+__device__ __forceinline__ int cta_col0(const DecodeParams& p) {
+  return WIDTH * (int)(blockIdx.z % p.cgroups);
+}
 __device__ __forceinline__ int cta_bgroup(const DecodeParams& p) { return (int)(blockIdx.z / p.cgroups); }
 
 // The CTAs that contribute to one (sequence, KV head, column group): this
@@ -185,8 +188,9 @@ __device__ __forceinline__ MergeSpan split_span(const DecodeParams& p, int b, in
 
 // COLGROUPS: the launch may split the columns into groups (multi-query
 // decode); otherwise the CTA holds all ncols columns.  DimOf: the stash
-// layout (row skew).
-template <int WARPS, bool COLGROUPS, typename DimOf>
+// layout (row skew).  MASS: groups are 4 columns wide and each column's final
+// (max, 1 / sum) goes to p.stats.
+template <int WARPS, bool COLGROUPS, typename DimOf, bool MASS = false>
 __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, int kvh, const MergeSpan& ms,
                                                 float* s_comb, int* s_last) {
   using C = CombineSmem<WARPS>;
@@ -195,8 +199,9 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
   const float* wl = s_comb + C::kL;
   float* wf = s_comb + C::kF;
   float* wM = s_comb + C::kMax;
-  const int col0 = COLGROUPS ? cta_col0(p) : 0;
-  const int G = COLGROUPS ? min(8, p.ncols - col0) : p.ncols;   // this CTA's columns
+  constexpr int WIDTH = MASS ? 4 : 8;
+  const int col0 = COLGROUPS ? cta_col0<WIDTH>(p) : 0;
+  const int G = COLGROUPS ? min(WIDTH, p.ncols - col0) : p.ncols;   // this CTA's columns
   const size_t split_stride = (size_t)p.ncols * kPartialStride;
   float* part = p.partials + ms.first + (size_t)ms.part * split_stride;
   const int n_parts = ms.n_parts;
@@ -225,6 +230,8 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
       for (int w = 0; w < WARPS; ++w) l += wl[w * 8 + h] * wf[w * 8 + h];
       if (n_parts == 1) {
         p.out[out_row(p, b, kvh, col0 + h) + d] = __float2half_rn(l > 0.f ? o / l : 0.f);
+        if constexpr (MASS)
+          if (d == 0) p.stats[(size_t)(b * p.Hkv + kvh) * p.ncols + col0 + h] = make_float2(wM[h], l > 0.f ? 1.f / l : 0.f);
         continue;
       }
       part[h * kPartialStride + 128] = wM[h];
@@ -318,6 +325,8 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
     }
     if (r == 0) {
       const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+      if constexpr (MASS)
+        if (d8 == 0) p.stats[(size_t)(b * p.Hkv + kvh) * p.ncols + col0 + h] = make_float2(M, inv);
       uint4 packed;
       packed.x = pack_half2(O[0] * inv, O[1] * inv);
       packed.y = pack_half2(O[2] * inv, O[3] * inv);
@@ -342,7 +351,8 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
 // Merge the split partials of softmax column blockIdx.x % ncols of KV head
 // blockIdx.x / ncols of sequence b = blockIdx.y into O (fp16); thread d owns
 // channel d.  The combine kernel
-// of plans that defer the merge.
+// of plans that defer the merge.  MASS: also the column's (max, 1 / sum).
+template <bool MASS = false>
 __device__ __forceinline__ void combine_splits(const DecodeParams& p) {
   constexpr int U = 8;   // splits whose loads are in flight together
   const int b = blockIdx.y, d = threadIdx.x;
@@ -370,6 +380,8 @@ __device__ __forceinline__ void combine_splits(const DecodeParams& p) {
     }
   }
   p.out[out_row(p, b, kvh, h) + d] = __float2half_rn(Ls > 0.f ? O / Ls : 0.f);
+  if constexpr (MASS)
+    if (d == 0) p.stats[(size_t)(b * p.Hkv + kvh) * p.ncols + h] = make_float2(M, Ls > 0.f ? 1.f / Ls : 0.f);
 }
 
 // Store one warp's (m, l, O) into the combine area.  acc holds O^T fragments:

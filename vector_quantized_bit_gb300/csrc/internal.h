@@ -50,6 +50,13 @@ struct DecodeParams {
   // timeout test withholds every warp's first bulk copy so its waits run out.
   unsigned max_polls = 1u << 22;
   int withhold_first_copy = 0;
+  // Attention weights (vqkv_decode_attn_mass), else unused: scores (log2
+  // domain, masked ones -inf) as [B][Hkv][cgroups][score_row tokens][4
+  // columns], and each column's final (max, 1 / sum) as [B][Hkv][ncols].
+  float* scores = nullptr;
+  float2* stats = nullptr;
+  float* mass = nullptr;    // [B][Hkv][cap_len]
+  int score_row = 0, cap_len = 0;
 };
 
 constexpr int kPartialStride = 132;  // O[128], m, l, pad (rows 16-byte aligned)
@@ -96,6 +103,11 @@ cudaError_t launch_decode_fp16(const DecodeParams& p, dim3 grid, cudaStream_t st
 // Host-side helpers of api.cu shared with decode_static.cu.
 vqkv_status decode_validate(const vqkv_decode_args* a);   // every check of vqkv_decode_attn
 size_t decode_ticket_region_bytes(int B, int Hkv);       // error word + tickets, bytes
+
+// Decode with attention weights (decode_mass.cu): the decode kernel, the
+// merge kernel of plans that defer it, and the accumulation into p.mass.
+cudaError_t decode_mass_prepare(int mode);
+cudaError_t launch_decode_mass(int mode, const DecodeParams& p, dim3 grid, cudaStream_t stream);
 
 // Draft-tree attention (decode_tree.cu): partials as in the split plan,
 // [B][Hkv][n_splits][ncols], always merged by launch_combine (n_splits > 1);
