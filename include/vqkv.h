@@ -339,7 +339,9 @@ vqkv_status vqkv_decode_attn_paged(const vqkv_decode_args* args, const vqkv_pagi
  * tensor cores, sums and softmax statistics are fp32.
  */
 typedef struct {
-  vqkv_decode_args decode;    /* q, out: [B][n_queries][Hq][128]; num_splits: 0 = automatic */
+  vqkv_decode_args decode;    /* q, out: [B][n_queries][Hq][128]; num_splits: shares of the
+                                 batch's tokens per KV head and group of columns, 0 = automatic,
+                                 at most 1024 are used */
   int32_t n_queries;          /* M, 1..64 */
   const uint64_t* tree_mask;  /* device [B][M], 8-byte aligned */
 } vqkv_decode_tree_args;

@@ -134,6 +134,48 @@ def test_tree_against_reference(mode, B, Hq, Hkv, M, lens, cap, num_splits, page
                 assert np.all(o[b, m] == 0)
 
 
+@pytest.mark.parametrize("mode,Hq,Hkv,M,num_splits,page", [
+    (0, 8, 2, 9, 0, 0), (0, 8, 2, 9, 5, 64), (0, 8, 1, 33, 7, 0), (0, 8, 1, 33, 0, 0), (1, 5, 1, 30, 3, 128),
+    (2, 4, 1, 64, 5, 0), (3, 8, 1, 20, 4, 0), (4, 8, 1, 50, 6, 64), (4, 3, 1, 7, 1, 0),
+])
+def test_tree_ragged_batches(mode, Hq, Hkv, M, num_splits, page):
+    """Shares that begin and end inside sequences, hold several of them, an odd number of tiles, or none; one and two
+    query tiles per CTA, a second one with few columns."""
+    lens = [1, 0, 700, 64, 65, 0, 333, 128, 449, 17]
+    B, cap = len(lens), 768
+    r, q, kc, vc, s, kcb, vcb = case(mode, B, Hq, Hkv, M, cap, seed=7 * mode + M)
+    masks = tree_masks(r, B, M, "tree")
+    o, err = gpu_tree(mode, q, masks, kc, vc, s, kcb, vcb, lens, cap, num_splits, page)
+    ref, _, tol = R.attend(q, kc, vc, kcb, vcb, s, lens, visible_of(masks, M))
+    R.check_output(o, ref, tol)
+    assert err == 0
+    assert np.all(o[1] == 0) and np.all(o[5] == 0)
+
+
+def test_tree_more_sequences_than_one_launch_takes():
+    B, M = 1030, 2
+    r = np.random.default_rng(3)
+    lens = r.integers(0, 40, size=B)
+    s, kcb, vcb = H.random_codebooks(0, 1, 4)
+    kc = [[r.integers(0, 256, size=(48, 32))] for _ in range(B)]
+    vc = [[r.integers(0, 256, size=(48, 32))] for _ in range(B)]
+    q = r.standard_normal((B, M, 2, 128)).astype(np.float16)
+    masks = tree_masks(r, B, M, "random")
+    o, err = gpu_tree(0, q, masks, kc, vc, s, kcb, vcb, lens, 48)
+    ref, _, tol = R.attend(q, kc, vc, kcb, vcb, s, lens, visible_of(masks, M))
+    R.check_output(o, ref, tol)
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2, 3, 4])
+def test_tree_long_prefix_two_query_tiles(mode):
+    r, q, kc, vc, s, kcb, vcb = case(mode, 1, 8, 1, 20, 3000, seed=mode)
+    masks = tree_masks(r, 1, 20, "tree")
+    o, err = gpu_tree(mode, q, masks, kc, vc, s, kcb, vcb, [2999], 3000, num_splits=2)
+    ref, _, tol = R.attend(q, kc, vc, kcb, vcb, s, [2999], visible_of(masks, 20))
+    R.check_output(o, ref, tol)
+    assert err == 0
+
+
 @pytest.mark.parametrize("mode", [0, 1, 2, 3, 4])
 def test_tree_long_prefix_many_tiles(mode):
     # enough tiles per CTA to wrap both rings and the code prefetch many times
@@ -145,9 +187,10 @@ def test_tree_long_prefix_many_tiles(mode):
     assert err == 0
 
 
-def test_tree_rising_scores_rescale_the_accumulator():
-    """Keys whose scores climb tile after tile: the running max moves in every tile."""
-    r, q, kc, vc, s, kcb, vcb = case(0, 1, 4, 1, 8, 1024, seed=5)
+@pytest.mark.parametrize("M", [8, 40])
+def test_tree_rising_scores_rescale_the_accumulator(M):
+    """Keys whose scores climb tile after tile: the running max moves in every tile (one and two query tiles)."""
+    r, q, kc, vc, s, kcb, vcb = case(0, 1, 4, 1, M, 1024, seed=5)
     s[:] = 1.0
     # codebook entry e is e/256 of a fixed direction, token t takes entry t / 4
     d = vo.transform_query(q[0, 0, 0][None], s[0])[0]
@@ -155,9 +198,9 @@ def test_tree_rising_scores_rescale_the_accumulator():
     kcb[0] = step.astype(np.float16)
     kc[0][0] = np.repeat((np.arange(1024) // 4)[:, None], 32, axis=1)
     q[:] = np.sign(vo.normalized_hadamard() @ np.tile(np.sign(d[:4]), 32)).astype(np.float16)[None, None, None]
-    masks = tree_masks(r, 1, 8, "chain")
+    masks = tree_masks(r, 1, M, "chain")
     o, err = gpu_tree(0, q, masks, kc, vc, s, kcb, vcb, [1024], 1024, num_splits=1)
-    ref, _, tol = R.attend(q, kc, vc, kcb, vcb, s, [1024], visible_of(masks, 8))
+    ref, _, tol = R.attend(q, kc, vc, kcb, vcb, s, [1024], visible_of(masks, M))
     R.check_output(o, ref, tol)
 
 

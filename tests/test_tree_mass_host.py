@@ -33,7 +33,7 @@ def _tree(n_queries=8, tree_mask=0xa000, **kw):
     (dict(n_queries=0), 1), (dict(n_queries=65), 2), (dict(tree_mask=None), 1), (dict(tree_mask=0xa004), 1),
     (dict(mode=5), 2), (dict(head_dim=64), 2), (dict(Hq=9), 2), (dict(Hq=6, Hkv=4), 1), (dict(max_seq_len=65), 1),
     (dict(q=None), 1), (dict(out=None), 1), (dict(k_codes=0x2008), 1), (dict(softmax_scale=float("inf")), 1),
-    (dict(num_splits=-1), 1), (dict(B=65536), 2), (dict(Hkv=65536, Hq=65536), 2), (dict(cap_len=2**30 + 1), 2),
+    (dict(num_splits=-1), 1), (dict(B=128, cap_len=2**30, max_seq_len=2**30), 2), (dict(Hkv=65536, Hq=65536), 2), (dict(cap_len=2**30 + 1), 2),
 ])
 def test_tree_validation(lib, kw, status):
     assert lib.vqkv_decode_attn_tree(ctypes.byref(_tree(**kw)), None, None) == status

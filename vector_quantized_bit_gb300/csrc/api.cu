@@ -297,9 +297,12 @@ vqkv_status plan_mass(const vqkv_decode_mass_args* am, MassPlan* pl) {
   return VQKV_OK;
 }
 
-// Draft-tree attention: split plan of one CTA per SM (its shared memory).
+// Draft-tree attention: one CTA per SM (its shared memory), all of them in one
+// wave over (share, KV head, column group); a share is an equal part of all
+// sequences' tiles, cut on the device.  Batches beyond the flat plan's limit
+// run as several launches of up to kFlatMaxB sequences.
 struct TreePlan {
-  int n_splits = 1, tps = 1, cgroups = 1;
+  int n_splits = 1, cgroups = 1;
   size_t ws_bytes = 0;
 };
 
@@ -309,8 +312,8 @@ vqkv_status validate_tree_sizes(const vqkv_decode_tree_args* at) {
   if (st != VQKV_OK) return st;
   if (at->n_queries < 1) return VQKV_ERR_INVALID_ARG;
   if (at->n_queries > 64) return VQKV_ERR_UNSUPPORTED;   // one mask word per query
-  const int cg = (at->n_queries * (at->decode.Hq / at->decode.Hkv) + decode_tree_cols() - 1) / decode_tree_cols();
-  if ((long long)at->decode.B * cg > kMaxGridYZ || at->decode.Hkv > kMaxGridYZ || at->decode.cap_len > kMaxTokens)
+  if (at->decode.Hkv > kMaxGridYZ || at->decode.cap_len > kMaxTokens ||
+      (long long)std::min(at->decode.B, kFlatMaxB) * ((at->decode.max_seq_len + 63) / 64) > kMaxTokens)
     return VQKV_ERR_UNSUPPORTED;
   return VQKV_OK;
 }
@@ -321,28 +324,15 @@ vqkv_status plan_tree(const vqkv_decode_tree_args* at, TreePlan* pl) {
   if (st != VQKV_OK) return st;
   const vqkv_decode_args* a = &at->decode;
   const int cols = at->n_queries * (a->Hq / a->Hkv);
-  pl->cgroups = (cols + decode_tree_cols() - 1) / decode_tree_cols();
-  const long long tiles = std::max(1, (a->max_seq_len + decode_tree_tile() - 1) / decode_tree_tile());
-  const long long pairs = (long long)std::max(a->B, 1) * a->Hkv * pl->cgroups;
-  long long best_n = 1;
-  if (a->num_splits > 0) {
-    best_n = std::min<long long>(a->num_splits, tiles);
-  } else {
-    // fewest (waves of CTAs) x (tiles per CTA + the prologue's and epilogue's worth of tiles)
-    const double setup_tiles = 10.0;
-    double best = 1e300;
-    const long long hi = std::min<long long>(tiles, 4 * ((di.sms + pairs - 1) / pairs) + 8);
-    for (long long n = 1; n <= hi; ++n) {
-      const double cost = (double)((pairs * n + di.sms - 1) / di.sms) * ((double)((tiles + n - 1) / n) + setup_tiles);
-      if (cost < best - 1e-9) best = cost, best_n = n;
-    }
-  }
-  const long long tps = (tiles + best_n - 1) / best_n;
-  pl->tps = (int)tps;
-  pl->n_splits = (int)((tiles + tps - 1) / tps);
+  pl->cgroups = (cols + decode_tree_cols(cols) - 1) / decode_tree_cols(cols);
+  const int B = std::max(std::min(a->B, kFlatMaxB), 1);
+  // a share has at least one tile when the sequences are full
+  const long long tiles = std::max<long long>(1, (long long)B * ((a->max_seq_len + 63) / 64));
+  const long long want = a->num_splits > 0 ? std::min(a->num_splits, 1024) : di.sms / ((long long)a->Hkv * pl->cgroups);
+  pl->n_splits = (int)std::max<long long>(1, std::min(want, tiles));
   pl->ws_bytes = kWsHeader;
   if (pl->n_splits > 1)
-    pl->ws_bytes += sizeof(float) * (size_t)std::max(a->B, 1) * a->Hkv * pl->n_splits * cols * kPartialStride;
+    pl->ws_bytes += sizeof(float) * (size_t)a->Hkv * (pl->n_splits + B - 1) * cols * kPartialStride;
   return VQKV_OK;
 }
 
@@ -716,14 +706,23 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_pa
   p.partials = reinterpret_cast<float*>(ws + kWsHeader);
   p.cgroups = pl.cgroups;
   p.n_splits = pl.n_splits;
-  p.tps = pl.tps;
-  p.bpg = 1;
-  p.defer_merge = 1;
-  const dim3 grid(pl.n_splits, a->Hkv, a->B * pl.cgroups);
-  if (launch_decode_tree(a->mode, p, reinterpret_cast<const unsigned long long*>(at->tree_mask), grid,
-                         static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return VQKV_ERR_CUDA;
-  if (pl.n_splits > 1 && launch_combine(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return VQKV_ERR_CUDA;
+  const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(at->tree_mask);
+  for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
+    DecodeParams c = p;
+    c.B = std::min(a->B - b0, kFlatMaxB);
+    const size_t rows = (size_t)b0 * p.M * p.Hq * 128;
+    c.q = p.q + rows;
+    c.out = p.out + rows;
+    c.seq_lens = p.seq_lens + b0;
+    if (p.block_table != nullptr) {
+      c.block_table = p.block_table + (size_t)b0 * p.max_blocks;
+    } else {
+      c.kc = p.kc + (size_t)b0 * p.Hkv * p.stream_bytes;
+      c.vc = p.vc + (size_t)b0 * p.Hkv * p.stream_bytes;
+    }
+    if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return VQKV_ERR_CUDA;
+  }
   return VQKV_OK;
 }
 

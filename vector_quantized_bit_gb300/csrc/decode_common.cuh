@@ -450,5 +450,40 @@ struct NaturalDim {   // channel offset gid, rows gid+8 eight channels on
   __device__ static int skew(int h) { return 8 * ((h >> 1) & 3); }
 };
 
+// Flat plan: s_pref[b] = super-tiles (TPI tiles of 16 tokens) of sequences
+// 0 .. b-1 at their clamped lengths, for b = 0 .. B.  All threads.
+template <int TPI>
+__device__ __forceinline__ void flat_prefix(const DecodeParams& p, int* s_pref) {
+  const int lane = threadIdx.x & 31;
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    const int raw = p.seq_lens[b], L = min(max(raw, 0), p.max_seq_len);
+    if (raw != L && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
+    s_pref[b + 1] = ((L + 16 - 1) / 16 + TPI - 1) / TPI;
+  }
+  if (threadIdx.x == 0) s_pref[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {   // inclusive scan of s_pref[1..B], 32 entries per step
+    int carry = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      const int i = base + lane;
+      int v = i < p.B ? s_pref[i + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+      }
+      if (i < p.B) s_pref[i + 1] = v + carry;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// Flat plan: the CTA (of S_eff) whose share [T s / S_eff, T (s+1) / S_eff)
+// of the T super-tiles holds super-tile x.
+__device__ __forceinline__ int flat_cta_of(long long x, long long T, int S_eff) {
+  return (int)(((x + 1) * S_eff - 1) / T);
+}
+
 }  // namespace
 }  // namespace vqkv

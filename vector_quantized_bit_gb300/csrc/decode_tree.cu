@@ -1,21 +1,31 @@
 // Attention of a tree of drafted tokens over a packed cache (sm_103a, tcgen05).
 //
 // M drafts x g query heads give up to 512 softmax columns per KV head, so the
-// two products are matrix products worth the tensor cores: a CTA takes up to
-// 128 columns (the MMA rows) and one token range ("split") of a sequence and
-// walks it in tiles of 64 tokens:
+// two products are matrix products worth the tensor cores.  A CTA takes up to
+// 128 or 256 columns (MMA rows) of one KV head and walks its share of the
+// batch's tokens in tiles of 64:
 //   dequantise  K' and V tiles into shared memory, each centroid gathered
 //               once per tile and CTA (8 warps: 4 for K, 4 for V)
 //   S = Q' K'^T 128 x 64 x 128, Q' in tensor memory (A), K' rows in shared
 //               memory (B, K-major), S in tensor memory
-//   softmax     one thread per column (4 warps): running max and sum in fp32,
-//               P = exp2(S - m) as fp16 back to tensor memory; O is rescaled
-//               only when a score exceeds the running max by 2^8
+//   softmax     one thread per column: running max and sum in fp32, P =
+//               exp2(S - m) as fp16 back to tensor memory; O is rescaled only
+//               when a score exceeds the running max by 2^8
 //   O += P V    128 x 128 x 64, P in tensor memory (A), V rows in shared
 //               memory (B, channel-major), O stays in tensor memory
-// K and V tiles have a two-stage ring each; S and P are double buffered, and
-// the score product of tile t + 1 is issued before the P.V product of tile t,
-// so the tensor cores, the softmax warps and the dequantisation overlap.
+// There are two softmax warpgroups with an S, P, O, max and sum each.  Up to
+// 128 columns (NQ = 1) they take the tiles in turn (one warpgroup alone spends
+// more time on a tile's 64 exponentials per thread than everything else
+// takes), and the second's state is merged into the first's at the end; a
+// warpgroup's next score product is issued as soon as it has read its last
+// scores.  Above 128 columns (NQ = 2) each warpgroup takes 128 columns of
+// every tile, so one dequantisation serves 256; P then overlays S (tensor
+// memory is full).
+//
+// Work: all sequences' tiles in order are cut into equal shares, one CTA per
+// share, KV head and column group (the flat plan of the single-query decode).
+// A share that holds a whole sequence writes its O, other overlaps leave
+// partials (m, l, O) that tree_combine_kernel merges.
 //
 // The query transform is that of the single-query decode: q' = (q * s) . Hn,
 // scaled by softmax_scale * log2 e.  q' and P are rounded to fp16 (2^-12
@@ -36,26 +46,39 @@ namespace vqkv {
 namespace {
 
 namespace tr {
-constexpr int COLS = 128;                 // softmax columns per CTA (MMA rows)
+constexpr int ROWS = 128;                 // MMA rows: softmax columns of one query tile
 constexpr int TOK = 64;                   // tokens per tile
-constexpr int SM_WARPS = 4, DQ_WARPS = 8;
+constexpr int SM_WARPS = 8, DQ_WARPS = 8; // two softmax warpgroups
 constexpr int MMA_WARP = SM_WARPS + DQ_WARPS;
-constexpr int THREADS = (MMA_WARP + 1) * 32;
+constexpr int THREADS = (MMA_WARP + 4) * 32;   // whole warpgroups, for the register split
+// Registers per thread: 96 at launch (640 threads), then 128 for the softmax
+// warpgroups (64 scores and 16 packed weights are live), 88 for the
+// dequantising ones, 40 for the last: 2 x 128 x 128 + 2 x 128 x 88 + 128 x 40
+// = 60,416 of the launch's 640 x 96 = 61,440.
+constexpr int REGS_SM = 128, REGS_DQ = 88, REGS_MMA = 40;
 constexpr int TILE_SMEM = TOK * 256;      // one dequantised K or V tile: two 64-channel halves of 64 x 128 bytes
 constexpr int HALF = TOK * 128;
-constexpr int STAGES = 2;
 constexpr int PREFETCH = 4;               // tiles whose codes a dequantising warp holds in registers
-constexpr int Q_PITCH = 272;              // staged q' row (fp16), padded against bank conflicts
-// tensor memory columns
-constexpr uint32_t T_O = 0, T_S = 128, T_P = 256, T_Q = 320, T_COLS = 512;
+// tensor memory columns: O, S and P of each softmax warpgroup, then q'
+constexpr uint32_t T_O = 0, T_S = 256, T_COLS = 512;
+template <int NQ>
+struct Tmem {
+  __device__ static constexpr uint32_t p(uint32_t wg) { return NQ == 1 ? 384 + TOK / 2 * wg : T_S + TOK * wg; }
+  __device__ static constexpr uint32_t q(uint32_t tile) { return NQ == 1 ? 448 : 384 + 64 * tile; }
+};
 constexpr uint32_t MAX_POLLS = 1u << 20;
 
 template <int MODE>
 struct Geo {
   static constexpr int CB_BYTES = MODE == VQKV_MODE_VQ15 || MODE == VQKV_MODE_VQ125 ? 131072 : 65536;
+  // ring stages of K and of V: what fits beside the codebooks (tile k is in
+  // stage k % STAGES and belongs to softmax warpgroup k % 2)
+  static constexpr int STAGES = CB_BYTES == 65536 ? 4 : 2;
   static constexpr int K_OFF = CB_BYTES, V_OFF = K_OFF + STAGES * TILE_SMEM;
   static constexpr int BAR_OFF = V_OFF + STAGES * TILE_SMEM;
-  static constexpr int SMEM = BAR_OFF + 256;
+  static constexpr int ML_OFF = BAR_OFF + 256;             // a warpgroup's max and sum per column, for the merge
+  static constexpr int PREF_OFF = ML_OFF + ROWS * 8;       // tiles of the sequences before each
+  static constexpr int SMEM = PREF_OFF + (kFlatMaxB + 1) * 4;
   static constexpr int LAYOUT_TOK = MODE == VQKV_MODE_VQ15 ? 64 : 16;
   static constexpr int TILE_BYTES = MODE == VQKV_MODE_VQ2    ? 512
                                     : MODE == VQKV_MODE_VQ4  ? 1024
@@ -66,8 +89,9 @@ struct Geo {
   static constexpr int KW = MODE == VQKV_MODE_VQ2 ? 4 : MODE == VQKV_MODE_VQ4 ? 8 : MODE == VQKV_MODE_VQ3 ? 6 : 3;
   static constexpr int VW = MODE == VQKV_MODE_VQ125 ? 5 : KW;
   static constexpr int W = VW;
-  static_assert(COLS * Q_PITCH <= 2 * STAGES * TILE_SMEM, "staged q' uses the K and V rings before the loop");
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(2 * ROWS * 256 <= 2 * STAGES * TILE_SMEM, "staged q' uses the K and V rings before the loop");
+  static_assert(ROWS * kHeadDim * 4 <= 2 * STAGES * TILE_SMEM, "the merge of O uses them after it");
+  static_assert(SMEM <= 226 * 1024, "shared memory");
 };
 }  // namespace tr
 
@@ -145,107 +169,152 @@ __device__ __forceinline__ void put_tile(unsigned char* tile, int row, int at, T
   *reinterpret_cast<T*>(tile + (at >> 7) * tr::HALF + row * 128 + ((((at >> 4) & 7) ^ (row & 7)) << 4) + (at & 15)) = v;
 }
 
-// Dequantises the lane's share of 16 key tokens (rows 16u ..) into a tile.
-// Lane (gid, tig) holds the codes of tokens gid, gid + 8 for every fourth
-// subvector; the stores of a warp cover the banks evenly.
-template <int MODE>
-__device__ __forceinline__ void dequant_k(const unsigned char* s_cb, unsigned char* tile, int u, int lane,
-                                          const uint32_t (&w)[tr::Geo<MODE>::W]) {
-  const int gid = lane >> 2, tig = lane & 3;
-  const int r0 = 16 * u + gid, r1 = r0 + 8;
-  if constexpr (MODE == VQKV_MODE_VQ2) {
-    const uint32_t kb = (uint32_t)(lane & 15) << 3;
-#define VQKV_K_STEP(S)                                                                                  \
-  {                                                                                                     \
-    const uint2 c = lds_at<uint2>(s_cb, cb_offset<(S)&3>((S) < 4 ? w[0] : w[1], kb));                     \
-    const uint2 d = lds_at<uint2>(s_cb, cb_offset<(S)&3>((S) < 4 ? w[2] : w[3], kb));                     \
-    put_tile(tile, r0, 32 * (S) + 8 * tig, c);                                                            \
-    put_tile(tile, r1, 32 * (S) + 8 * tig, d);                                                            \
+// A lane's share of 16 dequantised tokens: 128 bytes, gathered into registers
+// before the ring stage it goes to is known to be free.
+struct Centroids {
+  uint32_t r[32];
+  __device__ __forceinline__ void set(int i, uint32_t v) { r[i] = v; }
+  __device__ __forceinline__ void set(int i, uint2 v) { r[2 * i] = v.x, r[2 * i + 1] = v.y; }
+  __device__ __forceinline__ void set(int i, uint4 v) {
+    r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
   }
-    VQKV_K_STEP(0) VQKV_K_STEP(1) VQKV_K_STEP(2) VQKV_K_STEP(3)
-    VQKV_K_STEP(4) VQKV_K_STEP(5) VQKV_K_STEP(6) VQKV_K_STEP(7)
-#undef VQKV_K_STEP
+  template <typename T>
+  __device__ __forceinline__ T get(int i) const;
+};
+template <>
+__device__ __forceinline__ uint32_t Centroids::get<uint32_t>(int i) const {
+  return r[i];
+}
+template <>
+__device__ __forceinline__ uint2 Centroids::get<uint2>(int i) const {
+  return make_uint2(r[2 * i], r[2 * i + 1]);
+}
+template <>
+__device__ __forceinline__ uint4 Centroids::get<uint4>(int i) const {
+  return make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+}
+
+// Gathers the lane's share of 16 key tokens: lane (gid, tig) holds the codes
+// of tokens gid, gid + 8 for every fourth subvector; entry 2S (token gid) and
+// 2S + 1 (gid + 8) of step S.  Lanes of odd gid take the subvectors two (8-byte
+// centroids) or one (16-byte) steps apart from those of even gid: with the
+// rows' swizzle the lanes of a store phase then fall on distinct banks.
+template <int MODE>
+__device__ __forceinline__ void gather_k(const unsigned char* s_cb, int lane, const uint32_t (&w)[tr::Geo<MODE>::W],
+                                         Centroids& c) {
+  const int gid = lane >> 2, tig = lane & 3;
+  const uint32_t odd = gid & 1;
+  if constexpr (MODE == VQKV_MODE_VQ2) {
+    const uint32_t kb = (uint32_t)(lane & 15) << 3, rot = odd ? 0x1032u : 0x3210u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t g = __byte_perm(w[i], 0u, rot), h = __byte_perm(w[2 + i], 0u, rot);
+      c.set(8 * i, lds_at<uint2>(s_cb, cb_offset<0>(g, kb)));
+      c.set(8 * i + 1, lds_at<uint2>(s_cb, cb_offset<0>(h, kb)));
+      c.set(8 * i + 2, lds_at<uint2>(s_cb, cb_offset<1>(g, kb)));
+      c.set(8 * i + 3, lds_at<uint2>(s_cb, cb_offset<1>(h, kb)));
+      c.set(8 * i + 4, lds_at<uint2>(s_cb, cb_offset<2>(g, kb)));
+      c.set(8 * i + 5, lds_at<uint2>(s_cb, cb_offset<2>(h, kb)));
+      c.set(8 * i + 6, lds_at<uint2>(s_cb, cb_offset<3>(g, kb)));
+      c.set(8 * i + 7, lds_at<uint2>(s_cb, cb_offset<3>(h, kb)));
+    }
   } else if constexpr (MODE == VQKV_MODE_VQ4) {
     const uint32_t kb = (uint32_t)lane << 2;
-#define VQKV_K_STEP(S)                                                                                       \
-  {                                                                                                          \
-    const uint32_t wg = w[(S) >> 1], wh = w[4 + ((S) >> 1)];                                                   \
-    put_tile(tile, r0, 32 * (S) + 4 * tig, lds_at<uint32_t>(s_cb, cb_offset<((S)&1) * 2>(wg, kb)));            \
-    put_tile(tile, r0, 32 * (S) + 16 + 4 * tig, lds_at<uint32_t>(s_cb, cb_offset<((S)&1) * 2 + 1>(wg, kb)));   \
-    put_tile(tile, r1, 32 * (S) + 4 * tig, lds_at<uint32_t>(s_cb, cb_offset<((S)&1) * 2>(wh, kb)));            \
-    put_tile(tile, r1, 32 * (S) + 16 + 4 * tig, lds_at<uint32_t>(s_cb, cb_offset<((S)&1) * 2 + 1>(wh, kb)));   \
-  }
-    VQKV_K_STEP(0) VQKV_K_STEP(1) VQKV_K_STEP(2) VQKV_K_STEP(3)
-    VQKV_K_STEP(4) VQKV_K_STEP(5) VQKV_K_STEP(6) VQKV_K_STEP(7)
-#undef VQKV_K_STEP
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // steps 4i .. 4i + 3: bytes 0..3 of the tokens' words i
+      const uint32_t g = w[i], h = w[4 + i];
+      c.set(8 * i, lds_at<uint32_t>(s_cb, cb_offset<0>(g, kb)));
+      c.set(8 * i + 1, lds_at<uint32_t>(s_cb, cb_offset<0>(h, kb)));
+      c.set(8 * i + 2, lds_at<uint32_t>(s_cb, cb_offset<1>(g, kb)));
+      c.set(8 * i + 3, lds_at<uint32_t>(s_cb, cb_offset<1>(h, kb)));
+      c.set(8 * i + 4, lds_at<uint32_t>(s_cb, cb_offset<2>(g, kb)));
+      c.set(8 * i + 5, lds_at<uint32_t>(s_cb, cb_offset<2>(h, kb)));
+      c.set(8 * i + 6, lds_at<uint32_t>(s_cb, cb_offset<3>(g, kb)));
+      c.set(8 * i + 7, lds_at<uint32_t>(s_cb, cb_offset<3>(h, kb)));
+    }
   } else if constexpr (MODE == VQKV_MODE_VQ3) {
 #pragma unroll
-    for (int S = 0; S < 8; ++S) {
-      const uint32_t pg = pair_at(w, 3 * (S & 3)), ph = pair_at(w, 12 + 3 * (S & 3));
-      const uint32_t cg = S < 4 ? (pg & 0xfffu) : (pg >> 12), ch = S < 4 ? (ph & 0xfffu) : (ph >> 12);
-      put_tile(tile, r0, 32 * S + 8 * tig, lds_at<uint2>(s_cb, cg << 3));
-      put_tile(tile, r1, 32 * S + 8 * tig, lds_at<uint2>(s_cb, ch << 3));
+    for (int P = 0; P < 2; ++P) {   // pairs P and P + 2 of each token, in the lane's order
+      const uint32_t a0 = pair_at(w, 3 * P), a2 = pair_at(w, 3 * P + 6);
+      const uint32_t b0 = pair_at(w, 12 + 3 * P), b2 = pair_at(w, 18 + 3 * P);
+      const uint32_t pg[2] = {odd ? a2 : a0, odd ? a0 : a2}, ph[2] = {odd ? b2 : b0, odd ? b0 : b2};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {   // step S = P + 2 (q & 1) + 4 (q >> 1): low code for S < 4
+        const int S = P + 2 * (q & 1) + 4 * (q >> 1);
+        c.set(2 * S, lds_at<uint2>(s_cb, (q < 2 ? (pg[q & 1] & 0xfffu) : (pg[q & 1] >> 12)) << 3));
+        c.set(2 * S + 1, lds_at<uint2>(s_cb, (q < 2 ? (ph[q & 1] & 0xfffu) : (ph[q & 1] >> 12)) << 3));
+      }
     }
   } else if constexpr (MODE == VQKV_MODE_VQ15) {
-    // pairs tig, tig + 4 of token gid, then of token gid + 8
+    // pairs tig, tig + 4 of token gid, then of token gid + 8; low code for s2 < 2
+    const uint32_t a0 = pair24(w[0], w[1], w[2], 0), a1 = pair24(w[0], w[1], w[2], 1);
+    const uint32_t b0 = pair24(w[0], w[1], w[2], 2), b1 = pair24(w[0], w[1], w[2], 3);
+    const uint32_t pa[2] = {odd ? a1 : a0, odd ? a0 : a1}, pb[2] = {odd ? b1 : b0, odd ? b0 : b1};
 #pragma unroll
     for (int s2 = 0; s2 < 4; ++s2) {
-      const uint32_t pa = pair24(w[0], w[1], w[2], s2 & 1), pb = pair24(w[0], w[1], w[2], 2 + (s2 & 1));
-      const uint32_t ca = s2 < 2 ? (pa & 0xfffu) : (pa >> 12), cb = s2 < 2 ? (pb & 0xfffu) : (pb >> 12);
-      put_tile(tile, r0, 64 * s2 + 16 * tig, lds_at<uint4>(s_cb, ca << 4));
-      put_tile(tile, r1, 64 * s2 + 16 * tig, lds_at<uint4>(s_cb, cb << 4));
+      c.set(2 * s2, lds_at<uint4>(s_cb, (s2 < 2 ? (pa[s2 & 1] & 0xfffu) : (pa[s2 & 1] >> 12)) << 4));
+      c.set(2 * s2 + 1, lds_at<uint4>(s_cb, (s2 < 2 ? (pb[s2 & 1] & 0xfffu) : (pb[s2 & 1] >> 12)) << 4));
     }
   } else {
     const uint32_t kb = (uint32_t)tig << 5;
 #pragma unroll
     for (int s2 = 0; s2 < 4; ++s2) {
-      put_tile(tile, r0, 64 * s2 + 16 * tig, lds_at<uint4>(s_cb, kb + cb10_offset(bits10(w, 10 * s2))));
-      put_tile(tile, r1, 64 * s2 + 16 * tig, lds_at<uint4>(s_cb, kb + cb10_offset(bits10(w, 40 + 10 * s2))));
+      const uint32_t a0 = bits10(w, 10 * s2), a1 = bits10(w, 10 * (s2 ^ 1));
+      const uint32_t b0 = bits10(w, 40 + 10 * s2), b1 = bits10(w, 40 + 10 * (s2 ^ 1));
+      c.set(2 * s2, lds_at<uint4>(s_cb, kb + cb10_offset(odd ? a1 : a0)));
+      c.set(2 * s2 + 1, lds_at<uint4>(s_cb, kb + cb10_offset(odd ? b1 : b0)));
     }
   }
 }
 
-// The same for 16 value tokens: lane (gid, tig) holds the codes of tokens 2tig,
-// 2tig + 1, 2tig + 8, 2tig + 9 for the subvectors j with j % 8 == gid.
+// Writes them as rows 16u + gid, 16u + gid + 8 of a tile.
 template <int MODE>
-__device__ __forceinline__ void dequant_v(const unsigned char* s_cb, unsigned char* tile, int u, int lane,
-                                          const uint32_t (&w)[tr::Geo<MODE>::W]) {
+__device__ __forceinline__ void put_k(unsigned char* tile, int u, int lane, const Centroids& c) {
+  using T = typename std::conditional<MODE == VQKV_MODE_VQ4, uint32_t,
+                                      typename std::conditional<MODE == VQKV_MODE_VQ2 || MODE == VQKV_MODE_VQ3, uint2,
+                                                                uint4>::type>::type;
+  constexpr int STEP = 4 * (int)sizeof(T);   // the four lanes of a step are neighbours
+  const int gid = lane >> 2, tig = lane & 3, r0 = 16 * u + gid;
+  const int at = (int)sizeof(T) * tig + (MODE == VQKV_MODE_VQ4 ? 0 : 64 * (gid & 1));   // byte (STEP S) ^ at
+#pragma unroll
+  for (int S = 0; S < 256 / STEP; ++S) {
+    put_tile(tile, r0, (STEP * S) ^ at, c.get<T>(2 * S));
+    put_tile(tile, r0 + 8, (STEP * S) ^ at, c.get<T>(2 * S + 1));
+  }
+}
+
+// The same for 16 value tokens: lane (gid, tig) holds the codes of tokens 2tig,
+// 2tig + 1, 2tig + 8, 2tig + 9 (slots k) for the subvectors j with j % 8 ==
+// gid; entry 4i + k is subvector gid + 8i of slot k.
+template <int MODE>
+__device__ __forceinline__ void gather_v(const unsigned char* s_cb, int lane, const uint32_t (&w)[tr::Geo<MODE>::W],
+                                         Centroids& c) {
   const int gid = lane >> 2, tig = lane & 3;
-  const int r0 = 16 * u + 2 * tig;
-  if constexpr (MODE == VQKV_MODE_VQ2) {
-    const uint32_t vb = 128u | ((uint32_t)(lane & 15) << 3);
+  if constexpr (MODE == VQKV_MODE_VQ2 || MODE == VQKV_MODE_VQ4) {
+    using T = typename std::conditional<MODE == VQKV_MODE_VQ2, uint2, uint32_t>::type;
+    const uint32_t vb = 128u | (MODE == VQKV_MODE_VQ2 ? (uint32_t)(lane & 15) << 3 : (uint32_t)lane << 2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      put_tile(tile, r0, 64 * i + 8 * gid, lds_at<uint2>(s_cb, cb_offset<0>(w[i], vb)));
-      put_tile(tile, r0 + 1, 64 * i + 8 * gid, lds_at<uint2>(s_cb, cb_offset<1>(w[i], vb)));
-      put_tile(tile, r0 + 8, 64 * i + 8 * gid, lds_at<uint2>(s_cb, cb_offset<2>(w[i], vb)));
-      put_tile(tile, r0 + 9, 64 * i + 8 * gid, lds_at<uint2>(s_cb, cb_offset<3>(w[i], vb)));
-    }
-  } else if constexpr (MODE == VQKV_MODE_VQ4) {
-    const uint32_t vb = 128u | ((uint32_t)lane << 2);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      put_tile(tile, r0, 32 * i + 4 * gid, lds_at<uint32_t>(s_cb, cb_offset<0>(w[i], vb)));
-      put_tile(tile, r0 + 1, 32 * i + 4 * gid, lds_at<uint32_t>(s_cb, cb_offset<1>(w[i], vb)));
-      put_tile(tile, r0 + 8, 32 * i + 4 * gid, lds_at<uint32_t>(s_cb, cb_offset<2>(w[i], vb)));
-      put_tile(tile, r0 + 9, 32 * i + 4 * gid, lds_at<uint32_t>(s_cb, cb_offset<3>(w[i], vb)));
+    for (int i = 0; i < (MODE == VQKV_MODE_VQ2 ? 4 : 8); ++i) {
+      c.set(4 * i, lds_at<T>(s_cb, cb_offset<0>(w[i], vb)));
+      c.set(4 * i + 1, lds_at<T>(s_cb, cb_offset<1>(w[i], vb)));
+      c.set(4 * i + 2, lds_at<T>(s_cb, cb_offset<2>(w[i], vb)));
+      c.set(4 * i + 3, lds_at<T>(s_cb, cb_offset<3>(w[i], vb)));
     }
   } else if constexpr (MODE == VQKV_MODE_VQ3) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {   // token slot k: pair gid + 8 (i % 2), low code for i < 2
-        const uint32_t pr = pair_at(w, 6 * k + 3 * (i & 1));
-        put_tile(tile, r0 + (k & 1) + 8 * (k >> 1), 64 * i + 8 * gid,
-                 lds_at<uint2>(s_cb, 32768u + ((i < 2 ? (pr & 0xfffu) : (pr >> 12)) << 3)));
+      for (int k = 0; k < 4; ++k) {   // pair gid + 8h of slot k: subvectors gid + 8h, gid + 8h + 16
+        const uint32_t pr = pair_at(w, 6 * k + 3 * h);
+        c.set(4 * h + k, lds_at<uint2>(s_cb, 32768u + ((pr & 0xfffu) << 3)));
+        c.set(4 * (h + 2) + k, lds_at<uint2>(s_cb, 32768u + ((pr >> 12) << 3)));
       }
   } else if constexpr (MODE == VQKV_MODE_VQ15) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t pr = pair24(w[0], w[1], w[2], k);
-      const int row = r0 + (k & 1) + 8 * (k >> 1);
-      put_tile(tile, row, 16 * gid, lds_at<uint4>(s_cb, 65536u + ((pr & 0xfffu) << 4)));
-      put_tile(tile, row, 128 + 16 * gid, lds_at<uint4>(s_cb, 65536u + ((pr >> 12) << 4)));
+      c.set(k, lds_at<uint4>(s_cb, 65536u + ((pr & 0xfffu) << 4)));
+      c.set(4 + k, lds_at<uint4>(s_cb, 65536u + ((pr >> 12) << 4)));
     }
   } else {
     const uint32_t vb = 65536u + ((uint32_t)tig << 5), sh = 10u * (gid & 1);
@@ -256,16 +325,47 @@ __device__ __forceinline__ void dequant_v(const unsigned char* s_cb, unsigned ch
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        put_tile(tile, r0 + (k & 1) + 8 * (k >> 1), 128 * i + 16 * gid,
-                 lds_at<uint4>(s_cb, vb + cb10_offset(bits10(v, 40 * k + 20 * i))));
+      for (int k = 0; k < 4; ++k) c.set(4 * i + k, lds_at<uint4>(s_cb, vb + cb10_offset(bits10(v, 40 * k + 20 * i))));
   }
 }
 
-// Bounded wait by every lane in `mask`: false, with the abort flag and the
-// device error bit set, when it runs out or another role gave up.
-__device__ __forceinline__ bool tr_wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag, unsigned* err,
-                                        unsigned mask) {
+template <int MODE>
+__device__ __forceinline__ void put_v(unsigned char* tile, int u, int lane, const Centroids& c) {
+  using T = typename std::conditional<MODE == VQKV_MODE_VQ4, uint32_t,
+                                      typename std::conditional<MODE == VQKV_MODE_VQ2 || MODE == VQKV_MODE_VQ3, uint2,
+                                                                uint4>::type>::type;
+  const int gid = lane >> 2, r0 = 16 * u + 2 * (lane & 3);
+#pragma unroll
+  for (int i = 0; i < 32 / (int)sizeof(T); ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      put_tile(tile, r0 + (k & 1) + 8 * (k >> 1), (int)sizeof(T) * (8 * i + gid), c.get<T>(4 * i + k));
+}
+
+// Barrier of `threads` threads that leaves the others of the CTA alone.
+__device__ __forceinline__ void named_barrier_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Two fp32 additions in one instruction.
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 a, b, r; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 r, a, b; mov.b64 {%0, %1}, r; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e != 0;
+}
+
+// Bounded wait by a whole warp: false, with the abort flag and the device
+// error bit set, when it runs out or another role gave up.
+__device__ __forceinline__ bool tr_wait_long(uint32_t mbar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
   bool ok = false;
   for (uint32_t i = 0; i < tr::MAX_POLLS; ++i) {
     if (mbar_try_wait(mbar, parity)) {
@@ -274,18 +374,24 @@ __device__ __forceinline__ bool tr_wait(uint32_t mbar, uint32_t parity, volatile
     }
     if ((i & 31) == 31 && *abort_flag) break;
   }
-  ok = __all_sync(mask, ok);
+  ok = __all_sync(0xffffffffu, ok);
   if (!ok && !*abort_flag) {
     *abort_flag = 1;
     atomicOr(err, VQKV_DEVERR_TIMEOUT);
   }
   return ok;
 }
+__device__ __forceinline__ bool tr_wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(mbar, parity))) return true;
+  return tr_wait_long(mbar, parity, abort_flag, err);
+}
 
-// The dequantising warp of (role, 16-token group u of each tile): codes are
-// loaded PREFETCH tiles ahead into registers, block ids one tile further.
+// The dequantising warp of (role, 16-token group u of each tile) over n tiles
+// of sequence b from tile0 on; done: tiles the CTA has taken before (ring
+// phases).  Codes are loaded PREFETCH tiles ahead into registers, block ids
+// one tile further.
 template <int MODE, int ROLE, bool PAGED>
-__device__ __forceinline__ void dequant_loop(const DecodeParams& p, int b, int kvh, int tile0, int n, int L,
+__device__ __forceinline__ void dequant_loop(const DecodeParams& p, int b, int kvh, int tile0, int n, int L, uint32_t done,
                                              unsigned char* smem, uint32_t full, uint32_t empty, int u, int lane,
                                              volatile int* abort_flag) {
   using G = tr::Geo<MODE>;
@@ -294,10 +400,13 @@ __device__ __forceinline__ void dequant_loop(const DecodeParams& p, int b, int k
   uint32_t w[tr::PREFETCH][G::W];
   bool bad = false;
   // byte offset of the layout tile of this warp's group of tile t, -1 past the sequence
+  const int t_end = min(n, (last_group - u + 3) / 4 - tile0);   // tiles whose group u holds tokens
+  constexpr int STEP = G::LAYOUT_TOK == 64 ? G::TILE_BYTES : 4 * G::TILE_BYTES;
+  const long long first = PAGED ? 0 : tile_offset<false>(p, b, kvh, G::LAYOUT_TOK == 64 ? tile0 : 4 * tile0 + u, G::TILE_BYTES, &bad);
   auto place = [&](int t) -> long long {
-    const int grp = (tile0 + t) * (tr::TOK / 16) + u;
-    if (t >= n || grp >= last_group) return -1;
-    return tile_offset<PAGED>(p, b, kvh, G::LAYOUT_TOK == 64 ? tile0 + t : grp, G::TILE_BYTES, &bad);
+    if (t >= t_end) return -1;
+    if (!PAGED) return first + (long long)t * STEP;
+    return tile_offset<PAGED>(p, b, kvh, G::LAYOUT_TOK == 64 ? tile0 + t : 4 * (tile0 + t) + u, G::TILE_BYTES, &bad);
   };
   auto fetch = [&](long long off, uint32_t (&x)[G::W]) {
     if (off >= 0) {
@@ -315,51 +424,213 @@ __device__ __forceinline__ void dequant_loop(const DecodeParams& p, int b, int k
     for (int d = 0; d < tr::PREFETCH; ++d) {
       const int t = t0 + d;
       if (t >= n) break;
-      const int st = t & 1;
-      if (!tr_wait(empty + 8 * st, ((t >> 1) & 1) ^ 1, abort_flag, p.err, 0xffffffffu)) return;
+      const uint32_t k = done + t, st = k % G::STAGES;
+      Centroids c;   // the gathers need no free stage: their latency overlaps the wait
+      if constexpr (ROLE == VQKV_ROLE_K)
+        gather_k<MODE>(smem, lane, w[d], c);
+      else
+        gather_v<MODE>(smem, lane, w[d], c);
+      fetch(next, w[d]);
+      next = place(t + tr::PREFETCH + 1);
+      if (!tr_wait(empty + 8 * st, ((k / G::STAGES) & 1) ^ 1, abort_flag, p.err)) return;
       unsigned char* tile = smem + (ROLE == VQKV_ROLE_K ? G::K_OFF : G::V_OFF) + st * tr::TILE_SMEM;
       if constexpr (ROLE == VQKV_ROLE_K)
-        dequant_k<MODE>(smem, tile, u, lane, w[d]);
+        put_k<MODE>(tile, u, lane, c);
       else
-        dequant_v<MODE>(smem, tile, u, lane, w[d]);
+        put_v<MODE>(tile, u, lane, c);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full + 8 * st);
-      fetch(next, w[d]);
-      next = place(t + tr::PREFETCH + 1);
     }
   }
   if (PAGED && bad && lane == 0) atomicOr(p.err, VQKV_DEVERR_BLOCK);
 }
 
-// grid (splits, Hkv, B x column groups).
-template <int MODE, bool PAGED>
+// A CTA's pieces: the overlaps of its share with the sequences, in order.
+struct Pieces {
+  const int* pref;   // tiles of the sequences before each
+  int B, r0, r1;     // the share: tiles [r0, r1) of all sequences' tiles
+  int b, tile0, n;   // the current piece: n tiles of sequence b from tile0 on
+  int all;           // tiles of sequence b
+
+  __device__ __forceinline__ Pieces(const int* pref_, int B_, int split, int n_splits) : pref(pref_), B(B_), b(-1) {
+    const int T = pref[B], S = min(n_splits, T);
+    r0 = split < S ? (int)((long long)T * split / S) : 0;
+    r1 = split < S ? (int)((long long)T * (split + 1) / S) : 0;
+    if (r1 > r0) {   // the last sequence that starts at or before r0
+      int lo = 0, hi = B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pref[mid] <= r0) lo = mid; else hi = mid - 1;
+      }
+      b = lo - 1;
+    }
+  }
+  __device__ __forceinline__ bool empty() const { return r1 <= r0; }
+  __device__ __forceinline__ bool next() {
+    if (empty()) return false;
+    while (++b < B) {
+      const int lo = pref[b], hi = pref[b + 1];
+      if (lo >= r1) return false;
+      if (hi == lo) continue;
+      all = hi - lo;
+      tile0 = max(r0, lo) - lo;
+      n = min(r1, hi) - lo - tile0;
+      return true;
+    }
+    return false;
+  }
+};
+__device__ __forceinline__ int clamped_len(const DecodeParams& p, int b) {
+  return min(max(p.seq_lens[b], 0), p.max_seq_len);
+}
+
+// One warp of softmax warpgroup wg over a piece's tiles: thread = column.
+// Returns false when a wait gave up.  m, l: the column's running max and sum.
+template <int NQ, int STAGES>
+__device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Pieces& pc, uint32_t done, int wg, uint32_t t_lane,
+                                                 unsigned long long mask, int prefix, uint32_t s_full, uint32_t s_ready,
+                                                 uint32_t p_ready, uint32_t o_done, volatile int* abort_flag, float& m,
+                                                 float& l) {
+  using namespace tr;
+  const int lane = threadIdx.x & 31;
+  const uint32_t t_s = t_lane + T_S + TOK * wg, t_p = t_lane + Tmem<NQ>::p(wg), t_o = t_lane + T_O + kHeadDim * wg;
+  bool first = true;
+  // NQ 1: tiles whose number (counted over the CTA's pieces) has this parity; NQ 2: every tile
+  for (int t = NQ == 1 ? (int)((done + wg) & 1) : 0; t < pc.n; t += NQ == 1 ? 2 : 1) {
+    const uint32_t use = NQ == 1 ? (uint32_t)(done + t) >> 1 : (uint32_t)(done + t);
+    if (!tr_wait(s_full + 8 * wg, use & 1, abort_flag, p.err)) return false;
+    tcgen05_after_sync();
+    float x[2][32], top0 = neg_inf(), top1 = neg_inf();
+    tmem_ld32_max(t_s, x[0], top0);
+    tmem_ld32_max(t_s + 32, x[1], top1);
+    tmem_wait_ld();
+    if (NQ == 1) {   // the next score product may overwrite S
+      tcgen05_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_ready + 8 * ((done + t + 2) % STAGES));
+    }
+    float top = fmaxf(top0, top1);
+    const int d = prefix - (pc.tile0 + t) * TOK;
+    if (d < TOK) {   // bit i of vis: token i of the tile is visible
+      const unsigned long long vis = d >= 0 ? (mask << d) | ((1ull << d) - 1) : d > -64 ? mask >> -d : 0ull;
+      top = neg_inf();
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        if (!((vis >> i) & 1)) x[i >> 5][i & 31] = neg_inf();
+        top = fmaxf(top, x[i >> 5][i & 31]);
+      }
+    }
+    if (NQ == 1 && !first) {   // O and P of this warpgroup's previous tile are no longer in use
+      if (!tr_wait(o_done + 8 * wg, (use - 1) & 1, abort_flag, p.err)) return false;
+      tcgen05_after_sync();
+    }                          // (NQ 2: this tile's score product came after that P.V product)
+    if (__any_sync(0xffffffffu, top > m + kSoftmaxSlack)) {
+      const float mn = fmaxf(m, top), f = fast_exp2(m - mn);
+      m = mn;
+      l *= f;
+      if (!first) {
+#pragma unroll 1
+        for (int q = 0; q < kHeadDim / 16; ++q) {
+          uint32_t r[16];
+          tmem_ld16(t_o + 16 * q, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+          tmem_st16(t_o + 16 * q, r);
+        }
+      }
+    }
+    float2 sum = make_float2(0.f, 0.f);
+    const float2 minus_m = make_float2(-m, -m);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float2 e = add_f32x2(make_float2(x[h][2 * i], x[h][2 * i + 1]), minus_m);
+        e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+        sum = add_f32x2(sum, e);
+        r[i] = pack_half2(e.x, e.y);
+      }
+      tmem_st16(t_p + 16 * h, r);
+    }
+    l += sum.x + sum.y;
+    tmem_wait_st();
+    tcgen05_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(p_ready + 8 * (NQ == 1 ? (done + t) % STAGES : wg));
+    first = false;
+  }
+  return true;
+}
+
+// q' of the CTA's columns as fp16 rows of 256 bytes at s_q, 16-byte pieces
+// permuted by the row, zeros past the last column; the softmax and the
+// dequantising warps, four columns at a time each.
+__device__ __forceinline__ void stage_queries(const DecodeParams& p, int b, int kvh, int warp, int lane, int col0, int nloc,
+                                              unsigned char* s_q) {
+  constexpr int W = tr::SM_WARPS + tr::DQ_WARPS;
+  for (int c0 = warp; c0 < (nloc + 31) / 32 * 32; c0 += 4 * W) {
+    QueryLoad r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = load_query(p, b, kvh, c0 + i * W, lane, col0, nloc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * W;
+      const __half2 q01 = *reinterpret_cast<const __half2*>(&r[i].q.x), q23 = *reinterpret_cast<const __half2*>(&r[i].q.y);
+      float v[4] = {__low2float(q01) * r[i].s.x, __high2float(q01) * r[i].s.y, __low2float(q23) * r[i].s.z,
+                    __high2float(q23) * r[i].s.w};
+      fwht128_f32(v, lane);
+      if (c < (nloc + 31) / 32 * 32)
+        *reinterpret_cast<uint2*>(s_q + c * 256 + (((lane >> 1) ^ (c & 15)) << 4) + 8 * (lane & 1)) =
+            make_uint2(pack_half2(v[0] * p.qscale, v[1] * p.qscale), pack_half2(v[2] * p.qscale, v[3] * p.qscale));
+    }
+  }
+}
+
+// grid (shares, Hkv, column groups of 128 NQ).
+template <int MODE, bool PAGED, int NQ>
 __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const DecodeParams p,
                                                                      const unsigned long long* tree_mask) {
   using namespace tr;
   using G = Geo<MODE>;
+  using TM = Tmem<NQ>;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z / p.cgroups;
-  const int col0 = COLS * (int)(blockIdx.z % p.cgroups), nloc = min(COLS, p.ncols - col0);
+  const int split = blockIdx.x, kvh = blockIdx.y;
+  const int col0 = NQ * ROWS * (int)blockIdx.z, nloc = min(NQ * ROWS, p.ncols - col0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int active = (nloc + 31) >> 5;      // softmax warps with columns
+  // warps with columns in each softmax warpgroup (NQ 1: the same 128 columns)
+  const int active0 = (min(nloc, ROWS) + 31) >> 5;
+  const int active1 = NQ == 1 ? active0 : (max(nloc - ROWS, 0) + 31) >> 5;
+  const int jobs = active1 > 0 ? 2 : 1;     // NQ 2: query tiles with columns
   const uint32_t bar = smem_u32(smem + G::BAR_OFF);
-  const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_empty = bar + 48;
-  const uint32_t s_full = bar + 64, p_full = bar + 80, o_done = bar + 96, all_done = bar + 112;
+  // Per ring stage.  NQ 1: s_ready = K tile in place and the warpgroup's last
+  // scores read, pv_ready = V tile and P in place (a tile's warpgroup follows
+  // from its stage; one barrier each keeps the issuing warp at two waits per
+  // tile).  NQ 2: s_ready = K tile, pv_ready = V tile.  Per softmax warpgroup:
+  // s_full, o_done, and for NQ 2 p_ready.
+  constexpr uint32_t ST = G::STAGES;
+  const uint32_t s_ready = bar, k_empty = bar + 32, pv_ready = bar + 64, v_empty = bar + 96;
+  const uint32_t s_full = bar + 128, o_done = bar + 144, p_ready = bar + 160, all_done = bar + 176;
   volatile int* abort_flag = &s_abort;
+  int* s_pref = reinterpret_cast<int*>(smem + G::PREF_OFF);
   if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < ST; ++i) {
+      mbar_init(s_ready + 8 * i, NQ == 1 ? 4 + active0 : 4);
+      mbar_init(k_empty + 8 * i, NQ == 1 ? 1 : jobs);
+      mbar_init(pv_ready + 8 * i, NQ == 1 ? 4 + active0 : 4);
+      mbar_init(v_empty + 8 * i, NQ == 1 ? 1 : jobs);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + 8 * i, 4);
-      mbar_init(k_empty + 8 * i, 1);
-      mbar_init(v_full + 8 * i, 4);
-      mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, active);
       mbar_init(o_done + 8 * i, 1);
+      mbar_init(p_ready + 8 * i, max(i ? active1 : active0, 1));
     }
     mbar_init(all_done, 1);
+    mbar_init(all_done + 8, 1);
     s_abort = 0;
     mbar_init_fence();
   }
@@ -367,197 +638,259 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   grid_dependency_wait();
   grid_dependents_launch();
 
-  int L = p.seq_lens[b];
-  if (L < 0 || L > p.max_seq_len) {
-    if (split == 0 && kvh == 0 && threadIdx.x == 0) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
-    L = L < 0 ? 0 : p.max_seq_len;
-  }
-  const int tiles = (L + TOK - 1) / TOK;
-  const int tile0 = split * p.tps, n = min(p.tps, tiles - tile0);   // this CTA's tiles (n <= 0: none)
-
-  // q' of the CTA's columns as fp16 rows in the (still unused) tile rings
-  unsigned char* s_q = smem + G::K_OFF;
-  if (n > 0) {
-    fill_codebooks<MODE>(p, kvh, smem);
-    for (int c = warp; c < 32 * active; c += THREADS / 32) {
-      const QueryLoad r = load_query(p, b, kvh, c, lane, col0, nloc);   // zeros past the last column
-      const __half2 q01 = *reinterpret_cast<const __half2*>(&r.q.x), q23 = *reinterpret_cast<const __half2*>(&r.q.y);
-      float v[4] = {__low2float(q01) * r.s.x, __high2float(q01) * r.s.y, __low2float(q23) * r.s.z,
-                    __high2float(q23) * r.s.w};
-      fwht128_f32(v, lane);
-      *reinterpret_cast<uint2*>(s_q + c * Q_PITCH + 8 * lane) =
-          make_uint2(pack_half2(v[0] * p.qscale, v[1] * p.qscale), pack_half2(v[2] * p.qscale, v[3] * p.qscale));
+  flat_prefix<TOK / 16>(p, s_pref);
+  Pieces pc(s_pref, p.B, split, p.n_splits);
+  if (!pc.empty()) fill_codebooks<MODE>(p, kvh, smem);
+  if (split == 0)   // sequences without tokens
+    for (int i = threadIdx.x; i < p.B * nloc * kHeadDim; i += THREADS) {
+      const int bb = i / (nloc * kHeadDim), c = col0 + (i / kHeadDim) % nloc;
+      if (s_pref[bb + 1] == s_pref[bb]) p.out[out_row(p, bb, kvh, c) + (i & (kHeadDim - 1))] = __float2half_rn(0.f);
     }
-  }
   tcgen05_before_sync();
   __syncthreads();
   tcgen05_after_sync();
   const uint32_t tmem = s_tmem;
-  const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-  if (n > 0 && warp < active) {   // q' into tensor memory: lane = column
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t r[32];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(s_q + threadIdx.x * Q_PITCH + 128 * h + 16 * i);
-        r[4 * i] = x.x, r[4 * i + 1] = x.y, r[4 * i + 2] = x.z, r[4 * i + 3] = x.w;
-      }
-      tmem_st32(t_lane + T_Q + 32 * h, r);
-    }
-    tmem_wait_st();
-  }
-  tcgen05_before_sync();
-  __syncthreads();
-  tcgen05_after_sync();
+  uint32_t done = 0;   // tiles of earlier pieces
+  // q' of a piece's columns passes through the (idle) tile rings as fp16 rows
+  // of 256 bytes, 16-byte pieces permuted by the row
+  unsigned char* s_q = smem + G::K_OFF;
 
+  // Per piece, every role meets three times: q' staged; q' in tensor memory
+  // (and the staging area free); the piece's state written out.
   if (warp < SM_WARPS) {
-    // ---------------- softmax: thread = column col0 + threadIdx.x
-    const int cl = threadIdx.x, c = col0 + cl;
-    float m = kMInit, l = 0.f;
-    bool ok = warp < active;
-    if (ok && n > 0) {
-      const int prefix = L - p.M;            // tokens below it are visible to every column
-      unsigned long long mask = 0;
-      if (cl < nloc) {
-        mask = tree_mask[(size_t)b * p.M + c / p.g];
-        if (p.M < 64) mask &= (1ull << p.M) - 1;
-      }
-      for (int t = 0; t < n; ++t) {
-        const int st = t & 1;
-        if (!(ok = tr_wait(s_full + 8 * st, (t >> 1) & 1, abort_flag, p.err, 0xffffffffu))) break;
-        tcgen05_after_sync();
-        float x[2][32];
-        tmem_ld32(t_lane + T_S + 64 * st, x[0]);
-        tmem_ld32(t_lane + T_S + 64 * st + 32, x[1]);
-        tmem_wait_ld();
-        const int tok0 = (tile0 + t) * TOK, d = prefix - tok0;
-        if (d < TOK) {                       // bit i of vis: token tok0 + i is visible
-          unsigned long long vis = d >= 0 ? (mask << d) | ((1ull << d) - 1) : d > -64 ? mask >> -d : 0ull;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SM));
+    // ---------------- softmax warpgroup wg: thread = column c
+    const int wg = warp >> 2, row = threadIdx.x & (ROWS - 1);
+    const int cl = NQ == 1 ? row : wg * ROWS + row, c = col0 + cl;
+    const bool live = (warp & 3) < (wg ? active1 : active0);
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    if (NQ == 1 && live && lane == 0) mbar_arrive(s_ready + 8 * wg);   // no scores to read yet
+    for (int piece = 0; pc.next(); ++piece) {
+      stage_queries(p, pc.b, kvh, warp, lane, col0, nloc, s_q);
+      __syncthreads();
+      if (live && (NQ == 2 || wg == 0)) {   // q' into tensor memory: lane = column
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!((vis >> i) & 1)) x[i >> 5][i & 31] = neg_inf();
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4*>(s_q + cl * 256 + (((8 * h + i) ^ (cl & 15)) << 4));
+            r[4 * i] = x.x, r[4 * i + 1] = x.y, r[4 * i + 2] = x.z, r[4 * i + 3] = x.w;
+          }
+          tmem_st32(t_lane + TM::q(wg) + 32 * h, r);
         }
-        float top = fmaxf(x[0][0], x[1][0]);
-#pragma unroll
-        for (int i = 1; i < 32; ++i) top = fmaxf(top, fmaxf(x[0][i], x[1][i]));
-        if (__any_sync(0xffffffffu, top > m + kSoftmaxSlack)) {
-          const float mn = fmaxf(m, top), f = fast_exp2(m - mn);
-          m = mn;
-          l *= f;
-          if (t > 0) {   // O holds tiles 0 .. t - 1 once P.V of t - 1 is done
-            if (!(ok = tr_wait(o_done + 8 * (st ^ 1), ((t - 1) >> 1) & 1, abort_flag, p.err, 0xffffffffu))) break;
-            tcgen05_after_sync();
+        tmem_wait_st();
+      }
+      tcgen05_before_sync();
+      __syncthreads();
+      tcgen05_after_sync();
+      float m = kMInit, l = 0.f;
+      bool ok = live;
+      const int prefix = clamped_len(p, pc.b) - p.M;   // tokens below it are visible to every column
+      if (live) {
+        unsigned long long mask = 0;
+        if (cl < nloc) {
+          mask = tree_mask[(size_t)pc.b * p.M + c / p.g];
+          if (p.M < 64) mask &= (1ull << p.M) - 1;
+        }
+        ok = softmax_tiles_of<NQ, G::STAGES>(p, pc, done, wg, t_lane, mask, prefix, s_full, s_ready, NQ == 1 ? pv_ready : p_ready,
+                                  o_done, abort_flag, m, l);
+        if (NQ == 1) {   // this warpgroup's last tile of the piece, if it has one
+          const int last = pc.n - 1 - (int)((done + pc.n - 1 + wg) & 1);
+          if (ok && last >= 0) ok = tr_wait(o_done + 8 * wg, ((done + last) >> 1) & 1, abort_flag, p.err);
+        } else if (ok) {
+          ok = tr_wait(o_done + 8 * wg, piece & 1, abort_flag, p.err);
+        }
+        tcgen05_after_sync();
+      }
+      // NQ 1: the warpgroup of the piece's first tile takes in the other's
+      // state through shared memory (the tile rings are idle: every product of
+      // the piece is done), channel rows of ROWS columns
+      const int lead = NQ == 1 ? (int)(done & 1) : wg;
+      const bool both = NQ == 1 && pc.n > 1;
+      float* s_o = reinterpret_cast<float*>(smem + G::K_OFF);
+      float2* s_ml = reinterpret_cast<float2*>(smem + G::ML_OFF);
+      if (both) {
+        named_barrier_sync(1, SM_WARPS * 32);   // both warpgroups' last products are done
+        if (wg != lead && live && ok) {
+          s_ml[row] = make_float2(m, l);
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              float o[32];
-              tmem_ld32(t_lane + T_O + 32 * q, o);
-              tmem_wait_ld();
-              uint32_t r[32];
+          for (int q = 0; q < kHeadDim / 32; ++q) {
+            float o[32];
+            tmem_ld32(t_lane + T_O + kHeadDim * wg + 32 * q, o);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * f);
-              tmem_st32(t_lane + T_O + 32 * q, r);
+            for (int i = 0; i < 32; ++i) s_o[(32 * q + i) * ROWS + row] = o[i];
+          }
+        }
+        named_barrier_sync(1, SM_WARPS * 32);
+      }
+      if (wg == lead && live && ok && !*abort_flag) {
+        float fa = 1.f, fb = 0.f;
+        if (both) {
+          const float2 other = s_ml[row];
+          const float mn = fmaxf(m, other.x);
+          fa = fast_exp2(m - mn), fb = fast_exp2(other.x - mn);
+          m = mn;
+          l = l * fa + other.y * fb;
+        }
+        const bool whole = pc.n == pc.all;
+        if (whole) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          fa *= inv, fb *= inv;
+        }
+        float* part = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + split + pc.b) * p.ncols + c) * kPartialStride;
+#pragma unroll 1
+        for (int q = 0; q < kHeadDim / 32; ++q) {
+          float o[32];
+          tmem_ld32(t_lane + T_O + kHeadDim * wg + 32 * q, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = both ? o[i] * fa + s_o[(32 * q + i) * ROWS + row] * fb : o[i] * fa;
+          if (cl < nloc && !whole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(part + 32 * q + 4 * i) =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          } else if (cl < nloc) {
+            __half* dst = p.out + out_row(p, pc.b, kvh, c) + 32 * q;
+            if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(dst + 8 * i) =
+                    make_uint4(pack_half2(o[8 * i], o[8 * i + 1]), pack_half2(o[8 * i + 2], o[8 * i + 3]),
+                               pack_half2(o[8 * i + 4], o[8 * i + 5]), pack_half2(o[8 * i + 6], o[8 * i + 7]));
+            } else {   // out needs only 2-byte alignment
+#pragma unroll
+              for (int i = 0; i < 32; ++i) dst[i] = __float2half_rn(o[i]);
             }
           }
         }
-        uint32_t r[32];
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float p0 = fast_exp2(x[i >> 4][(2 * i) & 31] - m), p1 = fast_exp2(x[i >> 4][(2 * i + 1) & 31] - m);
-          l0 += p0;
-          l1 += p1;
-          r[i] = pack_half2(p0, p1);
-        }
-        l += l0 + l1;
-        tmem_st32(t_lane + T_P + 32 * st, r);
-        tmem_wait_st();
-        tcgen05_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * st);
+        if (!whole && cl < nloc) *reinterpret_cast<float2*>(part + 128) = make_float2(m, l);
       }
-      if (ok) ok = tr_wait(o_done + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, p.err, 0xffffffffu);
+      done += pc.n;
+      tcgen05_before_sync();
+      __syncthreads();
       tcgen05_after_sync();
-    }
-    if (ok) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const bool whole = p.n_splits == 1;
-      float* part = p.partials + (((size_t)(b * p.Hkv + kvh) * p.n_splits + split) * p.ncols + c) * kPartialStride;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        float o[32];
-        if (n > 0) {
-          tmem_ld32(t_lane + T_O + 32 * q, o);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        }
-        if (cl < nloc && !whole) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(part + 32 * q + 4 * i) =
-                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else if (cl < nloc) {
-          __half* dst = p.out + out_row(p, b, kvh, c) + 32 * q;
-          if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(dst + 8 * i) =
-                  make_uint4(pack_half2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_half2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                             pack_half2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_half2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-          } else {   // out needs only 2-byte alignment
-#pragma unroll
-            for (int i = 0; i < 32; ++i) dst[i] = __float2half_rn(o[i] * inv);
-          }
-        }
-      }
-      if (!whole && cl < nloc) *reinterpret_cast<float2*>(part + 128) = make_float2(m, l);
     }
   } else if (warp < MMA_WARP) {
     // ---------------- dequantisation
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DQ));
     const int dw = warp - SM_WARPS, u = dw & 3;
-    if (n > 0) {
+    while (pc.next()) {
+      stage_queries(p, pc.b, kvh, warp, lane, col0, nloc, s_q);
+      __syncthreads();
+      __syncthreads();
+      const int L = clamped_len(p, pc.b);
       if (dw < 4)
-        dequant_loop<MODE, VQKV_ROLE_K, PAGED>(p, b, kvh, tile0, n, L, smem, k_full, k_empty, u, lane, abort_flag);
+        dequant_loop<MODE, VQKV_ROLE_K, PAGED>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, s_ready, k_empty, u, lane,
+                                               abort_flag);
       else
-        dequant_loop<MODE, VQKV_ROLE_V, PAGED>(p, b, kvh, tile0, n, L, smem, v_full, v_empty, u, lane, abort_flag);
+        dequant_loop<MODE, VQKV_ROLE_V, PAGED>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, pv_ready, v_empty, u, lane,
+                                               abort_flag);
+      done += pc.n;
+      __syncthreads();
     }
-  } else if (lane == 0 && n > 0) {
-    // ---------------- one thread issues the products
-    constexpr uint32_t idesc_s = umma_idesc_f16_f32(COLS, TOK);
-    constexpr uint32_t idesc_o = umma_idesc_f16_f32(COLS, kHeadDim) | kIdescBMnMajor;
-    const uint32_t k_smem = smem_u32(smem + G::K_OFF), v_smem = smem_u32(smem + G::V_OFF);
-    auto scores = [&](int t) -> bool {
-      const int st = t & 1;
-      if (!tr_wait(k_full + 8 * st, (t >> 1) & 1, abort_flag, p.err, 1u)) return false;
-      tcgen05_after_sync();
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
+    // ---------------- the products.  An issuing warp waits and computes the
+    // operands' addresses as one, so they stay in uniform registers, and an
+    // elected lane issues.  Issue blocks while the tensor cores are busy, so
+    // two warps share it, one waiting while the other's products run: NQ 1,
+    // score products and P.V products; NQ 2, query tile 0 and query tile 1 (a
+    // tile's score product must follow its last P.V product: same warp, in
+    // order).
+    constexpr uint32_t idesc_s = umma_idesc_f16_f32(ROWS, TOK);
+    constexpr uint32_t idesc_o = umma_idesc_f16_f32(ROWS, kHeadDim) | kIdescBMnMajor;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t k_desc = umma_desc_sw128(smem_u32(smem + G::K_OFF), 1024, 16);
+    const uint64_t v_desc = umma_desc_sw128(smem_u32(smem + G::V_OFF), 1024, HALF);
+    const uint32_t k_lo = (uint32_t)k_desc, k_hi = (uint32_t)(k_desc >> 32);
+    const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
+    const bool issuer = elect_one();
+    // S of warpgroup wg (query tile qt) from the K tile in stage st: 16
+    // channels a step, 32 bytes of a 128-byte row, four per 64-channel half
+    auto scores = [&](uint32_t st, uint32_t wg, uint32_t qt) {
+      const uint32_t lo = k_lo + st * (TILE_SMEM / 16), ds = tm + T_S + TOK * wg, aq = tm + TM::q(qt);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)   // 16 channels each: 32 bytes of a 128-byte row, four per 64-channel half
-        umma_f16_ts(tmem + T_S + 64 * st, tmem + T_Q + 8 * k,
-                    umma_desc_sw128(k_smem + st * TILE_SMEM + (k >> 2) * HALF + (k & 3) * 32, 1024, 16), idesc_s, k > 0);
-      umma_commit(s_full + 8 * st);
-      umma_commit(k_empty + 8 * st);
-      return true;
+      for (int k = 0; k < 8; ++k)
+        umma_f16_ts(ds, aq + 8 * k, lo + ((k >> 2) * HALF + (k & 3) * 32) / 16, k_hi, idesc_s, k > 0);
+      umma_commit(s_full + 8 * wg);
     };
-    bool ok = scores(0);
-    for (int t = 0; ok && t < n; ++t) {
-      const int st = t & 1;
-      if (t + 1 < n) ok = scores(t + 1);
-      ok = ok && tr_wait(v_full + 8 * st, (t >> 1) & 1, abort_flag, p.err, 1u);
-      ok = ok && tr_wait(p_full + 8 * st, (t >> 1) & 1, abort_flag, p.err, 1u);
-      if (!ok) break;
-      tcgen05_after_sync();
+    // O of warpgroup wg += P V: 16 tokens a step, two 8-token groups
+    auto values = [&](uint32_t st, uint32_t wg, bool fresh) {
+      const uint32_t lo = v_lo + st * (TILE_SMEM / 16), dv = tm + T_O + kHeadDim * wg, ap = tm + TM::p(wg);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)   // 16 tokens each: two 8-token groups
-        umma_f16_ts(tmem + T_O, tmem + T_P + 32 * st + 8 * k,
-                    umma_desc_sw128(v_smem + st * TILE_SMEM + k * 2048, 1024, HALF), idesc_o, t > 0 || k > 0);
-      umma_commit(v_empty + 8 * st);
-      umma_commit(o_done + 8 * st);
+      for (int k = 0; k < 4; ++k) umma_f16_ts(dv, ap + 8 * k, lo + k * (2048 / 16), v_hi, idesc_o, !fresh || k > 0);
+    };
+    bool ok = true;
+    while (pc.next()) {
+      __syncthreads();
+      tcgen05_before_sync();
+      __syncthreads();
+      tcgen05_after_sync();
+      const int n = pc.n;
+      const int job = warp - MMA_WARP;
+      if (NQ == 1 && job == 0) {
+        for (int t = 0; ok && t < n; ++t) {
+          const uint32_t k = done + t, st = k % ST;
+          if (!(ok = tr_wait(s_ready + 8 * st, (k / ST) & 1, abort_flag, p.err))) break;
+          tcgen05_after_sync();
+          if (issuer) {
+            scores(st, k & 1, 0);
+            umma_commit(k_empty + 8 * st);
+          }
+          __syncwarp();
+        }
+      } else if (NQ == 1 && job == 1) {
+        for (int t = 0; ok && t < n; ++t) {
+          const uint32_t k = done + t, st = k % ST;
+          if (!(ok = tr_wait(pv_ready + 8 * st, (k / ST) & 1, abort_flag, p.err))) break;
+          tcgen05_after_sync();
+          if (issuer) {
+            values(st, k & 1, t < 2);
+            umma_commit(v_empty + 8 * st);
+            umma_commit(o_done + 8 * (k & 1));
+          }
+          __syncwarp();
+        }
+      } else if (NQ == 2 && job < jobs) {
+        for (int t = 0; ok && t <= n; ++t) {   // P.V of tile t - 1, then S of tile t
+          const uint32_t k = done + t;
+          if (t > 0) {
+            const uint32_t j = k - 1, st = j % ST;
+            ok = tr_wait(pv_ready + 8 * st, (j / ST) & 1, abort_flag, p.err) &&
+                 tr_wait(p_ready + 8 * job, j & 1, abort_flag, p.err);
+            if (!ok) break;
+            tcgen05_after_sync();
+            if (issuer) {
+              values(st, job, t == 1);
+              umma_commit(v_empty + 8 * st);
+              if (t == n) umma_commit(o_done + 8 * job);
+            }
+            __syncwarp();
+          }
+          if (t < n) {
+            const uint32_t st = k % ST;
+            if (!(ok = tr_wait(s_ready + 8 * st, (k / ST) & 1, abort_flag, p.err))) break;
+            tcgen05_after_sync();
+            if (issuer) {
+              scores(st, job, job);
+              umma_commit(k_empty + 8 * st);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      done += n;
+      __syncthreads();
     }
-    // every product issued has completed before the tensor memory is freed
-    umma_commit(all_done);
-    tr_wait(all_done, 0, abort_flag, p.err, 1u);
+    if (warp < MMA_WARP + 2) {   // every product issued has completed before the tensor memory is freed
+      const uint32_t mine = all_done + 8 * (warp - MMA_WARP);
+      if (issuer) umma_commit(mine);
+      __syncwarp();
+      tr_wait(mine, 0, abort_flag, p.err);
+    }
   }
   __syncwarp();
   tcgen05_before_sync();
@@ -566,17 +899,87 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   if (warp == MMA_WARP) tmem_dealloc(tmem, T_COLS);
 }
 
+// Merges the partials of softmax column blockIdx.x % ncols of KV head
+// blockIdx.x / ncols of sequence blockIdx.y, where several shares overlap it.
+// Warp w takes partials w, w + 8, ..., four in flight; lane = 4 channels; the
+// warps meet in shared memory.
+constexpr int TC_WARPS = 8;
+__global__ void __launch_bounds__(TC_WARPS * 32) tree_combine_kernel(const DecodeParams p) {
+  constexpr int U = 4;
+  __shared__ int s_sum[2][TC_WARPS];
+  __shared__ float4 s_o[TC_WARPS][32];
+  __shared__ float2 s_ml[TC_WARPS];
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.x / p.ncols, c = blockIdx.x - kvh * p.ncols;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  int before = 0, total = 0;   // tiles of the sequences before b, of all
+  for (int i = threadIdx.x; i < p.B; i += TC_WARPS * 32) {
+    const int t = (clamped_len(p, i) + tr::TOK - 1) / tr::TOK;
+    total += t;
+    if (i < b) before += t;
+  }
+  const int mine = (clamped_len(p, b) + tr::TOK - 1) / tr::TOK;
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) s_sum[0][warp] = before, s_sum[1][warp] = total;
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < TC_WARPS; ++w) before += s_sum[0][w], total += s_sum[1][w];
+  if (mine == 0) return;
+  const int S = min(p.n_splits, total);
+  const int s0 = flat_cta_of(before, total, S), parts = flat_cta_of(before + mine - 1, total, S) - s0 + 1;
+  if (parts == 1) return;   // its share wrote O
+  const size_t stride = (size_t)p.ncols * kPartialStride;
+  const float* base = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + s0 + b) * p.ncols + c) * kPartialStride;
+  float M = kMInit, l = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float2 ml, float4 o) {
+    const float n = fmaxf(M, ml.x), fa = fast_exp2(M - n), fb = fast_exp2(ml.x - n);
+    O.x = O.x * fa + o.x * fb, O.y = O.y * fa + o.y * fb, O.z = O.z * fa + o.z * fb, O.w = O.w * fa + o.w * fb;
+    l = l * fa + ml.y * fb;
+    M = n;
+  };
+  for (int i0 = warp; i0 < parts; i0 += U * TC_WARPS) {
+    float2 ml[U];
+    float4 o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * TC_WARPS;
+      if (i < parts) {
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(base + i * stride + 128));
+        o[u] = __ldcg(reinterpret_cast<const float4*>(base + i * stride) + lane);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * TC_WARPS < parts) add(ml[u], o[u]);
+  }
+  s_o[warp][lane] = O;
+  if (lane == 0) s_ml[warp] = make_float2(M, l);
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < TC_WARPS; ++w) add(s_ml[w], s_o[w][lane]);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  __half* dst = p.out + out_row(p, b, kvh, c) + 4 * lane;   // out needs only 2-byte alignment
+  dst[0] = __float2half_rn(O.x * inv), dst[1] = __float2half_rn(O.y * inv);
+  dst[2] = __float2half_rn(O.z * inv), dst[3] = __float2half_rn(O.w * inv);
+}
+
 using TreeKernel = void (*)(DecodeParams, const unsigned long long*);
 template <int MODE>
-TreeKernel tree_of(bool paged) {
-  return paged ? (TreeKernel)decode_tree_kernel<MODE, true> : (TreeKernel)decode_tree_kernel<MODE, false>;
+TreeKernel tree_of(bool paged, bool wide) {
+  return wide ? (paged ? (TreeKernel)decode_tree_kernel<MODE, true, 2> : (TreeKernel)decode_tree_kernel<MODE, false, 2>)
+              : (paged ? (TreeKernel)decode_tree_kernel<MODE, true, 1> : (TreeKernel)decode_tree_kernel<MODE, false, 1>);
 }
-TreeKernel tree_kernel(int mode, bool paged) {
-  return mode == VQKV_MODE_VQ2    ? tree_of<VQKV_MODE_VQ2>(paged)
-         : mode == VQKV_MODE_VQ4  ? tree_of<VQKV_MODE_VQ4>(paged)
-         : mode == VQKV_MODE_VQ3  ? tree_of<VQKV_MODE_VQ3>(paged)
-         : mode == VQKV_MODE_VQ15 ? tree_of<VQKV_MODE_VQ15>(paged)
-                                  : tree_of<VQKV_MODE_VQ125>(paged);
+TreeKernel tree_kernel(int mode, bool paged, bool wide) {
+  return mode == VQKV_MODE_VQ2    ? tree_of<VQKV_MODE_VQ2>(paged, wide)
+         : mode == VQKV_MODE_VQ4  ? tree_of<VQKV_MODE_VQ4>(paged, wide)
+         : mode == VQKV_MODE_VQ3  ? tree_of<VQKV_MODE_VQ3>(paged, wide)
+         : mode == VQKV_MODE_VQ15 ? tree_of<VQKV_MODE_VQ15>(paged, wide)
+                                  : tree_of<VQKV_MODE_VQ125>(paged, wide);
 }
 int tree_smem(int mode) {
   return mode == VQKV_MODE_VQ15 || mode == VQKV_MODE_VQ125 ? tr::Geo<VQKV_MODE_VQ15>::SMEM : tr::Geo<VQKV_MODE_VQ2>::SMEM;
@@ -584,20 +987,23 @@ int tree_smem(int mode) {
 
 }  // namespace
 
-int decode_tree_cols() { return tr::COLS; }
-int decode_tree_tile() { return tr::TOK; }
+int decode_tree_cols(int ncols) { return ncols > tr::ROWS ? 2 * tr::ROWS : tr::ROWS; }
 
 cudaError_t decode_tree_prepare(int mode) {
   cudaError_t e = cudaSuccess;
-  for (int paged = 0; paged < 2 && e == cudaSuccess; ++paged)
-    e = cudaFuncSetAttribute(tree_kernel(mode, paged != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem(mode));
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+    e = cudaFuncSetAttribute(tree_kernel(mode, (i & 1) != 0, i >= 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             tree_smem(mode));
   return e;
 }
 
-cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, dim3 grid,
-                               cudaStream_t stream) {
-  return launch_pdl(tree_kernel(mode, p.block_table != nullptr), grid, dim3(tr::THREADS), (size_t)tree_smem(mode), stream, p,
-                    tree_mask);
+cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, cudaStream_t stream) {
+  const bool wide = p.ncols > tr::ROWS;
+  cudaError_t e = launch_pdl(tree_kernel(mode, p.block_table != nullptr, wide), dim3(p.n_splits, p.Hkv, p.cgroups),
+                             dim3(tr::THREADS), (size_t)tree_smem(mode), stream, p, tree_mask);
+  if (e == cudaSuccess && p.n_splits > 1)
+    e = launch_pdl(tree_combine_kernel, dim3(p.Hkv * p.ncols, p.B), dim3(TC_WARPS * 32), 0, stream, p);
+  return e;
 }
 
 }  // namespace vqkv

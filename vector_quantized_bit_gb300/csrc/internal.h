@@ -109,15 +109,12 @@ size_t decode_ticket_region_bytes(int B, int Hkv);       // error word + tickets
 cudaError_t decode_mass_prepare(int mode);
 cudaError_t launch_decode_mass(int mode, const DecodeParams& p, dim3 grid, cudaStream_t stream);
 
-// Draft-tree attention (decode_tree.cu): partials as in the split plan,
-// [B][Hkv][n_splits][ncols], always merged by launch_combine (n_splits > 1);
-// grid (n_splits, Hkv, B x cgroups), cgroups groups of decode_tree_cols()
-// columns, splits of p.tps tiles of decode_tree_tile() tokens.
-int decode_tree_cols();
-int decode_tree_tile();
+// Draft-tree attention (decode_tree.cu), B <= kFlatMaxB: n_splits shares per
+// (KV head, column group of decode_tree_cols(ncols) columns); partials
+// [Hkv][n_splits + B - 1][ncols], indexed by share + sequence as in the flat plan.
+int decode_tree_cols(int ncols);
 cudaError_t decode_tree_prepare(int mode);
-cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, dim3 grid,
-                               cudaStream_t stream);
+cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, cudaStream_t stream);
 
 // Cache editing (cache_edit.cu): the in-place move of chosen tokens, and the
 // choice of the tokens a sequence keeps.
