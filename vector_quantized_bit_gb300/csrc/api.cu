@@ -303,7 +303,7 @@ vqkv_status plan_mass(const vqkv_decode_mass_args* am, MassPlan* pl) {
 // run as several launches of up to kFlatMaxB sequences.
 struct TreePlan {
   int n_splits = 1, cgroups = 1;
-  size_t ws_bytes = 0;
+  size_t partials_off = 0, ws_bytes = 0;   // error word, transformed queries, partials
 };
 
 vqkv_status validate_tree_sizes(const vqkv_decode_tree_args* at) {
@@ -330,7 +330,8 @@ vqkv_status plan_tree(const vqkv_decode_tree_args* at, TreePlan* pl) {
   const long long tiles = std::max<long long>(1, (long long)B * ((a->max_seq_len + 63) / 64));
   const long long want = a->num_splits > 0 ? std::min(a->num_splits, 1024) : di.sms / ((long long)a->Hkv * pl->cgroups);
   pl->n_splits = (int)std::max<long long>(1, std::min(want, tiles));
-  pl->ws_bytes = kWsHeader;
+  pl->partials_off = kWsHeader + round_up(decode_tree_query_bytes(B, a->Hkv, cols), 256);
+  pl->ws_bytes = pl->partials_off;
   if (pl->n_splits > 1)
     pl->ws_bytes += sizeof(float) * (size_t)a->Hkv * (pl->n_splits + B - 1) * cols * kPartialStride;
   return VQKV_OK;
@@ -703,7 +704,7 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_pa
   if (!aligned(a->workspace, 256)) return VQKV_ERR_INVALID_ARG;
   unsigned char* ws = static_cast<unsigned char*>(a->workspace);
   DecodeParams p = packed_params(a, at->n_queries, pg);
-  p.partials = reinterpret_cast<float*>(ws + kWsHeader);
+  p.partials = reinterpret_cast<float*>(ws + pl.partials_off);
   p.cgroups = pl.cgroups;
   p.n_splits = pl.n_splits;
   const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(at->tree_mask);
@@ -720,7 +721,8 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_pa
       c.kc = p.kc + (size_t)b0 * p.Hkv * p.stream_bytes;
       c.vc = p.vc + (size_t)b0 * p.Hkv * p.stream_bytes;
     }
-    if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, ws + kWsHeader, static_cast<cudaStream_t>(stream)) !=
+        cudaSuccess)
       return VQKV_ERR_CUDA;
   }
   return VQKV_OK;

@@ -5,7 +5,7 @@
 // 128 or 256 columns (MMA rows) of one KV head and walks its share of the
 // batch's tokens in tiles of 64:
 //   dequantise  K' and V tiles into shared memory, each centroid gathered
-//               once per tile and CTA (8 warps: 4 for K, 4 for V)
+//               once per tile and CTA (16 warps: 8 for K, 8 for V)
 //   S = Q' K'^T 128 x 64 x 128, Q' in tensor memory (A), K' rows in shared
 //               memory (B, K-major), S in tensor memory
 //   softmax     one thread per column: running max and sum in fp32, P =
@@ -16,7 +16,7 @@
 // There are two softmax warpgroups with an S, P, O, max and sum each.  Up to
 // 128 columns (NQ = 1) they take the tiles in turn (one warpgroup alone spends
 // more time on a tile's 64 exponentials per thread than everything else
-// takes), and the second's state is merged into the first's at the end; a
+// takes), and their states are merged at the end; a
 // warpgroup's next score product is issued as soon as it has read its last
 // scores.  Above 128 columns (NQ = 2) each warpgroup takes 128 columns of
 // every tile, so one dequantisation serves 256; P then overlays S (tensor
@@ -48,17 +48,17 @@ namespace {
 namespace tr {
 constexpr int ROWS = 128;                 // MMA rows: softmax columns of one query tile
 constexpr int TOK = 64;                   // tokens per tile
-constexpr int SM_WARPS = 8, DQ_WARPS = 8; // two softmax warpgroups
+constexpr int SM_WARPS = 8, DQ_WARPS = 16; // two softmax warpgroups, four dequantising ones
 constexpr int MMA_WARP = SM_WARPS + DQ_WARPS;
 constexpr int THREADS = (MMA_WARP + 4) * 32;   // whole warpgroups, for the register split
-// Registers per thread: 96 at launch (640 threads), then 128 for the softmax
-// warpgroups (64 scores and 16 packed weights are live), 88 for the
-// dequantising ones, 40 for the last: 2 x 128 x 128 + 2 x 128 x 88 + 128 x 40
-// = 60,416 of the launch's 640 x 96 = 61,440.
-constexpr int REGS_SM = 128, REGS_DQ = 88, REGS_MMA = 40;
+// Registers per thread: 72 at launch (896 threads), then 120 for the softmax
+// warpgroups (64 scores and 16 packed weights are live), 56 for the
+// dequantising ones (32 hold gathered centroids), 40 for the last:
+// 256 x 120 + 512 x 56 + 128 x 40 = 64,512 = 896 x 72.
+constexpr int REGS_SM = 120, REGS_DQ = 56, REGS_MMA = 40;
 constexpr int TILE_SMEM = TOK * 256;      // one dequantised K or V tile: two 64-channel halves of 64 x 128 bytes
 constexpr int HALF = TOK * 128;
-constexpr int PREFETCH = 4;               // tiles whose codes a dequantising warp holds in registers
+constexpr int PREFETCH = 2;               // of its tiles, whose codes a dequantising warp holds in registers
 // tensor memory columns: O, S and P of each softmax warpgroup, then q'
 constexpr uint32_t T_O = 0, T_S = 256, T_COLS = 512;
 template <int NQ>
@@ -76,8 +76,8 @@ struct Geo {
   static constexpr int STAGES = CB_BYTES == 65536 ? 4 : 2;
   static constexpr int K_OFF = CB_BYTES, V_OFF = K_OFF + STAGES * TILE_SMEM;
   static constexpr int BAR_OFF = V_OFF + STAGES * TILE_SMEM;
-  static constexpr int ML_OFF = BAR_OFF + 256;             // a warpgroup's max and sum per column, for the merge
-  static constexpr int PREF_OFF = ML_OFF + ROWS * 8;       // tiles of the sequences before each
+  static constexpr int ML_OFF = BAR_OFF + 256;             // the warpgroups' max and sum per column, for the merge
+  static constexpr int PREF_OFF = ML_OFF + 2 * ROWS * 8;       // tiles of the sequences before each
   static constexpr int SMEM = PREF_OFF + (kFlatMaxB + 1) * 4;
   static constexpr int LAYOUT_TOK = MODE == VQKV_MODE_VQ15 ? 64 : 16;
   static constexpr int TILE_BYTES = MODE == VQKV_MODE_VQ2    ? 512
@@ -89,8 +89,7 @@ struct Geo {
   static constexpr int KW = MODE == VQKV_MODE_VQ2 ? 4 : MODE == VQKV_MODE_VQ4 ? 8 : MODE == VQKV_MODE_VQ3 ? 6 : 3;
   static constexpr int VW = MODE == VQKV_MODE_VQ125 ? 5 : KW;
   static constexpr int W = VW;
-  static_assert(2 * ROWS * 256 <= 2 * STAGES * TILE_SMEM, "staged q' uses the K and V rings before the loop");
-  static_assert(ROWS * kHeadDim * 4 <= 2 * STAGES * TILE_SMEM, "the merge of O uses them after it");
+  static_assert(SM_WARPS * 32 * 32 * 4 <= 2 * STAGES * TILE_SMEM, "the epilogue's boxes are in the rings");
   static_assert(SMEM <= 226 * 1024, "shared memory");
 };
 }  // namespace tr
@@ -386,19 +385,21 @@ __device__ __forceinline__ bool tr_wait(uint32_t mbar, uint32_t parity, volatile
   return tr_wait_long(mbar, parity, abort_flag, err);
 }
 
-// The dequantising warp of (role, 16-token group u of each tile) over n tiles
-// of sequence b from tile0 on; done: tiles the CTA has taken before (ring
-// phases).  Codes are loaded PREFETCH tiles ahead into registers, block ids
-// one tile further.
+// The dequantising warp of (role, 16-token group u) over every other tile of a
+// piece (those whose number, counted over the CTA's pieces, has parity
+// `half`; done: tiles of earlier pieces).  Codes are loaded PREFETCH of its
+// tiles ahead into registers, block ids one further; the first ones before
+// the CTA meets (tile rings free).
 template <int MODE, int ROLE, bool PAGED>
-__device__ __forceinline__ void dequant_loop(const DecodeParams& p, int b, int kvh, int tile0, int n, int L, uint32_t done,
-                                             unsigned char* smem, uint32_t full, uint32_t empty, int u, int lane,
-                                             volatile int* abort_flag) {
+__device__ __forceinline__ void dequant_piece(const DecodeParams& p, int b, int kvh, int tile0, int n, int L, uint32_t done,
+                                              unsigned char* smem, uint32_t full, uint32_t empty, int u, int half,
+                                              int lane, volatile int* abort_flag) {
   using G = tr::Geo<MODE>;
   const uint8_t* codes = ROLE == VQKV_ROLE_K ? p.kc : p.vc;
   const int last_group = (L + 15) >> 4;   // 16-token groups that hold tokens
   uint32_t w[tr::PREFETCH][G::W];
   bool bad = false;
+  const int mine = (int)((done + half) & 1);   // its first tile
   // byte offset of the layout tile of this warp's group of tile t, -1 past the sequence
   const int t_end = min(n, (last_group - u + 3) / 4 - tile0);   // tiles whose group u holds tokens
   constexpr int STEP = G::LAYOUT_TOK == 64 ? G::TILE_BYTES : 4 * G::TILE_BYTES;
@@ -417,12 +418,13 @@ __device__ __forceinline__ void dequant_loop(const DecodeParams& p, int b, int k
     }
   };
 #pragma unroll
-  for (int d = 0; d < tr::PREFETCH; ++d) fetch(place(d), w[d]);
-  long long next = place(tr::PREFETCH);
-  for (int t0 = 0; t0 < n; t0 += tr::PREFETCH) {
+  for (int d = 0; d < tr::PREFETCH; ++d) fetch(place(mine + 2 * d), w[d]);
+  long long next = place(mine + 2 * tr::PREFETCH);
+  __syncthreads();   // q' is in tensor memory, the rings are free
+  for (int t0 = mine; t0 < n; t0 += 2 * tr::PREFETCH) {
 #pragma unroll
     for (int d = 0; d < tr::PREFETCH; ++d) {
-      const int t = t0 + d;
+      const int t = t0 + 2 * d;
       if (t >= n) break;
       const uint32_t k = done + t, st = k % G::STAGES;
       Centroids c;   // the gathers need no free stage: their latency overlaps the wait
@@ -431,7 +433,7 @@ __device__ __forceinline__ void dequant_loop(const DecodeParams& p, int b, int k
       else
         gather_v<MODE>(smem, lane, w[d], c);
       fetch(next, w[d]);
-      next = place(t + tr::PREFETCH + 1);
+      next = place(t + 2 * tr::PREFETCH + 2);
       if (!tr_wait(empty + 8 * st, ((k / G::STAGES) & 1) ^ 1, abort_flag, p.err)) return;
       unsigned char* tile = smem + (ROLE == VQKV_ROLE_K ? G::K_OFF : G::V_OFF) + st * tr::TILE_SMEM;
       if constexpr (ROLE == VQKV_ROLE_K)
@@ -565,34 +567,66 @@ __device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Pi
   return true;
 }
 
-// q' of the CTA's columns as fp16 rows of 256 bytes at s_q, 16-byte pieces
-// permuted by the row, zeros past the last column; the softmax and the
-// dequantising warps, four columns at a time each.
-__device__ __forceinline__ void stage_queries(const DecodeParams& p, int b, int kvh, int warp, int lane, int col0, int nloc,
-                                              unsigned char* s_q) {
-  constexpr int W = tr::SM_WARPS + tr::DQ_WARPS;
-  for (int c0 = warp; c0 < (nloc + 31) / 32 * 32; c0 += 4 * W) {
-    QueryLoad r[4];
+// q' of every softmax column as fp16, in the order the attention kernel's
+// threads load it: [B][Hkv][groups of 32 columns][16 pieces of 8 channels][32
+// columns], zeros past the last column.  A kernel of its own because every
+// share of a sequence needs the same rows (19 of them at 8 KV heads): doing it
+// per share took 2.2 us of each CTA at 64 columns and 6.4 us at 256.  It runs
+// while the attention kernel fills its codebooks.
+// Four lanes share a column, 32 channels each: five stages of the
+// Walsh-Hadamard transform are in registers, two across lanes.
+// grid (groups, Hkv, B), 128 threads.
+__global__ void __launch_bounds__(128) tree_query_kernel(const DecodeParams p, uint4* qx) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int kvh = blockIdx.y, b = blockIdx.z, part = threadIdx.x & 3;
+  const int r = threadIdx.x >> 2, c = 32 * blockIdx.x + r;
+  float v[32];
+  if (c < p.ncols) {
+    const int m = c / p.g, hq = kvh * p.g + c - m * p.g;
+    const float4* s4 = reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 32 * part);
+    const uint2* q = reinterpret_cast<const uint2*>(p.q + (((size_t)b * p.M + m) * p.Hq + hq) * kHeadDim + 32 * part);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = load_query(p, b, kvh, c0 + i * W, lane, col0, nloc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = c0 + i * W;
-      const __half2 q01 = *reinterpret_cast<const __half2*>(&r[i].q.x), q23 = *reinterpret_cast<const __half2*>(&r[i].q.y);
-      float v[4] = {__low2float(q01) * r[i].s.x, __high2float(q01) * r[i].s.y, __low2float(q23) * r[i].s.z,
-                    __high2float(q23) * r[i].s.w};
-      fwht128_f32(v, lane);
-      if (c < (nloc + 31) / 32 * 32)
-        *reinterpret_cast<uint2*>(s_q + c * 256 + (((lane >> 1) ^ (c & 15)) << 4) + 8 * (lane & 1)) =
-            make_uint2(pack_half2(v[0] * p.qscale, v[1] * p.qscale), pack_half2(v[2] * p.qscale, v[3] * p.qscale));
+    for (int i = 0; i < 8; ++i) {   // q is 8-byte aligned
+      const uint2 x = q[i];
+      const float4 f = s4[i];
+      const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
+      const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
+      v[4 * i] = lo.x * f.x, v[4 * i + 1] = lo.y * f.y, v[4 * i + 2] = hi.x * f.z, v[4 * i + 3] = hi.y * f.w;
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+  }
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(i & h)) {
+        const float x = v[i], y = v[i + h];
+        v[i] = x + y, v[i + h] = x - y;
+      }
+#pragma unroll
+  for (int h = 1; h < 4; h <<= 1) {
+    const float sign = (part & h) ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __fmaf_rn(v[i], sign, __shfl_xor_sync(0xffffffffu, v[i], h));
+  }
+  uint4* dst = qx + ((((size_t)b * p.Hkv + kvh) * gridDim.x + blockIdx.x) * 16 + 4 * part) * 32 + r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack_half2(v[8 * j + 2 * i] * p.qscale, v[8 * j + 2 * i + 1] * p.qscale);
+    dst[32 * j] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
 // grid (shares, Hkv, column groups of 128 NQ).
 template <int MODE, bool PAGED, int NQ>
 __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const DecodeParams p,
-                                                                     const unsigned long long* tree_mask) {
+                                                                     const unsigned long long* tree_mask,
+                                                                     const uint4* qx) {
   using namespace tr;
   using G = Geo<MODE>;
   using TM = Tmem<NQ>;
@@ -635,12 +669,14 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     mbar_init_fence();
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(&s_tmem), T_COLS);
-  grid_dependency_wait();
-  grid_dependents_launch();
-
+  // The query kernel right before this one lets it start only when everything
+  // before that has completed, and writes nothing but qx: the codebooks and
+  // lengths may be read now, qx (and any output written) after the wait.
+  fill_codebooks<MODE>(p, kvh, smem);
   flat_prefix<TOK / 16>(p, s_pref);
   Pieces pc(s_pref, p.B, split, p.n_splits);
-  if (!pc.empty()) fill_codebooks<MODE>(p, kvh, smem);
+  grid_dependency_wait();
+  grid_dependents_launch();
   if (split == 0)   // sequences without tokens
     for (int i = threadIdx.x; i < p.B * nloc * kHeadDim; i += THREADS) {
       const int bb = i / (nloc * kHeadDim), c = col0 + (i / kHeadDim) % nloc;
@@ -651,12 +687,8 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   tcgen05_after_sync();
   const uint32_t tmem = s_tmem;
   uint32_t done = 0;   // tiles of earlier pieces
-  // q' of a piece's columns passes through the (idle) tile rings as fp16 rows
-  // of 256 bytes, 16-byte pieces permuted by the row
-  unsigned char* s_q = smem + G::K_OFF;
-
-  // Per piece, every role meets three times: q' staged; q' in tensor memory
-  // (and the staging area free); the piece's state written out.
+  // Per piece, every role meets twice: q' in tensor memory; the piece's
+  // state written out.
   if (warp < SM_WARPS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SM));
     // ---------------- softmax warpgroup wg: thread = column c
@@ -666,15 +698,14 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     if (NQ == 1 && live && lane == 0) mbar_arrive(s_ready + 8 * wg);   // no scores to read yet
     for (int piece = 0; pc.next(); ++piece) {
-      stage_queries(p, pc.b, kvh, warp, lane, col0, nloc, s_q);
-      __syncthreads();
       if (live && (NQ == 2 || wg == 0)) {   // q' into tensor memory: lane = column
+        const uint4* q = qx + ((((size_t)pc.b * p.Hkv + kvh) * ((p.ncols + 31) / 32) + c / 32) * 16) * 32 + lane;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t r[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4*>(s_q + cl * 256 + (((8 * h + i) ^ (cl & 15)) << 4));
+            const uint4 x = __ldcg(q + 32 * (8 * h + i));
             r[4 * i] = x.x, r[4 * i + 1] = x.y, r[4 * i + 2] = x.z, r[4 * i + 3] = x.w;
           }
           tmem_st32(t_lane + TM::q(wg) + 32 * h, r);
@@ -703,70 +734,88 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         }
         tcgen05_after_sync();
       }
-      // NQ 1: the warpgroup of the piece's first tile takes in the other's
-      // state through shared memory (the tile rings are idle: every product of
-      // the piece is done), channel rows of ROWS columns
-      const int lead = NQ == 1 ? (int)(done & 1) : wg;
-      const bool both = NQ == 1 && pc.n > 1;
-      float* s_o = reinterpret_cast<float*>(smem + G::K_OFF);
-      float2* s_ml = reinterpret_cast<float2*>(smem + G::ML_OFF);
-      if (both) {
-        named_barrier_sync(1, SM_WARPS * 32);   // both warpgroups' last products are done
-        if (wg != lead && live && ok) {
-          s_ml[row] = make_float2(m, l);
-#pragma unroll 1
-          for (int q = 0; q < kHeadDim / 32; ++q) {
-            float o[32];
-            tmem_ld32(t_lane + T_O + kHeadDim * wg + 32 * q, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s_o[(32 * q + i) * ROWS + row] = o[i];
-          }
-        }
-        named_barrier_sync(1, SM_WARPS * 32);
+      // NQ 1: the two warpgroups' states are merged.  Both O's rows are in the
+      // same tensor-memory lanes, so each warp reads both and takes half of the
+      // channels; the maxima and sums pass through shared memory.
+      const bool both = NQ == 1 && pc.n > 1;                        // both warpgroups had tiles
+      const uint32_t own = NQ == 1 ? done & 1 : (uint32_t)wg;       // the O of the piece's first tile
+      float fa = 1.f, fb = 0.f;
+      if constexpr (NQ == 1) {
+        float2* s_ml = reinterpret_cast<float2*>(smem + G::ML_OFF);
+        s_ml[wg * ROWS + row] = make_float2(m, l);
+        tcgen05_before_sync();
+        named_barrier_sync(1, SM_WARPS * 32);   // both warpgroups' last products are done, too
+        tcgen05_after_sync();
+        const float2 a = s_ml[own * ROWS + row], z = s_ml[(own ^ 1) * ROWS + row];
+        m = fmaxf(a.x, z.x);
+        fa = fast_exp2(a.x - m), fb = fast_exp2(z.x - m);
+        l = a.y * fa + z.y * fb;
       }
-      if (wg == lead && live && ok && !*abort_flag) {
-        float fa = 1.f, fb = 0.f;
-        if (both) {
-          const float2 other = s_ml[row];
-          const float mn = fmaxf(m, other.x);
-          fa = fast_exp2(m - mn), fb = fast_exp2(other.x - mn);
-          m = mn;
-          l = l * fa + other.y * fb;
-        }
+      if (live && ok && !*abort_flag) {
         const bool whole = pc.n == pc.all;
         if (whole) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
           fa *= inv, fb *= inv;
         }
-        float* part = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + split + pc.b) * p.ncols + c) * kPartialStride;
+        // 32 channels at a time, transposed through the warp's own shared memory
+        // (the tile rings are idle: every product of the piece is done) so that
+        // the stores cover whole lines; 16-byte pieces permuted by the row
+        const int c0 = c - lane;   // the warp's first column
+        float* box = reinterpret_cast<float*>(smem + G::K_OFF) + warp * (32 * 32);
+        float* part = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + split + pc.b) * p.ncols + c0) * kPartialStride;
 #pragma unroll 1
-        for (int q = 0; q < kHeadDim / 32; ++q) {
+        for (int q = NQ == 1 ? 2 * wg : 0; q < (NQ == 1 ? 2 * wg + 2 : 4); ++q) {
           float o[32];
-          tmem_ld32(t_lane + T_O + kHeadDim * wg + 32 * q, o);
+          tmem_ld32(t_lane + T_O + kHeadDim * own + 32 * q, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = both ? o[i] * fa + s_o[(32 * q + i) * ROWS + row] * fb : o[i] * fa;
-          if (cl < nloc && !whole) {
+          for (int i = 0; i < 32; ++i) o[i] *= fa;
+          if (both) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(part + 32 * q + 4 * i) =
-                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          } else if (cl < nloc) {
-            __half* dst = p.out + out_row(p, pc.b, kvh, c) + 32 * q;
-            if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+            for (int h = 0; h < 2; ++h) {
+              uint32_t z[16];
+              tmem_ld16(t_lane + T_O + kHeadDim * (own ^ 1) + 32 * q + 16 * h, z);
+              tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(dst + 8 * i) =
-                    make_uint4(pack_half2(o[8 * i], o[8 * i + 1]), pack_half2(o[8 * i + 2], o[8 * i + 3]),
-                               pack_half2(o[8 * i + 4], o[8 * i + 5]), pack_half2(o[8 * i + 6], o[8 * i + 7]));
-            } else {   // out needs only 2-byte alignment
-#pragma unroll
-              for (int i = 0; i < 32; ++i) dst[i] = __float2half_rn(o[i]);
+              for (int i = 0; i < 16; ++i) o[16 * h + i] += __uint_as_float(z[i]) * fb;
             }
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(box + lane * 32 + ((i ^ (lane & 7)) << 2)) =
+                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          __syncwarp();
+          const int x = lane & 7;   // 16-byte piece of the rows 4 i + lane / 8
+          if (!whole) {
+            float* dst = part + (lane >> 3) * kPartialStride + 32 * q + 4 * x;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = 4 * i + (lane >> 3);
+              if (c0 - col0 + r < nloc)
+                *reinterpret_cast<float4*>(dst + 4 * i * kPartialStride) =
+                    *reinterpret_cast<const float4*>(box + r * 32 + ((x ^ (r & 7)) << 2));
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const int r = 4 * i + (lane >> 3);
+              if (c0 - col0 + r < nloc) {
+                const float4 v = *reinterpret_cast<const float4*>(box + r * 32 + ((x ^ (r & 7)) << 2));
+                __half* dst = p.out + out_row(p, pc.b, kvh, c0 + r) + 32 * q + 4 * x;
+                const uint2 h = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
+                if ((reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
+                  *reinterpret_cast<uint2*>(dst) = h;
+                } else {   // out needs only 2-byte alignment
+                  dst[0] = __ushort_as_half((unsigned short)h.x), dst[1] = __ushort_as_half((unsigned short)(h.x >> 16));
+                  dst[2] = __ushort_as_half((unsigned short)h.y), dst[3] = __ushort_as_half((unsigned short)(h.y >> 16));
+                }
+              }
+            }
+          }
+          __syncwarp();
         }
-        if (!whole && cl < nloc) *reinterpret_cast<float2*>(part + 128) = make_float2(m, l);
+        if (!whole && cl < nloc && (NQ == 2 || wg == 0))
+          *reinterpret_cast<float2*>(part + lane * kPartialStride + 128) = make_float2(m, l);
       }
       done += pc.n;
       tcgen05_before_sync();
@@ -776,18 +825,15 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   } else if (warp < MMA_WARP) {
     // ---------------- dequantisation
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DQ));
-    const int dw = warp - SM_WARPS, u = dw & 3;
+    const int dw = warp - SM_WARPS, u = dw & 3, half = (dw >> 2) & 1;
     while (pc.next()) {
-      stage_queries(p, pc.b, kvh, warp, lane, col0, nloc, s_q);
-      __syncthreads();
-      __syncthreads();
       const int L = clamped_len(p, pc.b);
-      if (dw < 4)
-        dequant_loop<MODE, VQKV_ROLE_K, PAGED>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, s_ready, k_empty, u, lane,
-                                               abort_flag);
+      if (dw < 8)
+        dequant_piece<MODE, VQKV_ROLE_K, PAGED>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, s_ready, k_empty, u, half, lane,
+                                                abort_flag);
       else
-        dequant_loop<MODE, VQKV_ROLE_V, PAGED>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, pv_ready, v_empty, u, lane,
-                                               abort_flag);
+        dequant_piece<MODE, VQKV_ROLE_V, PAGED>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, pv_ready, v_empty, u, half, lane,
+                                                abort_flag);
       done += pc.n;
       __syncthreads();
     }
@@ -825,7 +871,6 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     };
     bool ok = true;
     while (pc.next()) {
-      __syncthreads();
       tcgen05_before_sync();
       __syncthreads();
       tcgen05_after_sync();
@@ -899,18 +944,19 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   if (warp == MMA_WARP) tmem_dealloc(tmem, T_COLS);
 }
 
-// Merges the partials of softmax column blockIdx.x % ncols of KV head
-// blockIdx.x / ncols of sequence blockIdx.y, where several shares overlap it.
-// Warp w takes partials w, w + 8, ..., four in flight; lane = 4 channels; the
-// warps meet in shared memory.
-constexpr int TC_WARPS = 8;
+// Merges the partials of the softmax columns of (sequence blockIdx.y, all KV
+// heads) that several shares overlap.  One column per warp, or per block (WIDE:
+// many partials per sequence); lane = 4 channels, eight partials in flight.
+constexpr int TC_WARPS = 4;
+template <bool WIDE>
 __global__ void __launch_bounds__(TC_WARPS * 32) tree_combine_kernel(const DecodeParams p) {
-  constexpr int U = 4;
+  constexpr int U = 8;
   __shared__ int s_sum[2][TC_WARPS];
   __shared__ float4 s_o[TC_WARPS][32];
   __shared__ float2 s_ml[TC_WARPS];
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.x / p.ncols, c = blockIdx.x - kvh * p.ncols;
+  const int col = WIDE ? blockIdx.x : blockIdx.x * TC_WARPS + warp;
+  const int kvh = col / p.ncols, c = col - kvh * p.ncols;
   grid_dependency_wait();
   grid_dependents_launch();
   int before = 0, total = 0;   // tiles of the sequences before b, of all
@@ -930,9 +976,10 @@ __global__ void __launch_bounds__(TC_WARPS * 32) tree_combine_kernel(const Decod
   if (mine == 0) return;
   const int S = min(p.n_splits, total);
   const int s0 = flat_cta_of(before, total, S), parts = flat_cta_of(before + mine - 1, total, S) - s0 + 1;
-  if (parts == 1) return;   // its share wrote O
+  if (parts == 1 || kvh >= p.Hkv) return;   // one share wrote O, or no such column
   const size_t stride = (size_t)p.ncols * kPartialStride;
   const float* base = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + s0 + b) * p.ncols + c) * kPartialStride;
+  constexpr int STEP = WIDE ? TC_WARPS : 1;
   float M = kMInit, l = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float2 ml, float4 o) {
@@ -941,12 +988,12 @@ __global__ void __launch_bounds__(TC_WARPS * 32) tree_combine_kernel(const Decod
     l = l * fa + ml.y * fb;
     M = n;
   };
-  for (int i0 = warp; i0 < parts; i0 += U * TC_WARPS) {
+  for (int i0 = WIDE ? warp : 0; i0 < parts; i0 += U * STEP) {
     float2 ml[U];
     float4 o[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * TC_WARPS;
+      const int i = i0 + u * STEP;
       if (i < parts) {
         ml[u] = __ldcg(reinterpret_cast<const float2*>(base + i * stride + 128));
         o[u] = __ldcg(reinterpret_cast<const float4*>(base + i * stride) + lane);
@@ -954,21 +1001,23 @@ __global__ void __launch_bounds__(TC_WARPS * 32) tree_combine_kernel(const Decod
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i0 + u * TC_WARPS < parts) add(ml[u], o[u]);
+      if (i0 + u * STEP < parts) add(ml[u], o[u]);
   }
-  s_o[warp][lane] = O;
-  if (lane == 0) s_ml[warp] = make_float2(M, l);
-  __syncthreads();
-  if (warp != 0) return;
+  if (WIDE) {   // the block's warps meet in shared memory
+    s_o[warp][lane] = O;
+    if (lane == 0) s_ml[warp] = make_float2(M, l);
+    __syncthreads();
+    if (warp != 0) return;
 #pragma unroll
-  for (int w = 1; w < TC_WARPS; ++w) add(s_ml[w], s_o[w][lane]);
+    for (int w = 1; w < TC_WARPS; ++w) add(s_ml[w], s_o[w][lane]);
+  }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   __half* dst = p.out + out_row(p, b, kvh, c) + 4 * lane;   // out needs only 2-byte alignment
   dst[0] = __float2half_rn(O.x * inv), dst[1] = __float2half_rn(O.y * inv);
   dst[2] = __float2half_rn(O.z * inv), dst[3] = __float2half_rn(O.w * inv);
 }
 
-using TreeKernel = void (*)(DecodeParams, const unsigned long long*);
+using TreeKernel = void (*)(DecodeParams, const unsigned long long*, const uint4*);
 template <int MODE>
 TreeKernel tree_of(bool paged, bool wide) {
   return wide ? (paged ? (TreeKernel)decode_tree_kernel<MODE, true, 2> : (TreeKernel)decode_tree_kernel<MODE, false, 2>)
@@ -997,12 +1046,23 @@ cudaError_t decode_tree_prepare(int mode) {
   return e;
 }
 
-cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, cudaStream_t stream) {
+size_t decode_tree_query_bytes(int B, int Hkv, int ncols) { return (size_t)B * Hkv * ((ncols + 31) / 32) * 32 * kHeadDim * 2; }
+
+cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, void* qx,
+                               cudaStream_t stream) {
   const bool wide = p.ncols > tr::ROWS;
-  cudaError_t e = launch_pdl(tree_kernel(mode, p.block_table != nullptr, wide), dim3(p.n_splits, p.Hkv, p.cgroups),
-                             dim3(tr::THREADS), (size_t)tree_smem(mode), stream, p, tree_mask);
-  if (e == cudaSuccess && p.n_splits > 1)
-    e = launch_pdl(tree_combine_kernel, dim3(p.Hkv * p.ncols, p.B), dim3(TC_WARPS * 32), 0, stream, p);
+  cudaError_t e = launch_pdl(tree_query_kernel, dim3((p.ncols + 31) / 32, p.Hkv, p.B), dim3(128), 0, stream, p,
+                             static_cast<uint4*>(qx));
+  if (e == cudaSuccess)
+    e = launch_pdl(tree_kernel(mode, p.block_table != nullptr, wide), dim3(p.n_splits, p.Hkv, p.cgroups),
+                   dim3(tr::THREADS), (size_t)tree_smem(mode), stream, p, tree_mask, static_cast<const uint4*>(qx));
+  if (e == cudaSuccess && p.n_splits > 1) {
+    const int cols = p.Hkv * p.ncols;
+    if (p.n_splits > TC_WARPS * p.B)
+      e = launch_pdl(tree_combine_kernel<true>, dim3(cols, p.B), dim3(TC_WARPS * 32), 0, stream, p);
+    else
+      e = launch_pdl(tree_combine_kernel<false>, dim3((cols + TC_WARPS - 1) / TC_WARPS, p.B), dim3(TC_WARPS * 32), 0, stream, p);
+  }
   return e;
 }
 

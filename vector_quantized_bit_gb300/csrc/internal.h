@@ -114,7 +114,9 @@ cudaError_t launch_decode_mass(int mode, const DecodeParams& p, dim3 grid, cudaS
 // [Hkv][n_splits + B - 1][ncols], indexed by share + sequence as in the flat plan.
 int decode_tree_cols(int ncols);
 cudaError_t decode_tree_prepare(int mode);
-cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, cudaStream_t stream);
+size_t decode_tree_query_bytes(int B, int Hkv, int ncols);   // scratch qx of a launch (transformed queries)
+cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, void* qx,
+                               cudaStream_t stream);
 
 // Cache editing (cache_edit.cu): the in-place move of chosen tokens, and the
 // choice of the tokens a sequence keeps.
