@@ -56,8 +56,12 @@ cudaError_t launch_cluster(void (*kernel)(Args...), dim3 grid, int cluster, int 
 // that position.  A cluster of CTAs owns one stream and walks it in rounds of
 // consecutive destination tokens; a round's sources are >= its destinations,
 // so its writes can only hit sources of the same or an earlier round.  Hence:
-// read round r + 1 into registers, meet at the cluster barrier (every read of
-// rounds <= r + 1 is done), write round r.
+// read a round into registers, meet at the cluster barrier (every read of this
+// and of earlier rounds is done), write the round.
+//
+// Bound: latency of the dependent loads (source index, then the source's
+// bytes), so a warp keeps four or eight 16-token groups in flight per round and
+// loads the next round's indices before it writes.
 //
 // The layouts keep every token's bytes to itself, spread over the 32 lanes'
 // runs of a 16-token group (include/vqkv.h).  A lane of the destination group
@@ -251,83 +255,87 @@ __device__ __forceinline__ void move_codes(const CompactParams& p, const Move& m
   const int gid = lane >> 2, tig = lane & 3;
   uint8_t* codes = p.codes[ROLE];
   const int first = mv.start >> 4, last = mv.n > 0 ? (mv.start + mv.n + 15) >> 4 : first;   // 16-token groups
-  const int rounds = (last - first + cluster * CP_WARPS - 1) / (cluster * CP_WARPS);
-
-  // Round k's group of this warp: its run in w, its place (-1: nothing to write).
-  auto load = [&](int k, uint32_t (&w)[G::W], long long& place) {
-    const int grp = first + (k * cluster + rank) * CP_WARPS + warp;
-    place = -1;
+  constexpr int U = G::W <= 4 ? 8 : 4;   // groups per warp and round (32 words of runs at most)
+  const int per = cluster * CP_WARPS * U;
+  const int rounds = (last - first + per - 1) / per;
+  // the warp's groups of round k are neighbours; lane l looks up token l % 16
+  // of group 2 i + l / 16 (pair i of groups)
+  auto first_group = [&](int k) { return first + k * per + (rank * CP_WARPS + warp) * U; };
+  auto lookup = [&](int k, int (&s)[U / 2]) {
 #pragma unroll
-    for (int i = 0; i < G::W; ++i) w[i] = 0u;
-    if (grp >= last) return;
-    bool bad = false;
-    const long long dst = tile_offset<PAGED>(p, mv.b, mv.kvh, (grp << 4) / TT, TILE_BYTES, &bad);
-    // lane r < 16: where token 16 grp + r comes from: tile offset | position within the tile
-    const int d = (grp << 4) + (lane & 15);
-    int s = mv.source(p, d, ROLE == VQKV_ROLE_K && lane < 16);
-    bool sbad = false;
-    long long from = tile_offset<PAGED>(p, mv.b, mv.kvh, s / TT, TILE_BYTES, &sbad);
-    if (sbad) from = dst, s = d;
-    from |= s & 63;   // tile offsets are multiples of 64
-    if (PAGED && (bad || sbad) && p.err != nullptr) atomicOr(p.err, VQKV_DEVERR_BLOCK);
-    if (bad || __all_sync(0xffffffffu, s == d)) return;   // nothing moves: leave the group as it is
-    place = dst | ((grp & 3) << 4);
-#pragma unroll
-    for (int k2 = 0; k2 < G::SLOTS; ++k2) {
-      const int r = ROLE == VQKV_ROLE_K ? gid + 8 * k2 : 2 * tig + (k2 & 1) + 8 * (k2 >> 1);
-      const long long f = __shfl_sync(0xffffffffu, from, r);
-      if (!(MODE == VQKV_MODE_VQ125 && ROLE == VQKV_ROLE_V) || lane < 16) {
-        const int at = (int)(f & 63);
-        put_slot<MODE, ROLE>(w, k2, load_slot<MODE, ROLE>(codes + (f & ~63LL), at & 15, (at >> 4) & 3,
-                                                          ROLE == VQKV_ROLE_K ? tig : gid));
-      }
+    for (int i = 0; i < U / 2; ++i) {
+      const int grp = first_group(k) + 2 * i + (lane >> 4);
+      s[i] = grp < last ? mv.source(p, (grp << 4) + (lane & 15), ROLE == VQKV_ROLE_K) : -1;
     }
   };
-  uint32_t cur[G::W], nxt[G::W];
-  long long cur_at = -1, nxt_at = -1;
-  if (rounds > 0) load(0, cur, cur_at);
+  int src[U / 2];
+  if (rounds > 0) lookup(0, src);
   for (int k = 0; k < rounds; ++k) {
-    if (k + 1 < rounds) load(k + 1, nxt, nxt_at);
-    if (cluster > 1) cluster_sync(); else __syncthreads();
-    if (cur_at >= 0) store_run<MODE, ROLE>(codes + (cur_at & ~63LL), (int)((cur_at >> 4) & 3), lane, cur);
+    uint32_t w[U][G::W];
+    long long place[U];   // tile offset | 16 x (group within the tile), -1: nothing to write
 #pragma unroll
-    for (int i = 0; i < G::W; ++i) cur[i] = nxt[i];
-    cur_at = nxt_at;
+    for (int i = 0; i < U / 2; ++i) {
+      // where each of the 32 tokens comes from: tile offset | position within the tile
+      const int grp = first_group(k) + 2 * i + (lane >> 4), d = (grp << 4) + (lane & 15);
+      bool bad = false, sbad = false;
+      long long dst = 0, from = 0;
+      if (grp < last) {
+        dst = tile_offset<PAGED>(p, mv.b, mv.kvh, d / TT, TILE_BYTES, &bad);
+        from = tile_offset<PAGED>(p, mv.b, mv.kvh, src[i] / TT, TILE_BYTES, &sbad);
+        if (sbad) from = dst, src[i] = d;
+        if (PAGED && (bad || sbad) && p.err != nullptr) atomicOr(p.err, VQKV_DEVERR_BLOCK);
+      }
+      from |= src[i] & 63;   // tile offsets are multiples of 64
+      const unsigned moves = __ballot_sync(0xffffffffu, grp < last && !bad && src[i] != d);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = 2 * i + h;
+#pragma unroll
+        for (int q = 0; q < G::W; ++q) w[j][q] = 0u;
+        const long long at = __shfl_sync(0xffffffffu, dst, 16 * h);
+        place[j] = -1;
+        if (((moves >> (16 * h)) & 0xffffu) == 0) continue;   // nothing moves: leave the group as it is
+        place[j] = at | (((first_group(k) + j) & 3) << 4);
+#pragma unroll
+        for (int q = 0; q < G::SLOTS; ++q) {
+          const int r = ROLE == VQKV_ROLE_K ? gid + 8 * q : 2 * tig + (q & 1) + 8 * (q >> 1);
+          const long long f = __shfl_sync(0xffffffffu, from, 16 * h + r);
+          if (!(MODE == VQKV_MODE_VQ125 && ROLE == VQKV_ROLE_V) || lane < 16) {
+            const int pos = (int)(f & 63);
+            put_slot<MODE, ROLE>(w[j], q, load_slot<MODE, ROLE>(codes + (f & ~63LL), pos & 15, (pos >> 4) & 3,
+                                                                ROLE == VQKV_ROLE_K ? tig : gid));
+          }
+        }
+      }
+    }
+    if (k + 1 < rounds) lookup(k + 1, src);
+    if (cluster > 1) cluster_sync(); else __syncthreads();
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (place[j] >= 0) store_run<MODE, ROLE>(codes + (place[j] & ~63LL), (int)((place[j] >> 4) & 3), lane, w[j]);
   }
 }
 
 __device__ __forceinline__ void move_mass(const CompactParams& p, const Move& mv, int rank, int cluster) {
-  constexpr int U = 4;
+  constexpr int U = 8;
   float* row = p.mass + ((size_t)mv.b * p.Hkv + mv.kvh) * p.cap_len;
   const int per = cluster * CP_THREADS * U;
   const int rounds = (mv.n + per - 1) / per;
-  auto load = [&](int k, float (&v)[U], int (&at)[U]) {
+  for (int k = 0; k < rounds; ++k) {
+    float v[U];
+    int s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = k * per + (rank * U + u) * CP_THREADS + (int)threadIdx.x, d = mv.start + i;
-      at[u] = -1;
-      if (i < mv.n) {
-        const int s = mv.source(p, d, false);
-        if (s != d) {
-          at[u] = d;
-          v[u] = __uint_as_float(ld32(reinterpret_cast<const uint8_t*>(row + s)));
-        }
-      }
+      const int i = k * per + (rank * U + u) * CP_THREADS + (int)threadIdx.x;
+      s[u] = i < mv.n ? mv.source(p, mv.start + i, false) : -1;
     }
-  };
-  float cur[U], nxt[U];
-  int cur_at[U], nxt_at[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) cur[u] = nxt[u] = 0.f, cur_at[u] = nxt_at[u] = -1;
-  if (rounds > 0) load(0, cur, cur_at);
-  for (int k = 0; k < rounds; ++k) {
-    if (k + 1 < rounds) load(k + 1, nxt, nxt_at);
+    for (int u = 0; u < U; ++u)
+      if (s[u] >= 0) v[u] = __uint_as_float(ld32(reinterpret_cast<const uint8_t*>(row + s[u])));
     if (cluster > 1) cluster_sync(); else __syncthreads();
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (cur_at[u] >= 0) row[cur_at[u]] = cur[u];
-      cur[u] = nxt[u], cur_at[u] = nxt_at[u];
-    }
+    for (int u = 0; u < U; ++u)
+      if (s[u] >= 0) row[mv.start + k * per + (rank * U + u) * CP_THREADS + (int)threadIdx.x] = v[u];
   }
   // every source has been read: clear what the sequence no longer holds
   for (int t = mv.start + mv.n + rank * CP_THREADS + (int)threadIdx.x; t < mv.L; t += cluster * CP_THREADS) row[t] = 0.f;
@@ -362,6 +370,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const CompactParams
 
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_U = 8;
 constexpr int SEL_BINS = 2048;
 constexpr int SEL_MAX_CLUSTER = 8;
 constexpr int SEL_CACHE = 40960;   // keys of a CTA's part kept in shared memory (160 KB)
@@ -413,10 +422,20 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Sele
     __syncthreads();
     const uint32_t mask = (1u << bits) - 1u;
     if (pass == 0) {
-      for (int t = c0 + (int)threadIdx.x; t < c1; t += SEL_THREADS) {
-        const uint32_t k = make_key(t);
-        if (cached) s_keys[t - c0] = k;
-        atomicAdd(&s_hist[k >> shift], 1u);
+      for (int t0 = c0 + (int)threadIdx.x; t0 < c1; t0 += SEL_U * SEL_THREADS) {   // SEL_U loads in flight
+        uint32_t k[SEL_U];
+#pragma unroll
+        for (int i = 0; i < SEL_U; ++i) {
+          const int t = t0 + i * SEL_THREADS;
+          k[i] = t < c1 ? make_key(t) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < SEL_U; ++i) {
+          const int t = t0 + i * SEL_THREADS;
+          if (t >= c1) break;
+          if (cached) s_keys[t - c0] = k[i];
+          atomicAdd(&s_hist[k[i] >> shift], 1u);
+        }
       }
     } else {
       for (int t = c0 + (int)threadIdx.x; t < c1; t += SEL_THREADS) {
