@@ -367,11 +367,17 @@ __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const CompactParams
 // distributed shared memory.  Then the kept positions are counted per warp
 // and CTA, and written by ballot ranks: larger keys all, keys equal to the
 // K-th while some are still needed, lowest position first.
+//
+// Bound: instruction issue and, in the first pass, shared-memory atomics on
+// equal bins (weights share their leading bits).  So lanes take four
+// neighbouring keys at a time, and four copies of the counts, one per lane % 4,
+// keep equal bins of a warp apart.
 
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
-constexpr int SEL_U = 8;
+constexpr int SEL_U = 2;           // 16-byte loads in flight per thread in the first pass
 constexpr int SEL_BINS = 2048;
+constexpr int SEL_COPIES = 4;
 constexpr int SEL_MAX_CLUSTER = 8;
 constexpr int SEL_CACHE = 40960;   // keys of a CTA's part kept in shared memory (160 KB)
 
@@ -383,8 +389,10 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
 }
 
 __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const SelectParams p) {
-  extern __shared__ uint32_t s_keys[];   // [min(part, SEL_CACHE)]
-  __shared__ uint32_t s_hist[SEL_BINS], s_total[SEL_BINS];
+  extern __shared__ uint4 s_dyn[];
+  uint32_t* s_hist = reinterpret_cast<uint32_t*>(s_dyn);             // [SEL_COPIES][SEL_BINS]
+  uint32_t* s_total = s_hist + SEL_COPIES * SEL_BINS;                // [SEL_BINS]
+  uint4* s_keys = reinterpret_cast<uint4*>(s_total + SEL_BINS);      // [p.cache_keys / 4]
   __shared__ uint32_t s_warp[SEL_WARPS], s_warp2[SEL_WARPS];
   __shared__ uint32_t s_digit, s_above;
   __shared__ uint32_t s_cta[2 * SEL_MAX_CLUSTER];   // per CTA: larger, equal
@@ -402,48 +410,85 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Sele
     for (int t = rank * SEL_THREADS + (int)threadIdx.x; t < L; t += CL * SEL_THREADS) keep[t] = t;
     return;
   }
-  // parts of whole warp strides, so that each warp walks a contiguous piece
-  const int piece = ((L + CL * SEL_WARPS - 1) / (CL * SEL_WARPS) + 31) & ~31;
+  // parts of SEL_WARPS pieces of whole 128-token strides: a warp walks a
+  // contiguous piece, four tokens per lane
+  const int piece = ((L + CL * SEL_WARPS - 1) / (CL * SEL_WARPS) + 127) & ~127;
   const int c0 = min(rank * SEL_WARPS * piece, L), c1 = min(c0 + SEL_WARPS * piece, L);
   const float* mass = p.mass + ((size_t)b * p.Hkv + kvh) * p.cap_len;
   const bool cached = SEL_WARPS * piece <= p.cache_keys;
-  auto make_key = [&](int t) -> uint32_t {
-    if (t < p.n_sink || t >= L - p.n_recent) return 0xffffffffu;   // above +inf: always kept
-    return weight_key(mass[t]);
+  const bool aligned16 = (reinterpret_cast<uintptr_t>(mass) & 15) == 0;
+  // the keys of tokens t .. t + 3 (t a multiple of 4), 0 past the part's end;
+  // protected tokens rank above +inf
+  auto load_keys = [&](int t) -> uint4 {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (aligned16 && t + 3 < c1) {
+      const float4 v = *reinterpret_cast<const float4*>(mass + t);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i < c1) x[i] = mass[t + i];
+    }
+    uint32_t k[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      k[i] = t + i < p.n_sink || t + i >= L - p.n_recent ? 0xffffffffu : weight_key(x[i]);
+      if (t + i >= c1) k[i] = 0u;
+    }
+    return make_uint4(k[0], k[1], k[2], k[3]);
   };
-  auto key_at = [&](int t) -> uint32_t { return cached ? s_keys[t - c0] : make_key(t); };
+  auto keys_at = [&](int t) -> uint4 { return cached ? s_keys[(t - c0) >> 2] : load_keys(t); };
 
   uint32_t prefix = 0;                 // key bits found so far
   uint32_t need = (uint32_t)p.n_keep;  // tokens still to take among keys with that prefix
+  uint32_t* hist = s_hist + (lane % SEL_COPIES) * SEL_BINS;
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int bits = pass == 2 ? 10 : 11;
-    for (int i = threadIdx.x; i < SEL_BINS; i += SEL_THREADS) s_hist[i] = 0u;
+    for (int i = threadIdx.x; i < SEL_COPIES * SEL_BINS; i += SEL_THREADS) s_hist[i] = 0u;
     __syncthreads();
     const uint32_t mask = (1u << bits) - 1u;
     if (pass == 0) {
-      for (int t0 = c0 + (int)threadIdx.x; t0 < c1; t0 += SEL_U * SEL_THREADS) {   // SEL_U loads in flight
-        uint32_t k[SEL_U];
+      for (int t0 = c0 + 4 * (int)threadIdx.x; t0 < c1; t0 += 4 * SEL_U * SEL_THREADS) {
+        uint4 k[SEL_U];
 #pragma unroll
         for (int i = 0; i < SEL_U; ++i) {
-          const int t = t0 + i * SEL_THREADS;
-          k[i] = t < c1 ? make_key(t) : 0u;
+          const int t = t0 + 4 * i * SEL_THREADS;
+          if (t < c1) k[i] = load_keys(t);
         }
 #pragma unroll
         for (int i = 0; i < SEL_U; ++i) {
-          const int t = t0 + i * SEL_THREADS;
+          const int t = t0 + 4 * i * SEL_THREADS;
           if (t >= c1) break;
-          if (cached) s_keys[t - c0] = k[i];
-          atomicAdd(&s_hist[k[i] >> shift], 1u);
+          if (cached) s_keys[(t - c0) >> 2] = k[i];
+          atomicAdd(&hist[k[i].x >> 21], 1u);
+          if (t + 1 < c1) atomicAdd(&hist[k[i].y >> 21], 1u);
+          if (t + 2 < c1) atomicAdd(&hist[k[i].z >> 21], 1u);
+          if (t + 3 < c1) atomicAdd(&hist[k[i].w >> 21], 1u);
         }
       }
     } else {
-      for (int t = c0 + (int)threadIdx.x; t < c1; t += SEL_THREADS) {
-        const uint32_t k = key_at(t);
-        if ((k >> (shift + bits)) == prefix) atomicAdd(&s_hist[(k >> shift) & mask], 1u);
+      // (keys past the part's end are 0: with prefix 0 they would count, so the
+      // bound is tested there)
+      auto count = [&](uint32_t k, int t) {
+        if ((k >> (shift + bits)) == prefix && t < c1) atomicAdd(&hist[(k >> shift) & mask], 1u);
+      };
+      for (int t = c0 + 4 * (int)threadIdx.x; t < c1; t += 4 * SEL_THREADS) {
+        const uint4 k = keys_at(t);
+        count(k.x, t), count(k.y, t + 1), count(k.z, t + 2), count(k.w, t + 3);
       }
     }
-    if (CL > 1) {   // this CTA adds a share of the bins and gives every CTA the sums
+    __syncthreads();
+    // fold the copies: bins from the top, thread i holds 2047 - 2i and 2046 - 2i
+    const int hi = SEL_BINS - 1 - 2 * (int)threadIdx.x;
+    uint32_t x0 = 0, x1 = 0;
+#pragma unroll
+    for (int c = 0; c < SEL_COPIES; ++c) {
+      const uint2 v = *reinterpret_cast<const uint2*>(&s_hist[c * SEL_BINS + hi - 1]);
+      x0 += v.y, x1 += v.x;
+    }
+    if (CL > 1) {   // this CTA adds a share of the bins over the cluster and gives every CTA the sums
+      *reinterpret_cast<uint2*>(&s_hist[hi - 1]) = make_uint2(x1, x0);   // own bins of copy 0 only
       cluster_sync();
       const int share = SEL_BINS / CL;
       if ((int)threadIdx.x < share) {
@@ -454,13 +499,8 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Sele
         for (int r = 0; r < CL; ++r) cluster_st(cluster_addr(o, r), sum);
       }
       cluster_sync();
-    } else {
-      __syncthreads();
+      x0 = s_total[hi], x1 = s_total[hi - 1];
     }
-    // bins from the top: thread i holds bins 2047 - 2i and 2046 - 2i
-    const uint32_t* tot = CL > 1 ? s_total : s_hist;
-    const int hi = SEL_BINS - 1 - 2 * (int)threadIdx.x;
-    const uint32_t x0 = tot[hi], x1 = tot[hi - 1];
     uint32_t inc = x0 + x1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -469,17 +509,9 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Sele
     }
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-      uint32_t v = s_warp[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-      }
-      s_warp2[lane] = v;
-    }
-    __syncthreads();
-    const uint32_t before = inc - x0 - x1 + (warp > 0 ? s_warp2[warp - 1] : 0u);   // tokens in higher bins
+    // tokens in the bins of the warps before this one (SEL_WARPS == 32)
+    const uint32_t prior = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
+    const uint32_t before = inc - x0 - x1 + prior;   // tokens in higher bins
     if (before < need && need <= before + x0) {
       s_digit = hi, s_above = before;
     } else if (before + x0 < need && need <= before + x0 + x1) {
@@ -488,21 +520,21 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Sele
     __syncthreads();
     prefix = (prefix << bits) | s_digit;
     need -= s_above;
-    __syncthreads();
   }
   // prefix is the K-th largest key; `need` of the keys equal to it are kept
   const int w0 = min(c0 + warp * piece, c1), w1 = min(w0 + piece, c1);
   uint32_t larger = 0, equal = 0;
-  for (int t = w0 + lane; t < w1; t += 32) {
-    const uint32_t k = key_at(t);
-    larger += k > prefix;
-    equal += k == prefix;
+  for (int t = w0 + 4 * lane; t < w1; t += 128) {
+    const uint4 k = keys_at(t);
+    larger += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);   // 0 past the end: never larger
+    equal += (k.x == prefix) + (k.y == prefix && t + 1 < c1) + (k.z == prefix && t + 2 < c1) + (k.w == prefix && t + 3 < c1);
   }
   larger = __reduce_add_sync(0xffffffffu, larger);
   equal = __reduce_add_sync(0xffffffffu, equal);
+  __syncthreads();
   if (lane == 0) s_warp[warp] = larger, s_warp2[warp] = equal;
   __syncthreads();
-  uint32_t cl = s_warp[lane], ce = s_warp2[lane];   // SEL_WARPS == 32
+  uint32_t cl = s_warp[lane], ce = s_warp2[lane];
   uint32_t gl = __reduce_add_sync(0xffffffffu, lane < warp ? cl : 0u);
   uint32_t ge = __reduce_add_sync(0xffffffffu, lane < warp ? ce : 0u);
   if (CL > 1) {
@@ -517,16 +549,41 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Sele
   }
   uint32_t at = gl + min(ge, need), seen = ge;   // kept / equal tokens before this warp's piece
   const uint32_t lt = (1u << lane) - 1u;
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    const int t = t0 + lane;
-    const uint32_t k = t < w1 ? key_at(t) : 0u;
-    const bool eq = t < w1 && k == prefix;
-    const uint32_t beq = __ballot_sync(0xffffffffu, eq);
-    const bool kept = t < w1 && (k > prefix || (eq && seen + __popc(beq & lt) < need));
-    const uint32_t bk = __ballot_sync(0xffffffffu, kept);
-    if (kept) keep[at + __popc(bk & lt)] = t;
-    at += __popc(bk);
-    seen += __popc(beq);
+  for (int t0 = w0; t0 < w1; t0 += 128) {
+    const int t = t0 + 4 * lane;
+    const uint4 kk = t < w1 ? keys_at(t) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t k[4] = {kk.x, kk.y, kk.z, kk.w};
+    uint32_t kept = 0, eq = 0;   // bit i: token t + i
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      kept |= (uint32_t)(k[i] > prefix) << i;
+      eq |= (uint32_t)(k[i] == prefix && t + i < w1) << i;
+    }
+    if (__any_sync(0xffffffffu, eq != 0)) {
+      const uint32_t n = __popc(eq);
+      uint32_t rank_eq = seen;   // equal tokens before this lane's
+#pragma unroll
+      for (int q = 0; q < 3; ++q) rank_eq += __popc(__ballot_sync(0xffffffffu, (n >> q) & 1u) & lt) << q;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((eq >> i) & 1u) {
+          if (rank_eq < need) kept |= 1u << i;
+          ++rank_eq;
+        }
+      seen += __reduce_add_sync(0xffffffffu, n);
+    }
+    const uint32_t n = __popc(kept);
+    uint32_t pos = at, all = 0;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const uint32_t bal = __ballot_sync(0xffffffffu, (n >> q) & 1u);
+      pos += __popc(bal & lt) << q;
+      all += __popc(bal) << q;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((kept >> i) & 1u) keep[pos++] = t + i;
+    at += all;
   }
 }
 
@@ -554,8 +611,10 @@ cudaError_t launch_compact(int mode, const CompactParams& p, int sms, cudaStream
   return launch_cluster(k, dim3(cluster, p.Hkv * (p.mass != nullptr ? 3 : 2), p.B), cluster, CP_THREADS, 0, stream, p);
 }
 
+static int select_smem(int keys) { return ((SEL_COPIES + 1) * SEL_BINS + keys) * 4; }
+
 cudaError_t evict_select_prepare() {
-  return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_CACHE * 4);
+  return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, select_smem(SEL_CACHE));
 }
 
 cudaError_t launch_evict_select(SelectParams p, int sms, cudaStream_t stream) {
@@ -564,10 +623,10 @@ cudaError_t launch_evict_select(SelectParams p, int sms, cudaStream_t stream) {
   int cluster = 1;
   while (cluster < SEL_MAX_CLUSTER && rows * cluster * 2 <= sms && p.max_seq_len > 4096 * cluster) cluster *= 2;
   const long long part = ((long long)p.max_seq_len + cluster * SEL_WARPS - 1) / (cluster * SEL_WARPS);
-  const long long keys = (part + 31) / 32 * 32 * SEL_WARPS;
+  const long long keys = (part + 127) / 128 * 128 * SEL_WARPS;
   p.cache_keys = keys <= SEL_CACHE ? (int)keys : 0;
-  return launch_cluster(evict_select_kernel, dim3(cluster, p.Hkv, p.B), cluster, SEL_THREADS, (size_t)p.cache_keys * 4,
-                        stream, p);
+  return launch_cluster(evict_select_kernel, dim3(cluster, p.Hkv, p.B), cluster, SEL_THREADS,
+                        (size_t)select_smem(p.cache_keys), stream, p);
 }
 
 }  // namespace vqkv
