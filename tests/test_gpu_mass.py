@@ -78,6 +78,50 @@ def test_mass_against_reference(mode, B, Hq, Hkv, M, lens, cap, num_splits, page
     assert err == 0
 
 
+@pytest.mark.parametrize("mode,Hq,Hkv,M,num_splits,page", [
+    (0, 8, 2, 3, 0, 0), (0, 8, 2, 4, 0, 0), (0, 8, 2, 5, 0, 0), (0, 8, 2, 8, 3, 64), (0, 8, 2, 9, 0, 0), (0, 4, 1, 16, 5, 0), (1, 10, 2, 6, 0, 128),
+    (2, 8, 1, 8, 0, 64), (3, 8, 2, 16, 2, 0), (4, 3, 1, 21, 0, 64),
+])
+def test_mass_many_columns_ragged_batch(mode, Hq, Hkv, M, num_splits, page):
+    """More columns than the decode path takes: shares that begin and end inside sequences, hold several, or none."""
+    lens = [1, 0, 700, 128, 129, 0, 333, 127, 449, 17]
+    B, cap = len(lens), 768
+    r, q, kc, vc, s, kcb, vcb = case(mode, B, Hq, Hkv, M, cap, seed=3 * mode + M)
+    before = (r.random((B, Hkv, cap)) * M / 100).astype(np.float32)
+    o, mass, err = gpu_mass(mode, q, kc, vc, s, kcb, vcb, lens, cap, before, num_splits, page)
+    ref, w, tol = R.attend(q, kc, vc, kcb, vcb, s, lens, causal(M))
+    R.check_output(o, ref, tol)
+    R.check_mass(mass, before, w, lens, R.attend.score_size)
+    assert err == 0
+
+
+def test_mass_more_sequences_than_one_launch_takes():
+    B, M = 1027, 9
+    r = np.random.default_rng(3)
+    lens = r.integers(0, 40, size=B)
+    s, kcb, vcb = H.random_codebooks(0, 1, 4)
+    kc = [[r.integers(0, 256, size=(48, 32))] for _ in range(B)]
+    vc = [[r.integers(0, 256, size=(48, 32))] for _ in range(B)]
+    q = r.standard_normal((B, M, 2, 128)).astype(np.float16)
+    before = np.zeros((B, 1, 48), dtype=np.float32)
+    o, mass, err = gpu_mass(0, q, kc, vc, s, kcb, vcb, lens, 48, before)
+    ref, w, tol = R.attend(q, kc, vc, kcb, vcb, s, lens, causal(M))
+    R.check_output(o, ref, tol)
+    R.check_mass(mass, before, w, lens, R.attend.score_size)
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2, 3, 4])
+def test_mass_many_columns_long_and_repeatable(mode):
+    r, q, kc, vc, s, kcb, vcb = case(mode, 1, 8, 2, 12, 4100, seed=mode)
+    before = np.zeros((1, 2, 4100), dtype=np.float32)
+    o, mass, err = gpu_mass(mode, q, kc, vc, s, kcb, vcb, [4099], 4100, before, num_splits=2)
+    ref, w, tol = R.attend(q, kc, vc, kcb, vcb, s, [4099], causal(12))
+    R.check_output(o, ref, tol)
+    R.check_mass(mass, before, w, [4099], R.attend.score_size)
+    o2, again, _ = gpu_mass(mode, q, kc, vc, s, kcb, vcb, [4099], 4100, before, num_splits=2)
+    assert np.array_equal(mass, again) and np.array_equal(o, o2)
+
+
 @pytest.mark.parametrize("mode", [0, 1, 2, 3, 4])
 def test_mass_sums_to_the_number_of_columns_and_repeats(mode):
     """From zero: each (sequence, KV head) row gains g per call; a second run gives the same bits."""
@@ -101,13 +145,14 @@ def test_mass_scale_and_clamped_lengths():
     assert err == _lib.VQKV_DEVERR_SEQ_LEN
 
 
-def test_mass_large_scores_keep_fp32_weights():
-    """Scores near 40: a single fp16 part of q' would put 1e-2 into the weights."""
-    r, q, kc, vc, s, kcb, vcb = case(0, 1, 4, 1, 1, 512, seed=4)
+@pytest.mark.parametrize("M", [1, 9])
+def test_mass_large_scores_keep_fp32_weights(M):
+    """Scores near 40: a single fp16 part of q' would put 1e-2 into the weights (few and many columns)."""
+    r, q, kc, vc, s, kcb, vcb = case(0, 1, 4, 1, M, 512, seed=4)
     q = (q.astype(np.float32) * 12).astype(np.float16)
     before = np.zeros((1, 1, 512), dtype=np.float32)
     o, mass, _ = gpu_mass(0, q, kc, vc, s, kcb, vcb, [512], 512, before)
-    ref, w, tol = R.attend(q, kc, vc, kcb, vcb, s, [512], causal(1))
+    ref, w, tol = R.attend(q, kc, vc, kcb, vcb, s, [512], causal(M))
     rel = np.linalg.norm(mass[0, 0] - w[0][0]) / np.linalg.norm(w[0][0])
     assert rel <= 2 * 2.0 ** -17 * R.attend.score_size + 2.0 ** -17
 

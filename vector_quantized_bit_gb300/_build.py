@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libvqkv.so")
-SOURCES = ["api.cu", "cache_edit.cu", "decode.cu", "decode_fp16.cu", "decode_mass.cu", "decode_static.cu", "decode_tree.cu", "encode.cu", "kmeans.cu"]
+SOURCES = ["api.cu", "cache_edit.cu", "decode.cu", "decode_fp16.cu", "decode_mass.cu", "decode_static.cu", "decode_tree.cu", "encode.cu",
+           "kmeans.cu", "mass_tiles.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

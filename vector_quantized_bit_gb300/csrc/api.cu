@@ -36,7 +36,7 @@ vqkv_status device_info(DeviceInfo* out) {
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return VQKV_ERR_NO_DEVICE;
     for (int m = 0; m < kCodeModes; ++m) {
       if (decode_prepare(m) != cudaSuccess || encode_prepare(m) != cudaSuccess || decode_tree_prepare(m) != cudaSuccess ||
-          decode_mass_prepare(m) != cudaSuccess)
+          decode_mass_prepare(m) != cudaSuccess || mass_tiles_prepare(m) != cudaSuccess)
         return VQKV_ERR_CUDA;
       if (decode_occupancy(m, &d.decode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
       if (encode_occupancy(m, &d.encode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
@@ -260,41 +260,22 @@ DecodeParams packed_params(const vqkv_decode_args* a, int M, const vqkv_paging* 
   return p;
 }
 
-// Decode with attention weights: the decode's plan at 4 columns per CTA, then
-// the columns' statistics and the scores behind its workspace.
-struct MassPlan {
-  DecodePlan d;
-  size_t stats_off = 0, scores_off = 0, ws_bytes = 0;
-  int score_row = 0;
-};
-
-vqkv_status validate_mass_sizes(const vqkv_decode_mass_args* am) {
-  if (am == nullptr) return VQKV_ERR_INVALID_ARG;
-  const vqkv_status st = validate_decode_sizes(&am->decode);
-  if (st != VQKV_OK) return st;
-  const vqkv_decode_args& a = am->decode;
-  if (am->n_queries < 1) return VQKV_ERR_INVALID_ARG;
-  if (am->n_queries > 64 || am->n_queries * (a.Hq / a.Hkv) > 64) return VQKV_ERR_UNSUPPORTED;
-  const int cg = (am->n_queries * (a.Hq / a.Hkv) + 3) / 4;
-  if ((long long)a.B * cg > kMaxGridYZ || a.Hkv > kMaxGridYZ || a.cap_len > kMaxTokens) return VQKV_ERR_UNSUPPORTED;
-  return VQKV_OK;
-}
-
-vqkv_status plan_mass(const vqkv_decode_mass_args* am, MassPlan* pl) {
-  const vqkv_decode_args& a = am->decode;
-  PlanInput in = plan_input(&a);
-  in.M = am->n_queries;
-  in.width = 4;
-  const vqkv_status st = plan_decode(&in, &pl->d);
-  if (st != VQKV_OK) return st;
-  const size_t pairs = (size_t)std::max(a.B, 1) * a.Hkv;
-  const size_t cols = (size_t)am->n_queries * (a.Hq / a.Hkv);
-  // rows to the end of the last step: whole 16-token tiles, up to three of them
-  pl->score_row = (a.max_seq_len + 15) / 16 * 16 + 48;
-  pl->stats_off = round_up(pl->d.ws_bytes, 256);
-  pl->scores_off = round_up(pl->stats_off + pairs * cols * sizeof(float2), 256);
-  pl->ws_bytes = pl->scores_off + pairs * pl->d.cgroups * pl->score_row * 4 * sizeof(float);
-  return VQKV_OK;
+// Sequences b0 .. b0 + kFlatMaxB - 1 (at most) of a call's B.
+DecodeParams batch_part(const DecodeParams& p, int b0, int B) {
+  DecodeParams c = p;
+  c.B = std::min(B - b0, kFlatMaxB);
+  const size_t rows = (size_t)b0 * p.M * p.Hq * 128;
+  c.q = p.q + rows;
+  c.out = p.out + rows;
+  c.seq_lens = p.seq_lens + b0;
+  if (p.mass != nullptr) c.mass = p.mass + (size_t)b0 * p.Hkv * p.cap_len;
+  if (p.block_table != nullptr) {
+    c.block_table = p.block_table + (size_t)b0 * p.max_blocks;
+  } else {
+    c.kc = p.kc + (size_t)b0 * p.Hkv * p.stream_bytes;
+    c.vc = p.vc + (size_t)b0 * p.Hkv * p.stream_bytes;
+  }
+  return c;
 }
 
 // Draft-tree attention: one CTA per SM (its shared memory), all of them in one
@@ -334,6 +315,70 @@ vqkv_status plan_tree(const vqkv_decode_tree_args* at, TreePlan* pl) {
   pl->ws_bytes = pl->partials_off;
   if (pl->n_splits > 1)
     pl->ws_bytes += sizeof(float) * (size_t)a->Hkv * (pl->n_splits + B - 1) * cols * kPartialStride;
+  return VQKV_OK;
+}
+
+// Decode with attention weights.  Few columns: the decode's plan at 4 columns
+// per CTA, then the columns' statistics and the scores behind its workspace.
+// Many: the draft-tree attention, then statistics, query images and sums of
+// the key-only passes.  A group of 4 columns costs one decode pass, the other
+// path about the same for any number: at 196,608 tokens and 8 KV heads 4 / 8
+// columns take 44 / 86 us at 2 bit and 90 / 176 us at 3 bit on the first, and
+// 12 to 32 columns 218 to 223 us and 334 to 339 us on the second, so the first
+// is the faster one up to 16 columns at 3 and 1.5 bit and 20 to 24 at 2 and 4.
+constexpr int kMassFewCols = 16;
+struct MassPlan {
+  bool tiles = false;
+  DecodePlan d;
+  TreePlan t;
+  size_t stats_off = 0, scores_off = 0, image_off = 0, sums_off = 0, ws_bytes = 0;
+  int score_row = 0;
+};
+
+vqkv_status validate_mass_sizes(const vqkv_decode_mass_args* am) {
+  if (am == nullptr) return VQKV_ERR_INVALID_ARG;
+  const vqkv_status st = validate_decode_sizes(&am->decode);
+  if (st != VQKV_OK) return st;
+  const vqkv_decode_args& a = am->decode;
+  if (am->n_queries < 1) return VQKV_ERR_INVALID_ARG;
+  if (am->n_queries > 64 || am->n_queries * (a.Hq / a.Hkv) > 64) return VQKV_ERR_UNSUPPORTED;
+  const int cols = am->n_queries * (a.Hq / a.Hkv);
+  if (a.Hkv > kMaxGridYZ || a.cap_len > kMaxTokens) return VQKV_ERR_UNSUPPORTED;
+  if (cols <= kMassFewCols && (long long)a.B * ((cols + 3) / 4) > kMaxGridYZ) return VQKV_ERR_UNSUPPORTED;
+  if (cols > kMassFewCols && (long long)std::min(a.B, kFlatMaxB) * ((a.max_seq_len + 63) / 64) > kMaxTokens)
+    return VQKV_ERR_UNSUPPORTED;
+  return VQKV_OK;
+}
+
+vqkv_status plan_mass(const vqkv_decode_mass_args* am, MassPlan* pl) {
+  const vqkv_decode_args& a = am->decode;
+  const int ncols = am->n_queries * (a.Hq / a.Hkv);
+  if (ncols > kMassFewCols) {
+    pl->tiles = true;
+    vqkv_decode_tree_args at{};
+    at.decode = a;
+    at.n_queries = am->n_queries;
+    const vqkv_status st = plan_tree(&at, &pl->t);
+    if (st != VQKV_OK) return st;
+    const int B = std::max(std::min(a.B, kFlatMaxB), 1);
+    pl->stats_off = round_up(pl->t.ws_bytes, 256);
+    pl->image_off = round_up(pl->stats_off + (size_t)B * a.Hkv * ncols * sizeof(float2), 256);
+    pl->sums_off = round_up(pl->image_off + mass_tiles_image_bytes(B, a.Hkv, ncols), 256);
+    pl->ws_bytes = pl->sums_off + mass_tiles_sums_bytes(B, a.Hkv, pl->t.n_splits);
+    return VQKV_OK;
+  }
+  PlanInput in = plan_input(&a);
+  in.M = am->n_queries;
+  in.width = 4;
+  const vqkv_status st = plan_decode(&in, &pl->d);
+  if (st != VQKV_OK) return st;
+  const size_t pairs = (size_t)std::max(a.B, 1) * a.Hkv;
+  const size_t cols = (size_t)am->n_queries * (a.Hq / a.Hkv);
+  // rows to the end of the last step: whole 16-token tiles, up to three of them
+  pl->score_row = (a.max_seq_len + 15) / 16 * 16 + 48;
+  pl->stats_off = round_up(pl->d.ws_bytes, 256);
+  pl->scores_off = round_up(pl->stats_off + pairs * cols * sizeof(float2), 256);
+  pl->ws_bytes = pl->scores_off + pairs * pl->d.cgroups * pl->score_row * 4 * sizeof(float);
   return VQKV_OK;
 }
 
@@ -661,13 +706,26 @@ vqkv_status vqkv_decode_attn_mass(const vqkv_decode_mass_args* am, const vqkv_pa
   if (!aligned(a->workspace, 256)) return VQKV_ERR_INVALID_ARG;
   unsigned char* ws = static_cast<unsigned char*>(a->workspace);
   DecodeParams p = packed_params(a, am->n_queries, pg);
-  p.tickets = reinterpret_cast<unsigned*>(ws + pl.d.tickets_off);
-  p.partials = reinterpret_cast<float*>(ws + pl.d.partials_off);
-  p.stats = reinterpret_cast<float2*>(ws + pl.stats_off);
-  p.scores = reinterpret_cast<float*>(ws + pl.scores_off);
-  p.score_row = pl.score_row;
   p.mass = am->mass;
   p.cap_len = a->cap_len;
+  p.stats = reinterpret_cast<float2*>(ws + pl.stats_off);
+  if (pl.tiles) {
+    p.partials = reinterpret_cast<float*>(ws + pl.t.partials_off);
+    p.cgroups = pl.t.cgroups;
+    p.n_splits = pl.t.n_splits;
+    for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
+      const DecodeParams c = batch_part(p, b0, a->B);
+      cudaStream_t s = static_cast<cudaStream_t>(stream);
+      if (launch_decode_tree(a->mode, c, nullptr, ws + kWsHeader, s) != cudaSuccess ||
+          launch_mass_tiles(a->mode, c, ws + pl.image_off, reinterpret_cast<float*>(ws + pl.sums_off), s) != cudaSuccess)
+        return VQKV_ERR_CUDA;
+    }
+    return VQKV_OK;
+  }
+  p.tickets = reinterpret_cast<unsigned*>(ws + pl.d.tickets_off);
+  p.partials = reinterpret_cast<float*>(ws + pl.d.partials_off);
+  p.scores = reinterpret_cast<float*>(ws + pl.scores_off);
+  p.score_row = pl.score_row;
   p.n_splits = pl.d.n_splits;
   p.tps = pl.d.tps;
   p.bpg = pl.d.bpg;
@@ -709,18 +767,7 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_pa
   p.n_splits = pl.n_splits;
   const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(at->tree_mask);
   for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
-    DecodeParams c = p;
-    c.B = std::min(a->B - b0, kFlatMaxB);
-    const size_t rows = (size_t)b0 * p.M * p.Hq * 128;
-    c.q = p.q + rows;
-    c.out = p.out + rows;
-    c.seq_lens = p.seq_lens + b0;
-    if (p.block_table != nullptr) {
-      c.block_table = p.block_table + (size_t)b0 * p.max_blocks;
-    } else {
-      c.kc = p.kc + (size_t)b0 * p.Hkv * p.stream_bytes;
-      c.vc = p.vc + (size_t)b0 * p.Hkv * p.stream_bytes;
-    }
+    const DecodeParams c = batch_part(p, b0, a->B);
     if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, ws + kWsHeader, static_cast<cudaStream_t>(stream)) !=
         cudaSuccess)
       return VQKV_ERR_CUDA;

@@ -118,6 +118,14 @@ size_t decode_tree_query_bytes(int B, int Hkv, int ncols);   // scratch qx of a 
 cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, void* qx,
                                cudaStream_t stream);
 
+// Attention weights of many columns (mass_tiles.cu), after launch_decode_tree has
+// left the columns' running max in p.stats; B <= kFlatMaxB, at most 64 columns.
+// image: transformed queries, sums: the shares' softmax sums.
+cudaError_t mass_tiles_prepare(int mode);
+size_t mass_tiles_image_bytes(int B, int Hkv, int ncols);
+size_t mass_tiles_sums_bytes(int B, int Hkv, int shares);
+cudaError_t launch_mass_tiles(int mode, const DecodeParams& p, void* image, float* sums, cudaStream_t stream);
+
 // Cache editing (cache_edit.cu): the in-place move of chosen tokens, and the
 // choice of the tokens a sequence keeps.
 struct CompactParams {
