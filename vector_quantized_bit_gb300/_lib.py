@@ -406,36 +406,42 @@ def fp16_decode_workspace(B, Hq, Hkv, cap_len, max_seq_len, num_splits=0, device
 
 # ---------------------------------------------------------------- drafts and a changing cache
 
-def _need(what, dtype, *tensors) -> None:
-    """Raises unless every given tensor (None is skipped) is a contiguous ``dtype`` tensor on the current device."""
+def _enter(what, stream, tensors) -> int | None:
+    """The stream handle of a call, after checking its tensors.
+
+    ``tensors``: (name, tensor, dtype, shape) each; None tensors are skipped.
+    Every tensor has to be contiguous and on the current CUDA device.
+    """
     import torch
-    dev = torch.cuda.current_device()
-    for name, t in tensors:
-        if t is None:
+    if stream is None:
+        s = torch.cuda.current_stream()
+        dev, handle = s.device_index, s.cuda_stream
+    else:
+        dev, handle = torch.cuda.current_device(), _stream(stream)
+    for name, t, dtype, shape in tensors:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev):
             continue
         if t.dtype is not dtype:
             raise TypeError(f"{what}: {name} must be {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{what}: {name} must be contiguous")
-        if t.get_device() != dev:
-            raise ValueError(f"{what}: {name} must be on the current CUDA device")
+        raise ValueError(f"{what}: {name} must be on the current CUDA device")
+    return handle
 
 
-def _need_shape(what, name, t, *shape) -> None:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what}: {name} must have shape {shape}, not {tuple(t.shape)}")
-
-
-def _need_cache(what, mode, B, Hkv, cap_len, k_codes, v_codes, block_table, block_tokens, num_blocks) -> None:
-    """Shapes of a contiguous cache [B][Hkv][bytes], or of the pools and the table of a paged one."""
+def _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks):
+    """Shape of a contiguous cache [B][Hkv][bytes], or of the pools of a paged one."""
     if block_table is None:
-        shape = (B, Hkv, vqkv_code_bytes(mode, cap_len))
-    else:
-        shape = (num_blocks, Hkv, vqkv_code_bytes(mode, block_tokens))
-        if block_table.dim() != 2 or block_table.shape[0] != B:
-            raise ValueError(f"{what}: block_table must have shape ({B}, max_blocks)")
-    _need_shape(what, "k_codes", k_codes, *shape)
-    _need_shape(what, "v_codes", v_codes, *shape)
+        return (B, Hkv, vqkv_code_bytes(mode, cap_len))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"{what}: block_table must have shape ({B}, max_blocks)")
+    return (num_blocks, Hkv, vqkv_code_bytes(mode, block_tokens))
+
+
+def _paging_ref(block_table, block_tokens, num_blocks):
+    return ctypes.byref(paging(block_table, block_tokens, num_blocks)) if block_table is not None else None
 
 
 def _new_workspace(nbytes, what, device):
@@ -445,33 +451,31 @@ def _new_workspace(nbytes, what, device):
     return torch.zeros((nbytes + 255) // 256 * 256, dtype=torch.uint8, device=device)
 
 
-def _multi_decode_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace, cap_len,
-                       max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks) -> DecodeArgs:
-    """Checked arguments of a call with q, out [B][M][Hq][128]."""
-    import torch
-    _need(what, torch.float16, ("q", q), ("k_codebook", k_codebook), ("v_codebook", v_codebook), ("out", out))
-    _need(what, torch.uint8, ("k_codes", k_codes), ("v_codes", v_codes), ("workspace", workspace))
-    _need(what, torch.int32, ("seq_lens", seq_lens), ("block_table", block_table))
-    _need(what, torch.float32, ("s", s))
-    B, M, Hq, D = q.shape
-    Hkv = k_codebook.shape[0]
-    _need_cache(what, mode, B, Hkv, cap_len, k_codes, v_codes, block_table, block_tokens, num_blocks)
-    _need_shape(what, "out", out, B, M, Hq, D)
-    _need_shape(what, "seq_lens", seq_lens, B)
-    _need_shape(what, "s", s, Hkv, D)
-    if mode in CODEBOOK_SHAPE:   # the C entry refuses other modes
-        _need_shape(what, "k_codebook", k_codebook, Hkv, *CODEBOOK_SHAPE[mode])
-        _need_shape(what, "v_codebook", v_codebook, Hkv, *CODEBOOK_SHAPE[mode])
-    return DecodeArgs(mode=mode, B=B, Hq=Hq, Hkv=Hkv, head_dim=D, cap_len=cap_len, max_seq_len=max_seq_len,
-                      q=_ptr(q), k_codes=_ptr(k_codes), v_codes=_ptr(v_codes), seq_lens=_ptr(seq_lens),
-                      k_codebook=_ptr(k_codebook), v_codebook=_ptr(v_codebook), s=_ptr(s),
-                      softmax_scale=softmax_scale, num_splits=num_splits, workspace=_ptr(workspace),
-                      workspace_bytes=workspace.numel(), out=_ptr(out))
-
-
 def _size_args(mode, B, Hq, Hkv, cap_len, max_seq_len, num_splits) -> DecodeArgs:
     return DecodeArgs(mode=mode, B=B, Hq=Hq, Hkv=Hkv, head_dim=128, cap_len=cap_len, max_seq_len=max_seq_len,
                       num_splits=num_splits)
+
+
+def _many_query_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace, cap_len,
+                     max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks, stream, more):
+    """(DecodeArgs, stream handle) of a call with q, out [B][M][Hq][128]; ``more(B, M, Hkv)``: its other tensors."""
+    import torch
+    if q.dim() != 4:
+        raise ValueError(f"{what}: q must have shape (B, M, Hq, 128), not {tuple(q.shape)}")
+    B, M, Hq, D = q.shape
+    Hkv = k_codebook.shape[0]
+    f16, i32 = torch.float16, torch.int32
+    cache = _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks)
+    book = (Hkv, *CODEBOOK_SHAPE.get(mode, k_codebook.shape[1:]))   # the C entry refuses other modes
+    handle = _enter(what, stream, (
+        ("q", q, f16, q.shape), ("k_codes", k_codes, torch.uint8, cache), ("v_codes", v_codes, torch.uint8, cache),
+        ("seq_lens", seq_lens, i32, (B,)), ("k_codebook", k_codebook, f16, book), ("v_codebook", v_codebook, f16, book),
+        ("s", s, torch.float32, (Hkv, D)), ("out", out, f16, q.shape),
+        ("workspace", workspace, torch.uint8, workspace.shape),
+        ("block_table", block_table, i32, block_table.shape if block_table is not None else None), *more(B, M, Hkv)))
+    return DecodeArgs(mode, B, Hq, Hkv, D, cap_len, max_seq_len, q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
+                      seq_lens.data_ptr(), k_codebook.data_ptr(), v_codebook.data_ptr(), s.data_ptr(), softmax_scale,
+                      num_splits, workspace.data_ptr(), workspace.numel(), out.data_ptr()), handle
 
 
 def decode_tree_workspace(mode, B, Hq, Hkv, n_queries, cap_len, max_seq_len, num_splits=0, device="cuda"):
@@ -493,14 +497,11 @@ def vqkv_decode_attn_tree(mode, q, tree_mask, k_codes, v_codes, seq_lens, k_code
     """
     import torch
     what = "vqkv_decode_attn_tree"
-    _need(what, torch.int64, ("tree_mask", tree_mask))
-    d = _multi_decode_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace,
-                           cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks)
-    M = q.shape[1]
-    _need_shape(what, "tree_mask", tree_mask, d.B, M)
-    a = DecodeTreeArgs(decode=d, n_queries=M, tree_mask=_ptr(tree_mask))
-    pg = ctypes.byref(paging(block_table, block_tokens, num_blocks)) if block_table is not None else None
-    _check(lib().vqkv_decode_attn_tree(ctypes.byref(a), pg, _stream(stream)), what)
+    d, handle = _many_query_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace,
+                                 cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks,
+                                 stream, lambda B, M, Hkv: (("tree_mask", tree_mask, torch.int64, (B, M)),))
+    a = DecodeTreeArgs(d, q.shape[1], tree_mask.data_ptr())
+    _check(lib().vqkv_decode_attn_tree(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
 
 
 def decode_mass_workspace(mode, B, Hq, Hkv, n_queries, cap_len, max_seq_len, num_splits=0, device="cuda"):
@@ -519,13 +520,11 @@ def vqkv_decode_attn_mass(mode, q, k_codes, v_codes, seq_lens, k_codebook, v_cod
     [B][Hkv][cap_len])."""
     import torch
     what = "vqkv_decode_attn_mass"
-    _need(what, torch.float32, ("mass", mass))
-    d = _multi_decode_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace,
-                           cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks)
-    _need_shape(what, "mass", mass, d.B, d.Hkv, cap_len)
-    a = DecodeMassArgs(decode=d, n_queries=q.shape[1], mass=_ptr(mass))
-    pg = ctypes.byref(paging(block_table, block_tokens, num_blocks)) if block_table is not None else None
-    _check(lib().vqkv_decode_attn_mass(ctypes.byref(a), pg, _stream(stream)), what)
+    d, handle = _many_query_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace,
+                                 cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks,
+                                 stream, lambda B, M, Hkv: (("mass", mass, torch.float32, (B, Hkv, cap_len)),))
+    a = DecodeMassArgs(d, q.shape[1], mass.data_ptr())
+    _check(lib().vqkv_decode_attn_mass(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
 
 
 def vqkv_evict_select(mass, seq_lens, keep, keep_lens, n_sink=0, n_recent=0, max_seq_len=None, error_flags=None,
@@ -539,18 +538,16 @@ def vqkv_evict_select(mass, seq_lens, keep, keep_lens, n_sink=0, n_recent=0, max
     """
     import torch
     what = "vqkv_evict_select"
-    _need(what, torch.float32, ("mass", mass))
-    _need(what, torch.int32, ("seq_lens", seq_lens), ("keep", keep), ("keep_lens", keep_lens),
-          ("error_flags", error_flags))
+    i32 = torch.int32
     B, Hkv, cap = mass.shape
     n_keep = keep.shape[-1]
-    _need_shape(what, "keep", keep, B, Hkv, n_keep)
-    _need_shape(what, "seq_lens", seq_lens, B)
-    _need_shape(what, "keep_lens", keep_lens, B)
-    a = EvictSelectArgs(B=B, Hkv=Hkv, cap_len=cap, max_seq_len=cap if max_seq_len is None else max_seq_len,
-                        n_keep=n_keep, n_sink=n_sink, n_recent=n_recent, mass=_ptr(mass), seq_lens=_ptr(seq_lens),
-                        keep=_ptr(keep), keep_lens=_ptr(keep_lens), error_flags=_ptr(error_flags))
-    _check(lib().vqkv_evict_select(ctypes.byref(a), _stream(stream)), what)
+    handle = _enter(what, stream, (
+        ("mass", mass, torch.float32, mass.shape), ("seq_lens", seq_lens, i32, (B,)),
+        ("keep", keep, i32, (B, Hkv, n_keep)), ("keep_lens", keep_lens, i32, (B,)),
+        ("error_flags", error_flags, i32, (1,))))
+    a = EvictSelectArgs(B, Hkv, cap, cap if max_seq_len is None else max_seq_len, n_keep, n_sink, n_recent,
+                        mass.data_ptr(), seq_lens.data_ptr(), keep.data_ptr(), keep_lens.data_ptr(), _ptr(error_flags))
+    _check(lib().vqkv_evict_select(ctypes.byref(a), handle), what)
 
 
 def vqkv_cache_compact(mode, k_codes, v_codes, seq_lens, src, counts, cap_len, start=None, mass=None,
@@ -565,24 +562,19 @@ def vqkv_cache_compact(mode, k_codes, v_codes, seq_lens, src, counts, cap_len, s
     """
     import torch
     what = "vqkv_cache_compact"
-    _need(what, torch.uint8, ("k_codes", k_codes), ("v_codes", v_codes))
-    _need(what, torch.int32, ("seq_lens", seq_lens), ("src", src), ("counts", counts), ("start", start),
-          ("error_flags", error_flags), ("block_table", block_table))
-    _need(what, torch.float32, ("mass", mass))
+    i32 = torch.int32
     B, heads, n = src.shape
     Hkv = k_codes.shape[1]
-    _need_cache(what, mode, B, Hkv, cap_len, k_codes, v_codes, block_table, block_tokens, num_blocks)
-    _need_shape(what, "seq_lens", seq_lens, B)
-    _need_shape(what, "counts", counts, B)
-    if start is not None:
-        _need_shape(what, "start", start, B)
-    if mass is not None:
-        _need_shape(what, "mass", mass, B, Hkv, cap_len)
-    a = CacheCompactArgs(mode=mode, B=B, Hkv=Hkv, cap_len=cap_len, n_src=n, src_heads=heads, k_codes=_ptr(k_codes),
-                         v_codes=_ptr(v_codes), seq_lens=_ptr(seq_lens), src=_ptr(src), counts=_ptr(counts),
-                         start=_ptr(start), mass=_ptr(mass), error_flags=_ptr(error_flags))
-    pg = ctypes.byref(paging(block_table, block_tokens, num_blocks)) if block_table is not None else None
-    _check(lib().vqkv_cache_compact(ctypes.byref(a), pg, _stream(stream)), what)
+    cache = _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks)
+    handle = _enter(what, stream, (
+        ("k_codes", k_codes, torch.uint8, cache), ("v_codes", v_codes, torch.uint8, cache),
+        ("seq_lens", seq_lens, i32, (B,)), ("src", src, i32, src.shape), ("counts", counts, i32, (B,)),
+        ("start", start, i32, (B,)), ("mass", mass, torch.float32, (B, Hkv, cap_len)),
+        ("error_flags", error_flags, i32, (1,)),
+        ("block_table", block_table, i32, block_table.shape if block_table is not None else None)))
+    a = CacheCompactArgs(mode, B, Hkv, cap_len, n, heads, k_codes.data_ptr(), v_codes.data_ptr(), seq_lens.data_ptr(),
+                         src.data_ptr(), counts.data_ptr(), _ptr(start), _ptr(mass), _ptr(error_flags))
+    _check(lib().vqkv_cache_compact(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
 
 
 # ---------------------------------------------------------------- calibration
