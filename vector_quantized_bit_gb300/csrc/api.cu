@@ -21,6 +21,7 @@ struct DeviceInfo {
   int sms = 0;
   int decode_bpsm[kCodeModes + 1] = {};   // resident decode CTAs per SM: each code mode, then fp16
   int encode_bpsm[kCodeModes] = {};
+  int compact_cluster[kCodeModes] = {};   // largest cluster of the compaction
 };
 
 std::mutex g_mu;
@@ -36,7 +37,8 @@ vqkv_status device_info(DeviceInfo* out) {
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return VQKV_ERR_NO_DEVICE;
     for (int m = 0; m < kCodeModes; ++m) {
       if (decode_prepare(m) != cudaSuccess || encode_prepare(m) != cudaSuccess || decode_tree_prepare(m) != cudaSuccess ||
-          decode_mass_prepare(m) != cudaSuccess || mass_tiles_prepare(m) != cudaSuccess)
+          decode_mass_prepare(m) != cudaSuccess || mass_tiles_prepare(m) != cudaSuccess ||
+          compact_prepare(m, &d.compact_cluster[m]) != cudaSuccess)
         return VQKV_ERR_CUDA;
       if (decode_occupancy(m, &d.decode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
       if (encode_occupancy(m, &d.encode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
@@ -841,7 +843,9 @@ vqkv_status vqkv_cache_compact(const vqkv_cache_compact_args* a, const vqkv_pagi
   p.n_src = a->n_src;
   p.cap_len = a->cap_len;
   set_paging(p, pg, a->mode);
-  return launch_compact(a->mode, p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
+  return launch_compact(a->mode, p, di.sms, di.compact_cluster[a->mode], static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? VQKV_OK
+             : VQKV_ERR_CUDA;
 }
 
 const char* vqkv_status_string(vqkv_status s) {

@@ -60,8 +60,8 @@ cudaError_t launch_cluster(void (*kernel)(Args...), dim3 grid, int cluster, int 
 // and of earlier rounds is done), write the round.
 //
 // Bound: latency of the dependent loads (source index, then the source's
-// bytes), so a warp keeps four or eight 16-token groups in flight per round and
-// loads the next round's indices before it writes.
+// bytes), so a warp has two 16-token groups in flight at a time, two or four per
+// round, and loads the next round's indices before it writes.
 //
 // The layouts keep every token's bytes to itself, spread over the 32 lanes'
 // runs of a 16-token group (include/vqkv.h).  A lane of the destination group
@@ -255,7 +255,7 @@ __device__ __forceinline__ void move_codes(const CompactParams& p, const Move& m
   const int gid = lane >> 2, tig = lane & 3;
   uint8_t* codes = p.codes[ROLE];
   const int first = mv.start >> 4, last = mv.n > 0 ? (mv.start + mv.n + 15) >> 4 : first;   // 16-token groups
-  constexpr int U = G::W <= 4 ? 8 : 4;   // groups per warp and round (32 words of runs at most)
+  constexpr int U = G::W <= 4 ? 4 : 2;   // groups per warp and round (16 words of runs at most)
   const int per = cluster * CP_WARPS * U;
   const int rounds = (last - first + per - 1) / per;
   // the warp's groups of round k are neighbours; lane l looks up token l % 16
@@ -287,25 +287,31 @@ __device__ __forceinline__ void move_codes(const CompactParams& p, const Move& m
       }
       from |= src[i] & 63;   // tile offsets are multiples of 64
       const unsigned moves = __ballot_sync(0xffffffffu, grp < last && !bad && src[i] != d);
+      place[2 * i] = place[2 * i + 1] = -1;
+      if (moves == 0) continue;   // nothing moves: leave the groups as they are
+      // both groups' loads go out before the first is used (one that does not
+      // move, or lies past the last, reads some token of the cache for nothing)
+      Bytes<G::SB> v[2][G::SLOTS];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = 2 * i + h;
-#pragma unroll
-        for (int q = 0; q < G::W; ++q) w[j][q] = 0u;
-        const long long at = __shfl_sync(0xffffffffu, dst, 16 * h);
-        place[j] = -1;
-        if (((moves >> (16 * h)) & 0xffffu) == 0) continue;   // nothing moves: leave the group as it is
-        place[j] = at | (((first_group(k) + j) & 3) << 4);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int q = 0; q < G::SLOTS; ++q) {
           const int r = ROLE == VQKV_ROLE_K ? gid + 8 * q : 2 * tig + (q & 1) + 8 * (q >> 1);
           const long long f = __shfl_sync(0xffffffffu, from, 16 * h + r);
-          if (!(MODE == VQKV_MODE_VQ125 && ROLE == VQKV_ROLE_V) || lane < 16) {
-            const int pos = (int)(f & 63);
-            put_slot<MODE, ROLE>(w[j], q, load_slot<MODE, ROLE>(codes + (f & ~63LL), pos & 15, (pos >> 4) & 3,
-                                                                ROLE == VQKV_ROLE_K ? tig : gid));
-          }
+          const int pos = (int)(f & 63);
+          // (1.25-bit V: 16 runs, lanes 16 .. 31 repeat those of 0 .. 15)
+          const int x = ROLE == VQKV_ROLE_K ? tig : MODE == VQKV_MODE_VQ125 ? gid & 3 : gid;
+          v[h][q] = load_slot<MODE, ROLE>(codes + (f & ~63LL), pos & 15, (pos >> 4) & 3, x);
         }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = 2 * i + h;
+        const long long at = __shfl_sync(0xffffffffu, dst, 16 * h);
+        if ((moves >> (16 * h)) & 0xffffu) place[j] = at | (((first_group(k) + j) & 3) << 4);
+#pragma unroll
+        for (int q = 0; q < G::W; ++q) w[j][q] = 0u;
+#pragma unroll
+        for (int q = 0; q < G::SLOTS; ++q) put_slot<MODE, ROLE>(w[j], q, v[h][q]);
       }
     }
     if (k + 1 < rounds) lookup(k + 1, src);
@@ -343,7 +349,7 @@ __device__ __forceinline__ void move_mass(const CompactParams& p, const Move& mv
 
 // grid (cluster, Hkv x streams, B): stream 0 = K codes, 1 = V codes, 2 = mass.
 template <int MODE, bool PAGED>
-__global__ void __launch_bounds__(CP_THREADS) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(CP_THREADS, 2) compact_kernel(const CompactParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int streams = p.mass != nullptr ? 3 : 2;
@@ -595,19 +601,48 @@ constexpr CompactKernel compact_of(bool paged) {
 
 }  // namespace
 
-cudaError_t launch_compact(int mode, const CompactParams& p, int sms, cudaStream_t stream) {
-  const bool paged = p.block_table != nullptr;
-  const CompactKernel k = mode == VQKV_MODE_VQ2    ? compact_of<VQKV_MODE_VQ2>(paged)
-                          : mode == VQKV_MODE_VQ4  ? compact_of<VQKV_MODE_VQ4>(paged)
-                          : mode == VQKV_MODE_VQ3  ? compact_of<VQKV_MODE_VQ3>(paged)
-                          : mode == VQKV_MODE_VQ15 ? compact_of<VQKV_MODE_VQ15>(paged)
-                                                   : compact_of<VQKV_MODE_VQ125>(paged);
-  // CTAs per stream: enough that one round holds the destinations, at most
-  // eight (the portable cluster), fewer when the streams alone fill the GPU
+static CompactKernel compact_kernel_of(int mode, bool paged) {
+  return mode == VQKV_MODE_VQ2    ? compact_of<VQKV_MODE_VQ2>(paged)
+         : mode == VQKV_MODE_VQ4  ? compact_of<VQKV_MODE_VQ4>(paged)
+         : mode == VQKV_MODE_VQ3  ? compact_of<VQKV_MODE_VQ3>(paged)
+         : mode == VQKV_MODE_VQ15 ? compact_of<VQKV_MODE_VQ15>(paged)
+                                  : compact_of<VQKV_MODE_VQ125>(paged);
+}
+
+// Largest cluster the device can place: 16 CTAs where it can (beyond the
+// portable 8), so that the few streams of one sequence still cover the GPU.
+cudaError_t compact_prepare(int mode, int* max_cluster) {
+  cudaError_t e = cudaSuccess;
+  for (int paged = 0; paged < 2 && e == cudaSuccess; ++paged)
+    e = cudaFuncSetAttribute(compact_kernel_of(mode, paged != 0), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16, 1, 1);
+  cfg.blockDim = dim3(CP_THREADS);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 16;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, compact_kernel_of(mode, true), &cfg) != cudaSuccess) {
+    cudaGetLastError();   // not an error of the call: the portable size is used
+    n = 0;
+  }
+  *max_cluster = n > 0 ? 16 : 8;
+  return cudaSuccess;
+}
+
+cudaError_t launch_compact(int mode, const CompactParams& p, int sms, int max_cluster, cudaStream_t stream) {
+  const CompactKernel k = compact_kernel_of(mode, p.block_table != nullptr);
+  // CTAs per stream: enough that one round holds the destinations, fewer when
+  // the streams alone fill the GPU
   const long long streams = (long long)p.B * p.Hkv * (p.mass != nullptr ? 3 : 2);
   const long long groups = ((long long)p.n_src + 30) / 16;
   int cluster = 1;
-  while (cluster < 8 && (long long)cluster * CP_WARPS < groups && streams * cluster < 2LL * sms) cluster *= 2;
+  while (cluster < max_cluster && (long long)cluster * CP_WARPS < groups && streams * cluster < 2LL * sms) cluster *= 2;
   return launch_cluster(k, dim3(cluster, p.Hkv * (p.mass != nullptr ? 3 : 2), p.B), cluster, CP_THREADS, 0, stream, p);
 }
 

@@ -152,7 +152,8 @@ struct SelectParams {
   int B, Hkv, cap_len, max_seq_len, n_keep, n_sink, n_recent;
   int cache_keys = 0;       // keys of a CTA's part that fit in its shared memory (0: read again per pass)
 };
-cudaError_t launch_compact(int mode, const CompactParams& p, int sms, cudaStream_t stream);
+cudaError_t compact_prepare(int mode, int* max_cluster);   // once per device
+cudaError_t launch_compact(int mode, const CompactParams& p, int sms, int max_cluster, cudaStream_t stream);
 cudaError_t evict_select_prepare();   // set smem attributes (once per device)
 cudaError_t launch_evict_select(SelectParams p, int sms, cudaStream_t stream);
 
