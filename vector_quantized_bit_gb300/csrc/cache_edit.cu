@@ -56,12 +56,12 @@ cudaError_t launch_cluster(void (*kernel)(Args...), dim3 grid, int cluster, int 
 // that position.  A cluster of CTAs owns one stream and walks it in rounds of
 // consecutive destination tokens; a round's sources are >= its destinations,
 // so its writes can only hit sources of the same or an earlier round.  Hence:
-// read a round into registers, meet at the cluster barrier (every read of this
-// and of earlier rounds is done), write the round.
+// read a round into registers, arrive at the cluster barrier (this CTA's reads
+// of this and of earlier rounds are done), issue the reads of the next round,
+// wait for the cluster, write the round.
 //
 // Bound: latency of the dependent loads (source index, then the source's
-// bytes), so a warp has two 16-token groups in flight at a time, two or four per
-// round, and loads the next round's indices before it writes.
+// bytes): the indices are loaded two rounds ahead, the bytes one.
 //
 // The layouts keep every token's bytes to itself, spread over the 32 lanes'
 // runs of a 16-token group (include/vqkv.h).  A lane of the destination group
@@ -77,11 +77,6 @@ struct Bytes {
   uint32_t w[(BYTES + 3) / 4];
 };
 
-__device__ __forceinline__ uint32_t ld8(const uint8_t* p) {
-  uint32_t v;
-  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint32_t ld16(const uint8_t* p) {
   uint16_t v;
   asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
@@ -144,29 +139,30 @@ __device__ __forceinline__ Bytes<RunGeo<MODE, ROLE>::SB> load_slot(const uint8_t
     const uint32_t mid = slot ? a.x : ld32(p + 16 * L + 4);
     o.w[1] = mid, o.w[2] = slot ? a.y : a.x;
   } else if constexpr (MODE == VQKV_MODE_VQ3) {
-    uint32_t h[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const int n = 6 * slot + 2 * k;
-      h[k] = ld16(n < 16 ? p + 16 * L + n : p + 512 + 8 * L + n - 16);
-    }
-    o.w[0] = h[0] | (h[1] << 16), o.w[1] = h[2];
+    // run bytes 6 slot .. + 5 of the words (6 slot) / 4 and the next (plane 1 from word 4)
+    const int i = (6 * slot) >> 2, sh = 16 * (slot & 1);
+    auto word = [&](int n) { return ld32(n < 4 ? p + 16 * L + 4 * n : p + 512 + 8 * L + 4 * (n - 4)); };
+    const uint32_t a = word(i), b = word(i + 1);
+    o.w[0] = __funnelshift_r(a, b, sh), o.w[1] = b >> sh;
   } else if constexpr (MODE == VQKV_MODE_VQ15 && ROLE == VQKV_ROLE_K) {
-    const uint8_t* q = p + 48 * L + 12 * u + 6 * slot;
-    const uint32_t a = ld16(q), b = ld16(q + 2), c = ld16(q + 4);
-    o.w[0] = a | (b << 16), o.w[1] = c;
+    const uint8_t* q = p + 48 * L + 12 * u + 4 * slot;   // words slot, slot + 1 of the lane's 12 bytes
+    const uint32_t a = ld32(q), b = ld32(q + 4);
+    o.w[0] = __funnelshift_r(a, b, 16 * slot), o.w[1] = b >> (16 * slot);
   } else if constexpr (MODE == VQKV_MODE_VQ15) {
-    const uint8_t* q = p + 48 * L + 12 * u + 3 * slot;
-    o.w[0] = ld8(q) | (ld8(q + 1) << 8) | (ld8(q + 2) << 16);
-  } else {
-    constexpr int P0 = ROLE == VQKV_ROLE_K ? 8 : 16, P1 = ROLE == VQKV_ROLE_K ? 2 : 4;
-    uint32_t b[5];
-#pragma unroll
-    for (int k = 0; k < 5; ++k) {
-      const int n = 5 * slot + k;
-      b[k] = ld8(n < P0 ? p + P0 * L + n : p + 256 + P1 * L + n - P0);
-    }
-    o.w[0] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24), o.w[1] = b[4];
+    // bytes 3 slot .. + 2: words (3 slot) / 4 (at most the second) and the next
+    const int i = slot < 3 ? (3 * slot) >> 2 : 1;
+    const uint8_t* q = p + 48 * L + 12 * u + 4 * i;
+    const uint32_t a = ld32(q), b = ld32(q + 4);
+    o.w[0] = slot < 3 ? __funnelshift_r(a, b, 24 * slot - 32 * i) : b >> 8;
+  } else if constexpr (ROLE == VQKV_ROLE_K) {   // 80-bit run: 8 bytes, then 2 in plane 1
+    const uint2 a = ld64(p + 8 * L);
+    const uint32_t c = ld16(p + 256 + 2 * L);
+    o.w[0] = slot ? __funnelshift_r(a.y, c, 8) : a.x;   // bytes 5 .. 8 or 0 .. 3
+    o.w[1] = slot ? c >> 8 : a.y;                       // byte 9 or 4
+  } else {   // 160-bit run: words (5 slot) / 4 and the next (the fifth in plane 1)
+    const uint32_t a = ld32(p + 16 * L + 4 * slot);
+    const uint32_t b = ld32(slot < 3 ? p + 16 * L + 4 * slot + 4 : p + 256 + 4 * L);
+    o.w[0] = __funnelshift_r(a, b, 8 * slot), o.w[1] = b >> (8 * slot);
   }
   return o;
 }
@@ -268,30 +264,29 @@ __device__ __forceinline__ void move_codes(const CompactParams& p, const Move& m
       s[i] = grp < last ? mv.source(p, (grp << 4) + (lane & 15), ROLE == VQKV_ROLE_K) : -1;
     }
   };
-  int src[U / 2];
-  if (rounds > 0) lookup(0, src);
-  for (int k = 0; k < rounds; ++k) {
-    uint32_t w[U][G::W];
-    long long place[U];   // tile offset | 16 x (group within the tile), -1: nothing to write
+  int src[U / 2];                          // sources of the round whose bytes are loaded next
+  Bytes<G::SB> v[U][G::SLOTS];             // its bytes, in flight
+  long long dst[U / 2];                    // lane: tile offset of its group of pair i
+  unsigned moves[U / 2];                   // tokens of pair i that move
+  auto fetch = [&](int k) {
 #pragma unroll
     for (int i = 0; i < U / 2; ++i) {
-      // where each of the 32 tokens comes from: tile offset | position within the tile
+      // where each of the pair's 32 tokens comes from: tile offset | position within the tile
       const int grp = first_group(k) + 2 * i + (lane >> 4), d = (grp << 4) + (lane & 15);
       bool bad = false, sbad = false;
-      long long dst = 0, from = 0;
+      long long from = 0;
+      dst[i] = 0;
       if (grp < last) {
-        dst = tile_offset<PAGED>(p, mv.b, mv.kvh, d / TT, TILE_BYTES, &bad);
+        dst[i] = tile_offset<PAGED>(p, mv.b, mv.kvh, d / TT, TILE_BYTES, &bad);
         from = tile_offset<PAGED>(p, mv.b, mv.kvh, src[i] / TT, TILE_BYTES, &sbad);
-        if (sbad) from = dst, src[i] = d;
+        if (sbad) from = dst[i], src[i] = d;
         if (PAGED && (bad || sbad) && p.err != nullptr) atomicOr(p.err, VQKV_DEVERR_BLOCK);
       }
       from |= src[i] & 63;   // tile offsets are multiples of 64
-      const unsigned moves = __ballot_sync(0xffffffffu, grp < last && !bad && src[i] != d);
-      place[2 * i] = place[2 * i + 1] = -1;
-      if (moves == 0) continue;   // nothing moves: leave the groups as they are
-      // both groups' loads go out before the first is used (one that does not
-      // move, or lies past the last, reads some token of the cache for nothing)
-      Bytes<G::SB> v[2][G::SLOTS];
+      moves[i] = __ballot_sync(0xffffffffu, grp < last && !bad && src[i] != d);
+      if (moves[i] == 0) continue;   // nothing moves: leave the groups as they are
+      // (a group of the pair that does not move, or lies past the last, reads
+      // some token of the cache for nothing)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -301,21 +296,33 @@ __device__ __forceinline__ void move_codes(const CompactParams& p, const Move& m
           const int pos = (int)(f & 63);
           // (1.25-bit V: 16 runs, lanes 16 .. 31 repeat those of 0 .. 15)
           const int x = ROLE == VQKV_ROLE_K ? tig : MODE == VQKV_MODE_VQ125 ? gid & 3 : gid;
-          v[h][q] = load_slot<MODE, ROLE>(codes + (f & ~63LL), pos & 15, (pos >> 4) & 3, x);
+          v[2 * i + h][q] = load_slot<MODE, ROLE>(codes + (f & ~63LL), pos & 15, (pos >> 4) & 3, x);
         }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = 2 * i + h;
-        const long long at = __shfl_sync(0xffffffffu, dst, 16 * h);
-        if ((moves >> (16 * h)) & 0xffffu) place[j] = at | (((first_group(k) + j) & 3) << 4);
-#pragma unroll
-        for (int q = 0; q < G::W; ++q) w[j][q] = 0u;
-#pragma unroll
-        for (int q = 0; q < G::SLOTS; ++q) put_slot<MODE, ROLE>(w[j], q, v[h][q]);
-      }
     }
-    if (k + 1 < rounds) lookup(k + 1, src);
-    if (cluster > 1) cluster_sync(); else __syncthreads();
+  };
+  if (rounds > 0) {
+    lookup(0, src);
+    fetch(0);
+    if (rounds > 1) lookup(1, src);
+  }
+  for (int k = 0; k < rounds; ++k) {
+    uint32_t w[U][G::W];
+    long long place[U];   // tile offset | 16 x (group within the tile), -1: nothing to write
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const long long at = __shfl_sync(0xffffffffu, dst[j >> 1], 16 * (j & 1));
+      place[j] = ((moves[j >> 1] >> (16 * (j & 1))) & 0xffffu) ? at | (((first_group(k) + j) & 3) << 4) : -1;
+#pragma unroll
+      for (int q = 0; q < G::W; ++q) w[j][q] = 0u;
+#pragma unroll
+      for (int q = 0; q < G::SLOTS; ++q) put_slot<MODE, ROLE>(w[j], q, v[j][q]);
+    }
+    cluster_arrive();
+    if (k + 1 < rounds) {
+      fetch(k + 1);
+      if (k + 2 < rounds) lookup(k + 2, src);
+    }
+    cluster_wait();
 #pragma unroll
     for (int j = 0; j < U; ++j)
       if (place[j] >= 0) store_run<MODE, ROLE>(codes + (place[j] & ~63LL), (int)((place[j] >> 4) & 3), lane, w[j]);
@@ -338,7 +345,7 @@ __device__ __forceinline__ void move_mass(const CompactParams& p, const Move& mv
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (s[u] >= 0) v[u] = __uint_as_float(ld32(reinterpret_cast<const uint8_t*>(row + s[u])));
-    if (cluster > 1) cluster_sync(); else __syncthreads();
+    cluster_sync();
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (s[u] >= 0) row[mv.start + k * per + (rank * U + u) * CP_THREADS + (int)threadIdx.x] = v[u];
