@@ -644,12 +644,17 @@ cudaError_t compact_prepare(int mode, int* max_cluster) {
 
 cudaError_t launch_compact(int mode, const CompactParams& p, int sms, int max_cluster, cudaStream_t stream) {
   const CompactKernel k = compact_kernel_of(mode, p.block_table != nullptr);
-  // CTAs per stream: enough that one round holds the destinations, fewer when
-  // the streams alone fill the GPU
+  // CTAs per stream: at most what one round of its destinations needs, and up to
+  // 8 while all CTAs are fewer than eight per SM (384 streams of a paged
+  // 1.25-bit batch: 113 us at 1 CTA each, 88 at 4, 99 at 8).  Sixteen, beyond the
+  // portable size, only for so few streams that eight would leave SMs idle: 24
+  // streams of 196,608 tokens 46 -> 42 us, but 96 streams of 16,384 19 -> 36 us,
+  // because few clusters of 16 are placed at a time.
   const long long streams = (long long)p.B * p.Hkv * (p.mass != nullptr ? 3 : 2);
   const long long groups = ((long long)p.n_src + 30) / 16;
   int cluster = 1;
-  while (cluster < max_cluster && (long long)cluster * CP_WARPS < groups && streams * cluster < 2LL * sms) cluster *= 2;
+  while (cluster < 8 && (long long)cluster * CP_WARPS < groups && streams * cluster < 8LL * sms) cluster *= 2;
+  if (cluster == 8 && max_cluster == 16 && 8LL * CP_WARPS < groups && streams * 8 < 2LL * sms) cluster = 16;
   return launch_cluster(k, dim3(cluster, p.Hkv * (p.mass != nullptr ? 3 : 2), p.B), cluster, CP_THREADS, 0, stream, p);
 }
 
