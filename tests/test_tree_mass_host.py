@@ -55,7 +55,7 @@ def _mass(n_queries=2, mass=0xa000, **kw):
     (dict(n_queries=0), 1), (dict(n_queries=17), 2), (dict(n_queries=2**31 - 1), 2), (dict(mass=None), 1),
     (dict(mass=0xa002), 1), (dict(mode=7), 2), (dict(head_dim=64), 2), (dict(max_seq_len=65), 1), (dict(q=None), 1),
     (dict(v_codes=0x3008), 1), (dict(B=65536), 2), (dict(cap_len=2**30 + 1), 2),
-    (dict(n_queries=4, B=128, cap_len=2**30, max_seq_len=2**30), 2),
+    (dict(n_queries=16, B=128, cap_len=2**30, max_seq_len=2**30), 2),
 ])
 def test_mass_validation(lib, kw, status):
     assert lib.vqkv_decode_attn_mass(ctypes.byref(_mass(**kw)), None, None) == status

@@ -301,7 +301,7 @@ vqkv_status validate_tree_sizes(const vqkv_decode_tree_args* at) {
   return VQKV_OK;
 }
 
-vqkv_status plan_tree(const vqkv_decode_tree_args* at, TreePlan* pl) {
+vqkv_status plan_tree(const vqkv_decode_tree_args* at, bool pairs, TreePlan* pl) {
   DeviceInfo di;
   const vqkv_status st = device_info(&di);
   if (st != VQKV_OK) return st;
@@ -313,7 +313,7 @@ vqkv_status plan_tree(const vqkv_decode_tree_args* at, TreePlan* pl) {
   const long long tiles = std::max<long long>(1, (long long)B * ((a->max_seq_len + 63) / 64));
   const long long want = a->num_splits > 0 ? std::min(a->num_splits, 1024) : di.sms / ((long long)a->Hkv * pl->cgroups);
   pl->n_splits = (int)std::max<long long>(1, std::min(want, tiles));
-  pl->partials_off = kWsHeader + round_up(decode_tree_query_bytes(B, a->Hkv, cols), 256);
+  pl->partials_off = kWsHeader + round_up(decode_tree_query_bytes(B, a->Hkv, cols, pairs), 256);
   pl->ws_bytes = pl->partials_off;
   if (pl->n_splits > 1)
     pl->ws_bytes += sizeof(float) * (size_t)a->Hkv * (pl->n_splits + B - 1) * cols * kPartialStride;
@@ -322,18 +322,18 @@ vqkv_status plan_tree(const vqkv_decode_tree_args* at, TreePlan* pl) {
 
 // Decode with attention weights.  Few columns: the decode's plan at 4 columns
 // per CTA, then the columns' statistics and the scores behind its workspace.
-// Many: the draft-tree attention, then statistics, query images and sums of
-// the key-only passes.  A group of 4 columns costs one decode pass, the other
-// path about the same for any number: at 196,608 tokens and 8 KV heads 4 / 8
-// columns take 44 / 86 us at 2 bit and 90 / 176 us at 3 bit on the first, and
-// 12 to 32 columns 218 to 223 us and 334 to 339 us on the second, so the first
-// is the faster one up to 16 columns at 3 and 1.5 bit and 20 to 24 at 2 and 4.
-constexpr int kMassFewCols = 16;
+// Many: the draft-tree attention, then statistics and query images of the
+// key-only pass.  A group of 4 columns costs one decode, the other path about
+// the same for any number: at 196,608 tokens and 8 KV heads 12 / 16 columns take
+// 127 / 168 us at 2 bit, 151 / 199 at 4, 261 / 346 at 3 and 240 / 328 at 1.5 on
+// the first path, and 32 columns 186, 266, 267 and 260 us on the second.
+int mass_few_cols(int mode) { return mode == VQKV_MODE_VQ3 || mode == VQKV_MODE_VQ15 ? 12 : 16; }
+
 struct MassPlan {
   bool tiles = false;
   DecodePlan d;
   TreePlan t;
-  size_t stats_off = 0, scores_off = 0, image_off = 0, sums_off = 0, ws_bytes = 0;
+  size_t stats_off = 0, scores_off = 0, image_off = 0, ws_bytes = 0;
   int score_row = 0;
 };
 
@@ -346,8 +346,8 @@ vqkv_status validate_mass_sizes(const vqkv_decode_mass_args* am) {
   if (am->n_queries > 64 || am->n_queries * (a.Hq / a.Hkv) > 64) return VQKV_ERR_UNSUPPORTED;
   const int cols = am->n_queries * (a.Hq / a.Hkv);
   if (a.Hkv > kMaxGridYZ || a.cap_len > kMaxTokens) return VQKV_ERR_UNSUPPORTED;
-  if (cols <= kMassFewCols && (long long)a.B * ((cols + 3) / 4) > kMaxGridYZ) return VQKV_ERR_UNSUPPORTED;
-  if (cols > kMassFewCols && (long long)std::min(a.B, kFlatMaxB) * ((a.max_seq_len + 63) / 64) > kMaxTokens)
+  if (cols <= mass_few_cols(a.mode) && (long long)a.B * ((cols + 3) / 4) > kMaxGridYZ) return VQKV_ERR_UNSUPPORTED;
+  if (cols > mass_few_cols(a.mode) && (long long)std::min(a.B, kFlatMaxB) * ((a.max_seq_len + 63) / 64) > kMaxTokens)
     return VQKV_ERR_UNSUPPORTED;
   return VQKV_OK;
 }
@@ -355,18 +355,17 @@ vqkv_status validate_mass_sizes(const vqkv_decode_mass_args* am) {
 vqkv_status plan_mass(const vqkv_decode_mass_args* am, MassPlan* pl) {
   const vqkv_decode_args& a = am->decode;
   const int ncols = am->n_queries * (a.Hq / a.Hkv);
-  if (ncols > kMassFewCols) {
+  if (ncols > mass_few_cols(a.mode)) {
     pl->tiles = true;
     vqkv_decode_tree_args at{};
     at.decode = a;
     at.n_queries = am->n_queries;
-    const vqkv_status st = plan_tree(&at, &pl->t);
+    const vqkv_status st = plan_tree(&at, true, &pl->t);
     if (st != VQKV_OK) return st;
     const int B = std::max(std::min(a.B, kFlatMaxB), 1);
     pl->stats_off = round_up(pl->t.ws_bytes, 256);
     pl->image_off = round_up(pl->stats_off + (size_t)B * a.Hkv * ncols * sizeof(float2), 256);
-    pl->sums_off = round_up(pl->image_off + mass_tiles_image_bytes(B, a.Hkv, ncols), 256);
-    pl->ws_bytes = pl->sums_off + mass_tiles_sums_bytes(B, a.Hkv, pl->t.n_splits);
+    pl->ws_bytes = pl->image_off + mass_tiles_image_bytes(B, a.Hkv, ncols);
     return VQKV_OK;
   }
   PlanInput in = plan_input(&a);
@@ -718,8 +717,8 @@ vqkv_status vqkv_decode_attn_mass(const vqkv_decode_mass_args* am, const vqkv_pa
     for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
       const DecodeParams c = batch_part(p, b0, a->B);
       cudaStream_t s = static_cast<cudaStream_t>(stream);
-      if (launch_decode_tree(a->mode, c, nullptr, ws + kWsHeader, s) != cudaSuccess ||
-          launch_mass_tiles(a->mode, c, ws + pl.image_off, reinterpret_cast<float*>(ws + pl.sums_off), s) != cudaSuccess)
+      if (launch_decode_tree(a->mode, c, nullptr, true, ws + kWsHeader, s) != cudaSuccess ||
+          launch_mass_tiles(a->mode, c, ws + pl.image_off, s) != cudaSuccess)
         return VQKV_ERR_CUDA;
     }
     return VQKV_OK;
@@ -740,7 +739,7 @@ vqkv_status vqkv_decode_attn_mass(const vqkv_decode_mass_args* am, const vqkv_pa
 
 size_t vqkv_decode_tree_workspace_bytes(const vqkv_decode_tree_args* a) {
   TreePlan pl;
-  if (validate_tree_sizes(a) != VQKV_OK || plan_tree(a, &pl) != VQKV_OK) return 0;
+  if (validate_tree_sizes(a) != VQKV_OK || plan_tree(a, false, &pl) != VQKV_OK) return 0;
   return pl.ws_bytes;
 }
 
@@ -758,7 +757,7 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_pa
   if (a->B == 0) return VQKV_OK;
   if (!at->tree_mask || !aligned(at->tree_mask, 8)) return VQKV_ERR_INVALID_ARG;
   TreePlan pl;
-  st = plan_tree(at, &pl);
+  st = plan_tree(at, false, &pl);
   if (st != VQKV_OK) return st;
   if (a->workspace == nullptr || a->workspace_bytes < pl.ws_bytes) return VQKV_ERR_WORKSPACE;
   if (!aligned(a->workspace, 256)) return VQKV_ERR_INVALID_ARG;
@@ -770,7 +769,7 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_pa
   const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(at->tree_mask);
   for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
     const DecodeParams c = batch_part(p, b0, a->B);
-    if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, ws + kWsHeader, static_cast<cudaStream_t>(stream)) !=
+    if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, false, ws + kWsHeader, static_cast<cudaStream_t>(stream)) !=
         cudaSuccess)
       return VQKV_ERR_CUDA;
   }

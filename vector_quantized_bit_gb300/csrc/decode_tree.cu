@@ -32,10 +32,17 @@
 // relative, as in the other decode kernels) for the fp16 tensor-core product;
 // centroids are fp16 already, sums are fp32.
 //
+// PAIR (at most 64 columns; for the attention weights, whose softmax sums carry
+// fp32 accuracy): q' = hi + lo in two fp16 parts, exact to 2^-22.  The unused half
+// of the MMA rows takes the low parts, 16 columns to a warp: lanes 0..15 the high
+// parts, lanes 16..31 the low parts of the same columns, whose scores one shuffle
+// adds; both lanes then carry the column.  (Not for the plain tree: 64 shuffles
+// more per thread and tile.)
+//
 // Visibility: tokens t < L - M for every column, draft j for the columns
 // whose mask has bit j; only tiles that reach past L - M test it.  Without
 // masks the M queries are causal.  p.stats, where given, receives each column's
-// running max (and sum).
+// max and 1 / sum.
 #include <type_traits>
 
 #include "common.cuh"
@@ -86,7 +93,7 @@ struct Geo {
 
 // One warp of softmax warpgroup wg over a piece's tiles: thread = column.
 // Returns false when a wait gave up.  m, l: the column's running max and sum.
-template <int NQ, int STAGES>
+template <int NQ, int STAGES, bool PAIR>
 __device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Pieces& pc, uint32_t done, int wg, uint32_t t_lane,
                                                  unsigned long long mask, int prefix, uint32_t s_full, uint32_t s_ready,
                                                  uint32_t p_ready, uint32_t o_done, volatile int* abort_flag, float& m,
@@ -101,9 +108,22 @@ __device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Pi
     if (!tr_wait(s_full + 8 * wg, use & 1, abort_flag, p.err)) return false;
     tcgen05_after_sync();
     float x[2][32], top0 = neg_inf(), top1 = neg_inf();
-    tmem_ld32_max(t_s, x[0], top0);
-    tmem_ld32_max(t_s + 32, x[1], top1);
-    tmem_wait_ld();
+    if constexpr (PAIR) {
+      tmem_ld32(t_s, x[0]);
+      tmem_ld32(t_s + 32, x[1]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        x[0][i] += __shfl_xor_sync(0xffffffffu, x[0][i], 16);
+        x[1][i] += __shfl_xor_sync(0xffffffffu, x[1][i], 16);
+        top0 = fmaxf(top0, x[0][i]);
+        top1 = fmaxf(top1, x[1][i]);
+      }
+    } else {
+      tmem_ld32_max(t_s, x[0], top0);
+      tmem_ld32_max(t_s + 32, x[1], top1);
+      tmem_wait_ld();
+    }
     if (NQ == 1) {   // the next score product may overwrite S
       tcgen05_before_sync();
       __syncwarp();
@@ -170,26 +190,34 @@ __device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Pi
 // share of a sequence needs the same rows (19 of them at 8 KV heads): doing it
 // per share took 2.2 us of each CTA at 64 columns and 6.4 us at 256.  It runs
 // while the attention kernel fills its codebooks.
-// grid (groups, Hkv, B), 128 threads.
-__global__ void __launch_bounds__(128) tree_query_kernel(const DecodeParams p, uint4* qx) {
+// PAIR: groups of 16 columns, rows 0..15 the high and 16..31 the low parts.
+// grid (groups, Hkv, B), four threads per column.
+template <bool PAIR>
+__global__ void __launch_bounds__(PAIR ? 64 : 128) tree_query_kernel(const DecodeParams p, uint4* qx) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int kvh = blockIdx.y, b = blockIdx.z, part = threadIdx.x & 3;
-  const int r = threadIdx.x >> 2, c = 32 * blockIdx.x + r;
+  const int r = threadIdx.x >> 2, c = (PAIR ? 16 : 32) * blockIdx.x + r;
   float v[32];
   transform_column(p, b, kvh, c, part, v);
   uint4* dst = qx + ((((size_t)b * p.Hkv + kvh) * gridDim.x + blockIdx.x) * 16 + 4 * part) * 32 + r;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t w[4];
+    uint32_t w[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack_half2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+    for (int i = 0; i < 4; ++i) {
+      const float x = v[8 * j + 2 * i], y = v[8 * j + 2 * i + 1];
+      const __half2 h = __floats2half2_rn(x, y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      lo[i] = pack_half2(x - __low2float(h), y - __high2float(h));
+    }
     dst[32 * j] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (PAIR) dst[32 * j + 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
 // grid (shares, Hkv, column groups of 128 NQ).
-template <int MODE, bool PAGED, int NQ>
+template <int MODE, bool PAGED, int NQ, bool PAIR = false>
 __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const DecodeParams p,
                                                                      const unsigned long long* tree_mask,
                                                                      const uint4* qx) {
@@ -203,7 +231,9 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   const int col0 = NQ * ROWS * (int)blockIdx.z, nloc = min(NQ * ROWS, p.ncols - col0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // warps with columns in each softmax warpgroup (NQ 1: the same 128 columns)
-  const int active0 = (min(nloc, ROWS) + 31) >> 5;
+  static_assert(!PAIR || NQ == 1, "pairs take one query tile");
+  constexpr int WCOLS = PAIR ? 16 : 32;   // columns of a warp
+  const int active0 = (min(nloc, ROWS) + WCOLS - 1) / WCOLS;
   const int active1 = NQ == 1 ? active0 : (max(nloc - ROWS, 0) + 31) >> 5;
   const int jobs = active1 > 0 ? 2 : 1;     // NQ 2: query tiles with columns
   const uint32_t bar = smem_u32(smem + G::BAR_OFF);
@@ -259,13 +289,13 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SM));
     // ---------------- softmax warpgroup wg: thread = column c
     const int wg = warp >> 2, row = threadIdx.x & (ROWS - 1);
-    const int cl = NQ == 1 ? row : wg * ROWS + row, c = col0 + cl;
+    const int cl = PAIR ? 16 * (warp & 3) + (lane & 15) : NQ == 1 ? row : wg * ROWS + row, c = col0 + cl;
     const bool live = (warp & 3) < (wg ? active1 : active0);
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     if (NQ == 1 && live && lane == 0) mbar_arrive(s_ready + 8 * wg);   // no scores to read yet
     for (int piece = 0; pc.next(); ++piece) {
       if (live && (NQ == 2 || wg == 0)) {   // q' into tensor memory: lane = column
-        const uint4* q = qx + ((((size_t)pc.b * p.Hkv + kvh) * ((p.ncols + 31) / 32) + c / 32) * 16) * 32 + lane;
+        const uint4* q = qx + ((((size_t)pc.b * p.Hkv + kvh) * ((p.ncols + WCOLS - 1) / WCOLS) + c / WCOLS) * 16) * 32 + lane;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t r[32];
@@ -291,7 +321,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           mask = tree_mask != nullptr ? tree_mask[(size_t)pc.b * p.M + q] : (2ull << q) - 1;
           if (p.M < 64) mask &= (1ull << p.M) - 1;
         }
-        ok = softmax_tiles_of<NQ, G::STAGES>(p, pc, done, wg, t_lane, mask, prefix, s_full, s_ready, NQ == 1 ? pv_ready : p_ready,
+        ok = softmax_tiles_of<NQ, G::STAGES, PAIR>(p, pc, done, wg, t_lane, mask, prefix, s_full, s_ready, NQ == 1 ? pv_ready : p_ready,
                                   o_done, abort_flag, m, l);
         if (NQ == 1) {   // this warpgroup's last tile of the piece, if it has one
           const int last = pc.n - 1 - (int)((done + pc.n - 1 + wg) & 1);
@@ -327,7 +357,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         // 32 channels at a time, transposed through the warp's own shared memory
         // (the tile rings are idle: every product of the piece is done) so that
         // the stores cover whole lines; 16-byte pieces permuted by the row
-        const int c0 = c - lane;   // the warp's first column
+        const int c0 = c - (lane & (WCOLS - 1));   // the warp's first column
         float* box = reinterpret_cast<float*>(smem + G::K_OFF) + warp * (32 * 32);
         float* part = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + split + pc.b) * p.ncols + c0) * kPartialStride;
 #pragma unroll 1
@@ -356,7 +386,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           if (!whole) {
             float* dst = part + (lane >> 3) * kPartialStride + 32 * q + 4 * x;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < WCOLS / 4; ++i) {
               const int r = 4 * i + (lane >> 3);
               if (c0 - col0 + r < nloc)
                 *reinterpret_cast<float4*>(dst + 4 * i * kPartialStride) =
@@ -364,7 +394,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
             }
           } else {
 #pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < WCOLS / 4; ++i) {
               const int r = 4 * i + (lane >> 3);
               if (c0 - col0 + r < nloc) {
                 const float4 v = *reinterpret_cast<const float4*>(box + r * 32 + ((x ^ (r & 7)) << 2));
@@ -381,11 +411,11 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           }
           __syncwarp();
         }
-        if (cl < nloc && (NQ == 2 || wg == 0)) {
+        if (cl < nloc && lane < WCOLS && (NQ == 2 || wg == 0)) {
           if (!whole)
             *reinterpret_cast<float2*>(part + lane * kPartialStride + 128) = make_float2(m, l);
           else if (p.stats != nullptr)
-            p.stats[((size_t)pc.b * p.Hkv + kvh) * p.ncols + c] = make_float2(m, l);
+            p.stats[((size_t)pc.b * p.Hkv + kvh) * p.ncols + c] = make_float2(m, l > 0.f ? 1.f / l : 0.f);
         }
       }
       done += pc.n;
@@ -582,25 +612,29 @@ __global__ void __launch_bounds__(TC_WARPS * 32) tree_combine_kernel(const Decod
 #pragma unroll
     for (int w = 1; w < TC_WARPS; ++w) add(s_ml[w], s_o[w][lane]);
   }
-  if (p.stats != nullptr && lane == 0) p.stats[((size_t)b * p.Hkv + kvh) * p.ncols + c] = make_float2(M, l);
   const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (p.stats != nullptr && lane == 0) p.stats[((size_t)b * p.Hkv + kvh) * p.ncols + c] = make_float2(M, inv);
   __half* dst = p.out + out_row(p, b, kvh, c) + 4 * lane;   // out needs only 2-byte alignment
   dst[0] = __float2half_rn(O.x * inv), dst[1] = __float2half_rn(O.y * inv);
   dst[2] = __float2half_rn(O.z * inv), dst[3] = __float2half_rn(O.w * inv);
 }
 
 using TreeKernel = void (*)(DecodeParams, const unsigned long long*, const uint4*);
+enum TreeLayout : int { kOneTile = 0, kTwoTiles = 1, kPairs = 2 };   // columns on the MMA rows
 template <int MODE>
-TreeKernel tree_of(bool paged, bool wide) {
-  return wide ? (paged ? (TreeKernel)decode_tree_kernel<MODE, true, 2> : (TreeKernel)decode_tree_kernel<MODE, false, 2>)
-              : (paged ? (TreeKernel)decode_tree_kernel<MODE, true, 1> : (TreeKernel)decode_tree_kernel<MODE, false, 1>);
+TreeKernel tree_of(bool paged, int layout) {
+  if (layout == kPairs)
+    return paged ? (TreeKernel)decode_tree_kernel<MODE, true, 1, true> : (TreeKernel)decode_tree_kernel<MODE, false, 1, true>;
+  if (layout == kTwoTiles)
+    return paged ? (TreeKernel)decode_tree_kernel<MODE, true, 2> : (TreeKernel)decode_tree_kernel<MODE, false, 2>;
+  return paged ? (TreeKernel)decode_tree_kernel<MODE, true, 1> : (TreeKernel)decode_tree_kernel<MODE, false, 1>;
 }
-TreeKernel tree_kernel(int mode, bool paged, bool wide) {
-  return mode == VQKV_MODE_VQ2    ? tree_of<VQKV_MODE_VQ2>(paged, wide)
-         : mode == VQKV_MODE_VQ4  ? tree_of<VQKV_MODE_VQ4>(paged, wide)
-         : mode == VQKV_MODE_VQ3  ? tree_of<VQKV_MODE_VQ3>(paged, wide)
-         : mode == VQKV_MODE_VQ15 ? tree_of<VQKV_MODE_VQ15>(paged, wide)
-                                  : tree_of<VQKV_MODE_VQ125>(paged, wide);
+TreeKernel tree_kernel(int mode, bool paged, int layout) {
+  return mode == VQKV_MODE_VQ2    ? tree_of<VQKV_MODE_VQ2>(paged, layout)
+         : mode == VQKV_MODE_VQ4  ? tree_of<VQKV_MODE_VQ4>(paged, layout)
+         : mode == VQKV_MODE_VQ3  ? tree_of<VQKV_MODE_VQ3>(paged, layout)
+         : mode == VQKV_MODE_VQ15 ? tree_of<VQKV_MODE_VQ15>(paged, layout)
+                                  : tree_of<VQKV_MODE_VQ125>(paged, layout);
 }
 int tree_smem(int mode) {
   return mode == VQKV_MODE_VQ15 || mode == VQKV_MODE_VQ125 ? tr::Geo<VQKV_MODE_VQ15>::SMEM : tr::Geo<VQKV_MODE_VQ2>::SMEM;
@@ -612,21 +646,26 @@ int decode_tree_cols(int ncols) { return ncols > tr::ROWS ? 2 * tr::ROWS : tr::R
 
 cudaError_t decode_tree_prepare(int mode) {
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(tree_kernel(mode, (i & 1) != 0, i >= 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
+  for (int i = 0; i < 6 && e == cudaSuccess; ++i)
+    e = cudaFuncSetAttribute(tree_kernel(mode, (i & 1) != 0, i >> 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              tree_smem(mode));
   return e;
 }
 
-size_t decode_tree_query_bytes(int B, int Hkv, int ncols) { return (size_t)B * Hkv * ((ncols + 31) / 32) * 32 * kHeadDim * 2; }
+size_t decode_tree_query_bytes(int B, int Hkv, int ncols, bool pairs) {
+  const int w = pairs ? 16 : 32;
+  return (size_t)B * Hkv * ((ncols + w - 1) / w) * 32 * kHeadDim * 2;
+}
 
-cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, void* qx,
+cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, bool pairs, void* qx,
                                cudaStream_t stream) {
-  const bool wide = p.ncols > tr::ROWS;
-  cudaError_t e = launch_pdl(tree_query_kernel, dim3((p.ncols + 31) / 32, p.Hkv, p.B), dim3(128), 0, stream, p,
-                             static_cast<uint4*>(qx));
+  const int layout = pairs ? kPairs : p.ncols > tr::ROWS ? kTwoTiles : kOneTile;
+  cudaError_t e = pairs ? launch_pdl(tree_query_kernel<true>, dim3((p.ncols + 15) / 16, p.Hkv, p.B), dim3(64), 0, stream, p,
+                                     static_cast<uint4*>(qx))
+                        : launch_pdl(tree_query_kernel<false>, dim3((p.ncols + 31) / 32, p.Hkv, p.B), dim3(128), 0, stream,
+                                     p, static_cast<uint4*>(qx));
   if (e == cudaSuccess)
-    e = launch_pdl(tree_kernel(mode, p.block_table != nullptr, wide), dim3(p.n_splits, p.Hkv, p.cgroups),
+    e = launch_pdl(tree_kernel(mode, p.block_table != nullptr, layout), dim3(p.n_splits, p.Hkv, p.cgroups),
                    dim3(tr::THREADS), (size_t)tree_smem(mode), stream, p, tree_mask, static_cast<const uint4*>(qx));
   if (e == cudaSuccess && p.n_splits > 1) {
     const int cols = p.Hkv * p.ncols;

@@ -114,17 +114,18 @@ cudaError_t launch_decode_mass(int mode, const DecodeParams& p, dim3 grid, cudaS
 // [Hkv][n_splits + B - 1][ncols], indexed by share + sequence as in the flat plan.
 int decode_tree_cols(int ncols);
 cudaError_t decode_tree_prepare(int mode);
-size_t decode_tree_query_bytes(int B, int Hkv, int ncols);   // scratch qx of a launch (transformed queries)
-cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, void* qx,
+// tree_mask nullptr: causal queries.  pairs: scores of q' in two fp16 parts (at
+// most 64 columns).  qx: scratch for the transformed queries.
+size_t decode_tree_query_bytes(int B, int Hkv, int ncols, bool pairs);
+cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, bool pairs, void* qx,
                                cudaStream_t stream);
 
 // Attention weights of many columns (mass_tiles.cu), after launch_decode_tree has
-// left the columns' running max in p.stats; B <= kFlatMaxB, at most 64 columns.
-// image: transformed queries, sums: the shares' softmax sums.
+// left the columns' max and 1 / sum in p.stats; B <= kFlatMaxB, at most 64
+// columns.  image: scratch for the transformed queries.
 cudaError_t mass_tiles_prepare(int mode);
 size_t mass_tiles_image_bytes(int B, int Hkv, int ncols);
-size_t mass_tiles_sums_bytes(int B, int Hkv, int shares);
-cudaError_t launch_mass_tiles(int mode, const DecodeParams& p, void* image, float* sums, cudaStream_t stream);
+cudaError_t launch_mass_tiles(int mode, const DecodeParams& p, void* image, cudaStream_t stream);
 
 // Cache editing (cache_edit.cu): the in-place move of chosen tokens, and the
 // choice of the tokens a sequence keeps.

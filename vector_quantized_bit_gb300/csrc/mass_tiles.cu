@@ -3,20 +3,19 @@
 //
 // The decode kernels behind vqkv_decode_attn_mass carry 4 columns per CTA and
 // gather every centroid again for each group of 4.  Here one dequantisation
-// serves all (up to 64) columns.  After the draft-tree attention has written O
-// and left a running max m_c per column, two passes over the keys alone follow:
-//   sums     l_c = sum_t exp2(s_tc - m_c)
-//   weights  mass_t += sum_c exp2(s_tc - m_c) / l_c
-// Both recompute the scores S = K' [Q'hi Q'lo]^T (128 tokens x 2 columns x 128
+// serves all (up to 64) columns.  The draft-tree attention (paired q' parts) has
+// written O and left each column's max m_c and 1 / l_c; one pass over the keys
+// alone follows:
+//   mass_t += sum_c exp2(s_tc - m_c) / l_c
+// It recomputes the scores S = K' [Q'hi Q'lo]^T (128 tokens x 2 columns x 128
 // channels) with q' = hi + lo split into two fp16 parts, so that a score is
-// exact to 2^-22 of its terms and the sums carry fp32 accuracy; the single
-// fp16 part of the attention itself would leave 2^-12.  A thread owns a token
-// (tensor-memory lane): the sum over columns is in one thread, in order.  The
-// alternative, storing the scores, would move 512 bytes per token and KV head
-// at 64 columns; a second pass moves its key codes (32 bytes at 2 bit).
+// exact to 2^-22 of its terms and the sums carry fp32 accuracy.  A thread owns a
+// token (tensor-memory lane): the sum over columns is in one thread, in order.
+// The alternative, storing the scores, would move 512 bytes per token and KV
+// head at 64 columns; the second pass moves its key codes (32 bytes at 2 bit).
 //
-// What bounds a pass: shared memory (a K' tile is gathered, stored and read by
-// the tensor cores, 256 bytes a token each) next to 64 exponentials per token.
+// What bounds the pass: shared memory (a K' tile is gathered, stored and read
+// by the tensor cores, 256 bytes a token each) next to the exponentials.
 #include "dequant_tile.cuh"
 
 namespace vqkv {
@@ -36,8 +35,7 @@ constexpr int CB_BYTES = 65536;            // K codebook at the places of the de
 constexpr int K_OFF = CB_BYTES, Q_OFF = K_OFF + STAGES * TILE_SMEM;
 constexpr int Q_BYTES = 2 * MAX_COLS * 256;
 constexpr int COL_OFF = Q_OFF + Q_BYTES;   // per column: m, 1 / l (float2), then the visible length (int)
-constexpr int SUM_OFF = COL_OFF + MAX_COLS * 12;   // [EP_WARPS][MAX_COLS]
-constexpr int BAR_OFF = SUM_OFF + EP_WARPS * MAX_COLS * 4;
+constexpr int BAR_OFF = COL_OFF + MAX_COLS * 12;
 constexpr int PREF_OFF = BAR_OFF + 128;
 constexpr int SMEM = PREF_OFF + (kFlatMaxB + 1) * 4;
 static_assert(SMEM <= 226 * 1024, "shared memory");
@@ -73,12 +71,10 @@ __global__ void __launch_bounds__(128) mass_query_kernel(const DecodeParams p, u
   }
 }
 
-// WEIGHTS false: partial sums l of each (share, sequence) piece to `sums`
-// [Hkv][n_splits + B - 1][64]; true: the weights, added to p.mass.  grid (shares,
-// Hkv); the shares cut all sequences' 128-token tiles.
-template <int MODE, bool PAGED, int NC, bool WEIGHTS>
-__global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeParams p, const unsigned char* image,
-                                                                   float* sums) {
+// The weights of every token, added to p.mass.  grid (shares, Hkv); the shares
+// cut all sequences' 128-token tiles.
+template <int MODE, bool PAGED, int NC>
+__global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeParams p, const unsigned char* image) {
   using namespace mt;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_tmem;
@@ -91,7 +87,6 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
   int* s_pref = reinterpret_cast<int*>(smem + PREF_OFF);
   float2* s_col = reinterpret_cast<float2*>(smem + COL_OFF);
   int* s_lim = reinterpret_cast<int*>(smem + COL_OFF + MAX_COLS * 8);
-  float* s_sum = reinterpret_cast<float*>(smem + SUM_OFF);
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(k_full + 8 * i, 8);
@@ -138,16 +133,8 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
           float2 v = make_float2(__int_as_float(0x7f800000), 0.f);   // columns past the last: exp2(-inf)
           int lim = L;
           if (c < p.ncols) {
-            v.x = p.stats[pair * p.ncols + c].x;
+            v = p.stats[pair * p.ncols + c];
             lim = L - p.M + c / p.g + 1;
-            if (WEIGHTS) {   // the pieces' sums, in order
-              const int T = s_pref[p.B], S = min(p.n_splits, T);
-              const int s0 = flat_cta_of(s_pref[pc.b], T, S), s1 = flat_cta_of(s_pref[pc.b + 1] - 1, T, S);
-              float l = 0.f;
-              for (int i = s0; i <= s1; ++i)
-                l += __ldcg(sums + ((size_t)kvh * (p.n_splits + p.B - 1) + i + pc.b) * MAX_COLS + c);
-              v.y = l > 0.f ? 1.f / l : 0.f;
-            }
           }
           s_col[c] = v;
           s_lim[c] = lim;
@@ -155,15 +142,12 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
       }
       fence_proxy_async_smem();   // q' is read by the tensor cores
       __syncthreads();
-      float acc[WEIGHTS ? 1 : NC];
-#pragma unroll
-      for (int c = 0; c < (WEIGHTS ? 1 : NC); ++c) acc[c] = 0.f;
-      float* mass = WEIGHTS ? p.mass + pair * p.cap_len : nullptr;
+      float* mass = p.mass + pair * p.cap_len;
       bool ok = true;
       for (int t = (int)((done + wg) & 1); t < pc.n; t += 2) {
         const int tok0 = (pc.tile0 + t) * TOK, tok = tok0 + row;
         float old = 0.f;
-        if (WEIGHTS && tok < L) old = mass[tok];
+        if (tok < L) old = mass[tok];
         if (!(ok = tr_wait(d_full + 8 * wg, ((done + t) >> 1) & 1, abort_flag, p.err))) break;
         tcgen05_after_sync();
         const bool tail = tok0 + TOK > L - p.M + 1;   // some token is hidden from some column
@@ -179,34 +163,13 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
             const float2 col = s_col[cc + i];
             float s = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
             if (tail && tok >= s_lim[cc + i]) s = neg_inf();
-            const float e = fast_exp2(s - col.x);
-            if constexpr (WEIGHTS)
-              w = __fmaf_rn(e, col.y, w);
-            else
-              acc[cc + i] += e;
+            w = __fmaf_rn(fast_exp2(s - col.x), col.y, w);
           }
         }
         tcgen05_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(d_empty + 8 * wg);
-        if (WEIGHTS && tok < L) mass[tok] = old + w;
-      }
-      if constexpr (!WEIGHTS) {   // lanes, then warps in order
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          float x = acc[c];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (lane == (c & 31)) s_sum[warp * MAX_COLS + c] = x;
-        }
-        named_barrier_sync(1, EP_WARPS * 32);
-        const int c = threadIdx.x;
-        if (c < p.ncols) {
-          float l = 0.f;
-#pragma unroll
-          for (int i = 0; i < EP_WARPS; ++i) l += s_sum[i * MAX_COLS + c];
-          sums[((size_t)kvh * (p.n_splits + p.B - 1) + split + pc.b) * MAX_COLS + c] = l;
-        }
+        if (tok < L) mass[tok] = old + w;
       }
       done += pc.n;
       __syncthreads();
@@ -266,22 +229,19 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
   if (warp == MMA_WARP) tmem_dealloc(tmem, T_COLS);
 }
 
-using TileKernel = void (*)(DecodeParams, const unsigned char*, float*);
+using TileKernel = void (*)(DecodeParams, const unsigned char*);
 template <int MODE>
-TileKernel tile_of(bool paged, bool wide, bool weights) {
-  if (paged)
-    return wide ? (weights ? (TileKernel)mass_tile_kernel<MODE, true, 64, true> : (TileKernel)mass_tile_kernel<MODE, true, 64, false>)
-                : (weights ? (TileKernel)mass_tile_kernel<MODE, true, 32, true> : (TileKernel)mass_tile_kernel<MODE, true, 32, false>);
-  return wide ? (weights ? (TileKernel)mass_tile_kernel<MODE, false, 64, true> : (TileKernel)mass_tile_kernel<MODE, false, 64, false>)
-              : (weights ? (TileKernel)mass_tile_kernel<MODE, false, 32, true> : (TileKernel)mass_tile_kernel<MODE, false, 32, false>);
+TileKernel tile_of(bool paged, bool wide) {
+  return wide ? (paged ? (TileKernel)mass_tile_kernel<MODE, true, 64> : (TileKernel)mass_tile_kernel<MODE, false, 64>)
+              : (paged ? (TileKernel)mass_tile_kernel<MODE, true, 32> : (TileKernel)mass_tile_kernel<MODE, false, 32>);
 }
-TileKernel tile_kernel(int mode, bool paged, bool wide, bool weights) {
+TileKernel tile_kernel(int mode, bool paged, bool wide) {
   switch (mode) {
-    case VQKV_MODE_VQ2: return tile_of<VQKV_MODE_VQ2>(paged, wide, weights);
-    case VQKV_MODE_VQ4: return tile_of<VQKV_MODE_VQ4>(paged, wide, weights);
-    case VQKV_MODE_VQ3: return tile_of<VQKV_MODE_VQ3>(paged, wide, weights);
-    case VQKV_MODE_VQ15: return tile_of<VQKV_MODE_VQ15>(paged, wide, weights);
-    default: return tile_of<VQKV_MODE_VQ125>(paged, wide, weights);
+    case VQKV_MODE_VQ2: return tile_of<VQKV_MODE_VQ2>(paged, wide);
+    case VQKV_MODE_VQ4: return tile_of<VQKV_MODE_VQ4>(paged, wide);
+    case VQKV_MODE_VQ3: return tile_of<VQKV_MODE_VQ3>(paged, wide);
+    case VQKV_MODE_VQ15: return tile_of<VQKV_MODE_VQ15>(paged, wide);
+    default: return tile_of<VQKV_MODE_VQ125>(paged, wide);
   }
 }
 
@@ -289,26 +249,23 @@ TileKernel tile_kernel(int mode, bool paged, bool wide, bool weights) {
 
 cudaError_t mass_tiles_prepare(int mode) {
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 8 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(tile_kernel(mode, (i & 1) != 0, (i & 2) != 0, (i & 4) != 0),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, mt::SMEM);
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+    e = cudaFuncSetAttribute(tile_kernel(mode, (i & 1) != 0, (i & 2) != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             mt::SMEM);
   return e;
 }
 
-static int tile_cols(int ncols) { return ncols <= 32 ? 32 : 64; }
+size_t mass_tiles_image_bytes(int B, int Hkv, int ncols) { return (size_t)B * Hkv * 2 * (ncols <= 32 ? 32 : 64) * 256; }
 
-size_t mass_tiles_image_bytes(int B, int Hkv, int ncols) { return (size_t)B * Hkv * 2 * tile_cols(ncols) * 256; }
-size_t mass_tiles_sums_bytes(int B, int Hkv, int shares) { return (size_t)Hkv * (shares + B - 1) * mt::MAX_COLS * sizeof(float); }
-
-cudaError_t launch_mass_tiles(int mode, const DecodeParams& p, void* image, float* sums, cudaStream_t stream) {
-  const bool wide = p.ncols > 32, paged = p.block_table != nullptr;
+cudaError_t launch_mass_tiles(int mode, const DecodeParams& p, void* image, cudaStream_t stream) {
+  const bool wide = p.ncols > 32;
   unsigned char* img = static_cast<unsigned char*>(image);
   const dim3 qgrid(wide ? 2 : 1, p.Hkv, p.B);
   cudaError_t e = wide ? launch_pdl(mass_query_kernel<64>, qgrid, dim3(128), 0, stream, p, img)
                        : launch_pdl(mass_query_kernel<32>, qgrid, dim3(128), 0, stream, p, img);
-  for (int weights = 0; weights < 2 && e == cudaSuccess; ++weights)
-    e = launch_pdl(tile_kernel(mode, paged, wide, weights != 0), dim3(p.n_splits, p.Hkv), dim3(mt::THREADS), (size_t)mt::SMEM,
-                   stream, p, (const unsigned char*)img, sums);
+  if (e == cudaSuccess)
+    e = launch_pdl(tile_kernel(mode, p.block_table != nullptr, wide), dim3(p.n_splits, p.Hkv), dim3(mt::THREADS),
+                   (size_t)mt::SMEM, stream, p, (const unsigned char*)img);
   return e;
 }
 
