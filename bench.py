@@ -299,7 +299,8 @@ def replica_throughput(tokens_per_replica, ms_per_step, world):
     return world * tokens_per_replica / (ms_per_step * 1e-3)
 
 
-KERNEL_SOURCES = ("decode.cu", "decode_common.cuh", "encode_common.cuh", "common.cuh", "internal.h")
+KERNEL_SOURCES = ("decode.cu", "decode_kernels.cuh", "gather.cuh", "decode_common.cuh", "encode_common.cuh",
+                  "common.cuh", "internal.h")
 
 
 def kernel_sources_sha256():

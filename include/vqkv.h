@@ -367,8 +367,11 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* args, const vqkv_
  * scheduling.
  *
  * M * (Hq / Hkv) <= 64.  paging as in vqkv_decode_attn_tree (mass is indexed
- * by logical position).  The workspace (vqkv_decode_mass_workspace_bytes) also
- * holds the call's scores, 16 bytes per token and KV head for every 4 columns.
+ * by logical position).  The workspace (vqkv_decode_mass_workspace_bytes) holds,
+ * up to 12 or 16 columns M * (Hq / Hkv), the call's scores too (16 bytes per
+ * token and KV head for every 4 columns).  Like that of vqkv_decode_attn it is
+ * ready for the next call of the same sizes and n_queries; zero it before it
+ * serves others.
  */
 typedef struct {
   vqkv_decode_args decode;    /* q, out: [B][n_queries][Hq][128] */

@@ -15,11 +15,17 @@ from ._lib import (  # noqa: F401
     VQKV_ROLE_V,
     VqkvError,
     decode_args,
+    decode_mass_workspace,
+    decode_tree_workspace,
     decode_workspace,
     encode_args,
+    vqkv_cache_compact,
     vqkv_code_bytes,
     vqkv_decode_attn,
+    vqkv_decode_attn_mass,
+    vqkv_decode_attn_tree,
     vqkv_decode_num_splits,
     vqkv_decode_workspace_bytes,
     vqkv_encode,
+    vqkv_evict_select,
 )

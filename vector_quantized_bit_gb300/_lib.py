@@ -535,6 +535,7 @@ def vqkv_evict_select(mass, seq_lens, keep, keep_lens, n_sink=0, n_recent=0, max
     [B][Hkv][n_keep] (ascending; only the first keep_lens[b] entries of a row)
     and keep_lens int32 [B].  Always kept: the first n_sink and the last
     n_recent tokens; then those of the largest mass, ties to the lowest position.
+    error_flags: int32 [1], optional (VQKV_DEVERR_* bits are or-ed in).
     """
     import torch
     what = "vqkv_evict_select"
@@ -558,7 +559,7 @@ def vqkv_cache_compact(mode, k_codes, v_codes, seq_lens, src, counts, cap_len, s
     seq_lens[b]; counts int32 [B] entries used; start int32 [B] or None (0).
     k_codes / v_codes uint8 [B][Hkv][bytes], or pools with block_table.  mass
     (fp32 [B][Hkv][cap_len], optional) moves along and is cleared behind the
-    last moved token.
+    last moved token.  error_flags: int32 [1], optional.
     """
     import torch
     what = "vqkv_cache_compact"

@@ -66,6 +66,7 @@ constexpr int THREADS = (MMA_WARP + 4) * 32;   // whole warpgroups, for the regi
 // dequantising ones (32 hold gathered centroids), 40 for the last:
 // 256 x 120 + 512 x 56 + 128 x 40 = 64,512 = 896 x 72.
 constexpr int REGS_SM = 120, REGS_DQ = 56, REGS_MMA = 40;
+constexpr int SPLIT_REGS = 32 * (SM_WARPS * REGS_SM + DQ_WARPS * REGS_DQ + 4 * REGS_MMA);
 constexpr int TILE_SMEM = TOK * 256;      // one dequantised K or V tile: two 64-channel halves of 64 x 128 bytes
 constexpr int HALF = TOK * 128;
 // tensor memory columns: O, S and P of each softmax warpgroup, then q'
@@ -647,8 +648,7 @@ int decode_tree_cols(int ncols) { return ncols > tr::ROWS ? 2 * tr::ROWS : tr::R
 cudaError_t decode_tree_prepare(int mode) {
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < 6 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(tree_kernel(mode, (i & 1) != 0, i >> 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             tree_smem(mode));
+    e = prepare_split_kernel(tree_kernel(mode, (i & 1) != 0, i >> 1), tr::THREADS, tr::SPLIT_REGS, tree_smem(mode));
   return e;
 }
 

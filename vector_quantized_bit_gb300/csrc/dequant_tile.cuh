@@ -17,6 +17,18 @@ namespace {
 
 constexpr uint32_t kMaxPolls = 1u << 20;
 
+// Shared memory of a kernel that splits its registers between warpgroups
+// (setmaxnreg), after checking that the launch's registers cover the split: one
+// that does not would wait forever.
+template <typename K>
+cudaError_t prepare_split_kernel(K kernel, int threads, int registers_of_split, int smem) {
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+  if (e != cudaSuccess) return e;
+  if (a.numRegs * threads < registers_of_split) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
 template <int MODE>
 struct CodeGeo {
   static constexpr int LAYOUT_TOK = MODE == VQKV_MODE_VQ15 ? 64 : 16;

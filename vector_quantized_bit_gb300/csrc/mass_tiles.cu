@@ -28,6 +28,7 @@ constexpr int MMA_WARP = EP_WARPS + DQ_WARPS;
 constexpr int THREADS = (MMA_WARP + 4) * 32;
 // As in the draft-tree attention: 256 x 120 + 512 x 56 + 128 x 40 = 896 x 72.
 constexpr int REGS_EP = 120, REGS_DQ = 56, REGS_MMA = 40;
+constexpr int SPLIT_REGS = 32 * (EP_WARPS * REGS_EP + DQ_WARPS * REGS_DQ + 4 * REGS_MMA);
 constexpr int STAGES = 3;
 constexpr int TILE_SMEM = TOK * 256, HALF = TOK * 128;
 constexpr int MAX_COLS = 64;
@@ -250,8 +251,7 @@ TileKernel tile_kernel(int mode, bool paged, bool wide) {
 cudaError_t mass_tiles_prepare(int mode) {
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(tile_kernel(mode, (i & 1) != 0, (i & 2) != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             mt::SMEM);
+    e = prepare_split_kernel(tile_kernel(mode, (i & 1) != 0, (i & 2) != 0), mt::THREADS, mt::SPLIT_REGS, mt::SMEM);
   return e;
 }
 
