@@ -77,6 +77,20 @@ def test_select_against_sort(B, Hkv, cap, lens, n_keep, n_sink, n_recent):
     check_select(mass, lens, n_keep, n_sink, n_recent)
 
 
+@pytest.mark.parametrize("B,Hkv,cap,n_keep", [(1, 1, 21000, 7777), (40, 4, 9000, 100), (78, 1, 9001, 8990)])
+def test_select_long_rows_of_few_values(B, Hkv, cap, n_keep):
+    """More keys in the deciding bin than a warp lists; few rows (a cluster each) and many (one CTA each)."""
+    r = np.random.default_rng(cap)
+    mass = np.where(r.random((B, Hkv, cap)) < 0.97, 0.25, r.random((B, Hkv, cap))).astype(np.float32)
+    check_select(mass, [cap - (b % 7) for b in range(B)], n_keep, 3, 5)
+
+
+def test_select_many_rows_of_random_weights():
+    r = np.random.default_rng(8)
+    mass = np.exp(2 * r.standard_normal((60, 3, 6001))).astype(np.float32)
+    check_select(mass, r.integers(0, 6002, size=60), 1500, 4, 64)
+
+
 @pytest.mark.parametrize("n_keep", [1, 31, 32, 500, 1023])
 def test_select_ties_take_the_lowest_position(n_keep):
     r = np.random.default_rng(n_keep)
@@ -261,6 +275,63 @@ def test_compact_repeated_and_unordered_sources(mode):
     L, n = 3000, 1200
     src = r.integers(np.arange(n), L, size=(1, 2, n)).astype(np.int32)   # any source at or after its place
     assert run_compact(mode, 1, 2, L, [L], src, [n], None, seed=7) == 0
+
+
+def test_compact_twice_in_a_graph_and_on_another_stream():
+    """Two calls back to back, the second on what the first left, directly on a side stream and replayed twice."""
+    t = H.torch()
+    r = np.random.default_rng(11)
+    B, Hkv, cap, n1, n2 = 2, 2, 5008, 3500, 1700
+    lens = [5001, 3777]
+    toks = [r.integers(0, 256, size=(B, Hkv, cap, 32)) for _ in range(2)]
+    packed = [np.stack([np.stack([vo.pack_stream_fast(toks[role][b, h], 0, role, cap) for h in range(Hkv)])
+                        for b in range(B)]) for role in (0, 1)]
+    mass = r.random((B, Hkv, cap), dtype=np.float32)
+    src1, c1 = kept(r, B, Hkv, lens, n1)
+    src2, c2 = kept(r, B, Hkv, c1, n2)
+    full = [H.dev(x) for x in packed] + [H.dev(mass)]
+    k, v, dm = [x.clone() for x in full]
+    ints = [H.dev(np.asarray(x, dtype=np.int32)) for x in (lens, src1, c1, src2, c2)]
+    err = t.zeros(1, dtype=t.int32, device="cuda")
+
+    def restore():
+        for x, y in zip((k, v, dm), full):
+            x.copy_(y)
+
+    def both():
+        _lib.vqkv_cache_compact(0, k, v, ints[0], ints[1], ints[2], cap, mass=dm, error_flags=err)
+        _lib.vqkv_cache_compact(0, k, v, ints[2], ints[3], ints[4], cap, mass=dm, error_flags=err)
+
+    want, wmass = [x.copy() for x in packed], mass.copy()
+    for b in range(B):
+        for h in range(Hkv):
+            for role in (0, 1):
+                new = ref_move(toks[role][b, h], lens[b], 0, c1[b], src1[b, h])
+                want[role][b, h] = vo.pack_stream_fast(ref_move(new, c1[b], 0, c2[b], src2[b, h]), 0, role, cap)
+            m1 = ref_move(mass[b, h][:, None], lens[b], 0, c1[b], src1[b, h])[:, 0]
+            m1[c1[b]:lens[b]] = 0.0
+            m2 = ref_move(m1[:, None], c1[b], 0, c2[b], src2[b, h])[:, 0]
+            m2[c2[b]:c1[b]] = 0.0
+            wmass[b, h] = m2
+
+    def check():
+        assert np.array_equal(k.cpu().numpy(), want[0]) and np.array_equal(v.cpu().numpy(), want[1])
+        assert np.array_equal(dm.cpu().numpy(), wmass) and int(err.item()) == 0
+
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        both()
+    side.synchronize()
+    check()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        both()
+    for _ in range(2):
+        restore()
+        g.replay()
+        t.cuda.synchronize()
+        check()
 
 
 @pytest.mark.parametrize("mode", [0, 1, 2, 3, 4])

@@ -95,8 +95,9 @@ def test_mass_many_columns_ragged_batch(mode, Hq, Hkv, M, num_splits, page):
     assert err == 0
 
 
-def test_mass_more_sequences_than_one_launch_takes():
-    B, M = 1027, 9
+@pytest.mark.parametrize("M", [1, 9])   # few columns; many, in launches of at most 1024 sequences
+def test_mass_more_sequences_than_one_launch_takes(M):
+    B = 1027
     r = np.random.default_rng(3)
     lens = r.integers(0, 40, size=B)
     s, kcb, vcb = H.random_codebooks(0, 1, 4)
