@@ -20,6 +20,9 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
+__device__ __forceinline__ void cluster_add(uint32_t a, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_ld(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -372,43 +375,63 @@ __global__ void __launch_bounds__(CP_THREADS, 2) compact_kernel(const CompactPar
 
 // ------------------------------------------------------------------ selection
 //
-// The K largest of a row of n fp32 weights, in position order.  A cluster
-// owns one (sequence, KV head) row, each CTA a contiguous part of it (kept in
-// shared memory as order-preserving 32-bit keys while it fits).  Radix select
-// from the top: three passes over 11, 11 and 10 key bits find the K-th
-// largest key; per pass the CTAs' 2048-bin counts are added through
-// distributed shared memory.  Then the kept positions are counted per warp
-// and CTA, and written by ballot ranks: larger keys all, keys equal to the
-// K-th while some are still needed, lowest position first.
+// The K largest of a row of n fp32 weights, in position order.  A row belongs
+// to one CTA or to a cluster, each CTA a contiguous part of it, each warp a
+// contiguous piece of that.  Radix select on order-preserving 32-bit keys:
+//   1. counts of the top 12 bits, added over the cluster through distributed
+//      shared memory, give the bin of the K-th largest key;
+//   2. each warp counts the keys above that bin and lists those inside it
+//      (about 1 %: a bin is an eighth of an octave) in its own segment;
+//   3. two more digits of 10 bits over the listed keys alone.  Every CTA of a
+//      cluster reads all segments, so these steps exchange nothing;
+//   4. the pieces are read again and the kept positions written by ballot
+//      ranks: larger keys all, keys equal to the K-th while some are still
+//      needed, lowest position first.
+// A segment that overflows (long rows of many equal weights) sends the row
+// through the digits over all its keys instead.  Steps 2 and 4 compare the
+// weights as they are with the bounds' weights where 128 tokens hold nothing
+// special, and come to the keys only elsewhere.
 //
-// Bound: instruction issue and, in the first pass, shared-memory atomics on
-// equal bins (weights share their leading bits).  So lanes take four
-// neighbouring keys at a time, and four copies of the counts, one per lane % 4,
-// keep equal bins of a warp apart.
+// Few rows: 1024 threads per CTA, one CTA per SM, the part's weights kept in
+// shared memory.  More CTAs than SMs: 512 threads, two CTAs per SM, the weights
+// read again from L2, which overlaps the steps of two rows (256 rows of 16,384
+// to 32,768 tokens: 30.8 us, 32.6 with 1024 threads; 512 rows of 8,192: 22 and
+// 30).  Bound there: a row takes 38,000 cycles beside another one, 10,000 of them
+// in step 1 (memory bandwidth), 9,000 each in steps 2 and 4 (issue), the rest
+// the digits' scans and barriers.  8 rows of 196,608 in clusters of 8: 20 us, of
+// which the exchange of step 1 and the remote reads of step 3 take 7.
 
-constexpr int SEL_THREADS = 1024;
-constexpr int SEL_WARPS = SEL_THREADS / 32;
-constexpr int SEL_U = 2;           // 16-byte loads in flight per thread in the first pass
-constexpr int SEL_BINS = 2048;
-constexpr int SEL_COPIES = 4;
+constexpr int SEL_TOP = 12;        // bits of the first digit; the others have 10
+constexpr int SEL_BINS = 1 << SEL_TOP;
+constexpr int SEL_LIST = 8192;     // listed keys of a CTA, in one segment per warp
 constexpr int SEL_MAX_CLUSTER = 8;
-constexpr int SEL_CACHE = 40960;   // keys of a CTA's part kept in shared memory (160 KB)
+constexpr int SEL_CACHE = 36864;   // weights of a CTA's part kept in shared memory (144 KB)
 
 // Larger weight <=> larger key; NaN below everything, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float x) {
-  if (x != x) return 0u;
   const uint32_t u = __float_as_uint(x + 0.f);   // -0 + 0 = +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return x != x ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+// The weight of a key from -FLT_MAX's up (keys above +inf's give a NaN, which no weight reaches).
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+constexpr uint32_t SEL_KEY_FINITE = 0x00800000u;   // key of -FLT_MAX
 
-__global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const SelectParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const SelectParams p) {
+  constexpr int WARPS = THREADS / 32, PER = SEL_BINS / THREADS, SEG = SEL_LIST / WARPS;   // PER: bins per thread
+  constexpr int U = THREADS == 512 ? 4 : 2;   // 16-byte loads in flight per thread
   extern __shared__ uint4 s_dyn[];
-  uint32_t* s_hist = reinterpret_cast<uint32_t*>(s_dyn);             // [SEL_COPIES][SEL_BINS]
-  uint32_t* s_total = s_hist + SEL_COPIES * SEL_BINS;                // [SEL_BINS]
-  uint4* s_keys = reinterpret_cast<uint4*>(s_total + SEL_BINS);      // [p.cache_keys / 4]
-  __shared__ uint32_t s_warp[SEL_WARPS], s_warp2[SEL_WARPS];
+  uint32_t* s_hist = reinterpret_cast<uint32_t*>(s_dyn);             // [SEL_BINS]
+  uint32_t* s_total = s_hist + SEL_BINS;                             // [SEL_BINS]
+  uint32_t* s_list = s_total + SEL_BINS;                             // [WARPS][SEG]
+  float4* s_x = reinterpret_cast<float4*>(s_list + SEL_LIST);        // [p.cache_keys / 4]
+  __shared__ uint32_t s_warp[WARPS], s_warp2[WARPS];
   __shared__ uint32_t s_digit, s_above;
-  __shared__ uint32_t s_cta[2 * SEL_MAX_CLUSTER];   // per CTA: larger, equal
+  __shared__ uint32_t s_listed[WARPS];                // this CTA's segments
+  __shared__ uint32_t s_all[SEL_MAX_CLUSTER * WARPS];   // all CTAs'
+  __shared__ uint32_t s_cta[2 * SEL_MAX_CLUSTER];       // per CTA: larger, equal
   const int CL = gridDim.x, rank = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dependency_wait();
@@ -420,101 +443,63 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Sele
   }
   int32_t* keep = p.keep + ((size_t)b * p.Hkv + kvh) * p.n_keep;
   if (L <= p.n_keep) {   // everything stays
-    for (int t = rank * SEL_THREADS + (int)threadIdx.x; t < L; t += CL * SEL_THREADS) keep[t] = t;
+    for (int t = rank * THREADS + (int)threadIdx.x; t < L; t += CL * THREADS) keep[t] = t;
     return;
   }
-  // parts of SEL_WARPS pieces of whole 128-token strides: a warp walks a
+  // parts of WARPS pieces of whole 128-token strides: a warp walks a
   // contiguous piece, four tokens per lane
-  const int piece = ((L + CL * SEL_WARPS - 1) / (CL * SEL_WARPS) + 127) & ~127;
-  const int c0 = min(rank * SEL_WARPS * piece, L), c1 = min(c0 + SEL_WARPS * piece, L);
+  const int piece = ((L + CL * WARPS - 1) / (CL * WARPS) + 127) & ~127;
+  const int c0 = min(rank * WARPS * piece, L), c1 = min(c0 + WARPS * piece, L);
   const float* mass = p.mass + ((size_t)b * p.Hkv + kvh) * p.cap_len;
-  const bool cached = SEL_WARPS * piece <= p.cache_keys;
+  const bool cached = WARPS * piece <= p.cache_keys;
   const bool aligned16 = (reinterpret_cast<uintptr_t>(mass) & 15) == 0;
-  // the keys of tokens t .. t + 3 (t a multiple of 4), 0 past the part's end;
-  // protected tokens rank above +inf
-  auto load_keys = [&](int t) -> uint4 {
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (aligned16 && t + 3 < c1) {
-      const float4 v = *reinterpret_cast<const float4*>(mass + t);
-      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t + i < c1) x[i] = mass[t + i];
-    }
-    uint32_t k[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      k[i] = t + i < p.n_sink || t + i >= L - p.n_recent ? 0xffffffffu : weight_key(x[i]);
-      if (t + i >= c1) k[i] = 0u;
-    }
-    return make_uint4(k[0], k[1], k[2], k[3]);
+  // weights of tokens t .. t + 3 (t a multiple of 4), 0 past the part's end
+  auto load4 = [&](int t) -> float4 {
+    if (aligned16 && t + 3 < c1) return *reinterpret_cast<const float4*>(mass + t);
+    return make_float4(t < c1 ? mass[t] : 0.f, t + 1 < c1 ? mass[t + 1] : 0.f, t + 2 < c1 ? mass[t + 2] : 0.f,
+                       t + 3 < c1 ? mass[t + 3] : 0.f);
   };
-  auto keys_at = [&](int t) -> uint4 { return cached ? s_keys[(t - c0) >> 2] : load_keys(t); };
+  auto x4_at = [&](int t) -> float4 { return cached ? s_x[(t - c0) >> 2] : load4(t); };
+  // protected tokens rank above +inf
+  const int tail = L - p.n_recent;
+  auto key_of = [&](float x, int t) -> uint32_t { return t < p.n_sink || t >= tail ? 0xffffffffu : weight_key(x); };
+  // 128 tokens from t on of which none is protected or past the part's end
+  auto inner = [&](int t) { return t >= p.n_sink && t + 128 <= min(tail, c1); };
 
   uint32_t prefix = 0;                 // key bits found so far
   uint32_t need = (uint32_t)p.n_keep;  // tokens still to take among keys with that prefix
-  uint32_t* hist = s_hist + (lane % SEL_COPIES) * SEL_BINS;
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int bits = pass == 2 ? 10 : 11;
-    for (int i = threadIdx.x; i < SEL_COPIES * SEL_BINS; i += SEL_THREADS) s_hist[i] = 0u;
-    __syncthreads();
-    const uint32_t mask = (1u << bits) - 1u;
-    if (pass == 0) {
-      for (int t0 = c0 + 4 * (int)threadIdx.x; t0 < c1; t0 += 4 * SEL_U * SEL_THREADS) {
-        uint4 k[SEL_U];
+  auto clear_bins = [&] {
 #pragma unroll
-        for (int i = 0; i < SEL_U; ++i) {
-          const int t = t0 + 4 * i * SEL_THREADS;
-          if (t < c1) k[i] = load_keys(t);
-        }
-#pragma unroll
-        for (int i = 0; i < SEL_U; ++i) {
-          const int t = t0 + 4 * i * SEL_THREADS;
-          if (t >= c1) break;
-          if (cached) s_keys[(t - c0) >> 2] = k[i];
-          atomicAdd(&hist[k[i].x >> 21], 1u);
-          if (t + 1 < c1) atomicAdd(&hist[k[i].y >> 21], 1u);
-          if (t + 2 < c1) atomicAdd(&hist[k[i].z >> 21], 1u);
-          if (t + 3 < c1) atomicAdd(&hist[k[i].w >> 21], 1u);
-        }
-      }
-    } else {
-      // (keys past the part's end are 0: with prefix 0 they would count, so the
-      // bound is tested there)
-      auto count = [&](uint32_t k, int t) {
-        if ((k >> (shift + bits)) == prefix && t < c1) atomicAdd(&hist[(k >> shift) & mask], 1u);
-      };
-      for (int t = c0 + 4 * (int)threadIdx.x; t < c1; t += 4 * SEL_THREADS) {
-        const uint4 k = keys_at(t);
-        count(k.x, t), count(k.y, t + 1), count(k.z, t + 2), count(k.w, t + 3);
-      }
+    for (int i = 0; i < PER; i += 4) {
+      *reinterpret_cast<uint4*>(&s_hist[PER * threadIdx.x + i]) = make_uint4(0u, 0u, 0u, 0u);
+      if (CL > 1) *reinterpret_cast<uint4*>(&s_total[PER * threadIdx.x + i]) = make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
-    // fold the copies: bins from the top, thread i holds 2047 - 2i and 2046 - 2i
-    const int hi = SEL_BINS - 1 - 2 * (int)threadIdx.x;
-    uint32_t x0 = 0, x1 = 0;
+  };
+  // The digit of the K-th largest key from the counts in s_hist (summed over the
+  // cluster first, if `exchange`).
+  auto next_digit = [&](int bits, bool exchange) {
+    __syncthreads();
+    // bins from the top: thread i holds PER of them from SEL_BINS - 1 - PER i down
+    const int hi = SEL_BINS - 1 - PER * (int)threadIdx.x;
+    if (exchange) {   // every CTA adds its counts (few bins have any) to every CTA's sums
+      cluster_sync();   // all sums are cleared
 #pragma unroll
-    for (int c = 0; c < SEL_COPIES; ++c) {
-      const uint2 v = *reinterpret_cast<const uint2*>(&s_hist[c * SEL_BINS + hi - 1]);
-      x0 += v.y, x1 += v.x;
-    }
-    if (CL > 1) {   // this CTA adds a share of the bins over the cluster and gives every CTA the sums
-      *reinterpret_cast<uint2*>(&s_hist[hi - 1]) = make_uint2(x1, x0);   // own bins of copy 0 only
-      cluster_sync();
-      const int share = SEL_BINS / CL;
-      if ((int)threadIdx.x < share) {
-        const int bin = rank * share + threadIdx.x;
-        const uint32_t h = smem_u32(&s_hist[bin]), o = smem_u32(&s_total[bin]);
-        uint32_t sum = 0;
-        for (int r = 0; r < CL; ++r) sum += cluster_ld(cluster_addr(h, r));
-        for (int r = 0; r < CL; ++r) cluster_st(cluster_addr(o, r), sum);
+      for (int i = 0; i < PER; ++i) {
+        const uint32_t n = s_hist[threadIdx.x + i * THREADS];
+        if (n != 0)
+          for (int r = 0; r < CL; ++r) cluster_add(cluster_addr(smem_u32(&s_total[threadIdx.x + i * THREADS]), r), n);
       }
       cluster_sync();
-      x0 = s_total[hi], x1 = s_total[hi - 1];
     }
-    uint32_t inc = x0 + x1;
+    uint32_t down[PER], own = 0;
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(&(exchange ? s_total : s_hist)[hi - 3 - i]);
+      down[i] = x.w, down[i + 1] = x.z, down[i + 2] = x.y, down[i + 3] = x.x;
+      own += x.x + x.y + x.z + x.w;
+    }
+    uint32_t inc = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -522,32 +507,169 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Sele
     }
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    // tokens in the bins of the warps before this one (SEL_WARPS == 32)
-    const uint32_t prior = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
-    const uint32_t before = inc - x0 - x1 + prior;   // tokens in higher bins
-    if (before < need && need <= before + x0) {
-      s_digit = hi, s_above = before;
-    } else if (before + x0 < need && need <= before + x0 + x1) {
-      s_digit = hi - 1, s_above = before + x0;
+    // tokens in the bins of the warps before this one
+    uint32_t before = inc - own + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
+    if (before < need && need <= before + own) {   // this thread's bins hold the digit
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (before < need && need <= before + down[i]) s_digit = hi - i, s_above = before;
+        before += down[i];
+      }
     }
     __syncthreads();
     prefix = (prefix << bits) | s_digit;
     need -= s_above;
+  };
+
+  const int w0 = min(c0 + warp * piece, c1), w1 = min(w0 + piece, c1);   // this warp's tokens
+  clear_bins();
+  for (int t0 = w0; t0 < w1; t0 += 128 * U) {
+    float4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t0 + 128 * u < w1) x[u] = load4(t0 + 128 * u + 4 * lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + 128 * u + 4 * lane;
+      if (t0 + 128 * u >= w1) break;
+      if (cached) s_x[(t - c0) >> 2] = x[u];
+      const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      if (inner(t0 + 128 * u)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) atomicAdd(&s_hist[weight_key(v[i]) >> (32 - SEL_TOP)], 1u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t + i < w1) atomicAdd(&s_hist[key_of(v[i], t + i) >> (32 - SEL_TOP)], 1u);
+      }
+    }
+  }
+  next_digit(SEL_TOP, CL > 1);
+
+  const float* row = cached ? reinterpret_cast<const float*>(s_x) - c0 : mass;
+  // Keys above the bin are counted, those inside listed.  Where no token is
+  // special the weights are compared with the bin's bounds as they are.
+  const uint32_t lt = (1u << lane) - 1u;
+  uint32_t* seg = s_list + warp * SEG;
+  uint32_t larger = 0, equal = 0, listed = 0;
+  {
+    const float lo = key_weight(prefix << (32 - SEL_TOP)), hi = key_weight((prefix + 1) << (32 - SEL_TOP));
+    const bool finite = (prefix << (32 - SEL_TOP)) >= SEL_KEY_FINITE && prefix < SEL_BINS - 1;
+    for (int t0 = w0; t0 < w1; t0 += 128 * U) {
+      float4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (t0 + 128 * u < w1) x[u] = x4_at(t0 + 128 * u + 4 * lane);
+      uint32_t in = 0;   // bit 4 u + i: token t0 + 128 u + 4 lane + i is listed
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t0 + 128 * u >= w1) break;
+        const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        if (finite && inner(t0 + 128 * u)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            larger += v[i] >= hi;
+            in |= (uint32_t)(v[i] >= lo && !(v[i] >= hi)) << (4 * u + i);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 128 * u + 4 * lane + i;
+            const uint32_t bin = key_of(v[i], t) >> (32 - SEL_TOP);
+            larger += t < w1 && bin > prefix;
+            in |= (uint32_t)(t < w1 && bin == prefix) << (4 * u + i);
+          }
+        }
+      }
+      // one listed key of each lane per turn
+      for (uint32_t who; (who = __ballot_sync(0xffffffffu, in != 0)) != 0; in &= in - 1) {
+        const uint32_t at = listed + __popc(who & lt);
+        if (in != 0 && at < SEG) {
+          const int i = __ffs(in) - 1, t = t0 + 128 * (i >> 2) + 4 * lane + (i & 3);
+          seg[at] = key_of(row[t], t);
+        }
+        listed += __popc(who);
+      }
+    }
+  }
+  if (lane == 0) s_listed[warp] = listed;
+  if (CL > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  uint32_t n = 0;
+  if ((int)threadIdx.x < CL * WARPS) {
+    n = CL == 1 ? s_listed[lane % WARPS]
+                : cluster_ld(cluster_addr(smem_u32(&s_listed[lane % WARPS]), threadIdx.x / WARPS));
+    s_all[threadIdx.x] = n;
+  }
+  if (__syncthreads_or(n > SEG) == 0) {
+    for (int pass = 1; pass < 3; ++pass) {
+      clear_bins();
+      auto count = [&](uint32_t k) {
+        if (pass == 1)
+          atomicAdd(&s_hist[(k >> 10) & 1023u], 1u);
+        else if ((k >> 10) == prefix)
+          atomicAdd(&s_hist[k & 1023u], 1u);
+      };
+      if (CL == 1) {
+        for (uint32_t i = lane; i < listed; i += 32) count(seg[i]);
+      } else {   // a warp reads the segments of its number in every CTA, all CTAs' loads in flight
+        const uint32_t most = __reduce_max_sync(0xffffffffu, lane < CL ? s_all[lane * WARPS + warp] : 0u);
+        for (uint32_t i = lane; i < ((most + 31) & ~31u); i += 32) {
+          uint32_t k[SEL_MAX_CLUSTER];
+          uint32_t have = 0;
+#pragma unroll
+          for (int r = 0; r < SEL_MAX_CLUSTER; ++r)
+            if (r < CL && i < s_all[r * WARPS + warp]) {
+              k[r] = cluster_ld(cluster_addr(smem_u32(seg + i), r));
+              have |= 1u << r;
+            }
+#pragma unroll
+          for (int r = 0; r < SEL_MAX_CLUSTER; ++r)
+            if ((have >> r) & 1u) count(k[r]);
+        }
+      }
+      next_digit(10, false);
+    }
+    for (uint32_t i = lane; i < listed; i += 32) {
+      larger += (seg[i] > prefix);
+      equal += (seg[i] == prefix);
+    }
+  } else {
+    for (int pass = 1; pass < 3; ++pass) {
+      const int shift = pass == 1 ? 10 : 0;
+      clear_bins();
+      for (int t = c0 + 4 * (int)threadIdx.x; t < c1; t += 4 * THREADS) {
+        const float4 x = x4_at(t);
+        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t k = key_of(v[i], t + i);
+          if (t + i < c1 && (k >> (shift + 10)) == prefix) atomicAdd(&s_hist[(k >> shift) & 1023u], 1u);
+        }
+      }
+      next_digit(10, CL > 1);
+    }
+    larger = 0;
+    for (int t = w0 + 4 * lane; t < w1; t += 128) {
+      const float4 x = x4_at(t);
+      const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t k = key_of(v[i], t + i);
+        larger += t + i < w1 && k > prefix;
+        equal += t + i < w1 && k == prefix;
+      }
+    }
   }
   // prefix is the K-th largest key; `need` of the keys equal to it are kept
-  const int w0 = min(c0 + warp * piece, c1), w1 = min(w0 + piece, c1);
-  uint32_t larger = 0, equal = 0;
-  for (int t = w0 + 4 * lane; t < w1; t += 128) {
-    const uint4 k = keys_at(t);
-    larger += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);   // 0 past the end: never larger
-    equal += (k.x == prefix) + (k.y == prefix && t + 1 < c1) + (k.z == prefix && t + 2 < c1) + (k.w == prefix && t + 3 < c1);
-  }
   larger = __reduce_add_sync(0xffffffffu, larger);
   equal = __reduce_add_sync(0xffffffffu, equal);
   __syncthreads();
   if (lane == 0) s_warp[warp] = larger, s_warp2[warp] = equal;
   __syncthreads();
-  uint32_t cl = s_warp[lane], ce = s_warp2[lane];
+  uint32_t cl = lane < WARPS ? s_warp[lane] : 0u, ce = lane < WARPS ? s_warp2[lane] : 0u;
   uint32_t gl = __reduce_add_sync(0xffffffffu, lane < warp ? cl : 0u);
   uint32_t ge = __reduce_add_sync(0xffffffffu, lane < warp ? ce : 0u);
   if (CL > 1) {
@@ -561,42 +683,41 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Sele
     for (int r = 0; r < rank; ++r) gl += s_cta[2 * r], ge += s_cta[2 * r + 1];
   }
   uint32_t at = gl + min(ge, need), seen = ge;   // kept / equal tokens before this warp's piece
-  const uint32_t lt = (1u << lane) - 1u;
+  const float limit = key_weight(prefix);
+  const bool plain = equal == 0 && prefix >= SEL_KEY_FINITE;   // nothing of this piece ties with the K-th key
+  float ahead[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ahead[i] = w0 + 32 * i + lane < w1 ? row[w0 + 32 * i + lane] : 0.f;
   for (int t0 = w0; t0 < w1; t0 += 128) {
-    const int t = t0 + 4 * lane;
-    const uint4 kk = t < w1 ? keys_at(t) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t k[4] = {kk.x, kk.y, kk.z, kk.w};
-    uint32_t kept = 0, eq = 0;   // bit i: token t + i
+    float x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      kept |= (uint32_t)(k[i] > prefix) << i;
-      eq |= (uint32_t)(k[i] == prefix && t + i < w1) << i;
+      const int t = t0 + 128 + 32 * i + lane;
+      x[i] = ahead[i];
+      if (t < w1) ahead[i] = row[t];
     }
-    if (__any_sync(0xffffffffu, eq != 0)) {
-      const uint32_t n = __popc(eq);
-      uint32_t rank_eq = seen;   // equal tokens before this lane's
+    if (plain && inner(t0)) {
+      uint32_t all[4];
 #pragma unroll
-      for (int q = 0; q < 3; ++q) rank_eq += __popc(__ballot_sync(0xffffffffu, (n >> q) & 1u) & lt) << q;
+      for (int i = 0; i < 4; ++i) all[i] = __ballot_sync(0xffffffffu, x[i] > limit);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((eq >> i) & 1u) {
-          if (rank_eq < need) kept |= 1u << i;
-          ++rank_eq;
-        }
-      seen += __reduce_add_sync(0xffffffffu, n);
+      for (int i = 0; i < 4; ++i) {
+        if (x[i] > limit) keep[at + __popc(all[i] & lt)] = t0 + 32 * i + lane;
+        at += __popc(all[i]);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int t = t0 + 32 * i + lane;
+        const uint32_t k = key_of(i == 0 ? x[0] : i == 1 ? x[1] : i == 2 ? x[2] : x[3], t);
+        const uint32_t eq = __ballot_sync(0xffffffffu, k == prefix && t < w1);
+        const bool kept = (k > prefix && t < w1) || (((eq >> lane) & 1u) && seen + __popc(eq & lt) < need);
+        seen += __popc(eq);
+        const uint32_t all = __ballot_sync(0xffffffffu, kept);
+        if (kept) keep[at + __popc(all & lt)] = t;
+        at += __popc(all);
+      }
     }
-    const uint32_t n = __popc(kept);
-    uint32_t pos = at, all = 0;
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      const uint32_t bal = __ballot_sync(0xffffffffu, (n >> q) & 1u);
-      pos += __popc(bal & lt) << q;
-      all += __popc(bal) << q;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if ((kept >> i) & 1u) keep[pos++] = t + i;
-    at += all;
   }
 }
 
@@ -616,16 +737,13 @@ static CompactKernel compact_kernel_of(int mode, bool paged) {
                                   : compact_of<VQKV_MODE_VQ125>(paged);
 }
 
-// Largest cluster the device can place: 16 CTAs where it can (beyond the
-// portable 8), so that the few streams of one sequence still cover the GPU.
-cudaError_t compact_prepare(int mode, int* max_cluster) {
-  cudaError_t e = cudaSuccess;
-  for (int paged = 0; paged < 2 && e == cudaSuccess; ++paged)
-    e = cudaFuncSetAttribute(compact_kernel_of(mode, paged != 0), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
+// Whether the device places clusters of 16 CTAs, beyond the portable 8, of this kernel.
+template <typename K>
+static bool places_clusters_of_16(K kernel, int threads, size_t smem) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(16, 1, 1);
-  cfg.blockDim = dim3(CP_THREADS);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 16;
@@ -634,11 +752,21 @@ cudaError_t compact_prepare(int mode, int* max_cluster) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, compact_kernel_of(mode, true), &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();   // not an error of the call: the portable size is used
     n = 0;
   }
-  *max_cluster = n > 0 ? 16 : 8;
+  return n > 0;
+}
+
+// Largest cluster the device can place: 16 CTAs where it can (beyond the
+// portable 8), so that the few streams of one sequence still cover the GPU.
+cudaError_t compact_prepare(int mode, int* max_cluster) {
+  cudaError_t e = cudaSuccess;
+  for (int paged = 0; paged < 2 && e == cudaSuccess; ++paged)
+    e = cudaFuncSetAttribute(compact_kernel_of(mode, paged != 0), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  *max_cluster = places_clusters_of_16(compact_kernel_of(mode, true), CP_THREADS, 0) ? 16 : 8;
   return cudaSuccess;
 }
 
@@ -658,22 +786,27 @@ cudaError_t launch_compact(int mode, const CompactParams& p, int sms, int max_cl
   return launch_cluster(k, dim3(cluster, p.Hkv * (p.mass != nullptr ? 3 : 2), p.B), cluster, CP_THREADS, 0, stream, p);
 }
 
-static int select_smem(int keys) { return ((SEL_COPIES + 1) * SEL_BINS + keys) * 4; }
+static int select_smem(int keys) { return (2 * SEL_BINS + SEL_LIST + keys) * 4; }
 
 cudaError_t evict_select_prepare() {
-  return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, select_smem(SEL_CACHE));
+  const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<1024>, a, select_smem(SEL_CACHE));
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(evict_select_kernel<512>, a, select_smem(0));
 }
 
 cudaError_t launch_evict_select(SelectParams p, int sms, cudaStream_t stream) {
-  // CTAs per row: spread the rows over the GPU, but at least 4096 tokens each
+  // CTAs per row: spread few rows over the GPU, but at least 4096 tokens each
   const long long rows = (long long)p.B * p.Hkv;
   int cluster = 1;
   while (cluster < SEL_MAX_CLUSTER && rows * cluster * 2 <= sms && p.max_seq_len > 4096 * cluster) cluster *= 2;
-  const long long part = ((long long)p.max_seq_len + cluster * SEL_WARPS - 1) / (cluster * SEL_WARPS);
-  const long long keys = (part + 127) / 128 * 128 * SEL_WARPS;
-  p.cache_keys = keys <= SEL_CACHE ? (int)keys : 0;
-  return launch_cluster(evict_select_kernel, dim3(cluster, p.Hkv, p.B), cluster, SEL_THREADS,
-                        (size_t)select_smem(p.cache_keys), stream, p);
+  const dim3 grid(cluster, p.Hkv, p.B);
+  p.cache_keys = 0;
+  if (rows * cluster > sms) return launch_cluster(evict_select_kernel<512>, grid, cluster, 512, select_smem(0), stream, p);
+  // one CTA per SM
+  const long long part = ((long long)p.max_seq_len + cluster * 32 - 1) / (cluster * 32);
+  const long long keys = (part + 127) / 128 * 128 * 32;
+  if (keys <= SEL_CACHE) p.cache_keys = (int)keys;
+  return launch_cluster(evict_select_kernel<1024>, grid, cluster, 1024, (size_t)select_smem(p.cache_keys), stream, p);
 }
 
 }  // namespace vqkv
