@@ -325,8 +325,10 @@ vqkv_status plan_tree(const vqkv_decode_tree_args* at, bool pairs, TreePlan* pl)
 // Many: the draft-tree attention, then statistics and query images of the
 // key-only pass.  A group of 4 columns costs one decode, the other path about
 // the same for any number: at 196,608 tokens and 8 KV heads 12 / 16 columns take
-// 127 / 168 us at 2 bit, 151 / 199 at 4, 261 / 346 at 3 and 240 / 328 at 1.5 on
-// the first path, and 32 columns 186, 266, 267 and 260 us on the second.
+// 127 / 167 us at 2 bit, 151 / 199 at 4, 190 / 253 at 1.25 and 261, 240 (12 columns)
+// at 3 and 1.5 on the first path; 178, 258, 217, 260 and 250 on the second.  Short
+// sequences favour the first path further: 16 columns of 4,096 tokens 14 and 25 us
+// at 2 bit.
 int mass_few_cols(int mode) { return mode == VQKV_MODE_VQ3 || mode == VQKV_MODE_VQ15 ? 12 : 16; }
 
 struct MassPlan {
