@@ -406,24 +406,27 @@ def fp16_decode_workspace(B, Hq, Hkv, cap_len, max_seq_len, num_splits=0, device
 
 # ---------------------------------------------------------------- drafts and a changing cache
 
-def _enter(what, stream, tensors) -> int | None:
+# A short call is bound by the host, so the calls below look after their own
+# time: the raw handle of the current stream (torch.cuda.current_stream() builds
+# an object for it, 2.8 us of then 20), no comparison of a shape with itself, one
+# structure per call.
+
+def _enter(torch, what, stream, tensors) -> int | None:
     """The stream handle of a call, after checking its tensors.
 
-    ``tensors``: (name, tensor, dtype, shape) each; None tensors are skipped.
-    Every tensor has to be contiguous and on the current CUDA device.
+    ``tensors``: (name, tensor, dtype, shape or None for any) each; None
+    tensors are skipped.  Every tensor has to be contiguous and on the current
+    CUDA device.
     """
-    import torch
-    if stream is None:
-        s = torch.cuda.current_stream()
-        dev, handle = s.device_index, s.cuda_stream
-    else:
-        dev, handle = torch.cuda.current_device(), _stream(stream)
+    dev = torch.cuda.current_device()
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
     for name, t, dtype, shape in tensors:
-        if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev):
+        if t is None or (t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous()
+                         and t.get_device() == dev):
             continue
         if t.dtype is not dtype:
             raise TypeError(f"{what}: {name} must be {dtype}, not {t.dtype}")
-        if t.shape != shape:
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{what}: {name} must be contiguous")
@@ -456,26 +459,27 @@ def _size_args(mode, B, Hq, Hkv, cap_len, max_seq_len, num_splits) -> DecodeArgs
                       num_splits=num_splits)
 
 
-def _many_query_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace, cap_len,
-                     max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks, stream, more):
-    """(DecodeArgs, stream handle) of a call with q, out [B][M][Hq][128]; ``more(B, M, Hkv)``: its other tensors."""
+def _many_query_call(what, args, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace, cap_len,
+                     max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks, stream, name, extra):
+    """A call with q, out [B][M][Hq][128] and one tensor more: ``args(decode, M, extra)`` is its argument structure."""
     import torch
     if q.dim() != 4:
         raise ValueError(f"{what}: q must have shape (B, M, Hq, 128), not {tuple(q.shape)}")
-    B, M, Hq, D = q.shape
+    B, M, Hq, D = shape = q.shape
     Hkv = k_codebook.shape[0]
-    f16, i32 = torch.float16, torch.int32
+    f16, i32, u8 = torch.float16, torch.int32, torch.uint8
     cache = _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks)
     book = (Hkv, *CODEBOOK_SHAPE.get(mode, k_codebook.shape[1:]))   # the C entry refuses other modes
-    handle = _enter(what, stream, (
-        ("q", q, f16, q.shape), ("k_codes", k_codes, torch.uint8, cache), ("v_codes", v_codes, torch.uint8, cache),
+    last = (torch.int64, (B, M)) if name == "tree_mask" else (torch.float32, (B, Hkv, cap_len))
+    handle = _enter(torch, what, stream, (
+        ("q", q, f16, None), ("k_codes", k_codes, u8, cache), ("v_codes", v_codes, u8, cache),
         ("seq_lens", seq_lens, i32, (B,)), ("k_codebook", k_codebook, f16, book), ("v_codebook", v_codebook, f16, book),
-        ("s", s, torch.float32, (Hkv, D)), ("out", out, f16, q.shape),
-        ("workspace", workspace, torch.uint8, workspace.shape),
-        ("block_table", block_table, i32, block_table.shape if block_table is not None else None), *more(B, M, Hkv)))
-    return DecodeArgs(mode, B, Hq, Hkv, D, cap_len, max_seq_len, q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
-                      seq_lens.data_ptr(), k_codebook.data_ptr(), v_codebook.data_ptr(), s.data_ptr(), softmax_scale,
-                      num_splits, workspace.data_ptr(), workspace.numel(), out.data_ptr()), handle
+        ("s", s, torch.float32, (Hkv, D)), ("out", out, f16, shape), ("workspace", workspace, u8, None),
+        ("block_table", block_table, i32, None), (name, extra, *last)))
+    a = args((mode, B, Hq, Hkv, D, cap_len, max_seq_len, q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
+              seq_lens.data_ptr(), k_codebook.data_ptr(), v_codebook.data_ptr(), s.data_ptr(), softmax_scale,
+              num_splits, workspace.data_ptr(), workspace.numel(), out.data_ptr()), M, extra.data_ptr())
+    _check(getattr(lib(), what)(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
 
 
 def decode_tree_workspace(mode, B, Hq, Hkv, n_queries, cap_len, max_seq_len, num_splits=0, device="cuda"):
@@ -495,13 +499,9 @@ def vqkv_decode_attn_tree(mode, q, tree_mask, k_codes, v_codes, seq_lens, k_code
     [B][M]) is set.  k_codes / v_codes: [B][Hkv][bytes], or pools with
     block_table.
     """
-    import torch
-    what = "vqkv_decode_attn_tree"
-    d, handle = _many_query_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace,
-                                 cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks,
-                                 stream, lambda B, M, Hkv: (("tree_mask", tree_mask, torch.int64, (B, M)),))
-    a = DecodeTreeArgs(d, q.shape[1], tree_mask.data_ptr())
-    _check(lib().vqkv_decode_attn_tree(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
+    _many_query_call("vqkv_decode_attn_tree", DecodeTreeArgs, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook,
+                     s, out, workspace, cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens,
+                     num_blocks, stream, "tree_mask", tree_mask)
 
 
 def decode_mass_workspace(mode, B, Hq, Hkv, n_queries, cap_len, max_seq_len, num_splits=0, device="cuda"):
@@ -518,13 +518,9 @@ def vqkv_decode_attn_mass(mode, q, k_codes, v_codes, seq_lens, k_codebook, v_cod
     vqkv_decode_attn_multi) that adds each cached token's attention weight,
     summed over the M queries and the heads of its KV head, to mass (fp32
     [B][Hkv][cap_len])."""
-    import torch
-    what = "vqkv_decode_attn_mass"
-    d, handle = _many_query_args(what, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace,
-                                 cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens, num_blocks,
-                                 stream, lambda B, M, Hkv: (("mass", mass, torch.float32, (B, Hkv, cap_len)),))
-    a = DecodeMassArgs(d, q.shape[1], mass.data_ptr())
-    _check(lib().vqkv_decode_attn_mass(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
+    _many_query_call("vqkv_decode_attn_mass", DecodeMassArgs, mode, q, k_codes, v_codes, seq_lens, k_codebook, v_codebook,
+                     s, out, workspace, cap_len, max_seq_len, softmax_scale, num_splits, block_table, block_tokens,
+                     num_blocks, stream, "mass", mass)
 
 
 def vqkv_evict_select(mass, seq_lens, keep, keep_lens, n_sink=0, n_recent=0, max_seq_len=None, error_flags=None,
@@ -542,8 +538,8 @@ def vqkv_evict_select(mass, seq_lens, keep, keep_lens, n_sink=0, n_recent=0, max
     i32 = torch.int32
     B, Hkv, cap = mass.shape
     n_keep = keep.shape[-1]
-    handle = _enter(what, stream, (
-        ("mass", mass, torch.float32, mass.shape), ("seq_lens", seq_lens, i32, (B,)),
+    handle = _enter(torch, what, stream, (
+        ("mass", mass, torch.float32, None), ("seq_lens", seq_lens, i32, (B,)),
         ("keep", keep, i32, (B, Hkv, n_keep)), ("keep_lens", keep_lens, i32, (B,)),
         ("error_flags", error_flags, i32, (1,))))
     a = EvictSelectArgs(B, Hkv, cap, cap if max_seq_len is None else max_seq_len, n_keep, n_sink, n_recent,
@@ -567,12 +563,12 @@ def vqkv_cache_compact(mode, k_codes, v_codes, seq_lens, src, counts, cap_len, s
     B, heads, n = src.shape
     Hkv = k_codes.shape[1]
     cache = _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks)
-    handle = _enter(what, stream, (
+    handle = _enter(torch, what, stream, (
         ("k_codes", k_codes, torch.uint8, cache), ("v_codes", v_codes, torch.uint8, cache),
-        ("seq_lens", seq_lens, i32, (B,)), ("src", src, i32, src.shape), ("counts", counts, i32, (B,)),
+        ("seq_lens", seq_lens, i32, (B,)), ("src", src, i32, None), ("counts", counts, i32, (B,)),
         ("start", start, i32, (B,)), ("mass", mass, torch.float32, (B, Hkv, cap_len)),
         ("error_flags", error_flags, i32, (1,)),
-        ("block_table", block_table, i32, block_table.shape if block_table is not None else None)))
+        ("block_table", block_table, i32, None)))
     a = CacheCompactArgs(mode, B, Hkv, cap_len, n, heads, k_codes.data_ptr(), v_codes.data_ptr(), seq_lens.data_ptr(),
                          src.data_ptr(), counts.data_ptr(), _ptr(start), _ptr(mass), _ptr(error_flags))
     _check(lib().vqkv_cache_compact(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
