@@ -774,17 +774,20 @@ cudaError_t compact_prepare(int mode, int* max_cluster) {
 
 cudaError_t launch_compact(int mode, const CompactParams& p, int sms, int max_cluster, cudaStream_t stream) {
   const CompactKernel k = compact_kernel_of(mode, p.block_table != nullptr);
-  // CTAs per stream: at most what one round of its destinations needs, and up to
-  // 8 while all CTAs are fewer than eight per SM (384 streams of a paged
-  // 1.25-bit batch: 113 us at 1 CTA each, 88 at 4, 99 at 8).  Sixteen, beyond the
-  // portable size, only for so few streams that eight would leave SMs idle: 24
-  // streams of 196,608 tokens 46 -> 42 us, but 96 streams of 16,384 19 -> 36 us,
-  // because few clusters of 16 are placed at a time.
+  // CTAs per stream: what moves its tokens in one round (24 streams of 4,096 kept
+  // tokens at 2 bit: 15.9 us at 1, 4.8 at 4, 6.5 at 8, 9.6 at 16), up to 8 while all
+  // CTAs are fewer than eight per SM (384 streams of a paged 1.25-bit batch: 113 us
+  // at 1 CTA each, 88 at 4, 99 at 8).  Sixteen, beyond the portable size, only for
+  // so few streams that eight would leave SMs idle: 24 streams of 65,536 kept
+  // tokens 55 -> 42 us, but 96 streams of 8,192 22 -> 39 us, because few clusters
+  // of 16 are placed at a time.
   const long long streams = (long long)p.B * p.Hkv * (p.mass != nullptr ? 3 : 2);
-  const long long groups = ((long long)p.n_src + 30) / 16;
+  const long long groups = ((long long)p.n_src + (p.start != nullptr ? 30 : 15)) / 16;   // a start may lie inside a group
+  // groups per CTA and round (where K and V runs differ, those of K)
+  const long long round = CP_WARPS * (mode == VQKV_MODE_VQ3 || mode == VQKV_MODE_VQ4 ? 2 : 4);
   int cluster = 1;
-  while (cluster < 8 && (long long)cluster * CP_WARPS < groups && streams * cluster < 8LL * sms) cluster *= 2;
-  if (cluster == 8 && max_cluster == 16 && 8LL * CP_WARPS < groups && streams * 8 < 2LL * sms) cluster = 16;
+  while (cluster < 8 && cluster * round < groups && streams * cluster < 8LL * sms) cluster *= 2;
+  if (cluster == 8 && max_cluster == 16 && 8 * round < groups && streams * 8 < 2LL * sms) cluster = 16;
   return launch_cluster(k, dim3(cluster, p.Hkv * (p.mass != nullptr ? 3 : 2), p.B), cluster, CP_THREADS, 0, stream, p);
 }
 
