@@ -256,6 +256,24 @@ def test_compact_many_rounds(mode):
     assert run_compact(mode, 1, 1, L, [L], src, [7500], None, seed=40 + mode) == 0
 
 
+@pytest.mark.parametrize("mode,page", [(0, 0), (0, 256), (1, 0), (2, 0), (3, 64), (4, 0)])
+def test_compact_rounds_of_the_largest_cluster(mode, page):
+    # more kept tokens than the largest cluster moves in one round (16 x 16 warps x 4 groups of 16 tokens)
+    r = np.random.default_rng(70 + mode)
+    L, n = 70001, 60000
+    src = np.sort(r.permutation(L)[:n])[None, None].astype(np.int32)
+    assert run_compact(mode, 1, 1, L, [L], src, [n], None, seed=80 + mode, page=page) == 0
+
+
+@pytest.mark.parametrize("mode", [0, 3])
+def test_compact_unordered_sources_over_rounds(mode):
+    # every source at or after its place, in any order, many read by several tokens
+    r = np.random.default_rng(6)
+    L, n = 52000, 50000
+    src = np.minimum(np.arange(n) + r.integers(0, 2000, size=(1, 1, n)), L - 1).astype(np.int32)
+    assert run_compact(mode, 1, 1, L, [L], src, [n], None, seed=9) == 0
+
+
 @pytest.mark.parametrize("mode", [0, 1, 2, 3, 4])
 @pytest.mark.parametrize("page", [0, 128])
 def test_compact_accepted_path_shared_by_heads(mode, page):

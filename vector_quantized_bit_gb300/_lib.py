@@ -8,6 +8,7 @@ missing library raises on first use.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import _build
@@ -434,13 +435,18 @@ def _enter(torch, what, stream, tensors) -> int | None:
     return handle
 
 
+@functools.lru_cache(maxsize=256)
+def _code_bytes(mode, tokens):
+    return vqkv_code_bytes(mode, tokens)
+
+
 def _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks):
     """Shape of a contiguous cache [B][Hkv][bytes], or of the pools of a paged one."""
     if block_table is None:
-        return (B, Hkv, vqkv_code_bytes(mode, cap_len))
+        return (B, Hkv, _code_bytes(mode, cap_len))
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"{what}: block_table must have shape ({B}, max_blocks)")
-    return (num_blocks, Hkv, vqkv_code_bytes(mode, block_tokens))
+    return (num_blocks, Hkv, _code_bytes(mode, block_tokens))
 
 
 def _paging_ref(block_table, block_tokens, num_blocks):
