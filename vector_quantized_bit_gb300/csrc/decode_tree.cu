@@ -284,11 +284,10 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   Pieces pc(s_pref, p.B, split, p.n_splits);
   grid_dependency_wait();
   grid_dependents_launch();
-  if (split == 0)   // sequences without tokens
-    for (int i = threadIdx.x; i < p.B * nloc * kHeadDim; i += THREADS) {
-      const int bb = i / (nloc * kHeadDim), c = col0 + (i / kHeadDim) % nloc;
-      if (s_pref[bb + 1] == s_pref[bb]) p.out[out_row(p, bb, kvh, c) + (i & (kHeadDim - 1))] = __float2half_rn(0.f);
-    }
+  for (int bb = split; bb < p.B; bb += gridDim.x)   // sequences without tokens
+    if (s_pref[bb + 1] == s_pref[bb])
+      for (int i = threadIdx.x; i < nloc * kHeadDim; i += THREADS)
+        p.out[out_row(p, bb, kvh, col0 + i / kHeadDim) + (i & (kHeadDim - 1))] = __float2half_rn(0.f);
   tcgen05_before_sync();
   __syncthreads();
   tcgen05_after_sync();
