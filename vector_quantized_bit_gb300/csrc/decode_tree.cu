@@ -93,11 +93,11 @@ struct Geo {
   // stage k % STAGES and belongs to softmax warpgroup k % 2)
   static constexpr int STAGES = CB_BYTES == 65536 ? 4 : 2;
   static constexpr int K_OFF = CB_BYTES, V_OFF = K_OFF + STAGES * TILE_SMEM;
-  static constexpr int BAR_OFF = V_OFF + STAGES * TILE_SMEM;
+  static constexpr int BOX_OFF = V_OFF + STAGES * TILE_SMEM;   // 2 KB per softmax warp, for the epilogue
+  static constexpr int BAR_OFF = BOX_OFF + SM_WARPS * 2048;
   static constexpr int ML_OFF = BAR_OFF + 256;             // the warpgroups' max and sum per column, for the merge
   static constexpr int PREF_OFF = ML_OFF + 2 * ROWS * 8;       // tiles of the sequences before each
   static constexpr int SMEM = PREF_OFF + (kFlatMaxB + 1) * 4;
-  static_assert(SM_WARPS * 32 * 32 * 4 <= 2 * STAGES * TILE_SMEM, "the epilogue's boxes are in the rings");
   static_assert(SMEM <= 226 * 1024, "shared memory");
 };
 }  // namespace tr
@@ -293,8 +293,11 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   tcgen05_after_sync();
   const uint32_t tmem = s_tmem;
   uint32_t done = 0;   // tiles of earlier pieces
-  // Per piece, every role meets twice: q' in tensor memory; the piece's
-  // state written out.
+  // Per piece the softmax warps and the issuing ones meet once: q' in tensor
+  // memory, and the last piece's state read out of it.  (With the dequantising
+  // warps meeting there as well, which waits out a memory latency per piece, 64
+  // sequences of up to 512 tokens took 54 us.)
+  constexpr int MEET = (SM_WARPS + 2) * 32;
   if (warp < SM_WARPS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SM));
     // ---------------- softmax warpgroup wg: thread = column c
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         tmem_wait_st();
       }
       tcgen05_before_sync();
-      __syncthreads();
+      named_barrier_sync(2, MEET);
       tcgen05_after_sync();
       float m = kMInit, l = 0.f;
       bool ok = live;
@@ -364,52 +367,47 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           const float inv = l > 0.f ? 1.f / l : 0.f;
           fa *= inv, fb *= inv;
         }
-        // 32 channels at a time, transposed through the warp's own shared memory
-        // (the tile rings are idle: every product of the piece is done) so that
-        // the stores cover whole lines; 16-byte pieces permuted by the row
+        // 16 channels at a time, transposed through the warp's own shared memory so
+        // that a row's stores are neighbours; 16-byte pieces permuted by the row
         const int c0 = c - (lane & (WCOLS - 1));   // the warp's first column
-        float* box = reinterpret_cast<float*>(smem + G::K_OFF) + warp * (32 * 32);
+        float* box = reinterpret_cast<float*>(smem + G::BOX_OFF) + warp * (32 * 16);
         float* part = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + split + pc.b) * p.ncols + c0) * kPartialStride;
 #pragma unroll 1
-        for (int q = NQ == 1 ? 2 * wg : 0; q < (NQ == 1 ? 2 * wg + 2 : 4); ++q) {
-          float o[32];
-          tmem_ld32(t_lane + T_O + kHeadDim * own + 32 * q, o);
+        for (int q = NQ == 1 ? 4 * wg : 0; q < (NQ == 1 ? 4 * wg + 4 : 8); ++q) {
+          uint32_t o[16], z[16];
+          tmem_ld16(t_lane + T_O + kHeadDim * own + 16 * q, o);
+          if (both) tmem_ld16(t_lane + T_O + kHeadDim * (own ^ 1) + 16 * q, z);
           tmem_wait_ld();
+          float v[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= fa;
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * fa;
           if (both) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t z[16];
-              tmem_ld16(t_lane + T_O + kHeadDim * (own ^ 1) + 32 * q + 16 * h, z);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[16 * h + i] += __uint_as_float(z[i]) * fb;
-            }
+            for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(z[i]) * fb;
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(box + lane * 32 + ((i ^ (lane & 7)) << 2)) =
-                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(box + lane * 16 + ((i ^ ((lane >> 1) & 3)) << 2)) =
+                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           __syncwarp();
-          const int x = lane & 7;   // 16-byte piece of the rows 4 i + lane / 8
+          const int x = lane & 3;   // 16-byte piece of the rows 8 i + lane / 4
           if (!whole) {
-            float* dst = part + (lane >> 3) * kPartialStride + 32 * q + 4 * x;
+            float* dst = part + (lane >> 2) * kPartialStride + 16 * q + 4 * x;
 #pragma unroll
-            for (int i = 0; i < WCOLS / 4; ++i) {
-              const int r = 4 * i + (lane >> 3);
+            for (int i = 0; i < WCOLS / 8; ++i) {
+              const int r = 8 * i + (lane >> 2);
               if (c0 - col0 + r < nloc)
-                *reinterpret_cast<float4*>(dst + 4 * i * kPartialStride) =
-                    *reinterpret_cast<const float4*>(box + r * 32 + ((x ^ (r & 7)) << 2));
+                *reinterpret_cast<float4*>(dst + 8 * i * kPartialStride) =
+                    *reinterpret_cast<const float4*>(box + r * 16 + ((x ^ ((r >> 1) & 3)) << 2));
             }
           } else {
-#pragma unroll 1
-            for (int i = 0; i < WCOLS / 4; ++i) {
-              const int r = 4 * i + (lane >> 3);
+#pragma unroll
+            for (int i = 0; i < WCOLS / 8; ++i) {
+              const int r = 8 * i + (lane >> 2);
               if (c0 - col0 + r < nloc) {
-                const float4 v = *reinterpret_cast<const float4*>(box + r * 32 + ((x ^ (r & 7)) << 2));
-                __half* dst = p.out + out_row(p, pc.b, kvh, c0 + r) + 32 * q + 4 * x;
-                const uint2 h = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
+                const float4 w = *reinterpret_cast<const float4*>(box + r * 16 + ((x ^ ((r >> 1) & 3)) << 2));
+                __half* dst = p.out + out_row(p, pc.b, kvh, c0 + r) + 16 * q + 4 * x;
+                const uint2 h = make_uint2(pack_half2(w.x, w.y), pack_half2(w.z, w.w));
                 if ((reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
                   *reinterpret_cast<uint2*>(dst) = h;
                 } else {   // out needs only 2-byte alignment
@@ -429,9 +427,6 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         }
       }
       done += pc.n;
-      tcgen05_before_sync();
-      __syncthreads();
-      tcgen05_after_sync();
     }
   } else if (warp < MMA_WARP) {
     // ---------------- dequantisation
@@ -446,7 +441,6 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         dequant_piece<MODE, VQKV_ROLE_V, PAGED, TOK, G::STAGES>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::V_OFF,
                                                                 pv_ready, v_empty, u, half, lane, abort_flag);
       done += pc.n;
-      __syncthreads();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
@@ -481,9 +475,9 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
       for (int k = 0; k < 4; ++k) umma_f16_ts(dv, ap + 8 * k, lo + k * (2048 / 16), v_hi, idesc_o, !fresh || k > 0);
     };
     bool ok = true;
-    while (pc.next()) {
+    while (warp < MMA_WARP + 2 && pc.next()) {
       tcgen05_before_sync();
-      __syncthreads();
+      named_barrier_sync(2, MEET);
       tcgen05_after_sync();
       const int n = pc.n;
       const int job = warp - MMA_WARP;
@@ -539,7 +533,6 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         }
       }
       done += n;
-      __syncthreads();
     }
     if (warp < MMA_WARP + 2) {   // every product issued has completed before the tensor memory is freed
       const uint32_t mine = all_done + 8 * (warp - MMA_WARP);

@@ -339,8 +339,9 @@ __device__ __forceinline__ bool tr_wait(uint32_t mbar, uint32_t parity, volatile
 // other tile of a piece: n tiles of TOK tokens of sequence b from tile0 on,
 // those whose number, counted over the CTA's pieces, has parity `half` (done:
 // tiles of earlier pieces; tile k goes to stage k % STAGES of `ring`).  Codes are
-// loaded PREFETCH of its tiles ahead into registers, block ids one further; the
-// first ones before the CTA meets (rings free).
+// loaded PREFETCH of its tiles ahead into registers, block ids one further.
+// These warps meet the others only through the ring's barriers, so they run
+// ahead into the next piece while the others finish one.
 template <int MODE, int ROLE, bool PAGED, int TOK, int STAGES>
 __device__ __forceinline__ void dequant_piece(const DecodeParams& p, int b, int kvh, int tile0, int n, int L, uint32_t done,
                                               const unsigned char* s_cb, unsigned char* ring, uint32_t full, uint32_t empty,
@@ -373,7 +374,6 @@ __device__ __forceinline__ void dequant_piece(const DecodeParams& p, int b, int 
 #pragma unroll
   for (int d = 0; d < PREFETCH; ++d) fetch(place(mine + 2 * d), w[d]);
   long long next = place(mine + 2 * PREFETCH);
-  __syncthreads();   // the rings are free
   for (int t0 = mine; t0 < n; t0 += 2 * PREFETCH) {
 #pragma unroll
     for (int d = 0; d < PREFETCH; ++d) {

@@ -117,8 +117,9 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
   const uint32_t tmem = s_tmem;
   uint32_t done = 0;   // tiles of earlier pieces
 
-  // Per piece, every role meets twice: q' and the columns' values in place; the
-  // piece done.
+  // Per piece the epilogue warps and the issuing one meet twice: q' and the
+  // columns' values in place; the piece done.
+  constexpr int MEET = (EP_WARPS + 1) * 32;
   if (warp < EP_WARPS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EP));
     // ---------------- epilogue: warpgroup wg takes every other tile, thread = token
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
         }
       }
       fence_proxy_async_smem();   // q' is read by the tensor cores
-      __syncthreads();
+      named_barrier_sync(1, MEET);
       float* mass = p.mass + pair * p.cap_len;
       bool ok = true;
       for (int t = (int)((done + wg) & 1); t < pc.n; t += 2) {
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
         if (tok < L) mass[tok] = old + w;
       }
       done += pc.n;
-      __syncthreads();
+      named_barrier_sync(1, MEET);
     }
   } else if (warp < MMA_WARP) {
     // ---------------- dequantisation of the keys
@@ -185,7 +186,6 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
       dequant_piece<MODE, VQKV_ROLE_K, PAGED, TOK, STAGES>(p, pc.b, kvh, pc.tile0, pc.n, clamped_len(p, pc.b), done, smem,
                                                           smem + K_OFF, k_full, k_empty, dw & 7, dw >> 3, lane, abort_flag);
       done += pc.n;
-      __syncthreads();
     }
   } else {
     // ---------------- score products: one warp, an elected lane issues
@@ -196,28 +196,26 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
     const uint64_t q_desc = umma_desc_sw128(smem_u32(smem + Q_OFF), 1024, 16);
     const bool issuer = elect_one();
     bool ok = true;
-    while (pc.next()) {
-      __syncthreads();
-      if (warp == MMA_WARP) {
-        for (int t = 0; ok && t < pc.n; ++t) {
-          const uint32_t k = done + t, st = k % STAGES, wg = k & 1;
-          ok = tr_wait(k_full + 8 * st, (k / STAGES) & 1, abort_flag, p.err) &&
-               tr_wait(d_empty + 8 * wg, ((k >> 1) & 1) ^ 1, abort_flag, p.err);
-          if (!ok) break;
-          tcgen05_after_sync();
-          if (issuer) {
+    while (warp == MMA_WARP && pc.next()) {
+      named_barrier_sync(1, MEET);
+      for (int t = 0; ok && t < pc.n; ++t) {
+        const uint32_t k = done + t, st = k % STAGES, wg = k & 1;
+        ok = tr_wait(k_full + 8 * st, (k / STAGES) & 1, abort_flag, p.err) &&
+             tr_wait(d_empty + 8 * wg, ((k >> 1) & 1) ^ 1, abort_flag, p.err);
+        if (!ok) break;
+        tcgen05_after_sync();
+        if (issuer) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)   // 16 channels: 32 bytes of a 128-byte row, four per 64-channel half
-              umma_f16(tm + 128 * wg, k_desc + (st * TILE_SMEM + (i >> 2) * HALF + (i & 3) * 32) / 16,
-                       q_desc + ((i >> 2) * (2 * NC * 128) + (i & 3) * 32) / 16, idesc, i > 0);
-            umma_commit(k_empty + 8 * st);
-            umma_commit(d_full + 8 * wg);
-          }
-          __syncwarp();
+          for (int i = 0; i < 8; ++i)   // 16 channels: 32 bytes of a 128-byte row, four per 64-channel half
+            umma_f16(tm + 128 * wg, k_desc + (st * TILE_SMEM + (i >> 2) * HALF + (i & 3) * 32) / 16,
+                     q_desc + ((i >> 2) * (2 * NC * 128) + (i & 3) * 32) / 16, idesc, i > 0);
+          umma_commit(k_empty + 8 * st);
+          umma_commit(d_full + 8 * wg);
         }
+        __syncwarp();
       }
       done += pc.n;
-      __syncthreads();
+      named_barrier_sync(1, MEET);
     }
     if (warp == MMA_WARP) {   // every product issued has completed before the tensor memory is freed
       if (issuer) umma_commit(all_done);
