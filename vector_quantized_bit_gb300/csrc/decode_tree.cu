@@ -39,15 +39,15 @@
 // adds; both lanes then carry the column.  (Not for the plain tree: 64 shuffles
 // more per thread and tile.)
 //
-// Measured: 64 columns over 196,608 tokens and 8 KV heads at 2 bit take 97 us for the
-// call (530 TFLOP/s of the two products; plain torch 11.4 ms).  A 64-token
+// Measured: 64 columns over 196,608 tokens and 8 KV heads at 2 bit take 98 us for the
+// call (525 TFLOP/s of the two products; plain torch 11.4 ms).  A 64-token
 // tile takes 1,050 cycles.  Bound: shared memory (each token's 512 bytes are
 // gathered, stored and read by the MMAs; about three quarters of the time)
 // and the hand-offs between the roles.  A 256-column tile (NQ = 2) takes 2,180
 // cycles at 2 bit, as much per column as two CTAs of 128, and less at 1.5 bit,
 // where the gathers conflict, and it halves the partials: hence the border at 128.
-// 135 columns of 8 ragged sequences at 1.5 bit take 187 us, 256 columns of
-// 32,768 tokens at 4 bit 56 us, 20 of them for queries, prologue and merge.
+// 135 columns of 8 ragged sequences at 1.5 bit take 173 us, 256 columns of
+// 32,768 tokens at 4 bit 53 us, 18 of them for queries, prologue and merge.
 //
 // Visibility: tokens t < L - M for every column, draft j for the columns
 // whose mask has bit j; only tiles that reach past L - M test it.  Without
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   // Per piece the softmax warps and the issuing ones meet once: q' in tensor
   // memory, and the last piece's state read out of it.  (With the dequantising
   // warps meeting there as well, which waits out a memory latency per piece, 64
-  // sequences of up to 512 tokens took 54 us.)
+  // sequences of up to 512 tokens took 54 us, not 49.)
   constexpr int MEET = (SM_WARPS + 2) * 32;
   if (warp < SM_WARPS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SM));

@@ -16,8 +16,8 @@
 //
 // What bounds the pass: shared memory (a K' tile is gathered, stored and read
 // by the tensor cores, 256 bytes a token each) next to the exponentials: 1,480
-// cycles per 128 tokens of 64 columns at 3 bit, 36 us for 4 sequences of up to
-// 16,384 tokens and 8 KV heads (the attention before it takes 53 us).
+// cycles per 128 tokens of 64 columns at 3 bit, 32 us for 4 sequences of up to
+// 16,384 tokens and 8 KV heads (the attention before it takes 51 us).
 #include "dequant_tile.cuh"
 
 namespace vqkv {
