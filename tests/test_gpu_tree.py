@@ -152,6 +152,29 @@ def test_tree_ragged_batches(mode, Hq, Hkv, M, num_splits, page):
     assert np.all(o[1] == 0) and np.all(o[5] == 0)
 
 
+@pytest.mark.parametrize("mode,Hq,M", [(0, 4, 9), (1, 4, 9), (2, 8, 20), (3, 4, 33), (4, 8, 30)])   # one and two query tiles
+def test_tree_many_short_sequences_in_two_shares_repeat(mode, Hq, M):
+    """Twenty calls back to back over 24 short sequences in two CTAs, whose roles run ahead of each other from one
+    sequence to the next: every call the reference's result, and all the same bits."""
+    t = H.torch()
+    B, cap = 24, 208
+    r, q, kc, vc, s, kcb, vcb = case(mode, B, Hq, 1, M, cap, seed=31 + mode)
+    lens = r.integers(0, cap + 1, size=B).astype(np.int32)
+    masks = tree_masks(r, B, M, "tree")
+    k, v = (H.dev(H.pack_cache_role(mode, role, c, cap)) for role, c in ((0, kc), (1, vc)))
+    args = [H.dev(x) for x in (q, masks.astype(np.uint64).view(np.int64), lens, kcb, vcb, s)]
+    outs = [t.full((B, M, Hq, 128), float("nan"), dtype=t.float16, device="cuda") for _ in range(20)]
+    ws = _lib.decode_tree_workspace(mode, B, Hq, 1, M, cap, cap, 2)
+    for o in outs:
+        _lib.vqkv_decode_attn_tree(mode, args[0], args[1], k, v, args[2], args[3], args[4], args[5], o, ws, cap, cap,
+                                   num_splits=2)
+    t.cuda.synchronize()
+    ref, _, tol = R.attend(q, kc, vc, kcb, vcb, s, lens, visible_of(masks, M))
+    R.check_output(outs[0].cpu().numpy(), ref, tol)
+    assert all(t.equal(o, outs[0]) for o in outs[1:])
+    assert int(ws[:4].view(t.int32).item()) == 0
+
+
 def test_tree_more_sequences_than_one_launch_takes():
     B, M = 1030, 2
     r = np.random.default_rng(3)
