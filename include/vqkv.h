@@ -543,6 +543,20 @@ vqkv_status vqkv_decode_static_error(uint32_t* host_flags, void* stream);
  */
 vqkv_status vqkv_test_decode_ring_timeout(const vqkv_decode_args* args, uint32_t max_polls, void* stream);
 
+/*
+ * The same for the tile kernels, in all modes.  Every wait gives up after
+ * max_polls polls (1..4096), and stage 0 or 1 of each CTA's ring of key tiles
+ * waits for an arrival that nothing makes, so the tiles from that one on are
+ * not computed.  vqkv_test_decode_tree_timeout runs vqkv_decode_attn_tree on a
+ * contiguous cache.  vqkv_test_decode_mass_timeout runs vqkv_decode_attn_mass
+ * of so many columns that the tile kernels take it (else VQKV_ERR_UNSUPPORTED);
+ * the stage is that of the attention, or of the pass over the keys after it
+ * (key_pass != 0).  NULL args: VQKV_ERR_INVALID_ARG.
+ */
+vqkv_status vqkv_test_decode_tree_timeout(const vqkv_decode_tree_args* args, int32_t stage, uint32_t max_polls, void* stream);
+vqkv_status vqkv_test_decode_mass_timeout(const vqkv_decode_mass_args* args, int32_t key_pass, int32_t stage,
+                                          uint32_t max_polls, void* stream);
+
 /* ------------------------------------------------------------------------
  * Offline calibration: the key smoothing vector, the key transform variants
  * and K-Means codebook training.  These produce the s and codebook inputs of

@@ -38,7 +38,8 @@ EXPORTED = ["vqkv_code_bytes", "vqkv_decode_workspace_bytes", "vqkv_decode_num_s
             "vqkv_kmeans_workspace_bytes", "vqkv_kmeans", "vqkv_kmeans_seed", "vqkv_kmeans_assign",
             "vqkv_kmeans_update_workspace_bytes", "vqkv_kmeans_update", "vqkv_status_string",
             "vqkv_evict_select", "vqkv_cache_compact", "vqkv_decode_tree_workspace_bytes", "vqkv_decode_attn_tree",
-            "vqkv_decode_mass_workspace_bytes", "vqkv_decode_attn_mass"]
+            "vqkv_decode_mass_workspace_bytes", "vqkv_decode_attn_mass", "vqkv_test_decode_tree_timeout",
+            "vqkv_test_decode_mass_timeout"]
 STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -194,6 +195,12 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.vqkv_decode_mass_workspace_bytes.argtypes = [ctypes.POINTER(DecodeMassArgs)]
         L.vqkv_decode_attn_mass.restype = ctypes.c_int
         L.vqkv_decode_attn_mass.argtypes = [ctypes.POINTER(DecodeMassArgs), ctypes.POINTER(Paging), ctypes.c_void_p]
+        L.vqkv_test_decode_tree_timeout.restype = ctypes.c_int
+        L.vqkv_test_decode_tree_timeout.argtypes = [ctypes.POINTER(DecodeTreeArgs), ctypes.c_int32, ctypes.c_uint32,
+                                                    ctypes.c_void_p]
+        L.vqkv_test_decode_mass_timeout.restype = ctypes.c_int
+        L.vqkv_test_decode_mass_timeout.argtypes = [ctypes.POINTER(DecodeMassArgs), ctypes.c_int32, ctypes.c_int32,
+                                                    ctypes.c_uint32, ctypes.c_void_p]
         L.vqkv_evict_select.restype = ctypes.c_int
         L.vqkv_evict_select.argtypes = [ctypes.POINTER(EvictSelectArgs), ctypes.c_void_p]
         L.vqkv_cache_compact.restype = ctypes.c_int

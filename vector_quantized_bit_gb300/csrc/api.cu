@@ -385,6 +385,19 @@ vqkv_status plan_mass(const vqkv_decode_mass_args* am, MassPlan* pl) {
   return VQKV_OK;
 }
 
+// What a timeout test changes in the tile kernels: each wait's polls (0: no
+// test), and the ring stage that lacks an arrival in one of the two kernels.
+struct TestWaits {
+  unsigned polls = 0;
+  int stage = -1, key_stage = -1;
+  bool set(uint32_t max_polls, bool key_pass, int st) {   // every ring has two stages at least
+    if (max_polls < 1 || max_polls > 4096 || st < 0 || st > 1) return false;
+    polls = max_polls;
+    (key_pass ? key_stage : stage) = st;
+    return true;
+  }
+};
+
 vqkv_status validate_fp16(const vqkv_fp16_decode_args* a, bool sizes_only) {
   if (a == nullptr) return VQKV_ERR_INVALID_ARG;
   if (a->head_dim != 128) return VQKV_ERR_UNSUPPORTED;
@@ -689,7 +702,13 @@ size_t vqkv_decode_mass_workspace_bytes(const vqkv_decode_mass_args* a) {
   return pl.ws_bytes;
 }
 
-vqkv_status vqkv_decode_attn_mass(const vqkv_decode_mass_args* am, const vqkv_paging* pg, void* stream) {
+}  // extern "C"
+
+namespace vqkv {
+namespace {
+
+vqkv_status mass_launch(const vqkv_decode_mass_args* am, const vqkv_paging* pg, void* stream,
+                        const TestWaits& test = TestWaits()) {
   vqkv_status st = validate_mass_sizes(am);
   if (st != VQKV_OK) return st;
   const vqkv_decode_args* a = &am->decode;
@@ -712,7 +731,11 @@ vqkv_status vqkv_decode_attn_mass(const vqkv_decode_mass_args* am, const vqkv_pa
   p.mass = am->mass;
   p.cap_len = a->cap_len;
   p.stats = reinterpret_cast<float2*>(ws + pl.stats_off);
+  if (test.polls > 0 && !pl.tiles) return VQKV_ERR_UNSUPPORTED;
   if (pl.tiles) {
+    p.max_polls = test.polls > 0 ? test.polls : kTilePolls;
+    p.withhold_stage = test.stage;
+    p.withhold_key_stage = test.key_stage;
     p.partials = reinterpret_cast<float*>(ws + pl.t.partials_off);
     p.cgroups = pl.t.cgroups;
     p.n_splits = pl.t.n_splits;
@@ -739,13 +762,35 @@ vqkv_status vqkv_decode_attn_mass(const vqkv_decode_mass_args* am, const vqkv_pa
   return launch_decode_mass(a->mode, p, grid, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
 }
 
+}  // namespace
+}  // namespace vqkv
+
+extern "C" {
+
+vqkv_status vqkv_decode_attn_mass(const vqkv_decode_mass_args* am, const vqkv_paging* pg, void* stream) {
+  return mass_launch(am, pg, stream);
+}
+
+vqkv_status vqkv_test_decode_mass_timeout(const vqkv_decode_mass_args* am, int32_t key_pass, int32_t stage, uint32_t max_polls,
+                                          void* stream) {
+  TestWaits test;
+  if (!test.set(max_polls, key_pass != 0, stage)) return VQKV_ERR_INVALID_ARG;
+  return mass_launch(am, nullptr, stream, test);
+}
+
 size_t vqkv_decode_tree_workspace_bytes(const vqkv_decode_tree_args* a) {
   TreePlan pl;
   if (validate_tree_sizes(a) != VQKV_OK || plan_tree(a, false, &pl) != VQKV_OK) return 0;
   return pl.ws_bytes;
 }
 
-vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_paging* pg, void* stream) {
+}  // extern "C"
+
+namespace vqkv {
+namespace {
+
+vqkv_status tree_launch(const vqkv_decode_tree_args* at, const vqkv_paging* pg, void* stream,
+                        const TestWaits& test = TestWaits()) {
   vqkv_status st = validate_tree_sizes(at);
   if (st != VQKV_OK) return st;
   const vqkv_decode_args* a = &at->decode;
@@ -768,6 +813,8 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_pa
   p.partials = reinterpret_cast<float*>(ws + pl.partials_off);
   p.cgroups = pl.cgroups;
   p.n_splits = pl.n_splits;
+  p.max_polls = test.polls > 0 ? test.polls : kTilePolls;
+  p.withhold_stage = test.stage;
   const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(at->tree_mask);
   for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
     const DecodeParams c = batch_part(p, b0, a->B);
@@ -776,6 +823,21 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_pa
       return VQKV_ERR_CUDA;
   }
   return VQKV_OK;
+}
+
+}  // namespace
+}  // namespace vqkv
+
+extern "C" {
+
+vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* at, const vqkv_paging* pg, void* stream) {
+  return tree_launch(at, pg, stream);
+}
+
+vqkv_status vqkv_test_decode_tree_timeout(const vqkv_decode_tree_args* at, int32_t stage, uint32_t max_polls, void* stream) {
+  TestWaits test;
+  if (!test.set(max_polls, false, stage)) return VQKV_ERR_INVALID_ARG;
+  return tree_launch(at, nullptr, stream, test);
 }
 
 vqkv_status vqkv_evict_select(const vqkv_evict_select_args* a, void* stream) {

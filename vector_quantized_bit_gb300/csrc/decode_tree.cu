@@ -116,7 +116,7 @@ __device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Pi
   // NQ 1: tiles whose number (counted over the CTA's pieces) has this parity; NQ 2: every tile
   for (int t = NQ == 1 ? (int)((done + wg) & 1) : 0; t < pc.n; t += NQ == 1 ? 2 : 1) {
     const uint32_t use = NQ == 1 ? (uint32_t)(done + t) >> 1 : (uint32_t)(done + t);
-    if (!tr_wait(s_full + 8 * wg, use & 1, abort_flag, p.err)) return false;
+    if (!tr_wait(p, s_full + 8 * wg, use & 1, abort_flag)) return false;
     tcgen05_after_sync();
     float x[2][32], top0 = neg_inf(), top1 = neg_inf();
     if constexpr (PAIR) {
@@ -152,7 +152,7 @@ __device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Pi
       }
     }
     if (NQ == 1 && !first) {   // O and P of this warpgroup's previous tile are no longer in use
-      if (!tr_wait(o_done + 8 * wg, (use - 1) & 1, abort_flag, p.err)) return false;
+      if (!tr_wait(p, o_done + 8 * wg, (use - 1) & 1, abort_flag)) return false;
       tcgen05_after_sync();
     }                          // (NQ 2: this tile's score product came after that P.V product)
     if (__any_sync(0xffffffffu, top > m + kSoftmaxSlack)) {
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   int* s_pref = reinterpret_cast<int*>(smem + G::PREF_OFF);
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < ST; ++i) {
-      mbar_init(s_ready + 8 * i, NQ == 1 ? 4 + active0 : 4);
+      mbar_init(s_ready + 8 * i, (NQ == 1 ? 4 + active0 : 4) + ((int)i == p.withhold_stage));
       mbar_init(k_empty + 8 * i, NQ == 1 ? 1 : jobs);
       mbar_init(pv_ready + 8 * i, NQ == 1 ? 4 + active0 : 4);
       mbar_init(v_empty + 8 * i, NQ == 1 ? 1 : jobs);
@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     const bool live = (warp & 3) < (wg ? active1 : active0);
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     if (NQ == 1 && live && lane == 0) mbar_arrive(s_ready + 8 * wg);   // no scores to read yet
+    bool ok = live;   // no wait has given up
     for (int piece = 0; pc.next(); ++piece) {
       if (live && (NQ == 2 || wg == 0)) {   // q' into tensor memory: lane = column
         const uint4* q = qx + ((((size_t)pc.b * p.Hkv + kvh) * ((p.ncols + WCOLS - 1) / WCOLS) + c / WCOLS) * 16) * 32 + lane;
@@ -325,9 +326,8 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
       named_barrier_sync(2, MEET);
       tcgen05_after_sync();
       float m = kMInit, l = 0.f;
-      bool ok = live;
       const int prefix = clamped_len(p, pc.b) - p.M;   // tokens below it are visible to every column
-      if (live) {
+      if (ok) {
         unsigned long long mask = 0;
         if (cl < nloc) {
           const int q = c / p.g;   // no masks: causal queries
@@ -338,9 +338,9 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
                                   o_done, abort_flag, m, l);
         if (NQ == 1) {   // this warpgroup's last tile of the piece, if it has one
           const int last = pc.n - 1 - (int)((done + pc.n - 1 + wg) & 1);
-          if (ok && last >= 0) ok = tr_wait(o_done + 8 * wg, ((done + last) >> 1) & 1, abort_flag, p.err);
+          if (ok && last >= 0) ok = tr_wait(p, o_done + 8 * wg, ((done + last) >> 1) & 1, abort_flag);
         } else if (ok) {
-          ok = tr_wait(o_done + 8 * wg, piece & 1, abort_flag, p.err);
+          ok = tr_wait(p, o_done + 8 * wg, piece & 1, abort_flag);
         }
         tcgen05_after_sync();
       }
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         fa = fast_exp2(a.x - m), fb = fast_exp2(z.x - m);
         l = a.y * fa + z.y * fb;
       }
-      if (live && ok && !*abort_flag) {
+      if (ok && !*abort_flag) {
         const bool whole = pc.n == pc.all;
         if (whole) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -432,14 +432,14 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     // ---------------- dequantisation
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DQ));
     const int dw = warp - SM_WARPS, u = dw & 3, half = (dw >> 2) & 1;
-    while (pc.next()) {
+    for (bool ok = true; ok && pc.next();) {
       const int L = clamped_len(p, pc.b);
       if (dw < 8)
-        dequant_piece<MODE, VQKV_ROLE_K, PAGED, TOK, G::STAGES>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::K_OFF,
-                                                                s_ready, k_empty, u, half, lane, abort_flag);
+        ok = dequant_piece<MODE, VQKV_ROLE_K, PAGED, TOK, G::STAGES>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::K_OFF,
+                                                                     s_ready, k_empty, u, half, lane, abort_flag);
       else
-        dequant_piece<MODE, VQKV_ROLE_V, PAGED, TOK, G::STAGES>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::V_OFF,
-                                                                pv_ready, v_empty, u, half, lane, abort_flag);
+        ok = dequant_piece<MODE, VQKV_ROLE_V, PAGED, TOK, G::STAGES>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::V_OFF,
+                                                                     pv_ready, v_empty, u, half, lane, abort_flag);
       done += pc.n;
     }
   } else {
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
       if (NQ == 1 && job == 0) {
         for (int t = 0; ok && t < n; ++t) {
           const uint32_t k = done + t, st = k % ST;
-          if (!(ok = tr_wait(s_ready + 8 * st, (k / ST) & 1, abort_flag, p.err))) break;
+          if (!(ok = tr_wait(p, s_ready + 8 * st, (k / ST) & 1, abort_flag))) break;
           tcgen05_after_sync();
           if (issuer) {
             scores(st, k & 1, 0);
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
       } else if (NQ == 1 && job == 1) {
         for (int t = 0; ok && t < n; ++t) {
           const uint32_t k = done + t, st = k % ST;
-          if (!(ok = tr_wait(pv_ready + 8 * st, (k / ST) & 1, abort_flag, p.err))) break;
+          if (!(ok = tr_wait(p, pv_ready + 8 * st, (k / ST) & 1, abort_flag))) break;
           tcgen05_after_sync();
           if (issuer) {
             values(st, k & 1, t < 2);
@@ -509,8 +509,8 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           const uint32_t k = done + t;
           if (t > 0) {
             const uint32_t j = k - 1, st = j % ST;
-            ok = tr_wait(pv_ready + 8 * st, (j / ST) & 1, abort_flag, p.err) &&
-                 tr_wait(p_ready + 8 * job, j & 1, abort_flag, p.err);
+            ok = tr_wait(p, pv_ready + 8 * st, (j / ST) & 1, abort_flag) &&
+                 tr_wait(p, p_ready + 8 * job, j & 1, abort_flag);
             if (!ok) break;
             tcgen05_after_sync();
             if (issuer) {
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           }
           if (t < n) {
             const uint32_t st = k % ST;
-            if (!(ok = tr_wait(s_ready + 8 * st, (k / ST) & 1, abort_flag, p.err))) break;
+            if (!(ok = tr_wait(p, s_ready + 8 * st, (k / ST) & 1, abort_flag))) break;
             tcgen05_after_sync();
             if (issuer) {
               scores(st, job, job);
@@ -534,12 +534,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
       }
       done += n;
     }
-    if (warp < MMA_WARP + 2) {   // every product issued has completed before the tensor memory is freed
-      const uint32_t mine = all_done + 8 * (warp - MMA_WARP);
-      if (issuer) umma_commit(mine);
-      __syncwarp();
-      tr_wait(mine, 0, abort_flag, p.err);
-    }
+    if (warp < MMA_WARP + 2) drain_products(p, issuer, all_done + 8 * (warp - MMA_WARP));
   }
   __syncwarp();
   tcgen05_before_sync();

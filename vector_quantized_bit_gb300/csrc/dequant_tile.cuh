@@ -15,8 +15,6 @@
 namespace vqkv {
 namespace {
 
-constexpr uint32_t kMaxPolls = 1u << 20;
-
 // Shared memory of a kernel that splits its registers between warpgroups
 // (setmaxnreg), after checking that the launch's registers cover the split: one
 // that does not would wait forever.
@@ -313,10 +311,12 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // Bounded wait by a whole warp: false, with the abort flag and the device
-// error bit set, when it runs out or another role gave up.
-__device__ __forceinline__ bool tr_wait_long(uint32_t mbar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+// error bit set, when it runs out or another role gave up.  A warp that gave up
+// waits for nothing more, in later pieces either: a wait's parity only tells
+// neighbouring phases apart.
+__device__ __forceinline__ bool tr_wait_long(const DecodeParams& p, uint32_t mbar, uint32_t parity, volatile int* abort_flag) {
   bool ok = false;
-  for (uint32_t i = 0; i < kMaxPolls; ++i) {
+  for (uint32_t i = 0; i < p.max_polls; ++i) {
     if (mbar_try_wait(mbar, parity)) {
       ok = true;
       break;
@@ -326,13 +326,24 @@ __device__ __forceinline__ bool tr_wait_long(uint32_t mbar, uint32_t parity, vol
   ok = __all_sync(0xffffffffu, ok);
   if (!ok && !*abort_flag) {
     *abort_flag = 1;
-    atomicOr(err, VQKV_DEVERR_TIMEOUT);
+    atomicOr(p.err, VQKV_DEVERR_TIMEOUT);
   }
   return ok;
 }
-__device__ __forceinline__ bool tr_wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+__device__ __forceinline__ bool tr_wait(const DecodeParams& p, uint32_t mbar, uint32_t parity, volatile int* abort_flag) {
   if (__all_sync(0xffffffffu, mbar_try_wait(mbar, parity))) return true;
-  return tr_wait_long(mbar, parity, abort_flag, err);
+  return tr_wait_long(p, mbar, parity, abort_flag);
+}
+
+// Waits for every product that the issuing warp (lane `issuer`) started, before
+// the tiles and the tensor memory they use are given back: bounded by itself,
+// whether or not a wait gave up.
+__device__ __forceinline__ void drain_products(const DecodeParams& p, bool issuer, uint32_t mbar) {
+  if (issuer) umma_commit(mbar);
+  __syncwarp();
+  bool ok = false;
+  for (uint32_t i = 0; i < kTilePolls && !ok; ++i) ok = __all_sync(0xffffffffu, mbar_try_wait(mbar, 0));
+  if (!ok) atomicOr(p.err, VQKV_DEVERR_TIMEOUT);
 }
 
 // The dequantising warp of (role, 16-token group u of each tile) over every
@@ -341,9 +352,9 @@ __device__ __forceinline__ bool tr_wait(uint32_t mbar, uint32_t parity, volatile
 // tiles of earlier pieces; tile k goes to stage k % STAGES of `ring`).  Codes are
 // loaded PREFETCH of its tiles ahead into registers, block ids one further.
 // These warps meet the others only through the ring's barriers, so they run
-// ahead into the next piece while the others finish one.
+// ahead into the next piece while the others finish one.  False: a wait gave up.
 template <int MODE, int ROLE, bool PAGED, int TOK, int STAGES>
-__device__ __forceinline__ void dequant_piece(const DecodeParams& p, int b, int kvh, int tile0, int n, int L, uint32_t done,
+__device__ __forceinline__ bool dequant_piece(const DecodeParams& p, int b, int kvh, int tile0, int n, int L, uint32_t done,
                                               const unsigned char* s_cb, unsigned char* ring, uint32_t full, uint32_t empty,
                                               int u, int half, int lane, volatile int* abort_flag) {
   using G = CodeGeo<MODE>;
@@ -387,7 +398,7 @@ __device__ __forceinline__ void dequant_piece(const DecodeParams& p, int b, int 
         gather_v<MODE>(s_cb, lane, w[d], c);
       fetch(next, w[d]);
       next = place(t + 2 * PREFETCH + 2);
-      if (!tr_wait(empty + 8 * st, ((k / STAGES) & 1) ^ 1, abort_flag, p.err)) return;
+      if (!tr_wait(p, empty + 8 * st, ((k / STAGES) & 1) ^ 1, abort_flag)) return false;
       unsigned char* tile = ring + st * (TOK * 256);
       if constexpr (ROLE == VQKV_ROLE_K)
         put_k<MODE, TOK>(tile, u, lane, c);
@@ -399,6 +410,7 @@ __device__ __forceinline__ void dequant_piece(const DecodeParams& p, int b, int 
     }
   }
   if (PAGED && bad && lane == 0) atomicOr(p.err, VQKV_DEVERR_BLOCK);
+  return true;
 }
 
 // A CTA's pieces: the overlaps of its share with the sequences, in order.

@@ -50,6 +50,10 @@ struct DecodeParams {
   // timeout test withholds every warp's first bulk copy so its waits run out.
   unsigned max_polls = 1u << 22;
   int withhold_first_copy = 0;
+  // The same of the tile kernels (decode_tree.cu, mass_tiles.cu), whose limit is
+  // kTilePolls: their timeout tests give one ring stage's barrier (-1: none) an
+  // arrival that never comes, in the attention or in the key pass.
+  int withhold_stage = -1, withhold_key_stage = -1;
   // Attention weights (vqkv_decode_attn_mass), else unused: scores (log2
   // domain, masked ones -inf) as [B][Hkv][cgroups][score_row tokens][4
   // columns], and each column's final (max, 1 / sum) as [B][Hkv][ncols].
@@ -61,6 +65,7 @@ struct DecodeParams {
 
 constexpr int kPartialStride = 132;  // O[128], m, l, pad (rows 16-byte aligned)
 constexpr int kFlatMaxB = 1024;      // largest batch the flat plan takes
+constexpr unsigned kTilePolls = 1u << 20;   // polls before a wait of a tile kernel gives up
 
 struct EncodeParams {
   const __half* x;          // [B][Hkv][n_rows][128]

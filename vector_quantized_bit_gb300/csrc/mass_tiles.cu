@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
   int* s_lim = reinterpret_cast<int*>(smem + COL_OFF + MAX_COLS * 8);
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(k_full + 8 * i, 8);
+      mbar_init(k_full + 8 * i, 8 + (i == p.withhold_key_stage));
       mbar_init(k_empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
     // ---------------- epilogue: warpgroup wg takes every other tile, thread = token
     const int wg = warp >> 2, row = threadIdx.x & 127;
     const uint32_t t_d = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * wg;
+    bool ok = true;   // no wait has given up
     while (pc.next()) {
       const int L = clamped_len(p, pc.b);
       const size_t pair = (size_t)pc.b * p.Hkv + kvh;
@@ -147,12 +148,11 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
       fence_proxy_async_smem();   // q' is read by the tensor cores
       named_barrier_sync(1, MEET);
       float* mass = p.mass + pair * p.cap_len;
-      bool ok = true;
-      for (int t = (int)((done + wg) & 1); t < pc.n; t += 2) {
+      for (int t = (int)((done + wg) & 1); ok && t < pc.n; t += 2) {
         const int tok0 = (pc.tile0 + t) * TOK, tok = tok0 + row;
         float old = 0.f;
         if (tok < L) old = mass[tok];
-        if (!(ok = tr_wait(d_full + 8 * wg, ((done + t) >> 1) & 1, abort_flag, p.err))) break;
+        if (!(ok = tr_wait(p, d_full + 8 * wg, ((done + t) >> 1) & 1, abort_flag))) break;
         tcgen05_after_sync();
         const bool tail = tok0 + TOK > L - p.M + 1;   // some token is hidden from some column
         float w = 0.f;
@@ -182,9 +182,10 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
     // ---------------- dequantisation of the keys
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DQ));
     const int dw = warp - EP_WARPS;
-    while (pc.next()) {
-      dequant_piece<MODE, VQKV_ROLE_K, PAGED, TOK, STAGES>(p, pc.b, kvh, pc.tile0, pc.n, clamped_len(p, pc.b), done, smem,
-                                                          smem + K_OFF, k_full, k_empty, dw & 7, dw >> 3, lane, abort_flag);
+    for (bool ok = true; ok && pc.next();) {
+      ok = dequant_piece<MODE, VQKV_ROLE_K, PAGED, TOK, STAGES>(p, pc.b, kvh, pc.tile0, pc.n, clamped_len(p, pc.b), done, smem,
+                                                               smem + K_OFF, k_full, k_empty, dw & 7, dw >> 3, lane,
+                                                               abort_flag);
       done += pc.n;
     }
   } else {
@@ -200,8 +201,8 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
       named_barrier_sync(1, MEET);
       for (int t = 0; ok && t < pc.n; ++t) {
         const uint32_t k = done + t, st = k % STAGES, wg = k & 1;
-        ok = tr_wait(k_full + 8 * st, (k / STAGES) & 1, abort_flag, p.err) &&
-             tr_wait(d_empty + 8 * wg, ((k >> 1) & 1) ^ 1, abort_flag, p.err);
+        ok = tr_wait(p, k_full + 8 * st, (k / STAGES) & 1, abort_flag) &&
+             tr_wait(p, d_empty + 8 * wg, ((k >> 1) & 1) ^ 1, abort_flag);
         if (!ok) break;
         tcgen05_after_sync();
         if (issuer) {
@@ -217,11 +218,7 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
       done += pc.n;
       named_barrier_sync(1, MEET);
     }
-    if (warp == MMA_WARP) {   // every product issued has completed before the tensor memory is freed
-      if (issuer) umma_commit(all_done);
-      __syncwarp();
-      tr_wait(all_done, 0, abort_flag, p.err);
-    }
+    if (warp == MMA_WARP) drain_products(p, issuer, all_done);
   }
   __syncwarp();
   tcgen05_before_sync();
