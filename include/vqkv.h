@@ -366,6 +366,12 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* args, const vqkv_
  * summed by one thread in a fixed order: the result does not depend on
  * scheduling.
  *
+ * mass is a running sum that a repeated call would not put right, so nothing is
+ * added to it while VQKV_DEVERR_TIMEOUT is set in the workspace's error word:
+ * not by the call whose attention timed out, and not by later ones until the
+ * caller clears the word.  Where the pass that adds the weights itself times
+ * out, each entry has the call's weight or is as it was before.
+ *
  * M * (Hq / Hkv) <= 64.  paging as in vqkv_decode_attn_tree (mass is indexed
  * by logical position).  The workspace (vqkv_decode_mass_workspace_bytes) holds,
  * up to 12 or 16 columns M * (Hq / Hkv), the call's scores too (16 bytes per
@@ -548,10 +554,11 @@ vqkv_status vqkv_test_decode_ring_timeout(const vqkv_decode_args* args, uint32_t
  * max_polls polls (1..4096), and stage 0 or 1 of each CTA's ring of key tiles
  * waits for an arrival that nothing makes, so the tiles from that one on are
  * not computed.  vqkv_test_decode_tree_timeout runs vqkv_decode_attn_tree on a
- * contiguous cache.  vqkv_test_decode_mass_timeout runs vqkv_decode_attn_mass
- * of so many columns that the tile kernels take it (else VQKV_ERR_UNSUPPORTED);
+ * contiguous cache.  vqkv_test_decode_mass_timeout runs vqkv_decode_attn_mass;
  * the stage is that of the attention, or of the pass over the keys after it
- * (key_pass != 0).  NULL args: VQKV_ERR_INVALID_ARG.
+ * (key_pass != 0).  Where few columns take the single-query decode's kernel, it
+ * withholds that ring's first copies instead (2 bit and key_pass 0 only, else
+ * VQKV_ERR_UNSUPPORTED).  NULL args: VQKV_ERR_INVALID_ARG.
  */
 vqkv_status vqkv_test_decode_tree_timeout(const vqkv_decode_tree_args* args, int32_t stage, uint32_t max_polls, void* stream);
 vqkv_status vqkv_test_decode_mass_timeout(const vqkv_decode_mass_args* args, int32_t key_pass, int32_t stage,

@@ -14,6 +14,7 @@ import pytest
 
 from tests import attn_reference as R
 from tests import helpers as H
+from tests.test_gpu_mass import causal
 from tests.test_gpu_tree import case, tree_masks, visible_of
 from vector_quantized_bit_gb300 import _build, _lib
 
@@ -62,3 +63,67 @@ def test_tree_waits_run_out_and_are_reported(mode, Hq, Hkv, M, num_splits, stage
     assert flags(ws) == 0
     ref, _, tol = R.attend(q, kc, vc, kcb, vcb, s, LENS, visible_of(masks, M))
     R.check_output(out.cpu().numpy(), ref, tol)
+
+
+def mass_call(mode, Hq, Hkv, M, num_splits, key_pass, stage, polls, seed):
+    """The hooked call, then an ordinary one before and one after the error word is cleared: the weights before all,
+    after each of the three, the reference's, and the last call's O with its reference and bound."""
+    t = H.torch()
+    B = len(LENS)
+    r, q, kc, vc, s, kcb, vcb = case(mode, B, Hq, Hkv, M, CAP, seed=seed)
+    before = r.random((B, Hkv, CAP), dtype=np.float32)
+    k, v = (H.dev(H.pack_cache_role(mode, role, c, CAP)) for role, c in ((0, kc), (1, vc)))
+    dq, dl, dk, dv, ds = (H.dev(x) for x in (q, np.array(LENS, dtype=np.int32), kcb, vcb, s))
+    out = t.zeros((B, M, Hq, 128), dtype=t.float16, device="cuda")
+    mass = H.dev(before)
+    ws = _lib.decode_mass_workspace(mode, B, Hq, Hkv, M, CAP, CAP, num_splits)
+    a = _lib.DecodeMassArgs(decode=_lib.decode_args(mode, dq.view(B, M * Hq, 128), k, v, dl, dk, dv, ds, out, ws, CAP, CAP,
+                                                    num_splits=num_splits), n_queries=M, mass=mass.data_ptr())
+    a.decode.Hq = Hq
+    seen = []
+    for hooked in (True, False, False):
+        if hooked:
+            assert _lib.lib().vqkv_test_decode_mass_timeout(ctypes.byref(a), key_pass, stage, polls, None) == 0
+        else:
+            _lib.vqkv_decode_attn_mass(mode, dq, k, v, dl, dk, dv, ds, out, mass, ws, CAP, CAP, num_splits=num_splits)
+        t.cuda.synchronize()
+        assert flags(ws) == (_lib.VQKV_DEVERR_TIMEOUT if len(seen) < 2 else 0)
+        if len(seen) == 1:
+            ws[:4] = 0
+        seen.append(mass.cpu().numpy())
+    ref, w, tol = R.attend(q, kc, vc, kcb, vcb, s, LENS, causal(M))
+    R.check_output(out.cpu().numpy(), ref, tol)
+    return before, seen, w
+
+
+@pytest.mark.parametrize("mode,Hq,Hkv,M,num_splits,stage", [
+    (0, 8, 2, 9, 3, 0), (0, 8, 2, 9, 3, 1), (1, 8, 2, 4, 2, 1), (2, 8, 2, 9, 2, 0), (3, 4, 1, 16, 3, 1), (4, 8, 1, 3, 2, 0),
+    (0, 4, 1, 1, 0, 0), (0, 8, 2, 3, 3, 0),       # few columns: the ring's waits
+])
+def test_mass_is_left_alone_when_the_attention_times_out(mode, Hq, Hkv, M, num_splits, stage):
+    """Not by the call itself and not by the next one while the error word is set; once it is cleared, as ever."""
+    before, seen, w = mass_call(mode, Hq, Hkv, M, num_splits, 0, stage, 512, seed=80 + mode)
+    assert np.array_equal(seen[0], before) and np.array_equal(seen[1], before)
+    R.check_mass(seen[2], before, w, LENS, R.attend.score_size)
+
+
+@pytest.mark.parametrize("mode,Hq,Hkv,M,num_splits", [
+    (0, 8, 2, 9, 3), (1, 8, 2, 4, 2), (2, 8, 2, 9, 2), (3, 4, 1, 16, 3), (4, 8, 1, 3, 2),
+])
+@pytest.mark.parametrize("stage", [0, 1])
+def test_mass_of_a_timed_out_key_pass_is_whole_or_untouched(mode, Hq, Hkv, M, num_splits, stage):
+    """Stage 0: nothing is added.  Stage 1: at most each share's first tile of 128 tokens is."""
+    before, seen, w = mass_call(mode, Hq, Hkv, M, num_splits, 1, stage, 4096, seed=90 + mode)
+    assert np.array_equal(seen[1], seen[0])
+    added = seen[0] != before
+    if stage == 0:
+        assert not added.any()
+    assert added.sum() <= Hkv * num_splits * 128
+    whole = seen[2].astype(np.float64) - seen[0]        # the last call added every token's weight once
+    for b, L in enumerate(LENS):
+        for h in range(Hkv):
+            got = np.where(added[b, h, :L], seen[0][b, h, :L].astype(np.float64) - before[b, h, :L], w[b][h])
+            # two fp32 additions to values below 1 + M g round by 2^-24 of them each; the weights as in check_mass
+            tol = (2 * 2.0 ** -17 * R.attend.score_size + 2.0 ** -17) * w[b][h] + 2.0 ** -23 * (1 + w[b][h])
+            assert (np.abs(got - w[b][h]) <= tol).all()
+            assert (np.abs(whole[b, h, :L] - w[b][h]) <= 2 * tol).all()

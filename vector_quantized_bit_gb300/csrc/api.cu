@@ -731,7 +731,7 @@ vqkv_status mass_launch(const vqkv_decode_mass_args* am, const vqkv_paging* pg, 
   p.mass = am->mass;
   p.cap_len = a->cap_len;
   p.stats = reinterpret_cast<float2*>(ws + pl.stats_off);
-  if (test.polls > 0 && !pl.tiles) return VQKV_ERR_UNSUPPORTED;
+  if (test.polls > 0 && !pl.tiles && (a->mode != VQKV_MODE_VQ2 || test.key_stage >= 0)) return VQKV_ERR_UNSUPPORTED;
   if (pl.tiles) {
     p.max_polls = test.polls > 0 ? test.polls : kTilePolls;
     p.withhold_stage = test.stage;
@@ -750,6 +750,10 @@ vqkv_status mass_launch(const vqkv_decode_mass_args* am, const vqkv_paging* pg, 
   }
   p.tickets = reinterpret_cast<unsigned*>(ws + pl.d.tickets_off);
   p.partials = reinterpret_cast<float*>(ws + pl.d.partials_off);
+  if (test.polls > 0) {   // the ring's hook
+    p.max_polls = test.polls;
+    p.withhold_first_copy = 1;
+  }
   p.scores = reinterpret_cast<float*>(ws + pl.scores_off);
   p.score_row = pl.score_row;
   p.n_splits = pl.d.n_splits;

@@ -38,6 +38,12 @@ __device__ __forceinline__ int load_len(const DecodeParams& p, int b) {
   return L;
 }
 
+// Whether a wait of this or an earlier call on the workspace gave up and the
+// caller has not cleared the error word: running sums are then left alone.
+__device__ __forceinline__ bool timed_out(const DecodeParams& p) {
+  return (*p.err & VQKV_DEVERR_TIMEOUT) != 0;
+}
+
 // Online-softmax update for one tile.  sc = scores for tokens {gid, gid+8}
 // x heads {2tig, 2tig+1} (log2 domain).  Returns P packed for the P.V MMA.
 template <int NACC>

@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(MS_THREADS) decode_mass_kernel(const DecodePar
   const int kvh = blockIdx.y, b = blockIdx.z;
   grid_dependency_wait();
   grid_dependents_launch();
+  const bool skip = timed_out(p);   // scores or statistics may be missing; needed only at the end
   const int L = min(max(p.seq_lens[b], 0), p.max_seq_len);
   const int t0 = blockIdx.x * (MS_THREADS * MS_TOKENS) + threadIdx.x;
   if (t0 >= L) return;
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(MS_THREADS) decode_mass_kernel(const DecodePar
 #pragma unroll
   for (int i = 0; i < MS_TOKENS; ++i) {
     const int t = t0 + i * MS_THREADS;
-    if (t < L) mass[t] = old[i] + w[i];
+    if (t < L && !skip) mass[t] = old[i] + w[i];
   }
 }
 

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
   using namespace mt;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_skip;
   const int split = blockIdx.x, kvh = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bar = smem_u32(smem + BAR_OFF);
@@ -111,9 +111,11 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
   Pieces pc(s_pref, p.B, split, p.n_splits);
   grid_dependency_wait();
   grid_dependents_launch();
+  if (threadIdx.x == 0) s_skip = timed_out(p);   // one answer for all roles
   tcgen05_before_sync();
   __syncthreads();
   tcgen05_after_sync();
+  if (s_skip) pc.r1 = pc.r0;   // statistics may be missing: no weights are added
   const uint32_t tmem = s_tmem;
   uint32_t done = 0;   // tiles of earlier pieces
 
