@@ -206,7 +206,8 @@ typedef struct {
   int32_t num_splits;    /* CTAs per (sequence, KV head); 0 = planned automatically */
   void* workspace;       /* device, >= vqkv_decode_workspace_bytes(args), 256-byte aligned,
                             zero-filled before its first use; every completed call leaves
-                            it ready for the next.  Word 0 (uint32) is the device error
+                            it ready for the next of the same sizes (B, Hq, Hkv, max_seq_len,
+                            num_splits, n_queries; zero it before it serves others).  Word 0 (uint32) is the device error
                             word (VQKV_DEVERR_SEQ_LEN, VQKV_DEVERR_TIMEOUT; sticky, the
                             caller may clear it) */
   size_t workspace_bytes;
@@ -334,7 +335,10 @@ vqkv_status vqkv_decode_attn_paged(const vqkv_decode_args* args, const vqkv_pagi
  * M <= 64 with any group Hq / Hkv <= 8 (up to 512 softmax columns per KV
  * head).  paging: NULL for the contiguous cache, else the block pools of the
  * paged calls above.  The workspace holds
- * vqkv_decode_tree_workspace_bytes(args) bytes; everything else is as in
+ * vqkv_decode_tree_workspace_bytes(args) bytes.  The call leaves the workspace
+ * ready for further calls, and for vqkv_decode_attn, its _multi, _append and
+ * _paged forms of the same B and Hkv where it is large enough for them, too;
+ * zero it before it serves other sizes.  Everything else is as in
  * vqkv_decode_attn.  q' and the softmax weights are rounded to fp16 for the
  * tensor cores, sums and softmax statistics are fp32.
  */
@@ -377,7 +381,7 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* args, const vqkv_
  * up to 12 or 16 columns M * (Hq / Hkv), the call's scores too (16 bytes per
  * token and KV head for every 4 columns).  Like that of vqkv_decode_attn it is
  * ready for the next call of the same sizes and n_queries; zero it before it
- * serves others.
+ * serves others, another call's included.
  */
 typedef struct {
   vqkv_decode_args decode;    /* q, out: [B][n_queries][Hq][128] */

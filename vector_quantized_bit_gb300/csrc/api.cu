@@ -286,8 +286,12 @@ DecodeParams batch_part(const DecodeParams& p, int b0, int B) {
 // run as several launches of up to kFlatMaxB sequences.
 struct TreePlan {
   int n_splits = 1, cgroups = 1;
-  size_t partials_off = 0, ws_bytes = 0;   // error word, transformed queries, partials
+  size_t query_off = 0, partials_off = 0, ws_bytes = 0;   // transformed queries, partials
 };
+// Column groups of the decode calls, at most (64 columns in groups of 8).  The tree's
+// scratch begins behind the tickets of all of them, so that a serving loop's draft
+// and plain decode steps can share a workspace: it leaves the tickets zero.
+constexpr int kTicketGroups = 8;
 
 vqkv_status validate_tree_sizes(const vqkv_decode_tree_args* at) {
   if (at == nullptr) return VQKV_ERR_INVALID_ARG;
@@ -313,7 +317,8 @@ vqkv_status plan_tree(const vqkv_decode_tree_args* at, bool pairs, TreePlan* pl)
   const long long tiles = std::max<long long>(1, (long long)B * ((a->max_seq_len + 63) / 64));
   const long long want = a->num_splits > 0 ? std::min(a->num_splits, 1024) : di.sms / ((long long)a->Hkv * pl->cgroups);
   pl->n_splits = (int)std::max<long long>(1, std::min(want, tiles));
-  pl->partials_off = kWsHeader + round_up(decode_tree_query_bytes(B, a->Hkv, cols, pairs), 256);
+  pl->query_off = decode_ticket_region_bytes(a->B, a->Hkv * kTicketGroups);   // Hkv <= kMaxGridYZ
+  pl->partials_off = pl->query_off + round_up(decode_tree_query_bytes(B, a->Hkv, cols, pairs), 256);
   pl->ws_bytes = pl->partials_off;
   if (pl->n_splits > 1)
     pl->ws_bytes += sizeof(float) * (size_t)a->Hkv * (pl->n_splits + B - 1) * cols * kPartialStride;
@@ -742,7 +747,7 @@ vqkv_status mass_launch(const vqkv_decode_mass_args* am, const vqkv_paging* pg, 
     for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
       const DecodeParams c = batch_part(p, b0, a->B);
       cudaStream_t s = static_cast<cudaStream_t>(stream);
-      if (launch_decode_tree(a->mode, c, nullptr, true, ws + kWsHeader, s) != cudaSuccess ||
+      if (launch_decode_tree(a->mode, c, nullptr, true, ws + pl.t.query_off, s) != cudaSuccess ||
           launch_mass_tiles(a->mode, c, ws + pl.image_off, s) != cudaSuccess)
         return VQKV_ERR_CUDA;
     }
@@ -822,7 +827,7 @@ vqkv_status tree_launch(const vqkv_decode_tree_args* at, const vqkv_paging* pg, 
   const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(at->tree_mask);
   for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
     const DecodeParams c = batch_part(p, b0, a->B);
-    if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, false, ws + kWsHeader, static_cast<cudaStream_t>(stream)) !=
+    if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, false, ws + pl.query_off, static_cast<cudaStream_t>(stream)) !=
         cudaSuccess)
       return VQKV_ERR_CUDA;
   }
