@@ -16,8 +16,13 @@ constexpr size_t kWsHeader = 256;   // word 0: device error flags
 constexpr int kMaxGridYZ = 65535;   // CUDA's limit on gridDim.y and gridDim.z
 constexpr int kMaxTokens = 1 << 30; // longest row of the cache-editing calls (positions plus a stride stay in 32 bits)
 
+// Kernels that are prepared (attributes set, checks made) only when a call that
+// uses them is first planned, so that no other call loads them or fails with them.
+enum LazyKernels : int { kTreeKernels, kMassKernels, kMassTileKernels, kCompactKernels, kSelectKernels, kLazyKernels };
+
 struct DeviceInfo {
   bool ready = false;
+  bool prepared[kLazyKernels][kCodeModes] = {};
   int sms = 0;
   int decode_bpsm[kCodeModes + 1] = {};   // resident decode CTAs per SM: each code mode, then fp16
   int encode_bpsm[kCodeModes] = {};
@@ -36,10 +41,7 @@ vqkv_status device_info(DeviceInfo* out) {
   if (!d.ready) {
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return VQKV_ERR_NO_DEVICE;
     for (int m = 0; m < kCodeModes; ++m) {
-      if (decode_prepare(m) != cudaSuccess || encode_prepare(m) != cudaSuccess || decode_tree_prepare(m) != cudaSuccess ||
-          decode_mass_prepare(m) != cudaSuccess || mass_tiles_prepare(m) != cudaSuccess ||
-          compact_prepare(m, &d.compact_cluster[m]) != cudaSuccess)
-        return VQKV_ERR_CUDA;
+      if (decode_prepare(m) != cudaSuccess || encode_prepare(m) != cudaSuccess) return VQKV_ERR_CUDA;
       if (decode_occupancy(m, &d.decode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
       if (encode_occupancy(m, &d.encode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
       if (d.decode_bpsm[m] < 1) d.decode_bpsm[m] = 1;
@@ -48,9 +50,27 @@ vqkv_status device_info(DeviceInfo* out) {
     if (decode_fp16_prepare() != cudaSuccess || decode_fp16_occupancy(&d.decode_bpsm[kModeFp16]) != cudaSuccess)
       return VQKV_ERR_CUDA;
     if (d.decode_bpsm[kModeFp16] < 1) d.decode_bpsm[kModeFp16] = 1;
-    if (evict_select_prepare() != cudaSuccess) return VQKV_ERR_CUDA;
     d.ready = true;
   }
+  *out = d;
+  return VQKV_OK;
+}
+
+// device_info, and the kernels `what` of a mode ready to launch (kSelectKernels: mode 0).
+vqkv_status device_info(LazyKernels what, int mode, DeviceInfo* out) {
+  const vqkv_status st = device_info(out);
+  if (st != VQKV_OK || out->prepared[what][mode]) return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return VQKV_ERR_NO_DEVICE;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceInfo& d = g_dev[dev];
+  const cudaError_t e = what == kTreeKernels       ? decode_tree_prepare(mode)
+                        : what == kMassKernels     ? decode_mass_prepare(mode)
+                        : what == kMassTileKernels ? mass_tiles_prepare(mode)
+                        : what == kCompactKernels  ? compact_prepare(mode, &d.compact_cluster[mode])
+                                                   : evict_select_prepare();
+  if (e != cudaSuccess) return VQKV_ERR_CUDA;
+  d.prepared[what][mode] = true;
   *out = d;
   return VQKV_OK;
 }
@@ -306,10 +326,10 @@ vqkv_status validate_tree_sizes(const vqkv_decode_tree_args* at) {
 }
 
 vqkv_status plan_tree(const vqkv_decode_tree_args* at, bool pairs, TreePlan* pl) {
-  DeviceInfo di;
-  const vqkv_status st = device_info(&di);
-  if (st != VQKV_OK) return st;
   const vqkv_decode_args* a = &at->decode;
+  DeviceInfo di;
+  const vqkv_status st = device_info(kTreeKernels, a->mode, &di);
+  if (st != VQKV_OK) return st;
   const int cols = at->n_queries * (a->Hq / a->Hkv);
   pl->cgroups = (cols + decode_tree_cols(cols) - 1) / decode_tree_cols(cols);
   const int B = std::max(std::min(a->B, kFlatMaxB), 1);
@@ -362,7 +382,11 @@ vqkv_status validate_mass_sizes(const vqkv_decode_mass_args* am) {
 vqkv_status plan_mass(const vqkv_decode_mass_args* am, MassPlan* pl) {
   const vqkv_decode_args& a = am->decode;
   const int ncols = am->n_queries * (a.Hq / a.Hkv);
-  if (ncols > mass_few_cols(a.mode)) {
+  const bool tiles = ncols > mass_few_cols(a.mode);
+  DeviceInfo di;
+  const vqkv_status ready = device_info(tiles ? kMassTileKernels : kMassKernels, a.mode, &di);
+  if (ready != VQKV_OK) return ready;
+  if (tiles) {
     pl->tiles = true;
     vqkv_decode_tree_args at{};
     at.decode = a;
@@ -861,7 +885,7 @@ vqkv_status vqkv_evict_select(const vqkv_evict_select_args* a, void* stream) {
       !aligned(a->error_flags, 4))
     return VQKV_ERR_INVALID_ARG;
   DeviceInfo di;
-  const vqkv_status st = device_info(&di);
+  const vqkv_status st = device_info(kSelectKernels, 0, &di);
   if (st != VQKV_OK) return st;
   SelectParams p;
   p.mass = a->mass;
@@ -897,7 +921,7 @@ vqkv_status vqkv_cache_compact(const vqkv_cache_compact_args* a, const vqkv_pagi
     return VQKV_ERR_INVALID_ARG;
   if (a->n_src == 0 && a->mass == nullptr) return VQKV_OK;
   DeviceInfo di;
-  const vqkv_status st = device_info(&di);
+  const vqkv_status st = device_info(kCompactKernels, a->mode, &di);
   if (st != VQKV_OK) return st;
   CompactParams p;
   p.codes[VQKV_ROLE_K] = a->k_codes;
