@@ -443,7 +443,9 @@ vqkv_status vqkv_evict_select(const vqkv_evict_select_args* args, void* stream);
  * start outside [0, cap_len] sets VQKV_DEVERR_POSITION and changes nothing of
  * that sequence.  Blocks of a paged cache that several sequences share must not
  * be moved into; a table entry outside [0, num_blocks) is not dereferenced:
- * its tokens stay as they are and VQKV_DEVERR_BLOCK is set.
+ * tokens of that block, and tokens whose source lies in it, keep their codes and
+ * their mass, and VQKV_DEVERR_BLOCK is set.  (The mass behind the last moved
+ * token becomes 0 all the same.)
  */
 typedef struct {
   int32_t mode;               /* vqkv_mode */

@@ -334,8 +334,15 @@ __device__ __forceinline__ void move_codes(const CompactParams& p, const Move& m
   }
 }
 
+// Whether the table entry of the block that holds token t is one of the pool's.
+template <int TT>
+__device__ __forceinline__ bool block_held(const CompactParams& p, int b, int t) {
+  return (unsigned)__ldg(p.block_table + (size_t)b * p.max_blocks + ((t / TT) >> p.block_shift)) < (unsigned)p.num_blocks;
+}
+
+template <int MODE, bool PAGED>
 __device__ __forceinline__ void move_mass(const CompactParams& p, const Move& mv, int rank, int cluster) {
-  constexpr int U = 8;
+  constexpr int U = 8, TT = MODE == VQKV_MODE_VQ15 ? 64 : 16;
   float* row = p.mass + ((size_t)mv.b * p.Hkv + mv.kvh) * p.cap_len;
   const int per = cluster * CP_THREADS * U;
   const int rounds = (mv.n + per - 1) / per;
@@ -346,6 +353,8 @@ __device__ __forceinline__ void move_mass(const CompactParams& p, const Move& mv
     for (int u = 0; u < U; ++u) {
       const int i = k * per + (rank * U + u) * CP_THREADS + (int)threadIdx.x;
       s[u] = i < mv.n ? mv.source(p, mv.start + i, false) : -1;
+      // a weight goes where its token's codes go: not into or out of a block that is not there
+      if (PAGED && i < mv.n && !(block_held<TT>(p, mv.b, mv.start + i) && block_held<TT>(p, mv.b, s[u]))) s[u] = mv.start + i;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(CP_THREADS, 2) compact_kernel(const CompactPar
   else if (stream == 1)
     move_codes<MODE, VQKV_ROLE_V, PAGED>(p, mv, blockIdx.x, gridDim.x);
   else
-    move_mass(p, mv, blockIdx.x, gridDim.x);
+    move_mass<MODE, PAGED>(p, mv, blockIdx.x, gridDim.x);
 }
 
 // ------------------------------------------------------------------ selection
