@@ -415,7 +415,7 @@ typedef struct {
   const float* mass;          /* device fp32 [B][Hkv][cap_len] */
   const int32_t* seq_lens;    /* device [B] */
   int32_t* keep;              /* device int32 [B][Hkv][n_keep] out */
-  int32_t* keep_lens;         /* device int32 [B] out */
+  int32_t* keep_lens;         /* device int32 [B] out; must not overlap seq_lens */
   uint32_t* error_flags;      /* device, optional: VQKV_DEVERR_SEQ_LEN */
 } vqkv_evict_select_args;
 

@@ -542,7 +542,7 @@ def vqkv_evict_select(mass, seq_lens, keep, keep_lens, n_sink=0, n_recent=0, max
 
     mass fp32 [B][Hkv][cap_len]; seq_lens int32 [B]; writes keep int32
     [B][Hkv][n_keep] (ascending; only the first keep_lens[b] entries of a row)
-    and keep_lens int32 [B].  Always kept: the first n_sink and the last
+    and keep_lens int32 [B] (not seq_lens itself).  Always kept: the first n_sink and the last
     n_recent tokens; then those of the largest mass, ties to the lowest position.
     error_flags: int32 [1], optional (VQKV_DEVERR_* bits are or-ed in).
     """

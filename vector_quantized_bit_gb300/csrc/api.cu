@@ -80,6 +80,10 @@ bool is_code_mode(int m) {
          m == VQKV_MODE_VQ125;
 }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < a_bytes : x - y < b_bytes;
+}
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Sizes only (what the split plan and the workspace size depend on).
@@ -884,6 +888,8 @@ vqkv_status vqkv_evict_select(const vqkv_evict_select_args* a, void* stream) {
   if (!aligned(a->mass, 4) || !aligned(a->seq_lens, 4) || !aligned(a->keep, 4) || !aligned(a->keep_lens, 4) ||
       !aligned(a->error_flags, 4))
     return VQKV_ERR_INVALID_ARG;
+  // the lengths are read by every CTA of a sequence, the kept ones written by the first
+  if (overlap(a->keep_lens, 4 * (size_t)a->B, a->seq_lens, 4 * (size_t)a->B)) return VQKV_ERR_INVALID_ARG;
   DeviceInfo di;
   const vqkv_status st = device_info(kSelectKernels, 0, &di);
   if (st != VQKV_OK) return st;
