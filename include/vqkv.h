@@ -211,7 +211,7 @@ typedef struct {
                             word (VQKV_DEVERR_SEQ_LEN, VQKV_DEVERR_TIMEOUT; sticky, the
                             caller may clear it) */
   size_t workspace_bytes;
-  uint16_t* out;         /* device fp16 [B][Hq][128] */
+  uint16_t* out;         /* device fp16 [B][Hq][128]; may be q */
 } vqkv_decode_args;
 
 /* Bytes of one cache stream (one of K or V of one (sequence, KV head)):
@@ -361,7 +361,8 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* args, const vqkv_
  *
  * decode.q / decode.out are fp16 [B][M][Hq][128]; O is what
  * vqkv_decode_attn_multi returns for the same arguments (M = 1: what
- * vqkv_decode_attn returns), up to rounding.  In addition, for every
+ * vqkv_decode_attn returns), up to rounding; as there, out may be q's own
+ * buffer.  In addition, for every
  * sequence b, KV head h and t < L,
  *     mass[b][h][t] += sum over the M queries and the Hq / Hkv query heads
  *                      of KV head h of softmax(score)_t.

@@ -775,7 +775,8 @@ vqkv_status mass_launch(const vqkv_decode_mass_args* am, const vqkv_paging* pg, 
     for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
       const DecodeParams c = batch_part(p, b0, a->B);
       cudaStream_t s = static_cast<cudaStream_t>(stream);
-      if (launch_decode_tree(a->mode, c, nullptr, true, ws + pl.t.query_off, s) != cudaSuccess ||
+      if (launch_mass_queries(c, ws + pl.image_off, s) != cudaSuccess ||
+          launch_decode_tree(a->mode, c, nullptr, true, ws + pl.t.query_off, s) != cudaSuccess ||
           launch_mass_tiles(a->mode, c, ws + pl.image_off, s) != cudaSuccess)
         return VQKV_ERR_CUDA;
     }

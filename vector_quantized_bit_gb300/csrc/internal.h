@@ -125,12 +125,14 @@ size_t decode_tree_query_bytes(int B, int Hkv, int ncols, bool pairs);
 cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, bool pairs, void* qx,
                                cudaStream_t stream);
 
-// Attention weights of many columns (mass_tiles.cu), after launch_decode_tree has
-// left the columns' max and 1 / sum in p.stats; B <= kFlatMaxB, at most 64
-// columns.  image: scratch for the transformed queries.
+// Attention weights of many columns (mass_tiles.cu); B <= kFlatMaxB, at most 64
+// columns.  image: scratch for the transformed queries, which are taken before
+// launch_decode_tree (whose output may be the queries' own buffer); the weights
+// follow it, with the columns' max and 1 / sum that it leaves in p.stats.
 cudaError_t mass_tiles_prepare(int mode);
 size_t mass_tiles_image_bytes(int B, int Hkv, int ncols);
-cudaError_t launch_mass_tiles(int mode, const DecodeParams& p, void* image, cudaStream_t stream);
+cudaError_t launch_mass_queries(const DecodeParams& p, void* image, cudaStream_t stream);
+cudaError_t launch_mass_tiles(int mode, const DecodeParams& p, const void* image, cudaStream_t stream);
 
 // Cache editing (cache_edit.cu): the in-place move of chosen tokens, and the
 // choice of the tokens a sequence keeps.

@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(mt::THREADS, 1) mass_tile_kernel(const DecodeP
     mbar_init_fence();
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(&s_tmem), T_COLS);
-  // codebooks and lengths are inputs that no kernel of this call writes, and
-  // the kernel before started only when everything before it had completed
+  // codebooks and lengths are inputs that no kernel of this call writes, and the
+  // attention's last kernel started only when everything before the call had completed
   fill_codebooks<MODE, THREADS, false>(p, kvh, smem);
   flat_prefix<TOK / 16>(p, s_pref);
   Pieces pc(s_pref, p.B, split, p.n_splits);
@@ -256,16 +256,16 @@ cudaError_t mass_tiles_prepare(int mode) {
 
 size_t mass_tiles_image_bytes(int B, int Hkv, int ncols) { return (size_t)B * Hkv * 2 * (ncols <= 32 ? 32 : 64) * 256; }
 
-cudaError_t launch_mass_tiles(int mode, const DecodeParams& p, void* image, cudaStream_t stream) {
+cudaError_t launch_mass_queries(const DecodeParams& p, void* image, cudaStream_t stream) {
   const bool wide = p.ncols > 32;
+  const dim3 grid(wide ? 2 : 1, p.Hkv, p.B);
   unsigned char* img = static_cast<unsigned char*>(image);
-  const dim3 qgrid(wide ? 2 : 1, p.Hkv, p.B);
-  cudaError_t e = wide ? launch_pdl(mass_query_kernel<64>, qgrid, dim3(128), 0, stream, p, img)
-                       : launch_pdl(mass_query_kernel<32>, qgrid, dim3(128), 0, stream, p, img);
-  if (e == cudaSuccess)
-    e = launch_pdl(tile_kernel(mode, p.block_table != nullptr, wide), dim3(p.n_splits, p.Hkv), dim3(mt::THREADS),
-                   (size_t)mt::SMEM, stream, p, (const unsigned char*)img);
-  return e;
+  return launch_pdl(wide ? mass_query_kernel<64> : mass_query_kernel<32>, grid, dim3(128), 0, stream, p, img);
+}
+
+cudaError_t launch_mass_tiles(int mode, const DecodeParams& p, const void* image, cudaStream_t stream) {
+  return launch_pdl(tile_kernel(mode, p.block_table != nullptr, p.ncols > 32), dim3(p.n_splits, p.Hkv), dim3(mt::THREADS),
+                    (size_t)mt::SMEM, stream, p, static_cast<const unsigned char*>(image));
 }
 
 }  // namespace vqkv
