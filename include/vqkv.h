@@ -366,8 +366,10 @@ vqkv_status vqkv_decode_attn_tree(const vqkv_decode_tree_args* args, const vqkv_
  * sequence b, KV head h and t < L,
  *     mass[b][h][t] += sum over the M queries and the Hq / Hkv query heads
  *                      of KV head h of softmax(score)_t.
- * Entries t >= L are not touched.  The scores are computed from q' split into
- * two fp16 parts, so the added weights carry fp32 accuracy.  Each entry is
+ * Entries t >= L are not touched.  The scores (in the log2 domain: q' carries
+ * softmax_scale * log2 e) are computed from q' split into two fp16 parts, whose
+ * sum is off by at most max(2^-22 |q'_c|, 2^-25) in channel c, the half step of
+ * fp16's smallest numbers; sums and softmax statistics are fp32.  Each entry is
  * summed by one thread in a fixed order: the result does not depend on
  * scheduling.
  *

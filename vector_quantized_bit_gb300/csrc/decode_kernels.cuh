@@ -148,9 +148,10 @@ __device__ __forceinline__ void transform_queries(const DecodeParams& p, int b, 
 }
 
 // Attention weights: a CTA's 4 columns are computed from q' in two fp16 parts,
-// q' = hi + lo up to 2^-22 relative, hi in MMA columns 0..3 and lo in columns
-// 4..7 of the same product.  One part alone would put an error of 2^-12 of
-// the score into weights that are summed in fp32.
+// q' = hi + lo up to max(2^-22 |q'|, 2^-25) (lo is subnormal, in steps of 2^-24,
+// where |q'| < 2^-3), hi in MMA columns 0..3 and lo in columns 4..7 of the same
+// product.  One part alone would put an error of 2^-12 of the score into weights
+// that are summed in fp32.
 __device__ __forceinline__ uint32_t pack_part(float a, float b, bool low) {
   const __half2 h = __floats2half2_rn(a, b);
   if (!low) return *reinterpret_cast<const uint32_t*>(&h);

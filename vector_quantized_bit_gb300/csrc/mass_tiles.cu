@@ -8,9 +8,10 @@
 // alone follows:
 //   mass_t += sum_c exp2(s_tc - m_c) / l_c
 // It recomputes the scores S = K' [Q'hi Q'lo]^T (128 tokens x 2 columns x 128
-// channels) with q' = hi + lo split into two fp16 parts, so that a score is
-// exact to 2^-22 of its terms and the sums carry fp32 accuracy.  A thread owns a
-// token (tensor-memory lane): the sum over columns is in one thread, in order.
+// channels) with q' = hi + lo split into two fp16 parts, off by at most
+// max(2^-22 |q'|, 2^-25) per channel: near what fp32 keeps of q' down to 2^-3, an
+// absolute 2^-25 below.  A thread owns a token (tensor-memory lane): the sum over
+// columns is in one thread, in order.
 // The alternative, storing the scores, would move 512 bytes per token and KV
 // head at 64 columns; the second pass moves its key codes (32 bytes at 2 bit).
 //
