@@ -354,11 +354,17 @@ vqkv_status plan_tree(const vqkv_decode_tree_args* at, bool pairs, TreePlan* pl)
 // Many: the draft-tree attention, then statistics and query images of the
 // key-only pass.  A group of 4 columns costs one decode, the other path about
 // the same for any number: at 196,608 tokens and 8 KV heads 12 / 16 columns take
-// 127 / 167 us at 2 bit, 151 / 199 at 4, 190 / 253 at 1.25 and 261, 240 (12 columns)
-// at 3 and 1.5 on the first path; 178, 258, 217, 260 and 250 on the second.  Short
-// sequences favour the first path further: 16 columns of 4,096 tokens 14 and 25 us
+// 127 / 169 us at 2 bit, 151 / 200 at 4, 190 / 252 at 1.25 and 261, 240 (12 columns)
+// at 3 and 1.5 on the first path; 181, 257, 213, 260 and 250 on the second.  At
+// 1.25 bit 16 columns cross where the work does: 37 and 39 us at 16,384 tokens, 63
+// and 55 at 32,768, 28 and 36 for 8 sequences of 1,000, 94 and 66 for 32.  Short
+// sequences favour the first path further: 16 columns of 4,096 tokens 14 and 26 us
 // at 2 bit.
-int mass_few_cols(int mode) { return mode == VQKV_MODE_VQ3 || mode == VQKV_MODE_VQ15 ? 12 : 16; }
+int mass_few_cols(const vqkv_decode_args& a) {
+  if (a.mode == VQKV_MODE_VQ3 || a.mode == VQKV_MODE_VQ15) return 12;
+  const bool much = (long long)a.B * a.Hkv * a.max_seq_len > 196608;
+  return a.mode == VQKV_MODE_VQ125 && much ? 12 : 16;
+}
 
 struct MassPlan {
   bool tiles = false;
@@ -377,8 +383,8 @@ vqkv_status validate_mass_sizes(const vqkv_decode_mass_args* am) {
   if (am->n_queries > 64 || am->n_queries * (a.Hq / a.Hkv) > 64) return VQKV_ERR_UNSUPPORTED;
   const int cols = am->n_queries * (a.Hq / a.Hkv);
   if (a.Hkv > kMaxGridYZ || a.cap_len > kMaxTokens) return VQKV_ERR_UNSUPPORTED;
-  if (cols <= mass_few_cols(a.mode) && (long long)a.B * ((cols + 3) / 4) > kMaxGridYZ) return VQKV_ERR_UNSUPPORTED;
-  if (cols > mass_few_cols(a.mode) && (long long)std::min(a.B, kFlatMaxB) * ((a.max_seq_len + 63) / 64) > kMaxTokens)
+  if (cols <= mass_few_cols(a) && (long long)a.B * ((cols + 3) / 4) > kMaxGridYZ) return VQKV_ERR_UNSUPPORTED;
+  if (cols > mass_few_cols(a) && (long long)std::min(a.B, kFlatMaxB) * ((a.max_seq_len + 63) / 64) > kMaxTokens)
     return VQKV_ERR_UNSUPPORTED;
   return VQKV_OK;
 }
@@ -386,7 +392,7 @@ vqkv_status validate_mass_sizes(const vqkv_decode_mass_args* am) {
 vqkv_status plan_mass(const vqkv_decode_mass_args* am, MassPlan* pl) {
   const vqkv_decode_args& a = am->decode;
   const int ncols = am->n_queries * (a.Hq / a.Hkv);
-  const bool tiles = ncols > mass_few_cols(a.mode);
+  const bool tiles = ncols > mass_few_cols(a);
   DeviceInfo di;
   const vqkv_status ready = device_info(tiles ? kMassTileKernels : kMassKernels, a.mode, &di);
   if (ready != VQKV_OK) return ready;
