@@ -340,7 +340,8 @@ vqkv_status vqkv_decode_attn_paged(const vqkv_decode_args* args, const vqkv_pagi
  * _paged forms of the same B and Hkv where it is large enough for them, too;
  * zero it before it serves other sizes.  Everything else is as in
  * vqkv_decode_attn.  q' and the softmax weights are rounded to fp16 for the
- * tensor cores, sums and softmax statistics are fp32.
+ * tensor cores (q' to two fp16 parts, as in vqkv_decode_attn_mass, in short
+ * calls of up to 64 columns), sums and softmax statistics are fp32.
  */
 typedef struct {
   vqkv_decode_args decode;    /* q, out: [B][n_queries][Hq][128]; num_splits: shares of the

@@ -310,6 +310,7 @@ DecodeParams batch_part(const DecodeParams& p, int b0, int B) {
 // run as several launches of up to kFlatMaxB sequences.
 struct TreePlan {
   int n_splits = 1, cgroups = 1;
+  bool pairs = false;   // scores of q' in two fp16 parts
   size_t query_off = 0, partials_off = 0, ws_bytes = 0;   // transformed queries, partials
 };
 // Column groups of the decode calls, at most (64 columns in groups of 8).  The tree's
@@ -329,7 +330,13 @@ vqkv_status validate_tree_sizes(const vqkv_decode_tree_args* at) {
   return VQKV_OK;
 }
 
-vqkv_status plan_tree(const vqkv_decode_tree_args* at, bool pairs, TreePlan* pl) {
+// weights: the plan of the attention weights, whose scores always take both parts
+// of q'.  A draft tree of up to 64 columns takes them while a share has two tiles at
+// most: such a call is bound by the host (15 us), and the parts cost 0.2 to 0.4 us of
+// 11 to 13 on the GPU (519 tokens, 32 columns: 10.7 and 11.0; 2,000 tokens, 64
+// columns: 13.3 and 13.7).  Long ones would pay for them in every tile (196,608
+// tokens, 64 columns: 96 and 126 us; 8 sequences of 500: 23 and 25).
+vqkv_status plan_tree(const vqkv_decode_tree_args* at, bool weights, TreePlan* pl) {
   const vqkv_decode_args* a = &at->decode;
   DeviceInfo di;
   const vqkv_status st = device_info(kTreeKernels, a->mode, &di);
@@ -341,8 +348,9 @@ vqkv_status plan_tree(const vqkv_decode_tree_args* at, bool pairs, TreePlan* pl)
   const long long tiles = std::max<long long>(1, (long long)B * ((a->max_seq_len + 63) / 64));
   const long long want = a->num_splits > 0 ? std::min(a->num_splits, 1024) : di.sms / ((long long)a->Hkv * pl->cgroups);
   pl->n_splits = (int)std::max<long long>(1, std::min(want, tiles));
+  pl->pairs = weights || (cols <= 64 && tiles <= 2 * pl->n_splits);
   pl->query_off = decode_ticket_region_bytes(a->B, a->Hkv * kTicketGroups);   // Hkv <= kMaxGridYZ
-  pl->partials_off = pl->query_off + round_up(decode_tree_query_bytes(B, a->Hkv, cols, pairs), 256);
+  pl->partials_off = pl->query_off + round_up(decode_tree_query_bytes(B, a->Hkv, cols, pl->pairs), 256);
   pl->ws_bytes = pl->partials_off;
   if (pl->n_splits > 1)
     pl->ws_bytes += sizeof(float) * (size_t)a->Hkv * (pl->n_splits + B - 1) * cols * kPartialStride;
@@ -862,7 +870,7 @@ vqkv_status tree_launch(const vqkv_decode_tree_args* at, const vqkv_paging* pg, 
   const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(at->tree_mask);
   for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB) {
     const DecodeParams c = batch_part(p, b0, a->B);
-    if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, false, ws + pl.query_off, static_cast<cudaStream_t>(stream)) !=
+    if (launch_decode_tree(a->mode, c, mask + (size_t)b0 * p.M, pl.pairs, ws + pl.query_off, static_cast<cudaStream_t>(stream)) !=
         cudaSuccess)
       return VQKV_ERR_CUDA;
   }

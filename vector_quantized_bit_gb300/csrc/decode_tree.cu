@@ -33,11 +33,12 @@
 // centroids are fp16 already, sums are fp32.
 //
 // PAIR (at most 64 columns; for the attention weights, whose softmax sums have to
-// match the key pass's scores): q' = hi + lo in two fp16 parts, off by at most
-// max(2^-22 |q'|, 2^-25) per channel.  The unused half of the MMA rows takes the
-// low parts, 16 columns to a warp: lanes 0..15 the high parts, lanes 16..31 the low
-// parts of the same columns, whose scores one shuffle adds; both lanes then carry
-// the column.  (Not for the plain tree: 64 shuffles more per thread and tile.)
+// match the key pass's scores, and for short trees, which the host bounds):
+// q' = hi + lo in two fp16 parts, off by at most max(2^-22 |q'|, 2^-25) per channel.
+// The unused half of the MMA rows takes the low parts, 16 columns to a warp: lanes
+// 0..15 the high parts, lanes 16..31 the low parts of the same columns, whose scores
+// one shuffle adds; both lanes then carry the column.  (Not for long trees: 64
+// shuffles more per thread and tile.)
 //
 // Measured: 64 columns over 196,608 tokens and 8 KV heads at 2 bit take 98 us for the
 // call (525 TFLOP/s of the two products; plain torch 11.4 ms).  A 64-token
