@@ -438,9 +438,12 @@ vqkv_status vqkv_evict_select(const vqkv_evict_select_args* args, void* stream);
  * copied the sources out first.  A source must satisfy d <= src <
  * seq_lens[b] (tokens only move up); one that does not leaves token d as it
  * is and sets VQKV_DEVERR_POSITION, as does a d at or past cap_len.  Sources
- * need not ascend and may repeat.  No other token's codes change.  Where mass
- * is given, entries start[b] + counts[b] <= t < seq_lens[b] become 0 (those
- * tokens are no longer held; a token appended there later starts at 0).
+ * need not ascend and may repeat.  No other token's codes change; but the groups
+ * of 16 tokens (from multiples of 16) that hold a moved token's new place are read
+ * and written back whole, so no other work may write into them at the same time
+ * (an append on another stream just behind the last moved token, for instance).
+ * Where mass is given, entries start[b] + counts[b] <= t < seq_lens[b] become 0
+ * (those tokens are no longer held; a token appended there later starts at 0).
  *
  * seq_lens is the length before the call (clamped to [0, cap_len], with
  * VQKV_DEVERR_SEQ_LEN); the length afterwards is start[b] + counts[b].  A

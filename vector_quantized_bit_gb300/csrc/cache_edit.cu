@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(CP_THREADS, 2) compact_kernel(const CompactPar
 // to 32,768 tokens: 30.8 us, 32.6 with 1024 threads; 512 rows of 8,192: 22 and
 // 30).  Bound there: a row takes 38,000 cycles beside another one, 10,000 of them
 // in step 1 (memory bandwidth), 9,000 each in steps 2 and 4 (issue), the rest
-// the digits' scans and barriers.  8 rows of 196,608 in clusters of 8: 20 us, of
+// the digits' scans and barriers; issue slots are busy 55 % of the whole time.  8 rows of 196,608 in clusters of 8: 20 us, of
 // which the exchange of step 1 and the remote reads of step 3 take 7.
 
 constexpr int SEL_TOP = 12;        // bits of the first digit; the others have 10

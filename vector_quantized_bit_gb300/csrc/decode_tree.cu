@@ -75,7 +75,9 @@ constexpr int THREADS = (MMA_WARP + 4) * 32;   // whole warpgroups, for the regi
 // Registers per thread: 72 at launch (896 threads), then 120 for the softmax
 // warpgroups (64 scores and 16 packed weights are live), 56 for the
 // dequantising ones (32 hold gathered centroids), 40 for the last:
-// 256 x 120 + 512 x 56 + 128 x 40 = 64,512 = 896 x 72.
+// 256 x 120 + 512 x 56 + 128 x 40 = 64,512 = 896 x 72.  Two sets of code words
+// beside the centroids do not fit in 56: 44 to 136 bytes per thread spill, 216 to
+// 384 at 4 bit.
 constexpr int REGS_SM = 120, REGS_DQ = 56, REGS_MMA = 40;
 constexpr int SPLIT_REGS = 32 * (SM_WARPS * REGS_SM + DQ_WARPS * REGS_DQ + 4 * REGS_MMA);
 constexpr int TILE_SMEM = TOK * 256;      // one dequantised K or V tile: two 64-channel halves of 64 x 128 bytes

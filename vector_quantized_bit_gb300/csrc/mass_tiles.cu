@@ -29,7 +29,8 @@ constexpr int TOK = 128;                   // tokens per tile (MMA rows)
 constexpr int EP_WARPS = 8, DQ_WARPS = 16; // two epilogue warpgroups; K groups of 16 tokens x 2 tiles in flight
 constexpr int MMA_WARP = EP_WARPS + DQ_WARPS;
 constexpr int THREADS = (MMA_WARP + 4) * 32;
-// As in the draft-tree attention: 256 x 120 + 512 x 56 + 128 x 40 = 896 x 72.
+// As in the draft-tree attention: 256 x 120 + 512 x 56 + 128 x 40 = 896 x 72.  The
+// dequantising warps spill 44 to 92 bytes per thread, 112 to 220 at 4 bit.
 constexpr int REGS_EP = 120, REGS_DQ = 56, REGS_MMA = 40;
 constexpr int SPLIT_REGS = 32 * (EP_WARPS * REGS_EP + DQ_WARPS * REGS_DQ + 4 * REGS_MMA);
 constexpr int STAGES = 3;
