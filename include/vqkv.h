@@ -117,9 +117,16 @@ typedef enum {
   VQKV_ROLE_V = 1      /* values: quantised as they are                   */
 } vqkv_role;
 
+/* Element types, in the calls that take one (dtype). */
+typedef enum {
+  VQKV_DTYPE_F16 = 0,
+  VQKV_DTYPE_F32 = 1,
+  VQKV_DTYPE_BF16 = 2
+} vqkv_dtype;
+
 /* Bits of the device error word (see error_flags / workspace word 0). */
 #define VQKV_DEVERR_SEQ_LEN   0x1u  /* a seq_lens[b] outside [0, max_seq_len]: clamped */
-#define VQKV_DEVERR_POSITION  0x2u  /* an encode row outside [0, cap_len): not written */
+#define VQKV_DEVERR_POSITION  0x2u  /* a cache or rotary position out of range: its row is not written */
 #define VQKV_DEVERR_TIMEOUT   0x4u  /* a bounded on-chip wait gave up: see below */
 #define VQKV_DEVERR_BLOCK     0x8u  /* a block-table entry outside [0, num_blocks) (paged calls) */
 /*
@@ -472,6 +479,141 @@ typedef struct {
 } vqkv_cache_compact_args;
 
 vqkv_status vqkv_cache_compact(const vqkv_cache_compact_args* args, const vqkv_paging* paging, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions and the ragged append: what lies between a projection's
+ * output and the packed cache.  Models rotate queries and keys by their
+ * positions before attention sees them; the pages leave that step to the model.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * vqkv_rope_table — table[p][i] = amplitude * cos(p f_i) and
+ * table[p][rot_dim / 2 + i] = amplitude * sin(p f_i) for the positions
+ * p = 0 .. n_pos - 1 and the pairs i = 0 .. rot_dim / 2 - 1, fp32, each within
+ * 2^-22 * amplitude.  With r = rot_dim, g_i = base^(-2i / r) and n_i =
+ * original_len * g_i / 2 pi, the turns that pair i makes over original_len
+ * positions, the frequencies f_i (radians per position) are
+ *   NONE        g_i
+ *   LINEAR      g_i / factor
+ *   BASE        base'^(-2i / r), base' = base * factor^(r / (r - 2))
+ *   WAVELENGTH  g_i (k + (1 - k) / factor), k = (n_i - low_turns) /
+ *               (high_turns - low_turns) clamped to [0, 1]
+ *   RAMP        g_i (1 - k + k / factor), k = (i - a) / (z - a) clamped to [0, 1],
+ *               where pair number x(n) = r ln(original_len / (2 pi n)) / (2 ln base)
+ *               makes n turns, a = max(floor x(high_turns), 0), z = min(ceil
+ *               x(low_turns), r - 1) (z = a + 0.001 if it is not above a).  It is
+ *               usually given amplitude = 0.1 ln(factor) + 1.
+ * NONE reads none of factor, low_turns, high_turns, original_len; LINEAR and BASE
+ * only factor.  The frequencies are computed on the host in fp64.
+ */
+typedef enum {
+  VQKV_ROPE_NONE = 0,
+  VQKV_ROPE_LINEAR = 1,
+  VQKV_ROPE_BASE = 2,
+  VQKV_ROPE_WAVELENGTH = 3,
+  VQKV_ROPE_RAMP = 4
+} vqkv_rope_scaling;
+
+typedef struct {
+  int32_t n_pos;         /* rows, >= 0 */
+  int32_t rot_dim;       /* rotated channels of a head: a multiple of 8, 8..128 */
+  int32_t scaling;       /* vqkv_rope_scaling */
+  int32_t original_len;  /* >= 1 where it is read */
+  double base;           /* > 1, finite */
+  double factor;         /* > 0, finite */
+  double low_turns, high_turns;   /* 0 < low_turns < high_turns, finite */
+  double amplitude;      /* finite */
+  float* table;          /* device fp32 [n_pos][rot_dim] out, 16-byte aligned */
+} vqkv_rope_table_args;
+
+vqkv_status vqkv_rope_table(const vqkv_rope_table_args* args, void* stream);
+
+/*
+ * vqkv_rope — rotary positions of query or key rows.
+ *
+ * Row (t, h) is rotated by the table's row positions[t]: with r = rot_dim, pair
+ * i < r / 2 is channels (i, i + r / 2), or (2i, 2i + 1) where interleaved is
+ * nonzero, and becomes
+ *   (a cos - b sin, b cos + a sin)      or, where transpose is nonzero,
+ *   (a cos + b sin, b cos - a sin),
+ * the transposed map: the gradient with respect to the rows of a loss whose
+ * gradient with respect to the rotated rows is given (and, for amplitude 1, the
+ * way back).  Channels r and above pass through unchanged.  fp32 arithmetic, one
+ * rounding to the rows' type at the end.
+ *
+ * A position outside [0, n_pos) leaves its rows of out as they are and sets
+ * VQKV_DEVERR_POSITION.  out may be x itself with the same strides (in place);
+ * otherwise no element of the one may be an element of the other: what the
+ * strides do not show to be apart is refused (VQKV_ERR_INVALID_ARG), as are
+ * strides by which two rows of out would meet.
+ */
+typedef struct {
+  int32_t dtype;         /* vqkv_dtype of x and out */
+  int32_t n_tokens;      /* >= 0 */
+  int32_t n_heads;       /* 1..65535 */
+  int32_t head_dim;      /* must be 128 */
+  int32_t rot_dim;       /* as in the table */
+  int32_t n_pos;         /* rows of the table, >= 1 */
+  int32_t interleaved, transpose;
+  int64_t x_token_stride, x_head_stride;      /* elements; multiples of 4, >= 0; that of a single */
+  int64_t out_token_stride, out_head_stride;  /* token or head is not read */
+  const void* x;             /* device, row (t, h) at x + t * token stride + h * head stride, aligned to 4 elements */
+  const int32_t* positions;  /* device [n_tokens] */
+  const float* table;        /* device fp32 [n_pos][rot_dim], 16-byte aligned */
+  void* out;                 /* device, like x */
+  uint32_t* error_flags;     /* device, optional: VQKV_DEVERR_POSITION */
+} vqkv_rope_args;
+
+vqkv_status vqkv_rope(const vqkv_rope_args* args, void* stream);
+
+/*
+ * vqkv_append — the keys and values of a ragged batch's new tokens into the
+ * packed cache, both roles in one launch.
+ *
+ * k and v hold n_tokens rows of Hkv heads (slices of a projection's output, for
+ * instance).  Tokens row_start[b] .. row_start[b + 1] - 1 are sequence b's, and
+ * go to its cache positions pos[b], pos[b] + 1, ...; row_start ascends (equal
+ * neighbours: no new tokens).  Tokens before row_start[0] and from row_start[B]
+ * on are padding and are not read.  A key is rotated by the table's row
+ * rope_pos[t] (NULL: its cache position; after an eviction the two differ) as in
+ * vqkv_rope, rounded once to fp32, and then encoded as in vqkv_encode; a value
+ * is encoded as it is.  rope_table NULL: no rotation.  A token whose cache
+ * position lies outside [0, cap_len), or whose rotation's outside [0, n_pos), is
+ * not written, neither key nor value, and sets VQKV_DEVERR_POSITION.
+ *
+ * The rotated keys are computed in pairs of fp32, so they and the codes are
+ * those of vqkv_encode's reading: exact up to near-ties.  k and v are finite.
+ * paging: NULL for the contiguous cache, else the pools of the paged calls.
+ */
+typedef struct {
+  int32_t mode;          /* vqkv_mode */
+  int32_t dtype;         /* vqkv_dtype of k and v */
+  int32_t B;             /* sequences, >= 0 (0: nothing to do) */
+  int32_t Hkv;           /* KV heads, 1..32767 */
+  int32_t head_dim;      /* must be 128 */
+  int32_t n_tokens;      /* rows of k and v, >= 0 */
+  int32_t cap_len;       /* cache capacity in tokens, >= 1 */
+  int32_t rot_dim;       /* as in the table; not read without one */
+  int32_t n_pos;         /* rows of the table, >= 1; not read without one */
+  int32_t interleaved;   /* pairs, as in vqkv_rope */
+  int64_t k_token_stride, k_head_stride;   /* elements; multiples of 4, >= 0; that of a single */
+  int64_t v_token_stride, v_head_stride;   /* token or head is not read */
+  const void* k;              /* device, row (t, h) at k + t * token stride + h * head stride, aligned to 4 elements */
+  const void* v;              /* device, likewise */
+  const int32_t* row_start;   /* device [B + 1] */
+  const int32_t* pos;         /* device [B] */
+  const int32_t* rope_pos;    /* device [n_tokens], or NULL */
+  const float* rope_table;    /* device fp32 [n_pos][rot_dim], 16-byte aligned, or NULL */
+  const float* s;             /* device fp32 [Hkv][128], > 0, 16-byte aligned */
+  const uint16_t* k_codebook; /* device fp16 [Hkv][E][d_sub], 16-byte aligned, finite */
+  const uint16_t* v_codebook;
+  uint8_t* k_codes;           /* device [B][Hkv][vqkv_code_bytes], or a pool */
+  uint8_t* v_codes;
+  unsigned long long* near_tie_count; /* device, optional: as in vqkv_encode_args, for both roles */
+  uint32_t* error_flags;      /* device, optional: VQKV_DEVERR_POSITION, _BLOCK */
+} vqkv_append_args;
+
+vqkv_status vqkv_append(const vqkv_append_args* args, const vqkv_paging* paging, void* stream);
 
 /*
  * vqkv_decode_attn_fp16 — the same decode attention over a plain fp16 KV

@@ -23,6 +23,14 @@ CODEBOOK_SHAPE = {VQKV_MODE_VQ2: (256, 4), VQKV_MODE_VQ15: (4096, 8), VQKV_MODE_
                   VQKV_MODE_VQ125: (1024, 8)}
 VQKV_ROLE_K = 0
 VQKV_ROLE_V = 1
+VQKV_DTYPE_F16 = 0
+VQKV_DTYPE_F32 = 1
+VQKV_DTYPE_BF16 = 2
+VQKV_ROPE_NONE = 0
+VQKV_ROPE_LINEAR = 1
+VQKV_ROPE_BASE = 2
+VQKV_ROPE_WAVELENGTH = 3
+VQKV_ROPE_RAMP = 4
 VQKV_DEVERR_SEQ_LEN = 0x1
 VQKV_DEVERR_POSITION = 0x2
 VQKV_DEVERR_TIMEOUT = 0x4
@@ -39,7 +47,7 @@ EXPORTED = ["vqkv_code_bytes", "vqkv_decode_workspace_bytes", "vqkv_decode_num_s
             "vqkv_kmeans_update_workspace_bytes", "vqkv_kmeans_update", "vqkv_status_string",
             "vqkv_evict_select", "vqkv_cache_compact", "vqkv_decode_tree_workspace_bytes", "vqkv_decode_attn_tree",
             "vqkv_decode_mass_workspace_bytes", "vqkv_decode_attn_mass", "vqkv_test_decode_tree_timeout",
-            "vqkv_test_decode_mass_timeout"]
+            "vqkv_test_decode_mass_timeout", "vqkv_rope_table", "vqkv_rope", "vqkv_append"]
 STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -118,6 +126,28 @@ class CacheCompactArgs(ctypes.Structure):
                 ("v_codes", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("src", ctypes.c_void_p),
                 ("counts", ctypes.c_void_p), ("start", ctypes.c_void_p), ("mass", ctypes.c_void_p),
                 ("error_flags", ctypes.c_void_p)]
+
+
+class RopeTableArgs(ctypes.Structure):
+    _fields_ = [("n_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_len", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double), ("amplitude", ctypes.c_double),
+                ("table", ctypes.c_void_p)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "n_tokens", "n_heads", "head_dim", "rot_dim", "n_pos", "interleaved",
+                                              "transpose")] + \
+               [(n, ctypes.c_int64) for n in ("x_token_stride", "x_head_stride", "out_token_stride", "out_head_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("x", "positions", "table", "out", "error_flags")]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("mode", "dtype", "B", "Hkv", "head_dim", "n_tokens", "cap_len", "rot_dim", "n_pos",
+                                              "interleaved")] + \
+               [(n, ctypes.c_int64) for n in ("k_token_stride", "k_head_stride", "v_token_stride", "v_head_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("k", "v", "row_start", "pos", "rope_pos", "rope_table", "s", "k_codebook",
+                                               "v_codebook", "k_codes", "v_codes", "near_tie_count", "error_flags")]
 
 
 _lib = None
@@ -205,6 +235,12 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.vqkv_evict_select.argtypes = [ctypes.POINTER(EvictSelectArgs), ctypes.c_void_p]
         L.vqkv_cache_compact.restype = ctypes.c_int
         L.vqkv_cache_compact.argtypes = [ctypes.POINTER(CacheCompactArgs), ctypes.POINTER(Paging), ctypes.c_void_p]
+        L.vqkv_rope_table.restype = ctypes.c_int
+        L.vqkv_rope_table.argtypes = [ctypes.POINTER(RopeTableArgs), ctypes.c_void_p]
+        L.vqkv_rope.restype = ctypes.c_int
+        L.vqkv_rope.argtypes = [ctypes.POINTER(RopeArgs), ctypes.c_void_p]
+        L.vqkv_append.restype = ctypes.c_int
+        L.vqkv_append.argtypes = [ctypes.POINTER(AppendArgs), ctypes.POINTER(Paging), ctypes.c_void_p]
         L.vqkv_status_string.restype = ctypes.c_char_p
         L.vqkv_status_string.argtypes = [ctypes.c_int]
         _lib = L
@@ -585,6 +621,112 @@ def vqkv_cache_compact(mode, k_codes, v_codes, seq_lens, src, counts, cap_len, s
     a = CacheCompactArgs(mode, B, Hkv, cap_len, n, heads, k_codes.data_ptr(), v_codes.data_ptr(), seq_lens.data_ptr(),
                          src.data_ptr(), counts.data_ptr(), _ptr(start), _ptr(mass), _ptr(error_flags))
     _check(lib().vqkv_cache_compact(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
+
+
+# ---------------------------------------------------------------- rotary positions and the ragged append
+
+def _row_dtype(torch, what, name, t) -> int:
+    code = {torch.float16: VQKV_DTYPE_F16, torch.float32: VQKV_DTYPE_F32, torch.bfloat16: VQKV_DTYPE_BF16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: {name} must be fp16, bf16 or fp32, not {t.dtype}")
+    return code
+
+
+def _check_rows(what, name, t, shape, dtype, dev):
+    """Rows [tokens][heads][128] of any strides whose channels are neighbours, on the current CUDA device."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: {name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{what}: the channels of {name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: {name} must be on the current CUDA device")
+
+
+def _rows_shape(what, name, t):
+    if t.dim() != 3 or t.shape[2] != 128:
+        raise ValueError(f"{what}: {name} must have shape (tokens, heads, 128), not {tuple(t.shape)}")
+    return t.shape
+
+
+def _check_table(what, table):
+    if table.dim() != 2:
+        raise ValueError(f"{what}: the table must have shape (positions, rot_dim), not {tuple(table.shape)}")
+
+
+def vqkv_rope_table(table, base=10000.0, scaling=VQKV_ROPE_NONE, factor=1.0, low_turns=1.0, high_turns=4.0, original_len=0,
+                    amplitude=1.0, stream=None) -> None:
+    """Fills table fp32 [n_pos][rot_dim] with the cosines (first half) and sines of every position's rotation."""
+    import torch
+    what = "vqkv_rope_table"
+    _check_table(what, table)
+    handle = _enter(torch, what, stream, (("table", table, torch.float32, None),))
+    a = RopeTableArgs(table.shape[0], table.shape[1], scaling, original_len, base, factor, low_turns, high_turns, amplitude,
+                      table.data_ptr())
+    _check(lib().vqkv_rope_table(ctypes.byref(a), handle), what)
+
+
+def vqkv_rope(x, positions, table, out, interleaved=False, transpose=False, error_flags=None, stream=None) -> None:
+    """out <- the rows x [tokens][heads][128] (fp16, bf16 or fp32) rotated by their tokens' positions (int32 [tokens]).
+
+    x and out may be strided views whose channels are contiguous, and the same one.  table: that of
+    vqkv_rope_table; channels from table.shape[1] on pass through.  transpose: the gradient's map.
+    error_flags: int32 [1], optional (VQKV_DEVERR_POSITION is or-ed in).
+    """
+    import torch
+    what = "vqkv_rope"
+    T, H, D = shape = _rows_shape(what, "x", x)
+    code = _row_dtype(torch, what, "x", x)
+    _check_table(what, table)
+    handle = _enter(torch, what, stream, (("positions", positions, torch.int32, (T,)), ("table", table, torch.float32, None),
+                                          ("error_flags", error_flags, torch.int32, (1,))))
+    dev = positions.get_device()
+    _check_rows(what, "x", x, shape, x.dtype, dev)
+    _check_rows(what, "out", out, shape, x.dtype, dev)
+    a = RopeArgs(code, T, H, D, table.shape[1], table.shape[0], int(interleaved), int(transpose), x.stride(0), x.stride(1),
+                 out.stride(0), out.stride(1), x.data_ptr(), positions.data_ptr(), table.data_ptr(), out.data_ptr(),
+                 _ptr(error_flags))
+    _check(lib().vqkv_rope(ctypes.byref(a), handle), what)
+
+
+def vqkv_append(mode, k, v, row_start, pos, s, k_codebook, v_codebook, k_codes, v_codes, cap_len, rope_table=None, rope_pos=None,
+                interleaved=False, near_tie_count=None, error_flags=None, block_table=None, block_tokens=0, num_blocks=0,
+                stream=None) -> None:
+    """Encodes the keys and values of a ragged batch's new tokens into the packed cache.
+
+    k, v [tokens][Hkv][128] (fp16, bf16 or fp32; strided views whose channels are contiguous); tokens
+    row_start[b] .. row_start[b + 1] - 1 (int32 [B + 1]) go to positions pos[b], pos[b] + 1, ... (int32 [B]) of
+    sequence b, the others are padding.  Keys are rotated by rows rope_pos[t] (int32 [tokens]; None: the cache
+    positions) of rope_table (vqkv_rope_table; None: not at all).  k_codes / v_codes uint8 [B][Hkv][bytes], or
+    pools with block_table.  near_tie_count: int64 [1], error_flags: int32 [1], both optional.
+    """
+    import torch
+    what = "vqkv_append"
+    f16, f32, i32 = torch.float16, torch.float32, torch.int32
+    T, Hkv, D = shape = _rows_shape(what, "k", k)
+    code = _row_dtype(torch, what, "k", k)
+    B = pos.shape[0]
+    cache = _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks)
+    book = (Hkv, *CODEBOOK_SHAPE.get(mode, k_codebook.shape[1:]))   # the C entry refuses other modes
+    if rope_table is not None:
+        _check_table(what, rope_table)
+    handle = _enter(torch, what, stream, (
+        ("row_start", row_start, i32, (B + 1,)), ("pos", pos, i32, (B,)), ("s", s, f32, (Hkv, D)),
+        ("k_codebook", k_codebook, f16, book), ("v_codebook", v_codebook, f16, book),
+        ("k_codes", k_codes, torch.uint8, cache), ("v_codes", v_codes, torch.uint8, cache),
+        ("rope_table", rope_table, f32, None), ("rope_pos", rope_pos, i32, (T,)),
+        ("near_tie_count", near_tie_count, torch.int64, (1,)), ("error_flags", error_flags, i32, (1,)),
+        ("block_table", block_table, i32, None)))
+    dev = pos.get_device()
+    _check_rows(what, "k", k, shape, k.dtype, dev)
+    _check_rows(what, "v", v, shape, k.dtype, dev)
+    n_pos, rot = rope_table.shape if rope_table is not None else (0, 0)
+    a = AppendArgs(mode, code, B, Hkv, D, T, cap_len, rot, n_pos, int(interleaved), k.stride(0), k.stride(1), v.stride(0),
+                   v.stride(1), k.data_ptr(), v.data_ptr(), row_start.data_ptr(), pos.data_ptr(), _ptr(rope_pos),
+                   _ptr(rope_table), s.data_ptr(), k_codebook.data_ptr(), v_codebook.data_ptr(), k_codes.data_ptr(),
+                   v_codes.data_ptr(), _ptr(near_tie_count), _ptr(error_flags))
+    _check(lib().vqkv_append(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
 
 
 # ---------------------------------------------------------------- calibration

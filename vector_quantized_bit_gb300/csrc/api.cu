@@ -1,6 +1,7 @@
 // Host side of the C ABI declared in include/vqkv.h: argument validation,
 // the split-KV plan, workspace layout and kernel launches.  Nothing here
 // allocates device memory or synchronises the host.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -18,7 +19,7 @@ constexpr int kMaxTokens = 1 << 30; // longest row of the cache-editing calls (p
 
 // Kernels that are prepared (attributes set, checks made) only when a call that
 // uses them is first planned, so that no other call loads them or fails with them.
-enum LazyKernels : int { kTreeKernels, kMassKernels, kMassTileKernels, kCompactKernels, kSelectKernels, kLazyKernels };
+enum LazyKernels : int { kTreeKernels, kMassKernels, kMassTileKernels, kCompactKernels, kSelectKernels, kAppendKernels, kLazyKernels };
 
 struct DeviceInfo {
   bool ready = false;
@@ -68,6 +69,7 @@ vqkv_status device_info(LazyKernels what, int mode, DeviceInfo* out) {
                         : what == kMassKernels     ? decode_mass_prepare(mode)
                         : what == kMassTileKernels ? mass_tiles_prepare(mode)
                         : what == kCompactKernels  ? compact_prepare(mode, &d.compact_cluster[mode])
+                        : what == kAppendKernels   ? append_prepare(mode)
                                                    : evict_select_prepare();
   if (e != cudaSuccess) return VQKV_ERR_CUDA;
   d.prepared[what][mode] = true;
@@ -963,6 +965,180 @@ vqkv_status vqkv_cache_compact(const vqkv_cache_compact_args* a, const vqkv_pagi
   return launch_compact(a->mode, p, di.sms, di.compact_cluster[a->mode], static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? VQKV_OK
              : VQKV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace vqkv {
+namespace {
+
+bool is_dtype(int t) { return t == VQKV_DTYPE_F16 || t == VQKV_DTYPE_F32 || t == VQKV_DTYPE_BF16; }
+int dtype_bytes(int t) { return t == VQKV_DTYPE_F32 ? 4 : 2; }
+bool is_rot_dim(int r) { return r >= 8 && r <= 128 && r % 8 == 0; }
+// Below: no byte offset inside a strided array overflows.
+constexpr long long kMaxStride = 1LL << 40;
+
+// Rows [T][H][128] by strides, in elements; a single token's or head's stride counts as 0.
+struct StridedRows {
+  const void* base;
+  int T, H, bytes;   // bytes of an element
+  long long token, head;
+  StridedRows(const void* x, int dtype, int T_, int H_, long long t, long long h)
+      : base(x), T(T_), H(H_), bytes(dtype_bytes(dtype)), token(T_ > 1 ? t : 0), head(H_ > 1 ? h : 0) {}
+  bool valid() const {
+    return base != nullptr && aligned(base, 4 * bytes) && token >= 0 && head >= 0 && token % 4 == 0 && head % 4 == 0 &&
+           token <= kMaxStride / T && head <= kMaxStride / H;
+  }
+  long long token_span() const { return (H - 1) * head + 128; }   // elements from a token's first to behind its last
+  long long extent() const { return (T - 1) * token + token_span(); }
+  bool rows_apart() const {   // tokens outside heads, or heads outside tokens
+    const bool heads = H == 1 || head >= 128, tokens = T == 1 || token >= 128;
+    return (heads && (T == 1 || token >= token_span())) || (tokens && (H == 1 || head >= (T - 1) * token + 128));
+  }
+  bool same(const StridedRows& o) const { return base == o.base && token == o.token && head == o.head; }
+  // Known to share no element: apart as a whole, or interleaved token by token.
+  bool apart(const StridedRows& o) const {
+    if (!overlap(base, (size_t)extent() * bytes, o.base, (size_t)o.extent() * bytes)) return true;
+    if (token != o.token || token < token_span() || token < o.token_span()) return false;
+    const long long step = token * bytes;
+    const long long d = (long long)(reinterpret_cast<uintptr_t>(o.base) - reinterpret_cast<uintptr_t>(base));
+    const long long r = ((d % step) + step) % step;   // where o's tokens begin in this one's
+    return r >= token_span() * bytes && step - r >= o.token_span() * bytes;
+  }
+};
+
+// Frequencies of the pairs, radians per position; false for arguments out of range.
+bool rope_frequencies(const vqkv_rope_table_args* a, double (&f)[64]) {
+  const double r = a->rot_dim, pi = 3.14159265358979323846;
+  if (!(a->base > 1.0) || !std::isfinite(a->base) || !std::isfinite(a->amplitude)) return false;
+  const bool scaled = a->scaling != VQKV_ROPE_NONE;
+  const bool turns = a->scaling == VQKV_ROPE_WAVELENGTH || a->scaling == VQKV_ROPE_RAMP;
+  if (scaled && (!(a->factor > 0.0) || !std::isfinite(a->factor))) return false;
+  if (turns && (!(a->low_turns > 0.0) || !(a->high_turns > a->low_turns) || !std::isfinite(a->high_turns) || a->original_len < 1))
+    return false;
+  const double base = a->scaling == VQKV_ROPE_BASE ? a->base * std::pow(a->factor, r / (r - 2)) : a->base;
+  if (!(base > 0.0) || !std::isfinite(base)) return false;
+  double first = 0, last = 0;
+  if (a->scaling == VQKV_ROPE_RAMP) {
+    auto pair_of = [&](double n) { return r * std::log(a->original_len / (2 * pi * n)) / (2 * std::log(base)); };
+    first = std::max(std::floor(pair_of(a->high_turns)), 0.0);
+    last = std::min(std::ceil(pair_of(a->low_turns)), r - 1);
+    if (!(last > first)) last = first + 0.001;
+  }
+  for (int i = 0; i < a->rot_dim / 2; ++i) {
+    double g = std::pow(base, -2.0 * i / r);
+    if (a->scaling == VQKV_ROPE_LINEAR) {
+      g /= a->factor;
+    } else if (a->scaling == VQKV_ROPE_WAVELENGTH) {
+      const double n = a->original_len * g / (2 * pi);
+      const double k = std::min(std::max((n - a->low_turns) / (a->high_turns - a->low_turns), 0.0), 1.0);
+      g *= k + (1 - k) / a->factor;
+    } else if (a->scaling == VQKV_ROPE_RAMP) {
+      const double k = std::min(std::max((i - first) / (last - first), 0.0), 1.0);
+      g *= 1 - k + k / a->factor;
+    }
+    if (!std::isfinite(g)) return false;
+    f[i] = g;
+  }
+  return true;
+}
+
+}  // namespace
+}  // namespace vqkv
+
+extern "C" {
+
+vqkv_status vqkv_rope_table(const vqkv_rope_table_args* a, void* stream) {
+  if (a == nullptr) return VQKV_ERR_INVALID_ARG;
+  if (!is_rot_dim(a->rot_dim) || a->scaling < VQKV_ROPE_NONE || a->scaling > VQKV_ROPE_RAMP) return VQKV_ERR_UNSUPPORTED;
+  double f[64];
+  if (a->n_pos < 0 || !rope_frequencies(a, f)) return VQKV_ERR_INVALID_ARG;
+  if (a->n_pos == 0) return VQKV_OK;
+  if (!a->table || !aligned(a->table, 16)) return VQKV_ERR_INVALID_ARG;
+  DeviceInfo di;
+  const vqkv_status st = device_info(&di);
+  if (st != VQKV_OK) return st;
+  RopeTableParams p{};
+  for (int i = 0; i < a->rot_dim / 2; ++i) {
+    const double turns = f[i] / (2 * 3.14159265358979323846);
+    // 53 bits of the fraction; one that rounds up to a whole turn is none
+    const double part = std::ldexp(turns - std::floor(turns), 64);
+    p.step[i] = part < 18446744073709551616.0 ? (unsigned long long)part : 0ull;
+  }
+  p.table = a->table;
+  p.n_pos = a->n_pos;
+  p.rot = a->rot_dim;
+  p.amplitude = (float)a->amplitude;
+  return launch_rope_table(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
+}
+
+vqkv_status vqkv_rope(const vqkv_rope_args* a, void* stream) {
+  if (a == nullptr) return VQKV_ERR_INVALID_ARG;
+  if (!is_dtype(a->dtype) || a->head_dim != 128 || !is_rot_dim(a->rot_dim) || a->n_heads > kMaxGridYZ) return VQKV_ERR_UNSUPPORTED;
+  if (a->n_tokens < 0 || a->n_heads < 1 || a->n_pos < 1) return VQKV_ERR_INVALID_ARG;
+  if (a->n_tokens == 0) return VQKV_OK;
+  const StridedRows x(a->x, a->dtype, a->n_tokens, a->n_heads, a->x_token_stride, a->x_head_stride);
+  const StridedRows out(a->out, a->dtype, a->n_tokens, a->n_heads, a->out_token_stride, a->out_head_stride);
+  if (!x.valid() || !out.valid() || !out.rows_apart() || !(out.same(x) || out.apart(x))) return VQKV_ERR_INVALID_ARG;
+  if (!a->positions || !a->table || !aligned(a->positions, 4) || !aligned(a->table, 16) || !aligned(a->error_flags, 4))
+    return VQKV_ERR_INVALID_ARG;
+  DeviceInfo di;
+  const vqkv_status st = device_info(&di);
+  if (st != VQKV_OK) return st;
+  RopeParams p{};
+  p.x = a->x, p.out = a->out;
+  p.x_token = x.token, p.x_head = x.head, p.out_token = out.token, p.out_head = out.head;
+  p.pos = a->positions, p.table = a->table, p.err = a->error_flags;
+  p.T = a->n_tokens, p.H = a->n_heads, p.n_pos = a->n_pos, p.rot = a->rot_dim;
+  p.dtype = a->dtype, p.interleaved = a->interleaved != 0, p.transpose = a->transpose != 0;
+  return launch_rope(p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
+}
+
+vqkv_status vqkv_append(const vqkv_append_args* a, const vqkv_paging* pg, void* stream) {
+  if (a == nullptr) return VQKV_ERR_INVALID_ARG;
+  if (!is_code_mode(a->mode) || !is_dtype(a->dtype) || a->head_dim != 128 || 2LL * a->Hkv > kMaxGridYZ) return VQKV_ERR_UNSUPPORTED;
+  if (a->B < 0 || a->Hkv < 1 || a->n_tokens < 0 || a->cap_len < 1) return VQKV_ERR_INVALID_ARG;
+  if ((long long)a->B * a->Hkv > 0x7fffffffLL || a->n_tokens > kMaxTokens || a->cap_len > kMaxTokens) return VQKV_ERR_UNSUPPORTED;
+  if (a->rope_table != nullptr) {
+    if (!is_rot_dim(a->rot_dim)) return VQKV_ERR_UNSUPPORTED;
+    if (a->n_pos < 1 || !aligned(a->rope_table, 16)) return VQKV_ERR_INVALID_ARG;
+  }
+  if (pg != nullptr) {
+    const vqkv_status st = validate_paging(pg, a->mode, a->cap_len);
+    if (st != VQKV_OK) return st;
+    if (a->B > 0 && a->n_tokens > 0 && (!pg->block_table || !aligned(pg->block_table, 4))) return VQKV_ERR_INVALID_ARG;
+  }
+  if (a->B == 0 || a->n_tokens == 0) return VQKV_OK;
+  const StridedRows k(a->k, a->dtype, a->n_tokens, a->Hkv, a->k_token_stride, a->k_head_stride);
+  const StridedRows v(a->v, a->dtype, a->n_tokens, a->Hkv, a->v_token_stride, a->v_head_stride);
+  if (!k.valid() || !v.valid()) return VQKV_ERR_INVALID_ARG;
+  if (!a->row_start || !a->pos || !a->s || !a->k_codebook || !a->v_codebook || !a->k_codes || !a->v_codes)
+    return VQKV_ERR_INVALID_ARG;
+  if (!aligned(a->row_start, 4) || !aligned(a->pos, 4) || !aligned(a->rope_pos, 4) || !aligned(a->s, 16) ||
+      !aligned(a->k_codebook, 16) || !aligned(a->v_codebook, 16) || !aligned(a->near_tie_count, 8) || !aligned(a->error_flags, 4))
+    return VQKV_ERR_INVALID_ARG;
+  DeviceInfo di;
+  const vqkv_status st = device_info(kAppendKernels, a->mode, &di);
+  if (st != VQKV_OK) return st;
+  AppendParams p{};
+  for (int role = 0; role < 2; ++role) {
+    const StridedRows& x = role == VQKV_ROLE_K ? k : v;
+    EncodeParams& e = p.role[role];
+    e.s = role == VQKV_ROLE_K ? a->s : nullptr;
+    e.cb = reinterpret_cast<const __half*>(role == VQKV_ROLE_K ? a->k_codebook : a->v_codebook);
+    e.codes = role == VQKV_ROLE_K ? a->k_codes : a->v_codes;
+    e.near_tie = a->near_tie_count;
+    e.err = a->error_flags;
+    e.stream_bytes = (long long)vqkv_code_bytes(a->mode, a->cap_len);
+    e.B = a->B, e.Hkv = a->Hkv, e.cap_len = a->cap_len, e.role = role;
+    set_paging(e, pg, a->mode);
+    p.x[role] = x.base, p.token_stride[role] = x.token, p.head_stride[role] = x.head;
+  }
+  p.dtype = a->dtype, p.n_tokens = a->n_tokens;
+  p.row_start = a->row_start, p.pos = a->pos;
+  p.table = a->rope_table, p.rope_pos = a->rope_pos;
+  p.n_table = a->n_pos, p.rot = a->rot_dim, p.interleaved = a->interleaved != 0;
+  return launch_append(a->mode, p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
 }
 
 const char* vqkv_status_string(vqkv_status s) {

@@ -1,0 +1,66 @@
+// Ragged append (vqkv_append): the encode kernels over both roles' rows of a
+// batch's new tokens, keys rotated on the way.  A grid row per KV head and role,
+// so one launch writes the whole step.
+#include <algorithm>
+
+#include "common.cuh"
+#include "encode_kernels.cuh"
+#include "internal.h"
+
+namespace vqkv {
+namespace {
+
+using AppendKernel = void (*)(AppendParams);
+struct AppendVariant {
+  AppendKernel kernel;
+  int threads;
+  size_t smem;
+  int rows;     // rows a CTA takes at a time
+  int waves;    // CTAs per SM
+};
+
+// Few rows: one row per CTA, its candidates split over the CTA's warps.  Many:
+// the tensor-memory search, one persistent CTA per SM (4 bit: one warp per row).
+AppendVariant variant(int mode, bool few) {
+  switch (mode) {
+    case VQKV_MODE_VQ2:
+      if (few) return {encode_vq2_kernel<ENC_WARPS, 4, true>, ENC_THREADS, 0, 1, 1};
+      return {encode_umma_kernel<VQKV_MODE_VQ2, true>, um::THREADS, UmGeo<VQKV_MODE_VQ2>::SMEM, UmGeo<VQKV_MODE_VQ2>::ROWS, 1};
+    case VQKV_MODE_VQ4:
+      if (few) return {encode_vq2_kernel<ENC_WARPS, 2, true>, ENC_THREADS, 0, 1, 1};
+      return {encode_vq2_kernel<1, 2, true>, ENC_THREADS, 0, ENC_WARPS, 16};
+    case VQKV_MODE_VQ3:
+      if (few) return {encode_vq3_kernel<ENC3_SPLIT, true>, ENC3_SPLIT * 32, kEnc3Smem, 1, 1};
+      return {encode_umma_kernel<VQKV_MODE_VQ3, true>, um::THREADS, UmGeo<VQKV_MODE_VQ3>::SMEM, UmGeo<VQKV_MODE_VQ3>::ROWS, 1};
+    case VQKV_MODE_VQ125:
+      if (few) return {encode_vq125_kernel<ENC_WARPS, true>, ENC_THREADS, 0, 1, 1};
+      return {encode_umma_kernel<VQKV_MODE_VQ125, true>, um::THREADS, UmGeo<VQKV_MODE_VQ125>::SMEM,
+              UmGeo<VQKV_MODE_VQ125>::ROWS, 1};
+    default:
+      if (few) return {encode_vq15_tc_split_kernel<true>, TC_THREADS, kTcSplitSmem, 1, 1};
+      return {encode_umma_kernel<VQKV_MODE_VQ15, true>, um::THREADS, UmGeo<VQKV_MODE_VQ15>::SMEM,
+              UmGeo<VQKV_MODE_VQ15>::ROWS, 1};
+  }
+}
+
+}  // namespace
+
+cudaError_t append_prepare(int mode) {
+  cudaError_t e = cudaSuccess;
+  for (int few = 0; few < 2 && e == cudaSuccess; ++few) {
+    const AppendVariant v = variant(mode, few != 0);
+    if (v.smem > 0) e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)v.smem);
+  }
+  return e;
+}
+
+cudaError_t launch_append(int mode, const AppendParams& p, int sms, cudaStream_t stream) {
+  const int streams = 2 * p.role[0].Hkv;
+  const AppendVariant v = variant(mode, (long long)p.n_tokens * streams <= sms);
+  const long long want = (p.n_tokens + v.rows - 1) / v.rows;
+  // whole waves: with one CTA per SM a few CTAs more would double the time
+  const long long most = v.rows == 1 ? want : std::max<long long>(1, (long long)sms * v.waves / streams);
+  return launch_pdl(v.kernel, dim3((unsigned)std::min(want, most), streams), dim3(v.threads), v.smem, stream, p);
+}
+
+}  // namespace vqkv

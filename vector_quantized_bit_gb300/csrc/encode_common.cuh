@@ -117,10 +117,7 @@ __device__ __forceinline__ void lean_add(float ah, float al, float bh, float bl,
 // once at the end.  Every term keeps a relative error near 2^-44, so the
 // result is the correctly rounded fp32 of the fp64 transform except where
 // that lies within about 2^-20 of an fp32 ulp of a rounding boundary.
-__device__ __forceinline__ void transform_key_lean(uint2 raw, float4 s, float4 rs, int lane, float (&x)[4]) {
-  const __half2 x01 = *reinterpret_cast<const __half2*>(&raw.x);
-  const __half2 x23 = *reinterpret_cast<const __half2*>(&raw.y);
-  const float xv[4] = {__low2float(x01), __high2float(x01), __low2float(x23), __high2float(x23)};
+__device__ __forceinline__ void transform_key_values(const float (&xv)[4], float4 s, float4 rs, int lane, float (&x)[4]) {
   const float sv[4] = {s.x, s.y, s.z, s.w}, rv[4] = {rs.x, rs.y, rs.z, rs.w};
   float h[4], l[4];
 #pragma unroll
@@ -160,6 +157,12 @@ __device__ __forceinline__ void transform_key_lean(uint2 raw, float4 s, float4 r
     e = __fmaf_rn(v.l, sqrt2_hi(), e);
     x[i] = __fmul_rn(__fadd_rn(pr, e), 0.0625f);
   }
+}
+__device__ __forceinline__ void transform_key_lean(uint2 raw, float4 s, float4 rs, int lane, float (&x)[4]) {
+  const __half2 x01 = *reinterpret_cast<const __half2*>(&raw.x);
+  const __half2 x23 = *reinterpret_cast<const __half2*>(&raw.y);
+  const float xv[4] = {__low2float(x01), __high2float(x01), __low2float(x23), __high2float(x23)};
+  transform_key_values(xv, s, rs, lane, x);
 }
 
 // The same, reading the lane's 4 fp16 channels and smoothing factors (keys

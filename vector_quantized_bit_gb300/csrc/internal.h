@@ -83,6 +83,41 @@ struct EncodeParams {
   long long block_bytes = 0;
 };
 
+// Ragged append (append.cu): both roles' rows as they come out of a projection.
+struct AppendParams {
+  EncodeParams role[2];     // K, V; x and pos are those below
+  const void* x[2];         // token t, head h of role r: x[r] + t * token_stride[r] + h * head_stride[r] elements
+  long long token_stride[2], head_stride[2];
+  int dtype;                // vqkv_dtype
+  int n_tokens;
+  const int32_t* row_start; // [B + 1]
+  const int32_t* pos;       // [B]: cache position of each sequence's first token
+  const float* table;       // [n_table][rot] or nullptr
+  const int32_t* rope_pos;  // [n_tokens] or nullptr: the cache positions
+  int n_table, rot, interleaved;
+};
+cudaError_t append_prepare(int mode);
+cudaError_t launch_append(int mode, const AppendParams& p, int sms, cudaStream_t stream);
+
+// Rotary positions (rope.cu).
+struct RopeTableParams {
+  unsigned long long step[64];   // turns per position of each pair, modulo 1, in units of 2^-64
+  float* table;                  // [n_pos][rot]
+  int n_pos, rot;
+  float amplitude;
+};
+struct RopeParams {
+  const void* x;
+  void* out;
+  long long x_token, x_head, out_token, out_head;   // strides in elements
+  const int32_t* pos;       // [T]
+  const float* table;       // [n_pos][rot]
+  unsigned* err;
+  int T, H, n_pos, rot, dtype, interleaved, transpose;
+};
+cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t stream);
+cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t stream);
+
 // Decode kernels (decode.cu).  tile_tokens: 16 (VQ2) / 64 (VQ15).
 int decode_tile_tokens(int mode);
 int decode_tiles_per_step(int mode);   // tiles per split are a multiple of this
