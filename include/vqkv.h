@@ -616,6 +616,42 @@ typedef struct {
 vqkv_status vqkv_append(const vqkv_append_args* args, const vqkv_paging* paging, void* stream);
 
 /*
+ * vqkv_cross_attn — attention of ragged queries over all cached tokens of their
+ * sequence: a decoder's cross attention to an encoder's states, or questions to
+ * a shared document.
+ *
+ * Rows row_start[b] .. row_start[b + 1] - 1 of q and out are sequence b's
+ * queries; each sees its cached tokens t < seq_lens[b] (clamped as in
+ * vqkv_decode_attn), in no order.  A query whose sequence has no cached tokens
+ * is a zero row.  Rows before row_start[0] and from row_start[B] on, and those of
+ * a sequence beyond its first max_queries, are left as they are.  A sequence
+ * with more queries than max_queries, or whose starts do not ascend within
+ * [0, n_rows] (it then has none), sets VQKV_DEVERR_SEQ_LEN.
+ *
+ * decode.q is fp16 or bf16 (dtype) [n_rows][Hq][128] with rows q_row_stride
+ * elements apart, decode.out the same type, contiguous; out may be q's buffer
+ * where q is contiguous, too.  Sums and softmax statistics are fp32; the softmax
+ * weights are rounded to fp16 for the tensor cores, q' to two fp16 parts in fp16
+ * calls of up to 64 columns max_queries * (Hq / Hkv), else to one.
+ * num_splits: shares of the batch's work per KV head, 0 = automatic, at most
+ * 1024 are used.  paging as in vqkv_decode_attn_tree.  The workspace holds
+ * vqkv_cross_attn_workspace_bytes(args) bytes and may be shared like that of
+ * vqkv_decode_attn_tree.  Everything else is as in vqkv_decode_attn.
+ */
+typedef struct {
+  vqkv_decode_args decode;    /* q, out: [n_rows][Hq][128] */
+  int32_t dtype;              /* VQKV_DTYPE_F16 or VQKV_DTYPE_BF16 */
+  int32_t n_rows;             /* rows of q and out, 0..2^27 */
+  int32_t max_queries;        /* upper bound of a sequence's queries, >= 1 */
+  int64_t q_row_stride;       /* elements, a multiple of 4, >= Hq * 128 */
+  const int32_t* row_start;   /* device [B + 1] */
+} vqkv_cross_args;
+
+/* Workspace bytes (sizes only, as vqkv_decode_workspace_bytes; also reads dtype, n_rows, max_queries). */
+size_t vqkv_cross_attn_workspace_bytes(const vqkv_cross_args* args);
+vqkv_status vqkv_cross_attn(const vqkv_cross_args* args, const vqkv_paging* paging, void* stream);
+
+/*
  * vqkv_decode_attn_fp16 — the same decode attention over a plain fp16 KV
  * cache, the comparison point for the quantised path on the same shapes
  * (the paper measures its speed-up against FP16 attention, summary page,

@@ -47,7 +47,8 @@ EXPORTED = ["vqkv_code_bytes", "vqkv_decode_workspace_bytes", "vqkv_decode_num_s
             "vqkv_kmeans_update_workspace_bytes", "vqkv_kmeans_update", "vqkv_status_string",
             "vqkv_evict_select", "vqkv_cache_compact", "vqkv_decode_tree_workspace_bytes", "vqkv_decode_attn_tree",
             "vqkv_decode_mass_workspace_bytes", "vqkv_decode_attn_mass", "vqkv_test_decode_tree_timeout",
-            "vqkv_test_decode_mass_timeout", "vqkv_rope_table", "vqkv_rope", "vqkv_append"]
+            "vqkv_test_decode_mass_timeout", "vqkv_rope_table", "vqkv_rope", "vqkv_append",
+            "vqkv_cross_attn_workspace_bytes", "vqkv_cross_attn"]
 STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -150,6 +151,11 @@ class AppendArgs(ctypes.Structure):
                                                "v_codebook", "k_codes", "v_codes", "near_tie_count", "error_flags")]
 
 
+class CrossArgs(ctypes.Structure):
+    _fields_ = [("decode", DecodeArgs), ("dtype", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("max_queries", ctypes.c_int32),
+                ("q_row_stride", ctypes.c_int64), ("row_start", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -241,6 +247,10 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.vqkv_rope.argtypes = [ctypes.POINTER(RopeArgs), ctypes.c_void_p]
         L.vqkv_append.restype = ctypes.c_int
         L.vqkv_append.argtypes = [ctypes.POINTER(AppendArgs), ctypes.POINTER(Paging), ctypes.c_void_p]
+        L.vqkv_cross_attn_workspace_bytes.restype = ctypes.c_size_t
+        L.vqkv_cross_attn_workspace_bytes.argtypes = [ctypes.POINTER(CrossArgs)]
+        L.vqkv_cross_attn.restype = ctypes.c_int
+        L.vqkv_cross_attn.argtypes = [ctypes.POINTER(CrossArgs), ctypes.POINTER(Paging), ctypes.c_void_p]
         L.vqkv_status_string.restype = ctypes.c_char_p
         L.vqkv_status_string.argtypes = [ctypes.c_int]
         _lib = L
@@ -727,6 +737,53 @@ def vqkv_append(mode, k, v, row_start, pos, s, k_codebook, v_codebook, k_codes, 
                    _ptr(rope_table), s.data_ptr(), k_codebook.data_ptr(), v_codebook.data_ptr(), k_codes.data_ptr(),
                    v_codes.data_ptr(), _ptr(near_tie_count), _ptr(error_flags))
     _check(lib().vqkv_append(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
+
+
+# ---------------------------------------------------------------- cross attention
+
+def cross_attn_workspace(mode, B, Hq, Hkv, n_rows, max_queries, cap_len, max_seq_len, num_splits=0, dtype=VQKV_DTYPE_F16,
+                         device="cuda"):
+    """A zero-filled workspace tensor of the size vqkv_cross_attn needs (that of fp16 queries serves bf16 ones, too)."""
+    size = 0
+    for code in {dtype, VQKV_DTYPE_BF16}:
+        a = CrossArgs(decode=_size_args(mode, B, Hq, Hkv, cap_len, max_seq_len, num_splits), dtype=code, n_rows=n_rows,
+                      max_queries=max_queries)
+        size = max(size, int(lib().vqkv_cross_attn_workspace_bytes(ctypes.byref(a))))
+    return _new_workspace(size, "vqkv_cross_attn_workspace_bytes", device)
+
+
+def vqkv_cross_attn(mode, q, row_start, k_codes, v_codes, seq_lens, k_codebook, v_codebook, s, out, workspace, cap_len,
+                    max_seq_len, max_queries, softmax_scale=0.0, num_splits=0, block_table=None, block_tokens=0, num_blocks=0,
+                    stream=None) -> None:
+    """Attention of ragged queries over all cached tokens of their sequence.
+
+    q (fp16 or bf16 [rows][Hq][128], rows of any stride) and out (the same type, contiguous): rows row_start[b] ..
+    row_start[b + 1] - 1 (int32 [B + 1]), max_queries at most, are sequence b's queries and see its seq_lens[b]
+    tokens; the other rows of out are left as they are.  k_codes / v_codes: [B][Hkv][bytes], or pools with
+    block_table.
+    """
+    import torch
+    what = "vqkv_cross_attn"
+    f16, i32, u8 = torch.float16, torch.int32, torch.uint8
+    n, Hq, D = shape = _rows_shape(what, "q", q)
+    if q.dtype is not f16 and q.dtype is not torch.bfloat16:
+        raise TypeError(f"{what}: q must be fp16 or bf16, not {q.dtype}")
+    B, Hkv = seq_lens.shape[0], k_codebook.shape[0]
+    cache = _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks)
+    book = (Hkv, *CODEBOOK_SHAPE.get(mode, k_codebook.shape[1:]))   # the C entry refuses other modes
+    handle = _enter(torch, what, stream, (
+        ("row_start", row_start, i32, (B + 1,)), ("k_codes", k_codes, u8, cache), ("v_codes", v_codes, u8, cache),
+        ("seq_lens", seq_lens, i32, (B,)), ("k_codebook", k_codebook, f16, book), ("v_codebook", v_codebook, f16, book),
+        ("s", s, torch.float32, (Hkv, D)), ("out", out, q.dtype, shape), ("workspace", workspace, u8, None),
+        ("block_table", block_table, i32, None)))
+    _check_rows(what, "q", q, shape, q.dtype, seq_lens.get_device())
+    if Hq > 1 and q.stride(1) != D:
+        raise ValueError(f"{what}: the heads of q must be contiguous")
+    a = CrossArgs((mode, B, Hq, Hkv, D, cap_len, max_seq_len, q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
+                   seq_lens.data_ptr(), k_codebook.data_ptr(), v_codebook.data_ptr(), s.data_ptr(), softmax_scale,
+                   num_splits, workspace.data_ptr(), workspace.numel(), out.data_ptr()),
+                  VQKV_DTYPE_F16 if q.dtype is f16 else VQKV_DTYPE_BF16, n, max_queries, q.stride(0), row_start.data_ptr())
+    _check(lib().vqkv_cross_attn(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
 
 
 # ---------------------------------------------------------------- calibration

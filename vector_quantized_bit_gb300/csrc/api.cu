@@ -19,7 +19,7 @@ constexpr int kMaxTokens = 1 << 30; // longest row of the cache-editing calls (p
 
 // Kernels that are prepared (attributes set, checks made) only when a call that
 // uses them is first planned, so that no other call loads them or fails with them.
-enum LazyKernels : int { kTreeKernels, kMassKernels, kMassTileKernels, kCompactKernels, kSelectKernels, kAppendKernels, kLazyKernels };
+enum LazyKernels : int { kTreeKernels, kMassKernels, kMassTileKernels, kCompactKernels, kSelectKernels, kAppendKernels, kCrossKernels, kLazyKernels };
 
 struct DeviceInfo {
   bool ready = false;
@@ -70,6 +70,7 @@ vqkv_status device_info(LazyKernels what, int mode, DeviceInfo* out) {
                         : what == kMassTileKernels ? mass_tiles_prepare(mode)
                         : what == kCompactKernels  ? compact_prepare(mode, &d.compact_cluster[mode])
                         : what == kAppendKernels   ? append_prepare(mode)
+                        : what == kCrossKernels    ? cross_prepare(mode)
                                                    : evict_select_prepare();
   if (e != cudaSuccess) return VQKV_ERR_CUDA;
   d.prepared[what][mode] = true;
@@ -296,6 +297,10 @@ DecodeParams batch_part(const DecodeParams& p, int b0, int B) {
   c.q = p.q + rows;
   c.out = p.out + rows;
   c.seq_lens = p.seq_lens + b0;
+  if (p.row_start != nullptr) {   // packed rows: the starts say where
+    c.q = p.q, c.out = p.out;
+    c.row_start = p.row_start + b0;
+  }
   if (p.mass != nullptr) c.mass = p.mass + (size_t)b0 * p.Hkv * p.cap_len;
   if (p.block_table != nullptr) {
     c.block_table = p.block_table + (size_t)b0 * p.max_blocks;
@@ -1007,6 +1012,48 @@ struct StridedRows {
   }
 };
 
+// Cross attention: shares of all items' units per KV head, one CTA per SM in one wave.
+struct CrossPlan {
+  int n_splits = 1, layout = kOneTile;
+  bool wide_merge = false;   // many partials per item
+  size_t query_off = 0, partials_off = 0, ws_bytes = 0;
+};
+
+vqkv_status validate_cross_sizes(const vqkv_cross_args* ac) {
+  if (ac == nullptr) return VQKV_ERR_INVALID_ARG;
+  const vqkv_decode_args& a = ac->decode;
+  const vqkv_status st = validate_decode_sizes(&a);
+  if (st != VQKV_OK) return st;
+  if (ac->dtype != VQKV_DTYPE_F16 && ac->dtype != VQKV_DTYPE_BF16) return VQKV_ERR_UNSUPPORTED;
+  if (ac->n_rows < 0 || ac->max_queries < 1) return VQKV_ERR_INVALID_ARG;
+  const long long units = (long long)std::min(a.B, kFlatMaxB) * ((a.max_seq_len + 63) / 64);
+  if (a.Hkv > kMaxGridYZ || a.cap_len > kMaxTokens || ac->n_rows > (1 << 27) || ac->max_queries > (1 << 27) || units > kMaxTokens ||
+      units * ((ac->max_queries * (long long)(a.Hq / a.Hkv) + 63) / 64) > kMaxTokens)
+    return VQKV_ERR_UNSUPPORTED;
+  return VQKV_OK;
+}
+
+vqkv_status plan_cross(const vqkv_cross_args* ac, CrossPlan* pl) {
+  const vqkv_decode_args& a = ac->decode;
+  DeviceInfo di;
+  const vqkv_status st = device_info(kCrossKernels, a.mode, &di);
+  if (st != VQKV_OK) return st;
+  const long long g = a.Hq / a.Hkv, cols = ac->max_queries * g;
+  pl->layout = cols > 128 ? kTwoTiles : cols <= 64 && ac->dtype == VQKV_DTYPE_F16 ? kPairs : kOneTile;
+  const int width = cross_cols(pl->layout), B = std::max(std::min(a.B, kFlatMaxB), 1);
+  // items, and tiles of full sequences, at most
+  const long long items = std::max<long long>(1, std::min(B * ((cols + width - 1) / width), ac->n_rows * g / width + B));
+  const long long units = items * std::max(1, (a.max_seq_len + 63) / 64);
+  const long long want = a.num_splits > 0 ? std::min(a.num_splits, 1024) : di.sms / a.Hkv;
+  pl->n_splits = (int)std::max<long long>(1, std::min(want, units));
+  pl->wide_merge = pl->n_splits > 4 * items;
+  pl->query_off = decode_ticket_region_bytes(a.B, a.Hkv * kTicketGroups);
+  pl->partials_off = pl->query_off + round_up(cross_query_bytes(B, a.Hq, a.Hkv, ac->n_rows, pl->layout), 256);
+  pl->ws_bytes = pl->partials_off;
+  if (pl->n_splits > 1) pl->ws_bytes += sizeof(float) * (size_t)a.Hkv * pl->n_splits * 2 * width * kPartialStride;
+  return VQKV_OK;
+}
+
 // Frequencies of the pairs, radians per position; false for arguments out of range.
 bool rope_frequencies(const vqkv_rope_table_args* a, double (&f)[64]) {
   const double r = a->rot_dim, pi = 3.14159265358979323846;
@@ -1139,6 +1186,55 @@ vqkv_status vqkv_append(const vqkv_append_args* a, const vqkv_paging* pg, void* 
   p.table = a->rope_table, p.rope_pos = a->rope_pos;
   p.n_table = a->n_pos, p.rot = a->rot_dim, p.interleaved = a->interleaved != 0;
   return launch_append(a->mode, p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
+}
+
+size_t vqkv_cross_attn_workspace_bytes(const vqkv_cross_args* a) {
+  CrossPlan pl;
+  if (validate_cross_sizes(a) != VQKV_OK || plan_cross(a, &pl) != VQKV_OK) return 0;
+  return pl.ws_bytes;
+}
+
+vqkv_status vqkv_cross_attn(const vqkv_cross_args* ac, const vqkv_paging* pg, void* stream) {
+  vqkv_status st = validate_cross_sizes(ac);
+  if (st != VQKV_OK) return st;
+  const vqkv_decode_args* a = &ac->decode;
+  if (ac->n_rows > 0) {
+    st = validate_decode(a);
+    if (st != VQKV_OK) return st;
+  }
+  if (pg != nullptr) {
+    st = validate_paging(pg, a->mode, a->cap_len);
+    if (st != VQKV_OK) return st;
+    if (a->B > 0 && ac->n_rows > 0 && (!pg->block_table || !aligned(pg->block_table, 4))) return VQKV_ERR_INVALID_ARG;
+  }
+  if (a->B == 0 || ac->n_rows == 0) return VQKV_OK;
+  if (!ac->row_start || !aligned(ac->row_start, 4)) return VQKV_ERR_INVALID_ARG;
+  const long long row = a->Hq * 128LL, q_row = ac->n_rows > 1 ? ac->q_row_stride : row;
+  if (q_row < row || q_row % 4 != 0 || q_row > kMaxStride / ac->n_rows) return VQKV_ERR_INVALID_ARG;
+  if (!(a->q == a->out && q_row == row) &&
+      overlap(a->q, 2 * (size_t)((ac->n_rows - 1) * q_row + row), a->out, 2 * (size_t)ac->n_rows * row))
+    return VQKV_ERR_INVALID_ARG;
+  CrossPlan pl;
+  st = plan_cross(ac, &pl);
+  if (st != VQKV_OK) return st;
+  if (a->workspace == nullptr || a->workspace_bytes < pl.ws_bytes) return VQKV_ERR_WORKSPACE;
+  if (!aligned(a->workspace, 256)) return VQKV_ERR_INVALID_ARG;
+  unsigned char* ws = static_cast<unsigned char*>(a->workspace);
+  DecodeParams p = packed_params(a, 1, pg);
+  p.row_start = ac->row_start;
+  p.n_rows = ac->n_rows;
+  p.max_queries = ac->max_queries;
+  p.bf16 = ac->dtype == VQKV_DTYPE_BF16;
+  p.q_row = q_row;
+  p.ncols = (int)std::min<long long>(ac->max_queries * (long long)p.g, cross_cols(pl.layout));
+  p.partials = reinterpret_cast<float*>(ws + pl.partials_off);
+  p.n_splits = pl.n_splits;
+  p.max_polls = kTilePolls;
+  for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB)
+    if (launch_cross(a->mode, batch_part(p, b0, a->B), pl.layout, pl.wide_merge, ws + pl.query_off,
+                     static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return VQKV_ERR_CUDA;
+  return VQKV_OK;
 }
 
 const char* vqkv_status_string(vqkv_status s) {

@@ -448,16 +448,119 @@ struct Pieces {
     return false;
   }
 };
+// A sequence's rows of a cross attention: first row and number; none (and the
+// error bit) where the starts make no sense, at most max_queries.
+struct RowRange {
+  int first, n;
+};
+__device__ __forceinline__ RowRange row_range(const DecodeParams& p, int b, bool report) {
+  const int lo = __ldg(p.row_start + b), hi = __ldg(p.row_start + b + 1);
+  const bool fine = lo >= 0 && hi >= lo && hi <= p.n_rows;
+  const int n = fine ? min(hi - lo, p.max_queries) : 0;
+  if (report && (!fine || n != hi - lo)) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
+  return {lo, n};
+}
+
 __device__ __forceinline__ int clamped_len(const DecodeParams& p, int b) {
   return min(max(p.seq_lens[b], 0), p.max_seq_len);
 }
 
 
+// The Walsh-Hadamard transform of a column whose channels 32 part .. 32 part +
+// 31 this lane holds, part = lane % 4, times scale.  Five stages are in
+// registers, two across the column's four lanes (a lane with 4 channels would
+// need five across lanes: 20 shuffles per column and lane instead of 8).  Whole
+// warps.
+__device__ __forceinline__ void fwht_column(float (&v)[32], int part, float scale) {
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(i & h)) {
+        const float x = v[i], y = v[i + h];
+        v[i] = x + y, v[i + h] = x - y;
+      }
+#pragma unroll
+  for (int h = 1; h < 4; h <<= 1) {
+    const float sign = (part & h) ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __fmaf_rn(v[i], sign, __shfl_xor_sync(0xffffffffu, v[i], h));
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] *= scale;
+}
+
+// Units of a cross attention's items (a group of up to COLS columns of one
+// sequence over a tile of TOK tokens): s_pref[b] = units of sequences 0 .. b - 1.
+// All threads.
+template <int TOK>
+__device__ __forceinline__ void item_prefix(const DecodeParams& p, int cols, int* s_pref, bool report) {
+  const int lane = threadIdx.x & 31;
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    const int raw = p.seq_lens[b], L = min(max(raw, 0), p.max_seq_len);
+    if (report && raw != L) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
+    s_pref[b + 1] = (row_range(p, b, report).n * p.g + cols - 1) / cols * ((L + TOK - 1) / TOK);
+  }
+  if (threadIdx.x == 0) s_pref[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {   // inclusive scan, 32 entries per step
+    int carry = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      const int i = base + lane;
+      int v = i < p.B ? s_pref[i + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+      }
+      if (i < p.B) s_pref[i + 1] = v + carry;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// The last sequence that starts at or before unit x (x below the total).
+__device__ __forceinline__ int sequence_of(const int* pref, int B, int x) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pref[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A CTA's pieces of a cross attention: the overlaps of its share with the items.
+template <int TOK, int COLS>
+struct ItemPieces {
+  const DecodeParams& p;
+  const int* pref;
+  int at, r1;        // the share's units not yet taken: [at, r1)
+  int b, tile0, n;   // the current piece: n tiles of sequence b from tile0 on
+  int all, group;    // tiles of sequence b, the item's group of columns
+
+  __device__ __forceinline__ ItemPieces(const DecodeParams& p_, const int* pref_, int split, int n_splits) : p(p_), pref(pref_) {
+    const int T = pref[p.B], S = min(n_splits, T);
+    at = split < S ? (int)((long long)T * split / S) : 0;
+    r1 = split < S ? (int)((long long)T * (split + 1) / S) : 0;
+    b = at < r1 ? sequence_of(pref, p.B, at) : 0;
+  }
+  __device__ __forceinline__ bool next() {
+    if (at >= r1) return false;
+    while (pref[b + 1] <= at) ++b;   // at < r1 <= pref[B]
+    all = (min(max(__ldg(p.seq_lens + b), 0), p.max_seq_len) + TOK - 1) / TOK;
+    const int local = at - pref[b];
+    group = local / all;
+    tile0 = local - group * all;
+    n = min(all - tile0, r1 - at);
+    at += n;
+    return true;
+  }
+};
+
 // q' (scaled) of softmax column c of (sequence b, KV head kvh), zeros past the
 // last column: channels 32 part .. 32 part + 31 in this lane, part = lane % 4.
-// Five stages of the Walsh-Hadamard transform are in registers, two across
-// the column's four lanes (a lane with 4 channels would need five across lanes:
-// 20 shuffles per column and lane instead of 8).  Whole warps.
+// Whole warps.
 __device__ __forceinline__ void transform_column(const DecodeParams& p, int b, int kvh, int c, int part, float (&v)[32]) {
   if (c < p.ncols) {
     const int m = c / p.g, hq = kvh * p.g + c - m * p.g;
@@ -475,22 +578,7 @@ __device__ __forceinline__ void transform_column(const DecodeParams& p, int b, i
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = 0.f;
   }
-#pragma unroll
-  for (int h = 1; h < 32; h <<= 1)
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (!(i & h)) {
-        const float x = v[i], y = v[i + h];
-        v[i] = x + y, v[i + h] = x - y;
-      }
-#pragma unroll
-  for (int h = 1; h < 4; h <<= 1) {
-    const float sign = (part & h) ? -1.f : 1.f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __fmaf_rn(v[i], sign, __shfl_xor_sync(0xffffffffu, v[i], h));
-  }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] *= p.qscale;
+  fwht_column(v, part, p.qscale);
 }
 
 }  // namespace

@@ -61,6 +61,13 @@ struct DecodeParams {
   float2* stats = nullptr;
   float* mass = nullptr;    // [B][Hkv][cap_len]
   int score_row = 0, cap_len = 0;
+  // Cross attention (vqkv_cross_attn), else unused: the rows of q and out are
+  // packed, sequence b's are row_start[b] .. row_start[b + 1] - 1; ncols is the
+  // number of columns of an item (a group of a sequence's columns) that the
+  // kernel computes, q_row the stride of q's rows in elements.
+  const int32_t* row_start = nullptr;
+  int n_rows = 0, max_queries = 0, bf16 = 0;
+  long long q_row = 0;
 };
 
 constexpr int kPartialStride = 132;  // O[128], m, l, pad (rows 16-byte aligned)
@@ -159,6 +166,15 @@ cudaError_t decode_tree_prepare(int mode);
 size_t decode_tree_query_bytes(int B, int Hkv, int ncols, bool pairs);
 cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, bool pairs, void* qx,
                                cudaStream_t stream);
+
+// Cross attention (cross_attn.cu), B <= kFlatMaxB: n_splits shares per KV head;
+// partials [Hkv][2 n_splits][cross_cols(layout)].  layout: columns of an item,
+// as in the draft-tree attention.
+enum TileLayout : int { kOneTile = 0, kTwoTiles = 1, kPairs = 2 };   // columns on the MMA rows
+int cross_cols(int layout);   // columns of an item, at most
+cudaError_t cross_prepare(int mode);
+size_t cross_query_bytes(int B, int Hq, int Hkv, int n_rows, int layout);
+cudaError_t launch_cross(int mode, const DecodeParams& p, int layout, bool wide_merge, void* qx, cudaStream_t stream);
 
 // Attention weights of many columns (mass_tiles.cu); B <= kFlatMaxB, at most 64
 // columns.  image: scratch for the transformed queries, which are taken before
