@@ -490,12 +490,12 @@ vqkv_status vqkv_cache_compact(const vqkv_cache_compact_args* args, const vqkv_p
  * vqkv_rope_table — table[p][i] = amplitude * cos(p f_i) and
  * table[p][rot_dim / 2 + i] = amplitude * sin(p f_i) for the positions
  * p = 0 .. n_pos - 1 and the pairs i = 0 .. rot_dim / 2 - 1, fp32, each within
- * 2^-22 * amplitude.  With r = rot_dim, g_i = base^(-2i / r) and n_i =
+ * (2^-22 + p f_i 2^-50) * |amplitude|.  With r = rot_dim, g_i = base^(-2i / r) and n_i =
  * original_len * g_i / 2 pi, the turns that pair i makes over original_len
  * positions, the frequencies f_i (radians per position) are
  *   NONE        g_i
  *   LINEAR      g_i / factor
- *   BASE        base'^(-2i / r), base' = base * factor^(r / (r - 2))
+ *   BASE        base'^(-2i / r), base' = base * factor^(r / (r - 2)), which has to be above 1
  *   WAVELENGTH  g_i (k + (1 - k) / factor), k = (n_i - low_turns) /
  *               (high_turns - low_turns) clamped to [0, 1]
  *   RAMP        g_i (1 - k + k / factor), k = (i - a) / (z - a) clamped to [0, 1],
@@ -625,8 +625,9 @@ vqkv_status vqkv_append(const vqkv_append_args* args, const vqkv_paging* paging,
  * vqkv_decode_attn), in no order.  A query whose sequence has no cached tokens
  * is a zero row.  Rows before row_start[0] and from row_start[B] on, and those of
  * a sequence beyond its first max_queries, are left as they are.  A sequence
- * with more queries than max_queries, or whose starts do not ascend within
- * [0, n_rows] (it then has none), sets VQKV_DEVERR_SEQ_LEN.
+ * with more queries than max_queries sets VQKV_DEVERR_SEQ_LEN; so does one whose
+ * starts do not ascend within [0, n_rows]: it has no queries then, and what
+ * others share with it is undefined.
  *
  * decode.q is fp16 or bf16 (dtype) [n_rows][Hq][128] with rows q_row_stride
  * elements apart, decode.out the same type, contiguous; out may be q's buffer

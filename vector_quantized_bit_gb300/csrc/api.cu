@@ -1064,7 +1064,7 @@ bool rope_frequencies(const vqkv_rope_table_args* a, double (&f)[64]) {
   if (turns && (!(a->low_turns > 0.0) || !(a->high_turns > a->low_turns) || !std::isfinite(a->high_turns) || a->original_len < 1))
     return false;
   const double base = a->scaling == VQKV_ROPE_BASE ? a->base * std::pow(a->factor, r / (r - 2)) : a->base;
-  if (!(base > 0.0) || !std::isfinite(base)) return false;
+  if (!(base > 1.0) || !std::isfinite(base)) return false;
   double first = 0, last = 0;
   if (a->scaling == VQKV_ROPE_RAMP) {
     auto pair_of = [&](double n) { return r * std::log(a->original_len / (2 * pi * n)) / (2 * std::log(base)); };

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant_
     if (__ldg(p.row_start + mid) <= row) lo = mid; else hi = mid - 1;
   }
   const RowRange rows = row_range(p, lo, false);
-  const bool in = any && row >= rows.first && row - rows.first < rows.n;
+  const bool in = any && row >= rows.first && row - rows.first < rows.n;   // both in [0, n_rows]
   float v[32];
   if (in) {
     const float4* s4 = reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 32 * part);

@@ -454,11 +454,12 @@ struct RowRange {
   int first, n;
 };
 __device__ __forceinline__ RowRange row_range(const DecodeParams& p, int b, bool report) {
-  const int lo = __ldg(p.row_start + b), hi = __ldg(p.row_start + b + 1);
+  // (differences in 64 bits: starts of any bits must not overflow on the way to the comparisons)
+  const long long lo = __ldg(p.row_start + b), hi = __ldg(p.row_start + b + 1);
   const bool fine = lo >= 0 && hi >= lo && hi <= p.n_rows;
-  const int n = fine ? min(hi - lo, p.max_queries) : 0;
+  const int n = fine ? (int)min(hi - lo, (long long)p.max_queries) : 0;
   if (report && (!fine || n != hi - lo)) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
-  return {lo, n};
+  return {fine ? (int)lo : 0, n};
 }
 
 __device__ __forceinline__ int clamped_len(const DecodeParams& p, int b) {

@@ -131,7 +131,7 @@ struct Rows<true> {
         return {b, -1, 0};
       }
     }
-    const long long t = (long long)pos + (r - first);
+    const long long t = (long long)pos + ((long long)r - first);
     const bool in_cache = t >= 0 && t < p.cap_len;
     int angle = 0;
     bool turns = true;
