@@ -54,13 +54,19 @@ cudaError_t append_prepare(int mode) {
   return e;
 }
 
-cudaError_t launch_append(int mode, const AppendParams& p, int sms, cudaStream_t stream) {
-  const int streams = 2 * p.role[0].Hkv;
-  const AppendVariant v = variant(mode, (long long)p.n_tokens * streams <= sms);
-  const long long want = (p.n_tokens + v.rows - 1) / v.rows;
-  // whole waves: with one CTA per SM a few CTAs more would double the time
-  const long long most = v.rows == 1 ? want : std::max<long long>(1, (long long)sms * v.waves / streams);
-  return launch_pdl(v.kernel, dim3((unsigned)std::min(want, most), streams), dim3(v.threads), v.smem, stream, p);
+cudaError_t launch_append(int mode, AppendParams p, int sms, cudaStream_t stream) {
+  const int Hkv = p.role[0].Hkv;
+  const AppendVariant v = variant(mode, (long long)p.n_tokens * 2 * Hkv <= sms);
+  const int want = (p.n_tokens + v.rows - 1) / v.rows;   // CTAs of a KV head and role with work
+  int keys = want, values = want;
+  if (v.rows > 1) {
+    // whole waves: with one CTA per SM a few CTAs more would double the time
+    const int most = std::max(2, sms * v.waves / Hkv);
+    keys = std::min(want, (most + 1) / 2);
+    values = std::min(want, most - keys);
+  }
+  p.key_ctas = keys;
+  return launch_pdl(v.kernel, dim3(keys + values, Hkv), dim3(v.threads), v.smem, stream, p);
 }
 
 }  // namespace vqkv

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(ENC_THREADS)
   constexpr int kTileBytes = 16 * (kHeadDim / DSUB);
   __shared__ Centroid s_cb[256];
   __shared__ Best s_part[SPLIT > 1 ? ENC_WARPS * 32 : 1];
-  Rows<APPEND> src(a, blockIdx.y);
+  Rows<APPEND> src(a);
   const EncodeParams& p = src.p;
   const int kvh = src.kvh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -82,12 +82,12 @@ __global__ void __launch_bounds__(ENC_THREADS)
   }
   __syncthreads();
   const int rows = src.count();
-  const int r0 = (SPLIT == 1) ? blockIdx.x * ENC_WARPS + warp : blockIdx.x;
-  const int rstep = (SPLIT == 1) ? gridDim.x * ENC_WARPS : gridDim.x;
+  const int r0 = (SPLIT == 1) ? src.cta() * ENC_WARPS + warp : src.cta();
+  const int rstep = (SPLIT == 1) ? src.ctas() * ENC_WARPS : src.ctas();
   const int c_lo = (SPLIT == 1) ? 0 : warp * (256 / SPLIT);
   const int c_hi = c_lo + 256 / SPLIT;
   for (int r = r0; r < rows; r += rstep) {
-    const RowPlace w = src.place(r, lane == 0 && (SPLIT == 1 || warp == 0));
+    const RowPlace w = src.place(r, src.angle(r), lane == 0 && (SPLIT == 1 || warp == 0));
     if (w.t < 0) continue;
     const int b = w.b, t = w.t;
     float x[4];
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(SPLIT == 1 ? ENC_THREADS : SPLIT * 32)
   extern __shared__ __align__(16) unsigned char enc_smem[];
   float4* s_cb = reinterpret_cast<float4*>(enc_smem);
   __shared__ Best s_part[SPLIT > 1 ? SPLIT * 32 : 1];
-  Rows<APPEND> src(a, blockIdx.y);
+  Rows<APPEND> src(a);
   const EncodeParams& p = src.p;
   const int kvh = src.kvh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -189,10 +189,10 @@ __global__ void __launch_bounds__(SPLIT == 1 ? ENC_THREADS : SPLIT * 32)
   else
     __syncwarp();
   const int rows = src.count();
-  const int r0 = (SPLIT == 1) ? blockIdx.x * kWarps + warp : blockIdx.x;
-  const int rstep = (SPLIT == 1) ? gridDim.x * kWarps : gridDim.x;
+  const int r0 = (SPLIT == 1) ? src.cta() * kWarps + warp : src.cta();
+  const int rstep = (SPLIT == 1) ? src.ctas() * kWarps : src.ctas();
   for (int r = r0; r < rows; r += rstep) {
-    const RowPlace w = src.place(r, lane == 0 && (SPLIT == 1 || warp == 0));
+    const RowPlace w = src.place(r, src.angle(r), lane == 0 && (SPLIT == 1 || warp == 0));
     if (w.t < 0) continue;
     const int b = w.b, t = w.t;
     float x[4];
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(ENC_THREADS)
     encode_vq125_kernel(const __grid_constant__ typename Rows<APPEND>::Params a) {
   __shared__ float4 s_cb[2 * 1024];
   __shared__ Best s_part[SPLIT > 1 ? ENC_WARPS * 32 : 1];
-  Rows<APPEND> src(a, blockIdx.y);
+  Rows<APPEND> src(a);
   const EncodeParams& p = src.p;
   const int kvh = src.kvh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -279,10 +279,10 @@ __global__ void __launch_bounds__(ENC_THREADS)
   __syncthreads();
   const bool key = p.role == VQKV_ROLE_K;
   const int rows = src.count();
-  const int r0 = (SPLIT == 1) ? blockIdx.x * ENC_WARPS + warp : blockIdx.x;
-  const int rstep = (SPLIT == 1) ? gridDim.x * ENC_WARPS : gridDim.x;
+  const int r0 = (SPLIT == 1) ? src.cta() * ENC_WARPS + warp : src.cta();
+  const int rstep = (SPLIT == 1) ? src.ctas() * ENC_WARPS : src.ctas();
   for (int r = r0; r < rows; r += rstep) {
-    const RowPlace w = src.place(r, lane == 0 && (SPLIT == 1 || warp == 0));
+    const RowPlace w = src.place(r, src.angle(r), lane == 0 && (SPLIT == 1 || warp == 0));
     if (w.t < 0) continue;
     const int b = w.b, t = w.t;
     float x[4];
@@ -472,14 +472,16 @@ __device__ __forceinline__ float build_tc_table(const EncodeParams& p, int kvh, 
 // Many rows of 1.5-bit or 2-bit encode on the fifth-generation tensor cores.
 // A tile is 128 (row, subvector) pairs, the M of one tcgen05 MMA: 8 rows of
 // 16 subvectors (1.5 bit) or 4 rows of 32 (2 bit); the 4096 (256) centroids
-// are 32 (2) chunks of N = 128.  One MMA per chunk writes to tensor memory
-//   D[m][c] = [x_hi, 1, 1] . [-2c, |c|^2_hi, |c|^2_lo] = |c|^2 - 2 x_hi . c,
-// the screened distance less the subvector's own |x'_j|^2, with x_hi the fp16
-// rounding of the transformed subvector (A) and the [-2c, |c|^2_hi, |c|^2_lo]
+// are 32 (2) chunks of N = 128.  The MMAs of a chunk write to tensor memory
+//   D[m][c] = [x_hi, 1, 1] . [-2c, |c|^2_hi, |c|^2_lo] + x_lo . (-2c) = |c|^2 - 2 x . c,
+// the screened distance less the subvector's own |x'_j|^2, with x_hi + x_lo the
+// transformed subvector in two fp16 parts (A) and the [-2c, |c|^2_hi, |c|^2_lo]
 // table of all the KV head's centroids (B) in shared memory behind matrix
-// descriptors.  Its error is bounded by screen_eps_hi.  (A second MMA with
-// the fp16 remainder of x' would tighten the bound but doubles the shared
-// memory and tensor memory traffic, which bound this kernel.)
+// descriptors.  Its error is bounded by screen_eps.  With four channels the low
+// parts fit into the MMA's 16 (B holds -2c twice); with eight they are a second
+// MMA.  (x_hi alone, one MMA, leaves 2^-10 |x'| |c|, ten times the margin: several
+// lanes of every warp then have a second group to re-rank, each of them the whole
+// warp's work, and that took half of the kernel's time.)
 //
 // Roles (12 warps, one CTA per SM, persistent over the KV head's tiles; 12
 // warps leave each SM sub-partition 3 warps, so up to 168 registers a thread,
@@ -519,9 +521,9 @@ constexpr int N = 128;                        // centroids per MMA
 constexpr int NBUF = 2;                       // tensor-memory buffers per epilogue warpgroup
 constexpr int GROUP = 32;                     // centroids per group minimum
 constexpr int STAGES = 4;
-constexpr int PROD_WARPS = 2;
-constexpr int MMA_WARP = 8 + PROD_WARPS;      // 10 (warpgroup 0's issuer; 11: warpgroup 1's)
-constexpr int THREADS = (MMA_WARP + 2) * 32;  // 384
+constexpr int PROD_WARPS = 4;
+constexpr int MMA_WARP = 8 + PROD_WARPS;      // 12 (warpgroup 0's issuer; 13: warpgroup 1's)
+constexpr int THREADS = (MMA_WARP + 2) * 32;  // 448
 constexpr int A_BYTES = M * 32;               // one A tile: 128 x 16 fp16
 constexpr int NBAR = 2 * STAGES + 4 * NBUF + 2;   // A full / empty, tensor-memory full / empty, MMAs done x 2
 constexpr uint32_t TMEM_COLS = 512;           // 2 warpgroups x NBUF buffers x N
@@ -542,7 +544,9 @@ struct UmGeo {
   static constexpr int ROWS = um::M / SUBV;               // rows per tile
   static constexpr int CHUNKS = E / um::N;               // MMAs per tile
   static constexpr int TABLE_BYTES = E * 32;             // B: E centroids x 16 fp16
-  static constexpr int ST_A = 0, ST_X = um::A_BYTES;
+  // A's fp16 low parts: behind the high ones in the MMA's own 16 channels (4-channel
+  // subvectors), or a tile of their own
+  static constexpr int ST_A = 0, ST_LOW = um::A_BYTES, ST_X = ST_LOW + (DSUB == 8 ? um::A_BYTES : 0);
   static constexpr int ST_NORM = ST_X + ROWS * kHeadDim * 4, ST_FLAG = ST_NORM + um::M * 4;
   static constexpr int ST_POS = ST_FLAG + um::M * 4;
   static constexpr int STAGE_BYTES = ST_POS + 16 * 4;   // + cache position, then sequence, of each row
@@ -558,18 +562,6 @@ struct UmGeo {
   static_assert(SMEM <= 227 * 1024 && STAGE_BYTES % 16 == 0 && OFF_BAR % 8 == 0, "UMMA encode shared memory");
   static_assert(CHUNKS % um::NBUF == 0 && E / um::GROUP <= 128 && ROWS <= 8, "tile plan (7-bit group ids)");
 };
-
-// Bound on |screened - exact| for one candidate of the single-MMA screen:
-// the fp16 rounding of x' leaves |x' - x_hi| <= 2^-11 |x'| per channel
-// (normal range; subnormal steps are covered by the absolute term), so
-// |2 (x' - x_hi) . c| <= 2^-10 |x'| |c|; the |c|^2 split, the tensor-core
-// fp32 accumulation and the exact search's own roundings are covered as in
-// screen_eps.
-__device__ __forceinline__ float screen_eps_hi(float xnorm, float cmax) {
-  const float sc = xnorm + cmax;
-  return 9.765625e-4f * xnorm * cmax + 4.76837158203125e-7f * cmax * cmax + 1e-6f * (cmax + 1.f) +
-         1.5e-5f * sc * sc;
-}
 
 // Bounded wait on an mbarrier phase by every lane of a warp (or one thread:
 // pass a one-lane mask): false, with the abort flag set, when it runs out
@@ -668,7 +660,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   constexpr int ST_POS = Geo::ST_POS, STAGE_BYTES = Geo::STAGE_BYTES, OFF_STAGES = Geo::OFF_STAGES;
   constexpr int OFF_BAR = Geo::OFF_BAR, OFF_MISC = Geo::OFF_MISC;
   extern __shared__ __align__(1024) unsigned char smem[];
-  Rows<APPEND> src(a, blockIdx.y);
+  Rows<APPEND> src(a);
   const EncodeParams& p = src.p;
   const int kvh = src.kvh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -705,7 +697,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   __syncthreads();
 
   // B table: row c = [-2c (8 fp16), |c|^2 hi, |c|^2 lo, 0 x 6] (1.5 bit) or
-  // [-2c (4 fp16), |c|^2 hi, |c|^2 lo, 0 x 10] (2 bit)
+  // [-2c (4 fp16), |c|^2 hi, |c|^2 lo, 0, 0, -2c, 0 x 4] (2 bit)
   {
     float cmax = 0.f;
     for (int c = threadIdx.x; c < E; c += THREADS) {
@@ -737,7 +729,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         *reinterpret_cast<uint4*>(row + 128) = make_uint4(tw, 0u, 0u, 0u);
       } else {
         *reinterpret_cast<uint4*>(row) = make_uint4(m2[0], m2[1], tw, 0u);
-        *reinterpret_cast<uint4*>(row + 128) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(row + 128) = make_uint4(m2[0], m2[1], 0u, 0u);
         reinterpret_cast<uint2*>(smem + Geo::OFF_CB4)[c] = make_uint2(w[0], w[1]);
       }
       cmax = fmaxf(cmax, sqrtf(nn));
@@ -754,45 +746,59 @@ __global__ void __launch_bounds__(um::THREADS, 1)
 
   const int rows = src.count();
   const int tiles = (rows + ROWS - 1) / ROWS;
-  const int n_my = (int)blockIdx.x < tiles ? (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+  const int cta = src.cta(), ctas = src.ctas();
+  const int n_my = cta < tiles ? (tiles - cta + ctas - 1) / ctas : 0;
 
   if (warp >= 8 && warp < MMA_WARP) {
-    // ---------------- producers: rows pw, pw + 3, pw + 6 (< 8) of every tile.
+    // ---------------- producers: rows pw and pw + 4 (8-row tiles) of every tile.
     // The raw rows of tile k + 1 are loaded while tile k is transformed.
     const int pw = warp - 8;
     // 1.5 bit: lanes 2j, 2j + 1 hold subvector j; 2 bit: lane j holds subvector j
     const int j = DSUB == 8 ? lane >> 1 : lane, half = DSUB == 8 ? lane & 1 : 0;
-    constexpr int PR = (ROWS + PROD_WARPS - 1) / PROD_WARPS;   // rows per producer warp (4 / 2)
+    constexpr int PR = (ROWS + PROD_WARPS - 1) / PROD_WARPS;   // rows per producer warp (2 / 1)
     const bool key = p.role == VQKV_ROLE_K;
     const float4 s4 = key ? *reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 4 * lane)
                           : make_float4(1.f, 1.f, 1.f, 1.f);
     const float4 rs4 = make_float4(__frcp_rn(s4.x), __frcp_rn(s4.y), __frcp_rn(s4.z), __frcp_rn(s4.w));
     typename Rows<APPEND>::Raw raw[PR];
     RowPlace at[PR];   // t: cache position of the row, or -1 (no row / out of range)
-    auto fetch = [&](int k) {
-      const int gt = (int)blockIdx.x + k * (int)gridDim.x;
+    Turn turn[PR];
+    int angle[PR];     // of the tile after that
+    auto row_of = [&](int k, int i) {   // -1: none
+      const int r = pw + PROD_WARPS * i, row = (cta + k * ctas) * ROWS + r;
+      return r < ROWS && k < n_my && row < rows ? row : -1;
+    };
+    auto angles = [&](int k) {
+      if constexpr (APPEND) {
 #pragma unroll
-      for (int i = 0; i < PR; ++i) {
-        const int r = pw + PROD_WARPS * i, row = gt * ROWS + r;
-        at[i] = {0, -1, 0};
-        raw[i] = {};
-        if (r < ROWS && row < rows) {
-          at[i] = src.place(row, lane == 0);
-          if (at[i].t >= 0) raw[i] = src.load(row, lane);
+        for (int i = 0; i < PR; ++i) {
+          const int row = row_of(k, i);
+          angle[i] = row >= 0 ? src.angle(row) : 0;
         }
       }
     };
+    auto fetch = [&](int k) {
+#pragma unroll
+      for (int i = 0; i < PR; ++i) {
+        const int row = row_of(k, i);
+        at[i] = {0, -1, 0};
+        raw[i] = {};
+        if (row >= 0) {
+          at[i] = src.place(row, APPEND ? angle[i] : 0, lane == 0);
+          if (at[i].t >= 0) raw[i] = src.load(row, lane);
+        }
+        if constexpr (APPEND) turn[i] = src.turn(at[i].angle, lane);
+      }
+      angles(k + 1);
+    };
+    angles(0);
     if (n_my > 0) fetch(0);
     for (int k = 0; k < n_my; ++k) {
       typename Rows<APPEND>::Raw cur[PR];
       RowPlace w[PR];
       Turn turns[PR];
 #pragma unroll
-      for (int i = 0; i < PR; ++i) cur[i] = raw[i], w[i] = at[i];
-      if constexpr (APPEND) {
-#pragma unroll
-        for (int i = 0; i < PR; ++i) turns[i] = src.turn(w[i].angle, lane);
-      }
+      for (int i = 0; i < PR; ++i) cur[i] = raw[i], w[i] = at[i], turns[i] = turn[i];
       if (k + 1 < n_my) fetch(k + 1);
       const int s = k % STAGES;
       if (!um_wait(a_empty(s), ((k / STAGES) & 1) ^ 1, s_abort, p.err, 0xffffffffu)) break;
@@ -812,16 +818,20 @@ __global__ void __launch_bounds__(um::THREADS, 1)
           for (int e = 0; e < 4; ++e)
             if (!(fabsf(x[e]) < 32768.f)) flag = F_EXHAUSTIVE;
         }
+        uint32_t x01, x23, l01, l23;   // fp16 high and low parts
+        split_half2(x[0], x[1], x01, l01);
+        split_half2(x[2], x[3], x23, l23);
         if constexpr (DSUB == 8) {
           const uint32_t off = umma_kmajor_offset((uint32_t)m, 4u * half);
-          *reinterpret_cast<uint2*>(st + ST_A + off) = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
+          *reinterpret_cast<uint2*>(st + ST_A + off) = make_uint2(x01, x23);
           *reinterpret_cast<uint2*>(st + ST_A + off + 128) =
               make_uint2(half == 0 ? pack_half2(1.f, 1.f) : 0u, 0u);   // picks |c|^2 hi + lo
+          *reinterpret_cast<uint2*>(st + Geo::ST_LOW + off) = make_uint2(l01, l23);
+          *reinterpret_cast<uint2*>(st + Geo::ST_LOW + off + 128) = make_uint2(0u, 0u);
         } else {
           const uint32_t off = umma_kmajor_offset((uint32_t)m, 0u);
-          *reinterpret_cast<uint4*>(st + ST_A + off) =
-              make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(1.f, 1.f), 0u);
-          *reinterpret_cast<uint4*>(st + ST_A + off + 128) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(st + ST_A + off) = make_uint4(x01, x23, pack_half2(1.f, 1.f), 0u);
+          *reinterpret_cast<uint4*>(st + ST_A + off + 128) = make_uint4(l01, l23, 0u, 0u);
         }
         *reinterpret_cast<float4*>(st + ST_X + (r * kHeadDim + 4 * lane) * 4) = make_float4(x[0], x[1], x[2], x[3]);
         float nx = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
@@ -853,6 +863,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         const int s = k % STAGES;
         ok = um_wait(a_full(s), (k / STAGES) & 1, s_abort, p.err, 1u);
         const uint64_t dA = umma_desc_kmajor(sbase + OFF_STAGES + s * STAGE_BYTES + ST_A);
+        const uint64_t dLow = umma_desc_kmajor(sbase + OFF_STAGES + s * STAGE_BYTES + Geo::ST_LOW);
         tcgen05_after_sync();
         for (int q = 0; ok && q < CHUNKS; ++q) {
           const int bsel = q % NBUF;
@@ -860,8 +871,10 @@ __global__ void __launch_bounds__(um::THREADS, 1)
           ok = um_wait(t_empty(wg, bsel), (use & 1) ^ 1, s_abort, p.err, 1u);
           if (!ok) break;
           tcgen05_after_sync();
-          umma_f16(tmem + (uint32_t)((NBUF * wg + bsel) * N), dA, umma_desc_kmajor(sbase + (uint32_t)q * (N * 32)),
-                   idesc, 0u);
+          const uint64_t dB = umma_desc_kmajor(sbase + (uint32_t)q * (N * 32));
+          const uint32_t acc = tmem + (uint32_t)((NBUF * wg + bsel) * N);
+          umma_f16(acc, dA, dB, idesc, 0u);
+          if constexpr (DSUB == 8) umma_f16(acc, dLow, dB, idesc, 1u);
           umma_commit(t_full(wg, bsel));
         }
       }
@@ -949,7 +962,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
           xv[4] = b.x, xv[5] = b.y, xv[6] = b.z, xv[7] = b.w;
         }
       }
-      const float eps = screen_eps_hi(sqrtf(reinterpret_cast<const float*>(st + ST_NORM)[ml]), Cmax);
+      const float eps = screen_eps(sqrtf(reinterpret_cast<const float*>(st + ST_NORM)[ml]), Cmax);
       // a group can hold a candidate within 2 eps of the best when its packed
       // minimum is within 2 eps plus both packing errors (< 2^-16 of each
       // value) of the packed best
@@ -1012,7 +1025,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         if (lane == src) dex = d, cex = c, dsec = sd;   // every candidate: replaces the group search
       }
       count_near_ties(p.near_tie, flag != F_SKIP && is_near_tie(dex, dsec), lane, 0xffffffffu);
-      const int row = ((int)blockIdx.x + k * (int)gridDim.x) * ROWS + r;
+      const int row = (cta + k * ctas) * ROWS + r;
       int b;
       if constexpr (APPEND)
         b = reinterpret_cast<const int*>(st + ST_POS)[8 + r];
@@ -1093,7 +1106,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   int* s_hidden = reinterpret_cast<int*>(s_red + TC_WARPS * 16);  // [16]
   Best* s_fin = reinterpret_cast<Best*>(s_hidden + 16);           // [warp][16]
   Best* s_ex = s_fin + TC_WARPS * 16;                             // [warp] exhaustive partials
-  Rows<APPEND> src(a, blockIdx.y);
+  Rows<APPEND> src(a);
   const EncodeParams& p = src.p;
   const int kvh = src.kvh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1106,11 +1119,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   typename Rows<APPEND>::Raw xraw{};
   Turn turn{};
   float4 xs = make_float4(1.f, 1.f, 1.f, 1.f);
-  if (warp == 0 && (int)blockIdx.x < rows) {
-    xraw = src.load(blockIdx.x, lane);
+  if (warp == 0 && src.cta() < rows) {
+    xraw = src.load(src.cta(), lane);
     if (ks != nullptr) xs = *reinterpret_cast<const float4*>(ks + 4 * lane);
     if constexpr (APPEND) {
-      const RowPlace w = src.place(blockIdx.x, false);
+      const RowPlace w = src.place(src.cta(), src.angle(src.cta()), false);
       turn = src.turn(w.angle, lane);
     }
   }
@@ -1120,13 +1133,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const uint32_t tbl_lane = smem_u32(s_tbl) + (gid * 4 + tig) * 8;
   const float inf = __int_as_float(0x7f800000);
 
-  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-    const RowPlace w = src.place(r, threadIdx.x == 0);
+  for (int r = src.cta(); r < rows; r += src.ctas()) {
+    const RowPlace w = src.place(r, src.angle(r), threadIdx.x == 0);
     if (w.t < 0) continue;
     const int b = w.b, t = w.t;
     if (warp == 0) {
       float x[4];
-      if (r != (int)blockIdx.x) {
+      if (r != src.cta()) {
         xraw = src.load(r, lane);
         if constexpr (APPEND) turn = src.turn(w.angle, lane);
       }

@@ -102,9 +102,10 @@ struct AppendParams {
   const float* table;       // [n_table][rot] or nullptr
   const int32_t* rope_pos;  // [n_tokens] or nullptr: the cache positions
   int n_table, rot, interleaved;
+  int key_ctas;             // grid (CTAs of a KV head: first those of its keys, then of its values; Hkv)
 };
 cudaError_t append_prepare(int mode);
-cudaError_t launch_append(int mode, const AppendParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_append(int mode, AppendParams p, int sms, cudaStream_t stream);
 
 // Rotary positions (rope.cu).
 struct RopeTableParams {

@@ -67,9 +67,13 @@ struct Rows<false> {
   using Raw = uint2;
   const EncodeParams& p;
   const int kvh;
-  __device__ __forceinline__ Rows(const EncodeParams& a, int y) : p(a), kvh(y) {}
+  __device__ __forceinline__ explicit Rows(const EncodeParams& a) : p(a), kvh(blockIdx.y) {}
+  // This CTA's number among those that share its (KV head, role)'s rows.
+  __device__ __forceinline__ int cta() const { return (int)blockIdx.x; }
+  __device__ __forceinline__ int ctas() const { return (int)gridDim.x; }
   __device__ __forceinline__ int count() const { return p.B * p.n_rows; }
-  __device__ __forceinline__ RowPlace place(int r, bool report) {
+  __device__ __forceinline__ int angle(int) const { return 0; }
+  __device__ __forceinline__ RowPlace place(int r, int, bool report) {
     const int b = r / p.n_rows, n = r - b * p.n_rows;
     const int t = p.pos[b] + n;
     if (t < 0 || t >= p.cap_len) {
@@ -97,8 +101,8 @@ struct Rows<false> {
   }
 };
 
-// Grid y: the KV heads' keys, then their values.  Rows are the batch's tokens;
-// those behind the last sequence (and before the first) are padding.
+// Rows are the batch's tokens; those behind the last sequence (and before the
+// first) are padding.
 template <>
 struct Rows<true> {
   using Params = AppendParams;
@@ -107,13 +111,17 @@ struct Rows<true> {
   const EncodeParams& p;   // this CTA's role
   const int kvh;
   int b = 0, first = 0, last = 0, pos = 0;   // the sequence of the last row placed: its tokens, its first one's position
-  __device__ __forceinline__ Rows(const AppendParams& a_, int y)
-      : a(a_), p(a_.role[y >= a_.role[0].Hkv]), kvh(y >= a_.role[0].Hkv ? y - a_.role[0].Hkv : y) {}
+  __device__ __forceinline__ explicit Rows(const AppendParams& a_)
+      : a(a_), p(a_.role[(int)blockIdx.x >= a_.key_ctas ? VQKV_ROLE_V : VQKV_ROLE_K]), kvh(blockIdx.y) {}
+  __device__ __forceinline__ int cta() const { return (int)blockIdx.x - (p.role == VQKV_ROLE_V ? a.key_ctas : 0); }
+  __device__ __forceinline__ int ctas() const { return p.role == VQKV_ROLE_V ? (int)gridDim.x - a.key_ctas : a.key_ctas; }
   __device__ __forceinline__ int count() const { return a.n_tokens; }
   // Called by whole warps: the sequence is the last one that starts at or
   // before token r, found by 32 probes at a time.  Every index read lies in
   // [0, B] whatever the starts hold.
-  __device__ __forceinline__ RowPlace place(int r, bool report) {
+  // angle: that of token r (its load is a memory latency of its own).
+  __device__ __forceinline__ int angle(int r) const { return a.rope_pos != nullptr ? __ldg(a.rope_pos + r) : 0; }
+  __device__ __forceinline__ RowPlace place(int r, int angle, bool report) {
     if (!(first <= r && r < last)) {
       const int lane = threadIdx.x & 31;
       int lo = 0, hi = p.B;
@@ -133,10 +141,9 @@ struct Rows<true> {
     }
     const long long t = (long long)pos + ((long long)r - first);
     const bool in_cache = t >= 0 && t < p.cap_len;
-    int angle = 0;
     bool turns = true;
     if (a.table != nullptr) {
-      angle = a.rope_pos != nullptr ? __ldg(a.rope_pos + r) : in_cache ? (int)t : 0;
+      if (a.rope_pos == nullptr) angle = in_cache ? (int)t : 0;
       turns = angle >= 0 && angle < a.n_table;
     }
     if (!in_cache || !turns) {
