@@ -1168,19 +1168,17 @@ vqkv_status vqkv_append(const vqkv_append_args* a, const vqkv_paging* pg, void* 
   const vqkv_status st = device_info(kAppendKernels, a->mode, &di);
   if (st != VQKV_OK) return st;
   AppendParams p{};
-  for (int role = 0; role < 2; ++role) {
-    const StridedRows& x = role == VQKV_ROLE_K ? k : v;
-    EncodeParams& e = p.role[role];
-    e.s = role == VQKV_ROLE_K ? a->s : nullptr;
-    e.cb = reinterpret_cast<const __half*>(role == VQKV_ROLE_K ? a->k_codebook : a->v_codebook);
-    e.codes = role == VQKV_ROLE_K ? a->k_codes : a->v_codes;
-    e.near_tie = a->near_tie_count;
-    e.err = a->error_flags;
-    e.stream_bytes = (long long)vqkv_code_bytes(a->mode, a->cap_len);
-    e.B = a->B, e.Hkv = a->Hkv, e.cap_len = a->cap_len, e.role = role;
-    set_paging(e, pg, a->mode);
-    p.x[role] = x.base, p.token_stride[role] = x.token, p.head_stride[role] = x.head;
-  }
+  EncodeParams& e = p.both;
+  e.s = a->s;
+  e.near_tie = a->near_tie_count;
+  e.err = a->error_flags;
+  e.stream_bytes = (long long)vqkv_code_bytes(a->mode, a->cap_len);
+  e.B = a->B, e.Hkv = a->Hkv, e.cap_len = a->cap_len;
+  set_paging(e, pg, a->mode);
+  p.cb[VQKV_ROLE_K] = reinterpret_cast<const __half*>(a->k_codebook), p.cb[VQKV_ROLE_V] = reinterpret_cast<const __half*>(a->v_codebook);
+  p.codes[VQKV_ROLE_K] = a->k_codes, p.codes[VQKV_ROLE_V] = a->v_codes;
+  p.x[VQKV_ROLE_K] = k.base, p.token_stride[VQKV_ROLE_K] = k.token, p.head_stride[VQKV_ROLE_K] = k.head;
+  p.x[VQKV_ROLE_V] = v.base, p.token_stride[VQKV_ROLE_V] = v.token, p.head_stride[VQKV_ROLE_V] = v.head;
   p.dtype = a->dtype, p.n_tokens = a->n_tokens;
   p.row_start = a->row_start, p.pos = a->pos;
   p.table = a->rope_table, p.rope_pos = a->rope_pos;

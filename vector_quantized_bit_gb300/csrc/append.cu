@@ -55,7 +55,7 @@ cudaError_t append_prepare(int mode) {
 }
 
 cudaError_t launch_append(int mode, AppendParams p, int sms, cudaStream_t stream) {
-  const int Hkv = p.role[0].Hkv;
+  const int Hkv = p.both.Hkv;
   const AppendVariant v = variant(mode, (long long)p.n_tokens * 2 * Hkv <= sms);
   const int want = (p.n_tokens + v.rows - 1) / v.rows;   // CTAs of a KV head and role with work
   int keys = want, values = want;

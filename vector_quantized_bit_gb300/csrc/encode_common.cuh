@@ -165,7 +165,24 @@ __device__ __forceinline__ void transform_key_lean(uint2 raw, float4 s, float4 r
   transform_key_values(xv, s, rs, lane, x);
 }
 
-// The same, reading the lane's 4 fp16 channels and smoothing factors (keys
+// The key transform in plain fp32: scale = RN(RN(1 / s) / sqrt(128)), then the
+// butterflies.  Each channel is off the exact x' by at most kFastKey |x'| (the
+// row's norm): four roundings of 2^-24 up to the products, seven additions, and
+// sum |y_i| <= |x'| for y = x' . H / 128.
+constexpr float kFastKey = 13 * 5.9604644775390625e-8f;
+__device__ __forceinline__ void transform_key_fast(const float (&v)[4], float4 scale, int lane, float (&x)[4]) {
+  const float a = v[0] * scale.x, b = v[1] * scale.y, c = v[2] * scale.z, d = v[3] * scale.w;
+  const float ab = a + b, amb = a - b, cd = c + d, cmd = c - d;
+  x[0] = ab + cd, x[2] = ab - cd, x[1] = amb + cmd, x[3] = amb - cmd;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const float sign = (lane & m) ? -1.f : 1.f;   // lower lane: x + other, upper lane: other - x
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __fmaf_rn(x[i], sign, __shfl_xor_sync(0xffffffffu, x[i], m));
+  }
+}
+
+// transform_loaded, reading the lane's 4 fp16 channels and smoothing factors (keys
 // through transform_key_lean).
 __device__ __forceinline__ void transform_row(const __half* xrow, const float* s_row, int lane, float (&x)[4]) {
   const uint2 raw = *reinterpret_cast<const uint2*>(xrow + 4 * lane);

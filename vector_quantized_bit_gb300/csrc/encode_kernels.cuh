@@ -483,15 +483,14 @@ __device__ __forceinline__ float build_tc_table(const EncodeParams& p, int kvh, 
 // lanes of every warp then have a second group to re-rank, each of them the whole
 // warp's work, and that took half of the kernel's time.)
 //
-// Roles (12 warps, one CTA per SM, persistent over the KV head's tiles; 12
-// warps leave each SM sub-partition 3 warps, so up to 168 registers a thread,
-// enough for a whole 128-column chunk in flight per epilogue thread):
-//   warps 8, 9   producers: transform rows pw, pw + 2, ... of each tile
-//                (smoothing + Hadamard in double-float for keys), write
-//                A, x' and |x'_j|^2 into one of 4 stages;
-//   warps 10, 11 one thread each issues the MMAs of one epilogue warpgroup,
+// Roles (16 warps, one CTA per SM, persistent over the KV head's tiles; up to
+// 128 registers a thread, a 128-column chunk in flight per epilogue thread):
+//   warps 8-13   producers: transform every sixth row
+//                (smoothing + Hadamard for keys), write A, x', the key before
+//                the transform and |x'_j|^2 into one of 4 stages;
+//   warps 14, 15 one thread each issues the MMAs of one epilogue warpgroup,
 //                chunk by chunk into that warpgroup's two 128-column
-//                tensor-memory buffers (warp 10 also allocates the 512
+//                tensor-memory buffers (warp 14 also allocates the 512
 //                columns); separate issuers keep one warpgroup's wait for a
 //                free buffer from holding up the other's MMAs;
 //   warps 0-3, 4-7  two epilogue warpgroups taking alternate tiles: thread m
@@ -505,11 +504,16 @@ __device__ __forceinline__ float build_tc_table(const EncodeParams& p, int kvh, 
 // distance is within 2 eps of B1, so with B4 above that margin every
 // candidate lies in G1, G2 or G3 (the latter two only when B2, B3 are within
 // the margin): those groups are re-ranked with exact fp32 direct differences
-// (as exact_d8), the lowest index winning ties; G1 by each lane, the rarer
-// G2 / G3 by the whole warp, one lane's group at a time.  With B4 inside the
-// margin, or a row whose transformed values do not fit fp16, the warp
-// searches that subvector exhaustively.  Every decision therefore equals
-// the exhaustive fp32 search's.
+// (as exact_d8); G1 by each lane, the rarer G2 / G3 by the whole warp, one lane's
+// group at a time.  With B4 inside the margin, or a row whose transformed values
+// do not fit fp16, the warp searches that subvector exhaustively.
+//
+// Keys: the producers transform them in plain fp32 (60 instructions a row; in
+// double-float 450, which bound the kernel: 131,072 2-bit key rows took 299 us),
+// good to kFastKey of the row's norm.  Where the best two candidates lie closer
+// than that can move them, the warp transforms the row again in double-float and
+// searches exhaustively, the lowest index winning ties.  Every decision therefore
+// equals the exhaustive fp32 search's on the correctly rounded x'.
 //
 // Every wait is bounded: a wait that runs out sets VQKV_DEVERR_TIMEOUT (when
 // the caller passed an error word) and an abort flag that ends every role's
@@ -519,15 +523,14 @@ namespace um {
 constexpr int M = 128;                        // MMA rows: (row, subvector) pairs of a tile
 constexpr int N = 128;                        // centroids per MMA
 constexpr int NBUF = 2;                       // tensor-memory buffers per epilogue warpgroup
-constexpr int GROUP = 32;                     // centroids per group minimum
 constexpr int STAGES = 4;
-constexpr int PROD_WARPS = 4;
-constexpr int MMA_WARP = 8 + PROD_WARPS;      // 12 (warpgroup 0's issuer; 13: warpgroup 1's)
-constexpr int THREADS = (MMA_WARP + 2) * 32;  // 448
+constexpr int PROD_WARPS = 6;
+constexpr int MMA_WARP = 8 + PROD_WARPS;      // 14 (warpgroup 0's issuer; 15: warpgroup 1's)
+constexpr int THREADS = (MMA_WARP + 2) * 32;  // 512
 constexpr int A_BYTES = M * 32;               // one A tile: 128 x 16 fp16
 constexpr int NBAR = 2 * STAGES + 4 * NBUF + 2;   // A full / empty, tensor-memory full / empty, MMAs done x 2
 constexpr uint32_t TMEM_COLS = 512;           // 2 warpgroups x NBUF buffers x N
-static_assert(2 * NBUF * N <= (int)TMEM_COLS && N % GROUP == 0, "tensor-memory plan");
+static_assert(2 * NBUF * N <= (int)TMEM_COLS, "tensor-memory plan");
 constexpr uint32_t MAX_POLLS = 1u << 22;
 // row flags
 constexpr int F_OK = 0, F_EXHAUSTIVE = 1, F_SKIP = 2;
@@ -544,12 +547,16 @@ struct UmGeo {
   static constexpr int ROWS = um::M / SUBV;               // rows per tile
   static constexpr int CHUNKS = E / um::N;               // MMAs per tile
   static constexpr int TABLE_BYTES = E * 32;             // B: E centroids x 16 fp16
+  // Centroids per group minimum.  16: half as many to re-rank, twice the minima to
+  // keep; pays up to 1,024 centroids.
+  static constexpr int GROUP = E == 4096 ? 32 : 16;
   // A's fp16 low parts: behind the high ones in the MMA's own 16 channels (4-channel
   // subvectors), or a tile of their own
   static constexpr int ST_A = 0, ST_LOW = um::A_BYTES, ST_X = ST_LOW + (DSUB == 8 ? um::A_BYTES : 0);
-  static constexpr int ST_NORM = ST_X + ROWS * kHeadDim * 4, ST_FLAG = ST_NORM + um::M * 4;
+  static constexpr int ST_ROW = ST_X + ROWS * kHeadDim * 4;   // a key's values before the transform
+  static constexpr int ST_NORM = ST_ROW + ROWS * kHeadDim * 4, ST_FLAG = ST_NORM + um::M * 4;
   static constexpr int ST_POS = ST_FLAG + um::M * 4;
-  static constexpr int STAGE_BYTES = ST_POS + 16 * 4;   // + cache position, then sequence, of each row
+  static constexpr int STAGE_BYTES = ST_POS + 24 * 4;   // + each row's cache position, sequence, error of x'
   static constexpr int OFF_STAGES = TABLE_BYTES;
   static constexpr int OFF_BAR = OFF_STAGES + um::STAGES * STAGE_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + um::NBAR * 8;   // tensor-memory base, abort flag, max centroid norm
@@ -560,7 +567,7 @@ struct UmGeo {
   static constexpr int OFF_CB4 = OFF_MISC + 16;
   static constexpr size_t SMEM = OFF_CB4 + (DSUB == 4 ? E * 8 : 0);
   static_assert(SMEM <= 227 * 1024 && STAGE_BYTES % 16 == 0 && OFF_BAR % 8 == 0, "UMMA encode shared memory");
-  static_assert(CHUNKS % um::NBUF == 0 && E / um::GROUP <= 128 && ROWS <= 8, "tile plan (7-bit group ids)");
+  static_assert(CHUNKS % um::NBUF == 0 && E / GROUP <= 128 && um::N % GROUP == 0 && ROWS <= 8, "tile plan (7-bit group ids)");
 };
 
 // Bounded wait on an mbarrier phase by every lane of a warp (or one thread:
@@ -617,6 +624,13 @@ __device__ __forceinline__ float exact_d_umma(const float (&x)[D], const unsigne
   return d;
 }
 
+// Square root to about 2^-22, for bounds that allow for it.
+__device__ __forceinline__ float approx_sqrt(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Exact search state: best distance and index, second-best distance.
 // Candidates may come in any index order: lower distance, then lower index.
 __device__ __forceinline__ void exact_push(float d, int c, float& dex, int& cex, float& dsec) {
@@ -655,7 +669,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
     encode_umma_kernel(const __grid_constant__ typename Rows<APPEND>::Params a) {
   using namespace um;
   using Geo = UmGeo<MODE>;
-  constexpr int DSUB = Geo::DSUB, E = Geo::E, SUBV = Geo::SUBV, ROWS = Geo::ROWS, CHUNKS = Geo::CHUNKS;
+  constexpr int DSUB = Geo::DSUB, GROUP = Geo::GROUP, E = Geo::E, SUBV = Geo::SUBV, ROWS = Geo::ROWS, CHUNKS = Geo::CHUNKS;
   constexpr int ST_A = Geo::ST_A, ST_X = Geo::ST_X, ST_NORM = Geo::ST_NORM, ST_FLAG = Geo::ST_FLAG;
   constexpr int ST_POS = Geo::ST_POS, STAGE_BYTES = Geo::STAGE_BYTES, OFF_STAGES = Geo::OFF_STAGES;
   constexpr int OFF_BAR = Geo::OFF_BAR, OFF_MISC = Geo::OFF_MISC;
@@ -677,7 +691,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(a_full(s), PROD_WARPS);
+      mbar_init(a_full(s), ROWS);
       mbar_init(a_empty(s), 4);
     }
     for (int wg = 0; wg < 2; ++wg)
@@ -750,68 +764,64 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   const int n_my = cta < tiles ? (tiles - cta + ctas - 1) / ctas : 0;
 
   if (warp >= 8 && warp < MMA_WARP) {
-    // ---------------- producers: rows pw and pw + 4 (8-row tiles) of every tile.
-    // The raw rows of tile k + 1 are loaded while tile k is transformed.
+    // ---------------- producers
     const int pw = warp - 8;
     // 1.5 bit: lanes 2j, 2j + 1 hold subvector j; 2 bit: lane j holds subvector j
     const int j = DSUB == 8 ? lane >> 1 : lane, half = DSUB == 8 ? lane & 1 : 0;
-    constexpr int PR = (ROWS + PROD_WARPS - 1) / PROD_WARPS;   // rows per producer warp (2 / 1)
     const bool key = p.role == VQKV_ROLE_K;
     const float4 s4 = key ? *reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 4 * lane)
                           : make_float4(1.f, 1.f, 1.f, 1.f);
-    const float4 rs4 = make_float4(__frcp_rn(s4.x), __frcp_rn(s4.y), __frcp_rn(s4.z), __frcp_rn(s4.w));
-    typename Rows<APPEND>::Raw raw[PR];
-    RowPlace at[PR];   // t: cache position of the row, or -1 (no row / out of range)
-    Turn turn[PR];
-    int angle[PR];     // of the tile after that
-    auto row_of = [&](int k, int i) {   // -1: none
-      const int r = pw + PROD_WARPS * i, row = (cta + k * ctas) * ROWS + r;
-      return r < ROWS && k < n_my && row < rows ? row : -1;
+    constexpr float kNorm = 0.08838834764831845f;   // 1 / sqrt(128)
+    const float4 scale = make_float4(__frcp_rn(s4.x) * kNorm, __frcp_rn(s4.y) * kNorm, __frcp_rn(s4.z) * kNorm,
+                                     __frcp_rn(s4.w) * kNorm);
+    // Row job i is row i % ROWS of tile i / ROWS; warp pw takes jobs pw, pw +
+    // PROD_WARPS, ...  A job's row is loaded one job ahead, its angle two.
+    const int jobs = n_my * ROWS;
+    typename Rows<APPEND>::Raw raw{};
+    RowPlace at{};
+    Turn turn{};
+    int angle = 0;
+    auto row_of = [&](int job) {   // -1: none
+      const int row = (cta + job / ROWS * ctas) * ROWS + job % ROWS;
+      return job < jobs && row < rows ? row : -1;
     };
-    auto angles = [&](int k) {
+    auto next_angle = [&](int job) {
       if constexpr (APPEND) {
-#pragma unroll
-        for (int i = 0; i < PR; ++i) {
-          const int row = row_of(k, i);
-          angle[i] = row >= 0 ? src.angle(row) : 0;
-        }
+        const int row = row_of(job);
+        if (row >= 0) angle = src.angle(row);
       }
     };
-    auto fetch = [&](int k) {
-#pragma unroll
-      for (int i = 0; i < PR; ++i) {
-        const int row = row_of(k, i);
-        at[i] = {0, -1, 0};
-        raw[i] = {};
-        if (row >= 0) {
-          at[i] = src.place(row, APPEND ? angle[i] : 0, lane == 0);
-          if (at[i].t >= 0) raw[i] = src.load(row, lane);
-        }
-        if constexpr (APPEND) turn[i] = src.turn(at[i].angle, lane);
+    auto fetch = [&](int job) {
+      const int row = row_of(job);
+      at = {0, -1, 0};
+      if (row >= 0) {
+        at = src.place(row, angle, lane == 0);
+        if (at.t >= 0) raw = src.load(row, lane);
       }
-      angles(k + 1);
+      if constexpr (APPEND) turn = src.turn(at.angle, lane);
+      next_angle(job + PROD_WARPS);
     };
-    angles(0);
-    if (n_my > 0) fetch(0);
-    for (int k = 0; k < n_my; ++k) {
-      typename Rows<APPEND>::Raw cur[PR];
-      RowPlace w[PR];
-      Turn turns[PR];
-#pragma unroll
-      for (int i = 0; i < PR; ++i) cur[i] = raw[i], w[i] = at[i], turns[i] = turn[i];
-      if (k + 1 < n_my) fetch(k + 1);
-      const int s = k % STAGES;
+    next_angle(pw);
+    fetch(pw);
+    for (int job = pw; job < jobs; job += PROD_WARPS) {
+      const typename Rows<APPEND>::Raw cur = raw;
+      const RowPlace w = at;
+      const Turn u = turn;
+      fetch(job + PROD_WARPS);
+      const int k = job / ROWS, r = job % ROWS, s = k % STAGES;
       if (!um_wait(a_empty(s), ((k / STAGES) & 1) ^ 1, s_abort, p.err, 0xffffffffu)) break;
       unsigned char* st = smem + OFF_STAGES + s * STAGE_BYTES;
-#pragma unroll
-      for (int i = 0; i < PR; ++i) {
-        const int r = pw + PROD_WARPS * i;
-        if (r >= ROWS) break;
+      {
         const int m = SUBV * r + j;
         int flag = F_SKIP;
         float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (w[i].t >= 0) {
-          src.transform(cur[i], turns[i], s4, rs4, lane, x);
+        if (w.t >= 0) {
+          src.values(cur, u, lane, x);
+          if (key) {
+            *reinterpret_cast<float4*>(st + Geo::ST_ROW + (r * kHeadDim + 4 * lane) * 4) = make_float4(x[0], x[1], x[2], x[3]);
+            const float v[4] = {x[0], x[1], x[2], x[3]};
+            transform_key_fast(v, scale, lane, x);
+          }
           // beyond fp16 screening (or not finite), or a codebook beyond the table: exhaustive
           flag = Cmax <= kScreenCmax ? F_OK : F_EXHAUSTIVE;
 #pragma unroll
@@ -835,6 +845,11 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         }
         *reinterpret_cast<float4*>(st + ST_X + (r * kHeadDim + 4 * lane) * 4) = make_float4(x[0], x[1], x[2], x[3]);
         float nx = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+        float row = nx;   // |x'|^2
+        if (key) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) row += __shfl_xor_sync(0xffffffffu, row, o);
+        }
         if constexpr (DSUB == 8) {
           nx += __shfl_xor_sync(0xffffffffu, nx, 1);   // |x'_j|^2
           flag = max(flag, __shfl_xor_sync(0xffffffffu, flag, 1));
@@ -844,8 +859,9 @@ __global__ void __launch_bounds__(um::THREADS, 1)
           reinterpret_cast<int*>(st + ST_FLAG)[m] = flag;
         }
         if (lane == 0) {
-          reinterpret_cast<int*>(st + ST_POS)[r] = w[i].t;
-          if constexpr (APPEND) reinterpret_cast<int*>(st + ST_POS)[8 + r] = w[i].b;
+          reinterpret_cast<int*>(st + ST_POS)[r] = w.t;
+          if constexpr (APPEND) reinterpret_cast<int*>(st + ST_POS)[8 + r] = w.b;
+          reinterpret_cast<float*>(st + ST_POS)[16 + r] = key ? kFastKey * sqrtf(row) : 0.f;
         }
       }
       fence_proxy_async_smem();
@@ -933,20 +949,26 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         const uint32_t col = t_lane + (uint32_t)((NBUF * wg + bsel) * N);
         // the whole chunk in flight at once (one wait); the buffer is handed
         // back before the values are reduced
-        float v0[32], v1[32], v2[32], v3[32];
-        float g0 = inf, g1 = inf, g2 = inf, g3 = inf;
-        tmem_ld32_min(col, v0, g0);
-        tmem_ld32_min(col + 32, v1, g1);
-        tmem_ld32_min(col + 64, v2, g2);
-        tmem_ld32_min(col + 96, v3, g3);
-        tmem_wait_ld();
+        constexpr int GROUPS = N / GROUP;
+        float g[GROUPS];
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) g[i] = inf;
+        if constexpr (GROUP == 32) {
+          float v[GROUPS][32];
+#pragma unroll
+          for (int i = 0; i < GROUPS; ++i) tmem_ld32_min(col + 32 * i, v[i], g[i]);
+          tmem_wait_ld();
+        } else {
+          float v[GROUPS][16];
+#pragma unroll
+          for (int i = 0; i < GROUPS; ++i) tmem_ld16_min(col + 16 * i, v[i], g[i]);
+          tmem_wait_ld();
+        }
         tcgen05_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(t_empty(wg, bsel));
-        group(g0, 4u * q);
-        group(g1, 4u * q + 1u);
-        group(g2, 4u * q + 2u);
-        group(g3, 4u * q + 3u);
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) group(g[i], (uint32_t)(GROUPS * q + i));
       }
       if (!ok) break;
       const int s = k % STAGES;
@@ -962,7 +984,12 @@ __global__ void __launch_bounds__(um::THREADS, 1)
           xv[4] = b.x, xv[5] = b.y, xv[6] = b.z, xv[7] = b.w;
         }
       }
-      const float eps = screen_eps(sqrtf(reinterpret_cast<const float*>(st + ST_NORM)[ml]), Cmax);
+      // off: how far x' may be from the exact one, per channel.  A distance moves by
+      // 2 off sqrt(DSUB) times its root then; in terms of |x'| and Cmax, for the
+      // groups that have to be looked at:
+      const float off = reinterpret_cast<const float*>(st + ST_POS)[16 + r] * (DSUB == 8 ? 2.8284272f : 2.f);
+      const float xnorm = approx_sqrt(reinterpret_cast<const float*>(st + ST_NORM)[ml]);
+      const float eps = screen_eps(xnorm, Cmax) + 4.f * off * (xnorm + Cmax);
       // a group can hold a candidate within 2 eps of the best when its packed
       // minimum is within 2 eps plus both packing errors (< 2^-16 of each
       // value) of the packed best
@@ -972,46 +999,83 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       const int G1 = (int)(__float_as_uint(B1) & 0x7Fu);
       float dex = __int_as_float(0x7f800000), dsec = dex;
       int cex = 0x7fffffff;
-      // group G1 by each lane; lane l visits its group's centroids from the
-      // (l % 8)-th on (1.5 bit: a centroid's 16 bytes sit in bank group c % 8,
-      // so the 32 lanes spread over all 8 bank groups at every step) or the
-      // (l % 16)-th on (2 bit: 8 bytes at bank pair c % 16)
+      // group G1 by each lane; lane l visits its group's centroids in the order i ^ l
+      // of their low bits: 8-byte centroids (bank pair c % 16) and 16-byte ones (bank
+      // group c % 8) then fall on distinct banks at every step
       {
-        const int rot = lane & (DSUB == 8 ? 7 : 15);
-#pragma unroll 8
+        const int c0 = GROUP * G1, rot = lane & (DSUB == 8 ? 7 : 15);
+        int best = 0;
+#pragma unroll 16
         for (int i = 0; i < GROUP; ++i) {
-          const int c = GROUP * G1 + ((i + rot) & (GROUP - 1));
-          exact_push(exact(xv, c), c, dex, cex, dsec);
+          const float d = exact(xv, c0 + (i ^ rot));
+          best = d < dex ? i : best;
+          dsec = fminf(dsec, fmaxf(dex, d));
+          dex = fminf(dex, d);
         }
+        cex = c0 + (best ^ rot);
       }
-      // groups G2 / G3 (few lanes) by the whole warp, one (lane, group) at a
-      // time, one centroid per lane; exhaustive searches likewise
+      // groups G2 / G3 (few lanes) by the whole warp, one lane's at a time, one
+      // centroid per lane
+      auto rerank = [&](const float (&xs)[DSUB], int g, float& d, int& c, float& sd) {
+        sd = inf;
+        c = GROUP * g + (lane & (GROUP - 1));
+        d = lane < GROUP ? exact(xs, c) : inf;
+        exact_warp_reduce(d, c, sd);
+      };
+      auto group_of = [&](float X, int src_lane) { return __shfl_sync(0xffffffffu, (int)(__float_as_uint(X) & 0x7Fu), src_lane); };
       const unsigned m2 = __ballot_sync(0xffffffffu, need2), m3 = __ballot_sync(0xffffffffu, need3);
-      unsigned mx = __ballot_sync(0xffffffffu, exh);
       for (int pass = 0; pass < 2; ++pass) {
         unsigned mset = pass == 0 ? m2 : m3;
-        const float Bp = pass == 0 ? B2 : B3;
         while (mset) {
-          const int src = __ffs(mset) - 1;
+          const int src_lane = __ffs(mset) - 1;
           mset &= mset - 1;
-          const int g = __shfl_sync(0xffffffffu, (int)(__float_as_uint(Bp) & 0x7Fu), src);
-          float xs[DSUB];
+          float xs[DSUB], d, sd;
+          int c;
 #pragma unroll
-          for (int i = 0; i < DSUB; ++i) xs[i] = __shfl_sync(0xffffffffu, xv[i], src);
-          float d = exact(xs, GROUP * g + lane), sd = __int_as_float(0x7f800000);
-          int c = GROUP * g + lane;
-          exact_warp_reduce(d, c, sd);
-          if (lane == src) exact_merge(d, c, sd, dex, cex, dsec);
+          for (int i = 0; i < DSUB; ++i) xs[i] = __shfl_sync(0xffffffffu, xv[i], src_lane);
+          rerank(xs, group_of(pass == 0 ? B2 : B3, src_lane), d, c, sd);
+          if (lane == src_lane) exact_merge(d, c, sd, dex, cex, dsec);
         }
       }
+      // The best two are the exact x's best two, in this order, if what x' is off by
+      // and the roundings of the distances cannot close the gap between them.  If
+      // they can (one subvector in some thousands; also equal distances, whose
+      // lowest index the loop above does not keep), its groups are ranked again with
+      // the exact x'.
+      const float gap = off * 2.f * (approx_sqrt(dex) + approx_sqrt(dsec)) + 2.f * off * off + (off > 0.f ? 5e-6f * dsec : 0.f);
+      unsigned mx = __ballot_sync(0xffffffffu, exh || (flag == F_OK && !(dsec - dex > gap)));
+      const unsigned mexh = __ballot_sync(0xffffffffu, exh);
       while (mx) {
-        const int src = __ffs(mx) - 1;
+        const int src_lane = __ffs(mx) - 1;
         mx &= mx - 1;
         float xs[DSUB];
+        if (p.role == VQKV_ROLE_K) {   // the lane's row, transformed by the whole warp
+          const int rr = __shfl_sync(0xffffffffu, r, src_lane), jj = __shfl_sync(0xffffffffu, j, src_lane);
+          const float4 raw = *reinterpret_cast<const float4*>(st + Geo::ST_ROW + (rr * kHeadDim + 4 * lane) * 4);
+          const float4 s = __ldg(reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 4 * lane));
+          const float v[4] = {raw.x, raw.y, raw.z, raw.w};
+          float x[4];
+          transform_key_values(v, s, make_float4(__frcp_rn(s.x), __frcp_rn(s.y), __frcp_rn(s.z), __frcp_rn(s.w)), lane, x);
 #pragma unroll
-        for (int i = 0; i < DSUB; ++i) xs[i] = __shfl_sync(0xffffffffu, xv[i], src);
-        float d = __int_as_float(0x7f800000), sd = d;
+          for (int i = 0; i < DSUB; ++i) xs[i] = __shfl_sync(0xffffffffu, x[i & 3], DSUB / 4 * jj + i / 4);
+        } else {
+#pragma unroll
+          for (int i = 0; i < DSUB; ++i) xs[i] = __shfl_sync(0xffffffffu, xv[i], src_lane);
+        }
+        float d = inf, sd = inf;
         int c = 0x7fffffff;
+        if (!((mexh >> src_lane) & 1)) {
+          rerank(xs, group_of(B1, src_lane), d, c, sd);
+          for (int pass = 0; pass < 2; ++pass)
+            if (((pass == 0 ? m2 : m3) >> src_lane) & 1) {
+              float d2, sd2;
+              int c2;
+              rerank(xs, group_of(pass == 0 ? B2 : B3, src_lane), d2, c2, sd2);
+              exact_merge(d2, c2, sd2, d, c, sd);
+            }
+          if (lane == src_lane) dex = d, cex = c, dsec = sd;
+          continue;
+        }
         if (!(Cmax <= kScreenCmax)) {   // centroids beyond the table: from global memory
           const __half* cb_head = p.cb + (size_t)kvh * E * DSUB;
           for (int cc = lane; cc < E; cc += 32) {
@@ -1022,7 +1086,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
           for (int cc = lane; cc < E; cc += 32) exact_push(exact(xs, cc), cc, d, c, sd);
         }
         exact_warp_reduce(d, c, sd);
-        if (lane == src) dex = d, cex = c, dsec = sd;   // every candidate: replaces the group search
+        if (lane == src_lane) dex = d, cex = c, dsec = sd;   // every candidate: replaces the group search
       }
       count_near_ties(p.near_tie, flag != F_SKIP && is_near_tie(dex, dsec), lane, 0xffffffffu);
       const int row = (cta + k * ctas) * ROWS + r;

@@ -92,7 +92,9 @@ struct EncodeParams {
 
 // Ragged append (append.cu): both roles' rows as they come out of a projection.
 struct AppendParams {
-  EncodeParams role[2];     // K, V; x and pos are those below
+  EncodeParams both;        // what the roles share (s: the keys')
+  const __half* cb[2];      // [Hkv][E][d_sub], of K and of V
+  uint8_t* codes[2];
   const void* x[2];         // token t, head h of role r: x[r] + t * token_stride[r] + h * head_stride[r] elements
   long long token_stride[2], head_stride[2];
   int dtype;                // vqkv_dtype

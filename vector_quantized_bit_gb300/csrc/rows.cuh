@@ -38,10 +38,10 @@ __device__ __forceinline__ float turned(float x, float c, float q, float s) {
   return __fadd_rn(sum.h, __fadd_rn(sum.l, __fadd_rn(pe, re)));
 }
 
-// Four consecutive values of any type the calls take.
-__device__ __forceinline__ uint4 load_four(const void* x, long long at, int dtype) {
-  if (dtype == VQKV_DTYPE_F32) return __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at));
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + at));
+// The lane's four values of a row of any type the calls take.
+__device__ __forceinline__ uint4 load_four(const char* row, int lane, int dtype) {
+  if (dtype == VQKV_DTYPE_F32) return __ldg(reinterpret_cast<const uint4*>(row) + lane);
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(row) + lane);
   return make_uint4(v.x, v.y, 0u, 0u);
 }
 __device__ __forceinline__ void four_floats(uint4 raw, int dtype, float (&v)[4]) {
@@ -90,6 +90,11 @@ struct Rows<false> {
     return *reinterpret_cast<const uint2*>(row_ptr(r) + 4 * lane);
   }
   __device__ __forceinline__ Turn turn(int, int) const { return {}; }
+  __device__ __forceinline__ void values(Raw raw, const Turn&, int, float (&v)[4]) const {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+  }
   __device__ __forceinline__ void transform(Raw raw, const Turn&, float4 s, float4 rs, int lane, float (&x)[4]) const {
     if (p.role == VQKV_ROLE_K)
       transform_key_lean(raw, s, rs, lane, x);
@@ -108,11 +113,21 @@ struct Rows<true> {
   using Params = AppendParams;
   using Raw = uint4;
   const AppendParams& a;
-  const EncodeParams& p;   // this CTA's role
+  EncodeParams p;          // this CTA's role
   const int kvh;
+  const char* x;           // its rows
+  long long token_stride;  // bytes
   int b = 0, first = 0, last = 0, pos = 0;   // the sequence of the last row placed: its tokens, its first one's position
   __device__ __forceinline__ explicit Rows(const AppendParams& a_)
-      : a(a_), p(a_.role[(int)blockIdx.x >= a_.key_ctas ? VQKV_ROLE_V : VQKV_ROLE_K]), kvh(blockIdx.y) {}
+      : a(a_), p(a_.both), kvh(blockIdx.y) {
+    const int role = (int)blockIdx.x >= a.key_ctas ? VQKV_ROLE_V : VQKV_ROLE_K, bytes = a.dtype == VQKV_DTYPE_F32 ? 4 : 2;
+    p.role = role;
+    p.s = role == VQKV_ROLE_K ? p.s : nullptr;
+    p.cb = a.cb[role];
+    p.codes = a.codes[role];
+    x = static_cast<const char*>(a.x[role]) + (long long)kvh * a.head_stride[role] * bytes;
+    token_stride = a.token_stride[role] * bytes;
+  }
   __device__ __forceinline__ int cta() const { return (int)blockIdx.x - (p.role == VQKV_ROLE_V ? a.key_ctas : 0); }
   __device__ __forceinline__ int ctas() const { return p.role == VQKV_ROLE_V ? (int)gridDim.x - a.key_ctas : a.key_ctas; }
   __device__ __forceinline__ int count() const { return a.n_tokens; }
@@ -153,8 +168,7 @@ struct Rows<true> {
     return {b, (int)t, angle};
   }
   __device__ __forceinline__ Raw load(int r, int lane) const {
-    return load_four(a.x[p.role], (long long)r * a.token_stride[p.role] + (long long)kvh * a.head_stride[p.role] + 4 * lane,
-                     a.dtype);
+    return load_four(x + r * token_stride, lane, a.dtype);
   }
   __device__ __forceinline__ Turn turn(int angle, int lane) const {
     Turn u{make_float4(1.f, 1.f, 1.f, 1.f), make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -189,10 +203,14 @@ struct Rows<true> {
       v[2] = turned(v[2], u.c.z, q[2], u.s.z), v[3] = turned(v[3], u.c.w, q[3], u.s.w);
     }
   }
+  // A row's values as they are encoded: a key's after its rotation.
+  __device__ __forceinline__ void values(Raw raw, const Turn& u, int lane, float (&v)[4]) const {
+    four_floats(raw, a.dtype, v);
+    if (p.role == VQKV_ROLE_K && a.table != nullptr) rotate(v, u, lane);
+  }
   __device__ __forceinline__ void transform(Raw raw, const Turn& u, float4 s, float4 rs, int lane, float (&x)[4]) const {
-    four_floats(raw, a.dtype, x);
+    values(raw, u, lane, x);
     if (p.role != VQKV_ROLE_K) return;
-    if (a.table != nullptr) rotate(x, u, lane);
     const float v[4] = {x[0], x[1], x[2], x[3]};
     transform_key_values(v, s, rs, lane, x);
   }

@@ -164,6 +164,16 @@ __device__ __forceinline__ void tmem_ld32_min(uint32_t taddr, float (&v)[32], fl
       : "memory");
 }
 
+// The same over 16 columns.
+__device__ __forceinline__ void tmem_ld16_min(uint32_t taddr, float (&v)[16], float& m) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.min.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "+f"(m)
+      : "r"(taddr)
+      : "memory");
+}
+
 // The same with the maximum; m must be -inf on entry.
 __device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, float (&v)[32], float& m) {
   asm volatile(
