@@ -1015,7 +1015,7 @@ struct StridedRows {
 // Cross attention: shares of all items' units per KV head, one CTA per SM in one wave.
 struct CrossPlan {
   int n_splits = 1, layout = kOneTile;
-  bool wide_merge = false;   // many partials per item
+  int groups_max = 1;   // items of a sequence, at most
   size_t query_off = 0, partials_off = 0, ws_bytes = 0;
 };
 
@@ -1044,9 +1044,9 @@ vqkv_status plan_cross(const vqkv_cross_args* ac, CrossPlan* pl) {
   // items, and tiles of full sequences, at most
   const long long items = std::max<long long>(1, std::min(B * ((cols + width - 1) / width), ac->n_rows * g / width + B));
   const long long units = items * std::max(1, (a.max_seq_len + 63) / 64);
-  const long long want = a.num_splits > 0 ? std::min(a.num_splits, 1024) : di.sms / a.Hkv;
+  const long long want = a.num_splits > 0 ? std::min(a.num_splits, 1024) : (pl->layout == kTwoTiles ? 1 : 2) * (di.sms / a.Hkv);
   pl->n_splits = (int)std::max<long long>(1, std::min(want, units));
-  pl->wide_merge = pl->n_splits > 4 * items;
+  pl->groups_max = (int)((cols + width - 1) / width);
   pl->query_off = decode_ticket_region_bytes(a.B, a.Hkv * kTicketGroups);
   pl->partials_off = pl->query_off + round_up(cross_query_bytes(B, a.Hq, a.Hkv, ac->n_rows, pl->layout), 256);
   pl->ws_bytes = pl->partials_off;
@@ -1229,7 +1229,7 @@ vqkv_status vqkv_cross_attn(const vqkv_cross_args* ac, const vqkv_paging* pg, vo
   p.n_splits = pl.n_splits;
   p.max_polls = kTilePolls;
   for (int b0 = 0; b0 < a->B; b0 += kFlatMaxB)
-    if (launch_cross(a->mode, batch_part(p, b0, a->B), pl.layout, pl.wide_merge, ws + pl.query_off,
+    if (launch_cross(a->mode, batch_part(p, b0, a->B), pl.layout, pl.groups_max, ws + pl.query_off,
                      static_cast<cudaStream_t>(stream)) != cudaSuccess)
       return VQKV_ERR_CUDA;
   return VQKV_OK;

@@ -353,7 +353,8 @@ __device__ __forceinline__ void drain_products(const DecodeParams& p, bool issue
 // loaded PREFETCH of its tiles ahead into registers, block ids one further.
 // These warps meet the others only through the ring's barriers, so they run
 // ahead into the next piece while the others finish one.  False: a wait gave up.
-template <int MODE, int ROLE, bool PAGED, int TOK, int STAGES>
+// STREAM: every tile of the piece; it goes to one of the stages of parity `half`.
+template <int MODE, int ROLE, bool PAGED, int TOK, int STAGES, bool STREAM = false>
 __device__ __forceinline__ bool dequant_piece(const DecodeParams& p, int b, int kvh, int tile0, int n, int L, uint32_t done,
                                               const unsigned char* s_cb, unsigned char* ring, uint32_t full, uint32_t empty,
                                               int u, int half, int lane, volatile int* abort_flag) {
@@ -363,7 +364,8 @@ __device__ __forceinline__ bool dequant_piece(const DecodeParams& p, int b, int 
   const int last_group = (L + 15) >> 4;   // 16-token groups that hold tokens
   uint32_t w[PREFETCH][G::W];
   bool bad = false;
-  const int mine = (int)((done + half) & 1);   // its first tile
+  constexpr int NEXT = STREAM ? 1 : 2;
+  const int mine = STREAM ? 0 : (int)((done + half) & 1);   // its first tile
   // byte offset of the layout tile of this warp's group of tile t, -1 past the sequence
   const int t_end = min(n, (last_group - u + GROUPS - 1) / GROUPS - tile0);   // tiles whose group u holds tokens
   constexpr int STEP = TOK / G::LAYOUT_TOK * G::TILE_BYTES;
@@ -383,22 +385,23 @@ __device__ __forceinline__ bool dequant_piece(const DecodeParams& p, int b, int 
     }
   };
 #pragma unroll
-  for (int d = 0; d < PREFETCH; ++d) fetch(place(mine + 2 * d), w[d]);
-  long long next = place(mine + 2 * PREFETCH);
-  for (int t0 = mine; t0 < n; t0 += 2 * PREFETCH) {
+  for (int d = 0; d < PREFETCH; ++d) fetch(place(mine + NEXT * d), w[d]);
+  long long next = place(mine + NEXT * PREFETCH);
+  for (int t0 = mine; t0 < n; t0 += NEXT * PREFETCH) {
 #pragma unroll
     for (int d = 0; d < PREFETCH; ++d) {
-      const int t = t0 + 2 * d;
+      const int t = t0 + NEXT * d;
       if (t >= n) break;
-      const uint32_t k = done + t, st = k % STAGES;
+      const uint32_t k = done + t, st = STREAM ? 2 * (k % (STAGES / 2)) + half : k % STAGES;
+      const uint32_t round = STREAM ? k / (STAGES / 2) : k / STAGES;
       Centroids c;   // the gathers need no free stage: their latency overlaps the wait
       if constexpr (ROLE == VQKV_ROLE_K)
         gather_k<MODE>(s_cb, lane, w[d], c);
       else
         gather_v<MODE>(s_cb, lane, w[d], c);
       fetch(next, w[d]);
-      next = place(t + 2 * PREFETCH + 2);
-      if (!tr_wait(p, empty + 8 * st, ((k / STAGES) & 1) ^ 1, abort_flag)) return false;
+      next = place(t + NEXT * (PREFETCH + 1));
+      if (!tr_wait(p, empty + 8 * st, (round & 1) ^ 1, abort_flag)) return false;
       unsigned char* tile = ring + st * (TOK * 256);
       if constexpr (ROLE == VQKV_ROLE_K)
         put_k<MODE, TOK>(tile, u, lane, c);

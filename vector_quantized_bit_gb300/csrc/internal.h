@@ -172,12 +172,12 @@ cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned l
 
 // Cross attention (cross_attn.cu), B <= kFlatMaxB: n_splits shares per KV head;
 // partials [Hkv][2 n_splits][cross_cols(layout)].  layout: columns of an item,
-// as in the draft-tree attention.
+// as in the draft-tree attention; groups_max: items of a sequence, at most.
 enum TileLayout : int { kOneTile = 0, kTwoTiles = 1, kPairs = 2 };   // columns on the MMA rows
 int cross_cols(int layout);   // columns of an item, at most
 cudaError_t cross_prepare(int mode);
 size_t cross_query_bytes(int B, int Hq, int Hkv, int n_rows, int layout);
-cudaError_t launch_cross(int mode, const DecodeParams& p, int layout, bool wide_merge, void* qx, cudaStream_t stream);
+cudaError_t launch_cross(int mode, const DecodeParams& p, int layout, int groups_max, void* qx, cudaStream_t stream);
 
 // Attention weights of many columns (mass_tiles.cu); B <= kFlatMaxB, at most 64
 // columns.  image: scratch for the transformed queries, which are taken before

@@ -185,7 +185,13 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
                                                                      const uint4* qx) {
   using namespace tr;
   using G = Geo<MODE>;
-  using TM = Tmem<NQ>;
+  // Cross attention of items of one query tile: the softmax warpgroups work on two
+  // shares, each with items, tiles and half of the ring's stages of its own, so that
+  // one's passage to its next item (q', first tile, O) hides behind the other's
+  // products.  Tensor memory is dealt out as for two query tiles (P overlays S).
+  constexpr bool STREAMS = CROSS && NQ == 1;
+  constexpr int TQ = STREAMS ? 2 : NQ;
+  using TM = Tmem<TQ>;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -197,14 +203,15 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   static_assert(!PAIR || NQ == 1, "pairs take one query tile");
   constexpr int WCOLS = PAIR ? 16 : 32;   // columns of a warp
   const int active0 = (min(width, ROWS) + WCOLS - 1) / WCOLS;
-  const int active1 = NQ == 1 ? active0 : (max(width - ROWS, 0) + 31) >> 5;
+  const int active1 = STREAMS || NQ == 1 ? active0 : (max(width - ROWS, 0) + 31) >> 5;
   const int jobs = active1 > 0 ? 2 : 1;     // NQ 2: query tiles with columns
   const uint32_t bar = smem_u32(smem + G::BAR_OFF);
   // Per ring stage.  NQ 1: s_ready = K tile in place and the warpgroup's last
   // scores read, pv_ready = V tile and P in place (a tile's warpgroup follows
   // from its stage; one barrier each keeps the issuing warp at two waits per
   // tile).  NQ 2: s_ready = K tile, pv_ready = V tile.  Per softmax warpgroup:
-  // s_full, o_done, and for NQ 2 p_ready.
+  // s_full, o_done, and for NQ 2 p_ready.  (STREAMS: as NQ 2, stage 2 i + h is stream
+  // h's i-th.)
   constexpr uint32_t ST = G::STAGES;
   const uint32_t s_ready = bar, k_empty = bar + 32, pv_ready = bar + 64, v_empty = bar + 96;
   const uint32_t s_full = bar + 128, o_done = bar + 144, p_ready = bar + 160, all_done = bar + 176;
@@ -212,9 +219,9 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   int* s_pref = reinterpret_cast<int*>(smem + G::PREF_OFF);
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < ST; ++i) {
-      mbar_init(s_ready + 8 * i, (NQ == 1 ? 4 + active0 : 4) + ((int)i == p.withhold_stage));
+      mbar_init(s_ready + 8 * i, (TQ == 1 ? 4 + active0 : 4) + ((int)i == p.withhold_stage));
       mbar_init(k_empty + 8 * i, NQ == 1 ? 1 : jobs);
-      mbar_init(pv_ready + 8 * i, NQ == 1 ? 4 + active0 : 4);
+      mbar_init(pv_ready + 8 * i, TQ == 1 ? 4 + active0 : 4);
       mbar_init(v_empty + 8 * i, NQ == 1 ? 1 : jobs);
     }
     for (int i = 0; i < 2; ++i) {
@@ -237,7 +244,10 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   else
     flat_prefix<TOK / 16>(p, s_pref);
   auto pc = [&] {
-    if constexpr (CROSS)
+    // STREAMS: the stream of a softmax or dequantising warpgroup, or of an issuing warp
+    if constexpr (STREAMS)
+      return ItemPieces<TOK, COLS>(p, s_pref, 2 * split + (warp < MMA_WARP ? (warp >> 2) & 1 : warp & 1), p.n_splits);
+    else if constexpr (CROSS)
       return ItemPieces<TOK, COLS>(p, s_pref, split, p.n_splits);
     else
       return Pieces(s_pref, p.B, split, p.n_splits);
@@ -264,7 +274,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   // memory, and the last piece's state read out of it.  (With the dequantising
   // warps meeting there as well, which waits out a memory latency per piece, 64
   // sequences of up to 512 tokens took 54 us, not 49.)
-  constexpr int MEET = (SM_WARPS + 2) * 32;
+  constexpr int MEET = STREAMS ? (SM_WARPS / 2 + 1) * 32 : (SM_WARPS + 2) * 32;
   if (warp < SM_WARPS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SM));
     // ---------------- softmax warpgroup wg: thread = column c
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     const int cl = PAIR ? 16 * (warp & 3) + (lane & 15) : NQ == 1 ? row : wg * ROWS + row;
     const bool live = (warp & 3) < (wg ? active1 : active0);
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    if (NQ == 1 && live && lane == 0) mbar_arrive(s_ready + 8 * wg);   // no scores to read yet
+    if (TQ == 1 && live && lane == 0) mbar_arrive(s_ready + 8 * wg);   // no scores to read yet
     bool ok = live;   // no wait has given up
     for (int piece = 0; pc.next(); ++piece) {
       int col0 = grp0, nloc = width, row0 = 0;   // the piece's first column, its columns; CROSS: its sequence's first row
@@ -288,7 +298,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         qrow = ((size_t)pc.b * p.Hkv + kvh) * ((p.ncols + WCOLS - 1) / WCOLS) + (col0 + cl) / WCOLS;
       }
       const int c = col0 + cl;
-      if (live && (cl & ~(WCOLS - 1)) < nloc && (NQ == 2 || wg == 0)) {   // q' into tensor memory: lane = column
+      if (live && (cl & ~(WCOLS - 1)) < nloc && (TQ == 2 || wg == 0)) {   // q' into tensor memory: lane = column
         const uint4* q = qx + qrow * 16 * 32 + lane;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -303,7 +313,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         tmem_wait_st();
       }
       tcgen05_before_sync();
-      named_barrier_sync(2, MEET);
+      named_barrier_sync(STREAMS ? 2 + wg : 2, MEET);
       tcgen05_after_sync();
       float m = kMInit, l = 0.f;
       const int prefix = clamped_len(p, pc.b) - (CROSS ? 0 : p.M);   // tokens below it are visible to every column
@@ -314,9 +324,9 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           mask = tree_mask != nullptr ? tree_mask[(size_t)pc.b * p.M + q] : (2ull << q) - 1;
           if (p.M < 64) mask &= (1ull << p.M) - 1;
         }
-        ok = softmax_tiles_of<NQ, G::STAGES, PAIR>(p, pc, done, wg, t_lane, mask, prefix, s_full, s_ready, NQ == 1 ? pv_ready : p_ready,
+        ok = softmax_tiles_of<TQ, G::STAGES, PAIR>(p, pc, done, wg, t_lane, mask, prefix, s_full, s_ready, TQ == 1 ? pv_ready : p_ready,
                                   o_done, abort_flag, m, l);
-        if (NQ == 1) {   // this warpgroup's last tile of the piece, if it has one
+        if (TQ == 1) {   // this warpgroup's last tile of the piece, if it has one
           const int last = pc.n - 1 - (int)((done + pc.n - 1 + wg) & 1);
           if (ok && last >= 0) ok = tr_wait(p, o_done + 8 * wg, ((done + last) >> 1) & 1, abort_flag);
         } else if (ok) {
@@ -327,10 +337,10 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
       // NQ 1: the two warpgroups' states are merged.  Both O's rows are in the
       // same tensor-memory lanes, so each warp reads both and takes half of the
       // channels; the maxima and sums pass through shared memory.
-      const bool both = NQ == 1 && pc.n > 1;                        // both warpgroups had tiles
-      const uint32_t own = NQ == 1 ? done & 1 : (uint32_t)wg;       // the O of the piece's first tile
+      const bool both = TQ == 1 && pc.n > 1;                        // both warpgroups had tiles
+      const uint32_t own = TQ == 1 ? done & 1 : (uint32_t)wg;       // the O of the piece's first tile
       float fa = 1.f, fb = 0.f;
-      if constexpr (NQ == 1) {
+      if constexpr (TQ == 1) {
         float2* s_ml = reinterpret_cast<float2*>(smem + G::ML_OFF);
         s_ml[wg * ROWS + row] = make_float2(m, l);
         tcgen05_before_sync();
@@ -353,12 +363,12 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         float* box = reinterpret_cast<float*>(smem + G::BOX_OFF) + warp * (32 * 16);
         float* part;   // CROSS: a share has a piece that began before it, and one that ends behind it, at most
         if constexpr (CROSS)
-          part = p.partials + (((size_t)kvh * p.n_splits + split) * 2 + (pc.tile0 == 0)) * COLS * kPartialStride +
+          part = p.partials + (((size_t)kvh * p.n_splits + (STREAMS ? 2 * split + wg : split)) * 2 + (pc.tile0 == 0)) * COLS * kPartialStride +
                  (size_t)(c0 - col0) * kPartialStride;
         else
           part = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + split + pc.b) * p.ncols + c0) * kPartialStride;
 #pragma unroll 1
-        for (int q = NQ == 1 ? 4 * wg : 0; q < (NQ == 1 ? 4 * wg + 4 : 8); ++q) {
+        for (int q = TQ == 1 ? 4 * wg : 0; q < (TQ == 1 ? 4 * wg + 4 : 8); ++q) {
           uint32_t o[16], z[16];
           tmem_ld16(t_lane + T_O + kHeadDim * own + 16 * q, o);
           if (both) tmem_ld16(t_lane + T_O + kHeadDim * (own ^ 1) + 16 * q, z);
@@ -402,7 +412,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           }
           __syncwarp();
         }
-        if (cl < nloc && lane < WCOLS && (NQ == 2 || wg == 0)) {
+        if (cl < nloc && lane < WCOLS && (TQ == 2 || wg == 0)) {
           if (!whole)
             *reinterpret_cast<float2*>(part + lane * kPartialStride + 128) = make_float2(m, l);
           else if (!CROSS && p.stats != nullptr)
@@ -418,10 +428,10 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     for (bool ok = true; ok && pc.next();) {
       const int L = clamped_len(p, pc.b);
       if (dw < 8)
-        ok = dequant_piece<MODE, VQKV_ROLE_K, PAGED, TOK, G::STAGES>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::K_OFF,
+        ok = dequant_piece<MODE, VQKV_ROLE_K, PAGED, TOK, G::STAGES, STREAMS>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::K_OFF,
                                                                      s_ready, k_empty, u, half, lane, abort_flag);
       else
-        ok = dequant_piece<MODE, VQKV_ROLE_V, PAGED, TOK, G::STAGES>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::V_OFF,
+        ok = dequant_piece<MODE, VQKV_ROLE_V, PAGED, TOK, G::STAGES, STREAMS>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::V_OFF,
                                                                      pv_ready, v_empty, u, half, lane, abort_flag);
       done += pc.n;
     }
@@ -459,12 +469,12 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     };
     bool ok = true;
     while (warp < MMA_WARP + 2 && pc.next()) {
-      tcgen05_before_sync();
-      named_barrier_sync(2, MEET);
-      tcgen05_after_sync();
       const int n = pc.n;
       const int job = warp - MMA_WARP;
-      if (NQ == 1 && job == 0) {
+      tcgen05_before_sync();
+      named_barrier_sync(STREAMS ? 2 + job : 2, MEET);
+      tcgen05_after_sync();
+      if (TQ == 1 && job == 0) {
         for (int t = 0; ok && t < n; ++t) {
           const uint32_t k = done + t, st = k % ST;
           if (!(ok = tr_wait(p, s_ready + 8 * st, (k / ST) & 1, abort_flag))) break;
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           }
           __syncwarp();
         }
-      } else if (NQ == 1 && job == 1) {
+      } else if (TQ == 1 && job == 1) {
         for (int t = 0; ok && t < n; ++t) {
           const uint32_t k = done + t, st = k % ST;
           if (!(ok = tr_wait(p, pv_ready + 8 * st, (k / ST) & 1, abort_flag))) break;
@@ -487,12 +497,15 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           }
           __syncwarp();
         }
-      } else if (NQ == 2 && job < jobs) {
+      } else if (TQ == 2 && job < jobs) {
+        // stage and use of it of tile j
+        auto stage = [&](uint32_t j) { return STREAMS ? 2 * (j % (ST / 2)) + job : j % ST; };
+        auto round = [&](uint32_t j) { return STREAMS ? j / (ST / 2) : j / ST; };
         for (int t = 0; ok && t <= n; ++t) {   // P.V of tile t - 1, then S of tile t
           const uint32_t k = done + t;
           if (t > 0) {
-            const uint32_t j = k - 1, st = j % ST;
-            ok = tr_wait(p, pv_ready + 8 * st, (j / ST) & 1, abort_flag) &&
+            const uint32_t j = k - 1, st = stage(j);
+            ok = tr_wait(p, pv_ready + 8 * st, round(j) & 1, abort_flag) &&
                  tr_wait(p, p_ready + 8 * job, j & 1, abort_flag);
             if (!ok) break;
             tcgen05_after_sync();
@@ -504,8 +517,8 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
             __syncwarp();
           }
           if (t < n) {
-            const uint32_t st = k % ST;
-            if (!(ok = tr_wait(p, s_ready + 8 * st, (k / ST) & 1, abort_flag))) break;
+            const uint32_t st = stage(k);
+            if (!(ok = tr_wait(p, s_ready + 8 * st, round(k) & 1, abort_flag))) break;
             tcgen05_after_sync();
             if (issuer) {
               scores(st, job, job);
