@@ -1016,7 +1016,7 @@ struct StridedRows {
 struct CrossPlan {
   int n_splits = 1, layout = kOneTile;
   int groups_max = 1;   // items of a sequence, at most
-  size_t query_off = 0, partials_off = 0, ws_bytes = 0;
+  size_t query_off = 0, items_off = 0, partials_off = 0, ws_bytes = 0;
 };
 
 vqkv_status validate_cross_sizes(const vqkv_cross_args* ac) {
@@ -1048,7 +1048,8 @@ vqkv_status plan_cross(const vqkv_cross_args* ac, CrossPlan* pl) {
   pl->n_splits = (int)std::max<long long>(1, std::min(want, units));
   pl->groups_max = (int)((cols + width - 1) / width);
   pl->query_off = decode_ticket_region_bytes(a.B, a.Hkv * kTicketGroups);
-  pl->partials_off = pl->query_off + round_up(cross_query_bytes(B, a.Hq, a.Hkv, ac->n_rows, pl->layout), 256);
+  pl->items_off = pl->query_off + round_up(cross_query_bytes(B, a.Hq, a.Hkv, ac->n_rows, pl->layout), 256);
+  pl->partials_off = pl->items_off + round_up(sizeof(int4) * pl->n_splits, 256);
   pl->ws_bytes = pl->partials_off;
   if (pl->n_splits > 1) pl->ws_bytes += sizeof(float) * (size_t)a.Hkv * pl->n_splits * 2 * width * kPartialStride;
   return VQKV_OK;
@@ -1224,6 +1225,7 @@ vqkv_status vqkv_cross_attn(const vqkv_cross_args* ac, const vqkv_paging* pg, vo
   p.max_queries = ac->max_queries;
   p.bf16 = ac->dtype == VQKV_DTYPE_BF16;
   p.q_row = q_row;
+  p.tickets = reinterpret_cast<unsigned*>(ws + pl.items_off);
   p.ncols = (int)std::min<long long>(ac->max_queries * (long long)p.g, cross_cols(pl.layout));
   p.partials = reinterpret_cast<float*>(ws + pl.partials_off);
   p.n_splits = pl.n_splits;

@@ -16,6 +16,22 @@
 namespace vqkv {
 namespace {
 
+// Four consecutive values of an output row, whose address is a multiple of 2 bytes.
+__device__ __forceinline__ void store_four(const DecodeParams& p, __half* dst, float4 w) {
+  if (!p.bf16) {
+    store_out4(dst, w);
+    return;
+  }
+  const __nv_bfloat162 a = __floats2bfloat162_rn(w.x, w.y), b = __floats2bfloat162_rn(w.z, w.w);
+  const uint2 h = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if ((reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
+    *reinterpret_cast<uint2*>(dst) = h;
+  } else {
+    dst[0] = __ushort_as_half((unsigned short)h.x), dst[1] = __ushort_as_half((unsigned short)(h.x >> 16));
+    dst[2] = __ushort_as_half((unsigned short)h.y), dst[3] = __ushort_as_half((unsigned short)(h.y >> 16));
+  }
+}
+
 // q' of every column, as the attention kernel's threads load it (tree_query_kernel's
 // image): sequence b's groups of 32 columns (PAIR: 16) start at cross_query_slot.
 // Columns past a sequence's last are not written: they reach only rows of the
@@ -23,39 +39,36 @@ namespace {
 template <bool PAIR>
 __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant__ DecodeParams p, uint4* qx) {
   constexpr int W = PAIR ? 16 : 32;
-  __shared__ int s_start[kFlatMaxB];
+  __shared__ int s_start[kFlatMaxB + 1];
   grid_dependency_wait();
   grid_dependents_launch();
-  for (int i = threadIdx.x; i < p.B; i += 128) s_start[i] = __ldg(p.row_start + i);
   const int kvh = blockIdx.y, part = threadIdx.x & 3;
   const long long col = (long long)blockIdx.x * 32 + (threadIdx.x >> 2);
   const bool any = col < (long long)p.n_rows * p.g;
   const int row = any ? (int)(col / p.g) : 0, h = any ? (int)(col - (long long)row * p.g) : 0;
+  const uint2* q = reinterpret_cast<const uint2*>(p.q + (long long)row * p.q_row + (kvh * p.g + h) * kHeadDim + 32 * part);
+  uint2 x[8];   // in flight while the row's sequence is looked up
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = q[i];
+  for (int i = threadIdx.x; i <= p.B; i += 128) s_start[i] = __ldg(p.row_start + i);
   __syncthreads();
   const int lo = sequence_of(s_start, p.B, row);   // the last sequence that starts at or before the row
-  const RowRange rows = row_range(p, lo, false);
+  const RowRange rows = rows_between(p, s_start[lo], s_start[lo + 1]);
   const bool in = any && row >= rows.first && row - rows.first < rows.n;   // both in [0, n_rows]
   float v[32];
-  if (in) {
-    const float4* s4 = reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 32 * part);
-    const uint2* q = reinterpret_cast<const uint2*>(p.q + (long long)row * p.q_row + (kvh * p.g + h) * kHeadDim + 32 * part);
+  const float4* s4 = reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 32 * part);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint2 x = q[i];
-      const float4 f = s4[i];
-      float2 a, b;
-      if (p.bf16) {   // the upper halves of the fp32 values
-        a = make_float2(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
-        b = make_float2(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
-      } else {
-        a = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
-        b = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
-      }
-      v[4 * i] = a.x * f.x, v[4 * i + 1] = a.y * f.y, v[4 * i + 2] = b.x * f.z, v[4 * i + 3] = b.y * f.w;
+  for (int i = 0; i < 8; ++i) {
+    const float4 f = __ldg(s4 + i);
+    float2 a, b;
+    if (p.bf16) {   // the upper halves of the fp32 values
+      a = make_float2(__uint_as_float(x[i].x << 16), __uint_as_float(x[i].x & 0xffff0000u));
+      b = make_float2(__uint_as_float(x[i].y << 16), __uint_as_float(x[i].y & 0xffff0000u));
+    } else {
+      a = __half22float2(*reinterpret_cast<const __half2*>(&x[i].x));
+      b = __half22float2(*reinterpret_cast<const __half2*>(&x[i].y));
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    v[4 * i] = a.x * f.x, v[4 * i + 1] = a.y * f.y, v[4 * i + 2] = b.x * f.z, v[4 * i + 3] = b.y * f.w;
   }
   fwht_column(v, part, p.qscale);
   if (!in) return;
@@ -77,84 +90,115 @@ __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant_
   }
 }
 
-// Merges the partials of the item that share blockIdx.x begins and does not end,
-// if there is one.  CC_COLS columns per block, one after another per warp; WIDE
-// (many partials per item): one column per block, blockIdx.x = item.  Lane = 4 channels, eight
-// partials in flight.
-constexpr int CC_WARPS = 8, CC_COLS = 32;
-template <bool WIDE>
-__global__ void __launch_bounds__(CC_WARPS * 32) cross_combine_kernel(const __grid_constant__ DecodeParams p, int cols, int groups_max) {
+// Merges of the items that several shares overlap.  Of share `split`'s two partials
+// the second is an item's first part, the first any other.
+__device__ __forceinline__ const float4* cross_partial(const DecodeParams& p, int kvh, int split, int part, int cols) {
+  return reinterpret_cast<const float4*>(p.partials) +
+         (((size_t)kvh * p.n_splits + split + part) * 2 + (part == 0)) * (cols * kPartialStride / 4);
+}
+
+// Few partials per item: the item that share blockIdx.x begins, if it does not end
+// it.  Lane = column of 32, warp = 16 channels: every load is 512 neighbouring bytes.
+__global__ void __launch_bounds__(256) cross_combine_kernel(const __grid_constant__ DecodeParams p, int cols) {
+  const int split = blockIdx.x, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int4 item = __ldcg(reinterpret_cast<const int4*>(p.tickets) + split);
+  if (item.z == 0) return;
+  const RowRange rows = row_range(p, item.x, false);
+  const int cl = blockIdx.z * 32 + lane, c = item.y * cols + cl;
+  if (cl >= cols || c >= rows.n * p.g) return;
+  float M = kMInit, l = 0.f, O[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) O[i] = 0.f;
+  constexpr int U = 2;
+  for (int i0 = 0; i0 < item.z; i0 += U) {
+    float2 ml[U];
+    float4 o[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ml[u] = make_float2(kMInit, 0.f);
+      if (i0 + u < item.z) {
+        const float4* at = cross_partial(p, kvh, split, i0 + u, cols);
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(at + 32 * cols) + cl);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[u][k] = __ldcg(at + (4 * warp + k) * cols + cl);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float n = fmaxf(M, ml[u].x), fa = fast_exp2(M - n), fb = fast_exp2(ml[u].x - n);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        O[4 * k] = O[4 * k] * fa + o[u][k].x * fb, O[4 * k + 1] = O[4 * k + 1] * fa + o[u][k].y * fb;
+        O[4 * k + 2] = O[4 * k + 2] * fa + o[u][k].z * fb, O[4 * k + 3] = O[4 * k + 3] * fa + o[u][k].w * fb;
+      }
+      l = l * fa + ml[u].y * fb;
+      M = n;
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  __half* dst = p.out + cross_out_row(p, rows.first, kvh, c) + 16 * warp;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    store_four(p, dst + 4 * k, make_float4(O[4 * k] * inv, O[4 * k + 1] * inv, O[4 * k + 2] * inv, O[4 * k + 3] * inv));
+}
+
+// Many partials per item (few items): a block per column, a warp per every eighth
+// part, lane = 4 channels; item blockIdx.x of groups_max per sequence.
+constexpr int CW_WARPS = 8;
+__global__ void __launch_bounds__(CW_WARPS * 32) cross_combine_wide_kernel(const __grid_constant__ DecodeParams p, int cols,
+                                                                           int groups_max) {
   constexpr int U = 8;
   __shared__ int s_pref[kFlatMaxB + 1];
-  __shared__ float4 s_o[CC_WARPS][32];
-  __shared__ float2 s_ml[CC_WARPS];
-  const int kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float4 s_o[CW_WARPS][32];
+  __shared__ float2 s_ml[CW_WARPS];
+  const int kvh = blockIdx.y, cl = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_dependents_launch();
   item_prefix<tr::TOK>(p, cols, s_pref, false);
   const int T = s_pref[p.B], S = min(p.n_splits, T);
-  int split, b, group, all;
-  if (WIDE) {   // item blockIdx.x of groups_max per sequence
-    b = blockIdx.x / groups_max, group = blockIdx.x - b * groups_max;
-    all = (clamped_len(p, b) + tr::TOK - 1) / tr::TOK;
-    if (s_pref[b] + (long long)group * all >= s_pref[b + 1]) return;
-    split = flat_cta_of(s_pref[b] + group * all, T, S);
-  } else {      // that of the last unit of share blockIdx.x
-    split = blockIdx.x;
-    if (split >= S) return;
-    const int unit = (int)((long long)T * (split + 1) / S) - 1;
-    b = sequence_of(s_pref, p.B, unit);
-    all = (clamped_len(p, b) + tr::TOK - 1) / tr::TOK, group = (unit - s_pref[b]) / all;
-  }
-  const int r0 = (int)((long long)T * split / S), r1 = (int)((long long)T * (split + 1) / S);
-  const int first = s_pref[b] + group * all, last = first + all;   // the item's units
-  if (first < r0 || last <= r1) return;
+  const int b = blockIdx.x / groups_max, group = blockIdx.x - b * groups_max;
+  const int all = (clamped_len(p, b) + tr::TOK - 1) / tr::TOK;
+  if (s_pref[b] + (long long)group * all >= s_pref[b + 1]) return;
+  const int first = s_pref[b] + group * all, split = flat_cta_of(first, T, S);
+  const int parts = flat_cta_of(first + all - 1, T, S) - split + 1;
   const RowRange rows = row_range(p, b, false);
-  const int live = min(cols, rows.n * p.g - group * cols);
-  const int parts = flat_cta_of(last - 1, T, S) - split + 1;
-  const size_t stride = (size_t)2 * cols * kPartialStride;   // from share to share
-  constexpr int STEP = WIDE ? CC_WARPS : 1;
-  const int cl0 = WIDE ? blockIdx.z : blockIdx.z * CC_COLS, cl1 = min(live, cl0 + (WIDE ? 1 : CC_COLS));
-  for (int cl = WIDE ? cl0 : cl0 + warp; cl < cl1; cl += CC_WARPS) {
-    // the first part is its share's second partial, the others the first
-    const float* base = p.partials + (((size_t)kvh * p.n_splits + split) * 2 * cols + cl) * kPartialStride;
-    float M = kMInit, l = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 ml, float4 o) {
-      const float n = fmaxf(M, ml.x), fa = fast_exp2(M - n), fb = fast_exp2(ml.x - n);
-      O.x = O.x * fa + o.x * fb, O.y = O.y * fa + o.y * fb, O.z = O.z * fa + o.z * fb, O.w = O.w * fa + o.w * fb;
-      l = l * fa + ml.y * fb;
-      M = n;
-    };
-    for (int i0 = WIDE ? warp : 0; i0 < parts; i0 += U * STEP) {
-      float2 ml[U];
-      float4 o[U];
+  const int c = group * cols + cl;
+  if (parts == 1 || c >= rows.n * p.g) return;
+  float M = kMInit, l = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float2 ml, float4 o) {
+    const float n = fmaxf(M, ml.x), fa = fast_exp2(M - n), fb = fast_exp2(ml.x - n);
+    O.x = O.x * fa + o.x * fb, O.y = O.y * fa + o.y * fb, O.z = O.z * fa + o.z * fb, O.w = O.w * fa + o.w * fb;
+    l = l * fa + ml.y * fb;
+    M = n;
+  };
+  for (int i0 = warp; i0 < parts; i0 += U * CW_WARPS) {
+    float2 ml[U];
+    float4 o[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * STEP;
-        if (i < parts) {
-          const float* at = base + i * stride + (i == 0 ? (size_t)cols * kPartialStride : 0);
-          ml[u] = __ldcg(reinterpret_cast<const float2*>(at + 128));
-          o[u] = __ldcg(reinterpret_cast<const float4*>(at) + lane);
-        }
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * CW_WARPS < parts) {
+        const float4* at = cross_partial(p, kvh, split, i0 + u * CW_WARPS, cols);
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(at + 32 * cols) + cl);
+        o[u] = __ldcg(at + lane * cols + cl);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + u * STEP < parts) add(ml[u], o[u]);
-    }
-    if (WIDE) {   // the block's warps meet in shared memory
-      s_o[warp][lane] = O;
-      if (lane == 0) s_ml[warp] = make_float2(M, l);
-      __syncthreads();
-      if (warp != 0) return;
-#pragma unroll
-      for (int w = 1; w < CC_WARPS; ++w) add(s_ml[w], s_o[w][lane]);
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    __half* dst = p.out + cross_out_row(p, rows.first, kvh, group * cols + cl) + 4 * lane;
-    const float4 w = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-    if (p.bf16) store_out4<true>(dst, w); else store_out4<false>(dst, w);
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * CW_WARPS < parts) add(ml[u], o[u]);
   }
+  s_o[warp][lane] = O;
+  if (lane == 0) s_ml[warp] = make_float2(M, l);
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < CW_WARPS; ++w) add(s_ml[w], s_o[w][lane]);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  store_four(p, p.out + cross_out_row(p, rows.first, kvh, c) + 4 * lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
 }
 
 using CrossKernel = void (*)(DecodeParams, const unsigned long long*, const uint4*);
@@ -207,11 +251,10 @@ cudaError_t launch_cross(int mode, const DecodeParams& p, int layout, int groups
     const int cols = cross_cols(layout);
     const int wide_items = p.n_splits > 4LL * p.B * groups_max ? p.B * groups_max : 0;   // few items, many partials
     if (wide_items > 0)
-      e = launch_pdl(cross_combine_kernel<true>, dim3(wide_items, p.Hkv, p.ncols), dim3(CC_WARPS * 32), 0, stream, p, cols,
-                     wide_items / p.B);
+      e = launch_pdl(cross_combine_wide_kernel, dim3(wide_items, p.Hkv, p.ncols), dim3(CW_WARPS * 32), 0, stream, p, cols,
+                     groups_max);
     else
-      e = launch_pdl(cross_combine_kernel<false>, dim3(p.n_splits, p.Hkv, (p.ncols + CC_COLS - 1) / CC_COLS),
-                     dim3(CC_WARPS * 32), 0, stream, p, cols, 0);
+      e = launch_pdl(cross_combine_kernel, dim3(p.n_splits, p.Hkv, (p.ncols + 31) / 32), dim3(256), 0, stream, p, cols);
   }
   return e;
 }

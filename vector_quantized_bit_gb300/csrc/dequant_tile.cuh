@@ -456,13 +456,16 @@ struct Pieces {
 struct RowRange {
   int first, n;
 };
-__device__ __forceinline__ RowRange row_range(const DecodeParams& p, int b, bool report) {
+__device__ __forceinline__ RowRange rows_between(const DecodeParams& p, int start, int end, bool report = false) {
   // (differences in 64 bits: starts of any bits must not overflow on the way to the comparisons)
-  const long long lo = __ldg(p.row_start + b), hi = __ldg(p.row_start + b + 1);
+  const long long lo = start, hi = end;
   const bool fine = lo >= 0 && hi >= lo && hi <= p.n_rows;
   const int n = fine ? (int)min(hi - lo, (long long)p.max_queries) : 0;
   if (report && (!fine || n != hi - lo)) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
   return {fine ? (int)lo : 0, n};
+}
+__device__ __forceinline__ RowRange row_range(const DecodeParams& p, int b, bool report) {
+  return rows_between(p, __ldg(p.row_start + b), __ldg(p.row_start + b + 1), report);
 }
 
 __device__ __forceinline__ int clamped_len(const DecodeParams& p, int b) {
@@ -548,6 +551,7 @@ struct ItemPieces {
     at = split < S ? (int)((long long)T * split / S) : 0;
     r1 = split < S ? (int)((long long)T * (split + 1) / S) : 0;
     b = at < r1 ? sequence_of(pref, p.B, at) : 0;
+    n = 0;
   }
   __device__ __forceinline__ bool next() {
     if (at >= r1) return false;
@@ -559,6 +563,13 @@ struct ItemPieces {
     n = min(all - tile0, r1 - at);
     at += n;
     return true;
+  }
+  // After the last piece: (sequence, group, parts of its item, 0) if the item began in
+  // this share and ends in another, else no parts.
+  __device__ __forceinline__ int4 split_item(int split, int n_splits) const {
+    const int T = pref[p.B], S = min(n_splits, T);
+    if (split >= S || n == 0 || tile0 != 0 || n == all) return make_int4(0, 0, 0, 0);
+    return make_int4(b, group, flat_cta_of(pref[b] + (group + 1) * all - 1, T, S) - split + 1, 0);
   }
 };
 

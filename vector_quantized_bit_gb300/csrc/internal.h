@@ -64,7 +64,8 @@ struct DecodeParams {
   // Cross attention (vqkv_cross_attn), else unused: the rows of q and out are
   // packed, sequence b's are row_start[b] .. row_start[b + 1] - 1; ncols is the
   // number of columns of an item (a group of a sequence's columns) that the
-  // kernel computes, q_row the stride of q's rows in elements.
+  // kernel computes, q_row the stride of q's rows in elements; tickets are int4s,
+  // one per share: the item that it begins and does not end (sequence, group, parts).
   const int32_t* row_start = nullptr;
   int n_rows = 0, max_queries = 0, bf16 = 0;
   long long q_row = 0;
@@ -171,7 +172,8 @@ cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned l
                                cudaStream_t stream);
 
 // Cross attention (cross_attn.cu), B <= kFlatMaxB: n_splits shares per KV head;
-// partials [Hkv][2 n_splits][cross_cols(layout)].  layout: columns of an item,
+// partials [Hkv][2 n_splits] of [32 pieces of 4 channels][cross_cols(layout) columns],
+// then max and sum of each column.  layout: columns of an item,
 // as in the draft-tree attention; groups_max: items of a sequence, at most.
 enum TileLayout : int { kOneTile = 0, kTwoTiles = 1, kPairs = 2 };   // columns on the MMA rows
 int cross_cols(int layout);   // columns of an item, at most

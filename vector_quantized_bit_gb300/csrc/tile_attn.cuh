@@ -151,15 +151,8 @@ __device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Wo
 }
 
 // Four consecutive values of an output row, whose address is a multiple of 2 bytes.
-template <bool BF16>
 __device__ __forceinline__ void store_out4(__half* dst, float4 w) {
-  uint2 h;
-  if constexpr (BF16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(w.x, w.y), b = __floats2bfloat162_rn(w.z, w.w);
-    h = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  } else {
-    h = make_uint2(pack_half2(w.x, w.y), pack_half2(w.z, w.w));
-  }
+  const uint2 h = make_uint2(pack_half2(w.x, w.y), pack_half2(w.z, w.w));
   if ((reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
     *reinterpret_cast<uint2*>(dst) = h;
   } else {
@@ -176,6 +169,79 @@ __device__ __forceinline__ size_t cross_out_row(const DecodeParams& p, int row0,
 }
 __host__ __device__ __forceinline__ long long cross_query_slot(int row0, int b, int g, int width) {
   return (long long)row0 * g / width + b;
+}
+
+// Cross attention: what a softmax warp does with its columns of a piece's O (row =
+// column of the item in the lane's tensor memory from t_o on).  The output takes 32
+// channels at a time, packed, through the warp's own 2 KB of shared memory (16-byte
+// pieces permuted by the row), so that a row's stores are whole sectors; a partial
+// goes out as [32 pieces of 4 channels][cols columns], neighbours as they are in the
+// warp.  (Eight rounds of 16 channels with a row's address computed in each took
+// 5.5 us of a piece, now 1.5.)
+template <int WCOLS>
+__device__ __forceinline__ void cross_finish(const DecodeParams& p, bool whole, uint32_t t_o, float m, float l, uint4* box, float4* part,
+                                             int cols, int cl, int nloc, int col0, int row0, int kvh) {
+  const int lane = threadIdx.x & 31, cl0 = cl & ~(WCOLS - 1);
+  const bool mine = cl < nloc && lane < WCOLS;
+  if (cl0 >= nloc) return;   // the same for the whole warp
+  if (!whole) {
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      float v[32];
+      tmem_ld32(t_o + 32 * q, v);
+      tmem_wait_ld();
+      if (mine) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[(8 * q + i) * cols + cl] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+    }
+    if (mine) reinterpret_cast<float2*>(part + 32 * cols)[cl] = make_float2(m, l);
+    return;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int x = lane & 3;   // 16-byte piece of the rows 8 i + lane / 4
+  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;   // out needs only 2-byte alignment
+  __half* dst[WCOLS / 8];
+#pragma unroll
+  for (int i = 0; i < WCOLS / 8; ++i) {
+    const int c = cl0 + 8 * i + (lane >> 2);
+    dst[i] = c < nloc ? p.out + cross_out_row(p, row0, kvh, col0 + c) + 8 * x : nullptr;
+  }
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    float v[32];
+    tmem_ld32(t_o + 32 * q, v);
+    tmem_wait_ld();
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float a = v[2 * i] * inv, b = v[2 * i + 1] * inv;
+      if (p.bf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[i] = pack_half2(a, b);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      box[lane * 4 + (i ^ ((lane >> 1) & 3))] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < WCOLS / 8; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      const uint4 h = box[r * 4 + (x ^ ((r >> 1) & 3))];
+      if (dst[i] == nullptr) continue;
+      if (wide) {
+        *reinterpret_cast<uint4*>(dst[i] + 32 * q) = h;
+      } else {
+        const uint32_t e[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[i][32 * q + k] = __ushort_as_half((unsigned short)(e[k >> 1] >> (16 * (k & 1))));
+      }
+    }
+    __syncwarp();
+  }
 }
 
 // grid (shares, Hkv, column groups of 128 NQ; CROSS: 1).
@@ -243,12 +309,11 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     item_prefix<TOK>(p, COLS, s_pref, blockIdx.x == 0 && blockIdx.y == 0);
   else
     flat_prefix<TOK / 16>(p, s_pref);
+  // CROSS: this warp's share.  STREAMS: that of a softmax or dequantising warpgroup, or of an issuing warp
+  const int share = STREAMS ? 2 * split + (warp < MMA_WARP ? (warp >> 2) & 1 : warp & 1) : split;
   auto pc = [&] {
-    // STREAMS: the stream of a softmax or dequantising warpgroup, or of an issuing warp
-    if constexpr (STREAMS)
-      return ItemPieces<TOK, COLS>(p, s_pref, 2 * split + (warp < MMA_WARP ? (warp >> 2) & 1 : warp & 1), p.n_splits);
-    else if constexpr (CROSS)
-      return ItemPieces<TOK, COLS>(p, s_pref, split, p.n_splits);
+    if constexpr (CROSS)
+      return ItemPieces<TOK, COLS>(p, s_pref, share, p.n_splits);
     else
       return Pieces(s_pref, p.B, split, p.n_splits);
   }();
@@ -351,7 +416,15 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         fa = fast_exp2(a.x - m), fb = fast_exp2(z.x - m);
         l = a.y * fa + z.y * fb;
       }
-      if (ok && !*abort_flag) {
+      if constexpr (CROSS) {
+        // a share has a piece that began before it, and one that ends behind it, at most
+        if (ok && !*abort_flag)
+          cross_finish<WCOLS>(p, pc.n == pc.all, t_lane + T_O + kHeadDim * wg, m, l,
+                              reinterpret_cast<uint4*>(smem + G::BOX_OFF) + warp * 128,
+                              reinterpret_cast<float4*>(p.partials) +
+                                  (((size_t)kvh * p.n_splits + share) * 2 + (pc.tile0 == 0)) * (COLS * kPartialStride / 4),
+                              COLS, cl, nloc, col0, row0, kvh);
+      } else if (ok && !*abort_flag) {
         const bool whole = pc.n == pc.all;
         if (whole) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -361,12 +434,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         // that a row's stores are neighbours; 16-byte pieces permuted by the row
         const int c0 = c - (lane & (WCOLS - 1));   // the warp's first column
         float* box = reinterpret_cast<float*>(smem + G::BOX_OFF) + warp * (32 * 16);
-        float* part;   // CROSS: a share has a piece that began before it, and one that ends behind it, at most
-        if constexpr (CROSS)
-          part = p.partials + (((size_t)kvh * p.n_splits + (STREAMS ? 2 * split + wg : split)) * 2 + (pc.tile0 == 0)) * COLS * kPartialStride +
-                 (size_t)(c0 - col0) * kPartialStride;
-        else
-          part = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + split + pc.b) * p.ncols + c0) * kPartialStride;
+        float* part = p.partials + (((size_t)kvh * (p.n_splits + p.B - 1) + split + pc.b) * p.ncols + c0) * kPartialStride;
 #pragma unroll 1
         for (int q = TQ == 1 ? 4 * wg : 0; q < (TQ == 1 ? 4 * wg + 4 : 8); ++q) {
           uint32_t o[16], z[16];
@@ -401,12 +469,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
               const int r = 8 * i + (lane >> 2);
               if (c0 - col0 + r < nloc) {
                 const float4 w = *reinterpret_cast<const float4*>(box + r * 16 + ((x ^ ((r >> 1) & 3)) << 2));
-                if constexpr (CROSS) {
-                  __half* dst = p.out + cross_out_row(p, row0, kvh, c0 + r) + 16 * q + 4 * x;
-                  if (p.bf16) store_out4<true>(dst, w); else store_out4<false>(dst, w);
-                } else {
-                  store_out4<false>(p.out + out_row(p, pc.b, kvh, c0 + r) + 16 * q + 4 * x, w);
-                }
+                store_out4(p.out + out_row(p, pc.b, kvh, c0 + r) + 16 * q + 4 * x, w);
               }
             }
           }
@@ -415,11 +478,15 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         if (cl < nloc && lane < WCOLS && (TQ == 2 || wg == 0)) {
           if (!whole)
             *reinterpret_cast<float2*>(part + lane * kPartialStride + 128) = make_float2(m, l);
-          else if (!CROSS && p.stats != nullptr)
+          else if (p.stats != nullptr)
             p.stats[((size_t)pc.b * p.Hkv + kvh) * p.ncols + c] = make_float2(m, l > 0.f ? 1.f / l : 0.f);
         }
       }
       done += pc.n;
+    }
+    if constexpr (CROSS) {   // the item that this share begins and does not end, for the merge
+      if (kvh == 0 && (threadIdx.x & (ROWS - 1)) == 0 && (STREAMS || wg == 0) && share < p.n_splits)
+        reinterpret_cast<int4*>(p.tickets)[share] = pc.split_item(share, p.n_splits);
     }
   } else if (warp < MMA_WARP) {
     // ---------------- dequantisation
