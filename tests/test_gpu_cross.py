@@ -144,6 +144,49 @@ def test_every_instance(t, mode, block_tokens, queries):
     assert x.flags() == 0
 
 
+@pytest.mark.parametrize("mode", range(5))
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,queries,lens,kw", [
+    (3, 3, [1], [700], dict()),                                                          # one sequence: the split plan
+    (4, 2, [1, 0, 1, 1], [130, 300, 0, 1], dict(back=3, front=1)),                       # without a query, without tokens
+    (16, 2, [0, 1, 1], [200, 64, 1000], dict(block_tokens=64, stride=32)),               # eight columns: two groups
+    (5, 1, [1, 1], [65, 48], dict(block_tokens=128)),
+])
+@pytest.mark.parametrize("num_splits", [0, 3])
+def test_single_queries(t, mode, dt, Hq, Hkv, queries, lens, kw, num_splits):
+    x = Cross(t, mode, Hq, Hkv, queries, lens, dt=dt, seed=mode + Hq, **kw)
+    got = x.run(num_splits)
+    x.check(got, *x.reference())
+    assert x.flags() == 0
+    again = x.run(num_splits, out=t.full_like(x.out, 3.0), ws=x.ws)
+    assert t.equal(got, again)
+
+
+def test_single_queries_and_starts_that_make_no_sense(t):
+    for mode in (0, 1):
+        x = Cross(t, mode, 4, 2, [1, 1, 1], [100, 70, 90], seed=6)
+        x.dstarts = H.dev(np.array([0, 1, -7, 3], dtype=np.int32))
+        got = x.run()
+        assert x.flags() == _lib.VQKV_DEVERR_SEQ_LEN
+        ref, tol = x.reference()
+        ref[1:] = np.nan
+        x.check(got, ref, tol)
+        x = Cross(t, mode, 4, 2, [2, 1], [100, 70], seed=6)      # two queries where one was announced
+        got = x.run(most=1)
+        assert x.flags() == _lib.VQKV_DEVERR_SEQ_LEN
+        ref, tol = x.reference()
+        ref[1] = np.nan
+        x.check(got, ref, tol)
+
+
+def test_many_single_queries(t):
+    """More sequences than the flat plan takes."""
+    r = np.random.default_rng(21)
+    x = Cross(t, 0, 2, 1, r.integers(0, 2, 1100).tolist(), r.integers(0, 70, 1100).tolist(), cap=80, seed=13, dt="bf16")
+    x.check(x.run(), *x.reference())
+    assert x.flags() == 0
+
+
 def test_scale_and_large_scores(t):
     for qscale, scale in ((1.0, 0.5), (12.0, 0.0), (1e-3, 0.0)):
         x = Cross(t, 0, 8, 2, [20, 70], [300, 500], seed=3, qscale=qscale)

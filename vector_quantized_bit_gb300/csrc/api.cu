@@ -19,7 +19,7 @@ constexpr int kMaxTokens = 1 << 30; // longest row of the cache-editing calls (p
 
 // Kernels that are prepared (attributes set, checks made) only when a call that
 // uses them is first planned, so that no other call loads them or fails with them.
-enum LazyKernels : int { kTreeKernels, kMassKernels, kMassTileKernels, kCompactKernels, kSelectKernels, kAppendKernels, kCrossKernels, kLazyKernels };
+enum LazyKernels : int { kTreeKernels, kMassKernels, kMassTileKernels, kCompactKernels, kSelectKernels, kAppendKernels, kCrossKernels, kCrossRowsKernels, kLazyKernels };
 
 struct DeviceInfo {
   bool ready = false;
@@ -71,6 +71,7 @@ vqkv_status device_info(LazyKernels what, int mode, DeviceInfo* out) {
                         : what == kCompactKernels  ? compact_prepare(mode, &d.compact_cluster[mode])
                         : what == kAppendKernels   ? append_prepare(mode)
                         : what == kCrossKernels    ? cross_prepare(mode)
+                        : what == kCrossRowsKernels ? cross_rows_prepare(mode)
                                                    : evict_select_prepare();
   if (e != cudaSuccess) return VQKV_ERR_CUDA;
   d.prepared[what][mode] = true;
@@ -1014,6 +1015,8 @@ struct StridedRows {
 
 // Cross attention: shares of all items' units per KV head, one CTA per SM in one wave.
 struct CrossPlan {
+  bool rows = false;    // one query per sequence: the decode's kernels and plan
+  DecodePlan d;
   int n_splits = 1, layout = kOneTile;
   int groups_max = 1;   // items of a sequence, at most
   size_t query_off = 0, items_off = 0, partials_off = 0, ws_bytes = 0;
@@ -1036,6 +1039,16 @@ vqkv_status validate_cross_sizes(const vqkv_cross_args* ac) {
 vqkv_status plan_cross(const vqkv_cross_args* ac, CrossPlan* pl) {
   const vqkv_decode_args& a = ac->decode;
   DeviceInfo di;
+  if (ac->max_queries == 1 && (long long)a.B * ((a.Hq / a.Hkv + 3) / 4) <= kMaxGridYZ) {
+    pl->rows = true;
+    const vqkv_status ready = device_info(kCrossRowsKernels, a.mode, &di);
+    if (ready != VQKV_OK) return ready;
+    PlanInput in = plan_input(&a);
+    in.width = 4;
+    const vqkv_status st = plan_decode(&in, &pl->d);
+    pl->ws_bytes = pl->d.ws_bytes;
+    return st;
+  }
   const vqkv_status st = device_info(kCrossKernels, a.mode, &di);
   if (st != VQKV_OK) return st;
   const long long g = a.Hq / a.Hkv, cols = ac->max_queries * g;
@@ -1225,6 +1238,18 @@ vqkv_status vqkv_cross_attn(const vqkv_cross_args* ac, const vqkv_paging* pg, vo
   p.max_queries = ac->max_queries;
   p.bf16 = ac->dtype == VQKV_DTYPE_BF16;
   p.q_row = q_row;
+  if (pl.rows) {
+    p.tickets = reinterpret_cast<unsigned*>(ws + pl.d.tickets_off);
+    p.partials = reinterpret_cast<float*>(ws + pl.d.partials_off);
+    p.n_splits = pl.d.n_splits;
+    p.tps = pl.d.tps;
+    p.bpg = pl.d.bpg;
+    p.defer_merge = pl.d.bpg > 1 ? 1 : 0;
+    p.flat = pl.d.flat;
+    p.cgroups = pl.d.cgroups;
+    const dim3 grid(pl.d.n_splits, a->Hkv, pl.d.n_bgroups * pl.d.cgroups);
+    return launch_cross_rows(a->mode, p, grid, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VQKV_OK : VQKV_ERR_CUDA;
+  }
   p.tickets = reinterpret_cast<unsigned*>(ws + pl.items_off);
   p.ncols = (int)std::min<long long>(ac->max_queries * (long long)p.g, cross_cols(pl.layout));
   p.partials = reinterpret_cast<float*>(ws + pl.partials_off);

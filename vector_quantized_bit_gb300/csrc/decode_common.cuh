@@ -3,6 +3,8 @@
 // softmax states, and the last-CTA merge of the split partials.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -28,12 +30,47 @@ struct CombineSmem {
   static constexpr int kBytes = (kMax + 8) * 4;
 };
 
+// A sequence's rows of a cross attention: first row and number; none (and the
+// error bit) where the starts make no sense, at most max_queries.
+struct RowRange {
+  int first, n;
+};
+__device__ __forceinline__ RowRange rows_between(const DecodeParams& p, int start, int end, bool report = false) {
+  // (differences in 64 bits: starts of any bits must not overflow on the way to the comparisons)
+  const long long lo = start, hi = end;
+  const bool fine = lo >= 0 && hi >= lo && hi <= p.n_rows;
+  const int n = fine ? (int)min(hi - lo, (long long)p.max_queries) : 0;
+  if (report && (!fine || n != hi - lo)) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
+  return {fine ? (int)lo : 0, n};
+}
+__device__ __forceinline__ RowRange row_range(const DecodeParams& p, int b, bool report) {
+  return rows_between(p, __ldg(p.row_start + b), __ldg(p.row_start + b + 1), report);
+}
+
+// O's row of column c (query c / g, head c % g) of the sequence whose rows start at row0.
+__device__ __forceinline__ size_t cross_out_row(const DecodeParams& p, int row0, int kvh, int c) {
+  const int m = c / p.g, h = c - m * p.g;
+  return ((size_t)(row0 + m) * p.Hq + kvh * p.g + h) * kHeadDim;
+}
+
+// What a decode kernel is compiled for: the plain decode; attention weights
+// (scores and softmax statistics written out); or cross attention of one packed
+// row per sequence at most, fp16 or bf16.  The last two compute a CTA's 4 columns
+// from two fp16 parts of q'.
+enum DecodeForm : int { kPlain = 0, kMass = 1, kRows = 2 };
+
 // Clamp the sequence length to [0, max_seq_len]; report out-of-range once.
+// ROWS: a sequence without a query has nothing to compute.
+template <bool ROWS = false>
 __device__ __forceinline__ int load_len(const DecodeParams& p, int b) {
   int L = p.seq_lens[b];
   if (L < 0 || L > p.max_seq_len) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
     L = L < 0 ? 0 : p.max_seq_len;
+  }
+  if constexpr (ROWS) {
+    const bool report = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+    if (row_range(p, b, report).n == 0) L = 0;
   }
   return L;
 }
@@ -136,6 +173,22 @@ __device__ __forceinline__ size_t out_row(const DecodeParams& p, int b, int kvh,
   return (((size_t)b * p.M + m) * p.Hq + kvh * p.g + h) * kHeadDim;
 }
 
+// One value of O.
+template <bool ROWS>
+__device__ __forceinline__ void store_output(const DecodeParams& p, int b, int kvh, int c, int d, float v) {
+  if constexpr (ROWS) {
+    const RowRange rows = row_range(p, b, false);
+    if (rows.n == 0) return;
+    __half* dst = p.out + cross_out_row(p, rows.first, kvh, c) + d;
+    if (p.bf16)
+      *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(v);
+    else
+      *dst = __float2half_rn(v);
+  } else {
+    p.out[out_row(p, b, kvh, c) + d] = __float2half_rn(v);
+  }
+}
+
 // Per-lane visible-token limits of the lane's two softmax columns col0 +
 // 2tig and col0 + 2tig + 1 (col0: the CTA's first column): query m of M
 // sees tokens t < L - M + m + 1 (columns past ncols are padding and see all
@@ -194,9 +247,9 @@ __device__ __forceinline__ MergeSpan split_span(const DecodeParams& p, int b, in
 
 // COLGROUPS: the launch may split the columns into groups (multi-query
 // decode); otherwise the CTA holds all ncols columns.  DimOf: the stash
-// layout (row skew).  MASS: groups are 4 columns wide and each column's final
-// (max, 1 / sum) goes to p.stats.
-template <int WARPS, bool COLGROUPS, typename DimOf, bool MASS = false>
+// layout (row skew).  FORM other than kPlain: groups are 4 columns wide; kMass: each
+// column's final (max, 1 / sum) goes to p.stats.
+template <int WARPS, bool COLGROUPS, typename DimOf, int FORM = kPlain>
 __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, int kvh, const MergeSpan& ms,
                                                 float* s_comb, int* s_last) {
   using C = CombineSmem<WARPS>;
@@ -205,7 +258,8 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
   const float* wl = s_comb + C::kL;
   float* wf = s_comb + C::kF;
   float* wM = s_comb + C::kMax;
-  constexpr int WIDTH = MASS ? 4 : 8;
+  constexpr bool MASS = FORM == kMass, ROWS = FORM == kRows;
+  constexpr int WIDTH = FORM != kPlain ? 4 : 8;
   const int col0 = COLGROUPS ? cta_col0<WIDTH>(p) : 0;
   const int G = COLGROUPS ? min(WIDTH, p.ncols - col0) : p.ncols;   // this CTA's columns
   const size_t split_stride = (size_t)p.ncols * kPartialStride;
@@ -235,7 +289,7 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
 #pragma unroll 4
       for (int w = 0; w < WARPS; ++w) l += wl[w * 8 + h] * wf[w * 8 + h];
       if (n_parts == 1) {
-        p.out[out_row(p, b, kvh, col0 + h) + d] = __float2half_rn(l > 0.f ? o / l : 0.f);
+        store_output<ROWS>(p, b, kvh, col0 + h, d, l > 0.f ? o / l : 0.f);
         if constexpr (MASS)
           if (d == 0) p.stats[(size_t)(b * p.Hkv + kvh) * p.ncols + col0 + h] = make_float2(wM[h], l > 0.f ? 1.f / l : 0.f);
         continue;
@@ -333,20 +387,25 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
       const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
       if constexpr (MASS)
         if (d8 == 0) p.stats[(size_t)(b * p.Hkv + kvh) * p.ncols + col0 + h] = make_float2(M, inv);
-      uint4 packed;
-      packed.x = pack_half2(O[0] * inv, O[1] * inv);
-      packed.y = pack_half2(O[2] * inv, O[3] * inv);
-      packed.z = pack_half2(O[4] * inv, O[5] * inv);
-      packed.w = pack_half2(O[6] * inv, O[7] * inv);
-      __half* dst = p.out + out_row(p, b, kvh, col0 + h) + d8;
-      if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {   // out needs only 2-byte alignment
-        *reinterpret_cast<uint4*>(dst) = packed;
-      } else {
-        const uint32_t w[4] = {packed.x, packed.y, packed.z, packed.w};
+      if constexpr (ROWS) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dst[2 * i] = __ushort_as_half((unsigned short)(w[i] & 0xffffu));
-          dst[2 * i + 1] = __ushort_as_half((unsigned short)(w[i] >> 16));
+        for (int i = 0; i < 8; ++i) store_output<true>(p, b, kvh, col0 + h, d8 + i, O[i] * inv);
+      } else {
+        uint4 packed;
+        packed.x = pack_half2(O[0] * inv, O[1] * inv);
+        packed.y = pack_half2(O[2] * inv, O[3] * inv);
+        packed.z = pack_half2(O[4] * inv, O[5] * inv);
+        packed.w = pack_half2(O[6] * inv, O[7] * inv);
+        __half* dst = p.out + out_row(p, b, kvh, col0 + h) + d8;
+        if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {   // out needs only 2-byte alignment
+          *reinterpret_cast<uint4*>(dst) = packed;
+        } else {
+          const uint32_t w[4] = {packed.x, packed.y, packed.z, packed.w};
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dst[2 * i] = __ushort_as_half((unsigned short)(w[i] & 0xffffu));
+            dst[2 * i + 1] = __ushort_as_half((unsigned short)(w[i] >> 16));
+          }
         }
       }
     }
@@ -357,8 +416,8 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
 // Merge the split partials of softmax column blockIdx.x % ncols of KV head
 // blockIdx.x / ncols of sequence b = blockIdx.y into O (fp16); thread d owns
 // channel d.  The combine kernel
-// of plans that defer the merge.  MASS: also the column's (max, 1 / sum).
-template <bool MASS = false>
+// of plans that defer the merge.  kMass: also the column's (max, 1 / sum).
+template <int FORM = kPlain>
 __device__ __forceinline__ void combine_splits(const DecodeParams& p) {
   constexpr int U = 8;   // splits whose loads are in flight together
   const int b = blockIdx.y, d = threadIdx.x;
@@ -385,8 +444,8 @@ __device__ __forceinline__ void combine_splits(const DecodeParams& p) {
       M = n;
     }
   }
-  p.out[out_row(p, b, kvh, h) + d] = __float2half_rn(Ls > 0.f ? O / Ls : 0.f);
-  if constexpr (MASS)
+  store_output<FORM == kRows>(p, b, kvh, h, d, Ls > 0.f ? O / Ls : 0.f);
+  if constexpr (FORM == kMass)
     if (d == 0) p.stats[(size_t)(b * p.Hkv + kvh) * p.ncols + h] = make_float2(M, Ls > 0.f ? 1.f / Ls : 0.f);
 }
 
@@ -458,13 +517,16 @@ struct NaturalDim {   // channel offset gid, rows gid+8 eight channels on
 
 // Flat plan: s_pref[b] = super-tiles (TPI tiles of 16 tokens) of sequences
 // 0 .. b-1 at their clamped lengths, for b = 0 .. B.  All threads.
-template <int TPI>
+template <int TPI, bool ROWS = false>
 __device__ __forceinline__ void flat_prefix(const DecodeParams& p, int* s_pref) {
   const int lane = threadIdx.x & 31;
   for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
     const int raw = p.seq_lens[b], L = min(max(raw, 0), p.max_seq_len);
     if (raw != L && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
-    s_pref[b + 1] = ((L + 16 - 1) / 16 + TPI - 1) / TPI;
+    int tiles = ((L + 16 - 1) / 16 + TPI - 1) / TPI;
+    if constexpr (ROWS)   // a sequence without a query has nothing to compute
+      if (row_range(p, b, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0).n == 0) tiles = 0;
+    s_pref[b + 1] = tiles;
   }
   if (threadIdx.x == 0) s_pref[0] = 0;
   __syncthreads();

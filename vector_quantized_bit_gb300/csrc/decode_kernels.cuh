@@ -142,9 +142,10 @@ static_assert(CombineSmem<V2_WARPS>::kBytes <= V2Geo<VQKV_MODE_VQ2>::MBAR_OFF,
 constexpr size_t kV15Smem = 2 * V15_CB_BYTES + CombineSmem<V15_WARPS>::kBytes;
 static_assert(V15_Q_OFF + 8 * V15_Q_PITCH * 4 <= (int)kV15Smem, "q' must fit in the combine area");
 
+template <bool ROWS>
 __device__ __forceinline__ void transform_queries(const DecodeParams& p, int b, int kvh, int warp,
                                                   int lane, float* s_qp, int pitch, int col0, int nloc) {
-  transform_query(p, load_query(p, b, kvh, warp, lane, col0, nloc), warp, lane, s_qp, pitch, nloc);
+  transform_query<ROWS>(p, load_query<ROWS>(p, b, kvh, warp, lane, col0, nloc), warp, lane, s_qp, pitch, nloc);
 }
 
 // Attention weights: a CTA's 4 columns are computed from q' in two fp16 parts,
@@ -198,9 +199,9 @@ __device__ __forceinline__ void put_scores(float* row, const float (&sc)[4], int
 // bit), or the byte offset of the K / V codebook (3 bit).
 // Softmax state m0/l0, m1/l1 belongs to heads 2tig, 2tig+1, the columns of
 // this lane's O^T fragments.
-// MASS: the 8 columns are 4 queries' high fp16 parts, then their low parts
-// (scores_of_parts); srow: where token tile0 * 16 of the lane's columns goes.
-template <int T, int MODE, bool MASS>
+// FORM other than kPlain: the 8 columns are 4 queries' high fp16 parts, then their low
+// parts (scores_of_parts); srow (kMass): where token tile0 * 16 of the lane's columns goes.
+template <int T, int MODE, int FORM>
 __device__ __forceinline__ void vq2_step(const unsigned char* s_cb, uint32_t kbyte, uint32_t vbyte,
                                          const uint32_t (&qa)[8][2], const uint32_t (&kw)[T][V2Geo<MODE>::KW],
                                          const uint32_t (&vw)[T][V2Geo<MODE>::VW], int tile0,
@@ -247,7 +248,7 @@ __device__ __forceinline__ void vq2_step(const unsigned char* s_cb, uint32_t kby
 #pragma unroll
     for (int e = 0; e < 4; ++e) sc[i][e] = da[e] + db[e];
   }
-  if constexpr (MASS) {
+  if constexpr (FORM != kPlain) {
 #pragma unroll
     for (int i = 0; i < T; ++i) scores_of_parts(sc[i]);
   }
@@ -255,7 +256,7 @@ __device__ __forceinline__ void vq2_step(const unsigned char* s_cb, uint32_t kby
 #pragma unroll
     for (int i = 0; i < T; ++i) mask_scores(sc[i], (tile0 + i) * V2_TILE + gid, cl);
   }
-  if constexpr (MASS) {
+  if constexpr (FORM == kMass) {
 #pragma unroll
     for (int i = 0; i < T; ++i) put_scores(srow + i * (V2_TILE * 4), sc[i], lane);
   }
@@ -317,7 +318,7 @@ __device__ __forceinline__ void vq2_step(const unsigned char* s_cb, uint32_t kby
 // code at bit 40 slot + 20 pp once the run is shifted right by vshift
 // (10 bits for odd gid); each gather feeds four M-tiles (channel pairs).
 // kbyte / vbyte: this lane's codebook copy (tig) in the K / V table.
-template <int T, bool MASS>
+template <int T, int FORM>
 __device__ __forceinline__ void vq125_step(const unsigned char* s_cb, uint32_t kbyte, uint32_t vbyte,
                                            const uint32_t (&qa)[8][2], const uint32_t (&kw)[T][3],
                                            const uint32_t (&vw)[T][5], uint32_t vshift, int tile0,
@@ -338,7 +339,7 @@ __device__ __forceinline__ void vq125_step(const unsigned char* s_cb, uint32_t k
 #pragma unroll
     for (int e = 0; e < 4; ++e) sc[i][e] = da[e] + db[e];
   }
-  if constexpr (MASS) {
+  if constexpr (FORM != kPlain) {
 #pragma unroll
     for (int i = 0; i < T; ++i) scores_of_parts(sc[i]);
   }
@@ -346,7 +347,7 @@ __device__ __forceinline__ void vq125_step(const unsigned char* s_cb, uint32_t k
 #pragma unroll
     for (int i = 0; i < T; ++i) mask_scores(sc[i], (tile0 + i) * V2_TILE + gid, cl);
   }
-  if constexpr (MASS) {
+  if constexpr (FORM == kMass) {
 #pragma unroll
     for (int i = 0; i < T; ++i) put_scores(srow + i * (V2_TILE * 4), sc[i], lane);
   }
@@ -445,17 +446,18 @@ __device__ __noinline__ void append_rows(float4 xv, uint8_t* k_stream, uint8_t* 
 // several (kQueries: per-column causal limits, all columns in the CTA) or
 // several in column groups of up to 8, one CTA each (kQueryGroups).  PAGED:
 // tiles are found through the block table (at most two bulk copies per
-// step).  MASS (with kQueryGroups): column groups of 4, scores and softmax
-// statistics written out.
-template <int Q, bool PAGED, int MODE, bool FLAT, bool MASS = false>
+// step).  FORM (with kQueryGroups where it is not kPlain: column groups of 4):
+// kMass, scores and softmax statistics written out; kRows, packed rows.
+template <int Q, bool PAGED, int MODE, bool FLAT, int FORM = kPlain>
 __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeParams p) {
-  constexpr int WIDTH = MASS ? 4 : 8;   // columns of a group
+  constexpr bool MASS = FORM == kMass, PARTS = FORM != kPlain, ROWS = FORM == kRows;
+  constexpr int WIDTH = PARTS ? 4 : 8;   // columns of a group
   constexpr bool MULTI = Q != kOneQuery, GROUPS = Q == kQueryGroups;
   using G = V2Geo<MODE>;
   using Sm = V2Smem<MODE>;
   using Dim = typename std::conditional<MODE == VQKV_MODE_VQ4, Vq4Dim,
                                         typename std::conditional<G::TEN, Vq15Dim, Vq2Dim>::type>::type;
-  constexpr bool APPEND = !G::PAIRS && !G::TEN && !MASS;   // the fused append encodes one-byte codes only
+  constexpr bool APPEND = !G::PAIRS && !G::TEN && !PARTS;   // the fused append encodes one-byte codes only
   extern __shared__ __align__(128) unsigned char smem[];
   // Codebooks.  256 entries: centroid c at row c (256 bytes), K replicas at
   // c*256 + r*2*DSUB, V replicas at c*256 + 128 + r*2*DSUB; 2 bit: lane l
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeP
   int* s_flat = s_pref + kFlatMaxB + 1;   // T, S_eff, r0, r1 (read at piece boundaries only)
   int b = b_begin, b_stop = b_end;
   if (FLAT) {
-    flat_prefix<G::TPI>(p, s_pref);
+    flat_prefix<G::TPI, ROWS>(p, s_pref);
     const int T = s_pref[p.B], S_eff = min(p.n_splits, T);
     b = p.B;
     if (split < S_eff) {
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeP
     if (split == 0) {
       for (int i = threadIdx.x; i < p.B * nloc * kHeadDim; i += V2_THREADS) {
         const int bb = i / (nloc * kHeadDim), c = col0 + (i / kHeadDim) % nloc;
-        if (s_pref[bb + 1] == s_pref[bb]) p.out[out_row(p, bb, kvh, c) + (i & (kHeadDim - 1))] = __float2half_rn(0.f);
+        if (s_pref[bb + 1] == s_pref[bb]) store_output<ROWS>(p, bb, kvh, c, i & (kHeadDim - 1), 0.f);
       }
     }
     __syncthreads();
@@ -554,7 +556,7 @@ __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeP
       cb_entry = __ldg(reinterpret_cast<const CbEntry*>((threadIdx.x >> 8) ? p.vcb : p.kcb) + (size_t)kvh * 256 +
                        (threadIdx.x & 255));
     }
-    const QueryLoad qload = load_query(p, b, kvh, warp, lane, col0, nloc);
+    const QueryLoad qload = load_query<ROWS>(p, b, kvh, warp, lane, col0, nloc);
     uint2 xraw = make_uint2(0u, 0u);
     float4 xs = make_float4(1.f, 1.f, 1.f, 1.f);
     if (APPEND && p.k_new != nullptr) {
@@ -562,11 +564,11 @@ __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeP
       xraw = *reinterpret_cast<const uint2*>((warp < 8 ? p.k_new : p.v_new) + row);
       if (warp < 8) xs = *reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 4 * lane);
     }
-    const int L = load_len(p, b);
+    const int L = load_len<ROWS>(p, b);
     const int ntiles = (L + V2_TILE - 1) / V2_TILE;
     const int t_begin = FLAT ? piece_t0 : split * p.tps;
     const int t_end = min(FLAT ? piece_t1 : t_begin + p.tps, ntiles);
-    const ColumnLimits cl = MULTI ? column_limits(p, L, MASS ? tig & 1 : tig, col0) : ColumnLimits{L, L, L};
+    const ColumnLimits cl = MULTI ? column_limits(p, L, PARTS ? tig & 1 : tig, col0) : ColumnLimits{L, L, L};
     float acc[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
@@ -680,7 +682,7 @@ __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeP
 #pragma unroll 1
         for (int i = 0; i < G::REPL; ++i) row[(i + lane) & (G::REPL - 1)] = cb_entry;
       }
-      transform_query(p, qload, warp, lane, s_qp, V2_Q_PITCH, nloc);
+      transform_query<ROWS>(p, qload, warp, lane, s_qp, V2_Q_PITCH, nloc);
       __syncthreads();
       if constexpr (APPEND) if (append) {
         const size_t stream = (size_t)(b * p.Hkv + kvh) * p.stream_bytes;
@@ -694,8 +696,8 @@ __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeP
       // 4j..4j+3 of j = 4s+tig; 4 bit: channels 16s+2tig, +1 and
       // 16s+8+2tig, +1; 1.25 bit: channels 8j + 4(s%2) .. +3 of j = 4(s/2)+tig
       uint32_t qa[8][2];
-      const int qcol = MASS ? gid & 3 : gid;
-      auto part = [&](float x, float y) { return MASS ? pack_part(x, y, gid >= 4) : pack_half2(x, y); };
+      const int qcol = PARTS ? gid & 3 : gid;
+      auto part = [&](float x, float y) { return PARTS ? pack_part(x, y, gid >= 4) : pack_half2(x, y); };
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         if (qcol < nloc) {
@@ -762,10 +764,10 @@ __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeP
         const int tile = t_begin + (warp + j * V2_WARPS) * G::TPI;
         float* srow = MASS ? score_base + (size_t)tile * (V2_TILE * 4) : nullptr;
         if constexpr (G::TEN)
-          vq125_step<G::TPI, MASS>(s_cb, kbyte, vbyte, qa, kq, vq, 10u * (gid & 1), tile, cl, lane, m0, m1, l0, l1, acc,
+          vq125_step<G::TPI, FORM>(s_cb, kbyte, vbyte, qa, kq, vq, 10u * (gid & 1), tile, cl, lane, m0, m1, l0, l1, acc,
                                    srow);
         else
-          vq2_step<G::TPI, MODE, MASS>(s_cb, kbyte, vbyte, qa, kq, vq, tile, cl, lane, m0, m1, l0, l1, acc, srow);
+          vq2_step<G::TPI, MODE, FORM>(s_cb, kbyte, vbyte, qa, kq, vq, tile, cl, lane, m0, m1, l0, l1, acc, srow);
       }
       if (stalled >= 0) {
         // The copies in flight are exactly the ring indices issued but not
@@ -791,14 +793,15 @@ __global__ void __launch_bounds__(V2_THREADS, 1) decode_vq2_kernel(const DecodeP
       span = {split - s_first, s_last - s_first + 1,
               (((size_t)kvh * (p.n_splits + p.B - 1) + s_first + b) * p.ncols + col0) * kPartialStride};
     }
-    finish_sequence<V2_WARPS, GROUPS, Dim, MASS>(p, b, kvh, span, s_comb, &s_last);
+    finish_sequence<V2_WARPS, GROUPS, Dim, FORM>(p, b, kvh, span, s_comb, &s_last);
     __syncthreads();   // (a warp that timed out still takes part in every barrier)
   }
 }
 
-template <int Q, bool PAGED, bool MASS = false>
+template <int Q, bool PAGED, int FORM = kPlain>
 __global__ void __launch_bounds__(V15_THREADS, 1) decode_vq15_kernel(const DecodeParams p) {
-  constexpr int WIDTH = MASS ? 4 : 8;   // columns of a group
+  constexpr bool MASS = FORM == kMass, PARTS = FORM != kPlain, ROWS = FORM == kRows;
+  constexpr int WIDTH = PARTS ? 4 : 8;   // columns of a group
   constexpr bool MULTI = Q != kOneQuery, GROUPS = Q == kQueryGroups;
   extern __shared__ __align__(128) unsigned char smem[];
   uint4* s_kcb = reinterpret_cast<uint4*>(smem);
@@ -822,11 +825,11 @@ __global__ void __launch_bounds__(V15_THREADS, 1) decode_vq15_kernel(const Decod
   grid_dependents_launch();
 
   for (int b = b_begin; b < b_end; ++b) {
-    const int L = load_len(p, b);
+    const int L = load_len<ROWS>(p, b);
     const int ntiles = (L + V15_TILE - 1) / V15_TILE;
     const int t_begin = split * p.tps;
     const int t_end = min(t_begin + p.tps, ntiles);
-    const ColumnLimits cl = MULTI ? column_limits(p, L, MASS ? tig & 1 : tig, col0) : ColumnLimits{L, L, L};
+    const ColumnLimits cl = MULTI ? column_limits(p, L, PARTS ? tig & 1 : tig, col0) : ColumnLimits{L, L, L};
     float acc[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
@@ -859,11 +862,11 @@ __global__ void __launch_bounds__(V15_THREADS, 1) decode_vq15_kernel(const Decod
         }
         have_cb = true;
       }
-      transform_queries(p, b, kvh, warp, lane, s_qp, V15_Q_PITCH, col0, nloc);
+      transform_queries<ROWS>(p, b, kvh, warp, lane, s_qp, V15_Q_PITCH, col0, nloc);
       __syncthreads();
       uint32_t qf[8][2];
-      const int qcol = MASS ? gid & 3 : gid;
-      auto part = [&](float x, float y) { return MASS ? pack_part(x, y, gid >= 4) : pack_half2(x, y); };
+      const int qcol = PARTS ? gid & 3 : gid;
+      auto part = [&](float x, float y) { return PARTS ? pack_part(x, y, gid >= 4) : pack_half2(x, y); };
       float* score_base = MASS ? score_rows(p, b, kvh) : nullptr;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
@@ -918,7 +921,7 @@ __global__ void __launch_bounds__(V15_THREADS, 1) decode_vq15_kernel(const Decod
             mma_16816(sc, X.x, Y.x, X.y, Y.y, qf[2 * s2][0], qf[2 * s2][1]);
             mma_16816(sc, X.z, Y.z, X.w, Y.w, qf[2 * s2 + 1][0], qf[2 * s2 + 1][1]);
           }
-          if constexpr (MASS) scores_of_parts(sc);
+          if constexpr (PARTS) scores_of_parts(sc);
           if (tq + 16 > cl.lim_min) mask_scores(sc, tq + gid, cl);
           if constexpr (MASS) put_scores(score_base + (size_t)tq * 4, sc, lane);
           uint32_t bP0, bP1;
@@ -953,7 +956,7 @@ __global__ void __launch_bounds__(V15_THREADS, 1) decode_vq15_kernel(const Decod
     __syncthreads();   // every warp is done with its code slot: the combine area overlaps them
     stash_warp<V15_WARPS, 8>(s_comb, warp, lane, acc, m0, m1, l0, l1, Vq15Dim());
     __syncthreads();
-    finish_sequence<V15_WARPS, GROUPS, Vq15Dim, MASS>(p, b, kvh, split_span(p, b, kvh, split, col0), s_comb, &s_last);
+    finish_sequence<V15_WARPS, GROUPS, Vq15Dim, FORM>(p, b, kvh, split_span(p, b, kvh, split, col0), s_comb, &s_last);
     __syncthreads();
   }
 }

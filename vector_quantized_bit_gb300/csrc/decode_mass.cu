@@ -3,7 +3,7 @@
 //
 // The weight of token t is sum over columns of exp2(s_t - m) / l, and a
 // column's m and l are known only when every split has been merged.  The
-// decode kernels (decode_kernels.cuh, MASS) therefore store the scores as
+// decode kernels (decode_kernels.cuh, kMass) therefore store the scores as
 // they pass through the softmax, 16 bytes per token and KV head for 4
 // columns, and the merge leaves (m, 1 / l) per column; a second, streaming
 // kernel adds the weights.  The alternative, a second pass over the key codes,
@@ -69,16 +69,16 @@ __global__ void __launch_bounds__(MS_THREADS) decode_mass_kernel(const DecodePar
 __global__ void __launch_bounds__(kHeadDim) mass_combine_kernel(const DecodeParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
-  combine_splits<true>(p);
+  combine_splits<kMass>(p);
 }
 
 using DecodeKernel = void (*)(DecodeParams);
 template <int MODE>
 DecodeKernel ring_of(bool flat, bool paged) {
-  return flat ? (paged ? (DecodeKernel)decode_vq2_kernel<kQueryGroups, true, MODE, true, true>
-                       : (DecodeKernel)decode_vq2_kernel<kQueryGroups, false, MODE, true, true>)
-              : (paged ? (DecodeKernel)decode_vq2_kernel<kQueryGroups, true, MODE, false, true>
-                       : (DecodeKernel)decode_vq2_kernel<kQueryGroups, false, MODE, false, true>);
+  return flat ? (paged ? (DecodeKernel)decode_vq2_kernel<kQueryGroups, true, MODE, true, kMass>
+                       : (DecodeKernel)decode_vq2_kernel<kQueryGroups, false, MODE, true, kMass>)
+              : (paged ? (DecodeKernel)decode_vq2_kernel<kQueryGroups, true, MODE, false, kMass>
+                       : (DecodeKernel)decode_vq2_kernel<kQueryGroups, false, MODE, false, kMass>);
 }
 DecodeKernel mass_kernel_of(int mode, bool flat, bool paged) {
   switch (mode) {
@@ -87,8 +87,8 @@ DecodeKernel mass_kernel_of(int mode, bool flat, bool paged) {
     case VQKV_MODE_VQ3: return ring_of<VQKV_MODE_VQ3>(flat, paged);
     case VQKV_MODE_VQ125: return ring_of<VQKV_MODE_VQ125>(flat, paged);
     default:   // 1.5 bit has no flat plan
-      return paged ? (DecodeKernel)decode_vq15_kernel<kQueryGroups, true, true>
-                   : (DecodeKernel)decode_vq15_kernel<kQueryGroups, false, true>;
+      return paged ? (DecodeKernel)decode_vq15_kernel<kQueryGroups, true, kMass>
+                   : (DecodeKernel)decode_vq15_kernel<kQueryGroups, false, kMass>;
   }
 }
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "decode_common.cuh"
 #include "internal.h"
 
 namespace vqkv {
@@ -14,13 +15,19 @@ struct QueryLoad {
   uint2 q;
   float4 s;
 };
+template <bool ROWS = false>
 __device__ __forceinline__ QueryLoad load_query(const DecodeParams& p, int b, int kvh, int warp, int lane, int col0,
                                                 int nloc) {
   QueryLoad r{make_uint2(0u, 0u), make_float4(0.f, 0.f, 0.f, 0.f)};
   if (warp < nloc) {
     const int c = col0 + warp;
     const int m = c / p.g, hq = kvh * p.g + c - m * p.g;
-    r.q = *reinterpret_cast<const uint2*>(p.q + (((size_t)b * p.M + m) * p.Hq + hq) * kHeadDim + 4 * lane);
+    const __half* q;
+    if constexpr (ROWS)   // one packed row per sequence (or none: the lane's load is not used)
+      q = p.q + row_range(p, b, false).first * p.q_row + hq * kHeadDim;
+    else
+      q = p.q + (((size_t)b * p.M + m) * p.Hq + hq) * kHeadDim;
+    r.q = *reinterpret_cast<const uint2*>(q + 4 * lane);
     r.s = *reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 4 * lane);
   }
   return r;
@@ -28,6 +35,7 @@ __device__ __forceinline__ QueryLoad load_query(const DecodeParams& p, int b, in
 
 // q' of the CTA's softmax column col0 + warp into row `warp` of s_qp (fp32,
 // scaled, rows `pitch` floats apart), by warps 0..nloc-1.
+template <bool ROWS = false>
 __device__ __forceinline__ void transform_query(const DecodeParams& p, const QueryLoad& r, int warp, int lane,
                                                 float* s_qp, int pitch, int nloc) {
   if (warp < nloc) {
@@ -35,6 +43,11 @@ __device__ __forceinline__ void transform_query(const DecodeParams& p, const Que
     const __half2 q23 = *reinterpret_cast<const __half2*>(&r.q.y);
     float v[4] = {__low2float(q01) * r.s.x, __high2float(q01) * r.s.y, __low2float(q23) * r.s.z,
                   __high2float(q23) * r.s.w};
+    if constexpr (ROWS)
+      if (p.bf16) {   // the upper halves of the fp32 values
+        v[0] = __uint_as_float(r.q.x << 16) * r.s.x, v[1] = __uint_as_float(r.q.x & 0xffff0000u) * r.s.y;
+        v[2] = __uint_as_float(r.q.y << 16) * r.s.z, v[3] = __uint_as_float(r.q.y & 0xffff0000u) * r.s.w;
+      }
     fwht128_f32(v, lane);
     float4 o = make_float4(v[0] * p.qscale, v[1] * p.qscale, v[2] * p.qscale, v[3] * p.qscale);
     *reinterpret_cast<float4*>(s_qp + warp * pitch + 4 * lane) = o;

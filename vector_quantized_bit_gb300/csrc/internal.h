@@ -181,6 +181,11 @@ cudaError_t cross_prepare(int mode);
 size_t cross_query_bytes(int B, int Hq, int Hkv, int n_rows, int layout);
 cudaError_t launch_cross(int mode, const DecodeParams& p, int layout, int groups_max, void* qx, cudaStream_t stream);
 
+// Cross attention of one query per sequence (cross_rows.cu), on the decode's plan at
+// four columns per CTA.
+cudaError_t cross_rows_prepare(int mode);
+cudaError_t launch_cross_rows(int mode, const DecodeParams& p, dim3 grid, cudaStream_t stream);
+
 // Attention weights of many columns (mass_tiles.cu); B <= kFlatMaxB, at most 64
 // columns.  image: scratch for the transformed queries, which are taken before
 // launch_decode_tree (whose output may be the queries' own buffer); the weights

@@ -161,12 +161,8 @@ __device__ __forceinline__ void store_out4(__half* dst, float4 w) {
   }
 }
 
-// Cross attention: O's row of column c of the sequence whose rows start at row0, and
-// the first of the 32-column (PAIR: 16-column) groups of its queries in qx.
-__device__ __forceinline__ size_t cross_out_row(const DecodeParams& p, int row0, int kvh, int c) {
-  const int m = c / p.g, h = c - m * p.g;
-  return ((size_t)(row0 + m) * p.Hq + kvh * p.g + h) * kHeadDim;
-}
+// Cross attention: the first of the 32-column (PAIR: 16-column) groups of a sequence's
+// queries in qx.
 __host__ __device__ __forceinline__ long long cross_query_slot(int row0, int b, int g, int width) {
   return (long long)row0 * g / width + b;
 }
