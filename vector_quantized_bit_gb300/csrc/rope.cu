@@ -17,29 +17,49 @@ namespace {
 // f_i / 2 pi as a 64-bit fraction the 64-bit product's overflow is the range
 // reduction: exact for any 32-bit p but for the fraction's own rounding (2^-65
 // turns times p).  The nearest quarter turn is split off and the rest, at most
-// an eighth of a turn, goes to sincospif as a number of 24 bits or more.
-// One thread: four pairs of one position, two 16-byte stores.
-__global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ RopeTableParams p) {
+// an eighth of a turn, is a number of 24 bits or more for the series.
+// One thread: the same four pairs of RT_ROWS positions, two 16-byte stores each.  Its
+// steps come out of the parameters once (lanes with different indices read them one
+// after another), and from position to position the turn only grows by an exact 64-bit
+// sum.
+// sin and cos of a number x of half turns, |x| <= 1/4: Taylor's series, whose first
+// terms left out are below (pi / 4)^11 / 11! = 2e-9 and (pi / 4)^12 / 12! = 2e-10.
+__device__ __forceinline__ void sincos_half_turns(float x, float& s, float& c) {
+  const float y = x * x;
+  s = x * __fmaf_rn(y, __fmaf_rn(y, __fmaf_rn(y, __fmaf_rn(y, 0.0821458866f, -0.599264529f), 2.55016404f), -5.16771278f), 3.14159265f);
+  c = __fmaf_rn(y, __fmaf_rn(y, __fmaf_rn(y, __fmaf_rn(y, __fmaf_rn(y, -0.0258068914f, 0.23533063f), -1.33526277f), 4.05871213f), -4.9348022f), 1.f);
+}
+
+constexpr int RT_THREADS = 256, RT_ROWS = 8;
+__global__ void __launch_bounds__(RT_THREADS) rope_table_kernel(const __grid_constant__ RopeTableParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const int quads = p.rot >> 3;   // four-pair pieces of a row
-  const long long pieces = (long long)p.n_pos * quads;
-  for (long long k = (long long)blockIdx.x * 256 + threadIdx.x; k < pieces; k += (long long)gridDim.x * 256) {
-    const int pos = (int)(k / quads), i = 4 * (int)(k - (long long)pos * quads);
+  const int quads = p.rot >> 3, rows = RT_THREADS / quads;   // four-pair pieces of a row; rows of a round
+  const int r = threadIdx.x / quads, i = 4 * (threadIdx.x - r * quads);
+  if (r >= rows) return;
+  long long pos = (long long)blockIdx.x * (rows * RT_ROWS) + r;
+  unsigned long long turn[4], step[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    turn[j] = p.step[i + j] * (unsigned long long)pos;
+    step[j] = p.step[i + j] * (unsigned long long)rows;
+  }
+  float* row = p.table + pos * p.rot + i;
+#pragma unroll 2
+  for (int n = 0; n < RT_ROWS && pos < p.n_pos; ++n, pos += rows, row += (long long)rows * p.rot) {
     float c[4], s[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const unsigned long long turn = p.step[i + j] * (unsigned long long)pos;
-      const unsigned top = (unsigned)((turn + (1ull << 31)) >> 32);          // turns in units of 2^-32
+      const unsigned top = (unsigned)((turn[j] + (1ull << 31)) >> 32);       // turns in units of 2^-32
+      turn[j] += step[j];
       const unsigned quarter = (top + (1u << 29)) >> 30;
       const float rest = (float)(int)(top - (quarter << 30)) * 4.656612873077393e-10f;   // half turns: 2^-31 each
       float a, b;
-      sincospif(rest, &a, &b);
+      sincos_half_turns(rest, a, b);
       const float y = quarter & 1 ? b : a, x = quarter & 1 ? a : b;           // quarter turns swap and negate
       s[j] = (quarter & 2 ? -y : y) * p.amplitude;
       c[j] = ((quarter + 1) & 2 ? -x : x) * p.amplitude;
     }
-    float* row = p.table + (size_t)pos * p.rot + i;
     *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1], c[2], c[3]);
     *reinterpret_cast<float4*>(row + (p.rot >> 1)) = make_float4(s[0], s[1], s[2], s[3]);
   }
@@ -49,8 +69,8 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__
 // (y_i, z_i) = (a c - b s, b c + a s) over the row's pairs.  A row is 16 pieces of
 // two four-channel halves: a piece u below rot / 8 holds pairs 4u .. 4u + 3 (both
 // members, so no thread needs another's channels, and the rotation may be in
-// place), the others channels that pass through.  A thread keeps one piece's
-// cosines and sines and takes it in ROWS heads of its token.
+// place), the others channels that pass through.  A thread takes one piece of ROWS
+// heads of each of TOKENS tokens, all its loads in flight before the first is used.
 template <typename T>
 struct Four;   // four channels of a type
 template <>
@@ -86,86 +106,98 @@ struct Four<__nv_bfloat16> {
 
 constexpr int RP_THREADS = 256, RP_PIECES = 16, RP_HEADS = RP_THREADS / RP_PIECES;
 
-template <typename T, int ROWS>
+template <typename T, int ROWS, int TOKENS>
 __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant__ RopeParams p) {
   using F = Four<T>;
   using Word = typename F::Word;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int t = blockIdx.x, u = threadIdx.x & (RP_PIECES - 1);
+  const int t0 = blockIdx.x * TOKENS, u = threadIdx.x & (RP_PIECES - 1);
   const int h0 = (int)blockIdx.y * (RP_HEADS * ROWS) + (threadIdx.x >> 4);
   const bool turns = 8 * u < p.rot;
   const bool split = turns && !p.interleaved;
   const int lo = split ? 4 * u : 8 * u, hi = split ? lo + (p.rot >> 1) : lo + 4;
-  const T* x = static_cast<const T*>(p.x) + (long long)t * p.x_token;
-  T* out = static_cast<T*>(p.out) + (long long)t * p.out_token;
-  const int pos = __ldg(p.pos + t);
-  Word a[ROWS], b[ROWS];
+  int pos[TOKENS];
+  Word a[TOKENS][ROWS], b[TOKENS][ROWS];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int h = h0 + i * RP_HEADS;
-    if (h < p.H) {
-      const T* row = x + (long long)h * p.x_head;
-      a[i] = *reinterpret_cast<const Word*>(row + lo);
-      b[i] = *reinterpret_cast<const Word*>(row + hi);
-    }
-  }
-  if (pos < 0 || pos >= p.n_pos) {
-    if (threadIdx.x == 0 && blockIdx.y == 0 && p.err) atomicOr(p.err, VQKV_DEVERR_POSITION);
-    return;
-  }
-  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (turns) {
-    const float* row = p.table + (size_t)pos * p.rot + 4 * u;
-    c = __ldg(reinterpret_cast<const float4*>(row));
-    s = __ldg(reinterpret_cast<const float4*>(row + (p.rot >> 1)));
-    if (p.transpose) s = make_float4(-s.x, -s.y, -s.z, -s.w);
-  }
-  const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+  for (int k = 0; k < TOKENS; ++k) pos[k] = t0 + k < p.T ? __ldg(p.pos + t0 + k) : 0;
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int h = h0 + i * RP_HEADS;
-    if (h >= p.H) break;
-    if (turns) {
-      float v[4], w[4];
-      F::get(a[i], v);
-      F::get(b[i], w);
-      if (p.interleaved) {   // the halves hold two pairs each
-        float y[4], z[4];
+  for (int k = 0; k < TOKENS; ++k)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          y[2 * j] = v[2 * j] * cv[j] - v[2 * j + 1] * sv[j], y[2 * j + 1] = v[2 * j + 1] * cv[j] + v[2 * j] * sv[j];
-          z[2 * j] = w[2 * j] * cv[2 + j] - w[2 * j + 1] * sv[2 + j];
-          z[2 * j + 1] = w[2 * j + 1] * cv[2 + j] + w[2 * j] * sv[2 + j];
-        }
-        a[i] = F::put(y), b[i] = F::put(z);
-      } else {
-        float y[4], z[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = v[j] * cv[j] - w[j] * sv[j], z[j] = w[j] * cv[j] + v[j] * sv[j];
-        a[i] = F::put(y), b[i] = F::put(z);
+    for (int i = 0; i < ROWS; ++i) {
+      const int h = h0 + i * RP_HEADS;
+      if (h < p.H && t0 + k < p.T) {
+        const T* row = static_cast<const T*>(p.x) + (long long)(t0 + k) * p.x_token + (long long)h * p.x_head;
+        a[k][i] = *reinterpret_cast<const Word*>(row + lo);
+        b[k][i] = *reinterpret_cast<const Word*>(row + hi);
       }
     }
-    T* row = out + (long long)h * p.out_head;
-    *reinterpret_cast<Word*>(row + lo) = a[i];
-    *reinterpret_cast<Word*>(row + hi) = b[i];
+#pragma unroll
+  for (int k = 0; k < TOKENS; ++k) {
+    if (t0 + k >= p.T) break;
+    if (pos[k] < 0 || pos[k] >= p.n_pos) {
+      if (threadIdx.x == 0 && blockIdx.y == 0 && p.err) atomicOr(p.err, VQKV_DEVERR_POSITION);
+      continue;
+    }
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (turns) {
+      const float* row = p.table + (size_t)pos[k] * p.rot + 4 * u;
+      c = __ldg(reinterpret_cast<const float4*>(row));
+      s = __ldg(reinterpret_cast<const float4*>(row + (p.rot >> 1)));
+      if (p.transpose) s = make_float4(-s.x, -s.y, -s.z, -s.w);
+    }
+    const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int h = h0 + i * RP_HEADS;
+      if (h >= p.H) break;
+      Word y4 = a[k][i], z4 = b[k][i];
+      if (turns) {
+        float v[4], w[4], y[4], z[4];
+        F::get(y4, v);
+        F::get(z4, w);
+        if (p.interleaved) {   // the halves hold two pairs each
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            y[2 * j] = v[2 * j] * cv[j] - v[2 * j + 1] * sv[j], y[2 * j + 1] = v[2 * j + 1] * cv[j] + v[2 * j] * sv[j];
+            z[2 * j] = w[2 * j] * cv[2 + j] - w[2 * j + 1] * sv[2 + j];
+            z[2 * j + 1] = w[2 * j + 1] * cv[2 + j] + w[2 * j] * sv[2 + j];
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = v[j] * cv[j] - w[j] * sv[j], z[j] = w[j] * cv[j] + v[j] * sv[j];
+        }
+        y4 = F::put(y), z4 = F::put(z);
+      }
+      T* row = static_cast<T*>(p.out) + (long long)(t0 + k) * p.out_token + (long long)h * p.out_head;
+      *reinterpret_cast<Word*>(row + lo) = y4;
+      *reinterpret_cast<Word*>(row + hi) = z4;
+    }
   }
 }
 
+// Four rows a thread where that still fills the GPU: of one token, or of two
+// where a token has at most two.
+template <typename T, int ROWS, int TOKENS>
+cudaError_t launch_rope_as(const RopeParams& p, cudaStream_t stream) {
+  constexpr int per = RP_HEADS * ROWS;
+  return launch_pdl(rope_kernel<T, ROWS, TOKENS>, dim3((p.T + TOKENS - 1) / TOKENS, (p.H + per - 1) / per), dim3(RP_THREADS), 0,
+                    stream, p);
+}
 template <typename T>
 cudaError_t launch_rope_of(const RopeParams& p, int sms, cudaStream_t stream) {
-  // four heads a thread where that still fills the GPU
-  const int per4 = RP_HEADS * 4;
-  if ((long long)p.T * ((p.H + per4 - 1) / per4) >= 4 * sms)
-    return launch_pdl(rope_kernel<T, 4>, dim3(p.T, (p.H + per4 - 1) / per4), dim3(RP_THREADS), 0, stream, p);
-  return launch_pdl(rope_kernel<T, 1>, dim3(p.T, (p.H + RP_HEADS - 1) / RP_HEADS), dim3(RP_THREADS), 0, stream, p);
+  if ((long long)p.T * p.H < 64LL * 4 * sms) return launch_rope_as<T, 1, 1>(p, stream);
+  if (p.H <= RP_HEADS) return launch_rope_as<T, 1, 4>(p, stream);
+  if (p.H <= 2 * RP_HEADS) return launch_rope_as<T, 2, 2>(p, stream);
+  if (p.H <= 3 * RP_HEADS) return launch_rope_as<T, 3, 1>(p, stream);
+  return launch_rope_as<T, 4, 1>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t stream) {
-  const long long blocks = ((long long)p.n_pos * (p.rot >> 3) + 255) / 256;
-  return launch_pdl(rope_table_kernel, dim3((unsigned)std::min<long long>(blocks, 1 << 20)), dim3(256), 0, stream, p);
+  const int rows = RT_THREADS / (p.rot >> 3) * RT_ROWS;
+  return launch_pdl(rope_table_kernel, dim3((unsigned)(((long long)p.n_pos + rows - 1) / rows)), dim3(RT_THREADS), 0, stream, p);
 }
 
 cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t stream) {
