@@ -678,17 +678,15 @@ vqkv_status encode_launch(const vqkv_encode_args* a, void* stream, const vqkv_pa
   p.role = a->role;
   const long long rows = (long long)a->B * a->n_rows;   // per KV head
   // Few rows (a decode-step append): one row per CTA, its candidates split
-  // over the CTA's warps, for latency.  Many rows: one row per warp.
+  // over the CTA's warps, for latency.
   const bool split_rows = rows * a->Hkv * encode_warps_per_cta() <= (long long)di.sms * 8;
   int blocks_x;
   if (split_rows) {
     blocks_x = (int)rows;
   } else {
     const long long want = (rows + encode_warps_per_cta() - 1) / encode_warps_per_cta();
-    // every mode but 4 bit: persistent tensor-memory CTAs over tiles of 8 or
-    // 4 rows, one wave; 4 bit: one warp per row, 4 waves
-    const int waves = a->mode == VQKV_MODE_VQ4 ? 4 : 1;
-    long long cap = ((long long)di.sms * di.encode_bpsm[a->mode] * waves + a->Hkv - 1) / a->Hkv;
+    // persistent tensor-memory CTAs over tiles of 8, 4 or 2 rows, one wave
+    long long cap = ((long long)di.sms * di.encode_bpsm[a->mode] + a->Hkv - 1) / a->Hkv;
     if (cap < 1) cap = 1;
     blocks_x = (int)std::min(want, cap);
   }

@@ -16,30 +16,29 @@ struct AppendVariant {
   int threads;
   size_t smem;
   int rows;     // rows a CTA takes at a time
-  int waves;    // CTAs per SM
 };
 
 // Few rows: one row per CTA, its candidates split over the CTA's warps.  Many:
-// the tensor-memory search, one persistent CTA per SM (4 bit: one warp per row).
+// the tensor-memory search, one persistent CTA per SM.
 AppendVariant variant(int mode, bool few) {
   switch (mode) {
     case VQKV_MODE_VQ2:
-      if (few) return {encode_vq2_kernel<ENC_WARPS, 4, true>, ENC_THREADS, 0, 1, 1};
-      return {encode_umma_kernel<VQKV_MODE_VQ2, true>, um::THREADS, UmGeo<VQKV_MODE_VQ2>::SMEM, UmGeo<VQKV_MODE_VQ2>::ROWS, 1};
+      if (few) return {encode_vq2_kernel<ENC_WARPS, 4, true>, ENC_THREADS, 0, 1};
+      return {encode_umma_kernel<VQKV_MODE_VQ2, true>, um::THREADS, UmGeo<VQKV_MODE_VQ2>::SMEM, UmGeo<VQKV_MODE_VQ2>::ROWS};
     case VQKV_MODE_VQ4:
-      if (few) return {encode_vq2_kernel<ENC_WARPS, 2, true>, ENC_THREADS, 0, 1, 1};
-      return {encode_vq2_kernel<1, 2, true>, ENC_THREADS, 0, ENC_WARPS, 16};
+      if (few) return {encode_vq2_kernel<ENC_WARPS, 2, true>, ENC_THREADS, 0, 1};
+      return {encode_umma_kernel<VQKV_MODE_VQ4, true>, um::THREADS, UmGeo<VQKV_MODE_VQ4>::SMEM, UmGeo<VQKV_MODE_VQ4>::ROWS};
     case VQKV_MODE_VQ3:
-      if (few) return {encode_vq3_kernel<ENC3_SPLIT, true>, ENC3_SPLIT * 32, kEnc3Smem, 1, 1};
-      return {encode_umma_kernel<VQKV_MODE_VQ3, true>, um::THREADS, UmGeo<VQKV_MODE_VQ3>::SMEM, UmGeo<VQKV_MODE_VQ3>::ROWS, 1};
+      if (few) return {encode_vq3_kernel<ENC3_SPLIT, true>, ENC3_SPLIT * 32, kEnc3Smem, 1};
+      return {encode_umma_kernel<VQKV_MODE_VQ3, true>, um::THREADS, UmGeo<VQKV_MODE_VQ3>::SMEM, UmGeo<VQKV_MODE_VQ3>::ROWS};
     case VQKV_MODE_VQ125:
-      if (few) return {encode_vq125_kernel<ENC_WARPS, true>, ENC_THREADS, 0, 1, 1};
+      if (few) return {encode_vq125_kernel<ENC_WARPS, true>, ENC_THREADS, 0, 1};
       return {encode_umma_kernel<VQKV_MODE_VQ125, true>, um::THREADS, UmGeo<VQKV_MODE_VQ125>::SMEM,
-              UmGeo<VQKV_MODE_VQ125>::ROWS, 1};
+              UmGeo<VQKV_MODE_VQ125>::ROWS};
     default:
-      if (few) return {encode_vq15_tc_split_kernel<true>, TC_THREADS, kTcSplitSmem, 1, 1};
+      if (few) return {encode_vq15_tc_split_kernel<true>, TC_THREADS, kTcSplitSmem, 1};
       return {encode_umma_kernel<VQKV_MODE_VQ15, true>, um::THREADS, UmGeo<VQKV_MODE_VQ15>::SMEM,
-              UmGeo<VQKV_MODE_VQ15>::ROWS, 1};
+              UmGeo<VQKV_MODE_VQ15>::ROWS};
   }
 }
 
@@ -61,7 +60,7 @@ cudaError_t launch_append(int mode, AppendParams p, int sms, cudaStream_t stream
   int keys = want, values = want;
   if (v.rows > 1) {
     // whole waves: with one CTA per SM a few CTAs more would double the time
-    const int most = std::max(2, sms * v.waves / Hkv);
+    const int most = std::max(2, sms / Hkv);
     keys = std::min(want, (most + 1) / 2);
     values = std::min(want, most - keys);
   }

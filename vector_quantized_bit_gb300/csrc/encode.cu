@@ -21,6 +21,8 @@ cudaError_t encode_prepare(int mode) {
   if (mode == VQKV_MODE_VQ2)
     return cudaFuncSetAttribute(encode_umma_kernel<VQKV_MODE_VQ2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)UmGeo<VQKV_MODE_VQ2>::SMEM);
+  if (mode == VQKV_MODE_VQ4)
+    return cudaFuncSetAttribute(encode_umma_kernel<VQKV_MODE_VQ4>, smem_attr, (int)UmGeo<VQKV_MODE_VQ4>::SMEM);
   if (mode != VQKV_MODE_VQ15) return cudaSuccess;
   {
     const cudaError_t e0 = cudaFuncSetAttribute(encode_umma_kernel<VQKV_MODE_VQ15>,
@@ -39,7 +41,8 @@ cudaError_t encode_occupancy(int mode, int* blocks_per_sm) {
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, encode_umma_kernel<VQKV_MODE_VQ2>,
                                                          um::THREADS, UmGeo<VQKV_MODE_VQ2>::SMEM);
   if (mode == VQKV_MODE_VQ4)
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, encode_vq2_kernel<1, 2>, ENC_THREADS, 0);
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, encode_umma_kernel<VQKV_MODE_VQ4>,
+                                                         um::THREADS, UmGeo<VQKV_MODE_VQ4>::SMEM);
   if (mode == VQKV_MODE_VQ3)
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, encode_umma_kernel<VQKV_MODE_VQ3>,
                                                          um::THREADS, UmGeo<VQKV_MODE_VQ3>::SMEM);
@@ -60,7 +63,8 @@ cudaError_t launch_encode(int mode, const EncodeParams& p, int blocks_x, bool sp
   }
   if (mode == VQKV_MODE_VQ4) {
     if (split_rows) return launch_pdl(encode_vq2_kernel<ENC_WARPS, 2>, grid, dim3(ENC_THREADS), 0, stream, p);
-    return launch_pdl(encode_vq2_kernel<1, 2>, grid, dim3(ENC_THREADS), 0, stream, p);
+    return launch_pdl(encode_umma_kernel<VQKV_MODE_VQ4>, grid, dim3(um::THREADS), UmGeo<VQKV_MODE_VQ4>::SMEM,
+                      stream, p);
   }
   if (mode == VQKV_MODE_VQ125) {
     if (split_rows) return launch_pdl(encode_vq125_kernel<ENC_WARPS>, grid, dim3(ENC_THREADS), 0, stream, p);

@@ -4,9 +4,8 @@
 // a Hadamard rotation of the keys, K-Means codebook; arXiv summary page,
 // "方法详解", stages 1-2).
 //
-// 1.25-, 2-, 3- and 4-bit: one warp per row (or one CTA per row when rows
-// are few); lane l holds channels 4l..4l+3.  1.5-bit: tensor-core screening with an exact
-// re-rank (below).  For keys the transform
+// Few rows: one CTA per row; lane l holds channels 4l..4l+3.  Many: tensor-core
+// screening with an exact re-rank (below).  For keys the transform
 // x' = (x / s) . H / sqrt(128) is carried in double-float arithmetic (pairs
 // of fp32 with error-free sums and products) and rounded to fp32 once, so the
 // vector handed to the nearest-centroid search is the correctly rounded fp32
@@ -52,17 +51,15 @@ __device__ __forceinline__ const float* key_s(const EncodeParams& p, int kvh) {
 // 256-entry codebooks, one byte per code.  DSUB = 4 (2 bit): lane l holds
 // subvector l (channels 4l..4l+3); DSUB = 2 (4 bit): lane l holds
 // subvectors 2l and 2l+1 (channels 4l, 4l+1 and 4l+2, 4l+3).
-// SPLIT = 1: one warp per row, 256 candidates per lane (many 4-bit rows;
-// many 2-bit rows go to the tensor-memory kernel below).
-// SPLIT = 8: the CTA's 8 warps share one row, 32 candidates each (few rows,
-// e.g. a decode-step append: latency instead of throughput).
+// The CTA's SPLIT = 8 warps share one row, 32 candidates each (few rows, e.g. a
+// decode-step append: latency instead of throughput).
 template <int SPLIT, int DSUB, bool APPEND = false>
 __global__ void __launch_bounds__(ENC_THREADS)
     encode_vq2_kernel(const __grid_constant__ typename Rows<APPEND>::Params a) {
   using Centroid = typename std::conditional<DSUB == 4, float4, float2>::type;
   constexpr int kTileBytes = 16 * (kHeadDim / DSUB);
   __shared__ Centroid s_cb[256];
-  __shared__ Best s_part[SPLIT > 1 ? ENC_WARPS * 32 : 1];
+  __shared__ Best s_part[ENC_WARPS * 32];
   Rows<APPEND> src(a);
   const EncodeParams& p = src.p;
   const int kvh = src.kvh;
@@ -82,12 +79,11 @@ __global__ void __launch_bounds__(ENC_THREADS)
   }
   __syncthreads();
   const int rows = src.count();
-  const int r0 = (SPLIT == 1) ? src.cta() * ENC_WARPS + warp : src.cta();
-  const int rstep = (SPLIT == 1) ? src.ctas() * ENC_WARPS : src.ctas();
-  const int c_lo = (SPLIT == 1) ? 0 : warp * (256 / SPLIT);
+  const int r0 = src.cta(), rstep = src.ctas();
+  const int c_lo = warp * (256 / SPLIT);
   const int c_hi = c_lo + 256 / SPLIT;
   for (int r = r0; r < rows; r += rstep) {
-    const RowPlace w = src.place(r, src.angle(r), lane == 0 && (SPLIT == 1 || warp == 0));
+    const RowPlace w = src.place(r, src.angle(r), lane == 0 && warp == 0);
     if (w.t < 0) continue;
     const int b = w.b, t = w.t;
     float x[4];
@@ -95,7 +91,7 @@ __global__ void __launch_bounds__(ENC_THREADS)
     if constexpr (DSUB == 4) {   // lane = subvector j (channels 4j..4j+3)
       const Best part = vq2_search(x, c_lo, c_hi, [&](int c) { return s_cb[c]; });
       Best bst = merge_warps<SPLIT>(part, warp, lane, s_part);
-      if (SPLIT == 1 || warp == 0) {
+      if (warp == 0) {
         count_near_ties(p.near_tie, is_near_tie(bst.d, bst.s), lane, 0xffffffffu);
         uint8_t* tb = tile_base(p, b, kvh, t, 16, kTileBytes);
         if (tb) tb[vq2_code_offset(p.role, t & 15, lane)] = (uint8_t)bst.i;
@@ -105,7 +101,7 @@ __global__ void __launch_bounds__(ENC_THREADS)
       vq4_search(x, c_lo, c_hi, [&](int c) { return s_cb[c]; }, pa, pb);
       Best ba = merge_warps<SPLIT>(pa, warp, lane, s_part);
       Best bb = merge_warps<SPLIT>(pb, warp, lane, s_part);
-      if (SPLIT == 1 || warp == 0) {
+      if (warp == 0) {
         count_near_ties(p.near_tie, is_near_tie(ba.d, ba.s), lane, 0xffffffffu);
         count_near_ties(p.near_tie, is_near_tie(bb.d, bb.s), lane, 0xffffffffu);
         uint8_t* tb = tile_base(p, b, kvh, t, 16, kTileBytes);
@@ -120,13 +116,11 @@ __global__ void __launch_bounds__(ENC_THREADS)
 
 // ------------------------------------------------------------------ VQ3
 // 4096-entry codebooks of 4-channel subvectors, 12-bit codes in 3-byte
-// pairs (j, j+16).  Lane l holds subvector l (channels 4l..4l+3) and scans
-// the whole codebook (SPLIT = 1, 8 warps, one row per warp) or a slice of
-// 4096 / SPLIT candidates (SPLIT = 16 warps sharing one row per CTA), with
-// the fp32 codebook (or each warp's slice of it) in shared memory (64 KB,
-// read by broadcast).  Lanes 0..15 then write pair l from their own code
-// and lane l + 16's.  The library launches SPLIT = 16 for few rows (a
-// decode step's append); many rows go to the tensor-memory kernel below.
+// pairs (j, j+16).  Few rows (a decode step's append): SPLIT = 16 warps share
+// one row per CTA.  Lane l holds subvector l (channels 4l..4l+3) and scans its
+// warp's 4096 / SPLIT candidates, their slice of the fp32 codebook in shared
+// memory (64 KB in all, read by broadcast).  Lanes 0..15 then write pair l from
+// their own code and lane l + 16's.
 constexpr size_t kEnc3Smem = 4096 * sizeof(float4);
 constexpr int ENC3_SPLIT = 16;
 
@@ -152,54 +146,46 @@ __device__ __forceinline__ Best vq3_search(const float (&x)[4], int c_lo, int c_
 }
 
 template <int SPLIT, bool APPEND = false>
-__global__ void __launch_bounds__(SPLIT == 1 ? ENC_THREADS : SPLIT * 32)
+__global__ void __launch_bounds__(SPLIT * 32)
     encode_vq3_kernel(const __grid_constant__ typename Rows<APPEND>::Params a) {
-  constexpr int kThreads = SPLIT == 1 ? ENC_THREADS : SPLIT * 32;
-  constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) unsigned char enc_smem[];
   float4* s_cb = reinterpret_cast<float4*>(enc_smem);
-  __shared__ Best s_part[SPLIT > 1 ? SPLIT * 32 : 1];
+  __shared__ Best s_part[SPLIT * 32];
   Rows<APPEND> src(a);
   const EncodeParams& p = src.p;
   const int kvh = src.kvh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c_lo = (SPLIT == 1) ? 0 : warp * (4096 / SPLIT);
+  const int c_lo = warp * (4096 / SPLIT);
   const int c_hi = c_lo + 4096 / SPLIT;
   grid_dependency_wait();
   grid_dependents_launch();
   {
-    // the whole codebook (SPLIT = 1, by the CTA) or this warp's slice
-    // (SPLIT > 1, by the warp): every load in flight before the first store
-    constexpr int kPer = SPLIT == 1 ? 4096 / kThreads : 4096 / SPLIT / 32;
-    const int first = SPLIT == 1 ? threadIdx.x : c_lo + lane;
-    const int stride = SPLIT == 1 ? kThreads : 32;
+    // this warp's slice of the codebook: every load in flight before the first store
+    constexpr int kPer = 4096 / SPLIT / 32;
+    const int first = c_lo + lane;
     const uint2* g = reinterpret_cast<const uint2*>(p.cb) + (size_t)kvh * 4096 + first;
     uint2 raw[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) raw[i] = __ldg(g + i * stride);
+    for (int i = 0; i < kPer; ++i) raw[i] = __ldg(g + 32 * i);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const __half2 a = *reinterpret_cast<const __half2*>(&raw[i].x);
       const __half2 b = *reinterpret_cast<const __half2*>(&raw[i].y);
-      s_cb[first + i * stride] = make_float4(__low2float(a), __high2float(a), __low2float(b), __high2float(b));
+      s_cb[first + 32 * i] = make_float4(__low2float(a), __high2float(a), __low2float(b), __high2float(b));
     }
   }
-  if (SPLIT == 1)
-    __syncthreads();
-  else
-    __syncwarp();
+  __syncwarp();
   const int rows = src.count();
-  const int r0 = (SPLIT == 1) ? src.cta() * kWarps + warp : src.cta();
-  const int rstep = (SPLIT == 1) ? src.ctas() * kWarps : src.ctas();
+  const int r0 = src.cta(), rstep = src.ctas();
   for (int r = r0; r < rows; r += rstep) {
-    const RowPlace w = src.place(r, src.angle(r), lane == 0 && (SPLIT == 1 || warp == 0));
+    const RowPlace w = src.place(r, src.angle(r), lane == 0 && warp == 0);
     if (w.t < 0) continue;
     const int b = w.b, t = w.t;
     float x[4];
     src.row(w, r, lane, x);
     const Best part = vq3_search(x, c_lo, c_hi, [&](int c) { return s_cb[c]; });
     const Best bst = merge_warps<SPLIT>(part, warp, lane, s_part);
-    if (SPLIT == 1 || warp == 0) {
+    if (warp == 0) {
       count_near_ties(p.near_tie, is_near_tie(bst.d, bst.s), lane, 0xffffffffu);
       const int hi = __shfl_down_sync(0xffffffffu, bst.i, 16);
       uint8_t* tb = tile_base(p, b, kvh, t, 16, 768);
@@ -215,12 +201,11 @@ __global__ void __launch_bounds__(SPLIT == 1 ? ENC_THREADS : SPLIT * 32)
 // ------------------------------------------------------------------ VQ125
 // 1024-entry codebooks of 8-channel subvectors, 10-bit codes.  Lane l
 // searches subvector l % 16 (channels 8j..8j+7, taken from lanes 2j and
-// 2j+1) over half l / 16 of its warp's candidates (the whole codebook for
-// SPLIT = 1, 1024 / SPLIT per warp otherwise); the halves merge across
-// lanes l and l + 16.  Lanes 0..3 then pack the row's four 40-bit groups
+// 2j+1) over half l / 16 of its warp's 1024 / SPLIT candidates; the halves
+// merge across lanes l and l + 16.  Lanes 0..3 then pack the row's four 40-bit groups
 // (K: subvectors g, g+4, g+8, g+12; V: 2g, 2g+1, 2g+8, 2g+9) and write 5
-// bytes each.  The library launches SPLIT = 8 for few rows (a decode step's
-// append); many rows go to the tensor-memory kernel below.
+// bytes each.  SPLIT = 8, for few rows (a decode step's append); many rows go to
+// the tensor-memory kernel below.
 
 // Search of one 8-channel subvector over candidates [c_lo, c_hi) (a multiple
 // of 4): fp32 direct differences in channel order, four chains over the
@@ -251,13 +236,13 @@ template <int SPLIT, bool APPEND = false>
 __global__ void __launch_bounds__(ENC_THREADS)
     encode_vq125_kernel(const __grid_constant__ typename Rows<APPEND>::Params a) {
   __shared__ float4 s_cb[2 * 1024];
-  __shared__ Best s_part[SPLIT > 1 ? ENC_WARPS * 32 : 1];
+  __shared__ Best s_part[ENC_WARPS * 32];
   Rows<APPEND> src(a);
   const EncodeParams& p = src.p;
   const int kvh = src.kvh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kSpan = 1024 / SPLIT;   // candidates of one warp
-  const int c_lo = (SPLIT == 1 ? 0 : warp * kSpan) + (lane >> 4) * (kSpan / 2);
+  const int c_lo = warp * kSpan + (lane >> 4) * (kSpan / 2);
   const int c_hi = c_lo + kSpan / 2;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -279,10 +264,9 @@ __global__ void __launch_bounds__(ENC_THREADS)
   __syncthreads();
   const bool key = p.role == VQKV_ROLE_K;
   const int rows = src.count();
-  const int r0 = (SPLIT == 1) ? src.cta() * ENC_WARPS + warp : src.cta();
-  const int rstep = (SPLIT == 1) ? src.ctas() * ENC_WARPS : src.ctas();
+  const int r0 = src.cta(), rstep = src.ctas();
   for (int r = r0; r < rows; r += rstep) {
-    const RowPlace w = src.place(r, src.angle(r), lane == 0 && (SPLIT == 1 || warp == 0));
+    const RowPlace w = src.place(r, src.angle(r), lane == 0 && warp == 0);
     if (w.t < 0) continue;
     const int b = w.b, t = w.t;
     float x[4];
@@ -297,7 +281,7 @@ __global__ void __launch_bounds__(ENC_THREADS)
     Best part = vq125_search(xs, c_lo, c_hi, s_cb);
     part = best_merge(part, best_shfl_xor(part, 16));
     const Best bst = merge_warps<SPLIT>(part, warp, lane, s_part);
-    if (SPLIT == 1 || warp == 0) {
+    if (warp == 0) {
       count_near_ties(p.near_tie, is_near_tie(bst.d, bst.s), lane, 0xffffu);
       const int g = lane & 3;
       const uint32_t c0 = __shfl_sync(0xffffffffu, bst.i, key ? g : 2 * g);
@@ -424,6 +408,15 @@ __device__ __forceinline__ float exact_d4_cb(const float* x, const __half* cb4) 
   return __fmaf_rn(e, e, d);
 }
 
+// And for 2 channels (4-bit codebooks).
+__device__ __forceinline__ float exact_d2_cb(const float* x, const __half* cb2) {
+  const float2 a = __half22float2(__ldg(reinterpret_cast<const __half2*>(cb2)));
+  float e = __fsub_rn(x[0], a.x);
+  const float d = __fmul_rn(e, e);
+  e = __fsub_rn(x[1], a.y);
+  return __fmaf_rn(e, e, d);
+}
+
 // Largest centroid norm the fp16 screening tables hold exactly: -2c stays
 // exact and |c|^2 <= 16384 keeps its fp16 hi + lo split finite.  A KV head
 // with a larger centroid is searched exhaustively, from the codebook in
@@ -469,16 +462,16 @@ __device__ __forceinline__ float build_tc_table(const EncodeParams& p, int kvh, 
   return *s_cmax;
 }
 
-// Many rows of 1.5-bit or 2-bit encode on the fifth-generation tensor cores.
+// Many rows on the fifth-generation tensor cores.
 // A tile is 128 (row, subvector) pairs, the M of one tcgen05 MMA: 8 rows of
-// 16 subvectors (1.5 bit) or 4 rows of 32 (2 bit); the 4096 (256) centroids
-// are 32 (2) chunks of N = 128.  The MMAs of a chunk write to tensor memory
+// 16 subvectors (1.5 and 1.25 bit), 4 rows of 32 (2 and 3 bit) or 2 of 64 (4 bit);
+// the centroids are chunks of N = 128.  The MMAs of a chunk write to tensor memory
 //   D[m][c] = [x_hi, 1, 1] . [-2c, |c|^2_hi, |c|^2_lo] + x_lo . (-2c) = |c|^2 - 2 x . c,
 // the screened distance less the subvector's own |x'_j|^2, with x_hi + x_lo the
 // transformed subvector in two fp16 parts (A) and the [-2c, |c|^2_hi, |c|^2_lo]
 // table of all the KV head's centroids (B) in shared memory behind matrix
-// descriptors.  Its error is bounded by screen_eps.  With four channels the low
-// parts fit into the MMA's 16 (B holds -2c twice); with eight they are a second
+// descriptors.  Its error is bounded by screen_eps.  With two or four channels the
+// low parts fit into the MMA's 16 (B holds -2c twice); with eight they are a second
 // MMA.  (x_hi alone, one MMA, leaves 2^-10 |x'| |c|, ten times the margin: several
 // lanes of every warp then have a second group to re-rank, each of them the whole
 // warp's work, and that took half of the kernel's time.)
@@ -537,16 +530,26 @@ constexpr int F_OK = 0, F_EXHAUSTIVE = 1, F_SKIP = 2;
 }  // namespace um
 
 // Per code mode: 8-channel subvectors (1.5 bit: 4096 centroids; 1.25 bit:
-// 1024), 16 a row, 8 rows a tile; or 4-channel ones (2 bit: 256 centroids;
-// 3 bit: 4096), 32 a row, 4 rows a tile.
+// 1024), 16 a row, 8 rows a tile; 4-channel ones (2 bit: 256 centroids; 3 bit:
+// 4096), 32 a row, 4 rows a tile; or 2-channel ones (4 bit: 256), 64 a row, 2
+// rows a tile.
 template <int MODE>
 struct UmGeo {
-  static constexpr int DSUB = (MODE == VQKV_MODE_VQ15 || MODE == VQKV_MODE_VQ125) ? 8 : 4;
-  static constexpr int E = MODE == VQKV_MODE_VQ2 ? 256 : MODE == VQKV_MODE_VQ125 ? 1024 : 4096;
+  static constexpr int DSUB = (MODE == VQKV_MODE_VQ15 || MODE == VQKV_MODE_VQ125) ? 8 : MODE == VQKV_MODE_VQ4 ? 2 : 4;
+  static constexpr int E = MODE == VQKV_MODE_VQ2 || MODE == VQKV_MODE_VQ4 ? 256 : MODE == VQKV_MODE_VQ125 ? 1024 : 4096;
   static constexpr int SUBV = kHeadDim / DSUB;           // subvectors per row
   static constexpr int ROWS = um::M / SUBV;               // rows per tile
   static constexpr int CHUNKS = E / um::N;               // MMAs per tile
   static constexpr int TABLE_BYTES = E * 32;             // B: E centroids x 16 fp16
+  // Warps that take rows in turn.  A warp that comes to stage k % STAGES for tile k
+  // tells by the parity of one phase that tile k - 4 has been released; tile k - 8's
+  // release has to be certain then.  It is when the warp filled tile k - 2 or k - 4
+  // itself: that waited for tile k - 6 or k - 8, which the same epilogue warpgroup
+  // takes in order.  Six warps come to every tile (8 rows), or to two of three (4
+  // rows: k - 4 or k - 2 is among them); of 2 rows to every third, so there only four
+  // work (every second tile).
+  static constexpr int PRODUCERS = ROWS == 2 ? 4 : um::PROD_WARPS;
+  static_assert(um::STAGES == 4, "the argument above");
   // Centroids per group minimum.  16: half as many to re-rank, twice the minima to
   // keep; pays up to 1,024 centroids.
   static constexpr int GROUP = E == 4096 ? 32 : 16;
@@ -560,12 +563,12 @@ struct UmGeo {
   static constexpr int OFF_STAGES = TABLE_BYTES;
   static constexpr int OFF_BAR = OFF_STAGES + um::STAGES * STAGE_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + um::NBAR * 8;   // tensor-memory base, abort flag, max centroid norm
-  // 4-channel modes: the codebook again as plain fp16 [E][4], 8 bytes a
+  // 4- and 2-channel modes: the codebook again as plain fp16; with [E][4], 8 bytes a
   // centroid, so that 16 lanes reading 16 consecutive centroids hit 16
   // distinct bank pairs in the exact re-rank (the B table's 32-byte rows give
   // only 8)
   static constexpr int OFF_CB4 = OFF_MISC + 16;
-  static constexpr size_t SMEM = OFF_CB4 + (DSUB == 4 ? E * 8 : 0);
+  static constexpr size_t SMEM = OFF_CB4 + (DSUB == 8 ? 0 : E * DSUB * 2);
   static_assert(SMEM <= 227 * 1024 && STAGE_BYTES % 16 == 0 && OFF_BAR % 8 == 0, "UMMA encode shared memory");
   static_assert(CHUNKS % um::NBUF == 0 && E / GROUP <= 128 && um::N % GROUP == 0 && ROWS <= 8, "tile plan (7-bit group ids)");
 };
@@ -711,7 +714,8 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   __syncthreads();
 
   // B table: row c = [-2c (8 fp16), |c|^2 hi, |c|^2 lo, 0 x 6] (1.5 bit) or
-  // [-2c (4 fp16), |c|^2 hi, |c|^2 lo, 0, 0, -2c, 0 x 4] (2 bit)
+  // [-2c (4 fp16), |c|^2 hi, |c|^2 lo, 0, 0, -2c, 0 x 4] (2 bit) or
+  // [-2c (2 fp16), |c|^2 hi, |c|^2 lo, -2c, 0 x 10] (4 bit)
   {
     float cmax = 0.f;
     for (int c = threadIdx.x; c < E; c += THREADS) {
@@ -719,9 +723,11 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       if constexpr (DSUB == 8) {
         const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p.cb) + (size_t)kvh * E + c);
         w[0] = raw.x, w[1] = raw.y, w[2] = raw.z, w[3] = raw.w;
-      } else {
+      } else if constexpr (DSUB == 4) {
         const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.cb) + (size_t)kvh * E + c);
         w[0] = raw.x, w[1] = raw.y;
+      } else {
+        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p.cb) + (size_t)kvh * E + c);
       }
       uint32_t m2[DSUB / 2];
       float nn = 0.f;
@@ -741,10 +747,14 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       if constexpr (DSUB == 8) {
         *reinterpret_cast<uint4*>(row) = make_uint4(m2[0], m2[1], m2[2], m2[3]);
         *reinterpret_cast<uint4*>(row + 128) = make_uint4(tw, 0u, 0u, 0u);
-      } else {
+      } else if constexpr (DSUB == 4) {
         *reinterpret_cast<uint4*>(row) = make_uint4(m2[0], m2[1], tw, 0u);
         *reinterpret_cast<uint4*>(row + 128) = make_uint4(m2[0], m2[1], 0u, 0u);
         reinterpret_cast<uint2*>(smem + Geo::OFF_CB4)[c] = make_uint2(w[0], w[1]);
+      } else {
+        *reinterpret_cast<uint4*>(row) = make_uint4(m2[0], tw, m2[0], 0u);
+        *reinterpret_cast<uint4*>(row + 128) = make_uint4(0u, 0u, 0u, 0u);
+        reinterpret_cast<uint32_t*>(smem + Geo::OFF_CB4)[c] = w[0];
       }
       cmax = fmaxf(cmax, sqrtf(nn));
     }
@@ -766,8 +776,9 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   if (warp >= 8 && warp < MMA_WARP) {
     // ---------------- producers
     const int pw = warp - 8;
-    // 1.5 bit: lanes 2j, 2j + 1 hold subvector j; 2 bit: lane j holds subvector j
-    const int j = DSUB == 8 ? lane >> 1 : lane, half = DSUB == 8 ? lane & 1 : 0;
+    // 1.5 bit: lanes 2j, 2j + 1 hold subvector j; 2 bit: lane j holds subvector j;
+    // 4 bit: lane l holds subvectors j = 2l and j + 1
+    const int j = DSUB == 8 ? lane >> 1 : DSUB == 4 ? lane : 2 * lane, half = DSUB == 8 ? lane & 1 : 0;
     const bool key = p.role == VQKV_ROLE_K;
     const float4 s4 = key ? *reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 4 * lane)
                           : make_float4(1.f, 1.f, 1.f, 1.f);
@@ -775,8 +786,9 @@ __global__ void __launch_bounds__(um::THREADS, 1)
     const float4 scale = make_float4(__frcp_rn(s4.x) * kNorm, __frcp_rn(s4.y) * kNorm, __frcp_rn(s4.z) * kNorm,
                                      __frcp_rn(s4.w) * kNorm);
     // Row job i is row i % ROWS of tile i / ROWS; warp pw takes jobs pw, pw +
-    // PROD_WARPS, ...  A job's row is loaded one job ahead, its angle two.
-    const int jobs = n_my * ROWS;
+    // PRODUCERS, ...  A job's row is loaded one job ahead, its angle two.
+    constexpr int PRODUCERS = Geo::PRODUCERS;
+    const int jobs = pw < PRODUCERS ? n_my * ROWS : 0;
     typename Rows<APPEND>::Raw raw{};
     RowPlace at{};
     Turn turn{};
@@ -799,15 +811,15 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         if (at.t >= 0) raw = src.load(row, lane);
       }
       if constexpr (APPEND) turn = src.turn(at.angle, lane);
-      next_angle(job + PROD_WARPS);
+      next_angle(job + PRODUCERS);
     };
     next_angle(pw);
     fetch(pw);
-    for (int job = pw; job < jobs; job += PROD_WARPS) {
+    for (int job = pw; job < jobs; job += PRODUCERS) {
       const typename Rows<APPEND>::Raw cur = raw;
       const RowPlace w = at;
       const Turn u = turn;
-      fetch(job + PROD_WARPS);
+      fetch(job + PRODUCERS);
       const int k = job / ROWS, r = job % ROWS, s = k % STAGES;
       if (!um_wait(a_empty(s), ((k / STAGES) & 1) ^ 1, s_abort, p.err, 0xffffffffu)) break;
       unsigned char* st = smem + OFF_STAGES + s * STAGE_BYTES;
@@ -838,10 +850,16 @@ __global__ void __launch_bounds__(um::THREADS, 1)
               make_uint2(half == 0 ? pack_half2(1.f, 1.f) : 0u, 0u);   // picks |c|^2 hi + lo
           *reinterpret_cast<uint2*>(st + Geo::ST_LOW + off) = make_uint2(l01, l23);
           *reinterpret_cast<uint2*>(st + Geo::ST_LOW + off + 128) = make_uint2(0u, 0u);
-        } else {
+        } else if constexpr (DSUB == 4) {
           const uint32_t off = umma_kmajor_offset((uint32_t)m, 0u);
           *reinterpret_cast<uint4*>(st + ST_A + off) = make_uint4(x01, x23, pack_half2(1.f, 1.f), 0u);
           *reinterpret_cast<uint4*>(st + ST_A + off + 128) = make_uint4(l01, l23, 0u, 0u);
+        } else {
+          const uint32_t off = umma_kmajor_offset((uint32_t)m, 0u), next = umma_kmajor_offset((uint32_t)m + 1, 0u);
+          *reinterpret_cast<uint4*>(st + ST_A + off) = make_uint4(x01, pack_half2(1.f, 1.f), l01, 0u);
+          *reinterpret_cast<uint4*>(st + ST_A + next) = make_uint4(x23, pack_half2(1.f, 1.f), l23, 0u);
+          *reinterpret_cast<uint4*>(st + ST_A + off + 128) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(st + ST_A + next + 128) = make_uint4(0u, 0u, 0u, 0u);
         }
         *reinterpret_cast<float4*>(st + ST_X + (r * kHeadDim + 4 * lane) * 4) = make_float4(x[0], x[1], x[2], x[3]);
         float nx = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
@@ -854,7 +872,10 @@ __global__ void __launch_bounds__(um::THREADS, 1)
           nx += __shfl_xor_sync(0xffffffffu, nx, 1);   // |x'_j|^2
           flag = max(flag, __shfl_xor_sync(0xffffffffu, flag, 1));
         }
-        if (half == 0) {
+        if constexpr (DSUB == 2) {
+          reinterpret_cast<float2*>(st + ST_NORM)[m >> 1] = make_float2(x[0] * x[0] + x[1] * x[1], x[2] * x[2] + x[3] * x[3]);
+          reinterpret_cast<int2*>(st + ST_FLAG)[m >> 1] = make_int2(flag, flag);
+        } else if (half == 0) {
           reinterpret_cast<float*>(st + ST_NORM)[m] = nx;
           reinterpret_cast<int*>(st + ST_FLAG)[m] = flag;
         }
@@ -909,6 +930,12 @@ __global__ void __launch_bounds__(um::THREADS, 1)
     auto exact = [&](const float (&xx)[DSUB], int c) -> float {
       if constexpr (DSUB == 8) {
         return exact_d_umma<8>(xx, table, c);
+      } else if constexpr (DSUB == 2) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(smem + Geo::OFF_CB4 + 4 * c));
+        float e = __fsub_rn(xx[0], a.x);
+        const float d = __fmul_rn(e, e);
+        e = __fsub_rn(xx[1], a.y);
+        return __fmaf_rn(e, e, d);
       } else {
         const uint2 raw = *reinterpret_cast<const uint2*>(smem + Geo::OFF_CB4 + 8 * c);
         const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
@@ -977,8 +1004,13 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       const int flag = reinterpret_cast<const int*>(st + ST_FLAG)[ml];
       float xv[DSUB];
       {
-        const float4 a = *reinterpret_cast<const float4*>(st + ST_X + (r * kHeadDim + DSUB * j) * 4);
-        xv[0] = a.x, xv[1] = a.y, xv[2] = a.z, xv[3] = a.w;
+        if constexpr (DSUB == 2) {
+          const float2 a = *reinterpret_cast<const float2*>(st + ST_X + (r * kHeadDim + DSUB * j) * 4);
+          xv[0] = a.x, xv[1] = a.y;
+        } else {
+          const float4 a = *reinterpret_cast<const float4*>(st + ST_X + (r * kHeadDim + DSUB * j) * 4);
+          xv[0] = a.x, xv[1] = a.y, xv[2] = a.z, xv[3] = a.w;
+        }
         if constexpr (DSUB == 8) {
           const float4 b = *reinterpret_cast<const float4*>(st + ST_X + (r * kHeadDim + 8 * j + 4) * 4);
           xv[4] = b.x, xv[5] = b.y, xv[6] = b.z, xv[7] = b.w;
@@ -987,7 +1019,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       // off: how far x' may be from the exact one, per channel.  A distance moves by
       // 2 off sqrt(DSUB) times its root then; in terms of |x'| and Cmax, for the
       // groups that have to be looked at:
-      const float off = reinterpret_cast<const float*>(st + ST_POS)[16 + r] * (DSUB == 8 ? 2.8284272f : 2.f);
+      const float off = reinterpret_cast<const float*>(st + ST_POS)[16 + r] * (DSUB == 8 ? 2.8284272f : DSUB == 4 ? 2.f : 1.4142136f);
       const float xnorm = approx_sqrt(reinterpret_cast<const float*>(st + ST_NORM)[ml]);
       const float eps = screen_eps(xnorm, Cmax) + 4.f * off * (xnorm + Cmax);
       // a group can hold a candidate within 2 eps of the best when its packed
@@ -1057,7 +1089,12 @@ __global__ void __launch_bounds__(um::THREADS, 1)
           float x[4];
           transform_key_values(v, s, make_float4(__frcp_rn(s.x), __frcp_rn(s.y), __frcp_rn(s.z), __frcp_rn(s.w)), lane, x);
 #pragma unroll
-          for (int i = 0; i < DSUB; ++i) xs[i] = __shfl_sync(0xffffffffu, x[i & 3], DSUB / 4 * jj + i / 4);
+          for (int i = 0; i < DSUB; ++i) {
+            if constexpr (DSUB == 2)
+              xs[i] = __shfl_sync(0xffffffffu, (jj & 1) ? x[2 + i] : x[i], jj >> 1);
+            else
+              xs[i] = __shfl_sync(0xffffffffu, x[i & 3], DSUB / 4 * jj + i / 4);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < DSUB; ++i) xs[i] = __shfl_sync(0xffffffffu, xv[i], src_lane);
@@ -1079,7 +1116,13 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         if (!(Cmax <= kScreenCmax)) {   // centroids beyond the table: from global memory
           const __half* cb_head = p.cb + (size_t)kvh * E * DSUB;
           for (int cc = lane; cc < E; cc += 32) {
-            const float dd = DSUB == 8 ? exact_d8_cb(xs, cb_head + (size_t)cc * 8) : exact_d4_cb(xs, cb_head + (size_t)cc * 4);
+            float dd;
+            if constexpr (DSUB == 8)
+              dd = exact_d8_cb(xs, cb_head + (size_t)cc * 8);
+            else if constexpr (DSUB == 4)
+              dd = exact_d4_cb(xs, cb_head + (size_t)cc * 4);
+            else
+              dd = exact_d2_cb(xs, cb_head + (size_t)cc * 2);
             exact_push(dd, cc, d, c, sd);
           }
         } else {
@@ -1107,6 +1150,11 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         if (flag != F_SKIP) {
           uint8_t* tb = tile_base(p, b, kvh, t, 16, 512);
           if (tb) tb[vq2_code_offset(p.role, t & 15, j)] = (uint8_t)cex;
+        }
+      } else if constexpr (MODE == VQKV_MODE_VQ4) {
+        if (flag != F_SKIP) {
+          uint8_t* tb = tile_base(p, b, kvh, t, 16, 1024);
+          if (tb) tb[vq4_code_offset(p.role, t & 15, j)] = (uint8_t)cex;
         }
       } else if constexpr (MODE == VQKV_MODE_VQ3) {   // lane j < 16 stores the 12-bit pair (j, j + 16)
         const int hi = __shfl_down_sync(0xffffffffu, cex, 16);
