@@ -1050,12 +1050,12 @@ vqkv_status plan_cross(const vqkv_cross_args* ac, CrossPlan* pl) {
   const vqkv_status st = device_info(kCrossKernels, a.mode, &di);
   if (st != VQKV_OK) return st;
   const long long g = a.Hq / a.Hkv, cols = ac->max_queries * g;
-  pl->layout = cols > 128 ? kTwoTiles : cols <= 64 && ac->dtype == VQKV_DTYPE_F16 ? kPairs : kOneTile;
+  pl->layout = ac->dtype == VQKV_DTYPE_F16 ? (cols <= 64 ? kPairs : kBothParts) : cols > 128 ? kTwoTiles : kOneTile;
   const int width = cross_cols(pl->layout), B = std::max(std::min(a.B, kFlatMaxB), 1);
   // items, and tiles of full sequences, at most
   const long long items = std::max<long long>(1, std::min(B * ((cols + width - 1) / width), ac->n_rows * g / width + B));
   const long long units = items * std::max(1, (a.max_seq_len + 63) / 64);
-  const long long want = a.num_splits > 0 ? std::min(a.num_splits, 1024) : (pl->layout == kTwoTiles ? 1 : 2) * (di.sms / a.Hkv);
+  const long long want = a.num_splits > 0 ? std::min(a.num_splits, 1024) : cross_shares(pl->layout) * (di.sms / a.Hkv);
   pl->n_splits = (int)std::max<long long>(1, std::min(want, units));
   pl->groups_max = (int)((cols + width - 1) / width);
   pl->query_off = decode_ticket_region_bytes(a.B, a.Hkv * kTicketGroups);

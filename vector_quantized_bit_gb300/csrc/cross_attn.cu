@@ -35,8 +35,9 @@ __device__ __forceinline__ void store_four(const DecodeParams& p, __half* dst, f
 // q' of every column, as the attention kernel's threads load it (tree_query_kernel's
 // image): sequence b's groups of 32 columns (PAIR: 16) start at cross_query_slot.
 // Columns past a sequence's last are not written: they reach only rows of the
-// products that are not stored.  Four threads per column.
-template <bool PAIR>
+// products that are not stored.  Four threads per column.  LOW: a group's high parts,
+// then its low ones.
+template <bool PAIR, bool LOW>
 __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant__ DecodeParams p, uint4* qx) {
   constexpr int W = PAIR ? 16 : 32;
   __shared__ int s_start[kFlatMaxB + 1];
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant_
   if (!in) return;
   const int c = (row - rows.first) * p.g + h;
   const size_t slot = (size_t)kvh * (cross_query_slot(p.n_rows, p.B, p.g, W) + 1) + cross_query_slot(rows.first, lo, p.g, W) + c / W;
-  uint4* dst = qx + (slot * 16 + 4 * part) * 32 + (c & (W - 1));
+  uint4* dst = qx + ((LOW ? 2 * slot : slot) * 16 + 4 * part) * 32 + (c & (W - 1));
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t w[4], low[4];
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant_
       low[i] = pack_half2(x - __low2float(f), y - __high2float(f));
     }
     dst[32 * j] = make_uint4(w[0], w[1], w[2], w[3]);
-    if (PAIR) dst[32 * j + 16] = make_uint4(low[0], low[1], low[2], low[3]);
+    if (PAIR || LOW) dst[32 * j + (LOW ? 16 * 32 : 16)] = make_uint4(low[0], low[1], low[2], low[3]);
   }
 }
 
@@ -204,9 +205,10 @@ __global__ void __launch_bounds__(CW_WARPS * 32) cross_combine_wide_kernel(const
 using CrossKernel = void (*)(DecodeParams, const unsigned long long*, const uint4*);
 template <int MODE, bool PAGED>
 CrossKernel cross_of(int layout) {
-  if (layout == kPairs) return decode_tree_kernel<MODE, PAGED, 1, true, true>;
-  if (layout == kTwoTiles) return decode_tree_kernel<MODE, PAGED, 2, false, true>;
-  return decode_tree_kernel<MODE, PAGED, 1, false, true>;
+  if (layout == kPairs) return decode_tree_kernel<MODE, PAGED, 1, true, kCross>;
+  if (layout == kTwoTiles) return decode_tree_kernel<MODE, PAGED, 2, false, kCross>;
+  if (layout == kBothParts) return decode_tree_kernel<MODE, PAGED, 1, false, kCrossParts>;
+  return decode_tree_kernel<MODE, PAGED, 1, false, kCross>;
 }
 template <int MODE>
 CrossKernel cross_of(bool paged, int layout) {
@@ -226,25 +228,30 @@ int cross_smem(int mode) {
 }  // namespace
 
 int cross_cols(int layout) { return layout == kPairs ? 64 : layout == kTwoTiles ? 2 * tr::ROWS : tr::ROWS; }
+int cross_shares(int layout) { return layout == kPairs || layout == kOneTile ? 2 : 1; }
 
 cudaError_t cross_prepare(int mode) {
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 6 && e == cudaSuccess; ++i)
+  for (int i = 0; i < 8 && e == cudaSuccess; ++i)
     e = prepare_split_kernel(cross_kernel(mode, (i & 1) != 0, i >> 1), tr::THREADS, tr::SPLIT_REGS, cross_smem(mode));
   return e;
 }
 
 size_t cross_query_bytes(int B, int Hq, int Hkv, int n_rows, int layout) {
-  return (size_t)Hkv * (cross_query_slot(n_rows, B, Hq / Hkv, layout == kPairs ? 16 : 32) + 1) * 32 * kHeadDim * 2;
+  return (size_t)Hkv * (cross_query_slot(n_rows, B, Hq / Hkv, layout == kPairs ? 16 : 32) + 1) *
+         (layout == kBothParts ? 2 : 1) * 32 * kHeadDim * 2;
 }
 
 cudaError_t launch_cross(int mode, const DecodeParams& p, int layout, int groups_max, void* qx, cudaStream_t stream) {
   uint4* q = static_cast<uint4*>(qx);
   const dim3 grid((unsigned)(((long long)p.n_rows * p.g + 31) / 32), p.Hkv);
-  cudaError_t e = layout == kPairs ? launch_pdl(cross_query_kernel<true>, grid, dim3(128), 0, stream, p, q)
-                                   : launch_pdl(cross_query_kernel<false>, grid, dim3(128), 0, stream, p, q);
+  cudaError_t e = launch_pdl(layout == kPairs       ? cross_query_kernel<true, false>
+                             : layout == kBothParts ? cross_query_kernel<false, true>
+                                                    : cross_query_kernel<false, false>,
+                             grid, dim3(128), 0, stream, p, q);
   if (e == cudaSuccess)
-    e = launch_pdl(cross_kernel(mode, p.block_table != nullptr, layout), dim3(layout == kTwoTiles ? p.n_splits : (p.n_splits + 1) / 2, p.Hkv), dim3(tr::THREADS),
+    e = launch_pdl(cross_kernel(mode, p.block_table != nullptr, layout),
+                   dim3((p.n_splits + cross_shares(layout) - 1) / cross_shares(layout), p.Hkv), dim3(tr::THREADS),
                    (size_t)cross_smem(mode), stream, p, static_cast<const unsigned long long*>(nullptr),
                    static_cast<const uint4*>(qx));
   if (e == cudaSuccess && p.n_splits > 1) {

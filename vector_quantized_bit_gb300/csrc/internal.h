@@ -173,10 +173,17 @@ cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned l
 
 // Cross attention (cross_attn.cu), B <= kFlatMaxB: n_splits shares per KV head;
 // partials [Hkv][2 n_splits] of [32 pieces of 4 channels][cross_cols(layout) columns],
-// then max and sum of each column.  layout: columns of an item,
-// as in the draft-tree attention; groups_max: items of a sequence, at most.
-enum TileLayout : int { kOneTile = 0, kTwoTiles = 1, kPairs = 2 };   // columns on the MMA rows
-int cross_cols(int layout);   // columns of an item, at most
+// then max and sum of each column.  groups_max: items of a sequence, at most.
+// layout: an item's columns on the MMA rows, and whether q' is in one fp16 part
+// (bf16 results: 2^-11 of the scores is below their own rounding) or in two.
+enum TileLayout : int {
+  kOneTile = 0,    // 128 columns
+  kTwoTiles = 1,   // 256
+  kPairs = 2,      // 64, both parts of a column on two rows
+  kBothParts = 3   // 128, both parts as two products
+};
+int cross_cols(int layout);     // columns of an item, at most
+int cross_shares(int layout);   // shares that a CTA works on side by side
 cudaError_t cross_prepare(int mode);
 size_t cross_query_bytes(int B, int Hq, int Hkv, int n_rows, int layout);
 cudaError_t launch_cross(int mode, const DecodeParams& p, int layout, int groups_max, void* qx, cudaStream_t stream);
