@@ -353,11 +353,9 @@ __device__ __forceinline__ void drain_products(const DecodeParams& p, bool issue
 // loaded PREFETCH of its tiles ahead into registers, block ids one further.
 // These warps meet the others only through the ring's barriers, so they run
 // ahead into the next piece while the others finish one.  False: a wait gave up.
-// STREAM 1: every tile of the piece, 2: those of the piece whose number has parity
-// `half`, counted from its first; they go to the stages of that parity, and `done`
-// counts tiles of such stages.
-template <int MODE, int ROLE, bool PAGED, int TOK, int STAGES, int STREAM = 0>
-__device__ __forceinline__ bool dequant_piece(const DecodeParams& p, int b, int kvh, int tile0, int n_piece, int L, uint32_t done,
+// STREAM: every tile of the piece; it goes to one of the stages of parity `half`.
+template <int MODE, int ROLE, bool PAGED, int TOK, int STAGES, bool STREAM = false>
+__device__ __forceinline__ bool dequant_piece(const DecodeParams& p, int b, int kvh, int tile0, int n, int L, uint32_t done,
                                               const unsigned char* s_cb, unsigned char* ring, uint32_t full, uint32_t empty,
                                               int u, int half, int lane, volatile int* abort_flag) {
   using G = CodeGeo<MODE>;
@@ -368,15 +366,12 @@ __device__ __forceinline__ bool dequant_piece(const DecodeParams& p, int b, int 
   bool bad = false;
   constexpr int NEXT = STREAM ? 1 : 2;
   const int mine = STREAM ? 0 : (int)((done + half) & 1);   // its first tile
-  const int n = STREAM == 2 ? (n_piece - half + 1) >> 1 : n_piece;
-  auto tile_of = [&](int t) { return STREAM == 2 ? 2 * t + half : t; };   // of the piece
   // byte offset of the layout tile of this warp's group of tile t, -1 past the sequence
-  const int t_end = min(n_piece, (last_group - u + GROUPS - 1) / GROUPS - tile0);   // tiles whose group u holds tokens
+  const int t_end = min(n, (last_group - u + GROUPS - 1) / GROUPS - tile0);   // tiles whose group u holds tokens
   constexpr int STEP = TOK / G::LAYOUT_TOK * G::TILE_BYTES;
   auto layout_tile = [&](int t) { return (GROUPS * (tile0 + t) + u) / (G::LAYOUT_TOK / 16); };
   const long long first = PAGED ? 0 : tile_offset<false>(p, b, kvh, layout_tile(0), G::TILE_BYTES, &bad);
-  auto place = [&](int t_own) -> long long {
-    const int t = tile_of(t_own);
+  auto place = [&](int t) -> long long {
     if (t >= t_end) return -1;
     if (!PAGED) return first + (long long)t * STEP;
     return tile_offset<PAGED>(p, b, kvh, layout_tile(t), G::TILE_BYTES, &bad);

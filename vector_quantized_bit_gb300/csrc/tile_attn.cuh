@@ -34,8 +34,9 @@ constexpr int REGS_SM = 120, REGS_DQ = 56, REGS_MMA = 40;
 constexpr int SPLIT_REGS = 32 * (SM_WARPS * REGS_SM + DQ_WARPS * REGS_DQ + 4 * REGS_MMA);
 constexpr int TILE_SMEM = TOK * 256;      // one dequantised K or V tile: two 64-channel halves of 64 x 128 bytes
 constexpr int HALF = TOK * 128;
-// tensor memory columns: O, S and P of each softmax warpgroup, then q'
-constexpr uint32_t T_O = 0, T_S = 256, T_COLS = 512;
+// tensor memory columns: O, S and P of each softmax warpgroup, then q' (CROSS with
+// both parts: one O, q's low parts, then the same)
+constexpr uint32_t T_O = 0, T_Q_LOW = 128, T_S = 256, T_COLS = 512;
 template <int NQ>
 struct Tmem {
   __device__ static constexpr uint32_t p(uint32_t wg) { return NQ == 1 ? 384 + TOK / 2 * wg : T_S + TOK * wg; }
@@ -59,18 +60,20 @@ struct Geo {
 
 // One warp of softmax warpgroup wg over a piece's tiles: thread = column.
 // Returns false when a wait gave up.  m, l: the column's running max and sum.
-// ALT: n of the piece's tiles are this warpgroup's, every second one.
-template <int NQ, int STAGES, bool PAIR, bool ALT, typename Work>
-__device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Work& pc, int n, uint32_t done, int wg, uint32_t t_lane,
+// ONE_O: the warpgroups' tiles add to one O, so the running max goes from tile to
+// tile: s_ml[warpgroup][column].x holds that after the warpgroup's last one, m_done
+// (+ 32 wg + 8 warp) completes per tile.  l stays this warpgroup's own.
+template <int NQ, int STAGES, bool PAIR, bool ONE_O, typename Work>
+__device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Work& pc, uint32_t done, int wg, uint32_t t_lane,
                                                  unsigned long long mask, int prefix, uint32_t s_full, uint32_t s_ready,
-                                                 uint32_t p_ready, uint32_t o_done, volatile int* abort_flag, float& m,
-                                                 float& l) {
+                                                 uint32_t p_ready, uint32_t o_done, uint32_t m_done, float2* s_ml,
+                                                 volatile int* abort_flag, float& m, float& l) {
   using namespace tr;
-  const int lane = threadIdx.x & 31;
-  const uint32_t t_s = t_lane + T_S + TOK * wg, t_p = t_lane + Tmem<NQ>::p(wg), t_o = t_lane + T_O + kHeadDim * wg;
-  bool first = true;
+  const int lane = threadIdx.x & 31, row = threadIdx.x & (ROWS - 1), w = row >> 5;
+  const uint32_t t_s = t_lane + T_S + TOK * wg, t_p = t_lane + Tmem<NQ>::p(wg), t_o = t_lane + T_O + (ONE_O ? 0 : kHeadDim * wg);
+  bool first = true;   // of this warpgroup
   // NQ 1: tiles whose number (counted over the CTA's pieces) has this parity; NQ 2: every tile
-  for (int t = NQ == 1 ? (int)((done + wg) & 1) : 0; t < n; t += NQ == 1 ? 2 : 1) {
+  for (int t = NQ == 1 ? (int)((done + wg) & 1) : 0; t < pc.n; t += NQ == 1 ? 2 : 1) {
     const uint32_t use = NQ == 1 ? (uint32_t)(done + t) >> 1 : (uint32_t)(done + t);
     if (!tr_wait(p, s_full + 8 * wg, use & 1, abort_flag)) return false;
     tcgen05_after_sync();
@@ -97,7 +100,7 @@ __device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Wo
       if (lane == 0) mbar_arrive(s_ready + 8 * ((done + t + 2) % STAGES));
     }
     float top = fmaxf(top0, top1);
-    const int d = prefix - (pc.tile0 + (ALT ? 2 * t + wg : t)) * TOK;
+    const int d = prefix - (pc.tile0 + t) * TOK;
     if (d < TOK) {   // bit i of vis: token i of the tile is visible
       const unsigned long long vis = d >= 0 ? (mask << d) | ((1ull << d) - 1) : d > -64 ? mask >> -d : 0ull;
       top = neg_inf();
@@ -111,11 +114,26 @@ __device__ __forceinline__ bool softmax_tiles_of(const DecodeParams& p, const Wo
       if (!tr_wait(p, o_done + 8 * wg, (use - 1) & 1, abort_flag)) return false;
       tcgen05_after_sync();
     }                          // (NQ 2: this tile's score product came after that P.V product)
-    if (__any_sync(0xffffffffu, top > m + kSoftmaxSlack)) {
-      const float mn = fmaxf(m, top), f = fast_exp2(m - mn);
-      m = mn;
-      l *= f;
-      if (!first) {
+    if (ONE_O && t > 0) {   // the max after the tile before this one
+      if (!tr_wait(p, m_done + 32 * (wg ^ 1) + 8 * w, ((done + t - 1) >> 1) & 1, abort_flag)) return false;
+      const float mo = s_ml[(wg ^ 1) * ROWS + row].x;
+      l *= fast_exp2(m - mo);
+      m = mo;
+    }
+    const bool raise = __any_sync(0xffffffffu, top > m + kSoftmaxSlack);
+    const float f = raise ? fast_exp2(m - fmaxf(m, top)) : 1.f;
+    if (raise) m = fmaxf(m, top), l *= f;
+    if constexpr (ONE_O) {
+      s_ml[wg * ROWS + row].x = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(m_done + 32 * wg + 8 * w);
+    }
+    if (raise) {
+      if (ONE_O && t > 0) {   // O has every tile before this one
+        if (!tr_wait(p, o_done + 8 * (wg ^ 1), ((done + t - 1) >> 1) & 1, abort_flag)) return false;
+        tcgen05_after_sync();
+      }
+      if (ONE_O ? t > 0 : !first) {
 #pragma unroll 1
         for (int q = 0; q < kHeadDim / 16; ++q) {
           uint32_t r[16];
@@ -173,35 +191,20 @@ __host__ __device__ __forceinline__ long long cross_query_slot(int row0, int b, 
 // channels at a time, packed, through the warp's own 2 KB of shared memory (16-byte
 // pieces permuted by the row), so that a row's stores are whole sectors; a partial
 // goes out as [32 pieces of 4 channels][cols columns], neighbours as they are in the
-// warp.  32-channel quarters q0 .. q1 - 1; O = f0 times that at t_o, plus f1 times
-// that at t_other where `both`.  (Eight rounds of 16 channels with a row's address
-// computed in each took 5.5 us of a piece.)
+// warp.  Quarters q0 .. q1 - 1 of the channels.  (Eight rounds of 16 channels with a
+// row's address computed in each took 5.5 us of a piece.)
 template <int WCOLS>
-__device__ __forceinline__ void cross_finish(const DecodeParams& p, bool whole, bool both, uint32_t t_o, uint32_t t_other, float f0, float f1,
-                                             float m, float l, int q0, int q1, uint4* box, float4* part, int cols, int cl, int nloc,
-                                             int col0, int row0, int kvh) {
+__device__ __forceinline__ void cross_finish(const DecodeParams& p, bool whole, uint32_t t_o, float m, float l, int q0, int q1,
+                                             uint4* box, float4* part, int cols, int cl, int nloc, int col0, int row0, int kvh) {
   const int lane = threadIdx.x & 31, cl0 = cl & ~(WCOLS - 1);
   const bool mine = cl < nloc && lane < WCOLS;
   if (cl0 >= nloc) return;   // the same for the whole warp
-  auto quarter = [&](int q, float (&v)[32]) {
-    tmem_ld32(t_o + 32 * q, v);
-    if (both) {
-      float z[32];
-      tmem_ld32(t_other + 32 * q, z);
-      tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = v[i] * f0 + z[i] * f1;
-    } else {
-      tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= f0;
-    }
-  };
   if (!whole) {
 #pragma unroll 1
     for (int q = q0; q < q1; ++q) {
       float v[32];
-      quarter(q, v);
+      tmem_ld32(t_o + 32 * q, v);
+      tmem_wait_ld();
       if (mine) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) part[(8 * q + i) * cols + cl] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -211,7 +214,6 @@ __device__ __forceinline__ void cross_finish(const DecodeParams& p, bool whole, 
     return;
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  f0 *= inv, f1 *= inv;
   const int x = lane & 3;   // 16-byte piece of the rows 8 i + lane / 4
   const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;   // out needs only 2-byte alignment
   __half* dst[WCOLS / 8];
@@ -223,15 +225,16 @@ __device__ __forceinline__ void cross_finish(const DecodeParams& p, bool whole, 
 #pragma unroll 1
   for (int q = q0; q < q1; ++q) {
     float v[32];
-    quarter(q, v);
+    tmem_ld32(t_o + 32 * q, v);
+    tmem_wait_ld();
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       if (p.bf16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i] * inv, v[2 * i + 1] * inv);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       } else {
-        w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+        w[i] = pack_half2(v[2 * i] * inv, v[2 * i + 1] * inv);
       }
     }
 #pragma unroll
@@ -271,12 +274,12 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   // one's passage to its next item (q', first tile, O) hides behind the other's
   // products.  Tensor memory is dealt out as for two query tiles (P overlays S).
   constexpr bool STREAMS = CROSS == kCross && NQ == 1;
-  // Both fp16 parts of q' fill the tensor memory of two query tiles.  The warpgroups
-  // take the tiles of one item in turn as they do without CROSS, but with P over S,
-  // and as in STREAMS each has half of the ring's stages and an issuing warp.
-  constexpr bool ALT = CROSS == kCrossParts;
-  static_assert(!ALT || (NQ == 1 && !PAIR), "one query tile, both parts of q'");
-  constexpr int TQ = STREAMS || ALT ? 2 : NQ;
+  // Both fp16 parts of q': the low ones take the place of the second O, and the two
+  // warpgroups' tiles add to one O.  (With two of them and P over S, so that a
+  // warpgroup's next scores wait for its P V, a tile took 1,520 cycles, not 1,330.)
+  constexpr bool ONE_O = CROSS == kCrossParts;
+  static_assert(!ONE_O || (NQ == 1 && !PAIR), "one query tile, both parts of q'");
+  constexpr int TQ = STREAMS ? 2 : NQ;
   using TM = Tmem<TQ>;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_tmem;
@@ -296,13 +299,15 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   // scores read, pv_ready = V tile and P in place (a tile's warpgroup follows
   // from its stage; one barrier each keeps the issuing warp at two waits per
   // tile).  NQ 2: s_ready = K tile, pv_ready = V tile.  Per softmax warpgroup:
-  // s_full, o_done, and for NQ 2 p_ready.  (STREAMS, ALT: as NQ 2, stage 2 i + h is
-  // warpgroup h's i-th.)
+  // s_full, o_done, and for NQ 2 p_ready.  (STREAMS: as NQ 2, stage 2 i + h is stream
+  // h's i-th.)  ONE_O: m_done, per softmax warp.
   constexpr uint32_t ST = G::STAGES;
   const uint32_t s_ready = bar, k_empty = bar + 32, pv_ready = bar + 64, v_empty = bar + 96;
   const uint32_t s_full = bar + 128, o_done = bar + 144, p_ready = bar + 160, all_done = bar + 176;
+  const uint32_t m_done = bar + 192;
   volatile int* abort_flag = &s_abort;
   int* s_pref = reinterpret_cast<int*>(smem + G::PREF_OFF);
+  float2* s_ml = reinterpret_cast<float2*>(smem + G::ML_OFF);
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < ST; ++i) {
       mbar_init(s_ready + 8 * i, (TQ == 1 ? 4 + active0 : 4) + ((int)i == p.withhold_stage));
@@ -317,6 +322,8 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     }
     mbar_init(all_done, 1);
     mbar_init(all_done + 8, 1);
+    if (ONE_O)
+      for (int i = 0; i < SM_WARPS; ++i) mbar_init(m_done + 8 * i, 1);
     s_abort = 0;
     mbar_init_fence();
   }
@@ -369,8 +376,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     if (TQ == 1 && live && lane == 0) mbar_arrive(s_ready + 8 * wg);   // no scores to read yet
     bool ok = live;   // no wait has given up
-    for (int rounds = 0; pc.next();) {   // rounds: pieces with tiles of this warpgroup
-      const int n = ALT ? (pc.n - wg + 1) >> 1 : pc.n;
+    for (int piece = 0; pc.next(); ++piece) {
       int col0 = grp0, nloc = width, row0 = 0;   // the piece's first column, its columns; CROSS: its sequence's first row
       size_t qrow;                               // of this warp's columns in qx
       if constexpr (CROSS) {
@@ -384,9 +390,9 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         qrow = ((size_t)pc.b * p.Hkv + kvh) * ((p.ncols + WCOLS - 1) / WCOLS) + (col0 + cl) / WCOLS;
       }
       const int c = col0 + cl;
-      // q' into tensor memory: lane = column (ALT: warpgroup 0 the high parts, 1 the low ones)
-      if (live && (cl & ~(WCOLS - 1)) < nloc && (TQ == 2 || wg == 0)) {
-        const uint4* q = qx + (ALT ? 2 * qrow + wg : qrow) * 16 * 32 + lane;
+      // q' into tensor memory: lane = column (ONE_O: warpgroup 0 the high parts, 1 the low ones)
+      if (live && (cl & ~(WCOLS - 1)) < nloc && (TQ == 2 || wg == 0 || ONE_O)) {
+        const uint4* q = qx + (ONE_O ? 2 * qrow + wg : qrow) * 16 * 32 + lane;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t r[32];
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
             const uint4 x = __ldcg(q + 32 * (8 * h + i));
             r[4 * i] = x.x, r[4 * i + 1] = x.y, r[4 * i + 2] = x.z, r[4 * i + 3] = x.w;
           }
-          tmem_st32(t_lane + TM::q(wg) + 32 * h, r);
+          tmem_st32(t_lane + (ONE_O && wg ? T_Q_LOW : TM::q(wg)) + 32 * h, r);
         }
         tmem_wait_st();
       }
@@ -411,25 +417,23 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           mask = tree_mask != nullptr ? tree_mask[(size_t)pc.b * p.M + q] : (2ull << q) - 1;
           if (p.M < 64) mask &= (1ull << p.M) - 1;
         }
-        ok = softmax_tiles_of<TQ, G::STAGES, PAIR, ALT>(p, pc, n, done, wg, t_lane, mask, prefix, s_full, s_ready, TQ == 1 ? pv_ready : p_ready,
-                                  o_done, abort_flag, m, l);
+        ok = softmax_tiles_of<TQ, G::STAGES, PAIR, ONE_O>(p, pc, done, wg, t_lane, mask, prefix, s_full, s_ready,
+                                                          TQ == 1 ? pv_ready : p_ready, o_done, m_done, s_ml, abort_flag, m, l);
         if (TQ == 1) {   // this warpgroup's last tile of the piece, if it has one
           const int last = pc.n - 1 - (int)((done + pc.n - 1 + wg) & 1);
           if (ok && last >= 0) ok = tr_wait(p, o_done + 8 * wg, ((done + last) >> 1) & 1, abort_flag);
-        } else if (ok && n > 0) {
-          ok = tr_wait(p, o_done + 8 * wg, rounds & 1, abort_flag);
+        } else if (ok) {
+          ok = tr_wait(p, o_done + 8 * wg, piece & 1, abort_flag);
         }
         tcgen05_after_sync();
       }
       // NQ 1: the two warpgroups' states are merged.  Both O's rows are in the
       // same tensor-memory lanes, so each warp reads both and takes half of the
       // channels; the maxima and sums pass through shared memory.
-      rounds += n > 0;
-      const bool both = (TQ == 1 || ALT) && pc.n > 1;                        // both warpgroups had tiles
-      const uint32_t own = TQ == 1 ? done & 1 : ALT ? 0u : (uint32_t)wg;       // the O of the piece's first tile
+      const bool both = TQ == 1 && !ONE_O && pc.n > 1;             // both warpgroups had tiles, and an O each
+      const uint32_t own = TQ == 1 ? done & 1 : (uint32_t)wg;      // the O of the piece's first tile
       float fa = 1.f, fb = 0.f;
-      if constexpr (TQ == 1 || ALT) {
-        float2* s_ml = reinterpret_cast<float2*>(smem + G::ML_OFF);
+      if constexpr (TQ == 1) {
         s_ml[wg * ROWS + row] = make_float2(m, l);
         tcgen05_before_sync();
         named_barrier_sync(1, SM_WARPS * 32);   // both warpgroups' last products are done, too
@@ -438,12 +442,13 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         m = fmaxf(a.x, z.x);
         fa = fast_exp2(a.x - m), fb = fast_exp2(z.x - m);
         l = a.y * fa + z.y * fb;
+        if (ONE_O) fa = 1.f;   // O is relative to the last tile's max, the larger one
       }
       if constexpr (CROSS) {
         // a share has a piece that began before it, and one that ends behind it, at most
         if (ok && !*abort_flag)
-          cross_finish<WCOLS>(p, pc.n == pc.all, both, t_lane + T_O + kHeadDim * own, t_lane + T_O + kHeadDim * (own ^ 1), fa, fb, m, l,
-                              ALT ? 2 * wg : 0, ALT ? 2 * wg + 2 : 4, reinterpret_cast<uint4*>(smem + G::BOX_OFF) + warp * 128,
+          cross_finish<WCOLS>(p, pc.n == pc.all, t_lane + T_O + (STREAMS || NQ == 2 ? kHeadDim * wg : 0), m, l,
+                              ONE_O ? 2 * wg : 0, ONE_O ? 2 * wg + 2 : 4, reinterpret_cast<uint4*>(smem + G::BOX_OFF) + warp * 128,
                               reinterpret_cast<float4*>(p.partials) +
                                   (((size_t)kvh * p.n_splits + share) * 2 + (pc.tile0 == 0)) * (COLS * kPartialStride / 4),
                               COLS, cl, nloc, col0, row0, kvh);
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
             p.stats[((size_t)pc.b * p.Hkv + kvh) * p.ncols + c] = make_float2(m, l > 0.f ? 1.f / l : 0.f);
         }
       }
-      done += TQ == 1 ? pc.n : n;
+      done += pc.n;
     }
     if constexpr (CROSS) {   // the item that this share begins and does not end, for the merge
       if (kvh == 0 && (threadIdx.x & (ROWS - 1)) == 0 && (STREAMS || wg == 0) && share < p.n_splits)
@@ -518,12 +523,12 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     for (bool ok = true; ok && pc.next();) {
       const int L = clamped_len(p, pc.b);
       if (dw < 8)
-        ok = dequant_piece<MODE, VQKV_ROLE_K, PAGED, TOK, G::STAGES, STREAMS ? 1 : ALT ? 2 : 0>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::K_OFF,
+        ok = dequant_piece<MODE, VQKV_ROLE_K, PAGED, TOK, G::STAGES, STREAMS>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::K_OFF,
                                                                      s_ready, k_empty, u, half, lane, abort_flag);
       else
-        ok = dequant_piece<MODE, VQKV_ROLE_V, PAGED, TOK, G::STAGES, STREAMS ? 1 : ALT ? 2 : 0>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::V_OFF,
+        ok = dequant_piece<MODE, VQKV_ROLE_V, PAGED, TOK, G::STAGES, STREAMS>(p, pc.b, kvh, pc.tile0, pc.n, L, done, smem, smem + G::V_OFF,
                                                                      pv_ready, v_empty, u, half, lane, abort_flag);
-      done += ALT ? (pc.n - half + 1) >> 1 : pc.n;
+      done += pc.n;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
@@ -549,23 +554,23 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         umma_f16_ts(ds, aq + 8 * k, lo + ((k >> 2) * HALF + (k & 3) * 32) / 16, k_hi, idesc_s, k > 0);
-      if constexpr (ALT) {   // the low parts of q'
+      if constexpr (ONE_O) {   // the low parts of q'
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          umma_f16_ts(ds, tm + TM::q(1) + 8 * k, lo + ((k >> 2) * HALF + (k & 3) * 32) / 16, k_hi, idesc_s, true);
+          umma_f16_ts(ds, tm + T_Q_LOW + 8 * k, lo + ((k >> 2) * HALF + (k & 3) * 32) / 16, k_hi, idesc_s, true);
       }
       umma_commit(s_full + 8 * wg);
     };
     // O of warpgroup wg += P V: 16 tokens a step, two 8-token groups
     auto values = [&](uint32_t st, uint32_t wg, bool fresh) {
-      const uint32_t lo = v_lo + st * (TILE_SMEM / 16), dv = tm + T_O + kHeadDim * wg, ap = tm + TM::p(wg);
+      const uint32_t lo = v_lo + st * (TILE_SMEM / 16), dv = tm + T_O + (ONE_O ? 0 : kHeadDim * wg), ap = tm + TM::p(wg);
 #pragma unroll
       for (int k = 0; k < 4; ++k) umma_f16_ts(dv, ap + 8 * k, lo + k * (2048 / 16), v_hi, idesc_o, !fresh || k > 0);
     };
     bool ok = true;
     while (warp < MMA_WARP + 2 && pc.next()) {
       const int job = warp - MMA_WARP;
-      const int n = ALT ? (pc.n - job + 1) >> 1 : pc.n;
+      const int n = pc.n;
       tcgen05_before_sync();
       named_barrier_sync(STREAMS ? 2 + job : 2, MEET);
       tcgen05_after_sync();
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           if (!(ok = tr_wait(p, pv_ready + 8 * st, (k / ST) & 1, abort_flag))) break;
           tcgen05_after_sync();
           if (issuer) {
-            values(st, k & 1, t < 2);
+            values(st, k & 1, ONE_O ? t == 0 : t < 2);
             umma_commit(v_empty + 8 * st);
             umma_commit(o_done + 8 * (k & 1));
           }
@@ -594,8 +599,8 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         }
       } else if (TQ == 2 && job < jobs) {
         // stage and use of it of tile j
-        auto stage = [&](uint32_t j) { return STREAMS || ALT ? 2 * (j % (ST / 2)) + job : j % ST; };
-        auto round = [&](uint32_t j) { return STREAMS || ALT ? j / (ST / 2) : j / ST; };
+        auto stage = [&](uint32_t j) { return STREAMS ? 2 * (j % (ST / 2)) + job : j % ST; };
+        auto round = [&](uint32_t j) { return STREAMS ? j / (ST / 2) : j / ST; };
         for (int t = 0; ok && t <= n; ++t) {   // P.V of tile t - 1, then S of tile t
           const uint32_t k = done + t;
           if (t > 0) {
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
             if (!(ok = tr_wait(p, s_ready + 8 * st, round(k) & 1, abort_flag))) break;
             tcgen05_after_sync();
             if (issuer) {
-              scores(st, job, ALT ? 0 : job);
+              scores(st, job, job);
               umma_commit(k_empty + 8 * st);
             }
             __syncwarp();
