@@ -289,11 +289,6 @@ __device__ __forceinline__ void put_v(unsigned char* tile, int u, int lane, cons
       put_tile<TOK>(tile, r0 + (k & 1) + 8 * (k >> 1), (int)sizeof(T) * (8 * i + gid), c.get<T>(4 * i + k));
 }
 
-// Barrier of `threads` threads that leaves the others of the CTA alone.
-__device__ __forceinline__ void named_barrier_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // Two fp32 additions in one instruction.
 __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
   float2 r;

@@ -713,22 +713,76 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   grid_dependents_launch();
   __syncthreads();
 
+  const int rows = src.count();
+  const int tiles = (rows + ROWS - 1) / ROWS;
+  const int cta = src.cta(), ctas = src.ctas();
+  const int n_my = cta < tiles ? (tiles - cta + ctas - 1) / ctas : 0;
+  // A CTA's only tile: the warpgroups screen half of the centroids each.  (A decode
+  // step of 64 rows, 8 heads and both roles at 1.5 bit took 18.5 us without this and
+  // the early loads below, now 13.9.)
+  const bool halves = CHUNKS >= 8 && n_my == 1;
+
+  const bool producer = warp >= 8 && warp < MMA_WARP;
+  const int pw = warp - 8;
+  // Row job i is row i % ROWS of tile i / ROWS; warp pw takes jobs pw, pw +
+  // PRODUCERS, ...  A job's row is loaded one job ahead, its angle two.
+  constexpr int PRODUCERS = Geo::PRODUCERS;
+  const int jobs = producer && pw < PRODUCERS ? n_my * ROWS : 0;
+  typename Rows<APPEND>::Raw raw{};
+  RowPlace at{};
+  Turn turn{};
+  int angle = 0;
+  auto row_of = [&](int job) {   // -1: none
+    const int row = (cta + job / ROWS * ctas) * ROWS + job % ROWS;
+    return job < jobs && row < rows ? row : -1;
+  };
+  auto next_angle = [&](int job) {
+    if constexpr (APPEND) {
+      const int row = row_of(job);
+      if (row >= 0) angle = src.angle(row);
+    }
+  };
+  auto fetch = [&](int job) {
+    const int row = row_of(job);
+    at = {0, -1, 0};
+    if (row >= 0) {
+      at = src.place(row, angle, lane == 0);
+      if (at.t >= 0) raw = src.load(row, lane);
+    }
+    if constexpr (APPEND) turn = src.turn(at.angle, lane);
+    next_angle(job + PRODUCERS);
+  };
+
+  // The producers' first row (three or four dependent loads) comes in while the other
+  // warps build the table.
+  if (producer) {
+    next_angle(pw);
+    fetch(pw);
+  }
+
   // B table: row c = [-2c (8 fp16), |c|^2 hi, |c|^2 lo, 0 x 6] (1.5 bit) or
   // [-2c (4 fp16), |c|^2 hi, |c|^2 lo, 0, 0, -2c, 0 x 4] (2 bit) or
   // [-2c (2 fp16), |c|^2 hi, |c|^2 lo, -2c, 0 x 10] (4 bit)
-  {
+  else {
+    constexpr int BUILDERS = THREADS - 32 * PROD_WARPS, PER = (E + BUILDERS - 1) / BUILDERS;
+    const int first = warp < 8 ? threadIdx.x : threadIdx.x - 32 * PROD_WARPS;
+    using Word = std::conditional_t<DSUB == 8, uint4, std::conditional_t<DSUB == 4, uint2, uint32_t>>;
+    Word raw[PER];   // all in flight
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (first + i * BUILDERS < E) raw[i] = __ldg(reinterpret_cast<const Word*>(p.cb) + (size_t)kvh * E + first + i * BUILDERS);
     float cmax = 0.f;
-    for (int c = threadIdx.x; c < E; c += THREADS) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = first + i * BUILDERS;
+      if (c >= E) break;
       uint32_t w[DSUB / 2];
-      if constexpr (DSUB == 8) {
-        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p.cb) + (size_t)kvh * E + c);
-        w[0] = raw.x, w[1] = raw.y, w[2] = raw.z, w[3] = raw.w;
-      } else if constexpr (DSUB == 4) {
-        const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.cb) + (size_t)kvh * E + c);
-        w[0] = raw.x, w[1] = raw.y;
-      } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p.cb) + (size_t)kvh * E + c);
-      }
+      if constexpr (DSUB == 8)
+        w[0] = raw[i].x, w[1] = raw[i].y, w[2] = raw[i].z, w[3] = raw[i].w;
+      else if constexpr (DSUB == 4)
+        w[0] = raw[i].x, w[1] = raw[i].y;
+      else
+        w[0] = raw[i];
       uint32_t m2[DSUB / 2];
       float nn = 0.f;
 #pragma unroll
@@ -768,14 +822,8 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   const uint32_t tmem = *s_tmem;
   const float Cmax = *s_cmax;
 
-  const int rows = src.count();
-  const int tiles = (rows + ROWS - 1) / ROWS;
-  const int cta = src.cta(), ctas = src.ctas();
-  const int n_my = cta < tiles ? (tiles - cta + ctas - 1) / ctas : 0;
-
-  if (warp >= 8 && warp < MMA_WARP) {
+  if (producer) {
     // ---------------- producers
-    const int pw = warp - 8;
     // 1.5 bit: lanes 2j, 2j + 1 hold subvector j; 2 bit: lane j holds subvector j;
     // 4 bit: lane l holds subvectors j = 2l and j + 1
     const int j = DSUB == 8 ? lane >> 1 : DSUB == 4 ? lane : 2 * lane, half = DSUB == 8 ? lane & 1 : 0;
@@ -785,36 +833,6 @@ __global__ void __launch_bounds__(um::THREADS, 1)
     constexpr float kNorm = 0.08838834764831845f;   // 1 / sqrt(128)
     const float4 scale = make_float4(__frcp_rn(s4.x) * kNorm, __frcp_rn(s4.y) * kNorm, __frcp_rn(s4.z) * kNorm,
                                      __frcp_rn(s4.w) * kNorm);
-    // Row job i is row i % ROWS of tile i / ROWS; warp pw takes jobs pw, pw +
-    // PRODUCERS, ...  A job's row is loaded one job ahead, its angle two.
-    constexpr int PRODUCERS = Geo::PRODUCERS;
-    const int jobs = pw < PRODUCERS ? n_my * ROWS : 0;
-    typename Rows<APPEND>::Raw raw{};
-    RowPlace at{};
-    Turn turn{};
-    int angle = 0;
-    auto row_of = [&](int job) {   // -1: none
-      const int row = (cta + job / ROWS * ctas) * ROWS + job % ROWS;
-      return job < jobs && row < rows ? row : -1;
-    };
-    auto next_angle = [&](int job) {
-      if constexpr (APPEND) {
-        const int row = row_of(job);
-        if (row >= 0) angle = src.angle(row);
-      }
-    };
-    auto fetch = [&](int job) {
-      const int row = row_of(job);
-      at = {0, -1, 0};
-      if (row >= 0) {
-        at = src.place(row, angle, lane == 0);
-        if (at.t >= 0) raw = src.load(row, lane);
-      }
-      if constexpr (APPEND) turn = src.turn(at.angle, lane);
-      next_angle(job + PRODUCERS);
-    };
-    next_angle(pw);
-    fetch(pw);
     for (int job = pw; job < jobs; job += PRODUCERS) {
       const typename Rows<APPEND>::Raw cur = raw;
       const RowPlace w = at;
@@ -892,23 +910,24 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   } else if (warp >= MMA_WARP) {
     // ---------------- one thread per epilogue warpgroup issues its MMAs
     const int wg = warp - MMA_WARP;
+    const int q0 = halves ? wg * (CHUNKS / 2) : 0, n_q = halves ? CHUNKS / 2 : CHUNKS;   // its chunks
     if (lane == 0) {
       constexpr uint32_t idesc = umma_idesc_f16_f32(M, N);
       bool ok = true;
       int it = 0;
-      for (int k = wg; ok && k < n_my; k += 2, ++it) {
+      for (int k = halves ? 0 : wg; ok && k < n_my; k += 2, ++it) {
         const int s = k % STAGES;
         ok = um_wait(a_full(s), (k / STAGES) & 1, s_abort, p.err, 1u);
         const uint64_t dA = umma_desc_kmajor(sbase + OFF_STAGES + s * STAGE_BYTES + ST_A);
         const uint64_t dLow = umma_desc_kmajor(sbase + OFF_STAGES + s * STAGE_BYTES + Geo::ST_LOW);
         tcgen05_after_sync();
-        for (int q = 0; ok && q < CHUNKS; ++q) {
+        for (int q = 0; ok && q < n_q; ++q) {
           const int bsel = q % NBUF;
           const uint32_t use = (uint32_t)(it * (CHUNKS / NBUF) + q / NBUF);
           ok = um_wait(t_empty(wg, bsel), (use & 1) ^ 1, s_abort, p.err, 1u);
           if (!ok) break;
           tcgen05_after_sync();
-          const uint64_t dB = umma_desc_kmajor(sbase + (uint32_t)q * (N * 32));
+          const uint64_t dB = umma_desc_kmajor(sbase + (uint32_t)(q0 + q) * (N * 32));
           const uint32_t acc = tmem + (uint32_t)((NBUF * wg + bsel) * N);
           umma_f16(acc, dA, dB, idesc, 0u);
           if constexpr (DSUB == 8) umma_f16(acc, dLow, dB, idesc, 1u);
@@ -950,52 +969,68 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         return __fmaf_rn(e, e, d);
       }
     };
-    int it = 0;
-    for (int k = wg; k < n_my; k += 2, ++it) {
+    for (int k = halves ? 0 : wg; k < n_my; k += 2) {
       const float inf = __int_as_float(0x7f800000);
       float B1 = inf, B2 = inf, B3 = inf, B4 = inf;
       // the group minimum (from the tensor-memory load's own reduction) with
       // the group id in its 7 low mantissa bits, then the four smallest so
       // far: the packing moves a value by less than 2^-16 of itself, which
       // the margin below covers
-      auto group = [&](float g, uint32_t gid) {
-        const float gp = __uint_as_float((__float_as_uint(g) & ~0x7Fu) | gid);
+      auto keep = [&](float gp) {
         B4 = fminf(B4, fmaxf(B3, gp));
         B3 = fminf(B3, fmaxf(B2, gp));
         B2 = fminf(B2, fmaxf(B1, gp));
         B1 = fminf(B1, gp);
       };
+      auto group = [&](float g, uint32_t gid) { keep(__uint_as_float((__float_as_uint(g) & ~0x7Fu) | gid)); };
       bool ok = true;
+      auto scan = [&](auto chunks) {   // a number of chunks, from the warpgroup's first (a constant: no register)
 #pragma unroll 1
-      for (int q = 0; q < CHUNKS; ++q) {
-        const int bsel = q % NBUF;
-        const uint32_t use = (uint32_t)(it * (CHUNKS / NBUF) + q / NBUF);
-        ok = um_wait(t_full(wg, bsel), use & 1, s_abort, p.err, 0xffffffffu);
-        if (!ok) break;
-        tcgen05_after_sync();
-        const uint32_t col = t_lane + (uint32_t)((NBUF * wg + bsel) * N);
-        // the whole chunk in flight at once (one wait); the buffer is handed
-        // back before the values are reduced
-        constexpr int GROUPS = N / GROUP;
-        float g[GROUPS];
+        for (int q = 0; q < decltype(chunks)::value; ++q) {
+          const int bsel = q % NBUF;
+          const uint32_t use = (uint32_t)((k >> 1) * (CHUNKS / NBUF) + q / NBUF);
+          ok = um_wait(t_full(wg, bsel), use & 1, s_abort, p.err, 0xffffffffu);
+          if (!ok) break;
+          tcgen05_after_sync();
+          const uint32_t col = t_lane + (uint32_t)((NBUF * wg + bsel) * N);
+          // the whole chunk in flight at once (one wait); the buffer is handed
+          // back before the values are reduced
+          constexpr int GROUPS = N / GROUP;
+          float g[GROUPS];
 #pragma unroll
-        for (int i = 0; i < GROUPS; ++i) g[i] = inf;
-        if constexpr (GROUP == 32) {
-          float v[GROUPS][32];
+          for (int i = 0; i < GROUPS; ++i) g[i] = inf;
+          if constexpr (GROUP == 32) {
+            float v[GROUPS][32];
 #pragma unroll
-          for (int i = 0; i < GROUPS; ++i) tmem_ld32_min(col + 32 * i, v[i], g[i]);
-          tmem_wait_ld();
-        } else {
-          float v[GROUPS][16];
+            for (int i = 0; i < GROUPS; ++i) tmem_ld32_min(col + 32 * i, v[i], g[i]);
+            tmem_wait_ld();
+          } else {
+            float v[GROUPS][16];
 #pragma unroll
-          for (int i = 0; i < GROUPS; ++i) tmem_ld16_min(col + 16 * i, v[i], g[i]);
-          tmem_wait_ld();
+            for (int i = 0; i < GROUPS; ++i) tmem_ld16_min(col + 16 * i, v[i], g[i]);
+            tmem_wait_ld();
+          }
+          tcgen05_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(t_empty(wg, bsel));
+#pragma unroll
+          for (int i = 0; i < GROUPS; ++i) group(g[i], (uint32_t)(GROUPS * q + i));
         }
-        tcgen05_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(t_empty(wg, bsel));
-#pragma unroll
-        for (int i = 0; i < GROUPS; ++i) group(g[i], (uint32_t)(GROUPS * q + i));
+      };
+      if (halves)
+        scan(std::integral_constant<int, CHUNKS / 2>());
+      else
+        scan(std::integral_constant<int, CHUNKS>());
+      if (halves) {   // the second half's four smallest pass through the place of a second tile
+        float4* other = reinterpret_cast<float4*>(smem + OFF_STAGES + STAGE_BYTES);
+        constexpr uint32_t half = E / GROUP / 2;   // the first of its groups: a power of two
+        auto id = [&](float b) { return __uint_as_float(__float_as_uint(b) | half); };
+        if (wg == 1) other[ml] = make_float4(id(B1), id(B2), id(B3), id(B4));
+        named_barrier_sync(1, 256);   // reached whether or not a wait gave up
+        if (wg == 1) break;
+        const float4 o = other[ml];
+        keep(o.x), keep(o.y), keep(o.z), keep(o.w);
+        ok = ok && !*s_abort;
       }
       if (!ok) break;
       const int s = k % STAGES;

@@ -187,6 +187,11 @@ __device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, float (&v)[32], fl
       : "memory");
 }
 
+// Barrier of `threads` threads that leaves the others of the CTA alone.
+__device__ __forceinline__ void named_barrier_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // min(a, b, c) in one instruction.
 __device__ __forceinline__ float fmin3(float a, float b, float c) {
   float d;
