@@ -25,13 +25,20 @@ constexpr int SM_WARPS = 8, DQ_WARPS = 16; // two softmax warpgroups, four dequa
 constexpr int MMA_WARP = SM_WARPS + DQ_WARPS;
 constexpr int THREADS = (MMA_WARP + 4) * 32;   // whole warpgroups, for the register split
 // Registers per thread: 72 at launch (896 threads), then 120 for the softmax
-// warpgroups (64 scores and 16 packed weights are live), 56 for the
-// dequantising ones (32 hold gathered centroids), 40 for the last:
-// 256 x 120 + 512 x 56 + 128 x 40 = 64,512 = 896 x 72.  Two sets of code words
-// beside the centroids do not fit in 56: 44 to 136 bytes per thread spill, 216 to
-// 384 at 4 bit.
-constexpr int REGS_SM = 120, REGS_DQ = 56, REGS_MMA = 40;
-constexpr int SPLIT_REGS = 32 * (SM_WARPS * REGS_SM + DQ_WARPS * REGS_DQ + 4 * REGS_MMA);
+// warpgroups (64 scores and 16 packed weights are live), 56 for the dequantising
+// ones (32 hold gathered centroids), 40 for the last.  Two sets of code words beside
+// the centroids do not fit in 56: 44 to 136 bytes per thread spill.  At 4 bit, with
+// twice the words, it would be 216 to 480: there 112, 64 and 24 (120 to 190 spill;
+// ragged prompts over paged states 100 -> 93 us, 64 drafts over 32,768 tokens 51.3 ->
+// 50.7; at 1.5 bit, where the softmax warps wait for conflicting gathers, a tree of 135
+// columns would go from 192 to 212).  Either way 256, 512 and 128 threads hold 64,512 =
+// 896 x 72.
+template <int MODE>
+struct Regs {
+  static constexpr int SM = MODE == VQKV_MODE_VQ4 ? 112 : 120, DQ = MODE == VQKV_MODE_VQ4 ? 64 : 56, MMA = MODE == VQKV_MODE_VQ4 ? 24 : 40;
+  static_assert(32 * (SM_WARPS * SM + DQ_WARPS * DQ + 4 * MMA) == THREADS * 72, "the launch's registers");
+};
+constexpr int SPLIT_REGS = THREADS * 72;
 constexpr int TILE_SMEM = TOK * 256;      // one dequantised K or V tile: two 64-channel halves of 64 x 128 bytes
 constexpr int HALF = TOK * 128;
 // tensor memory columns: O, S and P of each softmax warpgroup, then q' (CROSS with
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
   // sequences of up to 512 tokens took 54 us, not 49.)
   constexpr int MEET = STREAMS ? (SM_WARPS / 2 + 1) * 32 : (SM_WARPS + 2) * 32;
   if (warp < SM_WARPS) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SM));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<MODE>::SM));
     // ---------------- softmax warpgroup wg: thread = column c
     const int wg = warp >> 2, row = threadIdx.x & (ROWS - 1);
     const int cl = PAIR ? 16 * (warp & 3) + (lane & 15) : NQ == 1 ? row : wg * ROWS + row;
@@ -518,7 +525,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
     }
   } else if (warp < MMA_WARP) {
     // ---------------- dequantisation
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DQ));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<MODE>::DQ));
     const int dw = warp - SM_WARPS, u = dw & 3, half = (dw >> 2) & 1;
     for (bool ok = true; ok && pc.next();) {
       const int L = clamped_len(p, pc.b);
@@ -531,7 +538,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
       done += pc.n;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<MODE>::MMA));
     // ---------------- the products.  An issuing warp waits and computes the
     // operands' addresses as one, so they stay in uniform registers, and an
     // elected lane issues.  Issue blocks while the tensor cores are busy, so
