@@ -632,13 +632,13 @@ vqkv_status vqkv_append(const vqkv_append_args* args, const vqkv_paging* paging,
  * decode.q is fp16 or bf16 (dtype) [n_rows][Hq][128] with rows q_row_stride
  * elements apart, decode.out the same type, contiguous; out may be q's buffer
  * where q is contiguous, too.  Sums and softmax statistics are fp32; the softmax
- * weights are rounded to fp16 for the tensor cores, q' to two fp16 parts in calls
- * of one query per sequence (max_queries = 1) and in fp16 calls of up to 64 columns
- * max_queries * (Hq / Hkv), else to one.
+ * weights are rounded to fp16 for the tensor cores, q' to two fp16 parts (bf16 calls
+ * with max_queries > 1: to one).
  * num_splits: shares of the batch's work per KV head, 0 = automatic, at most
- * 1024 are used (max_queries = 1: as in vqkv_decode_attn).  paging as in vqkv_decode_attn_tree.  The workspace holds
- * vqkv_cross_attn_workspace_bytes(args) bytes and may be shared like that of
- * vqkv_decode_attn_tree.  Everything else is as in vqkv_decode_attn.
+ * 1024 are used (max_queries = 1: as in vqkv_decode_attn).  paging as in
+ * vqkv_decode_attn_tree.  The workspace holds vqkv_cross_attn_workspace_bytes(args)
+ * bytes and may be shared like that of vqkv_decode_attn_tree.  Everything else is as
+ * in vqkv_decode_attn.
  */
 typedef struct {
   vqkv_decode_args decode;    /* q, out: [n_rows][Hq][128] */

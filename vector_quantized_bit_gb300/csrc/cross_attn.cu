@@ -7,6 +7,18 @@
 // STREAMS in tile_attn.cuh).  A share has a piece of an item that began before it and
 // one that ends behind it at most, so two partials per share hold whatever the
 // cut leaves for cross_combine_kernel.
+//
+// fp16 results take their scores from both fp16 parts of q' (above 64 columns: ONE_O
+// in tile_attn.cuh); bf16 ones, which are rounded to 2^-9 anyway, from the high parts
+// (2^-12), up to 256 columns per dequantised tile.  An error of 3.7e-4 of the output
+// became 2.7e-4 with the low parts (2.1e-4 is the output's own rounding), at 1.24
+// times the time.
+//
+// Bound: the chain of a tile (scores, softmax, P V) against dequantisation that only
+// 128 or 256 columns share, as in the draft trees.  2,048 queries of 32 heads over
+// 32,768 tokens at 2 bit: 1.19 ms (fp16; 0.92 PFLOP/s of the two products, 1.38 with
+// the low parts), 0.96 ms (bf16); 12 ragged prompts of 33 to 448 tokens over paged
+// 4-bit states of 600 to 1,500: 91 us, 7 to 10 of them q' and about 8 the merge.
 #include <algorithm>
 
 #include "common.cuh"
@@ -41,6 +53,7 @@ template <bool PAIR, bool LOW>
 __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant__ DecodeParams p, uint4* qx) {
   constexpr int W = PAIR ? 16 : 32;
   __shared__ int s_start[kFlatMaxB + 1];
+  __shared__ float4 s_s[4][9];   // s, 32 channels a row, rows in different banks
   grid_dependency_wait();
   grid_dependents_launch();
   const int kvh = blockIdx.y, part = threadIdx.x & 3;
@@ -51,16 +64,17 @@ __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant_
   uint2 x[8];   // in flight while the row's sequence is looked up
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = q[i];
+  if (threadIdx.x < kHeadDim / 4)
+    s_s[threadIdx.x >> 3][threadIdx.x & 7] = __ldg(reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim) + threadIdx.x);
   for (int i = threadIdx.x; i <= p.B; i += 128) s_start[i] = __ldg(p.row_start + i);
   __syncthreads();
   const int lo = sequence_of(s_start, p.B, row);   // the last sequence that starts at or before the row
   const RowRange rows = rows_between(p, s_start[lo], s_start[lo + 1]);
   const bool in = any && row >= rows.first && row - rows.first < rows.n;   // both in [0, n_rows]
   float v[32];
-  const float4* s4 = reinterpret_cast<const float4*>(p.s + (size_t)kvh * kHeadDim + 32 * part);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float4 f = __ldg(s4 + i);
+    const float4 f = s_s[part][i];
     float2 a, b;
     if (p.bf16) {   // the upper halves of the fp32 values
       a = make_float2(__uint_as_float(x[i].x << 16), __uint_as_float(x[i].x & 0xffff0000u));
