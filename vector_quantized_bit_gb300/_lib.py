@@ -635,29 +635,40 @@ def vqkv_cache_compact(mode, k_codes, v_codes, seq_lens, src, counts, cap_len, s
 
 # ---------------------------------------------------------------- rotary positions and the ragged append
 
+@functools.lru_cache(maxsize=1)
+def _row_dtypes(torch):
+    return {torch.float16: VQKV_DTYPE_F16, torch.float32: VQKV_DTYPE_F32, torch.bfloat16: VQKV_DTYPE_BF16}
+
+
 def _row_dtype(torch, what, name, t) -> int:
-    code = {torch.float16: VQKV_DTYPE_F16, torch.float32: VQKV_DTYPE_F32, torch.bfloat16: VQKV_DTYPE_BF16}.get(t.dtype)
+    code = _row_dtypes(torch).get(t.dtype)
     if code is None:
         raise TypeError(f"{what}: {name} must be fp16, bf16 or fp32, not {t.dtype}")
     return code
 
 
 def _check_rows(what, name, t, shape, dtype, dev):
-    """Rows [tokens][heads][128] of any strides whose channels are neighbours, on the current CUDA device."""
+    """Strides of rows [tokens][heads][128] whose channels are neighbours, on the current CUDA device.
+
+    ``shape``: None where it is t's own (_rows_shape).
+    """
+    strides = t.stride()
+    if t.dtype is dtype and (shape is None or t.shape == shape) and strides[2] == 1 and t.get_device() == dev:
+        return strides
     if t.dtype is not dtype:
         raise TypeError(f"{what}: {name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.stride(2) != 1:
+    if strides[2] != 1:
         raise ValueError(f"{what}: the channels of {name} must be contiguous")
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: {name} must be on the current CUDA device")
+    raise ValueError(f"{what}: {name} must be on the current CUDA device")
 
 
 def _rows_shape(what, name, t):
-    if t.dim() != 3 or t.shape[2] != 128:
-        raise ValueError(f"{what}: {name} must have shape (tokens, heads, 128), not {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 128:
+        raise ValueError(f"{what}: {name} must have shape (tokens, heads, 128), not {tuple(shape)}")
+    return shape
 
 
 def _check_table(what, table):
@@ -692,11 +703,11 @@ def vqkv_rope(x, positions, table, out, interleaved=False, transpose=False, erro
     handle = _enter(torch, what, stream, (("positions", positions, torch.int32, (T,)), ("table", table, torch.float32, None),
                                           ("error_flags", error_flags, torch.int32, (1,))))
     dev = positions.get_device()
-    _check_rows(what, "x", x, shape, x.dtype, dev)
-    _check_rows(what, "out", out, shape, x.dtype, dev)
-    a = RopeArgs(code, T, H, D, table.shape[1], table.shape[0], int(interleaved), int(transpose), x.stride(0), x.stride(1),
-                 out.stride(0), out.stride(1), x.data_ptr(), positions.data_ptr(), table.data_ptr(), out.data_ptr(),
-                 _ptr(error_flags))
+    xt, xh, _ = _check_rows(what, "x", x, None, x.dtype, dev)
+    ot, oh, _ = _check_rows(what, "out", out, shape, x.dtype, dev)
+    n_pos, rot = table.shape
+    a = RopeArgs(code, T, H, D, rot, n_pos, int(interleaved), int(transpose), xt, xh, ot, oh, x.data_ptr(),
+                 positions.data_ptr(), table.data_ptr(), out.data_ptr(), _ptr(error_flags))
     _check(lib().vqkv_rope(ctypes.byref(a), handle), what)
 
 
@@ -718,7 +729,7 @@ def vqkv_append(mode, k, v, row_start, pos, s, k_codebook, v_codebook, k_codes, 
     code = _row_dtype(torch, what, "k", k)
     B = pos.shape[0]
     cache = _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks)
-    book = (Hkv, *CODEBOOK_SHAPE.get(mode, k_codebook.shape[1:]))   # the C entry refuses other modes
+    book = (Hkv, *(CODEBOOK_SHAPE.get(mode) or k_codebook.shape[1:]))   # the C entry refuses other modes
     if rope_table is not None:
         _check_table(what, rope_table)
     handle = _enter(torch, what, stream, (
@@ -729,13 +740,13 @@ def vqkv_append(mode, k, v, row_start, pos, s, k_codebook, v_codebook, k_codes, 
         ("near_tie_count", near_tie_count, torch.int64, (1,)), ("error_flags", error_flags, i32, (1,)),
         ("block_table", block_table, i32, None)))
     dev = pos.get_device()
-    _check_rows(what, "k", k, shape, k.dtype, dev)
-    _check_rows(what, "v", v, shape, k.dtype, dev)
+    kt, kh, _ = _check_rows(what, "k", k, None, k.dtype, dev)
+    vt, vh, _ = _check_rows(what, "v", v, shape, k.dtype, dev)
     n_pos, rot = rope_table.shape if rope_table is not None else (0, 0)
-    a = AppendArgs(mode, code, B, Hkv, D, T, cap_len, rot, n_pos, int(interleaved), k.stride(0), k.stride(1), v.stride(0),
-                   v.stride(1), k.data_ptr(), v.data_ptr(), row_start.data_ptr(), pos.data_ptr(), _ptr(rope_pos),
-                   _ptr(rope_table), s.data_ptr(), k_codebook.data_ptr(), v_codebook.data_ptr(), k_codes.data_ptr(),
-                   v_codes.data_ptr(), _ptr(near_tie_count), _ptr(error_flags))
+    a = AppendArgs(mode, code, B, Hkv, D, T, cap_len, rot, n_pos, int(interleaved), kt, kh, vt, vh, k.data_ptr(),
+                   v.data_ptr(), row_start.data_ptr(), pos.data_ptr(), _ptr(rope_pos), _ptr(rope_table), s.data_ptr(),
+                   k_codebook.data_ptr(), v_codebook.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), _ptr(near_tie_count),
+                   _ptr(error_flags))
     _check(lib().vqkv_append(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
 
 
@@ -770,19 +781,19 @@ def vqkv_cross_attn(mode, q, row_start, k_codes, v_codes, seq_lens, k_codebook, 
         raise TypeError(f"{what}: q must be fp16 or bf16, not {q.dtype}")
     B, Hkv = seq_lens.shape[0], k_codebook.shape[0]
     cache = _cache_shape(what, mode, B, Hkv, cap_len, block_table, block_tokens, num_blocks)
-    book = (Hkv, *CODEBOOK_SHAPE.get(mode, k_codebook.shape[1:]))   # the C entry refuses other modes
+    book = (Hkv, *(CODEBOOK_SHAPE.get(mode) or k_codebook.shape[1:]))   # the C entry refuses other modes
     handle = _enter(torch, what, stream, (
         ("row_start", row_start, i32, (B + 1,)), ("k_codes", k_codes, u8, cache), ("v_codes", v_codes, u8, cache),
         ("seq_lens", seq_lens, i32, (B,)), ("k_codebook", k_codebook, f16, book), ("v_codebook", v_codebook, f16, book),
         ("s", s, torch.float32, (Hkv, D)), ("out", out, q.dtype, shape), ("workspace", workspace, u8, None),
         ("block_table", block_table, i32, None)))
-    _check_rows(what, "q", q, shape, q.dtype, seq_lens.get_device())
-    if Hq > 1 and q.stride(1) != D:
+    row, head, _ = _check_rows(what, "q", q, None, q.dtype, seq_lens.get_device())
+    if Hq > 1 and head != D:
         raise ValueError(f"{what}: the heads of q must be contiguous")
     a = CrossArgs((mode, B, Hq, Hkv, D, cap_len, max_seq_len, q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
                    seq_lens.data_ptr(), k_codebook.data_ptr(), v_codebook.data_ptr(), s.data_ptr(), softmax_scale,
                    num_splits, workspace.data_ptr(), workspace.numel(), out.data_ptr()),
-                  VQKV_DTYPE_F16 if q.dtype is f16 else VQKV_DTYPE_BF16, n, max_queries, q.stride(0), row_start.data_ptr())
+                  VQKV_DTYPE_F16 if q.dtype is f16 else VQKV_DTYPE_BF16, n, max_queries, row, row_start.data_ptr())
     _check(lib().vqkv_cross_attn(ctypes.byref(a), _paging_ref(block_table, block_tokens, num_blocks), handle), what)
 
 
