@@ -170,6 +170,7 @@ struct PlanInput {
   // max_seq_len + credit_tiles, so that split comes out this much shorter.
   int credit_tiles = 0;
   int width = 8;   // softmax columns per CTA
+  bool rows = false;   // packed rows (cross attention of one query per sequence)
 };
 
 vqkv_status plan_decode(const PlanInput* a, DecodePlan* pl) {
@@ -183,10 +184,13 @@ vqkv_status plan_decode(const PlanInput* a, DecodePlan* pl) {
   const long long slots = (long long)di.sms * di.decode_bpsm[a->mode];
   const int B = std::max(a->B, 1);
   // 1.5-bit CTAs load 128 KB of codebooks: keep one CTA per KV head and split
-  // across sequences only when the batch alone cannot fill the GPU.
+  // across sequences only when the batch alone cannot fill the GPU.  Not over packed
+  // rows: one query of 16 sequences x 8 heads over 700 to 1,500 tokens takes 17 us with
+  // a CTA each, 79 with shared ones; of 4 x 8 over 20,000 to 60,000 106 and 118.
   int bpg = 1;
-  if (a->mode == VQKV_MODE_VQ15 && (long long)B * a->Hkv < slots) bpg = B;
+  if (a->mode == VQKV_MODE_VQ15 && (long long)B * a->Hkv < slots && !a->rows) bpg = B;
   const int cgroups = (g * a->M + a->width - 1) / a->width;   // CTAs per (sequence group, KV head, split)
+  const long long S = std::max<long long>(1, slots / ((long long)a->Hkv * cgroups));
   // Flat plan for batches on the tile-ring decode: one wave of CTAs per (KV
   // head, column group), each taking an equal share of all sequences' tiles,
   // balanced by the actual lengths on the device (ragged batches leave no CTA
@@ -194,8 +198,18 @@ vqkv_status plan_decode(const PlanInput* a, DecodePlan* pl) {
   const bool ring = a->mode == VQKV_MODE_VQ2 || a->mode == VQKV_MODE_VQ4 || a->mode == VQKV_MODE_VQ3 ||
                     a->mode == VQKV_MODE_VQ125;
   const long long super_max = (tiles_max + unit_tiles - 1) / unit_tiles;
-  if (ring && a->num_splits == 0 && a->B > 1 && a->B <= kFlatMaxB && (long long)a->B * super_max < (1LL << 30)) {
-    const long long S = std::max<long long>(1, slots / ((long long)a->Hkv * cgroups));
+  // Packed rows of short sequences: a CTA per sequence, in waves.  A share's passage from
+  // sequence to sequence (prologue, merge of its warps, partial) costs as much as some
+  // 175 tiles, a wave's 120; the lengths are the host's bound, of which ragged batches may
+  // fill a quarter.  16 sequences x 16 heads at 2 bit: 700 to 1,500 tokens 17 us against
+  // 27 in shares, 100 to 300 tokens 11 against 22; 3,000 to 8,000 (shares) 49 against 50.
+  bool whole = false;
+  if (ring && a->rows && a->num_splits == 0 && a->B > 1) {
+    const long long waves = ((long long)B * a->Hkv * cgroups + slots - 1) / slots;
+    const double tiles = (a->mode == VQKV_MODE_VQ3 ? 2.0 : 1.0) * tiles_max;   // in time: its gathers conflict
+    whole = waves * (tiles + 120) <= 75 + 175.0 * (B + S) / S + 0.25 * tiles * B / S;
+  }
+  if (ring && !whole && a->num_splits == 0 && a->B > 1 && a->B <= kFlatMaxB && (long long)a->B * super_max < (1LL << 30)) {
     pl->flat = 1;
     pl->n_splits = (int)S;
     pl->tps = 0;
@@ -215,7 +229,7 @@ vqkv_status plan_decode(const PlanInput* a, DecodePlan* pl) {
   double best_cost = 1e300;
   if (a->num_splits > 0) {
     best_n = std::min<long long>(a->num_splits, tiles_max);
-  } else {
+  } else if (!whole) {
     const long long n_hi = std::min<long long>(tiles_max, 4 * ((slots + pairs - 1) / pairs) + 64);
     for (long long n = 1; n <= n_hi; ++n) {
       const long long tps = (tiles_max + n - 1) / n;
@@ -1043,6 +1057,7 @@ vqkv_status plan_cross(const vqkv_cross_args* ac, CrossPlan* pl) {
     if (ready != VQKV_OK) return ready;
     PlanInput in = plan_input(&a);
     in.width = 4;
+    in.rows = true;
     const vqkv_status st = plan_decode(&in, &pl->d);
     pl->ws_bytes = pl->d.ws_bytes;
     return st;

@@ -1,8 +1,9 @@
 // Cross attention of one query per sequence at most (vqkv_cross_attn with
 // max_queries = 1): the single-query decode's kernels on packed rows, four columns
-// of two fp16 parts of q' per CTA.  One column of 16 sequences of 700 to 1,500
-// tokens and 16 heads at 2 bit takes 27 us here and 39 us on the tile kernel, whose
-// products have 128 rows and whose softmax then hangs on one warp.
+// of two fp16 parts of q' per CTA, a CTA per sequence where they are short
+// (plan_decode).  One column of 16 sequences of 700 to 1,500 tokens and 16 heads at 2
+// bit takes 17 us here, 27 in equal shares of all tokens, and 39 us on the tile kernel,
+// whose products have 128 rows and whose softmax then hangs on one warp.
 #include "decode_kernels.cuh"
 
 namespace vqkv {
