@@ -54,3 +54,18 @@ def test_both_parts_of_the_query_count(t, mode, queries):
     ref, _ = x.reference()
     assert np.linalg.norm(got - ref) <= 4.1e-4 * np.linalg.norm(ref)
     assert x.flags() == 0
+
+
+@pytest.mark.parametrize("mode", range(5))
+@pytest.mark.parametrize("dt,block_tokens", [("fp16", 0), ("bf16", 64), ("fp16", 256)])
+@pytest.mark.parametrize("queries,lens", [
+    ([1, 1, 0, 1, 1], [6000, 17, 400, 0, 2500]),       # shares of all sequences' tokens, but at 1.5 bit
+    ([1] * 40, [300 + 7 * i for i in range(40)]),      # a CTA per sequence
+    ([1], [7000]),                                     # splits of one
+])
+def test_single_queries_long_and_short(t, mode, dt, block_tokens, queries, lens):
+    x = Cross(t, mode, 4, 2, queries, lens, dt=dt, block_tokens=block_tokens, seed=mode)
+    got = x.run()
+    x.check(got, *x.reference())
+    assert x.flags() == 0
+    assert t.equal(got, x.run(out=t.full_like(x.out, 3.0), ws=x.ws))
