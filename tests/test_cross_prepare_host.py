@@ -57,7 +57,7 @@ def test_kernels_whose_registers_do_not_cover_their_split_are_refused(run):  # n
     run(CALLS + """
 fake.fake_registers(64)
 for m in range(5):
-    assert [call(m) for call in calls] == [0, 0, 4, 4, 4, 0]
+    assert [call(m) for call in calls] == [0, 4, 4, 4, 4, 0]
     assert L.vqkv_cross_attn_workspace_bytes(ctypes.byref(cross(m))) == 0
     assert L.vqkv_cross_attn_workspace_bytes(ctypes.byref(cross(m, 2, 1))) > 0
 """)

@@ -19,14 +19,16 @@ constexpr int kMaxTokens = 1 << 30; // longest row of the cache-editing calls (p
 
 // Kernels that are prepared (attributes set, checks made) only when a call that
 // uses them is first planned, so that no other call loads them or fails with them.
-enum LazyKernels : int { kTreeKernels, kMassKernels, kMassTileKernels, kCompactKernels, kSelectKernels, kAppendKernels, kCrossKernels, kCrossRowsKernels, kLazyKernels };
+enum LazyKernels : int {
+  kTreeKernels, kMassKernels, kMassTileKernels, kCompactKernels, kSelectKernels, kEncodeTileKernels, kAppendKernels,
+  kAppendTileKernels, kCrossKernels, kCrossRowsKernels, kLazyKernels
+};
 
 struct DeviceInfo {
   bool ready = false;
   bool prepared[kLazyKernels][kCodeModes] = {};
   int sms = 0;
   int decode_bpsm[kCodeModes + 1] = {};   // resident decode CTAs per SM: each code mode, then fp16
-  int encode_bpsm[kCodeModes] = {};
   int compact_cluster[kCodeModes] = {};   // largest cluster of the compaction
 };
 
@@ -44,9 +46,7 @@ vqkv_status device_info(DeviceInfo* out) {
     for (int m = 0; m < kCodeModes; ++m) {
       if (decode_prepare(m) != cudaSuccess || encode_prepare(m) != cudaSuccess) return VQKV_ERR_CUDA;
       if (decode_occupancy(m, &d.decode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
-      if (encode_occupancy(m, &d.encode_bpsm[m]) != cudaSuccess) return VQKV_ERR_CUDA;
       if (d.decode_bpsm[m] < 1) d.decode_bpsm[m] = 1;
-      if (d.encode_bpsm[m] < 1) d.encode_bpsm[m] = 1;
     }
     if (decode_fp16_prepare() != cudaSuccess || decode_fp16_occupancy(&d.decode_bpsm[kModeFp16]) != cudaSuccess)
       return VQKV_ERR_CUDA;
@@ -69,7 +69,9 @@ vqkv_status device_info(LazyKernels what, int mode, DeviceInfo* out) {
                         : what == kMassKernels     ? decode_mass_prepare(mode)
                         : what == kMassTileKernels ? mass_tiles_prepare(mode)
                         : what == kCompactKernels  ? compact_prepare(mode, &d.compact_cluster[mode])
-                        : what == kAppendKernels   ? append_prepare(mode)
+                        : what == kEncodeTileKernels ? encode_tiles_prepare(mode)
+                        : what == kAppendKernels     ? append_prepare(mode, true)
+                        : what == kAppendTileKernels ? append_prepare(mode, false)
                         : what == kCrossKernels    ? cross_prepare(mode)
                         : what == kCrossRowsKernels ? cross_rows_prepare(mode)
                                                    : evict_select_prepare();
@@ -698,9 +700,11 @@ vqkv_status encode_launch(const vqkv_encode_args* a, void* stream, const vqkv_pa
   if (split_rows) {
     blocks_x = (int)rows;
   } else {
+    const vqkv_status ready = device_info(kEncodeTileKernels, a->mode, &di);
+    if (ready != VQKV_OK) return ready;
     const long long want = (rows + encode_warps_per_cta() - 1) / encode_warps_per_cta();
-    // persistent tensor-memory CTAs over tiles of 8, 4 or 2 rows, one wave
-    long long cap = ((long long)di.sms * di.encode_bpsm[a->mode] + a->Hkv - 1) / a->Hkv;
+    // persistent tensor-memory CTAs over tiles of 8, 4 or 2 rows, one per SM
+    long long cap = ((long long)di.sms + a->Hkv - 1) / a->Hkv;
     if (cap < 1) cap = 1;
     blocks_x = (int)std::min(want, cap);
   }
@@ -1192,7 +1196,9 @@ vqkv_status vqkv_append(const vqkv_append_args* a, const vqkv_paging* pg, void* 
       !aligned(a->k_codebook, 16) || !aligned(a->v_codebook, 16) || !aligned(a->near_tie_count, 8) || !aligned(a->error_flags, 4))
     return VQKV_ERR_INVALID_ARG;
   DeviceInfo di;
-  const vqkv_status st = device_info(kAppendKernels, a->mode, &di);
+  vqkv_status st = device_info(&di);
+  if (st != VQKV_OK) return st;
+  st = device_info(append_few_rows(a->n_tokens, a->Hkv, di.sms) ? kAppendKernels : kAppendTileKernels, a->mode, &di);
   if (st != VQKV_OK) return st;
   AppendParams p{};
   EncodeParams& e = p.both;

@@ -51,18 +51,17 @@ AppendVariant variant(int mode, bool few) {
 
 }  // namespace
 
-cudaError_t append_prepare(int mode) {
-  cudaError_t e = cudaSuccess;
-  for (int few = 0; few < 2 && e == cudaSuccess; ++few) {
-    const AppendVariant v = variant(mode, few != 0);
-    if (v.smem > 0) e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)v.smem);
-  }
-  return e;
+bool append_few_rows(int n_tokens, int Hkv, int sms) { return (long long)n_tokens * 2 * Hkv <= sms; }
+
+cudaError_t append_prepare(int mode, bool few) {
+  const AppendVariant v = variant(mode, few);
+  if (!few) return prepare_split_kernel(v.kernel, v.threads, um::SPLIT_REGS, (int)v.smem);
+  return v.smem > 0 ? cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)v.smem) : cudaSuccess;
 }
 
 cudaError_t launch_append(int mode, AppendParams p, int sms, cudaStream_t stream) {
   const int Hkv = p.both.Hkv;
-  const AppendVariant v = variant(mode, (long long)p.n_tokens * 2 * Hkv <= sms);
+  const AppendVariant v = variant(mode, append_few_rows(p.n_tokens, Hkv, sms));
   const int want = (p.n_tokens + v.rows - 1) / v.rows;   // CTAs of a KV head and role with work
   int keys = want, values = want;
   if (v.rows > 1) {

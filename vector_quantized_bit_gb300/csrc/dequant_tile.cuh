@@ -15,18 +15,6 @@
 namespace vqkv {
 namespace {
 
-// Shared memory of a kernel that splits its registers between warpgroups
-// (setmaxnreg), after checking that the launch's registers cover the split: one
-// that does not would wait forever.
-template <typename K>
-cudaError_t prepare_split_kernel(K kernel, int threads, int registers_of_split, int smem) {
-  cudaFuncAttributes a;
-  const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
-  if (e != cudaSuccess) return e;
-  if (a.numRegs * threads < registers_of_split) return cudaErrorInvalidConfiguration;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-}
-
 template <int MODE>
 struct CodeGeo {
   static constexpr int LAYOUT_TOK = MODE == VQKV_MODE_VQ15 ? 64 : 16;
@@ -296,13 +284,6 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
-}
-
-// True in one lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
-  return e != 0;
 }
 
 // Bounded wait by a whole warp: false, with the abort flag and the device

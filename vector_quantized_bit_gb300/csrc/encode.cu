@@ -1,5 +1,5 @@
-// Host side of the VQ encode (kernels in encode_kernels.cuh): preparation,
-// occupancy and launches.
+// Host side of the VQ encode (kernels in encode_kernels.cuh): preparation and
+// launches.
 #include "common.cuh"
 #include "encode_kernels.cuh"
 #include "internal.h"
@@ -10,47 +10,21 @@ int encode_warps_per_cta() { return ENC_WARPS; }
 
 cudaError_t encode_prepare(int mode) {
   const cudaFuncAttribute smem_attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  if (mode == VQKV_MODE_VQ3) {
-    cudaError_t e = cudaFuncSetAttribute(encode_vq3_kernel<ENC3_SPLIT>, smem_attr, (int)kEnc3Smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(encode_umma_kernel<VQKV_MODE_VQ3>, smem_attr, (int)UmGeo<VQKV_MODE_VQ3>::SMEM);
-    return e;
-  }
-  if (mode == VQKV_MODE_VQ125)
-    return cudaFuncSetAttribute(encode_umma_kernel<VQKV_MODE_VQ125>, smem_attr, (int)UmGeo<VQKV_MODE_VQ125>::SMEM);
-  if (mode == VQKV_MODE_VQ2)
-    return cudaFuncSetAttribute(encode_umma_kernel<VQKV_MODE_VQ2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)UmGeo<VQKV_MODE_VQ2>::SMEM);
-  if (mode == VQKV_MODE_VQ4)
-    return cudaFuncSetAttribute(encode_umma_kernel<VQKV_MODE_VQ4>, smem_attr, (int)UmGeo<VQKV_MODE_VQ4>::SMEM);
-  if (mode != VQKV_MODE_VQ15) return cudaSuccess;
-  {
-    const cudaError_t e0 = cudaFuncSetAttribute(encode_umma_kernel<VQKV_MODE_VQ15>,
-                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                (int)UmGeo<VQKV_MODE_VQ15>::SMEM);
-    if (e0 != cudaSuccess) return e0;
-    const cudaError_t e1 = cudaFuncSetAttribute(encode_vq15_tc_split_kernel<>,
-                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSplitSmem);
-    if (e1 != cudaSuccess) return e1;
-  }
+  if (mode == VQKV_MODE_VQ3) return cudaFuncSetAttribute(encode_vq3_kernel<ENC3_SPLIT>, smem_attr, (int)kEnc3Smem);
+  if (mode == VQKV_MODE_VQ15) return cudaFuncSetAttribute(encode_vq15_tc_split_kernel<>, smem_attr, (int)kTcSplitSmem);
   return cudaSuccess;
 }
 
-cudaError_t encode_occupancy(int mode, int* blocks_per_sm) {
-  if (mode == VQKV_MODE_VQ2)
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, encode_umma_kernel<VQKV_MODE_VQ2>,
-                                                         um::THREADS, UmGeo<VQKV_MODE_VQ2>::SMEM);
-  if (mode == VQKV_MODE_VQ4)
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, encode_umma_kernel<VQKV_MODE_VQ4>,
-                                                         um::THREADS, UmGeo<VQKV_MODE_VQ4>::SMEM);
-  if (mode == VQKV_MODE_VQ3)
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, encode_umma_kernel<VQKV_MODE_VQ3>,
-                                                         um::THREADS, UmGeo<VQKV_MODE_VQ3>::SMEM);
-  if (mode == VQKV_MODE_VQ125)
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, encode_umma_kernel<VQKV_MODE_VQ125>,
-                                                         um::THREADS, UmGeo<VQKV_MODE_VQ125>::SMEM);
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, encode_umma_kernel<VQKV_MODE_VQ15>,
-                                                       um::THREADS, UmGeo<VQKV_MODE_VQ15>::SMEM);
+template <int MODE>
+cudaError_t prepare_tiles() {
+  return prepare_split_kernel(encode_umma_kernel<MODE>, um::THREADS, um::SPLIT_REGS, (int)UmGeo<MODE>::SMEM);
+}
+cudaError_t encode_tiles_prepare(int mode) {
+  return mode == VQKV_MODE_VQ2    ? prepare_tiles<VQKV_MODE_VQ2>()
+         : mode == VQKV_MODE_VQ4  ? prepare_tiles<VQKV_MODE_VQ4>()
+         : mode == VQKV_MODE_VQ3  ? prepare_tiles<VQKV_MODE_VQ3>()
+         : mode == VQKV_MODE_VQ15 ? prepare_tiles<VQKV_MODE_VQ15>()
+                                  : prepare_tiles<VQKV_MODE_VQ125>();
 }
 
 // split_rows: one row per CTA, candidates split over the CTA's warps.

@@ -476,21 +476,20 @@ __device__ __forceinline__ float build_tc_table(const EncodeParams& p, int kvh, 
 // lanes of every warp then have a second group to re-rank, each of them the whole
 // warp's work, and that took half of the kernel's time.)
 //
-// Roles (16 warps, one CTA per SM, persistent over the KV head's tiles; up to
-// 128 registers a thread, a 128-column chunk in flight per epilogue thread):
-//   warps 8-13   producers: transform every sixth row
-//                (smoothing + Hadamard for keys), write A, x', the key before
-//                the transform and |x'_j|^2 into one of 4 stages;
-//   warps 14, 15 one thread each issues the MMAs of one epilogue warpgroup,
-//                chunk by chunk into that warpgroup's two 128-column
-//                tensor-memory buffers (warp 14 also allocates the 512
-//                columns); separate issuers keep one warpgroup's wait for a
-//                free buffer from holding up the other's MMAs;
-//   warps 0-3, 4-7  two epilogue warpgroups taking alternate tiles: thread m
-//                owns tensor-memory lane m, i.e. subvector m % S of row m / S
-//                (S = 16 or 32 subvectors a row).
-// The epilogue does not rank candidates one by one: per group of 32
-// consecutive centroids it takes the group minimum, which the tensor-memory
+// Roles (24 warps, one CTA per SM, persistent over the KV head's tiles):
+//   warps 0-15   four epilogue warpgroups taking tiles in turn: thread m owns
+//                tensor-memory lane m, i.e. subvector m % S of row m / S (S = 16, 32 or
+//                64 subvectors a row).  Each has one 128-column tensor-memory buffer; its
+//                first warp issues the next chunk's MMAs as soon as all four have read
+//                the last one.  (Two warpgroups with two buffers each and issuing
+//                warps of their own, at 128 registers: 131,072 rows of 2-bit keys took
+//                207 us, now 183; 4 bit 473 and 389, 3 bit 1,134 and 1,080: a chunk's
+//                loads, the ranking and another tile's re-rank overlap more.)
+//   warps 16-23  producers: transform every eighth row (smoothing + Hadamard for
+//                keys), write A, x', the key before the transform and |x'_j|^2 into one
+//                of the stages.
+// The epilogue does not rank candidates one by one: per group of 32 (or
+// 16) consecutive centroids it takes the group minimum, which the tensor-memory
 // load computes itself (tcgen05.ld.red ... .min, one load per group), and
 // keeps the four smallest group minima B1 <= B2 <= B3 <= B4, each carrying
 // its group id.  A centroid can be the exact nearest only if its screened
@@ -510,20 +509,22 @@ __device__ __forceinline__ float build_tc_table(const EncodeParams& p, int kvh, 
 //
 // Every wait is bounded: a wait that runs out sets VQKV_DEVERR_TIMEOUT (when
 // the caller passed an error word) and an abort flag that ends every role's
-// loop; the MMA thread then waits (bounded) for its MMAs before the tensor
+// loop; the issuing warps then wait (bounded) for their MMAs before the tensor
 // memory is freed.
 namespace um {
 constexpr int M = 128;                        // MMA rows: (row, subvector) pairs of a tile
 constexpr int N = 128;                        // centroids per MMA
-constexpr int NBUF = 2;                       // tensor-memory buffers per epilogue warpgroup
-constexpr int STAGES = 4;
-constexpr int PROD_WARPS = 6;
-constexpr int MMA_WARP = 8 + PROD_WARPS;      // 14 (warpgroup 0's issuer; 15: warpgroup 1's)
-constexpr int THREADS = (MMA_WARP + 2) * 32;  // 512
+constexpr int WGS = 4;                        // epilogue warpgroups, each with a tensor-memory buffer of N columns
+constexpr int EP_WARPS = 4 * WGS, PROD_WARPS = 8;
+constexpr int THREADS = (EP_WARPS + PROD_WARPS) * 32;   // 768
+// Registers per thread: 80 at launch, then 88 for the epilogue and 64 for the producers:
+// 512 x 88 + 256 x 64 = 61,440 = 768 x 80.  (With 80 throughout, the ranking spills in its
+// loop: 131,072 3-bit key rows 1,329 us, not 1,080.  With 96 and 48 the rotating
+// producers spill: 17,450 appended 2-bit tokens 438 us, not 405.)
+constexpr int REGS_EP = 88, REGS_PROD = 64, SPLIT_REGS = THREADS * 80;
+static_assert(32 * (EP_WARPS * REGS_EP + PROD_WARPS * REGS_PROD) == SPLIT_REGS, "the launch's registers");
 constexpr int A_BYTES = M * 32;               // one A tile: 128 x 16 fp16
-constexpr int NBAR = 2 * STAGES + 4 * NBUF + 2;   // A full / empty, tensor-memory full / empty, MMAs done x 2
-constexpr uint32_t TMEM_COLS = 512;           // 2 warpgroups x NBUF buffers x N
-static_assert(2 * NBUF * N <= (int)TMEM_COLS, "tensor-memory plan");
+constexpr uint32_t TMEM_COLS = WGS * N;
 constexpr uint32_t MAX_POLLS = 1u << 22;
 // row flags
 constexpr int F_OK = 0, F_EXHAUSTIVE = 1, F_SKIP = 2;
@@ -541,15 +542,14 @@ struct UmGeo {
   static constexpr int ROWS = um::M / SUBV;               // rows per tile
   static constexpr int CHUNKS = E / um::N;               // MMAs per tile
   static constexpr int TABLE_BYTES = E * 32;             // B: E centroids x 16 fp16
-  // Warps that take rows in turn.  A warp that comes to stage k % STAGES for tile k
-  // tells by the parity of one phase that tile k - 4 has been released; tile k - 8's
-  // release has to be certain then.  It is when the warp filled tile k - 2 or k - 4
-  // itself: that waited for tile k - 6 or k - 8, which the same epilogue warpgroup
-  // takes in order.  Six warps come to every tile (8 rows), or to two of three (4
-  // rows: k - 4 or k - 2 is among them); of 2 rows to every third, so there only four
-  // work (every second tile).
-  static constexpr int PRODUCERS = ROWS == 2 ? 4 : um::PROD_WARPS;
-  static_assert(um::STAGES == 4, "the argument above");
+  static constexpr int STAGES = E == 4096 ? 4 : 8;       // rings of A tiles; a warpgroup's tiles share 1 or 2 of them
+  static constexpr int NBAR = 2 * STAGES + 3 * um::WGS;  // A full / empty, tensor memory full / empty, MMAs done
+  // Eight producing warps take rows in turn: a row of every tile (8 rows a tile), of
+  // every second (4) or of every fourth (2).  A warp that comes to stage k % STAGES tells
+  // by the parity of one phase that tile k - STAGES has been released, which is
+  // unambiguous as tile k - 2 STAGES's release is certain: the warp filled tile
+  // k - STAGES itself, a multiple of four before, and waited for it then.
+  static_assert(um::PROD_WARPS % ROWS == 0 && STAGES % (um::PROD_WARPS / ROWS) == 0, "the argument above");
   // Centroids per group minimum.  16: half as many to re-rank, twice the minima to
   // keep; pays up to 1,024 centroids.
   static constexpr int GROUP = E == 4096 ? 32 : 16;
@@ -561,8 +561,8 @@ struct UmGeo {
   static constexpr int ST_POS = ST_FLAG + um::M * 4;
   static constexpr int STAGE_BYTES = ST_POS + 24 * 4;   // + each row's cache position, sequence, error of x'
   static constexpr int OFF_STAGES = TABLE_BYTES;
-  static constexpr int OFF_BAR = OFF_STAGES + um::STAGES * STAGE_BYTES;
-  static constexpr int OFF_MISC = OFF_BAR + um::NBAR * 8;   // tensor-memory base, abort flag, max centroid norm
+  static constexpr int OFF_BAR = OFF_STAGES + STAGES * STAGE_BYTES;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor-memory base, abort flag, max centroid norm
   // 4- and 2-channel modes: the codebook again as plain fp16; with [E][4], 8 bytes a
   // centroid, so that 16 lanes reading 16 consecutive centroids hit 16
   // distinct bank pairs in the exact re-rank (the B table's 32-byte rows give
@@ -570,7 +570,7 @@ struct UmGeo {
   static constexpr int OFF_CB4 = OFF_MISC + 16;
   static constexpr size_t SMEM = OFF_CB4 + (DSUB == 8 ? 0 : E * DSUB * 2);
   static_assert(SMEM <= 227 * 1024 && STAGE_BYTES % 16 == 0 && OFF_BAR % 8 == 0, "UMMA encode shared memory");
-  static_assert(CHUNKS % um::NBUF == 0 && E / GROUP <= 128 && um::N % GROUP == 0 && ROWS <= 8, "tile plan (7-bit group ids)");
+  static_assert(E / GROUP <= 128 && um::N % GROUP == 0 && ROWS <= 8, "tile plan (7-bit group ids)");
 };
 
 // Bounded wait on an mbarrier phase by every lane of a warp (or one thread:
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
     encode_umma_kernel(const __grid_constant__ typename Rows<APPEND>::Params a) {
   using namespace um;
   using Geo = UmGeo<MODE>;
-  constexpr int DSUB = Geo::DSUB, GROUP = Geo::GROUP, E = Geo::E, SUBV = Geo::SUBV, ROWS = Geo::ROWS, CHUNKS = Geo::CHUNKS;
+  constexpr int DSUB = Geo::DSUB, GROUP = Geo::GROUP, E = Geo::E, SUBV = Geo::SUBV, ROWS = Geo::ROWS, CHUNKS = Geo::CHUNKS, STAGES = Geo::STAGES;
   constexpr int ST_A = Geo::ST_A, ST_X = Geo::ST_X, ST_NORM = Geo::ST_NORM, ST_FLAG = Geo::ST_FLAG;
   constexpr int ST_POS = Geo::ST_POS, STAGE_BYTES = Geo::STAGE_BYTES, OFF_STAGES = Geo::OFF_STAGES;
   constexpr int OFF_BAR = Geo::OFF_BAR, OFF_MISC = Geo::OFF_MISC;
@@ -685,9 +685,9 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   const uint32_t bar = sbase + OFF_BAR;
   auto a_full = [&](int s) { return bar + 8u * s; };
   auto a_empty = [&](int s) { return bar + 8u * (STAGES + s); };
-  auto t_full = [&](int wg, int b) { return bar + 8u * (2 * STAGES + NBUF * wg + b); };
-  auto t_empty = [&](int wg, int b) { return bar + 8u * (2 * STAGES + 2 * NBUF + NBUF * wg + b); };
-  auto done_bar = [&](int wg) { return bar + 8u * (2 * STAGES + 4 * NBUF + wg); };
+  auto t_full = [&](int wg) { return bar + 8u * (2 * STAGES + wg); };
+  auto t_empty = [&](int wg) { return bar + 8u * (2 * STAGES + WGS + wg); };
+  auto done_bar = [&](int wg) { return bar + 8u * (2 * STAGES + 2 * WGS + wg); };
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   float* s_cmax = reinterpret_cast<float*>(smem + OFF_MISC + 8);
@@ -697,18 +697,16 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       mbar_init(a_full(s), ROWS);
       mbar_init(a_empty(s), 4);
     }
-    for (int wg = 0; wg < 2; ++wg)
-      for (int b = 0; b < NBUF; ++b) {
-        mbar_init(t_full(wg, b), 1);
-        mbar_init(t_empty(wg, b), 4);
-      }
-    mbar_init(done_bar(0), 1);
-    mbar_init(done_bar(1), 1);
+    for (int wg = 0; wg < WGS; ++wg) {
+      mbar_init(t_full(wg), 1);
+      mbar_init(t_empty(wg), 4);
+      mbar_init(done_bar(wg), 1);
+    }
     *s_abort = 0;
     *s_cmax = 0.f;
     mbar_init_fence();
   }
-  if (warp == MMA_WARP) tmem_alloc(smem_u32(s_tmem), TMEM_COLS);
+  if (warp == EP_WARPS) tmem_alloc(smem_u32(s_tmem), TMEM_COLS);
   grid_dependency_wait();
   grid_dependents_launch();
   __syncthreads();
@@ -717,17 +715,16 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   const int tiles = (rows + ROWS - 1) / ROWS;
   const int cta = src.cta(), ctas = src.ctas();
   const int n_my = cta < tiles ? (tiles - cta + ctas - 1) / ctas : 0;
-  // A CTA's only tile: the warpgroups screen half of the centroids each.  (A decode
+  // A CTA's only tile: the warpgroups screen a quarter of the centroids each.  (A decode
   // step of 64 rows, 8 heads and both roles at 1.5 bit took 18.5 us without this and
   // the early loads below, now 13.9.)
-  const bool halves = CHUNKS >= 8 && n_my == 1;
-
-  const bool producer = warp >= 8 && warp < MMA_WARP;
-  const int pw = warp - 8;
+  const bool shared_tile = CHUNKS >= 8 && n_my == 1;
+  const bool producer = warp >= EP_WARPS;
+  const int pw = warp - EP_WARPS;
   // Row job i is row i % ROWS of tile i / ROWS; warp pw takes jobs pw, pw +
   // PRODUCERS, ...  A job's row is loaded one job ahead, its angle two.
-  constexpr int PRODUCERS = Geo::PRODUCERS;
-  const int jobs = producer && pw < PRODUCERS ? n_my * ROWS : 0;
+  constexpr int PRODUCERS = PROD_WARPS;
+  const int jobs = producer ? n_my * ROWS : 0;
   typename Rows<APPEND>::Raw raw{};
   RowPlace at{};
   Turn turn{};
@@ -764,8 +761,8 @@ __global__ void __launch_bounds__(um::THREADS, 1)
   // [-2c (4 fp16), |c|^2 hi, |c|^2 lo, 0, 0, -2c, 0 x 4] (2 bit) or
   // [-2c (2 fp16), |c|^2 hi, |c|^2 lo, -2c, 0 x 10] (4 bit)
   else {
-    constexpr int BUILDERS = THREADS - 32 * PROD_WARPS, PER = (E + BUILDERS - 1) / BUILDERS;
-    const int first = warp < 8 ? threadIdx.x : threadIdx.x - 32 * PROD_WARPS;
+    constexpr int BUILDERS = 32 * EP_WARPS, PER = (E + BUILDERS - 1) / BUILDERS;
+    const int first = threadIdx.x;
     using Word = std::conditional_t<DSUB == 8, uint4, std::conditional_t<DSUB == 4, uint2, uint32_t>>;
     Word raw[PER];   // all in flight
 #pragma unroll
@@ -824,6 +821,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
 
   if (producer) {
     // ---------------- producers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_PROD));
     // 1.5 bit: lanes 2j, 2j + 1 hold subvector j; 2 bit: lane j holds subvector j;
     // 4 bit: lane l holds subvectors j = 2l and j + 1
     const int j = DSUB == 8 ? lane >> 1 : DSUB == 4 ? lane : 2 * lane, half = DSUB == 8 ? lane & 1 : 0;
@@ -907,40 +905,10 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(a_full(s));
     }
-  } else if (warp >= MMA_WARP) {
-    // ---------------- one thread per epilogue warpgroup issues its MMAs
-    const int wg = warp - MMA_WARP;
-    const int q0 = halves ? wg * (CHUNKS / 2) : 0, n_q = halves ? CHUNKS / 2 : CHUNKS;   // its chunks
-    if (lane == 0) {
-      constexpr uint32_t idesc = umma_idesc_f16_f32(M, N);
-      bool ok = true;
-      int it = 0;
-      for (int k = halves ? 0 : wg; ok && k < n_my; k += 2, ++it) {
-        const int s = k % STAGES;
-        ok = um_wait(a_full(s), (k / STAGES) & 1, s_abort, p.err, 1u);
-        const uint64_t dA = umma_desc_kmajor(sbase + OFF_STAGES + s * STAGE_BYTES + ST_A);
-        const uint64_t dLow = umma_desc_kmajor(sbase + OFF_STAGES + s * STAGE_BYTES + Geo::ST_LOW);
-        tcgen05_after_sync();
-        for (int q = 0; ok && q < n_q; ++q) {
-          const int bsel = q % NBUF;
-          const uint32_t use = (uint32_t)(it * (CHUNKS / NBUF) + q / NBUF);
-          ok = um_wait(t_empty(wg, bsel), (use & 1) ^ 1, s_abort, p.err, 1u);
-          if (!ok) break;
-          tcgen05_after_sync();
-          const uint64_t dB = umma_desc_kmajor(sbase + (uint32_t)(q0 + q) * (N * 32));
-          const uint32_t acc = tmem + (uint32_t)((NBUF * wg + bsel) * N);
-          umma_f16(acc, dA, dB, idesc, 0u);
-          if constexpr (DSUB == 8) umma_f16(acc, dLow, dB, idesc, 1u);
-          umma_commit(t_full(wg, bsel));
-        }
-      }
-      // every MMA issued has completed before the tensor memory is freed
-      umma_commit(done_bar(wg));
-      um_wait(done_bar(wg), 0, s_abort, p.err, 1u);
-    }
-    __syncwarp();
   } else {
-    // ---------------- epilogue warpgroup wg: tiles wg, wg + 2, ...
+    // ---------------- epilogue warpgroup wg: tiles wg, wg + WGS, ...; its first warp
+    // issues its MMAs, the next chunk's as soon as all four have read the last one
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EP));
     const int wg = warp >> 2, ml = 32 * (warp & 3) + lane;   // tensor-memory lane = MMA row
     const int r = ml / SUBV, j = ml % SUBV;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -969,7 +937,25 @@ __global__ void __launch_bounds__(um::THREADS, 1)
         return __fmaf_rn(e, e, d);
       }
     };
-    for (int k = halves ? 0 : wg; k < n_my; k += 2) {
+    uint32_t use = 0;   // chunks of this warpgroup so far
+    const bool issuing = (warp & 3) == 0, issuer = elect_one();
+    // chunk q of the tile in stage st into this warpgroup's buffer, use `u` of it
+    auto issue = [&](int st, int q, uint32_t u) -> bool {
+      if (!um_wait(t_empty(wg), (u & 1) ^ 1, s_abort, p.err, 0xffffffffu)) return false;
+      tcgen05_after_sync();
+      if (issuer) {
+        constexpr uint32_t idesc = umma_idesc_f16_f32(M, N);
+        const uint64_t dA = umma_desc_kmajor(sbase + OFF_STAGES + st * STAGE_BYTES + ST_A);
+        const uint64_t dB = umma_desc_kmajor(sbase + (uint32_t)q * (N * 32));
+        umma_f16(tmem + (uint32_t)(wg * N), dA, dB, idesc, 0u);
+        if constexpr (DSUB == 8)
+          umma_f16(tmem + (uint32_t)(wg * N), umma_desc_kmajor(sbase + OFF_STAGES + st * STAGE_BYTES + Geo::ST_LOW), dB, idesc, 1u);
+        umma_commit(t_full(wg));
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int k = shared_tile ? 0 : wg; k < n_my; k += WGS) {
       const float inf = __int_as_float(0x7f800000);
       float B1 = inf, B2 = inf, B3 = inf, B4 = inf;
       // the group minimum (from the tensor-memory load's own reduction) with
@@ -984,15 +970,18 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       };
       auto group = [&](float g, uint32_t gid) { keep(__uint_as_float((__float_as_uint(g) & ~0x7Fu) | gid)); };
       bool ok = true;
-      auto scan = [&](auto chunks) {   // a number of chunks, from the warpgroup's first (a constant: no register)
+      const int s = k % STAGES;
+      auto scan = [&](auto chunks, int q0) {   // a number of chunks (a constant: no register) from q0 on
+        ok = um_wait(a_full(s), (k / STAGES) & 1, s_abort, p.err, 0xffffffffu);
+        if (ok && issuing) ok = issue(s, q0, use);
 #pragma unroll 1
-        for (int q = 0; q < decltype(chunks)::value; ++q) {
-          const int bsel = q % NBUF;
-          const uint32_t use = (uint32_t)((k >> 1) * (CHUNKS / NBUF) + q / NBUF);
-          ok = um_wait(t_full(wg, bsel), use & 1, s_abort, p.err, 0xffffffffu);
-          if (!ok) break;
+        for (int q = 0; q < decltype(chunks)::value; ++q, ++use) {
+          if (!ok || !um_wait(t_full(wg), use & 1, s_abort, p.err, 0xffffffffu)) {
+            ok = false;
+            break;
+          }
           tcgen05_after_sync();
-          const uint32_t col = t_lane + (uint32_t)((NBUF * wg + bsel) * N);
+          const uint32_t col = t_lane + (uint32_t)(wg * N);
           // the whole chunk in flight at once (one wait); the buffer is handed
           // back before the values are reduced
           constexpr int GROUPS = N / GROUP;
@@ -1012,29 +1001,32 @@ __global__ void __launch_bounds__(um::THREADS, 1)
           }
           tcgen05_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(t_empty(wg, bsel));
+          if (lane == 0) mbar_arrive(t_empty(wg));
+          if (issuing && q + 1 < decltype(chunks)::value) ok = issue(s, q0 + q + 1, use + 1);
 #pragma unroll
           for (int i = 0; i < GROUPS; ++i) group(g[i], (uint32_t)(GROUPS * q + i));
         }
       };
-      if (halves)
-        scan(std::integral_constant<int, CHUNKS / 2>());
+      if (shared_tile)
+        scan(std::integral_constant<int, CHUNKS / WGS>(), wg * (CHUNKS / WGS));
       else
-        scan(std::integral_constant<int, CHUNKS>());
-      if (halves) {   // the second half's four smallest pass through the place of a second tile
+        scan(std::integral_constant<int, CHUNKS>(), 0);
+      if (shared_tile) {   // the other quarters' four smallest pass through the place of a second tile
         float4* other = reinterpret_cast<float4*>(smem + OFF_STAGES + STAGE_BYTES);
-        constexpr uint32_t half = E / GROUP / 2;   // the first of its groups: a power of two
-        auto id = [&](float b) { return __uint_as_float(__float_as_uint(b) | half); };
-        if (wg == 1) other[ml] = make_float4(id(B1), id(B2), id(B3), id(B4));
-        named_barrier_sync(1, 256);   // reached whether or not a wait gave up
-        if (wg == 1) break;
-        const float4 o = other[ml];
-        keep(o.x), keep(o.y), keep(o.z), keep(o.w);
+        static_assert((WGS - 1) * M * 16 <= STAGE_BYTES || CHUNKS < 8, "room for them");
+        const uint32_t first = (uint32_t)wg * (E / GROUP / WGS);   // of its groups: bits that the others leave free
+        auto id = [&](float b) { return __uint_as_float(__float_as_uint(b) | first); };
+        if (wg > 0) other[(wg - 1) * M + ml] = make_float4(id(B1), id(B2), id(B3), id(B4));
+        named_barrier_sync(1, EP_WARPS * 32);   // reached whether or not a wait gave up
+        if (wg > 0) break;
+#pragma unroll 1
+        for (int i = 0; i < WGS - 1; ++i) {
+          const float4 o = other[i * M + ml];
+          keep(o.x), keep(o.y), keep(o.z), keep(o.w);
+        }
         ok = ok && !*s_abort;
       }
       if (!ok) break;
-      const int s = k % STAGES;
-      if (!um_wait(a_full(s), (k / STAGES) & 1, s_abort, p.err, 0xffffffffu)) break;   // (complete already)
       const unsigned char* st = smem + OFF_STAGES + s * STAGE_BYTES;
       const int flag = reinterpret_cast<const int*>(st + ST_FLAG)[ml];
       float xv[DSUB];
@@ -1224,11 +1216,16 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(a_empty(s));
     }
+    if (issuing) {   // every MMA issued has completed before the tensor memory is freed
+      if (issuer) umma_commit(done_bar(wg));
+      __syncwarp();
+      um_wait(done_bar(wg), 0, s_abort, p.err, 0xffffffffu);
+    }
   }
   tcgen05_before_sync();
   __syncthreads();
   tcgen05_after_sync();
-  if (warp == MMA_WARP) tmem_dealloc(tmem, TMEM_COLS);
+  if (warp == EP_WARPS) tmem_dealloc(tmem, TMEM_COLS);
 }
 
 

@@ -107,7 +107,8 @@ struct AppendParams {
   int n_table, rot, interleaved;
   int key_ctas;             // grid (CTAs of a KV head: first those of its keys, then of its values; Hkv)
 };
-cudaError_t append_prepare(int mode);
+bool append_few_rows(int n_tokens, int Hkv, int sms);   // one row per CTA
+cudaError_t append_prepare(int mode, bool few);
 cudaError_t launch_append(int mode, AppendParams p, int sms, cudaStream_t stream);
 
 // Rotary positions (rope.cu).
@@ -234,8 +235,8 @@ cudaError_t evict_select_prepare();   // set smem attributes (once per device)
 cudaError_t launch_evict_select(SelectParams p, int sms, cudaStream_t stream);
 
 // Encode kernels (encode.cu).
-cudaError_t encode_prepare(int mode);
-cudaError_t encode_occupancy(int mode, int* blocks_per_sm);
+cudaError_t encode_prepare(int mode);         // the kernels of few rows
+cudaError_t encode_tiles_prepare(int mode);   // those of many: one CTA per SM
 cudaError_t launch_encode(int mode, const EncodeParams& p, int blocks_x, bool split_rows, cudaStream_t stream);
 int encode_warps_per_cta();
 

@@ -187,6 +187,25 @@ __device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, float (&v)[32], fl
       : "memory");
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e != 0;
+}
+
+// Shared memory of a kernel that splits its registers between warpgroups
+// (setmaxnreg), after checking that the launch's registers cover the split: one
+// that does not would wait forever.
+template <typename K>
+cudaError_t prepare_split_kernel(K kernel, int threads, int registers_of_split, int smem) {
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+  if (e != cudaSuccess) return e;
+  if (a.numRegs * threads < registers_of_split) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
 // Barrier of `threads` threads that leaves the others of the CTA alone.
 __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
