@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "row_range.h"
 
 namespace vqkv {
 namespace {
@@ -30,18 +31,13 @@ struct CombineSmem {
   static constexpr int kBytes = (kMax + 8) * 4;
 };
 
-// A sequence's rows of a cross attention: first row and number; none (and the
-// error bit) where the starts make no sense, at most max_queries.
-struct RowRange {
-  int first, n;
-};
+// A sequence's rows of a cross attention (rows_of_starts), with the error bit where the
+// starts make no sense or there are more than max_queries.
 __device__ __forceinline__ RowRange rows_between(const DecodeParams& p, int start, int end, bool report = false) {
-  // (differences in 64 bits: starts of any bits must not overflow on the way to the comparisons)
-  const long long lo = start, hi = end;
-  const bool fine = lo >= 0 && hi >= lo && hi <= p.n_rows;
-  const int n = fine ? (int)min(hi - lo, (long long)p.max_queries) : 0;
-  if (report && (!fine || n != hi - lo)) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
-  return {fine ? (int)lo : 0, n};
+  bool fine;
+  const RowRange rows = rows_of_starts(start, end, p.n_rows, p.max_queries, &fine);
+  if (report && !fine) atomicOr(p.err, VQKV_DEVERR_SEQ_LEN);
+  return rows;
 }
 __device__ __forceinline__ RowRange row_range(const DecodeParams& p, int b, bool report) {
   return rows_between(p, __ldg(p.row_start + b), __ldg(p.row_start + b + 1), report);

@@ -23,7 +23,7 @@ __device__ __forceinline__ QueryLoad load_query(const DecodeParams& p, int b, in
     const int c = col0 + warp;
     const int m = c / p.g, hq = kvh * p.g + c - m * p.g;
     const __half* q;
-    if constexpr (ROWS)   // one packed row per sequence (or none: the lane's load is not used)
+    if constexpr (ROWS)   // one packed row per sequence (or none: row 0, and the load is not used)
       q = p.q + row_range(p, b, false).first * p.q_row + hq * kHeadDim;
     else
       q = p.q + (((size_t)b * p.M + m) * p.Hq + hq) * kHeadDim;
