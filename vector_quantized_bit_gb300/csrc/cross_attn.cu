@@ -46,9 +46,8 @@ __device__ __forceinline__ void store_four(const DecodeParams& p, __half* dst, f
 
 // q' of every column, as the attention kernel's threads load it (tree_query_kernel's
 // image): sequence b's groups of 32 columns (PAIR: 16) start at cross_query_slot.
-// Columns past a sequence's last are not written: they reach only rows of the
-// products that are not stored.  Four threads per column.  LOW: a group's high parts,
-// then its low ones.
+// Columns past a sequence's last are neither written nor read.  Four threads per
+// column.  LOW: a group's high parts, then its low ones.
 template <bool PAIR, bool LOW>
 __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant__ DecodeParams p, uint4* qx) {
   constexpr int W = PAIR ? 16 : 32;

@@ -397,7 +397,10 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
         qrow = ((size_t)pc.b * p.Hkv + kvh) * ((p.ncols + WCOLS - 1) / WCOLS) + (col0 + cl) / WCOLS;
       }
       const int c = col0 + cl;
-      // q' into tensor memory: lane = column (ONE_O: warpgroup 0 the high parts, 1 the low ones)
+      // q' into tensor memory: lane = column (ONE_O: warpgroup 0 the high parts, 1 the low
+      // ones).  CROSS: zeros for the columns past the last, which share a warp, and with it
+      // the decision to raise the running max, but have nothing in qx: what an earlier call
+      // left there would move the others' roundings.
       if (live && (cl & ~(WCOLS - 1)) < nloc && (TQ == 2 || wg == 0 || ONE_O)) {
         const uint4* q = qx + (ONE_O ? 2 * qrow + wg : qrow) * 16 * 32 + lane;
 #pragma unroll
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
           uint32_t r[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 x = __ldcg(q + 32 * (8 * h + i));
+            const uint4 x = !CROSS || cl < nloc ? __ldcg(q + 32 * (8 * h + i)) : make_uint4(0u, 0u, 0u, 0u);
             r[4 * i] = x.x, r[4 * i + 1] = x.y, r[4 * i + 2] = x.z, r[4 * i + 3] = x.w;
           }
           tmem_st32(t_lane + (ONE_O && wg ? T_Q_LOW : TM::q(wg)) + 32 * h, r);
