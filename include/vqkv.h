@@ -635,10 +635,10 @@ vqkv_status vqkv_append(const vqkv_append_args* args, const vqkv_paging* paging,
  * weights are rounded to fp16 for the tensor cores, q' to two fp16 parts (bf16 calls
  * with max_queries > 1: to one).
  * num_splits: shares of the batch's work per KV head, 0 = automatic, at most
- * 1024 are used (max_queries = 1: as in vqkv_decode_attn).  paging as in
+ * 1024 are used (max_queries = 1: as in vqkv_decode_attn, at most 65,535).  paging as in
  * vqkv_decode_attn_tree.  The workspace holds vqkv_cross_attn_workspace_bytes(args)
- * bytes and may be shared like that of vqkv_decode_attn_tree.  Everything else is as
- * in vqkv_decode_attn.
+ * bytes and may be shared like that of vqkv_decode_attn_tree, before and after the
+ * calls named there.  Everything else is as in vqkv_decode_attn.
  */
 typedef struct {
   vqkv_decode_args decode;    /* q, out: [n_rows][Hq][128] */

@@ -1062,8 +1062,12 @@ vqkv_status plan_cross(const vqkv_cross_args* ac, CrossPlan* pl) {
     PlanInput in = plan_input(&a);
     in.width = 4;
     in.rows = true;
+    in.num_splits = std::min(in.num_splits, kRowsMaxSplits);
     const vqkv_status st = plan_decode(&in, &pl->d);
-    pl->ws_bytes = pl->d.ws_bytes;
+    // partials behind the tickets of all decode calls, which stay zero
+    const size_t partials_off = decode_ticket_region_bytes(a.B, a.Hkv * kTicketGroups);
+    pl->ws_bytes = pl->d.ws_bytes + (partials_off - pl->d.partials_off);
+    pl->d.partials_off = partials_off;
     return st;
   }
   const vqkv_status st = device_info(kCrossKernels, a.mode, &di);

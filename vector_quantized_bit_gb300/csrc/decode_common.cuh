@@ -261,8 +261,12 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
   const size_t split_stride = (size_t)p.ncols * kPartialStride;
   float* part = p.partials + ms.first + (size_t)ms.part * split_stride;
   const int n_parts = ms.n_parts;
-  const unsigned ticket = COLGROUPS ? (unsigned)((b * p.Hkv + kvh) * p.cgroups + blockIdx.z % p.cgroups)
-                                    : (unsigned)(b * p.Hkv + kvh);
+  const unsigned group = COLGROUPS ? blockIdx.z % p.cgroups : 0u;
+  // Packed rows: the column groups, two at most, count in the halves of one ticket per
+  // (sequence, KV head), which every decode call of the same B and Hkv leaves zero: behind
+  // these tickets a decode has its partials.  (n_parts <= kRowsMaxSplits)
+  const unsigned ticket = COLGROUPS && !ROWS ? (unsigned)((b * p.Hkv + kvh) * p.cgroups + group) : (unsigned)(b * p.Hkv + kvh);
+  const unsigned shift = ROWS ? 16 * group : 0u;
   // each warp's scale against the CTA's max of the column, once per (warp,
   // column) rather than once per output
   for (int i = threadIdx.x; i < WARPS * 8; i += WARPS * 32) {
@@ -299,10 +303,11 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
   __syncthreads();
   if (threadIdx.x == 0) {
     unsigned prev;
-    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;"
                  : "=r"(prev)
-                 : "l"(p.tickets + ticket)
+                 : "l"(p.tickets + ticket), "r"(1u << shift)
                  : "memory");
+    if constexpr (ROWS) prev = (prev >> shift) & 0xffffu;
     *s_last = (prev == (unsigned)(n_parts - 1));
   }
   __syncthreads();
@@ -405,7 +410,12 @@ __device__ __forceinline__ void finish_sequence(const DecodeParams& p, int b, in
         }
       }
     }
-    if (threadIdx.x == 0) p.tickets[ticket] = 0u;   // ready for the next call
+    if (threadIdx.x == 0) {   // ready for the next call
+      if constexpr (ROWS)
+        atomicSub(p.tickets + ticket, (unsigned)n_parts << shift);
+      else
+        p.tickets[ticket] = 0u;
+    }
   }
 }
 

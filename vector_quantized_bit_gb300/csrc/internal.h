@@ -71,6 +71,10 @@ struct DecodeParams {
   long long q_row = 0;
 };
 
+// Cross attention of packed rows: CTAs per (sequence, KV head), at most, so that half a
+// ticket counts them.
+constexpr int kRowsMaxSplits = 65535;
+
 constexpr int kPartialStride = 132;  // O[128], m, l, pad (rows 16-byte aligned)
 constexpr int kFlatMaxB = 1024;      // largest batch the flat plan takes
 constexpr unsigned kTilePolls = 1u << 20;   // polls before a wait of a tile kernel gives up
