@@ -632,8 +632,7 @@ vqkv_status vqkv_append(const vqkv_append_args* args, const vqkv_paging* paging,
  * decode.q is fp16 or bf16 (dtype) [n_rows][Hq][128] with rows q_row_stride
  * elements apart, decode.out the same type, contiguous; out may be q's buffer
  * where q is contiguous, too.  Sums and softmax statistics are fp32; the softmax
- * weights are rounded to fp16 for the tensor cores, q' to two fp16 parts (bf16 calls
- * with max_queries > 1: to one).
+ * weights are rounded to fp16 for the tensor cores, q' to two fp16 parts.
  * num_splits: shares of the batch's work per KV head, 0 = automatic, at most
  * 1024 are used (max_queries = 1: as in vqkv_decode_attn, at most 65,535).  paging as in
  * vqkv_decode_attn_tree.  The workspace holds vqkv_cross_attn_workspace_bytes(args)

@@ -754,12 +754,10 @@ def vqkv_append(mode, k, v, row_start, pos, s, k_codebook, v_codebook, k_codes, 
 
 def cross_attn_workspace(mode, B, Hq, Hkv, n_rows, max_queries, cap_len, max_seq_len, num_splits=0, dtype=VQKV_DTYPE_F16,
                          device="cuda"):
-    """A zero-filled workspace tensor of the size vqkv_cross_attn needs (that of fp16 queries serves bf16 ones, too)."""
-    size = 0
-    for code in {dtype, VQKV_DTYPE_BF16}:
-        a = CrossArgs(decode=_size_args(mode, B, Hq, Hkv, cap_len, max_seq_len, num_splits), dtype=code, n_rows=n_rows,
-                      max_queries=max_queries)
-        size = max(size, int(lib().vqkv_cross_attn_workspace_bytes(ctypes.byref(a))))
+    """A zero-filled workspace tensor of the size vqkv_cross_attn needs (the same for fp16 and bf16 queries)."""
+    a = CrossArgs(decode=_size_args(mode, B, Hq, Hkv, cap_len, max_seq_len, num_splits), dtype=dtype, n_rows=n_rows,
+                  max_queries=max_queries)
+    size = int(lib().vqkv_cross_attn_workspace_bytes(ctypes.byref(a)))
     return _new_workspace(size, "vqkv_cross_attn_workspace_bytes", device)
 
 

@@ -1033,7 +1033,7 @@ struct StridedRows {
 struct CrossPlan {
   bool rows = false;    // one query per sequence: the decode's kernels and plan
   DecodePlan d;
-  int n_splits = 1, layout = kOneTile;
+  int n_splits = 1, layout = kBothParts;
   int groups_max = 1;   // items of a sequence, at most
   size_t query_off = 0, items_off = 0, partials_off = 0, ws_bytes = 0;
 };
@@ -1073,7 +1073,7 @@ vqkv_status plan_cross(const vqkv_cross_args* ac, CrossPlan* pl) {
   const vqkv_status st = device_info(kCrossKernels, a.mode, &di);
   if (st != VQKV_OK) return st;
   const long long g = a.Hq / a.Hkv, cols = ac->max_queries * g;
-  pl->layout = ac->dtype == VQKV_DTYPE_F16 ? (cols <= 64 ? kPairs : kBothParts) : cols > 128 ? kTwoTiles : kOneTile;
+  pl->layout = cols <= 64 ? kPairs : kBothParts;
   const int width = cross_cols(pl->layout), B = std::max(std::min(a.B, kFlatMaxB), 1);
   // items, and tiles of full sequences, at most
   const long long items = std::max<long long>(1, std::min(B * ((cols + width - 1) / width), ac->n_rows * g / width + B));

@@ -1,24 +1,25 @@
 // Cross attention over a packed cache (vqkv_cross_attn): ragged queries, each of
 // which sees all cached tokens of its sequence.  The kernel is that of the draft
-// trees (decode_tree.cu) with other work units: an item is a group of up to 64,
-// 128 or 256 of a sequence's columns (query, head of the KV head), its units the
-// tiles of 64 tokens.  All items' units in order are cut into equal shares; a CTA of
-// a KV head takes one share, or two side by side (items of up to 128 columns:
-// STREAMS in tile_attn.cuh).  A share has a piece of an item that began before it and
-// one that ends behind it at most, so two partials per share hold whatever the
-// cut leaves for cross_combine_kernel.
+// trees (decode_tree.cu) with other work units: an item is a group of up to 64 or
+// 128 of a sequence's columns (query, head of the KV head), its units the tiles of
+// 64 tokens.  All items' units in order are cut into equal shares; a CTA of a KV head
+// takes one share, or two side by side (items of 64 columns: STREAMS in tile_attn.cuh).
+// A share has a piece of an item that began before it and one that ends behind it at
+// most, so two partials per share hold whatever the cut leaves for
+// cross_combine_kernel.
 //
-// fp16 results take their scores from both fp16 parts of q' (above 64 columns: ONE_O
-// in tile_attn.cuh); bf16 ones, which are rounded to 2^-9 anyway, from the high parts
-// (2^-12), up to 256 columns per dequantised tile.  An error of 3.7e-4 of the output
-// became 2.7e-4 with the low parts (2.1e-4 is the output's own rounding), at 1.24
-// times the time.
+// The scores come from both fp16 parts of q' (above 64 columns: ONE_O in
+// tile_attn.cuh).  One part is off by 2^-12 rms, and a weight by that times its score
+// in nats, a size that has no bound: fp16 results with errors of 2.7e-4 (2.1e-4 is the
+// output's own rounding) had 3.7e-4; bf16 ones, rounded to 1.7e-3 rms, 1.9e-3 at
+// scores of 11 nats rms and 2.1e-3 at 22.  With one part and up to 256 columns per
+// dequantised tile the ragged bf16 prompts below took 90 us.
 //
 // Bound: the chain of a tile (scores, softmax, P V) against dequantisation that only
-// 128 or 256 columns share, as in the draft trees.  2,048 queries of 32 heads over
-// 32,768 tokens at 2 bit: 1.19 ms (fp16; 0.92 PFLOP/s of the two products, 1.38 with
-// the low parts), 0.96 ms (bf16); 12 ragged prompts of 33 to 448 tokens over paged
-// 4-bit states of 600 to 1,500: 90 us, 7 to 10 of them q' and about 8 the merge.
+// 64 or 128 columns share, as in the draft trees.  2,048 queries of 32 heads over
+// 32,768 tokens at 2 bit: 1.19 ms (0.92 PFLOP/s of the two products, 1.38 with the
+// low parts); 12 ragged prompts of 33 to 448 tokens over paged 4-bit states of 600 to
+// 1,500: 111 us, 7 to 10 of them q' and about 8 the merge.
 #include <algorithm>
 
 #include "common.cuh"
@@ -47,8 +48,9 @@ __device__ __forceinline__ void store_four(const DecodeParams& p, __half* dst, f
 // q' of every column, as the attention kernel's threads load it (tree_query_kernel's
 // image): sequence b's groups of 32 columns (PAIR: 16) start at cross_query_slot.
 // Columns past a sequence's last are neither written nor read.  Four threads per
-// column.  LOW: a group's high parts, then its low ones.
-template <bool PAIR, bool LOW>
+// column.  PAIR: a group's 16 columns' high and low parts side by side; else a group's
+// high parts, then its low ones.
+template <bool PAIR>
 __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant__ DecodeParams p, uint4* qx) {
   constexpr int W = PAIR ? 16 : 32;
   __shared__ int s_start[kFlatMaxB + 1];
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant_
   if (!in) return;
   const int c = (row - rows.first) * p.g + h;
   const size_t slot = (size_t)kvh * (cross_query_slot(p.n_rows, p.B, p.g, W) + 1) + cross_query_slot(rows.first, lo, p.g, W) + c / W;
-  uint4* dst = qx + ((LOW ? 2 * slot : slot) * 16 + 4 * part) * 32 + (c & (W - 1));
+  uint4* dst = qx + ((PAIR ? slot : 2 * slot) * 16 + 4 * part) * 32 + (c & (W - 1));
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t w[4], low[4];
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(128) cross_query_kernel(const __grid_constant_
       low[i] = pack_half2(x - __low2float(f), y - __high2float(f));
     }
     dst[32 * j] = make_uint4(w[0], w[1], w[2], w[3]);
-    if (PAIR || LOW) dst[32 * j + (LOW ? 16 * 32 : 16)] = make_uint4(low[0], low[1], low[2], low[3]);
+    dst[32 * j + (PAIR ? 16 : 16 * 32)] = make_uint4(low[0], low[1], low[2], low[3]);
   }
 }
 
@@ -218,10 +220,8 @@ __global__ void __launch_bounds__(CW_WARPS * 32) cross_combine_wide_kernel(const
 using CrossKernel = void (*)(DecodeParams, const unsigned long long*, const uint4*);
 template <int MODE, bool PAGED>
 CrossKernel cross_of(int layout) {
-  if (layout == kPairs) return decode_tree_kernel<MODE, PAGED, 1, true, kCross>;
-  if (layout == kTwoTiles) return decode_tree_kernel<MODE, PAGED, 2, false, kCross>;
-  if (layout == kBothParts) return decode_tree_kernel<MODE, PAGED, 1, false, kCrossParts>;
-  return decode_tree_kernel<MODE, PAGED, 1, false, kCross>;
+  if (layout == kPairs) return decode_tree_kernel<MODE, PAGED, 1, true, kCrossPairs>;
+  return decode_tree_kernel<MODE, PAGED, 1, false, kCrossParts>;
 }
 template <int MODE>
 CrossKernel cross_of(bool paged, int layout) {
@@ -240,28 +240,26 @@ int cross_smem(int mode) {
 
 }  // namespace
 
-int cross_cols(int layout) { return layout == kPairs ? 64 : layout == kTwoTiles ? 2 * tr::ROWS : tr::ROWS; }
-int cross_shares(int layout) { return layout == kPairs || layout == kOneTile ? 2 : 1; }
+int cross_cols(int layout) { return layout == kPairs ? 64 : tr::ROWS; }
+int cross_shares(int layout) { return layout == kPairs ? 2 : 1; }
 
 cudaError_t cross_prepare(int mode) {
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 8 && e == cudaSuccess; ++i)
-    e = prepare_split_kernel(cross_kernel(mode, (i & 1) != 0, i >> 1), tr::THREADS, tr::SPLIT_REGS, cross_smem(mode));
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+    e = prepare_split_kernel(cross_kernel(mode, (i & 1) != 0, i < 2 ? kPairs : kBothParts), tr::THREADS, tr::SPLIT_REGS, cross_smem(mode));
   return e;
 }
 
 size_t cross_query_bytes(int B, int Hq, int Hkv, int n_rows, int layout) {
   return (size_t)Hkv * (cross_query_slot(n_rows, B, Hq / Hkv, layout == kPairs ? 16 : 32) + 1) *
-         (layout == kBothParts ? 2 : 1) * 32 * kHeadDim * 2;
+         (layout == kPairs ? 1 : 2) * 32 * kHeadDim * 2;
 }
 
 cudaError_t launch_cross(int mode, const DecodeParams& p, int layout, int groups_max, void* qx, cudaStream_t stream) {
   uint4* q = static_cast<uint4*>(qx);
   const dim3 grid((unsigned)(((long long)p.n_rows * p.g + 31) / 32), p.Hkv);
-  cudaError_t e = launch_pdl(layout == kPairs       ? cross_query_kernel<true, false>
-                             : layout == kBothParts ? cross_query_kernel<false, true>
-                                                    : cross_query_kernel<false, false>,
-                             grid, dim3(128), 0, stream, p, q);
+  cudaError_t e = launch_pdl(layout == kPairs ? cross_query_kernel<true> : cross_query_kernel<false>, grid, dim3(128), 0, stream,
+                             p, q);
   if (e == cudaSuccess)
     e = launch_pdl(cross_kernel(mode, p.block_table != nullptr, layout),
                    dim3((p.n_splits + cross_shares(layout) - 1) / cross_shares(layout), p.Hkv), dim3(tr::THREADS),

@@ -176,17 +176,19 @@ size_t decode_tree_query_bytes(int B, int Hkv, int ncols, bool pairs);
 cudaError_t launch_decode_tree(int mode, const DecodeParams& p, const unsigned long long* tree_mask, bool pairs, void* qx,
                                cudaStream_t stream);
 
-// Cross attention (cross_attn.cu), B <= kFlatMaxB: n_splits shares per KV head;
-// partials [Hkv][2 n_splits] of [32 pieces of 4 channels][cross_cols(layout) columns],
-// then max and sum of each column.  groups_max: items of a sequence, at most.
-// layout: an item's columns on the MMA rows, and whether q' is in one fp16 part
-// (bf16 results: 2^-11 of the scores is below their own rounding) or in two.
+// How columns lie on the MMA rows of the tile kernels, and whether q' is in one fp16
+// part or in two.
 enum TileLayout : int {
-  kOneTile = 0,    // 128 columns
-  kTwoTiles = 1,   // 256
+  kOneTile = 0,    // 128 columns, one part
+  kTwoTiles = 1,   // 256, one part
   kPairs = 2,      // 64, both parts of a column on two rows
   kBothParts = 3   // 128, both parts as two products
 };
+
+// Cross attention (cross_attn.cu), B <= kFlatMaxB: n_splits shares per KV head;
+// partials [Hkv][2 n_splits] of [32 pieces of 4 channels][cross_cols(layout) columns],
+// then max and sum of each column.  groups_max: items of a sequence, at most.
+// layout: kPairs or kBothParts.
 int cross_cols(int layout);     // columns of an item, at most
 int cross_shares(int layout);   // shares that a CTA works on side by side
 cudaError_t cross_prepare(int mode);

@@ -265,9 +265,9 @@ __device__ __forceinline__ void cross_finish(const DecodeParams& p, bool whole, 
   }
 }
 
-// What the kernel attends: a tree or causal queries; a cross attention; one whose
-// scores take both fp16 parts of q' (items of 128 columns).
-enum CrossKind : int { kNoCross = 0, kCross = 1, kCrossParts = 2 };
+// What the kernel attends: a tree or causal queries; a cross attention, whose scores
+// take both fp16 parts of q', with items of 64 columns (pairs) or of 128.
+enum CrossKind : int { kNoCross = 0, kCrossPairs = 1, kCrossParts = 2 };
 
 // grid (shares, Hkv, column groups of 128 NQ; CROSS: 1).
 template <int MODE, bool PAGED, int NQ, bool PAIR = false, int CROSS = kNoCross>
@@ -276,16 +276,16 @@ __global__ void __launch_bounds__(tr::THREADS, 1) decode_tree_kernel(const Decod
                                                                      const uint4* qx) {
   using namespace tr;
   using G = Geo<MODE>;
-  // Cross attention of items of one query tile: the softmax warpgroups work on two
+  // Cross attention of items of 64 columns: the softmax warpgroups work on two
   // shares, each with items, tiles and half of the ring's stages of its own, so that
   // one's passage to its next item (q', first tile, O) hides behind the other's
   // products.  Tensor memory is dealt out as for two query tiles (P overlays S).
-  constexpr bool STREAMS = CROSS == kCross && NQ == 1;
+  constexpr bool STREAMS = CROSS == kCrossPairs;
   // Both fp16 parts of q': the low ones take the place of the second O, and the two
   // warpgroups' tiles add to one O.  (With two of them and P over S, so that a
   // warpgroup's next scores wait for its P V, a tile took 1,520 cycles, not 1,330.)
   constexpr bool ONE_O = CROSS == kCrossParts;
-  static_assert(!ONE_O || (NQ == 1 && !PAIR), "one query tile, both parts of q'");
+  static_assert(!CROSS || (NQ == 1 && PAIR == STREAMS), "cross attention: pairs, or one query tile of both parts of q'");
   constexpr int TQ = STREAMS ? 2 : NQ;
   using TM = Tmem<TQ>;
   extern __shared__ __align__(1024) unsigned char smem[];
