@@ -695,18 +695,18 @@ vqkv_status encode_launch(const vqkv_encode_args* a, void* stream, const vqkv_pa
   const long long rows = (long long)a->B * a->n_rows;   // per KV head
   // Few rows (a decode-step append): one row per CTA, its candidates split
   // over the CTA's warps, for latency.
-  const bool split_rows = rows * a->Hkv * encode_warps_per_cta() <= (long long)di.sms * 8;
+  const bool split_rows = rows * a->Hkv <= di.sms;
   int blocks_x;
   if (split_rows) {
     blocks_x = (int)rows;
   } else {
     const vqkv_status ready = device_info(kEncodeTileKernels, a->mode, &di);
     if (ready != VQKV_OK) return ready;
-    const long long want = (rows + encode_warps_per_cta() - 1) / encode_warps_per_cta();
-    // persistent tensor-memory CTAs over tiles of 8, 4 or 2 rows, one per SM
-    long long cap = ((long long)di.sms + a->Hkv - 1) / a->Hkv;
-    if (cap < 1) cap = 1;
-    blocks_x = (int)std::min(want, cap);
+    // Persistent tensor-memory CTAs over tiles of 8, 4 or 2 rows, one per SM, in one wave
+    // (a few CTAs more would run after the others: 1,000 key rows of 5 heads at 4 bit
+    // 33 us with 31 CTAs a head, 21 with 30).
+    const long long tiles = (rows + encode_tile_rows(a->mode) - 1) / encode_tile_rows(a->mode);
+    blocks_x = (int)std::min<long long>(tiles, std::max(1, di.sms / a->Hkv));
   }
   set_paging(p, pg, a->mode);
   if (launch_encode(a->mode, p, blocks_x, split_rows, static_cast<cudaStream_t>(stream)) != cudaSuccess)

@@ -6,7 +6,13 @@
 
 namespace vqkv {
 
-int encode_warps_per_cta() { return ENC_WARPS; }
+int encode_tile_rows(int mode) {
+  return mode == VQKV_MODE_VQ2    ? UmGeo<VQKV_MODE_VQ2>::ROWS
+         : mode == VQKV_MODE_VQ4  ? UmGeo<VQKV_MODE_VQ4>::ROWS
+         : mode == VQKV_MODE_VQ3  ? UmGeo<VQKV_MODE_VQ3>::ROWS
+         : mode == VQKV_MODE_VQ15 ? UmGeo<VQKV_MODE_VQ15>::ROWS
+                                  : UmGeo<VQKV_MODE_VQ125>::ROWS;
+}
 
 cudaError_t encode_prepare(int mode) {
   const cudaFuncAttribute smem_attr = cudaFuncAttributeMaxDynamicSharedMemorySize;

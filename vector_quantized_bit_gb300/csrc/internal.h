@@ -244,6 +244,6 @@ cudaError_t launch_evict_select(SelectParams p, int sms, cudaStream_t stream);
 cudaError_t encode_prepare(int mode);         // the kernels of few rows
 cudaError_t encode_tiles_prepare(int mode);   // those of many: one CTA per SM
 cudaError_t launch_encode(int mode, const EncodeParams& p, int blocks_x, bool split_rows, cudaStream_t stream);
-int encode_warps_per_cta();
+int encode_tile_rows(int mode);   // rows of a tile of the latter
 
 }  // namespace vqkv
