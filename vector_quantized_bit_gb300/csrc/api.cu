@@ -1266,8 +1266,7 @@ vqkv_status vqkv_cross_attn(const vqkv_cross_args* ac, const vqkv_paging* pg, vo
     p.partials = reinterpret_cast<float*>(ws + pl.d.partials_off);
     p.n_splits = pl.d.n_splits;
     p.tps = pl.d.tps;
-    p.bpg = pl.d.bpg;
-    p.defer_merge = pl.d.bpg > 1 ? 1 : 0;
+    p.bpg = 1;   // plan_decode, rows
     p.flat = pl.d.flat;
     p.cgroups = pl.d.cgroups;
     const dim3 grid(pl.d.n_splits, a->Hkv, pl.d.n_bgroups * pl.d.cgroups);

@@ -9,12 +9,6 @@
 namespace vqkv {
 namespace {
 
-__global__ void __launch_bounds__(kHeadDim) rows_combine_kernel(const DecodeParams p) {
-  grid_dependency_wait();
-  grid_dependents_launch();
-  combine_splits<kRows>(p);
-}
-
 using DecodeKernel = void (*)(DecodeParams);
 template <int MODE>
 DecodeKernel ring_of(bool flat, bool paged) {
@@ -48,11 +42,8 @@ cudaError_t cross_rows_prepare(int mode) {
 }
 
 cudaError_t launch_cross_rows(int mode, const DecodeParams& p, dim3 grid, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(rows_kernel_of(mode, p.flat != 0, p.block_table != nullptr), grid, dim3(decode_threads(mode)),
-                             decode_smem_bytes(mode), stream, p);
-  if (e == cudaSuccess && p.defer_merge && p.n_splits > 1)
-    e = launch_pdl(rows_combine_kernel, dim3(p.Hkv * p.ncols, p.B), dim3(kHeadDim), 0, stream, p);
-  return e;
+  return launch_pdl(rows_kernel_of(mode, p.flat != 0, p.block_table != nullptr), grid, dim3(decode_threads(mode)),
+                    decode_smem_bytes(mode), stream, p);
 }
 
 }  // namespace vqkv

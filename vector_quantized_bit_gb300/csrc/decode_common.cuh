@@ -450,7 +450,7 @@ __device__ __forceinline__ void combine_splits(const DecodeParams& p) {
       M = n;
     }
   }
-  store_output<FORM == kRows>(p, b, kvh, h, d, Ls > 0.f ? O / Ls : 0.f);
+  p.out[out_row(p, b, kvh, h) + d] = __float2half_rn(Ls > 0.f ? O / Ls : 0.f);
   if constexpr (FORM == kMass)
     if (d == 0) p.stats[(size_t)(b * p.Hkv + kvh) * p.ncols + h] = make_float2(M, Ls > 0.f ? 1.f / Ls : 0.f);
 }

@@ -95,12 +95,6 @@ struct Rows<false> {
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
     v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
   }
-  __device__ __forceinline__ void transform(Raw raw, const Turn&, float4 s, float4 rs, int lane, float (&x)[4]) const {
-    if (p.role == VQKV_ROLE_K)
-      transform_key_lean(raw, s, rs, lane, x);
-    else
-      transform_loaded(raw, false, s, lane, x);
-  }
   __device__ __forceinline__ void row(const RowPlace&, int r, int lane, float (&x)[4]) const {
     transform_row(row_ptr(r), p.role == VQKV_ROLE_K ? p.s + (size_t)kvh * kHeadDim : nullptr, lane, x);
   }
