@@ -522,7 +522,7 @@ typedef struct {
   double base;           /* > 1, finite */
   double factor;         /* > 0, finite */
   double low_turns, high_turns;   /* 0 < low_turns < high_turns, finite */
-  double amplitude;      /* finite */
+  double amplitude;      /* within fp32's range */
   float* table;          /* device fp32 [n_pos][rot_dim] out, 16-byte aligned */
 } vqkv_rope_table_args;
 

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 #include <mutex>
 
 #include "internal.h"
@@ -1092,7 +1093,7 @@ vqkv_status plan_cross(const vqkv_cross_args* ac, CrossPlan* pl) {
 // Frequencies of the pairs, radians per position; false for arguments out of range.
 bool rope_frequencies(const vqkv_rope_table_args* a, double (&f)[64]) {
   const double r = a->rot_dim, pi = 3.14159265358979323846;
-  if (!(a->base > 1.0) || !std::isfinite(a->base) || !std::isfinite(a->amplitude)) return false;
+  if (!(a->base > 1.0) || !std::isfinite(a->base) || !(std::fabs(a->amplitude) <= std::numeric_limits<float>::max())) return false;
   const bool scaled = a->scaling != VQKV_ROPE_NONE;
   const bool turns = a->scaling == VQKV_ROPE_WAVELENGTH || a->scaling == VQKV_ROPE_RAMP;
   if (scaled && (!(a->factor > 0.0) || !std::isfinite(a->factor))) return false;
