@@ -1264,11 +1264,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   Turn turn{};
   float4 xs = make_float4(1.f, 1.f, 1.f, 1.f);
   if (warp == 0 && src.cta() < rows) {
-    xraw = src.load(src.cta(), lane);
     if (ks != nullptr) xs = *reinterpret_cast<const float4*>(ks + 4 * lane);
     if constexpr (APPEND) {
       const RowPlace w = src.place(src.cta(), src.angle(src.cta()), false);
-      turn = src.turn(w.angle, lane);
+      if (w.t >= 0) {   // padding is not read
+        xraw = src.load(src.cta(), lane);
+        turn = src.turn(w.angle, lane);
+      }
+    } else {
+      xraw = src.load(src.cta(), lane);
     }
   }
   const float Cmax = build_tc_table(p, kvh, s_tbl, s_cmax);
