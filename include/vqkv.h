@@ -130,15 +130,18 @@ typedef enum {
 #define VQKV_DEVERR_TIMEOUT   0x4u  /* a bounded on-chip wait gave up: see below */
 #define VQKV_DEVERR_BLOCK     0x8u  /* a block-table entry outside [0, num_blocks) (paged calls) */
 /*
- * VQKV_DEVERR_TIMEOUT: every on-chip wait of the decode kernels (the bulk
- * copies of the 2-bit code ring) gives up after a bounded number of polls
- * instead of hanging.  The CTA then waits, again bounded, for the copies it
- * still has in flight, sets this bit and finishes.  After it is set, the
+ * VQKV_DEVERR_TIMEOUT: every on-chip wait gives up after a bounded number of
+ * polls instead of hanging: those of the decode kernels (the bulk copies of
+ * the code ring), of the tile kernels (draft trees, attention weights, cross
+ * attention) and of the encode kernels of many rows (vqkv_encode,
+ * vqkv_append).  The CTA then waits, again bounded, for the copies or products
+ * it still has in flight, sets this bit and finishes.  After it is set, the
  * launch's output O (and the shared memory of that CTA, which a late copy
- * may still write) are undefined.  A wait runs out only when a copy did not
- * complete in about 10^6 polls, which points at a fault outside the
- * library: treat the context as suspect, and do not trust later results on
- * it without checking them.
+ * may still write) are undefined; of an encode's or append's rows any may be
+ * unwritten or written in part, and where error_flags is NULL nothing tells.
+ * A wait runs out only when a copy or product did not complete in about
+ * 10^6 polls, which points at a fault outside the library: treat the context
+ * as suspect, and do not trust later results on it without checking them.
  */
 
 /*
@@ -177,7 +180,8 @@ typedef struct {
                                          second-best fp32 distances differ by less than
                                          1e-6 relative */
   uint32_t* error_flags;      /* device, optional: VQKV_DEVERR_POSITION is or-ed in when a
-                                 row's position is outside [0, cap_len) (row not written) */
+                                 row's position is outside [0, cap_len) (row not written);
+                                 _TIMEOUT, and _BLOCK in the paged call */
 } vqkv_encode_args;
 
 /*
@@ -610,7 +614,7 @@ typedef struct {
   uint8_t* k_codes;           /* device [B][Hkv][vqkv_code_bytes], or a pool */
   uint8_t* v_codes;
   unsigned long long* near_tie_count; /* device, optional: as in vqkv_encode_args, for both roles */
-  uint32_t* error_flags;      /* device, optional: VQKV_DEVERR_POSITION, _BLOCK */
+  uint32_t* error_flags;      /* device, optional: VQKV_DEVERR_POSITION, _BLOCK, _TIMEOUT */
 } vqkv_append_args;
 
 vqkv_status vqkv_append(const vqkv_append_args* args, const vqkv_paging* paging, void* stream);
