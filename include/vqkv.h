@@ -586,7 +586,8 @@ vqkv_status vqkv_rope(const vqkv_rope_args* args, void* stream);
  * not written, neither key nor value, and sets VQKV_DEVERR_POSITION.
  *
  * The rotated keys are computed in pairs of fp32, so they and the codes are
- * those of vqkv_encode's reading: exact up to near-ties.  k and v are finite.
+ * those of vqkv_encode's reading: exact up to near-ties.  k and v are finite, and
+ * so is a key's x' in fp32.
  * paging: NULL for the contiguous cache, else the pools of the paged calls.
  */
 typedef struct {

@@ -19,7 +19,7 @@
 // 64 or 128 columns share, as in the draft trees.  2,048 queries of 32 heads over
 // 32,768 tokens at 2 bit: 1.19 ms (0.92 PFLOP/s of the two products, 1.38 with the
 // low parts); 12 ragged prompts of 33 to 448 tokens over paged 4-bit states of 600 to
-// 1,500: 111 us, 7 to 10 of them q' and about 8 the merge.
+// 1,500: 112 us, about a sixth of them q' and the merge.
 #include <algorithm>
 
 #include "common.cuh"

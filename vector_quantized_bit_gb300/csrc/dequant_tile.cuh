@@ -1,7 +1,8 @@
 // Dequantised tiles of packed codes in shared memory, as tensor-core operands:
 // codebooks, code loads, centroid gathers, swizzled tile stores, the loop of a
 // dequantising warp, and the shares of a ragged batch.  Used by the kernels
-// that run many softmax columns on tcgen05 (decode_tree.cu, mass_tiles.cu).
+// that run many softmax columns on tcgen05 (decode_tree.cu, cross_attn.cu,
+// mass_tiles.cu).
 #pragma once
 
 #include <type_traits>
